@@ -34,6 +34,9 @@ EXPORTS = (
     "dsv_selftest_wait_timeout",
     "dsv_predict_topk_workspace_bytes", "dsv_predict_topk_blocks",
     "dsv_dispatch_heads",
+    "dsv_rope_axes_fwd", "dsv_rope_axes_bwd_workspace_bytes", "dsv_rope_axes_bwd",
+    "dsv_packed_attn_fwd_workspace_bytes", "dsv_packed_attn_fwd",
+    "dsv_packed_attn_bwd_workspace_bytes", "dsv_packed_attn_bwd",
 )
 SELFTEST_WAIT_ID = 0xD5F0
 
@@ -41,6 +44,22 @@ SELFTEST_WAIT_ID = 0xD5F0
 class Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("N", ctypes.c_int32),
                 ("d", ctypes.c_int32), ("block", ctypes.c_int32), ("r", ctypes.c_int32)]
+
+
+class View(ctypes.Structure):
+    """dsv_view: the address and element strides of a [batch, heads, tokens, d] tensor."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("N", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("section", ctypes.c_int32 * 4), ("theta", ctypes.c_double)]
+
+
+class Packed(ctypes.Structure):
+    _fields_ = [("S", ctypes.c_int32), ("H", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("Tq", ctypes.c_int32),
+                ("Tk", ctypes.c_int32), ("d", ctypes.c_int32)]
 
 
 class DsvError(RuntimeError):
@@ -110,6 +129,22 @@ def _load() -> ctypes.CDLL:
     lib.dsv_dispatch_heads.restype = ctypes.c_int
     lib.dsv_selftest_wait_timeout.argtypes = [vp]
     lib.dsv_selftest_wait_timeout.restype = ctypes.c_int
+    f32, i64 = ctypes.c_float, ctypes.c_int64
+    lib.dsv_rope_axes_fwd.argtypes = [View, vp, i64, Rope, vp, f32, View, vp]
+    lib.dsv_rope_axes_fwd.restype = ctypes.c_int
+    lib.dsv_rope_axes_bwd_workspace_bytes.argtypes = [Rope]
+    lib.dsv_rope_axes_bwd_workspace_bytes.restype = sz
+    lib.dsv_rope_axes_bwd.argtypes = [View, View, vp, i64, Rope, vp, f32, View, vp, vp, sz, vp]
+    lib.dsv_rope_axes_bwd.restype = ctypes.c_int
+    lib.dsv_packed_attn_fwd_workspace_bytes.argtypes = [Packed]
+    lib.dsv_packed_attn_fwd_workspace_bytes.restype = sz
+    lib.dsv_packed_attn_fwd.argtypes = [View, View, View, Packed, vp, vp, i32, f32, View, vp, vp, sz, vp]
+    lib.dsv_packed_attn_fwd.restype = ctypes.c_int
+    lib.dsv_packed_attn_bwd_workspace_bytes.argtypes = [Packed]
+    lib.dsv_packed_attn_bwd_workspace_bytes.restype = sz
+    lib.dsv_packed_attn_bwd.argtypes = [View, View, View, View, View, vp, Packed, vp, vp, i32, f32, View, View, View,
+                                        vp, sz, vp]
+    lib.dsv_packed_attn_bwd.restype = ctypes.c_int
     lib.dsv_version.argtypes = []
     lib.dsv_version.restype = i32
     return lib
@@ -147,6 +182,20 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, device: Optional[torch
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _need_rows(t: torch.Tensor, name: str, device: Optional[torch.device] = None):
+    """t is a bf16 CUDA tensor whose last dimension is contiguous; the library checks its other strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
 def _dims(t, name: str, n: int) -> Tuple[int, ...]:
@@ -559,6 +608,207 @@ def attn_bwd_dq(Q, K, V, dO, fwd_ptr, fwd_col, block: int, softmax_scale: float 
         _check(lib.dsv_attn_bwd_dq(_ptr(Q), _ptr(K), _ptr(V), _ptr(dO), s, _ptr(fwd_ptr), _ptr(fwd_col),
                                    float(softmax_scale), _ptr(out), _ptr(workspace), _nbytes(workspace),
                                    _stream(dev, stream)), "dsv_attn_bwd_dq")
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions with several axes, and attention of packed sequences
+# ---------------------------------------------------------------------------
+
+def _scratch(nbytes: int, device, workspace: Optional[torch.Tensor]) -> torch.Tensor:
+    """`workspace`, which must be contiguous memory of this device with room for nbytes, or a new one."""
+    if workspace is not None:
+        _need(workspace, "workspace", workspace.dtype, device)
+    return _workspace(nbytes, device, workspace)
+
+
+def _view(t: Optional[torch.Tensor]) -> View:
+    """dsv_view of a [.., heads, tokens, d] tensor of 3 or 4 dimensions."""
+    if t is None:
+        return View(None, 0, 0, 0)
+    st = t.stride()
+    return View(t.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2])
+
+
+def _rope_shape(t, name: str, pos, sections: Sequence[int], theta: float) -> Tuple[Rope, int]:
+    """(dsv_rope, elements between batches of pos)."""
+    B, H, N, d = _dims(t, name, 4)
+    sections = [int(c) for c in sections]
+    if not 1 <= len(sections) <= 4:
+        raise ValueError(f"sections has {len(sections)} entries, expected one per axis, 1 to 4")
+    if not isinstance(pos, torch.Tensor):
+        raise TypeError("pos must be a torch.Tensor")
+    A = len(sections)
+    if tuple(pos.shape) not in ((N, A), (B, N, A)):
+        raise ValueError(f"pos has shape {tuple(pos.shape)}, expected {(N, A)} or {(B, N, A)}")
+    return (Rope(B, H, N, d, A, (ctypes.c_int32 * 4)(*sections), float(theta)),
+            N * A if pos.dim() == 3 else 0)
+
+
+def rope_axes(x, pos, sections: Sequence[int], *, theta: float = 10000.0, weight=None, eps: float = 1e-6, out=None,
+              stream=None) -> torch.Tensor:
+    """Rotary positions with several axes, bf16 [B,H,N,d], behind the RMS norm
+    of each row where a weight (fp32 [d]) is given; see dsv_rope_axes_fwd.
+
+    sections: channels of each axis' band; pos: int32 [N, axes] or [B, N,
+    axes].  x may be any view whose last dimension is contiguous (such as the
+    transposed [B,N,H,d] of a projection).  out may be x; without it the result
+    has x's dimension order in memory."""
+    r, pos_b = _rope_shape(x, "x", pos, sections, theta)
+    if out is not None:
+        _shape(out, "out", x.shape)
+    if weight is not None:
+        _shape(weight, "weight", (r.d,))
+    _need_rows(x, "x")
+    dev = x.device
+    _need(pos, "pos", torch.int32, dev)
+    if weight is not None:
+        _need(weight, "weight", torch.float32, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need_rows(out, "out", dev)
+    with torch.cuda.device(dev):
+        _check(lib.dsv_rope_axes_fwd(_view(x), _ptr(pos), pos_b, r, _ptr(weight), float(eps), _view(out),
+                                     _stream(dev, stream)), "dsv_rope_axes_fwd")
+    return out
+
+
+def rope_axes_bwd_workspace_bytes(d: int) -> int:
+    return int(lib.dsv_rope_axes_bwd_workspace_bytes(Rope(1, 1, 1, d, 1, (ctypes.c_int32 * 4)(d), 10000.0)))
+
+
+def rope_axes_bwd(dy, pos, sections: Sequence[int], *, theta: float = 10000.0, x=None, weight=None, eps: float = 1e-6,
+                  dx=None, dweight=None, workspace=None, stream=None):
+    """Gradient of rope_axes: dx, or (dx, dweight fp32 [d]) with a weight (then
+    x, the forward's input, is needed); see dsv_rope_axes_bwd.  dx may be dy or x."""
+    r, pos_b = _rope_shape(dy, "dy", pos, sections, theta)
+    if dx is not None:
+        _shape(dx, "dx", dy.shape)
+    if weight is not None:
+        if x is None:
+            raise ValueError("the gradient through the norm needs x")
+        _shape(x, "x", dy.shape)
+        _shape(weight, "weight", (r.d,))
+        if dweight is not None:
+            _shape(dweight, "dweight", (r.d,))
+    elif dweight is not None:
+        raise ValueError("dweight without a weight")
+    _need_rows(dy, "dy")
+    dev = dy.device
+    _need(pos, "pos", torch.int32, dev)
+    if dx is None:
+        dx = torch.empty_like(dy)
+    else:
+        _need_rows(dx, "dx", dev)
+    nbytes, ws = 0, None
+    if weight is not None:
+        _need_rows(x, "x", dev)
+        _need(weight, "weight", torch.float32, dev)
+        if dweight is None:
+            dweight = torch.empty(r.d, dtype=torch.float32, device=dev)
+        _need(dweight, "dweight", torch.float32, dev)
+        nbytes = lib.dsv_rope_axes_bwd_workspace_bytes(r)
+        ws = _scratch(nbytes, dev, workspace)
+    with torch.cuda.device(dev):
+        _check(lib.dsv_rope_axes_bwd(_view(dy), _view(x if weight is not None else None), _ptr(pos), pos_b, r,
+                                     _ptr(weight), float(eps), _view(dx), _ptr(dweight), _ptr(ws), nbytes,
+                                     _stream(dev, stream)), "dsv_rope_axes_bwd")
+    return dx if weight is None else (dx, dweight)
+
+
+def _packed_shape(Q, K, V, q_ptr, k_ptr) -> Packed:
+    H, Tq, d = _dims(Q, "Q", 3)
+    Hkv, Tk, dk = _dims(K, "K", 3)
+    if dk != d:
+        raise ValueError(f"K has head dimension {dk}, expected {d}")
+    if Hkv < 1 or H % Hkv != 0:
+        raise ValueError(f"Q has {H} heads, expected a multiple of K's {Hkv}")
+    _shape(V, "V", (Hkv, Tk, d))
+    S = _dims(q_ptr, "q_ptr", 1)[0] - 1
+    if S < 0:
+        raise ValueError("q_ptr must hold at least one element")
+    _shape(k_ptr, "k_ptr", (S + 1,))
+    return Packed(S, H, Hkv, Tq, Tk, d)
+
+
+def packed_attn_fwd_workspace_bytes(S: int, H: int, Hkv: int, Tq: int, Tk: int, d: int) -> int:
+    return int(lib.dsv_packed_attn_fwd_workspace_bytes(Packed(S, H, Hkv, Tq, Tk, d)))
+
+
+def packed_attn_bwd_workspace_bytes(S: int, H: int, Hkv: int, Tq: int, Tk: int, d: int) -> int:
+    return int(lib.dsv_packed_attn_bwd_workspace_bytes(Packed(S, H, Hkv, Tq, Tk, d)))
+
+
+def packed_attn_fwd(Q, K, V, q_ptr, k_ptr, softmax_scale: float = 0.0, *, causal: bool = False, out=None, lse=None,
+                    workspace=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(O bf16 [H,Tq,d], lse fp32 [H,Tq]) of sequences packed along the token
+    axis: sequence s owns the queries q_ptr[s]:q_ptr[s+1] and the keys
+    k_ptr[s]:k_ptr[s+1]; see dsv_packed_attn_fwd.
+
+    Q [H,Tq,d], K and V [Hkv,Tk,d] may be any views whose last dimension is
+    contiguous (such as transposed [T,H,d] projections).  Rows outside the
+    sequences are not written: in an output that this call allocates they are
+    uninitialised."""
+    p = _packed_shape(Q, K, V, q_ptr, k_ptr)
+    if out is not None:
+        _shape(out, "out", Q.shape)
+    if lse is not None:
+        _shape(lse, "lse", (p.H, p.Tq))
+    _need_rows(Q, "Q")
+    dev = Q.device
+    _need_rows(K, "K", dev)
+    _need_rows(V, "V", dev)
+    _need(q_ptr, "q_ptr", torch.int32, dev)
+    _need(k_ptr, "k_ptr", torch.int32, dev)
+    if out is None:
+        out = torch.empty_like(Q)
+    else:
+        _need_rows(out, "out", dev)
+    if lse is None:
+        lse = torch.empty(p.H, p.Tq, dtype=torch.float32, device=dev)
+    _need(lse, "lse", torch.float32, dev)
+    nbytes = lib.dsv_packed_attn_fwd_workspace_bytes(p)
+    ws = _scratch(nbytes, dev, workspace) if nbytes else None
+    with torch.cuda.device(dev):
+        _check(lib.dsv_packed_attn_fwd(_view(Q), _view(K), _view(V), p, _ptr(q_ptr), _ptr(k_ptr), 1 if causal else 0,
+                                       float(softmax_scale), _view(out), _ptr(lse), _ptr(ws), nbytes,
+                                       _stream(dev, stream)), "dsv_packed_attn_fwd")
+    return out, lse
+
+
+def packed_attn_bwd(Q, K, V, O, dO, lse, q_ptr, k_ptr, softmax_scale: float = 0.0, *, causal: bool = False, outs=None,
+                    workspace=None, stream=None):
+    """(dQ [H,Tq,d], dK, dV [Hkv,Tk,d]) bf16 of packed_attn_fwd, from its O and
+    lse; see dsv_packed_attn_bwd."""
+    p = _packed_shape(Q, K, V, q_ptr, k_ptr)
+    _shape(O, "O", Q.shape)
+    _shape(dO, "dO", Q.shape)
+    _shape(lse, "lse", (p.H, p.Tq))
+    if outs is not None:
+        if len(outs) != 3:
+            raise ValueError("outs must be (dQ, dK, dV)")
+        for name, t, like in zip(("dQ", "dK", "dV"), outs, (Q, K, V)):
+            _shape(t, name, like.shape)
+    _need_rows(Q, "Q")
+    dev = Q.device
+    for name, t in (("K", K), ("V", V), ("O", O), ("dO", dO)):
+        _need_rows(t, name, dev)
+    _need(lse, "lse", torch.float32, dev)
+    _need(q_ptr, "q_ptr", torch.int32, dev)
+    _need(k_ptr, "k_ptr", torch.int32, dev)
+    if outs is None:
+        outs = (torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V))
+    else:
+        for name, t in zip(("dQ", "dK", "dV"), outs):
+            _need_rows(t, name, dev)
+    nbytes = lib.dsv_packed_attn_bwd_workspace_bytes(p)
+    ws = _scratch(nbytes, dev, workspace) if nbytes else None
+    with torch.cuda.device(dev):
+        _check(lib.dsv_packed_attn_bwd(_view(Q), _view(K), _view(V), _view(O), _view(dO), _ptr(lse), p, _ptr(q_ptr),
+                                       _ptr(k_ptr), 1 if causal else 0, float(softmax_scale),
+                                       *[_view(t) for t in outs], _ptr(ws), nbytes, _stream(dev, stream)),
+               "dsv_packed_attn_bwd")
+    return outs
 
 
 # ---------------------------------------------------------------------------

@@ -141,6 +141,104 @@ dsv_status check_shape(const dsv_shape& s, bool need_r) {
   return DSV_OK;
 }
 
+// 3D map over heads x tokens x d bf16 with the view's strides, box = [box_tok,
+// box_heads, 64 columns]: the rows of a box come token by token, the heads of
+// a token one behind the other.  128-byte swizzle.
+cudaError_t make_map_view(CUtensorMap* map, const dsv_view& v, int heads, int tokens, int d, int box_heads,
+                          int box_tok) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  cudaError_t e = get_encode(&enc);
+  if (e != cudaSuccess) return e;
+  // the stride of a dimension of one element is never used: any valid one will do
+  const long long hs = heads > 1 ? v.head_stride : d, ts = tokens > 1 ? v.token_stride : d;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+  cuuint64_t strides[2] = {(cuuint64_t)hs * 2, (cuuint64_t)ts * 2};
+  cuuint32_t box[3] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_tok};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, v.ptr, dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// A view's strides: multiples of 8 elements (16 bytes) below 2^38, at least d
+// along every dimension of more than one element.
+constexpr long long kMaxStride = 1LL << 38;
+bool stride_ok(long long stride, long long size, int d) {
+  return size <= 1 || (stride >= d && stride < kMaxStride && stride % 8 == 0);
+}
+// The rows of an output must not overlap: with the dimensions sorted by
+// stride, each stride spans the smaller dimensions.
+bool disjoint(const long long* stride, const long long* size, int n, int d) {
+  bool used[3] = {false, false, false};
+  long long span = d;
+  for (int k = 0; k < n; ++k) {
+    int at = -1;
+    for (int i = 0; i < n; ++i)
+      if (!used[i] && size[i] > 1 && (at < 0 || stride[i] < stride[at])) at = i;
+    if (at < 0) return true;
+    if (stride[at] < span) return false;
+    span = stride[at] * (size[at] - 1) + span;
+    used[at] = true;
+  }
+  return true;
+}
+bool view_ok(const dsv_view& v, long long heads, long long tokens, int d, bool output) {
+  if (!v.ptr || !al16(v.ptr)) return false;
+  if (!stride_ok(v.head_stride, heads, d) || !stride_ok(v.token_stride, tokens, d)) return false;
+  const long long st[2] = {v.head_stride, v.token_stride}, sz[2] = {heads, tokens};
+  return !output || disjoint(st, sz, 2, d);
+}
+bool view4_ok(const dsv_view& v, long long B, long long H, long long N, int d, bool output) {
+  if (!view_ok(v, H, N, d, false) || !stride_ok(v.batch_stride, B, d)) return false;
+  const long long st[3] = {v.batch_stride, v.head_stride, v.token_stride}, sz[3] = {B, H, N};
+  return !output || disjoint(st, sz, 3, d);
+}
+
+// The same rows as `a`, where both start at the same address.
+bool same_or_apart(const dsv_view& a, const dsv_view& b, long long B, long long H, long long N) {
+  if (a.ptr != b.ptr) return true;
+  return (B <= 1 || a.batch_stride == b.batch_stride) && (H <= 1 || a.head_stride == b.head_stride) &&
+         (N <= 1 || a.token_stride == b.token_stride);
+}
+
+// Packed attention: sizes, then whether a call has anything to do.
+dsv_status check_packed(const dsv_packed& p) {
+  if (p.S < 0 || p.H < 0 || p.Hkv < 0 || p.Tq < 0 || p.Tk < 0) return DSV_ERR_INVALID_ARG;
+  if (p.d != 64 && p.d != 128) return DSV_ERR_UNSUPPORTED;
+  if (p.H > kMaxHeads) return DSV_ERR_UNSUPPORTED;
+  if (p.H == 0 || p.S == 0) return DSV_OK;
+  if (p.Hkv == 0 || p.H % p.Hkv != 0) return DSV_ERR_INVALID_ARG;
+  if (p.H / p.Hkv > 128) return DSV_ERR_UNSUPPORTED;
+  // slots, work indexes and token coordinates stay inside 32 bits
+  const long long q = packed_slots(p.Tq, 128 / (p.H / p.Hkv), p.S), k = packed_slots(p.Tk, 128, p.S);
+  if ((long long)p.Tq + 128LL * p.S >= (1LL << 31) || (long long)p.Tk + 128LL * p.S >= (1LL << 31))
+    return DSV_ERR_UNSUPPORTED;
+  if (q * p.Hkv >= (1LL << 31) || k * p.Hkv >= (1LL << 31)) return DSV_ERR_UNSUPPORTED;
+  return DSV_OK;
+}
+bool no_queries(const dsv_packed& p) { return p.S == 0 || p.H == 0 || p.Tq == 0; }
+bool no_keys(const dsv_packed& p) { return p.S == 0 || p.H == 0 || p.Tk == 0; }
+float packed_scale(int d, float scale) { return (scale > 0.f && isfinite(scale)) ? scale : 1.0f / sqrtf((float)d); }
+
+dsv_status check_rope(const dsv_rope& r) {
+  if (r.B < 0 || r.H < 0 || r.N < 0) return DSV_ERR_INVALID_ARG;
+  if (r.d != 64 && r.d != 128) return DSV_ERR_UNSUPPORTED;
+  if (r.axes < 1 || r.axes > 4) return DSV_ERR_UNSUPPORTED;
+  int sum = 0;
+  for (int a = 0; a < r.axes; ++a) {
+    if (r.section[a] < 2 || r.section[a] > r.d || r.section[a] % 2 != 0) return DSV_ERR_INVALID_ARG;
+    sum += r.section[a];
+  }
+  if (sum > r.d) return DSV_ERR_INVALID_ARG;
+  if (!(r.theta >= 1.0) || !isfinite(r.theta)) return DSV_ERR_INVALID_ARG;
+  if (r.H > kMaxHeads || r.B > 65535) return DSV_ERR_UNSUPPORTED;
+  if ((long long)r.B * r.H * (r.N / 16 + 1) >= (1LL << 31)) return DSV_ERR_UNSUPPORTED;
+  return DSV_OK;
+}
+bool empty_rope(const dsv_rope& r) { return r.B == 0 || r.H == 0 || r.N == 0; }
+bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 bool empty(const dsv_shape& s) { return (long long)s.B * s.H * s.N == 0; }
 
 float resolve_scale(const dsv_shape& s, float scale) {
@@ -554,6 +652,129 @@ dsv_status dsv_attn_bwd_dq(const void* Q, const void* K, const void* V, const vo
     return DSV_ERR_CUDA;
   return from_cuda(launch_attn_bwd_q(tq, tk, tv, tdo, s, fwd_ptr, fwd_col, resolve_scale(s, softmax_scale), dQ,
                                      workspace, ctl, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t dsv_packed_attn_fwd_workspace_bytes(dsv_packed p) {
+  if (check_packed(p) != DSV_OK || no_queries(p) || no_keys(p)) return 0;
+  return packed_fwd_ws_bytes(p);
+}
+
+dsv_status dsv_packed_attn_fwd(dsv_view Q, dsv_view K, dsv_view V, dsv_packed p, const int32_t* q_ptr,
+                               const int32_t* k_ptr, int32_t causal, float softmax_scale, dsv_view O, float* lse,
+                               void* workspace, size_t workspace_bytes, dsv_stream_t stream) {
+  dsv_status v = check_packed(p);
+  if (v != DSV_OK) return v;
+  if (causal != 0 && causal != 1) return DSV_ERR_INVALID_ARG;
+  if (no_queries(p)) return DSV_OK;
+  if (!q_ptr || !k_ptr || !lse || !al4(q_ptr) || !al4(k_ptr) || !al4(lse)) return DSV_ERR_INVALID_ARG;
+  if (!view_ok(Q, p.H, p.Tq, p.d, false) || !view_ok(O, p.H, p.Tq, p.d, true)) return DSV_ERR_INVALID_ARG;
+  if (!no_keys(p) && (!view_ok(K, p.Hkv, p.Tk, p.d, false) || !view_ok(V, p.Hkv, p.Tk, p.d, false)))
+    return DSV_ERR_INVALID_ARG;
+  if (O.ptr == Q.ptr || O.ptr == K.ptr || O.ptr == V.ptr) return DSV_ERR_INVALID_ARG;
+  const size_t need = dsv_packed_attn_fwd_workspace_bytes(p);
+  if (need > 0 && (!workspace || !al256(workspace) || workspace_bytes < need)) return DSV_ERR_INVALID_ARG;
+  Ctl ctl;
+  if (current_ctl(&ctl) != cudaSuccess) return DSV_ERR_CUDA;
+  const int group = p.H / p.Hkv;
+  CUtensorMap tq, tk, tv;
+  if (make_map_view(&tq, Q, p.H, p.Tq, p.d, group, 128 / group) != cudaSuccess) return DSV_ERR_CUDA;
+  if (no_keys(p)) {
+    tk = tv = tq;                          // never loaded: no row has a key tile
+  } else if (make_map_view(&tk, K, p.Hkv, p.Tk, p.d, 1, 128) != cudaSuccess ||
+             make_map_view(&tv, V, p.Hkv, p.Tk, p.d, 1, 128) != cudaSuccess) {
+    return DSV_ERR_CUDA;
+  }
+  return from_cuda(launch_packed_fwd(tq, tk, tv, p, q_ptr, k_ptr, causal, packed_scale(p.d, softmax_scale), O, lse,
+                                     workspace, ctl, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t dsv_packed_attn_bwd_workspace_bytes(dsv_packed p) {
+  if (check_packed(p) != DSV_OK || no_queries(p)) return 0;
+  return packed_bwd_ws_bytes(p);
+}
+
+dsv_status dsv_packed_attn_bwd(dsv_view Q, dsv_view K, dsv_view V, dsv_view O, dsv_view dO, const float* lse,
+                               dsv_packed p, const int32_t* q_ptr, const int32_t* k_ptr, int32_t causal,
+                               float softmax_scale, dsv_view dQ, dsv_view dK, dsv_view dV, void* workspace,
+                               size_t workspace_bytes, dsv_stream_t stream) {
+  dsv_status v = check_packed(p);
+  if (v != DSV_OK) return v;
+  if (causal != 0 && causal != 1) return DSV_ERR_INVALID_ARG;
+  const bool nq = no_queries(p), nk = no_keys(p);
+  if (nq && nk) return DSV_OK;
+  if (!q_ptr || !k_ptr || !al4(q_ptr) || !al4(k_ptr)) return DSV_ERR_INVALID_ARG;
+  if (!nq) {
+    if (!lse || !al4(lse)) return DSV_ERR_INVALID_ARG;
+    if (!view_ok(Q, p.H, p.Tq, p.d, false) || !view_ok(O, p.H, p.Tq, p.d, false) ||
+        !view_ok(dO, p.H, p.Tq, p.d, false) || !view_ok(dQ, p.H, p.Tq, p.d, true))
+      return DSV_ERR_INVALID_ARG;
+  }
+  if (!nk && (!view_ok(K, p.Hkv, p.Tk, p.d, false) || !view_ok(V, p.Hkv, p.Tk, p.d, false) ||
+              !view_ok(dK, p.Hkv, p.Tk, p.d, true) || !view_ok(dV, p.Hkv, p.Tk, p.d, true)))
+    return DSV_ERR_INVALID_ARG;
+  const void* const in[5] = {Q.ptr, K.ptr, V.ptr, O.ptr, dO.ptr};
+  const void* const res[3] = {dQ.ptr, dK.ptr, dV.ptr};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 5; ++j)
+      if (res[i] && res[i] == in[j]) return DSV_ERR_INVALID_ARG;
+    if (res[i] && res[i] == res[(i + 1) % 3]) return DSV_ERR_INVALID_ARG;
+  }
+  const size_t need = dsv_packed_attn_bwd_workspace_bytes(p);
+  if (need > 0 && (!workspace || !al256(workspace) || workspace_bytes < need)) return DSV_ERR_INVALID_ARG;
+  Ctl ctl;
+  if (current_ctl(&ctl) != cudaSuccess) return DSV_ERR_CUDA;
+  const int group = p.H / p.Hkv;
+  PackedMaps m;
+  if (!nq && (make_map_view(&m.Q, Q, p.H, p.Tq, p.d, group, 128 / group) != cudaSuccess ||
+              make_map_view(&m.dO, dO, p.H, p.Tq, p.d, group, 128 / group) != cudaSuccess))
+    return DSV_ERR_CUDA;
+  if (!nk && (make_map_view(&m.K, K, p.Hkv, p.Tk, p.d, 1, 128) != cudaSuccess ||
+              make_map_view(&m.V, V, p.Hkv, p.Tk, p.d, 1, 128) != cudaSuccess))
+    return DSV_ERR_CUDA;
+  // a side without tokens is never loaded
+  if (nq) m.Q = m.dO = m.K;
+  if (nk) m.K = m.V = m.Q;
+  return from_cuda(launch_packed_bwd(m, p, q_ptr, k_ptr, causal, packed_scale(p.d, softmax_scale), O, dO, lse, dQ, dK,
+                                     dV, workspace, ctl, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dsv_status dsv_rope_axes_fwd(dsv_view x, const int32_t* pos, int64_t pos_batch_stride, dsv_rope r,
+                             const float* weight, float eps, dsv_view y, dsv_stream_t stream) {
+  dsv_status v = check_rope(r);
+  if (v != DSV_OK) return v;
+  if (weight && (!(eps > 0.f) || !isfinite(eps) || !al4(weight))) return DSV_ERR_INVALID_ARG;
+  if (empty_rope(r)) return DSV_OK;
+  if (!pos || !al4(pos) || pos_batch_stride < 0) return DSV_ERR_INVALID_ARG;
+  if (!view4_ok(x, r.B, r.H, r.N, r.d, false) || !view4_ok(y, r.B, r.H, r.N, r.d, true)) return DSV_ERR_INVALID_ARG;
+  if (!same_or_apart(x, y, r.B, r.H, r.N)) return DSV_ERR_INVALID_ARG;
+  return from_cuda(launch_rope_fwd(x, pos, pos_batch_stride, r, weight, eps, y, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t dsv_rope_axes_bwd_workspace_bytes(dsv_rope r) {
+  if (check_rope(r) != DSV_OK || empty_rope(r)) return 0;
+  return rope_bwd_ws_bytes(r);
+}
+
+dsv_status dsv_rope_axes_bwd(dsv_view dy, dsv_view x, const int32_t* pos, int64_t pos_batch_stride, dsv_rope r,
+                             const float* weight, float eps, dsv_view dx, float* dweight, void* workspace,
+                             size_t workspace_bytes, dsv_stream_t stream) {
+  dsv_status v = check_rope(r);
+  if (v != DSV_OK) return v;
+  if (weight && (!(eps > 0.f) || !isfinite(eps) || !al4(weight) || !dweight || !al4(dweight)))
+    return DSV_ERR_INVALID_ARG;
+  if (empty_rope(r)) {                     // no rows: the sum over them is zero
+    if (!weight) return DSV_OK;
+    return from_cuda(cudaMemsetAsync(dweight, 0, (size_t)r.d * sizeof(float), reinterpret_cast<cudaStream_t>(stream)));
+  }
+  if (!pos || !al4(pos) || pos_batch_stride < 0) return DSV_ERR_INVALID_ARG;
+  if (!view4_ok(dy, r.B, r.H, r.N, r.d, false) || !view4_ok(dx, r.B, r.H, r.N, r.d, true)) return DSV_ERR_INVALID_ARG;
+  if (!same_or_apart(dy, dx, r.B, r.H, r.N)) return DSV_ERR_INVALID_ARG;
+  if (weight) {
+    if (!view4_ok(x, r.B, r.H, r.N, r.d, false) || !same_or_apart(x, dx, r.B, r.H, r.N)) return DSV_ERR_INVALID_ARG;
+    if (!workspace || !al256(workspace) || workspace_bytes < rope_bwd_ws_bytes(r)) return DSV_ERR_INVALID_ARG;
+  }
+  return from_cuda(launch_rope_bwd(dy, x, pos, pos_batch_stride, r, weight, eps, dx, dweight, workspace,
+                                   reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -473,6 +473,9 @@ enum : unsigned int {
   KID_BWD_KV = 2,
   KID_BWD_Q = 3,
   KID_MAXPOOL = 5,
+  KID_PACKED_FWD = 6,
+  KID_PACKED_KV = 7,
+  KID_PACKED_Q = 8,
 };
 
 }  // namespace dsv

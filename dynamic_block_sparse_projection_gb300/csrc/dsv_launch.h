@@ -102,6 +102,35 @@ size_t attn_bwd_ws_bytes(const dsv_shape& s);
 cudaError_t launch_cube_permute(const void* src, void* dst, const dsv_shape& s, int T, int Hl, int Wl, int ct, int cy,
                                 int cx, int inverse, cudaStream_t st);
 
+// Rotary positions with several axes, optionally behind an RMS norm (rope.cu).
+// dw (and ws) only with a weight.
+constexpr int kRopeParts = 1216;              // partial sums of the weight's gradient: 8 CTAs on each of 152 SMs
+cudaError_t launch_rope_fwd(const dsv_view& x, const int32_t* pos, int64_t pos_batch, const dsv_rope& r,
+                            const float* weight, float eps, const dsv_view& y, cudaStream_t st);
+cudaError_t launch_rope_bwd(const dsv_view& dy, const dsv_view& x, const int32_t* pos, int64_t pos_batch,
+                            const dsv_rope& r, const float* weight, float eps, const dsv_view& dx, float* dw, void* ws,
+                            cudaStream_t st);
+size_t rope_bwd_ws_bytes(const dsv_rope& r);
+
+// Attention of packed sequences (packed_fwd.cu, packed_bwd.cu).
+constexpr int kPackedSMs = 152;               // what the split rules and head chunks are sized for
+constexpr int kPackedMinPart = 4;             // fewest key tiles of one part of a split query tile
+// Tile slots of T tokens in S sequences (packed.cuh).
+inline long long packed_slots(int T, int tile, int S) { return (long long)T / tile + S; }
+struct PackedMaps {
+  CUtensorMap Q, K, V, dO;
+};
+cudaError_t launch_packed_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                              const dsv_packed& p, const int32_t* q_ptr, const int32_t* k_ptr, int causal, float scale,
+                              const dsv_view& O, float* lse, void* ws, const Ctl& ctl, cudaStream_t st);
+int packed_fwd_splits(const dsv_packed& p);
+size_t packed_fwd_ws_bytes(const dsv_packed& p);
+cudaError_t launch_packed_bwd(const PackedMaps& m, const dsv_packed& p, const int32_t* q_ptr, const int32_t* k_ptr,
+                              int causal, float scale, const dsv_view& O, const dsv_view& dO, const float* lse,
+                              const dsv_view& dQ, const dsv_view& dK, const dsv_view& dV, void* ws, const Ctl& ctl,
+                              cudaStream_t st);
+size_t packed_bwd_ws_bytes(const dsv_packed& p);
+
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace dsv

@@ -1,0 +1,927 @@
+// packed_bwd.cu — gradient of the packed-sequence attention, without atomics.
+//
+// With P_ij = exp(s_ij - lse_i) over the pairs that the forward's mask leaves:
+//   D_i  = sum_c dO_ic O_ic,   dS_ij = P_ij (dO_i . v_j - D_i)
+//   dV_j = sum_i P_ij dO_i,  dK_j = scale sum_i dS_ij q_i   (i over every query
+//          head that shares the key head),  dQ_i = scale sum_j dS_ij k_j
+//
+// The dense companion of attn_bwd.cu, with its two kernels and their pipelines
+// over packed.cuh's tiles (a query tile's rows are tokens x shared heads):
+//   prepare  D_i and -lse_i log2(e) into 128-row slots, one per query tile.  A
+//            row that saw no key (lse = -inf), and a row behind the tile's
+//            tokens, gets -inf there, so its P is exp2(-inf) = 0.
+//   kv       one CTA per key tile and key head, over the sequence's query
+//            tiles: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.
+//            Shared heads add up inside the product, so nothing is reduced
+//            afterwards and every output tile has one writer.
+//   q        persistent CTAs over the query tiles: S = Q K^T, dP = dO V^T,
+//            dQ += dS K.
+// S and dP are computed twice (seven products per tile pair instead of five),
+// which buys results that do not depend on the order CTAs run in.
+//
+// Rows of a tile that belong to no token of it are other sequences' data.  As
+// rows of the A operands they only reach accumulator rows that are not stored;
+// as rows of the B operands they would meet a zero of P or dS, and 0 * NaN is
+// not 0, so the last query tile of a sequence (kv) and its last key tile (q,
+// K only) are zeroed from the end on in shared memory before the MMAs see them.
+#include <math.h>
+
+#include "packed.cuh"
+
+namespace dsv {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kKVThreads = 320;        // producer, MMA issuer, 8 compute warps
+constexpr int kQVWarp = 10;            // q kernel: V producer, which also finds the work items
+constexpr int kQThreads = 352;
+constexpr int kComputeThreads = 256;
+
+// ---------------------------------------------------------------------------
+// D_i and -lse_i log2(e), 128 rows per query tile
+// ---------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(256) packed_bwd_prep_kernel(const __grid_constant__ PackedGeom g,
+                                                              const __nv_bfloat16* O, long long o_head,
+                                                              long long o_tok, const __nv_bfloat16* dO,
+                                                              long long d_head, long long d_tok,
+                                                              const float* __restrict__ lse, float* __restrict__ Dw,
+                                                              float* __restrict__ L2w, Ctl ctl) {
+  constexpr int TPR = D / 8;             // threads per row, 16 bytes each
+  constexpr int RPC = 256 / TPR;         // rows per pass
+  const int slot = blockIdx.x, kvh = blockIdx.y;
+  if (slot == 0 && kvh == 0 && threadIdx.x < 32) packed_check_ptrs(g, ctl, threadIdx.x);
+  PackedSeq q;
+  if (!packed_find(g, g.q_ptr, g.TQ, slot, q)) return;
+  const int t0 = (slot - (q.q0 / g.TQ + q.s)) * g.TQ;
+  if (t0 >= q.lq) return;
+  const int rows = min(g.TQ, q.lq - t0) * g.group;
+  const int c = threadIdx.x % TPR;
+  const long long base = ((long long)kvh * g.nslot_q + slot) * 128;
+#pragma unroll 4
+  for (int r = threadIdx.x / TPR; r < 128; r += RPC) {
+    const int rt = r / g.group, head = kvh * g.group + (r - rt * g.group);
+    const long long tok = (long long)q.q0 + t0 + rt;
+    float acc = 0.f;
+    if (r < rows) {
+      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(O + head * o_head + tok * o_tok) + c);
+      const uint4 b = __ldcs(reinterpret_cast<const uint4*>(dO + head * d_head + tok * d_tok) + c);
+      const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc = fmaf(__uint_as_float(wa[i] << 16), __uint_as_float(wb[i] << 16), acc);
+        acc = fmaf(__uint_as_float(wa[i] & 0xFFFF0000u), __uint_as_float(wb[i] & 0xFFFF0000u), acc);
+      }
+    }
+#pragma unroll
+    for (int o = TPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (c == 0) {
+      const float L = r < rows ? lse[(long long)head * g.Tq + tok] : -INFINITY;
+      Dw[base + r] = r < rows ? acc : 0.f;
+      L2w[base + r] = L == -INFINITY ? -INFINITY : -L * kLog2e;
+    }
+  }
+}
+
+enum : unsigned int {
+  W_KV = 1, W_GFULL, W_GEMPTY, W_S, W_P, W_ACC, W_DRAIN, W_KFULL, W_VFULL, W_KVEMPTY, W_SPFREE, W_DSFULL, W_DSEMPTY,
+  W_ITEM, W_ITEMFREE, W_TAIL
+};
+
+// ---------------------------------------------------------------------------
+// dK, dV: one CTA per key tile and key head
+// ---------------------------------------------------------------------------
+template <int D>
+struct PKVTraits {
+  static constexpr int NCH = D / 64;
+  static constexpr int CHUNK = 128 * 128;
+  static constexpr int TILE = NCH * CHUNK;
+  static constexpr int NST = 2;
+  static constexpr int VEC_BYTES = 128 * 4;                    // -lse2 or D of a query tile
+  static constexpr int STAGE_BYTES = (2 * TILE + 2 * VEC_BYTES + 1023) / 1024 * 1024;
+  static constexpr int NBAR = 1 + 2 * NST + 7 + 1;
+  static constexpr int SMEM_USED = 1024 + 2 * TILE + NST * STAGE_BYTES + NBAR * 8 + 16;
+  static_assert(SMEM_USED <= 227 * 1024, "dK/dV tiles exceed shared memory");
+  static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
+  // TMEM: S^T at 0, dP^T at 128, dV at 256, dK at 256 + D; P^T and dS^T (bf16
+  // pairs) go over the columns they were read from, each warp half hf packing
+  // its 64 queries into its first 32 columns, handed over in two chunks.
+  static constexpr uint32_t S_COL = 0, DP_COL = 128, DV_COL = 256, DK_COL = 256 + D, TMEM_COLS = 512;
+  static constexpr int W = 64;                                  // columns per compute warp
+  __host__ __device__ static constexpr uint32_t packed_col(int q) { return (uint32_t)((q / W) * W + (q % W) / 2); }
+  __host__ __device__ static constexpr int chunk_of(int q) { return (q % W) / (W / 2); }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kKVThreads, 1)
+    packed_bwd_kv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
+                         const __grid_constant__ PackedGeom g, const float* __restrict__ L2w,
+                         const float* __restrict__ Dw, float scale, __nv_bfloat16* dK, long long dk_head,
+                         long long dk_tok, __nv_bfloat16* dV, long long dv_head, long long dv_tok, Ctl ctl) {
+  using T = PKVTraits<D>;
+  constexpr int NST = T::NST;
+  constexpr int W = T::W;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+
+  // the CTA's key tile; every thread works it out (the same loads for all)
+  int kvh, slot;
+  packed_order(g, g.nslot_k, false, blockIdx.x, kvh, slot);
+  PackedSeq q;
+  if (!packed_find(g, g.k_ptr, 128, slot, q)) return;
+  const int kt0 = (slot - (q.k0 / 128 + q.s)) * 128;          // first key of the tile inside its sequence
+  if (kt0 >= q.lk) return;
+  const int keys = min(128, q.lk - kt0);
+  // query token t sees key k when k <= t + off (causal)
+  const int off = q.lk - q.lq;
+  const int qtiles = (q.lq + g.TQ - 1) / g.TQ;
+  const long long t_first = g.causal ? min((long long)q.lq, max(0LL, (long long)kt0 - off)) : 0;
+  const int i0 = (int)t_first / g.TQ;                         // first query tile that sees key kt0
+  const int cnt = max(0, qtiles - i0);
+  const int qslot0 = q.q0 / g.TQ + q.s + i0;
+
+  uint8_t* sbase = smem_align1024(smem_raw);
+  uint8_t* sK = sbase;
+  uint8_t* sV = sK + T::TILE;
+  uint8_t* sStage = sV + T::TILE;                 // NST x [Q | dO | lse2 | D]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sStage + NST * T::STAGE_BYTES);
+  uint64_t* kv_full = bars;
+  uint64_t* g_full = bars + 1;
+  uint64_t* g_empty = g_full + NST;
+  uint64_t* s_full = g_empty + NST;               // S^T in TMEM
+  uint64_t* dp_full = s_full + 1;                 // dP^T in TMEM
+  uint64_t* p_full = dp_full + 1;                 // [2] P^T chunk written back (bf16)
+  uint64_t* ds_full = p_full + 2;                 // [2] dS^T chunk written back (bf16)
+  uint64_t* acc_done = ds_full + 2;
+  uint64_t* g_tail = acc_done + 1;                // the sequence's last query tile, before its rows are cut
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(g_tail + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned int kid = (unsigned int)KID_PACKED_KV << 8;
+  const long long krow0 = (long long)q.k0 + kt0;
+
+  if (cnt == 0) {                                 // no query sees these keys
+    for (int i = threadIdx.x; i < keys * (D / 8); i += blockDim.x) {
+      const int r = i / (D / 8), c = i % (D / 8);
+      *reinterpret_cast<uint4*>(dK + kvh * dk_head + (krow0 + r) * dk_tok + c * 8) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(dV + kvh * dv_head + (krow0 + r) * dv_tok + c * 8) = make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+
+  const int box = g.group * g.TQ;                 // rows a query tile's copy brings
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&g_full[s], 1);
+      mbar_init(&g_empty[s], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    for (int c = 0; c < 2; ++c) {
+      mbar_init(&p_full[c], kComputeThreads);
+      mbar_init(&ds_full[c], kComputeThreads);
+    }
+    mbar_init(acc_done, 1);
+    mbar_init(g_tail, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (box < 128 && warp >= 2 && warp < 2 + 2 * NST) {
+    // rows box..127 of every query tile are never loaded
+    const int w = warp - 2;
+    zero_tile_rows(sStage + (w >> 1) * T::STAGE_BYTES + (w & 1) * T::TILE, T::NCH, box, lane);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, T::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // one CTA owns the SM's whole TMEM, so its addresses start at 0 (attn_fwd.cu)
+  const uint32_t tmem_base = *tmem_slot;
+  constexpr uint32_t tmem = 0;
+
+  if (tmem_base != tmem) {
+    if (threadIdx.x == 0) set_error(ctl, DSV_ERR_INTERNAL, blockIdx.x);
+  } else if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      tma_prefetch_desc(&tmdO);
+      mbar_arrive_expect_tx(kv_full, 2 * T::TILE);
+      for (int c = 0; c < T::NCH; ++c) {
+        tma_load_3d(sK + c * T::CHUNK, &tmK, kv_full, c * 64, kvh, (int)krow0);
+        tma_load_3d(sV + c * T::CHUNK, &tmV, kv_full, c * 64, kvh, (int)krow0);
+      }
+    }
+    int issued = 0;
+    for (int n = 0; n < cnt; ++n) {
+      const int s = n % NST;
+      if (!mbar_wait_warp(&g_empty[s], ((uint32_t)(n / NST) & 1u) ^ 1u, abort_flag, ctl, kid | W_GEMPTY)) break;
+      const int t0 = (i0 + n) * g.TQ;
+      const int rows = min(g.TQ, q.lq - t0) * g.group;
+      const bool tail = rows < box;
+      uint64_t* bar = tail ? g_tail : &g_full[s];
+      uint8_t* st = sStage + s * T::STAGE_BYTES;
+      if (lane == 0) {
+        const long long vec = ((long long)kvh * g.nslot_q + qslot0 + n) * 128;
+        mbar_arrive_expect_tx(bar, 2 * (uint32_t)box * D * 2 + 2 * T::VEC_BYTES);
+        for (int c = 0; c < T::NCH; ++c) {
+          tma_load_3d(st + c * T::CHUNK, &tmQ, bar, c * 64, kvh * g.group, q.q0 + t0);
+          tma_load_3d(st + T::TILE + c * T::CHUNK, &tmdO, bar, c * 64, kvh * g.group, q.q0 + t0);
+        }
+        bulk_load(st + 2 * T::TILE, L2w + vec, T::VEC_BYTES, bar);
+        bulk_load(st + 2 * T::TILE + T::VEC_BYTES, Dw + vec, T::VEC_BYTES, bar);
+      }
+      if (tail) {
+        if (!mbar_wait_warp(g_tail, 0, nullptr, ctl, kid | W_TAIL)) {
+          *abort_flag = 1;
+          break;
+        }
+        zero_tile_rows(st, T::NCH, rows, lane);
+        zero_tile_rows(st + T::TILE, T::NCH, rows, lane);
+        if (lane == 0) mbar_arrive(&g_full[s]);
+      }
+      issued = n + 1;
+    }
+    // every copy this warp started must land before the CTA exits
+    mbar_wait(kv_full, 0, nullptr, ctl, kid | W_DRAIN);
+    for (int n = (issued > NST ? issued - NST : 0); n < issued; ++n)
+      mbar_wait(&g_full[n % NST], (uint32_t)(n / NST) & 1u, nullptr, ctl, kid | W_DRAIN);
+  } else if (warp == 1) {
+    // ---------------- MMA issuer (whole warp, one elected lane issues) ----------------
+    // Order, as in attn_bwd.cu: S^T(0), dP^T(0), then per query tile n
+    //   dV(n) [P^T(n) written], S^T(n+1), dK(n) [dS^T(n) written], dP^T(n+1),
+    // so the tensor core runs the next tile's products while the compute warps
+    // convert; each barrier is tested half-way through the products before it.
+    constexpr uint32_t ID_S = idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t ID_G = idesc_bf16_f32(128, D, false, true);
+    const uint64_t dK0 = sdesc_sw128(smem_u32(sK), 16, 1024);
+    const uint64_t dV0 = sdesc_sw128(smem_u32(sV), 16, 1024);
+    const uint64_t dS0 = sdesc_sw128(smem_u32(sStage), 16, 1024);          // K-major view of a stage
+    const uint64_t dSmn0 = sdesc_sw128(smem_u32(sStage), T::CHUNK, 1024);  // MN-major view
+    // S^T = K Q^T (t = 0) or dP^T = V dO^T (t = 1); returns the test of `probe`
+    auto issue_sdp = [&](int n, int t, uint64_t* probe, uint32_t probe_par) -> uint32_t {
+      const uint64_t a0 = t ? dV0 : dK0;
+      const uint64_t b0 = desc_off(dS0, (uint32_t)((n % NST) * T::STAGE_BYTES + t * T::TILE));
+      uint32_t r = 0u;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t o = (kk >> 2) * T::CHUNK + (kk & 3) * 32;
+        mma_ss_w(tmem + (t ? T::DP_COL : T::S_COL), desc_off(a0, o), desc_off(b0, o), ID_S, kk > 0 ? 1u : 0u);
+        if (kk == D / 32 - 1 && probe != nullptr) r = mbar_test(probe, probe_par);
+      }
+      mma_commit_w(t ? dp_full : s_full);
+      return r;
+    };
+    // chunk c of dV += P^T dO (t = 0) or dK += dS^T Q (t = 1); returns the test of `probe`
+    auto issue_grad = [&](int n, int t, int c, uint64_t* probe, uint32_t probe_par) -> uint32_t {
+      const uint64_t b0 = desc_off(dSmn0, (uint32_t)((n % NST) * T::STAGE_BYTES + (t ? 0 : T::TILE)));
+      uint32_t r = 0u;
+      int m = 0;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        if (T::chunk_of(kk * 16) != c) continue;
+        mma_ts_w(tmem + (t ? T::DK_COL : T::DV_COL), tmem + (t ? T::DP_COL : T::S_COL) + T::packed_col(kk * 16),
+                 desc_off(b0, kk * 16 * 128), ID_G, (n > 0 || kk > 0) ? 1u : 0u);
+        if (++m == 2 && probe != nullptr) r = mbar_test(probe, probe_par);
+      }
+      return r;
+    };
+    bool ok = mbar_wait_warp(kv_full, 0, abort_flag, ctl, kid | W_KV) &&
+              mbar_wait_warp(&g_full[0], 0, abort_flag, ctl, kid | W_GFULL);
+    uint32_t tp0 = 0u;
+    if (ok) {
+      tc_fence_after();
+      issue_sdp(0, 0, nullptr, 0u);
+      tp0 = issue_sdp(0, 1, &p_full[0], 0u);
+    }
+    for (int n = 0; ok && n < cnt; ++n) {
+      const bool more = n + 1 < cnt;
+      const uint32_t par = (uint32_t)n & 1u;
+      const uint32_t tg = more ? mbar_test(&g_full[(n + 1) % NST], (uint32_t)((n + 1) / NST) & 1u) : 0u;
+      if (!mbar_wait_warp_tested(&p_full[0], par, tp0, abort_flag, ctl, kid | W_P)) break;
+      tc_fence_after();
+      const uint32_t tp1 = issue_grad(n, 0, 0, &p_full[1], par);
+      if (!mbar_wait_warp_tested(&p_full[1], par, tp1, abort_flag, ctl, kid | W_P)) break;
+      tc_fence_after();
+      issue_grad(n, 0, 1, nullptr, 0u);
+      uint32_t td0 = 0u;
+      if (more) {
+        if (!mbar_wait_warp_tested(&g_full[(n + 1) % NST], (uint32_t)((n + 1) / NST) & 1u, tg, abort_flag, ctl,
+                                   kid | W_GFULL))
+          break;
+        tc_fence_after();
+        td0 = issue_sdp(n + 1, 0, &ds_full[0], par);
+      }
+      if (!mbar_wait_warp_tested(&ds_full[0], par, td0, abort_flag, ctl, kid | W_DSFULL)) break;
+      tc_fence_after();
+      const uint32_t td1 = issue_grad(n, 1, 0, &ds_full[1], par);
+      if (!mbar_wait_warp_tested(&ds_full[1], par, td1, abort_flag, ctl, kid | W_DSFULL)) break;
+      tc_fence_after();
+      issue_grad(n, 1, 1, nullptr, 0u);
+      mma_commit_w(&g_empty[n % NST]);
+      if (more) tp0 = issue_sdp(n + 1, 1, &p_full[0], par ^ 1u);
+    }
+    mma_commit_w(acc_done);
+    mbar_wait_warp(acc_done, 0, nullptr, ctl, kid | W_DRAIN);
+  } else {
+    // ------------- compute warps: key row kr, 64 rows of the query tile -------------
+    const int sp = warp & 3;
+    const int hf = (warp - 2) >> 2;
+    const int kr = sp * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(sp * 32) << 16;
+    const float scale_log2 = scale * kLog2e;
+    const uint64_t c2 = f2_pack(scale_log2, scale_log2);
+    const uint32_t cs = tmem + lane_off + T::S_COL + hf * W;
+    const uint32_t cp = tmem + lane_off + T::DP_COL + hf * W;
+    const int q0 = hf * W;                         // first tile row of this warp's columns
+    bool ok = true;
+    for (int n = 0; ok && n < cnt; ++n) {
+      const int s = n % NST;
+      if (!mbar_wait_warp(&g_full[s], (uint32_t)(n / NST) & 1u, abort_flag, ctl, kid | W_GFULL) ||
+          !mbar_wait_warp(s_full, (uint32_t)n & 1u, abort_flag, ctl, kid | W_S)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const float4* l4 = reinterpret_cast<const float4*>(sStage + s * T::STAGE_BYTES + 2 * T::TILE) + q0 / 4;
+      const float4* d4 = l4 + 32;
+      // causal: tile row q sees this thread's key from q >= lo on (tokens in order, heads inside a token)
+      const int first = (i0 + n) * g.TQ + off;     // last key that the tile's first token sees
+      const bool mask = g.causal && first < kt0 + 127;
+      const int lo = mask ? (kt0 + kr - first) * g.group - q0 : 0;
+      uint32_t x[W];
+      uint64_t p2[W / 2];                          // P^T of this row's 64 queries, fp32 pairs
+      tmem_ld_w<W>(cs, x);
+      tmem_ld_wait();
+      if (mask) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) x[i] = i >= lo ? x[i] : 0xff800000u;   // -inf: P = 0
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t pw[W / 4];
+#pragma unroll
+        for (int qq = c * (W / 8); qq < (c + 1) * (W / 8); ++qq) {
+          const float4 L = l4[qq];                 // -lse*log2(e) of four queries
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int j0 = 4 * qq + 2 * e;
+            float x0, x1;
+            f2_unpack(fma2(f2_pack(__uint_as_float(x[j0]), __uint_as_float(x[j0 + 1])), c2,
+                           e ? f2_pack(L.z, L.w) : f2_pack(L.x, L.y)), x0, x1);
+            const float a = ex2(x0), b = ex2(x1);
+            p2[2 * qq + e] = f2_pack(a, b);
+            pw[2 * qq + e - c * (W / 4)] = pack_bf16x2(a, b);
+          }
+        }
+        // each warp overwrites only the TMEM lanes and columns it has read
+        tmem_st_w<W / 4>(cs + c * (W / 4), pw);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_full[c]);
+      }
+      if (!mbar_wait_warp(dp_full, (uint32_t)n & 1u, abort_flag, ctl, kid | W_S)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      tmem_ld_w<W>(cp, x);
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t dw[W / 4];
+#pragma unroll
+        for (int qq = c * (W / 8); qq < (c + 1) * (W / 8); ++qq) {
+          const float4 Dd = d4[qq];                // D of four queries
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int j0 = 4 * qq + 2 * e;
+            const uint64_t t = sub2(f2_pack(__uint_as_float(x[j0]), __uint_as_float(x[j0 + 1])),
+                                    e ? f2_pack(Dd.z, Dd.w) : f2_pack(Dd.x, Dd.y));
+            float d0, d1;
+            f2_unpack(mul2(p2[2 * qq + e], t), d0, d1);
+            dw[2 * qq + e - c * (W / 4)] = pack_bf16x2(d0, d1);
+          }
+        }
+        tmem_st_w<W / 4>(cp + c * (W / 4), dw);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&ds_full[c]);
+      }
+    }
+    if (ok) ok = mbar_wait_warp(acc_done, 0, abort_flag, ctl, kid | W_ACC);
+    if (ok) {
+      tc_fence_after();
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t col = (t == 0 ? T::DV_COL : T::DK_COL) + hf * (D / 2);
+        const float mul = t == 0 ? 1.0f : scale;
+        __nv_bfloat16* outp = (t == 0 ? dV + kvh * dv_head + (krow0 + kr) * dv_tok
+                                      : dK + kvh * dk_head + (krow0 + kr) * dk_tok) + hf * (D / 2);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tmem + lane_off + col + c * 32, o);
+          tmem_ld_wait();
+          if (kr < keys) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              w[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * mul, __uint_as_float(o[2 * i + 1]) * mul);
+            uint4* dst = reinterpret_cast<uint4*>(outp + c * 32);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) dst[p] = make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, T::TMEM_COLS);
+}
+
+// ---------------------------------------------------------------------------
+// dQ: persistent CTAs over the query tiles
+// ---------------------------------------------------------------------------
+struct QItem {
+  int valid;
+  int kvh;
+  int tok;      // first query token of the tile (absolute)
+  int ntok;
+  int key0;     // first key (absolute)
+  int nt;       // key tiles
+  int lim0;     // keys that the first token sees (may be <= 0)
+  int left;     // keys of the sequence
+  int slot;     // query slot: rows of D and -lse2
+  int pad;
+};
+
+template <int D>
+struct PQTraits {
+  static constexpr int NCH = D / 64;
+  static constexpr int CHUNK = 128 * 128;
+  static constexpr int TILE = NCH * CHUNK;
+  // K_j is read by S (early) and by dQ (late); V_j only by dP: separate rings
+  static constexpr int NK = 3;
+  static constexpr int NV = (8 * TILE + 2048 <= 227 * 1024) ? 3 : 2;
+  static constexpr int NBAR = 1 + 2 * NK + 2 * NV + 8 + 4;
+  static constexpr int SMEM_USED = 1024 + 2 * TILE + (NK + NV) * TILE + NBAR * 8 + 16 + 2 * (int)sizeof(QItem);
+  static_assert(SMEM_USED <= 227 * 1024, "dQ tiles exceed shared memory");
+  static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
+  static constexpr uint32_t S_COL = 0, DP_COL = 128, DQ_COL = 256, DS_COL = 256 + D, TMEM_COLS = 512;
+  static constexpr uint32_t TX = 128 * D * 2;
+  static constexpr int HALF = 64;
+  static constexpr int CONSUMERS = 10;            // warps 0..9 read each item
+};
+
+template <int D>
+__global__ void __launch_bounds__(kQThreads, 1)
+    packed_bwd_q_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
+                        const __grid_constant__ PackedGeom g, const float* __restrict__ L2w,
+                        const float* __restrict__ Dw, long long total, float scale, __nv_bfloat16* dQ,
+                        long long dq_head, long long dq_tok, Ctl ctl) {
+  using T = PQTraits<D>;
+  constexpr int NK = T::NK, NV = T::NV;
+  constexpr int HALF = T::HALF;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sbase = smem_align1024(smem_raw);
+  uint8_t* sdO = sbase;
+  uint8_t* sQ = sdO + T::TILE;
+  uint8_t* sK = sQ + T::TILE;
+  uint8_t* sV = sK + NK * T::TILE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + NV * T::TILE);
+  uint64_t* qd_full = bars;                       // Q and dO landed in smem
+  uint64_t* k_full = bars + 1;
+  uint64_t* k_empty = k_full + NK;
+  uint64_t* v_full = k_empty + NK;
+  uint64_t* v_empty = v_full + NV;
+  uint64_t* s_full = v_empty + NV;
+  uint64_t* sp_free = s_full + 1;                 // compute threads have read S, dP
+  uint64_t* ds_full = sp_free + 1;
+  uint64_t* ds_empty = ds_full + 1;
+  uint64_t* acc_done = ds_empty + 1;              // dQ of the current tile is complete
+  uint64_t* mma_drain = acc_done + 1;
+  uint64_t* qd_free = mma_drain + 1;              // the current tile's last dP product is done
+  uint64_t* k_tail = qd_free + 1;                 // the last K tile of a sequence, before its rows are cut
+  uint64_t* item_full = k_tail + 1;               // [2]
+  uint64_t* item_free = item_full + 2;            // [2]
+  QItem* items = reinterpret_cast<QItem*>(item_free + 2);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned int kid = (unsigned int)KID_PACKED_Q << 8;
+  const uint32_t q_bytes = (uint32_t)(g.group * g.TQ) * D * 2;
+
+  if (threadIdx.x == 0) {
+    mbar_init(qd_full, 1);
+    for (int s = 0; s < NK; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < NV; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(sp_free, kComputeThreads);
+    mbar_init(ds_full, kComputeThreads);
+    mbar_init(ds_empty, 1);
+    mbar_init(acc_done, 1);
+    mbar_init(mma_drain, 1);
+    mbar_init(qd_free, 1);
+    mbar_init(k_tail, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&item_full[s], 1);
+      mbar_init(&item_free[s], T::CONSUMERS);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, T::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // one CTA owns the SM's whole TMEM, so its addresses start at 0 (attn_fwd.cu)
+  const uint32_t tmem_base = *tmem_slot;
+  constexpr uint32_t tmem = 0;
+
+  // the next item of the ring, copied to registers; false at the end or on an abort
+  auto take = [&](uint32_t i, QItem& it) -> bool {
+    if (!mbar_wait_warp(&item_full[i & 1], (i >> 1) & 1u, abort_flag, ctl, kid | W_ITEM)) return false;
+    it = items[i & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_free[i & 1]);
+    return it.valid != 0;
+  };
+
+  if (tmem_base != tmem) {
+    if (threadIdx.x == 0) set_error(ctl, DSV_ERR_INTERNAL, blockIdx.x);
+  } else if (warp == kQVWarp) {
+    // ---------------- work items and the V ring (one lane) ----------------
+    // A twelfth warp for the items would leave 160 registers a thread, too few
+    // for the compute warps; here an item is found once the V tiles of the one
+    // before it are under way.
+    if (lane == 0) {
+      tma_prefetch_desc(&tmV);
+      uint32_t gq = 0, i = 0;
+      bool ok = true;
+      for (long long idx = blockIdx.x; ok; idx += gridDim.x) {
+        QItem it = {};
+        if (idx < total) {
+          int slot;
+          packed_order(g, g.nslot_q, true, idx, it.kvh, slot);
+          PackedSeq q;
+          if (!packed_find(g, g.q_ptr, g.TQ, slot, q)) continue;
+          const int t0 = (slot - (q.q0 / g.TQ + q.s)) * g.TQ;
+          if (t0 >= q.lq) continue;
+          it.valid = 1;
+          it.tok = q.q0 + t0;
+          it.ntok = min(g.TQ, q.lq - t0);
+          const int last = g.causal ? min(q.lk, q.lk - q.lq + t0 + it.ntok) : q.lk;
+          it.nt = last > 0 ? (last + 127) / 128 : 0;
+          it.key0 = q.k0;
+          it.left = q.lk;
+          it.lim0 = g.causal ? min(q.lk, q.lk - q.lq + t0 + 1) : q.lk;
+          it.slot = slot;
+        }
+        if (!mbar_wait(&item_free[i & 1], ((i >> 1) & 1u) ^ 1u, abort_flag, ctl, kid | W_ITEMFREE)) break;
+        items[i & 1] = it;
+        mbar_arrive(&item_full[i & 1]);
+        ++i;
+        if (!it.valid) break;
+        for (int n = 0; n < it.nt; ++n) {
+          const int s = (int)(gq % NV);
+          if (!mbar_wait(&v_empty[s], ((gq / NV) & 1u) ^ 1u, abort_flag, ctl, kid | W_KVEMPTY)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&v_full[s], T::TX);
+          for (int c = 0; c < T::NCH; ++c)
+            tma_load_3d(sV + s * T::TILE + c * T::CHUNK, &tmV, &v_full[s], c * 64, it.kvh, it.key0 + n * 128);
+          ++gq;
+        }
+      }
+      for (uint32_t n = (gq > NV ? gq - NV : 0u); n < gq; ++n)
+        mbar_wait(&v_full[n % NV], (n / NV) & 1u, nullptr, ctl, kid | W_DRAIN);
+    }
+  } else if (warp == 0) {
+    // ---------------- Q, dO and the K ring ----------------
+    if (lane == 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmdO);
+      tma_prefetch_desc(&tmQ);
+    }
+    uint32_t gq = 0, tails = 0;
+    int qd_issued = 0;
+    bool ok = true;
+    QItem it;
+    for (uint32_t i = 0; ok && take(i, it); ++i) {
+      if (it.nt == 0) continue;
+      // Q and dO are A operands of every S and dP product: the previous tile's last ones must be done
+      if (qd_issued > 0 &&
+          !mbar_wait_warp(qd_free, (uint32_t)(qd_issued - 1) & 1u, abort_flag, ctl, kid | W_KVEMPTY))
+        break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(qd_full, 2 * q_bytes);
+        for (int c = 0; c < T::NCH; ++c) {
+          tma_load_3d(sdO + c * T::CHUNK, &tmdO, qd_full, c * 64, it.kvh * g.group, it.tok);
+          tma_load_3d(sQ + c * T::CHUNK, &tmQ, qd_full, c * 64, it.kvh * g.group, it.tok);
+        }
+      }
+      ++qd_issued;
+      for (int n = 0; n < it.nt; ++n) {
+        const int s = (int)(gq % NK);
+        if (!mbar_wait_warp(&k_empty[s], ((gq / NK) & 1u) ^ 1u, abort_flag, ctl, kid | W_KVEMPTY)) {
+          ok = false;
+          break;
+        }
+        const int have = it.left - n * 128;
+        const bool tail = have < 128;
+        uint64_t* bar = tail ? k_tail : &k_full[s];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, T::TX);
+          for (int c = 0; c < T::NCH; ++c)
+            tma_load_3d(sK + s * T::TILE + c * T::CHUNK, &tmK, bar, c * 64, it.kvh, it.key0 + n * 128);
+        }
+        if (tail) {
+          const bool landed = mbar_wait_warp(k_tail, tails & 1u, nullptr, ctl, kid | W_TAIL);
+          ++tails;
+          if (!landed) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          zero_tile_rows(sK + s * T::TILE, T::NCH, have, lane);
+          if (lane == 0) mbar_arrive(&k_full[s]);
+        }
+        ++gq;
+      }
+    }
+    // every copy this warp started must land before the CTA exits
+    if (qd_issued > 0) mbar_wait(qd_full, (uint32_t)(qd_issued - 1) & 1u, nullptr, ctl, kid | W_DRAIN);
+    for (uint32_t n = (gq > NK ? gq - NK : 0u); n < gq; ++n)
+      mbar_wait(&k_full[n % NK], (n / NK) & 1u, nullptr, ctl, kid | W_DRAIN);
+  } else if (warp == 1) {
+    // ---------------- MMA issuer (whole warp, one elected lane issues) ----------------
+    constexpr uint32_t ID_S = idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t ID_Q = idesc_bf16_f32(128, D, false, true);
+    const uint64_t ddO0 = sdesc_sw128(smem_u32(sdO), 16, 1024);
+    const uint64_t dQ0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t dK0 = sdesc_sw128(smem_u32(sK), 16, 1024);
+    const uint64_t dV0 = sdesc_sw128(smem_u32(sV), 16, 1024);
+    const uint64_t dKmn0 = sdesc_sw128(smem_u32(sK), T::CHUNK, 1024);
+    // tk / tv: early tests of K_n / V_n (see mbar_test); td: of dS of tile n-1
+    auto issue_sdp = [&](uint32_t gn, uint32_t tk, uint32_t tv, uint32_t* td) -> bool {
+      const int sk = (int)(gn % NK), sv = (int)(gn % NV);
+      if (!mbar_wait_warp_tested(&k_full[sk], (gn / NK) & 1u, tk, abort_flag, ctl, kid | W_KFULL)) return false;
+      tc_fence_after();
+      const uint64_t kb = desc_off(dK0, (uint32_t)sk * T::TILE);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t o = (kk >> 2) * T::CHUNK + (kk & 3) * 32;
+        mma_ss_w(tmem + T::S_COL, desc_off(dQ0, o), desc_off(kb, o), ID_S, kk > 0 ? 1u : 0u);
+      }
+      if (td != nullptr) *td = mbar_test(ds_full, (gn - 1) & 1u);
+      if (!mbar_wait_warp_tested(&v_full[sv], (gn / NV) & 1u, tv, abort_flag, ctl, kid | W_VFULL)) return false;
+      tc_fence_after();
+      const uint64_t vb = desc_off(dV0, (uint32_t)sv * T::TILE);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t o = (kk >> 2) * T::CHUNK + (kk & 3) * 32;
+        mma_ss_w(tmem + T::DP_COL, desc_off(ddO0, o), desc_off(vb, o), ID_S, kk > 0 ? 1u : 0u);
+      }
+      mma_commit_w(s_full);
+      mma_commit_w(&v_empty[sv]);   // V_j is only needed by dP
+      return true;
+    };
+    uint32_t gq = 0;
+    int ne = 0;
+    bool ok = true;
+    QItem it;
+    for (uint32_t i = 0; ok && take(i, it); ++i) {
+      if (it.nt == 0) continue;
+      // S and dP are single-buffered: the previous tile's last ones must have been read
+      ok = mbar_wait_warp(qd_full, (uint32_t)ne & 1u, abort_flag, ctl, kid | W_KV) &&
+           (gq == 0 || mbar_wait_warp(sp_free, (gq - 1) & 1u, abort_flag, ctl, kid | W_SPFREE));
+      if (ok) ok = issue_sdp(gq, 0u, 0u, nullptr);
+      if (ok && it.nt == 1) mma_commit_w(qd_free);    // the tile's last read of dO
+      for (int n = 0; ok && n < it.nt; ++n) {
+        const uint32_t gn = gq + (uint32_t)n;
+        uint32_t td = 0u;
+        if (n + 1 < it.nt) {
+          const uint32_t tk = mbar_test(&k_full[(gn + 1) % NK], ((gn + 1) / NK) & 1u);
+          const uint32_t tv = mbar_test(&v_full[(gn + 1) % NV], ((gn + 1) / NV) & 1u);
+          // overwrite S and dP once the compute warps hold tile n
+          if (!mbar_wait_warp(sp_free, gn & 1u, abort_flag, ctl, kid | W_SPFREE)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (!issue_sdp(gn + 1, tk, tv, &td)) {
+            ok = false;
+            break;
+          }
+          if (n + 2 == it.nt) mma_commit_w(qd_free);    // the tile's last read of dO
+        }
+        // ds_full of an item's first tile also means that the previous item's dQ has been read
+        if (!mbar_wait_warp_tested(ds_full, gn & 1u, td, abort_flag, ctl, kid | W_DSFULL)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int s = (int)(gn % NK);
+        const uint64_t kmn = desc_off(dKmn0, (uint32_t)s * T::TILE);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts_w(tmem + T::DQ_COL, tmem + T::DS_COL + kk * 8, desc_off(kmn, kk * 16 * 128), ID_Q,
+                   (n > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_w(&k_empty[s]);
+        mma_commit_w(ds_empty);
+      }
+      if (!ok) break;
+      mma_commit_w(acc_done);
+      gq += (uint32_t)it.nt;
+      ++ne;
+    }
+    // TMEM is freed after the closing CTA-wide sync only once every MMA is done
+    mma_commit_w(mma_drain);
+    mbar_wait_warp(mma_drain, 0, nullptr, ctl, kid | W_DRAIN);
+  } else {
+    // ------------- compute warps: query row r, key half hf -------------
+    const int sp = warp & 3;
+    const int hf = (warp - 2) >> 2;
+    const int r = sp * 32 + lane;
+    const int rt = r / g.group, rh = r - rt * g.group;   // the row's token and head in the tile
+    const uint32_t lane_off = (uint32_t)(sp * 32) << 16;
+    const float scale_log2 = scale * kLog2e;
+    bool ok = true;
+    uint32_t gq = 0;
+    int ne = 0;
+    QItem it;
+    for (uint32_t i = 0; ok && take(i, it); ++i) {
+      const bool row_ok = rt < it.ntok;
+      __nv_bfloat16* out = dQ + (long long)(it.kvh * g.group + rh) * dq_head + ((long long)it.tok + rt) * dq_tok +
+                           hf * (D / 2);
+      if (it.nt == 0) {
+        if (row_ok) {
+#pragma unroll
+          for (int q = 0; q < D / 16; ++q) reinterpret_cast<uint4*>(out)[q] = make_uint4(0, 0, 0, 0);
+        }
+        continue;
+      }
+      const long long vec = ((long long)it.kvh * g.nslot_q + it.slot) * 128 + r;
+      const float nlse2 = L2w[vec];                // -lse*log2(e); -inf for a row without keys
+      const float dd = Dw[vec];
+      const int lim_r = g.causal ? min(it.left, it.lim0 + rt) : it.left;   // keys that the row sees
+
+      uint32_t s_tested = 0u;
+      for (int n = 0; n < it.nt; ++n) {
+        const uint32_t gn = gq + (uint32_t)n;
+        if (!mbar_wait_warp_tested(s_full, gn & 1u, s_tested, abort_flag, ctl, kid | W_S)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t xs[HALF], xp[HALF];
+#pragma unroll
+        for (int c = 0; c < HALF / 32; ++c) {
+          tmem_ld32(tmem + lane_off + T::S_COL + hf * HALF + c * 32, xs + c * 32);
+          tmem_ld32(tmem + lane_off + T::DP_COL + hf * HALF + c * 32, xp + c * 32);
+        }
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(sp_free);
+        const uint32_t e_tested = mbar_test(ds_empty, (gn & 1u) ^ 1u);
+        if (n * 128 + 128 > it.lim0) {
+          // past the row's limit: P = 0 by s = -inf, and dP = 0 so that no NaN of it is left
+          const int lim = lim_r - n * 128 - hf * HALF;
+#pragma unroll
+          for (int j = 0; j < HALF; ++j) {
+            xs[j] = j < lim ? xs[j] : 0xff800000u;
+            xp[j] = j < lim ? xp[j] : 0u;
+          }
+        }
+        // exponent, dP - D and dS on packed fp32 pairs
+        uint32_t dw[HALF / 2];
+        const uint64_t c2 = f2_pack(scale_log2, scale_log2), nl2 = f2_pack(nlse2, nlse2), dd2 = f2_pack(dd, dd);
+#pragma unroll
+        for (int j = 0; j < HALF / 2; ++j) {
+          float x0, x1, d0, d1;
+          f2_unpack(fma2(f2_pack(__uint_as_float(xs[2 * j]), __uint_as_float(xs[2 * j + 1])), c2, nl2), x0, x1);
+          const float p0 = ex2(x0), p1 = ex2(x1);
+          const uint64_t t = sub2(f2_pack(__uint_as_float(xp[2 * j]), __uint_as_float(xp[2 * j + 1])), dd2);
+          f2_unpack(mul2(f2_pack(p0, p1), t), d0, d1);
+          dw[j] = pack_bf16x2(d0, d1);
+        }
+        // the single dS buffer is free once dQ of the previous tile is done
+        if (n + 1 < it.nt) s_tested = mbar_test(s_full, (gn + 1) & 1u);
+        if (!mbar_wait_warp_tested(ds_empty, (gn & 1u) ^ 1u, e_tested, abort_flag, ctl, kid | W_DSEMPTY)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < HALF / 32; ++c)
+          tmem_st16(tmem + lane_off + T::DS_COL + hf * (HALF / 2) + c * 16, dw + c * 16);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(ds_full);
+      }
+      if (ok) ok = mbar_wait_warp(acc_done, (uint32_t)ne & 1u, abort_flag, ctl, kid | W_ACC);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tmem + lane_off + T::DQ_COL + hf * (D / 2) + c * 32, o);
+        tmem_ld_wait();
+        if (row_ok) {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            w[j] = pack_bf16x2(__uint_as_float(o[2 * j]) * scale, __uint_as_float(o[2 * j + 1]) * scale);
+          uint4* dst = reinterpret_cast<uint4*>(out + c * 32);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) dst[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+        }
+      }
+      gq += (uint32_t)it.nt;
+      ++ne;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, T::TMEM_COLS);
+}
+
+template <int D>
+cudaError_t launch_t(const PackedMaps& m, const PackedGeom& g, const dsv_view& O, const dsv_view& dO, const float* lse,
+                     float scale, const dsv_view& dQ, const dsv_view& dK, const dsv_view& dV, void* ws,
+                     const Ctl& ctl, cudaStream_t st) {
+  cudaError_t e;
+  const size_t vec = (size_t)g.Hkv * g.nslot_q * 128;
+  float* Dw = static_cast<float*>(ws);
+  float* L2w = Dw + vec;
+  if (g.Tq > 0) {
+    packed_bwd_prep_kernel<D><<<dim3((unsigned)g.nslot_q, (unsigned)g.Hkv), 256, 0, st>>>(
+        g, static_cast<const __nv_bfloat16*>(O.ptr), O.head_stride, O.token_stride,
+        static_cast<const __nv_bfloat16*>(dO.ptr), dO.head_stride, dO.token_stride, lse, Dw, L2w, ctl);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (g.Tk > 0) {
+    auto kv = packed_bwd_kv_kernel<D>;
+    constexpr int smem = PKVTraits<D>::SMEM;
+    if ((e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    kv<<<(unsigned)((long long)g.Hkv * g.nslot_k), kKVThreads, smem, st>>>(
+        m.Q, m.K, m.V, m.dO, g, L2w, Dw, scale, static_cast<__nv_bfloat16*>(dK.ptr), dK.head_stride, dK.token_stride,
+        static_cast<__nv_bfloat16*>(dV.ptr), dV.head_stride, dV.token_stride, ctl);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (g.Tq == 0) return cudaSuccess;
+  auto qk = packed_bwd_q_kernel<D>;
+  constexpr int smem = PQTraits<D>::SMEM;
+  if ((e = cudaFuncSetAttribute(qk, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+  int dev = 0, nsm = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  const long long total = (long long)g.Hkv * g.nslot_q;
+  qk<<<(unsigned)(total < nsm ? total : nsm), kQThreads, smem, st>>>(
+      m.Q, m.K, m.V, m.dO, g, L2w, Dw, total, scale, static_cast<__nv_bfloat16*>(dQ.ptr), dQ.head_stride,
+      dQ.token_stride, ctl);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t packed_bwd_ws_bytes(const dsv_packed& p) {
+  return 2 * (size_t)p.Hkv * packed_slots(p.Tq, 128 / (p.H / p.Hkv), p.S) * 128 * sizeof(float);
+}
+
+cudaError_t launch_packed_bwd(const PackedMaps& m, const dsv_packed& p, const int32_t* q_ptr, const int32_t* k_ptr,
+                              int causal, float scale, const dsv_view& O, const dsv_view& dO, const float* lse,
+                              const dsv_view& dQ, const dsv_view& dK, const dsv_view& dV, void* ws, const Ctl& ctl,
+                              cudaStream_t st) {
+  const PackedGeom g = packed_geom(p, q_ptr, k_ptr, causal);
+  return p.d == 128 ? launch_t<128>(m, g, O, dO, lse, scale, dQ, dK, dV, ws, ctl, st)
+                    : launch_t<64>(m, g, O, dO, lse, scale, dQ, dK, dV, ws, ctl, st);
+}
+
+}  // namespace dsv

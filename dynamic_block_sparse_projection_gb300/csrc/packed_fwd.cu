@@ -1,0 +1,598 @@
+// packed_fwd.cu — softmax attention of packed sequences, forward, on tcgen05.
+//
+//   s_ij = scale q_i . k_j over the keys j of i's own sequence (causal: also
+//   j <= i + Lk - Lq, positions counted inside the sequence),
+//   O_i = sum_j softmax(s_i)_j v_j,  lse_i = ln sum_j exp(s_ij);
+//   a row that sees no key gets O = 0, lse = -inf.
+//
+// The dense companion of the block-sparse forward (attn_fwd.cu): the same
+// pipeline of one 128-row query tile against a stream of 128-key tiles with S,
+// P and O in tensor memory and an online softmax whose reference is the first
+// tile's row maximum, redone only when a later value of P would pass 2^64.
+// What differs: tiles come from packed.cuh's slots (a tile's rows are tokens x
+// shared heads), rows end at their own limit, and where there are fewer tiles
+// than SMs each tile's keys are split over several CTAs.
+//
+// Key limit.  Row r (token t of the tile) sees keys [0, lim_r).  A tile of
+// keys that every row sees whole takes the unmasked path; in the others a key
+// at or past the row's limit is set to -inf by selection, so whatever the
+// loaded row holds there (the next sequence's keys) never enters.  The last
+// tile's V rows past the sequence's end are zeroed in shared memory: their P
+// is 0, but 0 * NaN is not.
+//
+// Warp roles (256 threads): warp 0 loads Q and the K ring, warp 1 issues the
+// MMAs, warps 2..5 softmax and epilogue (one row per thread), warp 6 loads the
+// V ring, warp 7 finds the work items and hands them to the others through a
+// two-entry ring, so that a search in the row pointers never stops the others.
+//
+// Split over the keys.  Each part writes its normalised O (fp32) and base-2
+// log-sum to the workspace and combine_kernel joins them in part order:
+// results do not depend on which part finished first.
+#include <math.h>
+
+#include "packed.cuh"
+
+namespace dsv {
+
+namespace {
+
+constexpr float kLn2 = 0.69314718055994530942f;
+
+struct FwdItem {
+  int valid;
+  int kvh;     // key head
+  int tok;     // first query token of the tile (absolute)
+  int ntok;    // tokens in the tile
+  int key0;    // first key of this part (absolute)
+  int nt;      // key tiles of this part
+  int lim0;    // keys of this part that the first token sees (may be <= 0, may exceed the part)
+  int left;    // keys of the sequence from key0 on
+  int part;    // (split * Hkv + kvh) * nslot + slot
+  int pad;
+};
+
+template <int D>
+struct PFwdTraits {
+  static constexpr int NCH = D / 64;
+  static constexpr int CHUNK = 128 * 128;
+  static constexpr int TILE = NCH * CHUNK;
+  static constexpr int NST = 3;
+  static constexpr int NBAR = 1 + 2 * NST + 3 * NST + 2 + 1 + 4;
+  static constexpr int SMEM_USED = 1024 + TILE + 2 * NST * TILE + NBAR * 8 + 16 + 2 * (int)sizeof(FwdItem);
+  static_assert(SMEM_USED <= 227 * 1024, "forward tiles exceed shared memory");
+  // at least 120 KB so that one CTA owns an SM (and its 512 TMEM columns)
+  static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
+  static constexpr uint32_t S_COL = 128, O_COL = 384, TMEM_COLS = 512;
+  static constexpr uint32_t TX = 128 * D * 2;
+};
+
+constexpr int kVWarp = 6, kItemWarp = 7, kFwdThreads = 256, kConsumers = 7;
+
+enum : unsigned int { W_Q = 1, W_KEMPTY, W_K, W_P, W_V, W_S, W_O, W_OFINAL, W_DRAIN, W_QEMPTY, W_ITEM, W_ITEMFREE,
+                      W_TAIL };
+
+template <int D>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PackedGeom g, int nsplit,
+                      long long total, float scale_log2, __nv_bfloat16* O, long long o_head, long long o_tok,
+                      float* LSE, float* Opart, float* Lpart, Ctl ctl) {
+  using T = PFwdTraits<D>;
+  constexpr int NST = T::NST;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sbase = smem_align1024(smem_raw);
+  uint8_t* sQ = sbase;
+  uint8_t* sK = sQ + T::TILE;
+  uint8_t* sV = sK + NST * T::TILE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + NST * T::TILE);
+  uint64_t* q_full = bars;
+  uint64_t* k_full = bars + 1;
+  uint64_t* v_full = k_full + NST;
+  uint64_t* s_full = v_full + NST;    // [3] S(n) in buffer n%3; also frees K slot n%3
+  uint64_t* p_full = s_full + NST;    // [3] P(n) written over S(n)
+  uint64_t* o_done = p_full + NST;    // [3] O += P(n) V_n done; also frees V slot n%3
+  uint64_t* o_final = o_done + NST;   // all PV products of the current item are done
+  uint64_t* mma_drain = o_final + 1;
+  uint64_t* v_tail = mma_drain + 1;   // the last V tile of a sequence, before its rows are cut
+  uint64_t* item_full = v_tail + 1;   // [2]
+  uint64_t* item_free = item_full + 2;  // [2]
+  FwdItem* items = reinterpret_cast<FwdItem*>(item_free + 2);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned int kid = (unsigned int)KID_PACKED_FWD << 8;
+  const uint32_t q_bytes = (uint32_t)(g.group * g.TQ) * D * 2;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 128);
+      mbar_init(&o_done[s], 1);
+    }
+    mbar_init(o_final, 1);
+    mbar_init(mma_drain, 1);
+    mbar_init(v_tail, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&item_full[s], 1);
+      mbar_init(&item_free[s], kConsumers);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, T::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // one CTA owns the SM's whole TMEM, so its addresses start at 0 (attn_fwd.cu)
+  const uint32_t tmem_base = *tmem_slot;
+  constexpr uint32_t tmem = 0;
+
+  // the next item of the ring, copied to registers; false at the end or on an abort
+  auto take = [&](uint32_t i, FwdItem& it) -> bool {
+    if (!mbar_wait_warp(&item_full[i & 1], (i >> 1) & 1u, abort_flag, ctl, kid | W_ITEM)) return false;
+    it = items[i & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_free[i & 1]);
+    return it.valid != 0;
+  };
+
+  if (tmem_base != tmem) {
+    if (threadIdx.x == 0) set_error(ctl, DSV_ERR_INTERNAL, blockIdx.x);
+  } else if (warp == kItemWarp) {
+    // ---------------- work items ----------------
+    if (blockIdx.x == 0) packed_check_ptrs(g, ctl, lane);
+    if (lane == 0) {
+      uint32_t i = 0;
+      for (long long idx = blockIdx.x;; idx += gridDim.x) {
+        FwdItem it = {};
+        if (idx < total) {
+          const int sp = (int)(idx % nsplit);
+          int slot;
+          packed_order(g, g.nslot_q, true, idx / nsplit, it.kvh, slot);
+          PackedSeq q;
+          if (!packed_find(g, g.q_ptr, g.TQ, slot, q)) continue;
+          const int t0 = (slot - (q.q0 / g.TQ + q.s)) * g.TQ;
+          if (t0 >= q.lq) continue;
+          it.valid = 1;
+          it.tok = q.q0 + t0;
+          it.ntok = min(g.TQ, q.lq - t0);
+          // keys that the first and the last token of the tile see
+          const int first = g.causal ? min(q.lk, q.lk - q.lq + t0 + 1) : q.lk;
+          const int last = g.causal ? min(q.lk, q.lk - q.lq + t0 + it.ntok) : q.lk;
+          const int tiles = last > 0 ? (last + 127) / 128 : 0;
+          // a part takes at least kMinPart tiles, so that short sequences are not cut
+          const int per = max((tiles + nsplit - 1) / nsplit, nsplit > 1 ? kPackedMinPart : 1);
+          const int j0 = sp * per;
+          it.nt = max(0, min(per, tiles - j0));
+          it.key0 = q.k0 + j0 * 128;
+          it.left = q.lk - j0 * 128;
+          it.lim0 = first - j0 * 128;
+          it.part = (sp * g.Hkv + it.kvh) * g.nslot_q + slot;
+        }
+        if (!mbar_wait(&item_free[i & 1], ((i >> 1) & 1u) ^ 1u, abort_flag, ctl, kid | W_ITEMFREE)) break;
+        items[i & 1] = it;
+        mbar_arrive(&item_full[i & 1]);
+        ++i;
+        if (!it.valid) break;
+      }
+    }
+  } else if (warp == 0) {
+    // ---------------- Q and the K ring ----------------
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+    }
+    uint32_t gq = 0;                            // tiles issued so far
+    int q_issued = 0;
+    bool ok = true;
+    FwdItem it;
+    for (uint32_t i = 0; ok && take(i, it); ++i) {
+      if (it.nt == 0) continue;
+      // Q is the A operand of every S product: the previous item's last one must be done
+      if (q_issued > 0 &&
+          !mbar_wait_warp(&s_full[(gq - 1) % NST], ((gq - 1) / NST) & 1u, abort_flag, ctl, kid | W_QEMPTY))
+        break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(q_full, q_bytes);
+        for (int c = 0; c < T::NCH; ++c)
+          tma_load_3d(sQ + c * T::CHUNK, &tmQ, q_full, c * 64, it.kvh * g.group, it.tok);
+      }
+      ++q_issued;
+      for (int n = 0; n < it.nt; ++n) {
+        const int s = (int)(gq % NST);
+        if (gq >= NST && !mbar_wait_warp(&s_full[s], ((gq - NST) / NST) & 1u, abort_flag, ctl, kid | W_KEMPTY)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&k_full[s], T::TX);
+          for (int c = 0; c < T::NCH; ++c)
+            tma_load_3d(sK + s * T::TILE + c * T::CHUNK, &tmK, &k_full[s], c * 64, it.kvh, it.key0 + n * 128);
+        }
+        ++gq;
+      }
+    }
+    // every copy this warp started must land before the CTA exits
+    if (q_issued > 0) mbar_wait(q_full, (uint32_t)(q_issued - 1) & 1u, nullptr, ctl, kid | W_DRAIN);
+    for (uint32_t n = (gq > NST ? gq - NST : 0u); n < gq; ++n)
+      mbar_wait(&k_full[n % NST], (n / NST) & 1u, nullptr, ctl, kid | W_DRAIN);
+  } else if (warp == kVWarp) {
+    // ---------------- the V ring ----------------
+    if (lane == 0) tma_prefetch_desc(&tmV);
+    uint32_t gq = 0, tails = 0;
+    bool ok = true;
+    FwdItem it;
+    for (uint32_t i = 0; ok && take(i, it); ++i) {
+      for (int n = 0; n < it.nt; ++n) {
+        const int s = (int)(gq % NST);
+        if (gq >= NST && !mbar_wait_warp(&o_done[s], ((gq - NST) / NST) & 1u, abort_flag, ctl, kid | W_KEMPTY)) {
+          ok = false;
+          break;
+        }
+        const int have = it.left - n * 128;
+        const bool tail = have < 128;
+        uint64_t* bar = tail ? v_tail : &v_full[s];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, T::TX);
+          for (int c = 0; c < T::NCH; ++c)
+            tma_load_3d(sV + s * T::TILE + c * T::CHUNK, &tmV, bar, c * 64, it.kvh, it.key0 + n * 128);
+        }
+        if (tail) {
+          // rows past the sequence's end belong to the next one (or to nobody)
+          const bool landed = mbar_wait_warp(v_tail, tails & 1u, nullptr, ctl, kid | W_TAIL);
+          ++tails;
+          if (!landed) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          zero_tile_rows(sV + s * T::TILE, T::NCH, have, lane);
+          if (lane == 0) mbar_arrive(&v_full[s]);
+        }
+        ++gq;
+      }
+    }
+    for (uint32_t n = (gq > NST ? gq - NST : 0u); n < gq; ++n)
+      mbar_wait(&v_full[n % NST], (n / NST) & 1u, nullptr, ctl, kid | W_DRAIN);
+  } else if (warp == 1) {
+    // ---------------- MMA issuer (whole warp, one elected lane issues) ----------------
+    constexpr uint32_t IDS = idesc_bf16_f32(128, 128, false, false);
+    constexpr uint32_t IDO = idesc_bf16_f32(128, D, false, true);
+    const uint64_t dQ0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t dK0 = sdesc_sw128(smem_u32(sK), 16, 1024);
+    const uint64_t dV0 = sdesc_sw128(smem_u32(sV), T::CHUNK, 1024);
+    auto issue_S = [&](uint32_t gn) -> bool {
+      const int s = (int)(gn % NST);
+      if (!mbar_wait_warp(&k_full[s], (gn / NST) & 1u, abort_flag, ctl, kid | W_K)) return false;
+      tc_fence_after();
+      const uint32_t d_tmem = tmem + (uint32_t)s * T::S_COL;
+      const uint64_t kb = desc_off(dK0, (uint32_t)s * T::TILE);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * T::CHUNK + (kk & 3) * 32;
+        mma_ss_w(d_tmem, desc_off(dQ0, off), desc_off(kb, off), IDS, kk > 0 ? 1u : 0u);
+      }
+      mma_commit_w(&s_full[s]);
+      return true;
+    };
+    uint32_t gq = 0;
+    int ne = 0;
+    bool ok = true;
+    FwdItem it;
+    for (uint32_t i = 0; ok && take(i, it); ++i) {
+      if (it.nt == 0) continue;
+      ok = mbar_wait_warp(q_full, (uint32_t)ne & 1u, abort_flag, ctl, kid | W_Q);
+      if (ok) ok = issue_S(gq);
+      if (ok && it.nt > 1) ok = issue_S(gq + 1);
+      for (int n = 0; ok && n < it.nt; ++n) {
+        // S(n+2) reuses the buffer of P(n-1), whose PV product is already queued
+        const uint32_t gn = gq + (uint32_t)n;
+        const int s = (int)(gn % NST);
+        const uint32_t ph = (gn / NST) & 1u;
+        const uint32_t v_tested = mbar_test(&v_full[s], ph);   // V_n normally landed long ago
+        if (n + 2 < it.nt && !issue_S(gn + 2)) {
+          ok = false;
+          break;
+        }
+        // P(0) of an item also means the softmax warps have read the previous item's O
+        if (!mbar_wait_warp(&p_full[s], ph, abort_flag, ctl, kid | W_P) ||
+            !mbar_wait_warp_tested(&v_full[s], ph, v_tested, abort_flag, ctl, kid | W_V)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t p_tmem = tmem + (uint32_t)s * T::S_COL;
+        const uint64_t vb = desc_off(dV0, (uint32_t)s * T::TILE);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts_w(tmem + T::O_COL, p_tmem + kk * 8, desc_off(vb, kk * 16 * 128), IDO, (n > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_w(&o_done[s]);
+      }
+      if (!ok) break;
+      mma_commit_w(o_final);
+      gq += (uint32_t)it.nt;
+      ++ne;
+    }
+    // TMEM is freed after the closing CTA-wide sync only once every MMA is done
+    mma_commit_w(mma_drain);
+    mbar_wait_warp(mma_drain, 0, nullptr, ctl, kid | W_DRAIN);
+  } else {
+    // ---------------- softmax warpgroup (warps 2..5) ----------------
+    const int sp = warp & 3;
+    const int r = sp * 32 + lane;
+    const int rt = r / g.group, rh = r - rt * g.group;   // the row's token and head in the tile
+    const uint32_t lane_off = (uint32_t)(sp * 32) << 16;
+    uint32_t gq = 0;
+    int ne = 0;
+    bool ok = true;
+    FwdItem it;
+    for (uint32_t i = 0; ok && take(i, it); ++i) {
+      const bool row_ok = rt < it.ntok;
+      const int head = it.kvh * g.group + rh;
+      const long long tok = (long long)it.tok + rt;
+      const long long prow = (long long)it.part * 128 + r;
+      if (it.nt == 0) {
+        if (row_ok && nsplit > 1) Lpart[prow] = -INFINITY;
+        if (row_ok && nsplit == 1) {
+          uint4* dst = reinterpret_cast<uint4*>(O + head * o_head + tok * o_tok);
+#pragma unroll
+          for (int q = 0; q < D / 8; ++q) dst[q] = make_uint4(0, 0, 0, 0);
+          LSE[(long long)head * g.Tq + tok] = -INFINITY;
+        }
+        continue;
+      }
+      const int lim_r = g.causal ? min(it.left, it.lim0 + rt) : it.left;   // keys of this part that the row sees
+      float m = 0.f, l = 0.f;
+      uint32_t s_tested = 0u;   // S(n) already known complete (tested during tile n-1)
+      for (int n = 0; n < it.nt; ++n) {
+        const uint32_t gn = gq + (uint32_t)n;
+        const int s = (int)(gn % NST);
+        if (!mbar_wait_warp_tested(&s_full[s], (gn / NST) & 1u, s_tested, abort_flag, ctl, kid | W_S)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sb = tmem + lane_off + (uint32_t)s * T::S_COL;
+        uint32_t xr[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(sb + c * 32, xr + c * 32);
+        s_tested = (n + 1 < it.nt) ? mbar_test(&s_full[(gn + 1) % NST], ((gn + 1) / NST) & 1u) : 0u;
+        tmem_ld_wait();
+        if (n * 128 + 128 > it.lim0) {
+          const int lim = lim_r - n * 128;
+#pragma unroll
+          for (int j = 0; j < 128; ++j) xr[j] = j < lim ? xr[j] : 0xff800000u;   // -inf
+        }
+        // row max as 8 independent partial maxima (short dependency chains)
+        auto row_max = [&]() -> float {
+          float mx8[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) mx8[j] = __uint_as_float(xr[j]);
+#pragma unroll
+          for (int j = 8; j < 128; j += 16)
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              mx8[q] = j + 8 < 128 ? max3f(mx8[q], __uint_as_float(xr[j + q]), __uint_as_float(xr[j + 8 + q]))
+                                   : fmaxf(mx8[q], __uint_as_float(xr[j + q]));
+          return fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                       fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+        };
+        // P = exp2(S c - m): exponent and row sum on packed fp32 pairs.  P is
+        // rounded to bf16 as the tensor core's operand (V's type); the row sum
+        // takes the unrounded values, so the rounding errors of P average out.
+        uint32_t pk[64];
+        auto exponentiate = [&](float mref) -> float {
+          const uint64_t c2 = f2_pack(scale_log2, scale_log2), nm2 = f2_pack(-mref, -mref);
+          uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int j = 0; j < 64; ++j) {
+            float x0, x1;
+            f2_unpack(fma2(f2_pack(__uint_as_float(xr[2 * j]), __uint_as_float(xr[2 * j + 1])), c2, nm2), x0, x1);
+            const float p0 = ex2(x0);
+            const float p1 = ex2(x1);
+            rs2[j & 3] = add2(rs2[j & 3], f2_pack(p0, p1));
+            pk[j] = pack_bf16x2(p0, p1);
+          }
+          float a0, a1;
+          f2_unpack(add2(add2(rs2[0], rs2[1]), add2(rs2[2], rs2[3])), a0, a1);
+          return a0 + a1;
+        };
+        // The reference is the first tile's row maximum (every row's limit
+        // covers a prefix of the part's keys, so a row that sees any of them
+        // sees one in the first tile; one that sees none keeps 0).  A later
+        // tile keeps it unless one of its values would pass 2^64.
+        float tsum;
+        if (n == 0) {
+          const float mx = row_max() * scale_log2;
+          m = mx == -INFINITY ? 0.f : mx;
+          tsum = exponentiate(m);
+        } else {
+          tsum = exponentiate(m);
+          // rows behind the tile's tokens hold another sequence's queries: they must not decide
+          if (__any_sync(0xffffffffu, row_ok && !(tsum <= 18446744073709551616.0f))) {   // 2^64
+            const float m_new = fmaxf(m, row_max() * scale_log2);
+            // rescale this warp's O rows once the previous PV product has landed
+            const uint32_t gp = gn - 1;
+            if (!mbar_wait_warp(&o_done[gp % NST], (gp / NST) & 1u, abort_flag, ctl, kid | W_O)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const float alpha = ex2(m - m_new);
+            l *= alpha;
+            m = m_new;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tmem + lane_off + T::O_COL + c * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              tmem_st32(tmem + lane_off + T::O_COL + c * 32, o);
+            }
+            tmem_st_wait();
+            tsum = exponentiate(m);
+          }
+        }
+        l += tsum;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_st16(sb + c * 16, pk + c * 16);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_full[s]);
+      }
+      if (ok) ok = mbar_wait_warp(o_final, (uint32_t)ne & 1u, abort_flag, ctl, kid | W_OFINAL);
+      if (!ok) break;
+      tc_fence_after();
+      // a row that saw no key has l = 0 and an O of zeros
+      const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
+      const float lse2 = m + log2f(l);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tmem + lane_off + T::O_COL + c * 32, o);
+        tmem_ld_wait();
+        if (row_ok && nsplit > 1) {
+          float4* dst = reinterpret_cast<float4*>(Opart + prow * D + c * 32);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            dst[q] = make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
+                                 __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
+        } else if (row_ok) {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            w[j] = pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+          uint4* dst = reinterpret_cast<uint4*>(O + head * o_head + tok * o_tok + c * 32);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) dst[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+        }
+      }
+      if (row_ok) {
+        if (nsplit > 1) Lpart[prow] = lse2; else LSE[(long long)head * g.Tq + tok] = lse2 * kLn2;
+      }
+      gq += (uint32_t)it.nt;
+      ++ne;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, T::TMEM_COLS);
+}
+
+// Joins the parts of a tile: with L_p the base-2 log-sums, M = max L_p and
+// w_p = 2^(L_p - M):  O = sum w_p O_p / sum w_p,  lse = (M + log2 sum w_p) ln 2.
+// One warp per row, parts in order.
+template <int D>
+__global__ void __launch_bounds__(128) packed_combine_kernel(const __grid_constant__ PackedGeom g, int nsplit,
+                                                             const float* __restrict__ Opart,
+                                                             const float* __restrict__ Lpart, __nv_bfloat16* O,
+                                                             long long o_head, long long o_tok, float* LSE) {
+  constexpr int V = D / 32;            // channels per lane
+  const int slot = blockIdx.x, kvh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  PackedSeq q;
+  if (!packed_find(g, g.q_ptr, g.TQ, slot, q)) return;
+  const int t0 = (slot - (q.q0 / g.TQ + q.s)) * g.TQ;
+  if (t0 >= q.lq) return;
+  const int rows = min(g.TQ, q.lq - t0) * g.group;
+  const long long step = (long long)g.Hkv * g.nslot_q * 128;
+  for (int r = blockIdx.z * 4 + warp; r < rows; r += 4 * gridDim.z) {
+    const long long row = ((long long)kvh * g.nslot_q + slot) * 128 + r;
+    float M = -INFINITY;
+    for (int p = lane; p < nsplit; p += 32) M = fmaxf(M, Lpart[row + p * step]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float acc[V] = {};
+    float sum = 0.f;
+    if (M != -INFINITY) {
+      for (int p = 0; p < nsplit; ++p) {
+        const float L = Lpart[row + p * step];
+        if (L == -INFINITY) continue;          // a part that saw nothing of this row wrote no O
+        const float w = ex2(L - M);
+        const float* src = Opart + (row + p * step) * D + lane * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(w, src[i], acc[i]);
+        sum += w;
+      }
+    }
+    const float inv = M != -INFINITY ? 1.0f / sum : 0.f;
+    const int rt = r / g.group, head = kvh * g.group + (r - rt * g.group);
+    const long long tok = (long long)q.q0 + t0 + rt;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(O + head * o_head + tok * o_tok + lane * V);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) dst[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    if (lane == 0) LSE[(long long)head * g.Tq + tok] = M != -INFINITY ? (M + log2f(sum)) * kLn2 : -INFINITY;
+  }
+}
+
+template <int D>
+cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, const PackedGeom& g,
+                     int nsplit, float scale, const dsv_view& O, float* lse, void* ws, const Ctl& ctl,
+                     cudaStream_t st) {
+  using T = PFwdTraits<D>;
+  auto kern = packed_fwd_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+  if (e != cudaSuccess) return e;
+  int dev = 0, nsm = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  const long long total = (long long)g.Hkv * g.nslot_q * nsplit;
+  const unsigned grid = (unsigned)(total < nsm ? total : nsm);
+  float* Opart = nsplit > 1 ? static_cast<float*>(ws) : nullptr;
+  float* Lpart = nsplit > 1 ? Opart + (size_t)total * 128 * D : nullptr;
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(O.ptr);
+  kern<<<grid, kFwdThreads, T::SMEM, st>>>(tmQ, tmK, tmV, g, nsplit, total, scale * 1.4426950408889634f, o,
+                                           O.head_stride, O.token_stride, lse, Opart, Lpart, ctl);
+  if ((e = cudaGetLastError()) != cudaSuccess || nsplit == 1) return e;
+  // rows of a tile over a few CTAs when the tiles alone would not fill the SMs
+  const long long tiles = (long long)g.Hkv * g.nslot_q;
+  const int rows = g.group * (g.Tq < g.TQ ? g.Tq : g.TQ);
+  long long z = (2LL * kPackedSMs + tiles - 1) / tiles;
+  z = z < (rows + 3) / 4 ? z : (rows + 3) / 4;
+  packed_combine_kernel<D><<<dim3((unsigned)g.nslot_q, (unsigned)g.Hkv, (unsigned)(z > 0 ? z : 1)), 128, 0, st>>>(
+      g, nsplit, Opart, Lpart, o, O.head_stride, O.token_stride, lse);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Parts per query tile.  With at least one tile per SM the keys stay whole.
+// With fewer, parts of at least kPackedMinPart key tiles fill four rounds of
+// the SMs (the lengths are not known here: uneven ones even out over rounds).
+int packed_fwd_splits(const dsv_packed& p) {
+  if (p.S <= 0 || p.Tq <= 0 || p.Tk <= 0) return 1;
+  const int TQ = 128 / (p.H / p.Hkv);
+  const long long q_tiles = (p.Tq + TQ - 1) / TQ;
+  const long long tiles = (long long)p.Hkv * (q_tiles > p.S ? q_tiles : p.S);
+  if (tiles >= kPackedSMs) return 1;
+  long long n = (4LL * kPackedSMs + tiles - 1) / tiles;
+  const long long most = ((p.Tk + 127) / 128 + kPackedMinPart - 1) / kPackedMinPart;
+  n = n < most ? n : most;
+  return (int)(n < 1 ? 1 : n > 64 ? 64 : n);
+}
+
+size_t packed_fwd_ws_bytes(const dsv_packed& p) {
+  const int n = packed_fwd_splits(p);
+  if (n == 1) return 0;
+  return (size_t)n * p.Hkv * packed_slots(p.Tq, 128 / (p.H / p.Hkv), p.S) * 128 * (p.d + 1) * sizeof(float);
+}
+
+cudaError_t launch_packed_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                              const dsv_packed& p, const int32_t* q_ptr, const int32_t* k_ptr, int causal, float scale,
+                              const dsv_view& O, float* lse, void* ws, const Ctl& ctl, cudaStream_t st) {
+  const PackedGeom g = packed_geom(p, q_ptr, k_ptr, causal);
+  const int n = packed_fwd_splits(p);
+  return p.d == 128 ? launch_t<128>(tmQ, tmK, tmV, g, n, scale, O, lse, ws, ctl, st)
+                    : launch_t<64>(tmQ, tmK, tmV, g, n, scale, O, lse, ws, ctl, st);
+}
+
+}  // namespace dsv

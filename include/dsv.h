@@ -336,6 +336,110 @@ dsv_status dsv_dispatch_heads(const int32_t* k_per_head, int32_t H, int32_t nb, 
                               const float* ratio, int32_t n, int32_t* k_out, int32_t* dense_out);
 
 /* ------------------------------------------------------------------------
+ * Strided views, for the calls below: bf16 rows of d contiguous elements at
+ * ptr + b * batch_stride + h * head_stride + t * token_stride (strides in
+ * elements).  [heads, tokens, d] and the [tokens, heads, d] a projection
+ * writes are both views of this kind.  ptr is 16-byte aligned; along a
+ * dimension of more than one element a stride is a multiple of 8, at least d
+ * and below 2^38; the rows of an output do not overlap.  (DSV_ERR_INVALID_ARG
+ * otherwise.)
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  void* ptr;
+  int64_t batch_stride, head_stride, token_stride;
+} dsv_view;
+
+/* ------------------------------------------------------------------------
+ * dsv_rope_axes_fwd, dsv_rope_axes_bwd — rotary positions with several axes,
+ * optionally behind the RMS norm of queries and keys ([nl] 1, [hi] 1: the
+ * tokens are those of a 3D video latent; the pages leave the positions open)
+ *
+ * The d channels of a head are cut into one band of section[a] channels per
+ * axis a, in order; in a band of c channels pair i (channels 2i, 2i+1 of the
+ * band) of token n turns by the angle pos[n, a] * theta^(-2i/c):
+ *   y_2i = x_2i cos - x_2i+1 sin,   y_2i+1 = x_2i sin + x_2i+1 cos.
+ * Channels behind the bands pass through.  With a weight w the rotation is
+ * applied to x rsqrt(mean_channels(x^2) + eps) w instead of x.
+ * The backward writes dx and, with a weight,
+ *   dweight = sum over b, h, n of (R^T dy) x rsqrt(mean(x^2) + eps).
+ *
+ * x, y, dy, dx  views of [B, H, N, d].  y may be x, and dx may be dy or x (the
+ *           same view); other overlaps of an output with an input are not
+ *           allowed.
+ * pos       int32 [N, axes], or [B, N, axes] with pos_batch_stride = N * axes
+ *           (0: shared by the batch).  Any value: an angle is worked out to
+ *           |pos| * 2^-56 turns, far positions included.
+ * weight    fp32 [d], or NULL (no norm; then x, dweight and the workspace of
+ *           the backward may be NULL, and eps is not read).  eps > 0.
+ * workspace >= dsv_rope_axes_bwd_workspace_bytes(r) bytes, 256-byte aligned
+ *           (partial sums of dweight).
+ * d in {64, 128}; 1 to 4 axes; sections even, at least 2, together at most d;
+ * theta >= 1, finite; H <= 1024; B <= 65535.  Sums are fp32 in a fixed order.
+ * With B*H*N == 0 only dweight is written (zeros).
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t B, H, N, d;
+  int32_t axes;
+  int32_t section[4];
+  double theta;
+} dsv_rope;
+dsv_status dsv_rope_axes_fwd(dsv_view x, const int32_t* pos, int64_t pos_batch_stride, dsv_rope r,
+                             const float* weight, float eps, dsv_view y, dsv_stream_t stream);
+size_t dsv_rope_axes_bwd_workspace_bytes(dsv_rope r);
+dsv_status dsv_rope_axes_bwd(dsv_view dy, dsv_view x, const int32_t* pos, int64_t pos_batch_stride, dsv_rope r,
+                             const float* weight, float eps, dsv_view dx, float* dweight, void* workspace,
+                             size_t workspace_bytes, dsv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * dsv_packed_attn_fwd, dsv_packed_attn_bwd — softmax attention of sequences
+ * of different lengths, packed one behind the other; every pair, or causal;
+ * query heads may share key heads.  The dense companion of
+ * dsv_sparse_attn_fwd / _bwd, for layers and lengths the sparse path does not
+ * take (clips of any length, text, one new token against a history).
+ *
+ * Sequence s owns the query tokens q_ptr[s] .. q_ptr[s+1] - 1 and the key
+ * tokens k_ptr[s] .. k_ptr[s+1] - 1; query head h reads key head
+ * h / (H / Hkv).  With Lq, Lk the sequence's lengths, query i (from 0) sees its
+ * keys j < Lk, with causal = 1 only j <= i + Lk - Lq (the last query sees all):
+ *   s_ij = scale q_i . k_j,  O_i = sum_j softmax(s_i)_j v_j,
+ *   lse_i = ln sum_j exp(s_ij)  (natural log).
+ * A query that sees no key gets O = 0, lse = -inf and a zero gradient; a key
+ * that no query sees gets zero gradients.  Tokens outside [ptr[0], ptr[S])
+ * are neither read into any result nor written.  A non-finite value of a
+ * sequence reaches no other sequence.
+ *
+ * Q, O, dO, dQ   views of [H, Tq, d];  K, V, dK, dV  views of [Hkv, Tk, d]
+ *           (batch_stride is not read).  No output overlaps an input or
+ *           another output.
+ * q_ptr, k_ptr   int32 [S + 1] on the device, each rising (equal neighbours:
+ *           an empty sequence) within [0, Tq] and [0, Tk].  A sequence whose
+ *           pointers break this is skipped and DSV_ERR_BAD_INDEX recorded in
+ *           the device error word, with the sequence as its info.
+ * causal    0 or 1.  softmax_scale <= 0 selects 1/sqrt(d).
+ * lse       fp32 [H, Tq] contiguous; the backward reads the forward's O and lse.
+ * workspace >= the matching _workspace_bytes(p) bytes, 256-byte aligned (may
+ *           be NULL where that is 0).  Forward: where query tiles are fewer
+ *           than the SMs, the keys of a tile are split over several CTAs and
+ *           their fp32 parts joined in order.  Backward: D_i = dO_i . O_i and
+ *           -lse_i log2(e).
+ * d in {64, 128}; H <= 1024, a multiple of Hkv; H / Hkv <= 128;
+ * Tq + 128 S and Tk + 128 S < 2^31.  Outputs are bit-identical from run to run
+ * (one writer per output tile, no atomics).
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t S, H, Hkv, Tq, Tk, d;
+} dsv_packed;
+size_t dsv_packed_attn_fwd_workspace_bytes(dsv_packed p);
+dsv_status dsv_packed_attn_fwd(dsv_view Q, dsv_view K, dsv_view V, dsv_packed p, const int32_t* q_ptr,
+                               const int32_t* k_ptr, int32_t causal, float softmax_scale, dsv_view O, float* lse,
+                               void* workspace, size_t workspace_bytes, dsv_stream_t stream);
+size_t dsv_packed_attn_bwd_workspace_bytes(dsv_packed p);
+dsv_status dsv_packed_attn_bwd(dsv_view Q, dsv_view K, dsv_view V, dsv_view O, dsv_view dO, const float* lse,
+                               dsv_packed p, const int32_t* q_ptr, const int32_t* k_ptr, int32_t causal,
+                               float softmax_scale, dsv_view dQ, dsv_view dK, dsv_view dV, void* workspace,
+                               size_t workspace_bytes, dsv_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Status and device-side error reporting.
  * ------------------------------------------------------------------------ */
 const char* dsv_status_string(dsv_status status);

@@ -522,3 +522,99 @@ def mass_lists(S, tau: float, temperature: float, kmin: int, kmax: int) -> Tuple
                 cols.append(topk_row(S[b, h, g], m))
                 ptr.append(ptr[-1] + m)
     return np.asarray(ptr, dtype=np.int64), (np.concatenate(cols).astype(np.int64) if cols else np.zeros(0, np.int64))
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions with several axes; attention of packed sequences
+# ---------------------------------------------------------------------------
+
+def _rope_angles(pos, sections, d, theta):
+    """[.., N, d/2] angles: band by band, pair i of a band of c channels turns by p theta^(-2i/c)."""
+    pos = np.asarray(pos, np.float64)
+    ang = np.zeros(pos.shape[:-1] + (d // 2,))
+    at = 0
+    for a, c in enumerate(sections):
+        for i in range(c // 2):
+            ang[..., at + i] = pos[..., a] * theta ** (-2.0 * i / c)
+        at += c // 2
+    return ang
+
+
+def rope_axes(x, pos, sections, theta=10000.0, weight=None, eps=1e-6):
+    """x [B, H, N, d]; pos [N, axes] or [B, N, axes].  Every row (its RMS norm
+    times `weight`, where given) times its block-diagonal rotation matrix."""
+    x = np.asarray(x, np.float64)
+    d = x.shape[-1]
+    if weight is not None:
+        x = x / np.sqrt(np.mean(x * x, axis=-1, keepdims=True) + eps) * np.asarray(weight, np.float64)
+    ang = _rope_angles(pos, sections, d, theta)
+    ang = ang[:, None] if ang.ndim == 3 else ang
+    y = np.empty_like(x)
+    y[..., 0::2] = x[..., 0::2] * np.cos(ang) - x[..., 1::2] * np.sin(ang)
+    y[..., 1::2] = x[..., 0::2] * np.sin(ang) + x[..., 1::2] * np.cos(ang)
+    return y
+
+
+def rope_axes_bwd(dy, pos, sections, theta=10000.0, x=None, weight=None, eps=1e-6):
+    """dx, or (dx, dweight) with a weight: the transposed rotation, then the
+    Jacobian of the norm, J = (I - x x^T / (d m)) / sqrt(m), m = mean(x^2) + eps."""
+    g = rope_axes(dy, -np.asarray(pos, np.int64), sections, theta)
+    if weight is None:
+        return g
+    x, w = np.asarray(x, np.float64), np.asarray(weight, np.float64)
+    m = np.mean(x * x, axis=-1, keepdims=True) + eps
+    gw = g * w
+    dx = (gw - x * np.sum(gw * x, axis=-1, keepdims=True) / (x.shape[-1] * m)) / np.sqrt(m)
+    return dx, np.sum(g * x / np.sqrt(m), axis=(0, 1, 2))
+
+
+def _packed_parts(Q, K, q_ptr, k_ptr, causal):
+    """(head, key head, query slice, key slice, mask) of every sequence and head with queries and keys."""
+    H, Hkv = Q.shape[0], K.shape[0]
+    for s in range(len(q_ptr) - 1):
+        qs, ks = slice(int(q_ptr[s]), int(q_ptr[s + 1])), slice(int(k_ptr[s]), int(k_ptr[s + 1]))
+        lq, lk = qs.stop - qs.start, ks.stop - ks.start
+        if lq == 0 or lk == 0:
+            continue
+        mask = np.ones((lq, lk), bool)
+        if causal:
+            mask = np.arange(lk)[None, :] <= np.arange(lq)[:, None] + (lk - lq)
+        for h in range(H):
+            yield h, h // (H // Hkv), qs, ks, mask
+
+
+def _packed_softmax(q, k, mask, scale):
+    """P (zero where masked) and ln sum exp (-inf for an empty row)."""
+    s = np.where(mask, scale * (q @ k.T), -np.inf)
+    m = s.max(-1, keepdims=True)
+    e = np.where(mask, np.exp(s - np.where(np.isfinite(m), m, 0.0)), 0.0)
+    l = e.sum(-1, keepdims=True)
+    with np.errstate(divide="ignore"):
+        lse = (np.where(np.isfinite(m), m, 0.0) + np.log(l))[:, 0]
+    return e / np.where(l > 0, l, 1.0), lse
+
+
+def packed_attn_fwd(Q, K, V, q_ptr, k_ptr, causal=False, scale=None):
+    """O [H, Tq, d] and lse [H, Tq]; rows of no sequence, and rows that see no key: 0 and -inf."""
+    Q, K, V = (np.asarray(t, np.float64) for t in (Q, K, V))
+    scale = 1.0 / math.sqrt(Q.shape[-1]) if scale is None else scale
+    O, lse = np.zeros_like(Q), np.full(Q.shape[:2], -np.inf)
+    for h, j, qs, ks, mask in _packed_parts(Q, K, q_ptr, k_ptr, causal):
+        P, lse[h, qs] = _packed_softmax(Q[h, qs], K[j, ks], mask, scale)
+        O[h, qs] = P @ V[j, ks]
+    return O, lse
+
+
+def packed_attn_bwd(Q, K, V, dO, q_ptr, k_ptr, causal=False, scale=None):
+    """dQ, dK, dV by the chain rule through the softmax, D_i = sum_j P_ij dP_ij from its definition."""
+    Q, K, V, dO = (np.asarray(t, np.float64) for t in (Q, K, V, dO))
+    scale = 1.0 / math.sqrt(Q.shape[-1]) if scale is None else scale
+    dQ, dK, dV = np.zeros_like(Q), np.zeros_like(K), np.zeros_like(V)
+    for h, j, qs, ks, mask in _packed_parts(Q, K, q_ptr, k_ptr, causal):
+        P, _ = _packed_softmax(Q[h, qs], K[j, ks], mask, scale)
+        dP = dO[h, qs] @ V[j, ks].T
+        dS = P * (dP - np.sum(P * dP, -1, keepdims=True))
+        dV[j, ks] += P.T @ dO[h, qs]
+        dQ[h, qs] = scale * (dS @ K[j, ks])
+        dK[j, ks] += scale * (dS.T @ Q[h, qs])
+    return dQ, dK, dV

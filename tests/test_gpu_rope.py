@@ -1,0 +1,207 @@
+"""GPU parity of the rotary positions (with and without the RMS norm) against
+the fp64 oracle, forward and backward (needs a GB300).
+
+Tolerances.  y is rounded once to bf16 (half a step: 2^-8 of the value) after
+fp32 arithmetic; angle, sine, cosine, norm and the two products of a pair cost
+at most a few 2^-24 of the pair's size each, taken together as 2^-20 (|a| + |b|).
+dweight is an fp32 sum of R terms, each good to 2^-20: at most
+(2^-20 + R 2^-24) sum |term|."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from parity_util import to64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dsv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from dynamic_block_sparse_projection_gb300 import binding
+    return binding
+
+
+def _grid_pos(T, Hl, Wl, start=0):
+    n = torch.arange(T * Hl * Wl, device="cuda")
+    return torch.stack([start + n // (Hl * Wl), (n // Wl) % Hl, n % Wl], 1).to(torch.int32)
+
+
+def _rand(seed, *shape):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)
+
+
+def _pair_size(z):
+    s = np.abs(z[..., 0::2]) + np.abs(z[..., 1::2])
+    return np.repeat(s, 2, -1)
+
+
+def _close(got, ref, scale, what):
+    tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -20 * scale + 1e-30
+    err = np.abs(to64(got) - ref)
+    assert np.all(err <= tol), f"{what}: {np.max(err / tol):.3f} of the tolerance"
+
+
+CASES = [  # B, H, grid, d, sections, start, layout
+    (1, 2, (4, 8, 8), 64, (20, 20, 20), 0, "bhnd"),          # the tiny workload's queries
+    (2, 3, (3, 5, 7), 128, (42, 42, 42), 0, "bnhd"),         # odd token count, projection layout
+    (1, 24, (2, 6, 10), 128, (16, 56, 56), 1000003, "qkv"),  # far positions, a slice of a fused projection
+    (3, 5, (1, 1, 1), 64, (16, 24, 24), 7, "bhnd"),          # one token
+    (1, 1, (1, 17, 61), 128, (128,), -5, "bnhd"),            # one axis, negative positions
+    (2, 2, (1, 9, 11), 64, (32, 16), 1 << 30, "bhnd"),       # two axes, very far
+    (1, 7, (2, 5, 5), 128, (2, 4, 6, 8), 0, "bnhd"),         # four axes, most channels unrotated
+]
+
+
+def _case(seed, B, H, grid, d, sections, start, layout):
+    N = grid[0] * grid[1] * grid[2]
+
+    def t(k):
+        if layout == "bhnd":
+            return _rand(seed + k, B, H, N, d)
+        if layout == "bnhd":
+            return _rand(seed + k, B, N, H, d).transpose(1, 2)
+        return _rand(seed + k, B, N, 3 * H, d).transpose(1, 2)[:, H:2 * H]
+
+    pos = _grid_pos(*grid, start)
+    A = len(sections)
+    pos = torch.cat([pos, pos[:, 1:2] * 3 - 4], 1)[:, :A].contiguous()
+    w = 1 + 0.25 * torch.randn(d, generator=torch.Generator(device="cuda").manual_seed(seed + 9), device="cuda")
+    return t(0), t(1), pos, w
+
+
+@pytest.mark.parametrize("case", CASES)
+@pytest.mark.parametrize("norm", [False, True])
+def test_rope_forward(dsv, case, norm):
+    sec = case[4]
+    x, _, pos, w = _case(11, *case)
+    w = w if norm else None
+    y = dsv.rope_axes(x, pos, sec, weight=w, eps=1e-5)
+    x64, p = to64(x), pos.cpu().numpy()
+    ref = oracle.rope_axes(x64, p, sec, weight=None if w is None else to64(w), eps=1e-5)
+    _close(y, ref, _pair_size(ref), "y")
+    assert torch.equal(y, dsv.rope_axes(x, pos, sec, weight=w, eps=1e-5))
+    if not norm:
+        k = sum(sec)
+        assert torch.equal(y[..., k:], x[..., k:])           # channels behind the bands: the same bits
+    z = x.clone()
+    assert dsv.rope_axes(z, pos, sec, weight=w, eps=1e-5, out=z) is z and torch.equal(z, y)   # in place
+
+
+@pytest.mark.parametrize("case", CASES)
+@pytest.mark.parametrize("norm", [False, True])
+def test_rope_backward(dsv, case, norm):
+    sec = case[4]
+    x, dy, pos, w = _case(23, *case)
+    w = w if norm else None
+    x64, g64, p = to64(x), to64(dy), pos.cpu().numpy()
+    if not norm:
+        ref = oracle.rope_axes_bwd(g64, p, sec)
+        dx = dsv.rope_axes_bwd(dy, pos, sec)
+        _close(dx, ref, _pair_size(ref), "dx")
+        return
+    dx, dw = dsv.rope_axes_bwd(dy, pos, sec, x=x, weight=w, eps=1e-5)
+    w64 = to64(w)
+    ref, dwr = oracle.rope_axes_bwd(g64, p, sec, x=x64, weight=w64, eps=1e-5)
+    g = oracle.rope_axes_bwd(g64, p, sec)
+    r = 1 / np.sqrt((x64 ** 2).mean(-1, keepdims=True) + 1e-5)
+    xh = x64 * r
+    # dx is a difference of two terms: its fp32 error goes by their sizes
+    size = r * (_pair_size(g * w64) + np.abs(xh) * np.mean(np.abs(g * w64 * xh), -1, keepdims=True))
+    _close(dx, ref, size, "dx")
+    R = x64[..., 0].size
+    tol = (2.0 ** -20 + R * 2.0 ** -24) * np.sum(_pair_size(g) * np.abs(xh), axis=(0, 1, 2))
+    assert np.all(np.abs(to64(dw) - dwr) <= tol), np.max(np.abs(to64(dw) - dwr) / tol)
+    # the gradient is that of the kernel's own forward: <dx, u> against differences of the fp64 forward
+    u = np.random.default_rng(5).standard_normal(x64.shape)
+    h = 1e-5
+    f = lambda t: (oracle.rope_axes(t, p, sec, weight=w64, eps=1e-5) * g64).sum()   # noqa: E731
+    num = (f(x64 + h * u) - f(x64 - h * u)) / (2 * h)
+    bound = np.sum((2.0 ** -8 * np.abs(ref) + 2.0 ** -20 * size) * np.abs(u)) + 1e-6 * np.sum(size * np.abs(u))
+    assert abs(num - (to64(dx) * u).sum()) <= bound
+    # the same again, in place over dy, with the caller's workspace
+    ws = torch.empty(dsv.rope_axes_bwd_workspace_bytes(case[3]), dtype=torch.uint8, device="cuda")
+    z = dy.clone()
+    dx2, dw2 = dsv.rope_axes_bwd(z, pos, sec, x=x, weight=w, eps=1e-5, dx=z, workspace=ws)
+    assert dx2 is z and torch.equal(z, dx) and torch.equal(dw, dw2)
+
+
+def test_rope_many_tokens_and_heads(dsv):
+    """More token tiles and heads than CTAs hold at once; per-batch positions; rows sampled."""
+    B, H, N, d, sec = 2, 9, 40961, 64, (20, 20, 20)
+    x, dy = _rand(1, B, N, H, d).transpose(1, 2), _rand(2, B, H, N, d)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    pos = torch.randint(-1000, 100000, (B, N, 3), generator=g, device="cuda", dtype=torch.int32)
+    w = 1 + 0.25 * torch.randn(d, generator=g, device="cuda")
+    y = dsv.rope_axes(x, pos, sec, weight=w)
+    dx, dw = dsv.rope_axes_bwd(dy, pos, sec, x=x, weight=w)
+    ref = oracle.rope_axes(to64(x), pos.cpu().numpy(), sec, weight=to64(w))
+    _close(y, ref, _pair_size(ref), "y")
+    _, dwr = oracle.rope_axes_bwd(to64(dy), pos.cpu().numpy(), sec, x=to64(x), weight=to64(w))
+    # each of the sums has random signs: the worst-case bound would allow R 2^-24 = 4 %; the chain of
+    # additions is at most 1216 parts / 32 + 32 in the join and items * heads rows in a part
+    chain = 32 + 38 + 32 + (B * H * N) // 1216
+    gg = oracle.rope_axes_bwd(to64(dy), pos.cpu().numpy(), sec)
+    xh = to64(x) / np.sqrt((to64(x) ** 2).mean(-1, keepdims=True) + 1e-6)
+    tol = (2.0 ** -20 + chain * 2.0 ** -24) * np.sum(_pair_size(gg) * np.abs(xh), axis=(0, 1, 2))
+    assert np.all(np.abs(to64(dw) - dwr) <= tol)
+
+
+def test_rope_values_that_are_not_numbers_stay_in_their_row(dsv):
+    x = _rand(4, 1, 2, 40, 64)
+    pos = _grid_pos(1, 5, 8)
+    clean = dsv.rope_axes(x, pos, (16, 16, 16), weight=torch.ones(64, device="cuda"))
+    x[0, 1, 7, 3] = float("nan")
+    x[0, 0, 9, 60] = float("inf")
+    y = dsv.rope_axes(x, pos, (16, 16, 16), weight=torch.ones(64, device="cuda"))
+    keep = torch.ones(2, 40, dtype=torch.bool, device="cuda")
+    keep[1, 7] = keep[0, 9] = False
+    assert torch.equal(y[0][keep], clean[0][keep]) and y[0, 1, 7].isnan().all()
+    z = dsv.rope_axes(x, pos, (16, 16, 16))
+    # without the norm a pair keeps to itself, and unrotated channels pass as they are
+    assert z[0, 1, 7, 2:4].isnan().all() and z[0, 1, 7].isnan().sum() == 2
+    assert torch.equal(z[0, 0, 9], dsv.rope_axes(x, pos, (16, 16, 16))[0, 0, 9]) and z[0, 0, 9, 60].isinf()
+
+
+def test_rope_empty(dsv):
+    x = torch.empty(0, 2, 5, 64, dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros(5, 1, dtype=torch.int32, device="cuda")
+    assert dsv.rope_axes(x, pos, (64,)).shape == x.shape
+    dx, dw = dsv.rope_axes_bwd(x, pos, (64,), x=x, weight=torch.ones(64, device="cuda"),
+                               dweight=torch.full((64,), 7.0, device="cuda"))
+    torch.cuda.synchronize()
+    assert not dw.any()
+
+
+def test_rope_offsets_beyond_32_bits(dsv):
+    """Rows whose element offset passes 2^31 (a strided view of a 4.4 GB buffer)."""
+    big = torch.empty(2, 1 << 23, 2, 64, dtype=torch.bfloat16, device="cuda")    # [B, N, H, d], 2^31 elements
+    x = big.transpose(1, 2)[:, :, -70:]
+    x.copy_(_rand(6, 2, 2, 70, 64))
+    pos = _grid_pos(1, 7, 10, 5)
+    y = dsv.rope_axes(x, pos, (20, 20, 20), out=x.new_empty(2, 2, 70, 64))
+    ref = oracle.rope_axes(to64(x), pos.cpu().numpy(), (20, 20, 20))
+    _close(y, ref, _pair_size(ref), "y")
+
+
+def test_rope_on_a_stream_and_in_a_graph(dsv):
+    x, pos = _rand(8, 1, 4, 300, 128), _grid_pos(3, 10, 10)
+    w = torch.full((128,), 1.5, device="cuda")
+    ref = dsv.rope_axes(x, pos, (42, 42, 42), weight=w)
+    dxr, dwr = dsv.rope_axes_bwd(ref, pos, (42, 42, 42), x=x, weight=w)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    y, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty(128, device="cuda")
+    ws = torch.empty(dsv.rope_axes_bwd_workspace_bytes(128), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        dsv.rope_axes(x, pos, (42, 42, 42), weight=w, out=y, stream=st)
+        dsv.rope_axes_bwd(y, pos, (42, 42, 42), x=x, weight=w, dx=dx, dweight=dw, workspace=ws, stream=st)
+    for _ in range(2):
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, ref) and torch.equal(dx, dxr) and torch.equal(dw, dwr)
