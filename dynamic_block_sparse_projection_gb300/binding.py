@@ -8,6 +8,7 @@ module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from pathlib import Path
@@ -171,6 +172,17 @@ def _stream(device: torch.device, stream=None) -> Optional[int]:
     return s.cuda_stream
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """The context of a launch on `device`: nothing to do where it is the current
+    device already (torch.cuda.device costs more than a small kernel's launch)."""
+    if device.type == "cuda" and device.index == torch.cuda.current_device():
+        return _HERE
+    return torch.cuda.device(device)
+
+
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, device: Optional[torch.device] = None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -204,16 +216,15 @@ def _dims(t, name: str, n: int) -> Tuple[int, ...]:
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != n:
         raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
-    return tuple(int(v) for v in t.shape)
+    return tuple(t.shape)
 
 
 def _shape(t, name: str, shape) -> None:
     """t must have exactly this shape (the library reads and writes whole tensors)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    want = tuple(int(v) for v in shape)
-    if tuple(t.shape) != want:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {want}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _room(t, name: str, n: int) -> None:
@@ -667,7 +678,7 @@ def rope_axes(x, pos, sections: Sequence[int], *, theta: float = 10000.0, weight
         out = torch.empty_like(x)
     else:
         _need_rows(out, "out", dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib.dsv_rope_axes_fwd(_view(x), _ptr(pos), pos_b, r, _ptr(weight), float(eps), _view(out),
                                      _stream(dev, stream)), "dsv_rope_axes_fwd")
     return out
@@ -709,7 +720,7 @@ def rope_axes_bwd(dy, pos, sections: Sequence[int], *, theta: float = 10000.0, x
         _need(dweight, "dweight", torch.float32, dev)
         nbytes = lib.dsv_rope_axes_bwd_workspace_bytes(r)
         ws = _scratch(nbytes, dev, workspace)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib.dsv_rope_axes_bwd(_view(dy), _view(x if weight is not None else None), _ptr(pos), pos_b, r,
                                      _ptr(weight), float(eps), _view(dx), _ptr(dweight), _ptr(ws), nbytes,
                                      _stream(dev, stream)), "dsv_rope_axes_bwd")
@@ -769,7 +780,7 @@ def packed_attn_fwd(Q, K, V, q_ptr, k_ptr, softmax_scale: float = 0.0, *, causal
     _need(lse, "lse", torch.float32, dev)
     nbytes = lib.dsv_packed_attn_fwd_workspace_bytes(p)
     ws = _scratch(nbytes, dev, workspace) if nbytes else None
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib.dsv_packed_attn_fwd(_view(Q), _view(K), _view(V), p, _ptr(q_ptr), _ptr(k_ptr), 1 if causal else 0,
                                        float(softmax_scale), _view(out), _ptr(lse), _ptr(ws), nbytes,
                                        _stream(dev, stream)), "dsv_packed_attn_fwd")
@@ -803,7 +814,7 @@ def packed_attn_bwd(Q, K, V, O, dO, lse, q_ptr, k_ptr, softmax_scale: float = 0.
             _need_rows(t, name, dev)
     nbytes = lib.dsv_packed_attn_bwd_workspace_bytes(p)
     ws = _scratch(nbytes, dev, workspace) if nbytes else None
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib.dsv_packed_attn_bwd(_view(Q), _view(K), _view(V), _view(O), _view(dO), _ptr(lse), p, _ptr(q_ptr),
                                        _ptr(k_ptr), 1 if causal else 0, float(softmax_scale),
                                        *[_view(t) for t in outs], _ptr(ws), nbytes, _stream(dev, stream)),

@@ -14,8 +14,8 @@
 //            tiles: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.
 //            Shared heads add up inside the product, so nothing is reduced
 //            afterwards and every output tile has one writer.
-//   q        persistent CTAs over the query tiles: S = Q K^T, dP = dO V^T,
-//            dQ += dS K.
+//   q        one CTA per SM over the query tiles, taking over the grid's other
+//            CTAs as it goes (packed_fwd.cu): S = Q K^T, dP = dO V^T, dQ += dS K.
 // S and dP are computed twice (seven products per tile pair instead of five),
 // which buys results that do not depend on the order CTAs run in.
 //
@@ -34,8 +34,9 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kKVThreads = 320;        // producer, MMA issuer, 8 compute warps
-constexpr int kQVWarp = 10;            // q kernel: V producer, which also finds the work items
-constexpr int kQThreads = 352;
+constexpr int kQVWarp = 10;            // q kernel: V producer
+constexpr int kQItemWarp = 11;         // q kernel: takes the work items
+constexpr int kQThreads = 384;
 constexpr int kComputeThreads = 256;
 
 // ---------------------------------------------------------------------------
@@ -452,7 +453,7 @@ __global__ void __launch_bounds__(kKVThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// dQ: persistent CTAs over the query tiles
+// dQ: one CTA per SM over the query tiles
 // ---------------------------------------------------------------------------
 struct QItem {
   int valid;
@@ -475,14 +476,15 @@ struct PQTraits {
   // K_j is read by S (early) and by dQ (late); V_j only by dP: separate rings
   static constexpr int NK = 3;
   static constexpr int NV = (8 * TILE + 2048 <= 227 * 1024) ? 3 : 2;
-  static constexpr int NBAR = 1 + 2 * NK + 2 * NV + 8 + 4;
-  static constexpr int SMEM_USED = 1024 + 2 * TILE + (NK + NV) * TILE + NBAR * 8 + 16 + 2 * (int)sizeof(QItem);
+  static constexpr int NBAR = 1 + 2 * NK + 2 * NV + 8 + 4 + 2 + 1;   // even: the answer after it is 16-byte aligned
+  static_assert(NBAR % 2 == 0, "alignment of the work request's answer");
+  static constexpr int SMEM_USED = 1024 + 2 * TILE + (NK + NV) * TILE + NBAR * 8 + 16 + 16 + 2 * (int)sizeof(QItem);
   static_assert(SMEM_USED <= 227 * 1024, "dQ tiles exceed shared memory");
   static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
   static constexpr uint32_t S_COL = 0, DP_COL = 128, DQ_COL = 256, DS_COL = 256 + D, TMEM_COLS = 512;
   static constexpr uint32_t TX = 128 * D * 2;
   static constexpr int HALF = 64;
-  static constexpr int CONSUMERS = 10;            // warps 0..9 read each item
+  static constexpr int CONSUMERS = 11;            // warps 0..10 read each item
 };
 
 template <int D>
@@ -490,8 +492,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
     packed_bwd_q_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
                         const __grid_constant__ PackedGeom g, const float* __restrict__ L2w,
-                        const float* __restrict__ Dw, long long total, float scale, __nv_bfloat16* dQ,
-                        long long dq_head, long long dq_tok, Ctl ctl) {
+                        const float* __restrict__ Dw, float scale, __nv_bfloat16* dQ, long long dq_head,
+                        long long dq_tok, Ctl ctl) {
   using T = PQTraits<D>;
   constexpr int NK = T::NK, NV = T::NV;
   constexpr int HALF = T::HALF;
@@ -517,7 +519,10 @@ __global__ void __launch_bounds__(kQThreads, 1)
   uint64_t* k_tail = qd_free + 1;                 // the last K tile of a sequence, before its rows are cut
   uint64_t* item_full = k_tail + 1;               // [2]
   uint64_t* item_free = item_full + 2;            // [2]
-  QItem* items = reinterpret_cast<QItem*>(item_free + 2);
+  uint64_t* near_end = item_free + 2;             // the K producer is about to finish its item
+  uint64_t* clc_full = near_end + 1;              // the work request's answer is there
+  void* clc = clc_full + 2;                       // 16 bytes
+  QItem* items = reinterpret_cast<QItem*>(clc_full + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -547,6 +552,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
       mbar_init(&item_full[s], 1);
       mbar_init(&item_free[s], T::CONSUMERS);
     }
+    mbar_init(near_end, 1);
+    mbar_init(clc_full, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -572,24 +579,17 @@ __global__ void __launch_bounds__(kQThreads, 1)
 
   if (tmem_base != tmem) {
     if (threadIdx.x == 0) set_error(ctl, DSV_ERR_INTERNAL, blockIdx.x);
-  } else if (warp == kQVWarp) {
-    // ---------------- work items and the V ring (one lane) ----------------
-    // A twelfth warp for the items would leave 160 registers a thread, too few
-    // for the compute warps; here an item is found once the V tiles of the one
-    // before it are under way.
-    if (lane == 0) {
-      tma_prefetch_desc(&tmV);
-      uint32_t gq = 0, i = 0;
-      bool ok = true;
-      for (long long idx = blockIdx.x; ok; idx += gridDim.x) {
-        QItem it = {};
-        if (idx < total) {
-          int slot;
-          packed_order(g, g.nslot_q, true, idx, it.kvh, slot);
-          PackedSeq q;
-          if (!packed_find(g, g.q_ptr, g.TQ, slot, q)) continue;
-          const int t0 = (slot - (q.q0 / g.TQ + q.s)) * g.TQ;
-          if (t0 >= q.lq) continue;
+  } else if (warp == kQItemWarp) {
+    // ---------------- work items (as in packed_fwd.cu) ----------------
+    int idx = blockIdx.x;
+    for (uint32_t i = 0, asked = 0;; ++asked) {
+      QItem it = {};
+      int slot;
+      packed_order(g, g.nslot_q, true, idx, it.kvh, slot);
+      PackedSeq q;
+      if (packed_find(g, g.q_ptr, g.TQ, slot, q)) {
+        const int t0 = (slot - (q.q0 / g.TQ + q.s)) * g.TQ;
+        if (t0 < q.lq) {
           it.valid = 1;
           it.tok = q.q0 + t0;
           it.ntok = min(g.TQ, q.lq - t0);
@@ -600,26 +600,55 @@ __global__ void __launch_bounds__(kQThreads, 1)
           it.lim0 = g.causal ? min(q.lk, q.lk - q.lq + t0 + 1) : q.lk;
           it.slot = slot;
         }
-        if (!mbar_wait(&item_free[i & 1], ((i >> 1) & 1u) ^ 1u, abort_flag, ctl, kid | W_ITEMFREE)) break;
-        items[i & 1] = it;
-        mbar_arrive(&item_full[i & 1]);
+      }
+      if (it.valid) {
+        if (!mbar_wait_warp(&item_free[i & 1], ((i >> 1) & 1u) ^ 1u, abort_flag, ctl, kid | W_ITEMFREE)) break;
+        if (lane == 0) {
+          items[i & 1] = it;
+          mbar_arrive(&item_full[i & 1]);
+        }
+        if (!mbar_wait_warp(near_end, i & 1u, abort_flag, ctl, kid | W_ITEM)) break;
         ++i;
-        if (!it.valid) break;
-        for (int n = 0; n < it.nt; ++n) {
-          const int s = (int)(gq % NV);
-          if (!mbar_wait(&v_empty[s], ((gq / NV) & 1u) ^ 1u, abort_flag, ctl, kid | W_KVEMPTY)) {
-            ok = false;
-            break;
-          }
+      }
+      if (lane == 0) clc_request(clc, clc_full);
+      if (!mbar_wait_warp(clc_full, asked & 1u, nullptr, ctl, kid | W_ITEM)) {
+        *abort_flag = 1;
+        break;
+      }
+      idx = clc_answer(clc);
+      fence_proxy_async_smem();        // read before the next answer is written
+      __syncwarp();
+      if (idx < 0) {
+        if (mbar_wait_warp(&item_free[i & 1], ((i >> 1) & 1u) ^ 1u, abort_flag, ctl, kid | W_ITEMFREE) && lane == 0) {
+          items[i & 1].valid = 0;
+          mbar_arrive(&item_full[i & 1]);
+        }
+        break;
+      }
+    }
+  } else if (warp == kQVWarp) {
+    // ---------------- the V ring ----------------
+    if (lane == 0) tma_prefetch_desc(&tmV);
+    uint32_t gq = 0;
+    bool ok = true;
+    QItem it;
+    for (uint32_t i = 0; ok && take(i, it); ++i) {
+      for (int n = 0; n < it.nt; ++n) {
+        const int s = (int)(gq % NV);
+        if (!mbar_wait_warp(&v_empty[s], ((gq / NV) & 1u) ^ 1u, abort_flag, ctl, kid | W_KVEMPTY)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
           mbar_arrive_expect_tx(&v_full[s], T::TX);
           for (int c = 0; c < T::NCH; ++c)
             tma_load_3d(sV + s * T::TILE + c * T::CHUNK, &tmV, &v_full[s], c * 64, it.kvh, it.key0 + n * 128);
-          ++gq;
         }
+        ++gq;
       }
-      for (uint32_t n = (gq > NV ? gq - NV : 0u); n < gq; ++n)
-        mbar_wait(&v_full[n % NV], (n / NV) & 1u, nullptr, ctl, kid | W_DRAIN);
     }
+    for (uint32_t n = (gq > NV ? gq - NV : 0u); n < gq; ++n)
+      mbar_wait(&v_full[n % NV], (n / NV) & 1u, nullptr, ctl, kid | W_DRAIN);
   } else if (warp == 0) {
     // ---------------- Q, dO and the K ring ----------------
     if (lane == 0) {
@@ -632,7 +661,10 @@ __global__ void __launch_bounds__(kQThreads, 1)
     bool ok = true;
     QItem it;
     for (uint32_t i = 0; ok && take(i, it); ++i) {
-      if (it.nt == 0) continue;
+      if (it.nt == 0) {
+        if (lane == 0) mbar_arrive(near_end);
+        continue;
+      }
       // Q and dO are A operands of every S and dP product: the previous tile's last ones must be done
       if (qd_issued > 0 &&
           !mbar_wait_warp(qd_free, (uint32_t)(qd_issued - 1) & 1u, abort_flag, ctl, kid | W_KVEMPTY))
@@ -658,6 +690,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
           mbar_arrive_expect_tx(bar, T::TX);
           for (int c = 0; c < T::NCH; ++c)
             tma_load_3d(sK + s * T::TILE + c * T::CHUNK, &tmK, bar, c * 64, it.kvh, it.key0 + n * 128);
+          if (n == max(0, it.nt - 2)) mbar_arrive(near_end);
         }
         if (tail) {
           const bool landed = mbar_wait_warp(k_tail, tails & 1u, nullptr, ctl, kid | W_TAIL);
@@ -899,13 +932,9 @@ cudaError_t launch_t(const PackedMaps& m, const PackedGeom& g, const dsv_view& O
   auto qk = packed_bwd_q_kernel<D>;
   constexpr int smem = PQTraits<D>::SMEM;
   if ((e = cudaFuncSetAttribute(qk, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-  int dev = 0, nsm = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  const long long total = (long long)g.Hkv * g.nslot_q;
-  qk<<<(unsigned)(total < nsm ? total : nsm), kQThreads, smem, st>>>(
-      m.Q, m.K, m.V, m.dO, g, L2w, Dw, total, scale, static_cast<__nv_bfloat16*>(dQ.ptr), dQ.head_stride,
-      dQ.token_stride, ctl);
+  qk<<<(unsigned)((long long)g.Hkv * g.nslot_q), kQThreads, smem, st>>>(
+      m.Q, m.K, m.V, m.dO, g, L2w, Dw, scale, static_cast<__nv_bfloat16*>(dQ.ptr), dQ.head_stride, dQ.token_stride,
+      ctl);
   return cudaGetLastError();
 }
 

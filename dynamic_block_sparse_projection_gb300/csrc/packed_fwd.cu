@@ -22,7 +22,8 @@
 //
 // Warp roles (256 threads): warp 0 loads Q and the K ring, warp 1 issues the
 // MMAs, warps 2..5 softmax and epilogue (one row per thread), warp 6 loads the
-// V ring, warp 7 finds the work items and hands them to the others through a
+// V ring, warp 7 takes the work items (one CTA of the grid each, taken over
+// while they have not started) and hands them to the others through a
 // two-entry ring, so that a search in the row pointers never stops the others.
 //
 // Split over the keys.  Each part writes its normalised O (fp32) and base-2
@@ -57,8 +58,9 @@ struct PFwdTraits {
   static constexpr int CHUNK = 128 * 128;
   static constexpr int TILE = NCH * CHUNK;
   static constexpr int NST = 3;
-  static constexpr int NBAR = 1 + 2 * NST + 3 * NST + 2 + 1 + 4;
-  static constexpr int SMEM_USED = 1024 + TILE + 2 * NST * TILE + NBAR * 8 + 16 + 2 * (int)sizeof(FwdItem);
+  static constexpr int NBAR = 1 + 2 * NST + 3 * NST + 2 + 1 + 4 + 2 + 1;   // even: the answer after it is 16-byte aligned
+  static constexpr int SMEM_USED = 1024 + TILE + 2 * NST * TILE + NBAR * 8 + 16 + 16 + 2 * (int)sizeof(FwdItem);
+  static_assert(NBAR % 2 == 0, "alignment of the work request's answer");
   static_assert(SMEM_USED <= 227 * 1024, "forward tiles exceed shared memory");
   // at least 120 KB so that one CTA owns an SM (and its 512 TMEM columns)
   static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
@@ -75,7 +77,7 @@ template <int D>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PackedGeom g, int nsplit,
-                      long long total, float scale_log2, __nv_bfloat16* O, long long o_head, long long o_tok,
+                      float scale_log2, __nv_bfloat16* O, long long o_head, long long o_tok,
                       float* LSE, float* Opart, float* Lpart, Ctl ctl) {
   using T = PFwdTraits<D>;
   constexpr int NST = T::NST;
@@ -96,7 +98,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   uint64_t* v_tail = mma_drain + 1;   // the last V tile of a sequence, before its rows are cut
   uint64_t* item_full = v_tail + 1;   // [2]
   uint64_t* item_free = item_full + 2;  // [2]
-  FwdItem* items = reinterpret_cast<FwdItem*>(item_free + 2);
+  uint64_t* near_end = item_free + 2;   // the K producer is about to finish its item
+  uint64_t* clc_full = near_end + 1;    // the work request's answer is there
+  void* clc = clc_full + 2;             // 16 bytes
+  FwdItem* items = reinterpret_cast<FwdItem*>(clc_full + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -120,6 +125,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       mbar_init(&item_full[s], 1);
       mbar_init(&item_free[s], kConsumers);
     }
+    mbar_init(near_end, 1);
+    mbar_init(clc_full, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -147,19 +154,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if (threadIdx.x == 0) set_error(ctl, DSV_ERR_INTERNAL, blockIdx.x);
   } else if (warp == kItemWarp) {
     // ---------------- work items ----------------
-    if (blockIdx.x == 0) packed_check_ptrs(g, ctl, lane);
-    if (lane == 0) {
-      uint32_t i = 0;
-      for (long long idx = blockIdx.x;; idx += gridDim.x) {
-        FwdItem it = {};
-        if (idx < total) {
-          const int sp = (int)(idx % nsplit);
-          int slot;
-          packed_order(g, g.nslot_q, true, idx / nsplit, it.kvh, slot);
-          PackedSeq q;
-          if (!packed_find(g, g.q_ptr, g.TQ, slot, q)) continue;
-          const int t0 = (slot - (q.q0 / g.TQ + q.s)) * g.TQ;
-          if (t0 >= q.lq) continue;
+    // The grid has a CTA for every item; the ones that run take over those
+    // that have not started, one at a time and only when the item in hand is
+    // nearly loaded, so that none waits in a queue while another SM idles.
+    int idx = blockIdx.x;
+    for (uint32_t i = 0, asked = 0;; ++asked) {
+      if (idx == 0) packed_check_ptrs(g, ctl, lane);
+      FwdItem it = {};
+      const int sp = idx % nsplit;
+      int slot;
+      packed_order(g, g.nslot_q, true, idx / nsplit, it.kvh, slot);
+      PackedSeq q;
+      if (packed_find(g, g.q_ptr, g.TQ, slot, q)) {
+        const int t0 = (slot - (q.q0 / g.TQ + q.s)) * g.TQ;
+        if (t0 < q.lq) {
           it.valid = 1;
           it.tok = q.q0 + t0;
           it.ntok = min(g.TQ, q.lq - t0);
@@ -167,7 +175,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const int first = g.causal ? min(q.lk, q.lk - q.lq + t0 + 1) : q.lk;
           const int last = g.causal ? min(q.lk, q.lk - q.lq + t0 + it.ntok) : q.lk;
           const int tiles = last > 0 ? (last + 127) / 128 : 0;
-          // a part takes at least kMinPart tiles, so that short sequences are not cut
+          // a part takes at least kPackedMinPart tiles, so that short sequences are not cut
           const int per = max((tiles + nsplit - 1) / nsplit, nsplit > 1 ? kPackedMinPart : 1);
           const int j0 = sp * per;
           it.nt = max(0, min(per, tiles - j0));
@@ -176,11 +184,30 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           it.lim0 = first - j0 * 128;
           it.part = (sp * g.Hkv + it.kvh) * g.nslot_q + slot;
         }
-        if (!mbar_wait(&item_free[i & 1], ((i >> 1) & 1u) ^ 1u, abort_flag, ctl, kid | W_ITEMFREE)) break;
-        items[i & 1] = it;
-        mbar_arrive(&item_full[i & 1]);
+      }
+      if (it.valid) {
+        if (!mbar_wait_warp(&item_free[i & 1], ((i >> 1) & 1u) ^ 1u, abort_flag, ctl, kid | W_ITEMFREE)) break;
+        if (lane == 0) {
+          items[i & 1] = it;
+          mbar_arrive(&item_full[i & 1]);
+        }
+        if (!mbar_wait_warp(near_end, i & 1u, abort_flag, ctl, kid | W_ITEM)) break;
         ++i;
-        if (!it.valid) break;
+      }
+      if (lane == 0) clc_request(clc, clc_full);
+      if (!mbar_wait_warp(clc_full, asked & 1u, nullptr, ctl, kid | W_ITEM)) {
+        *abort_flag = 1;
+        break;
+      }
+      idx = clc_answer(clc);
+      fence_proxy_async_smem();        // read before the next answer is written
+      __syncwarp();
+      if (idx < 0) {
+        if (mbar_wait_warp(&item_free[i & 1], ((i >> 1) & 1u) ^ 1u, abort_flag, ctl, kid | W_ITEMFREE) && lane == 0) {
+          items[i & 1].valid = 0;
+          mbar_arrive(&item_full[i & 1]);
+        }
+        break;
       }
     }
   } else if (warp == 0) {
@@ -194,7 +221,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     bool ok = true;
     FwdItem it;
     for (uint32_t i = 0; ok && take(i, it); ++i) {
-      if (it.nt == 0) continue;
+      if (it.nt == 0) {
+        if (lane == 0) mbar_arrive(near_end);
+        continue;
+      }
       // Q is the A operand of every S product: the previous item's last one must be done
       if (q_issued > 0 &&
           !mbar_wait_warp(&s_full[(gq - 1) % NST], ((gq - 1) / NST) & 1u, abort_flag, ctl, kid | W_QEMPTY))
@@ -215,6 +245,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           mbar_arrive_expect_tx(&k_full[s], T::TX);
           for (int c = 0; c < T::NCH; ++c)
             tma_load_3d(sK + s * T::TILE + c * T::CHUNK, &tmK, &k_full[s], c * 64, it.kvh, it.key0 + n * 128);
+          if (n == max(0, it.nt - 2)) mbar_arrive(near_end);
         }
         ++gq;
       }
@@ -542,15 +573,11 @@ cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
   auto kern = packed_fwd_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
   if (e != cudaSuccess) return e;
-  int dev = 0, nsm = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   const long long total = (long long)g.Hkv * g.nslot_q * nsplit;
-  const unsigned grid = (unsigned)(total < nsm ? total : nsm);
   float* Opart = nsplit > 1 ? static_cast<float*>(ws) : nullptr;
   float* Lpart = nsplit > 1 ? Opart + (size_t)total * 128 * D : nullptr;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(O.ptr);
-  kern<<<grid, kFwdThreads, T::SMEM, st>>>(tmQ, tmK, tmV, g, nsplit, total, scale * 1.4426950408889634f, o,
+  kern<<<(unsigned)total, kFwdThreads, T::SMEM, st>>>(tmQ, tmK, tmV, g, nsplit, scale * 1.4426950408889634f, o,
                                            O.head_stride, O.token_stride, lse, Opart, Lpart, ctl);
   if ((e = cudaGetLastError()) != cudaSuccess || nsplit == 1) return e;
   // rows of a tile over a few CTAs when the tiles alone would not fill the SMs

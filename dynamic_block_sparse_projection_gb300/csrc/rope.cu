@@ -271,12 +271,12 @@ RopeTable rope_table(const dsv_rope& r) {
     t.turn[i] = 0;
     t.axis[i] = -1;
   }
+  const double lt = log(r.theta);
   int at = 0;
   for (int a = 0; a < r.axes; ++a)
     for (int i = 0; i < r.section[a] / 2; ++i, ++at) {
-      // theta >= 1, so the frequency is at most 1 / (2 pi) turns
-      const double f = pow(r.theta, -2.0 * i / r.section[a]) * 0.15915494309189533577;
-      t.turn[at] = (uint64_t)ldexp(f, 64);
+      // theta^(-2i/c) / (2 pi) turns, at most 1 / (2 pi) as theta >= 1; * 2^64
+      t.turn[at] = (uint64_t)(exp(lt * (-2.0 * i / r.section[a])) * (0.15915494309189533577 * 18446744073709551616.0));
       t.axis[at] = (int8_t)a;
     }
   return t;
