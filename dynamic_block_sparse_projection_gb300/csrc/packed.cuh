@@ -65,7 +65,8 @@ __device__ __forceinline__ bool packed_find(const PackedGeom& g, const int32_t* 
   int lo = 0, hi = g.S - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (ptr[mid] / tile + mid <= slot) lo = mid; else hi = mid - 1;
+    // ptr[mid] / tile + mid <= slot
+    if (ptr[mid] < (long long)(slot - mid + 1) * tile) lo = mid; else hi = mid - 1;
   }
   q.s = lo;
   const int a = g.q_ptr[lo], b = g.q_ptr[lo + 1], c = g.k_ptr[lo], d = g.k_ptr[lo + 1];
@@ -74,7 +75,7 @@ __device__ __forceinline__ bool packed_find(const PackedGeom& g, const int32_t* 
   q.lq = b - a;
   q.k0 = c;
   q.lk = d - c;
-  return ptr[lo] / tile + lo <= slot;
+  return ptr[lo] < (long long)(slot - lo + 1) * tile;
 }
 
 // Both row pointers must rise within [0, T]: one warp reports the first
@@ -89,13 +90,13 @@ __device__ __forceinline__ void packed_check_ptrs(const PackedGeom& g, const Ctl
 // (key head, slot) of work index idx: chunks of head_chunk key heads, inside a
 // chunk the slots (descending where the later tiles of a causal sequence are
 // the longest), inside a slot the heads.
-__device__ __forceinline__ void packed_order(const PackedGeom& g, int nslot, bool descending, long long idx, int& kvh,
+__device__ __forceinline__ void packed_order(const PackedGeom& g, int nslot, bool descending, int idx, int& kvh,
                                              int& slot) {
-  const long long per = (long long)g.head_chunk * nslot;
-  const int c = (int)(idx / per);
-  const int in = (int)(idx - c * per);
+  const unsigned per = (unsigned)g.head_chunk * (unsigned)nslot;   // Hkv * nslot < 2^31
+  const int c = (int)((unsigned)idx / per);
+  const int in = idx - c * (int)per;
   const int heads = min(g.head_chunk, g.Hkv - c * g.head_chunk);
-  const int sl = in / heads;
+  const int sl = (int)((unsigned)in / (unsigned)heads);
   kvh = c * g.head_chunk + (in - sl * heads);
   slot = descending ? nslot - 1 - sl : sl;
 }

@@ -37,6 +37,7 @@ constexpr int kKVThreads = 320;        // producer, MMA issuer, 8 compute warps
 constexpr int kQVWarp = 10;            // q kernel: V producer
 constexpr int kQItemWarp = 11;         // q kernel: takes the work items
 constexpr int kQThreads = 384;
+constexpr int kAskAhead = 6;           // q kernel: key tiles before an item's last one at which the next is asked for
 constexpr int kComputeThreads = 256;
 
 // ---------------------------------------------------------------------------
@@ -601,7 +602,14 @@ __global__ void __launch_bounds__(kQThreads, 1)
           it.slot = slot;
         }
       }
-      if (it.valid) {
+      if (it.valid && it.nt == 0) {
+        // no key for any of its rows: written here, so that an item in the ring always has tiles
+        for (int r = lane; r < it.ntok * g.group; r += 32) {
+          const int rt = r / g.group, head = it.kvh * g.group + (r - rt * g.group);
+          uint4* dst = reinterpret_cast<uint4*>(dQ + head * dq_head + ((long long)it.tok + rt) * dq_tok);
+          for (int q = 0; q < D / 8; ++q) dst[q] = make_uint4(0, 0, 0, 0);
+        }
+      } else if (it.valid) {
         if (!mbar_wait_warp(&item_free[i & 1], ((i >> 1) & 1u) ^ 1u, abort_flag, ctl, kid | W_ITEMFREE)) break;
         if (lane == 0) {
           items[i & 1] = it;
@@ -661,10 +669,6 @@ __global__ void __launch_bounds__(kQThreads, 1)
     bool ok = true;
     QItem it;
     for (uint32_t i = 0; ok && take(i, it); ++i) {
-      if (it.nt == 0) {
-        if (lane == 0) mbar_arrive(near_end);
-        continue;
-      }
       // Q and dO are A operands of every S and dP product: the previous tile's last ones must be done
       if (qd_issued > 0 &&
           !mbar_wait_warp(qd_free, (uint32_t)(qd_issued - 1) & 1u, abort_flag, ctl, kid | W_KVEMPTY))
@@ -690,7 +694,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
           mbar_arrive_expect_tx(bar, T::TX);
           for (int c = 0; c < T::NCH; ++c)
             tma_load_3d(sK + s * T::TILE + c * T::CHUNK, &tmK, bar, c * 64, it.kvh, it.key0 + n * 128);
-          if (n == max(0, it.nt - 2)) mbar_arrive(near_end);
+          if (n == max(0, it.nt - kAskAhead)) mbar_arrive(near_end);
         }
         if (tail) {
           const bool landed = mbar_wait_warp(k_tail, tails & 1u, nullptr, ctl, kid | W_TAIL);
@@ -744,16 +748,14 @@ __global__ void __launch_bounds__(kQThreads, 1)
       return true;
     };
     uint32_t gq = 0;
-    int ne = 0;
     bool ok = true;
     QItem it;
     for (uint32_t i = 0; ok && take(i, it); ++i) {
-      if (it.nt == 0) continue;
-      // S and dP are single-buffered: the previous tile's last ones must have been read
-      ok = mbar_wait_warp(qd_full, (uint32_t)ne & 1u, abort_flag, ctl, kid | W_KV) &&
+      // S and dP are single-buffered: the previous item's last ones must have been read
+      ok = mbar_wait_warp(qd_full, i & 1u, abort_flag, ctl, kid | W_KV) &&
            (gq == 0 || mbar_wait_warp(sp_free, (gq - 1) & 1u, abort_flag, ctl, kid | W_SPFREE));
       if (ok) ok = issue_sdp(gq, 0u, 0u, nullptr);
-      if (ok && it.nt == 1) mma_commit_w(qd_free);    // the tile's last read of dO
+      if (ok && it.nt == 1) mma_commit_w(qd_free);    // the item's last read of dO
       for (int n = 0; ok && n < it.nt; ++n) {
         const uint32_t gn = gq + (uint32_t)n;
         uint32_t td = 0u;
@@ -770,7 +772,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
             ok = false;
             break;
           }
-          if (n + 2 == it.nt) mma_commit_w(qd_free);    // the tile's last read of dO
+          if (n + 2 == it.nt) mma_commit_w(qd_free);    // the item's last read of dO
         }
         // ds_full of an item's first tile also means that the previous item's dQ has been read
         if (!mbar_wait_warp_tested(ds_full, gn & 1u, td, abort_flag, ctl, kid | W_DSFULL)) {
@@ -790,7 +792,6 @@ __global__ void __launch_bounds__(kQThreads, 1)
       if (!ok) break;
       mma_commit_w(acc_done);
       gq += (uint32_t)it.nt;
-      ++ne;
     }
     // TMEM is freed after the closing CTA-wide sync only once every MMA is done
     mma_commit_w(mma_drain);
@@ -811,13 +812,6 @@ __global__ void __launch_bounds__(kQThreads, 1)
       const bool row_ok = rt < it.ntok;
       __nv_bfloat16* out = dQ + (long long)(it.kvh * g.group + rh) * dq_head + ((long long)it.tok + rt) * dq_tok +
                            hf * (D / 2);
-      if (it.nt == 0) {
-        if (row_ok) {
-#pragma unroll
-          for (int q = 0; q < D / 16; ++q) reinterpret_cast<uint4*>(out)[q] = make_uint4(0, 0, 0, 0);
-        }
-        continue;
-      }
       const long long vec = ((long long)it.kvh * g.nslot_q + it.slot) * 128 + r;
       const float nlse2 = L2w[vec];                // -lse*log2(e); -inf for a row without keys
       const float dd = Dw[vec];

@@ -20,11 +20,18 @@
 // tile's V rows past the sequence's end are zeroed in shared memory: their P
 // is 0, but 0 * NaN is not.
 //
-// Warp roles (256 threads): warp 0 loads Q and the K ring, warp 1 issues the
-// MMAs, warps 2..5 softmax and epilogue (one row per thread), warp 6 loads the
-// V ring, warp 7 takes the work items (one CTA of the grid each, taken over
-// while they have not started) and hands them to the others through a
-// two-entry ring, so that a search in the row pointers never stops the others.
+// Warp roles (three warpgroups): warp 0 loads Q and the K ring, warp 1 issues
+// the MMAs, warp 2 loads the V ring, warp 3 takes the work items (one CTA of
+// the grid each, taken over while they have not started) and hands them to the
+// others through a two-entry ring, so that a search in the row pointers never
+// stops the others; warps 4..7 softmax, warps 8..11 write O (one row per
+// thread each).  The softmax of the next item starts while the last PV product
+// and the output of this one are still under way: the writers copy O out of
+// tensor memory and give it back (o_free) before they store it.
+//
+// Registers.  A softmax row holds 128 scores and their 64 packed P at once (a
+// row whose sum overflows is redone), more than the 168 registers of 384 equal
+// threads: the warpgroups split the CTA's registers 88 : 256 : 160.
 //
 // Split over the keys.  Each part writes its normalised O (fp32) and base-2
 // log-sum to the workspace and combine_kernel joins them in part order:
@@ -58,8 +65,8 @@ struct PFwdTraits {
   static constexpr int CHUNK = 128 * 128;
   static constexpr int TILE = NCH * CHUNK;
   static constexpr int NST = 3;
-  static constexpr int NBAR = 1 + 2 * NST + 3 * NST + 2 + 1 + 4 + 2 + 1;   // even: the answer after it is 16-byte aligned
-  static constexpr int SMEM_USED = 1024 + TILE + 2 * NST * TILE + NBAR * 8 + 16 + 16 + 2 * (int)sizeof(FwdItem);
+  static constexpr int NBAR = 1 + 2 * NST + 3 * NST + 2 + 1 + 4 + 2 + 2 + 1;   // even: the answer after it is 16-byte aligned
+  static constexpr int SMEM_USED = 1024 + TILE + 2 * NST * TILE + NBAR * 8 + 16 + 16 + 2 * (int)sizeof(FwdItem) + 1024;
   static_assert(NBAR % 2 == 0, "alignment of the work request's answer");
   static_assert(SMEM_USED <= 227 * 1024, "forward tiles exceed shared memory");
   // at least 120 KB so that one CTA owns an SM (and its 512 TMEM columns)
@@ -68,17 +75,22 @@ struct PFwdTraits {
   static constexpr uint32_t TX = 128 * D * 2;
 };
 
-constexpr int kVWarp = 6, kItemWarp = 7, kFwdThreads = 256, kConsumers = 7;
+constexpr int kVWarp = 2, kItemWarp = 3, kFwdThreads = 384, kConsumers = 11;
+// Key tiles before an item's last one at which the next item is asked for: an
+// answer, the search and the loads take ~6000 clocks, a tile ~1600.
+constexpr int kAskAhead = 6;
+constexpr int kRegsControl = 88, kRegsSoftmax = 256, kRegsOut = 160, kRegsLaunch = 168;
+static_assert(kRegsControl + kRegsSoftmax + kRegsOut <= 3 * kRegsLaunch, "warpgroup registers exceed the launch's");
 
 enum : unsigned int { W_Q = 1, W_KEMPTY, W_K, W_P, W_V, W_S, W_O, W_OFINAL, W_DRAIN, W_QEMPTY, W_ITEM, W_ITEMFREE,
-                      W_TAIL };
+                      W_TAIL, W_OFREE, W_STAT };
 
 template <int D>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PackedGeom g, int nsplit,
                       float scale_log2, __nv_bfloat16* O, long long o_head, long long o_tok,
-                      float* LSE, float* Opart, float* Lpart, Ctl ctl) {
+                      float* LSE, float* Opart, float* Lpart, int wide, Ctl ctl) {
   using T = PFwdTraits<D>;
   constexpr int NST = T::NST;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -100,8 +112,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   uint64_t* item_free = item_full + 2;  // [2]
   uint64_t* near_end = item_free + 2;   // the K producer is about to finish its item
   uint64_t* clc_full = near_end + 1;    // the work request's answer is there
-  void* clc = clc_full + 2;             // 16 bytes
-  FwdItem* items = reinterpret_cast<FwdItem*>(clc_full + 4);
+  uint64_t* stat_full = clc_full + 1;   // l and m of the item's rows are in `stat`
+  uint64_t* o_free = stat_full + 1;     // O and `stat` of the item have been read
+  void* clc = bars + T::NBAR;           // 16 bytes
+  float2* stat = reinterpret_cast<float2*>(bars + T::NBAR + 2);   // [128] 1 / l, base-2 log-sum
+  FwdItem* items = reinterpret_cast<FwdItem*>(stat + 128);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -127,6 +142,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
     mbar_init(near_end, 1);
     mbar_init(clc_full, 1);
+    mbar_init(stat_full, 128);
+    mbar_init(o_free, 128);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -152,213 +169,245 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
   if (tmem_base != tmem) {
     if (threadIdx.x == 0) set_error(ctl, DSV_ERR_INTERNAL, blockIdx.x);
-  } else if (warp == kItemWarp) {
-    // ---------------- work items ----------------
-    // The grid has a CTA for every item; the ones that run take over those
-    // that have not started, one at a time and only when the item in hand is
-    // nearly loaded, so that none waits in a queue while another SM idles.
-    int idx = blockIdx.x;
-    for (uint32_t i = 0, asked = 0;; ++asked) {
-      if (idx == 0) packed_check_ptrs(g, ctl, lane);
-      FwdItem it = {};
-      const int sp = idx % nsplit;
-      int slot;
-      packed_order(g, g.nslot_q, true, idx / nsplit, it.kvh, slot);
-      PackedSeq q;
-      if (packed_find(g, g.q_ptr, g.TQ, slot, q)) {
-        const int t0 = (slot - (q.q0 / g.TQ + q.s)) * g.TQ;
-        if (t0 < q.lq) {
-          it.valid = 1;
-          it.tok = q.q0 + t0;
-          it.ntok = min(g.TQ, q.lq - t0);
-          // keys that the first and the last token of the tile see
-          const int first = g.causal ? min(q.lk, q.lk - q.lq + t0 + 1) : q.lk;
-          const int last = g.causal ? min(q.lk, q.lk - q.lq + t0 + it.ntok) : q.lk;
-          const int tiles = last > 0 ? (last + 127) / 128 : 0;
-          // a part takes at least kPackedMinPart tiles, so that short sequences are not cut
-          const int per = max((tiles + nsplit - 1) / nsplit, nsplit > 1 ? kPackedMinPart : 1);
-          const int j0 = sp * per;
-          it.nt = max(0, min(per, tiles - j0));
-          it.key0 = q.k0 + j0 * 128;
-          it.left = q.lk - j0 * 128;
-          it.lim0 = first - j0 * 128;
-          it.part = (sp * g.Hkv + it.kvh) * g.nslot_q + slot;
+  } else if (warp < 4) {
+    regs_dec<kRegsControl>();
+    if (warp == kItemWarp) {
+      // ---------------- work items ----------------
+      // The grid has a CTA for every item; the ones that run take over those
+      // that have not started, one at a time and only when the item in hand is
+      // nearly loaded, so that none waits in a queue while another SM idles.
+      int idx = blockIdx.x;
+      for (uint32_t i = 0, asked = 0;; ++asked) {
+        if (idx == 0) packed_check_ptrs(g, ctl, lane);
+        FwdItem it = {};
+        const int sp = idx % nsplit;
+        int slot;
+        packed_order(g, g.nslot_q, true, idx / nsplit, it.kvh, slot);
+        PackedSeq q;
+        if (packed_find(g, g.q_ptr, g.TQ, slot, q)) {
+          const int t0 = (slot - (q.q0 / g.TQ + q.s)) * g.TQ;
+          if (t0 < q.lq) {
+            it.valid = 1;
+            it.tok = q.q0 + t0;
+            it.ntok = min(g.TQ, q.lq - t0);
+            // keys that the first and the last token of the tile see
+            const int first = g.causal ? min(q.lk, q.lk - q.lq + t0 + 1) : q.lk;
+            const int last = g.causal ? min(q.lk, q.lk - q.lq + t0 + it.ntok) : q.lk;
+            const int tiles = last > 0 ? (last + 127) / 128 : 0;
+            // a part takes at least kPackedMinPart tiles, so that short sequences are not cut
+            const int per = max((tiles + nsplit - 1) / nsplit, nsplit > 1 ? kPackedMinPart : 1);
+            const int j0 = sp * per;
+            it.nt = max(0, min(per, tiles - j0));
+            it.key0 = q.k0 + j0 * 128;
+            it.left = q.lk - j0 * 128;
+            it.lim0 = first - j0 * 128;
+            it.part = (sp * g.Hkv + it.kvh) * g.nslot_q + slot;
+          }
+        }
+        if (it.valid && it.nt == 0) {
+          // no key for any of its rows: written here, so that an item in the ring always has tiles
+          for (int r = lane; r < it.ntok * g.group; r += 32) {
+            if (nsplit > 1) {
+              Lpart[(long long)it.part * 128 + r] = -INFINITY;
+              continue;
+            }
+            const int rt = r / g.group, head = it.kvh * g.group + (r - rt * g.group);
+            const long long tok = (long long)it.tok + rt;
+            uint4* dst = reinterpret_cast<uint4*>(O + head * o_head + tok * o_tok);
+            for (int q = 0; q < D / 8; ++q) dst[q] = make_uint4(0, 0, 0, 0);
+            LSE[(long long)head * g.Tq + tok] = -INFINITY;
+          }
+        } else if (it.valid) {
+          if (!mbar_wait_warp(&item_free[i & 1], ((i >> 1) & 1u) ^ 1u, abort_flag, ctl, kid | W_ITEMFREE)) break;
+          if (lane == 0) {
+            items[i & 1] = it;
+            mbar_arrive(&item_full[i & 1]);
+          }
+          if (!mbar_wait_warp(near_end, i & 1u, abort_flag, ctl, kid | W_ITEM)) break;
+          ++i;
+        }
+        if (lane == 0) clc_request(clc, clc_full);
+        if (!mbar_wait_warp(clc_full, asked & 1u, nullptr, ctl, kid | W_ITEM)) {
+          *abort_flag = 1;
+          break;
+        }
+        idx = clc_answer(clc);
+        fence_proxy_async_smem();        // read before the next answer is written
+        __syncwarp();
+        if (idx < 0) {
+          if (mbar_wait_warp(&item_free[i & 1], ((i >> 1) & 1u) ^ 1u, abort_flag, ctl, kid | W_ITEMFREE) && lane == 0) {
+            items[i & 1].valid = 0;
+            mbar_arrive(&item_full[i & 1]);
+          }
+          break;
         }
       }
-      if (it.valid) {
-        if (!mbar_wait_warp(&item_free[i & 1], ((i >> 1) & 1u) ^ 1u, abort_flag, ctl, kid | W_ITEMFREE)) break;
-        if (lane == 0) {
-          items[i & 1] = it;
-          mbar_arrive(&item_full[i & 1]);
-        }
-        if (!mbar_wait_warp(near_end, i & 1u, abort_flag, ctl, kid | W_ITEM)) break;
-        ++i;
-      }
-      if (lane == 0) clc_request(clc, clc_full);
-      if (!mbar_wait_warp(clc_full, asked & 1u, nullptr, ctl, kid | W_ITEM)) {
-        *abort_flag = 1;
-        break;
-      }
-      idx = clc_answer(clc);
-      fence_proxy_async_smem();        // read before the next answer is written
-      __syncwarp();
-      if (idx < 0) {
-        if (mbar_wait_warp(&item_free[i & 1], ((i >> 1) & 1u) ^ 1u, abort_flag, ctl, kid | W_ITEMFREE) && lane == 0) {
-          items[i & 1].valid = 0;
-          mbar_arrive(&item_full[i & 1]);
-        }
-        break;
-      }
-    }
-  } else if (warp == 0) {
-    // ---------------- Q and the K ring ----------------
-    if (lane == 0) {
-      tma_prefetch_desc(&tmQ);
-      tma_prefetch_desc(&tmK);
-    }
-    uint32_t gq = 0;                            // tiles issued so far
-    int q_issued = 0;
-    bool ok = true;
-    FwdItem it;
-    for (uint32_t i = 0; ok && take(i, it); ++i) {
-      if (it.nt == 0) {
-        if (lane == 0) mbar_arrive(near_end);
-        continue;
-      }
-      // Q is the A operand of every S product: the previous item's last one must be done
-      if (q_issued > 0 &&
-          !mbar_wait_warp(&s_full[(gq - 1) % NST], ((gq - 1) / NST) & 1u, abort_flag, ctl, kid | W_QEMPTY))
-        break;
+    } else if (warp == 0) {
+      // ---------------- Q and the K ring ----------------
       if (lane == 0) {
-        mbar_arrive_expect_tx(q_full, q_bytes);
-        for (int c = 0; c < T::NCH; ++c)
-          tma_load_3d(sQ + c * T::CHUNK, &tmQ, q_full, c * 64, it.kvh * g.group, it.tok);
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmK);
       }
-      ++q_issued;
-      for (int n = 0; n < it.nt; ++n) {
-        const int s = (int)(gq % NST);
-        if (gq >= NST && !mbar_wait_warp(&s_full[s], ((gq - NST) / NST) & 1u, abort_flag, ctl, kid | W_KEMPTY)) {
-          ok = false;
+      uint32_t gq = 0;                            // tiles issued so far
+      int q_issued = 0;
+      bool ok = true;
+      FwdItem it;
+      for (uint32_t i = 0; ok && take(i, it); ++i) {
+        // Q is the A operand of every S product: the previous item's last one must be done
+        if (q_issued > 0 &&
+            !mbar_wait_warp(&s_full[(gq - 1) % NST], ((gq - 1) / NST) & 1u, abort_flag, ctl, kid | W_QEMPTY))
           break;
-        }
         if (lane == 0) {
-          mbar_arrive_expect_tx(&k_full[s], T::TX);
+          mbar_arrive_expect_tx(q_full, q_bytes);
           for (int c = 0; c < T::NCH; ++c)
-            tma_load_3d(sK + s * T::TILE + c * T::CHUNK, &tmK, &k_full[s], c * 64, it.kvh, it.key0 + n * 128);
-          if (n == max(0, it.nt - 2)) mbar_arrive(near_end);
+            tma_load_3d(sQ + c * T::CHUNK, &tmQ, q_full, c * 64, it.kvh * g.group, it.tok);
         }
-        ++gq;
-      }
-    }
-    // every copy this warp started must land before the CTA exits
-    if (q_issued > 0) mbar_wait(q_full, (uint32_t)(q_issued - 1) & 1u, nullptr, ctl, kid | W_DRAIN);
-    for (uint32_t n = (gq > NST ? gq - NST : 0u); n < gq; ++n)
-      mbar_wait(&k_full[n % NST], (n / NST) & 1u, nullptr, ctl, kid | W_DRAIN);
-  } else if (warp == kVWarp) {
-    // ---------------- the V ring ----------------
-    if (lane == 0) tma_prefetch_desc(&tmV);
-    uint32_t gq = 0, tails = 0;
-    bool ok = true;
-    FwdItem it;
-    for (uint32_t i = 0; ok && take(i, it); ++i) {
-      for (int n = 0; n < it.nt; ++n) {
-        const int s = (int)(gq % NST);
-        if (gq >= NST && !mbar_wait_warp(&o_done[s], ((gq - NST) / NST) & 1u, abort_flag, ctl, kid | W_KEMPTY)) {
-          ok = false;
-          break;
-        }
-        const int have = it.left - n * 128;
-        const bool tail = have < 128;
-        uint64_t* bar = tail ? v_tail : &v_full[s];
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar, T::TX);
-          for (int c = 0; c < T::NCH; ++c)
-            tma_load_3d(sV + s * T::TILE + c * T::CHUNK, &tmV, bar, c * 64, it.kvh, it.key0 + n * 128);
-        }
-        if (tail) {
-          // rows past the sequence's end belong to the next one (or to nobody)
-          const bool landed = mbar_wait_warp(v_tail, tails & 1u, nullptr, ctl, kid | W_TAIL);
-          ++tails;
-          if (!landed) {
-            *abort_flag = 1;
+        ++q_issued;
+        for (int n = 0; n < it.nt; ++n) {
+          const int s = (int)(gq % NST);
+          if (gq >= NST && !mbar_wait_warp(&s_full[s], ((gq - NST) / NST) & 1u, abort_flag, ctl, kid | W_KEMPTY)) {
             ok = false;
             break;
           }
-          zero_tile_rows(sV + s * T::TILE, T::NCH, have, lane);
-          if (lane == 0) mbar_arrive(&v_full[s]);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&k_full[s], T::TX);
+            for (int c = 0; c < T::NCH; ++c)
+              tma_load_3d(sK + s * T::TILE + c * T::CHUNK, &tmK, &k_full[s], c * 64, it.kvh, it.key0 + n * 128);
+            if (n == max(0, it.nt - kAskAhead)) mbar_arrive(near_end);
+          }
+          ++gq;
         }
-        ++gq;
       }
-    }
-    for (uint32_t n = (gq > NST ? gq - NST : 0u); n < gq; ++n)
-      mbar_wait(&v_full[n % NST], (n / NST) & 1u, nullptr, ctl, kid | W_DRAIN);
-  } else if (warp == 1) {
-    // ---------------- MMA issuer (whole warp, one elected lane issues) ----------------
-    constexpr uint32_t IDS = idesc_bf16_f32(128, 128, false, false);
-    constexpr uint32_t IDO = idesc_bf16_f32(128, D, false, true);
-    const uint64_t dQ0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
-    const uint64_t dK0 = sdesc_sw128(smem_u32(sK), 16, 1024);
-    const uint64_t dV0 = sdesc_sw128(smem_u32(sV), T::CHUNK, 1024);
-    auto issue_S = [&](uint32_t gn) -> bool {
-      const int s = (int)(gn % NST);
-      if (!mbar_wait_warp(&k_full[s], (gn / NST) & 1u, abort_flag, ctl, kid | W_K)) return false;
-      tc_fence_after();
-      const uint32_t d_tmem = tmem + (uint32_t)s * T::S_COL;
-      const uint64_t kb = desc_off(dK0, (uint32_t)s * T::TILE);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * T::CHUNK + (kk & 3) * 32;
-        mma_ss_w(d_tmem, desc_off(dQ0, off), desc_off(kb, off), IDS, kk > 0 ? 1u : 0u);
+      // every copy this warp started must land before the CTA exits
+      if (q_issued > 0) mbar_wait(q_full, (uint32_t)(q_issued - 1) & 1u, nullptr, ctl, kid | W_DRAIN);
+      for (uint32_t n = (gq > NST ? gq - NST : 0u); n < gq; ++n)
+        mbar_wait(&k_full[n % NST], (n / NST) & 1u, nullptr, ctl, kid | W_DRAIN);
+    } else if (warp == kVWarp) {
+      // ---------------- the V ring ----------------
+      if (lane == 0) tma_prefetch_desc(&tmV);
+      uint32_t gq = 0, tails = 0;
+      bool ok = true;
+      FwdItem it;
+      for (uint32_t i = 0; ok && take(i, it); ++i) {
+        for (int n = 0; n < it.nt; ++n) {
+          const int s = (int)(gq % NST);
+          if (gq >= NST && !mbar_wait_warp(&o_done[s], ((gq - NST) / NST) & 1u, abort_flag, ctl, kid | W_KEMPTY)) {
+            ok = false;
+            break;
+          }
+          const int have = it.left - n * 128;
+          const bool tail = have < 128;
+          uint64_t* bar = tail ? v_tail : &v_full[s];
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar, T::TX);
+            for (int c = 0; c < T::NCH; ++c)
+              tma_load_3d(sV + s * T::TILE + c * T::CHUNK, &tmV, bar, c * 64, it.kvh, it.key0 + n * 128);
+          }
+          if (tail) {
+            // rows past the sequence's end belong to the next one (or to nobody)
+            const bool landed = mbar_wait_warp(v_tail, tails & 1u, nullptr, ctl, kid | W_TAIL);
+            ++tails;
+            if (!landed) {
+              *abort_flag = 1;
+              ok = false;
+              break;
+            }
+            zero_tile_rows(sV + s * T::TILE, T::NCH, have, lane);
+            if (lane == 0) mbar_arrive(&v_full[s]);
+          }
+          ++gq;
+        }
       }
-      mma_commit_w(&s_full[s]);
-      return true;
-    };
-    uint32_t gq = 0;
-    int ne = 0;
-    bool ok = true;
-    FwdItem it;
-    for (uint32_t i = 0; ok && take(i, it); ++i) {
-      if (it.nt == 0) continue;
-      ok = mbar_wait_warp(q_full, (uint32_t)ne & 1u, abort_flag, ctl, kid | W_Q);
-      if (ok) ok = issue_S(gq);
-      if (ok && it.nt > 1) ok = issue_S(gq + 1);
-      for (int n = 0; ok && n < it.nt; ++n) {
-        // S(n+2) reuses the buffer of P(n-1), whose PV product is already queued
-        const uint32_t gn = gq + (uint32_t)n;
+      for (uint32_t n = (gq > NST ? gq - NST : 0u); n < gq; ++n)
+        mbar_wait(&v_full[n % NST], (n / NST) & 1u, nullptr, ctl, kid | W_DRAIN);
+    } else if (warp == 1) {
+      // ---------------- MMA issuer (whole warp, one elected lane issues) ----------------
+      constexpr uint32_t IDS = idesc_bf16_f32(128, 128, false, false);
+      constexpr uint32_t IDO = idesc_bf16_f32(128, D, false, true);
+      const uint64_t dQ0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dK0 = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t dV0 = sdesc_sw128(smem_u32(sV), T::CHUNK, 1024);
+      auto issue_S = [&](uint32_t gn) -> bool {
         const int s = (int)(gn % NST);
-        const uint32_t ph = (gn / NST) & 1u;
-        const uint32_t v_tested = mbar_test(&v_full[s], ph);   // V_n normally landed long ago
-        if (n + 2 < it.nt && !issue_S(gn + 2)) {
-          ok = false;
-          break;
-        }
-        // P(0) of an item also means the softmax warps have read the previous item's O
-        if (!mbar_wait_warp(&p_full[s], ph, abort_flag, ctl, kid | W_P) ||
-            !mbar_wait_warp_tested(&v_full[s], ph, v_tested, abort_flag, ctl, kid | W_V)) {
-          ok = false;
-          break;
-        }
+        if (!mbar_wait_warp(&k_full[s], (gn / NST) & 1u, abort_flag, ctl, kid | W_K)) return false;
         tc_fence_after();
-        const uint32_t p_tmem = tmem + (uint32_t)s * T::S_COL;
-        const uint64_t vb = desc_off(dV0, (uint32_t)s * T::TILE);
+        const uint32_t d_tmem = tmem + (uint32_t)s * T::S_COL;
+        const uint64_t kb = desc_off(dK0, (uint32_t)s * T::TILE);
+  #pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * T::CHUNK + (kk & 3) * 32;
+          mma_ss_w(d_tmem, desc_off(dQ0, off), desc_off(kb, off), IDS, kk > 0 ? 1u : 0u);
+        }
+        mma_commit_w(&s_full[s]);
+        return true;
+      };
+      // S runs two tiles ahead of PV, and over the item's end: the next item's
+      // S(0) is issued before the last P of this one is waited for, so that the
+      // softmax finds it when it is done with this item.
+      uint32_t gq = 0;
+      int ne = 0;
+      FwdItem it;
+      bool ok = take(0, it);
+      if (ok) ok = mbar_wait_warp(q_full, 0, abort_flag, ctl, kid | W_Q) && issue_S(0);
+      while (ok) {
+        if (it.nt > 1 && !issue_S(gq + 1)) break;
+        FwdItem nx;
+        bool more = false;
+        for (int n = 0; n < it.nt; ++n) {
+          // S(n+2) reuses the buffer of P(n-1), whose PV product is already queued
+          const uint32_t gn = gq + (uint32_t)n;
+          const int s = (int)(gn % NST);
+          const uint32_t ph = (gn / NST) & 1u;
+          const uint32_t v_tested = mbar_test(&v_full[s], ph);   // V_n normally landed long ago
+          uint32_t ts = gn + 2;
+          bool ahead = n + 2 < it.nt;
+          if (n + 1 == it.nt) {
+            more = ahead = take((uint32_t)ne + 1, nx);
+            ts = gn + 1;
+            if (more && !mbar_wait_warp(q_full, (uint32_t)(ne + 1) & 1u, abort_flag, ctl, kid | W_Q)) {
+              ok = false;
+              break;
+            }
+          }
+          if (ahead && !issue_S(ts)) {
+            ok = false;
+            break;
+          }
+          // the first PV product overwrites O: the previous item's must have been read
+          if (n == 0 && ne > 0 && !mbar_wait_warp(o_free, (uint32_t)(ne - 1) & 1u, abort_flag, ctl, kid | W_OFREE)) {
+            ok = false;
+            break;
+          }
+          if (!mbar_wait_warp(&p_full[s], ph, abort_flag, ctl, kid | W_P) ||
+              !mbar_wait_warp_tested(&v_full[s], ph, v_tested, abort_flag, ctl, kid | W_V)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t p_tmem = tmem + (uint32_t)s * T::S_COL;
+          const uint64_t vb = desc_off(dV0, (uint32_t)s * T::TILE);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts_w(tmem + T::O_COL, p_tmem + kk * 8, desc_off(vb, kk * 16 * 128), IDO, (n > 0 || kk > 0) ? 1u : 0u);
-        mma_commit_w(&o_done[s]);
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts_w(tmem + T::O_COL, p_tmem + kk * 8, desc_off(vb, kk * 16 * 128), IDO, (n > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_w(&o_done[s]);
+        }
+        if (!ok) break;
+        mma_commit_w(o_final);
+        gq += (uint32_t)it.nt;
+        ++ne;
+        if (!more) break;
+        it = nx;
       }
-      if (!ok) break;
-      mma_commit_w(o_final);
-      gq += (uint32_t)it.nt;
-      ++ne;
+      // TMEM is freed after the closing CTA-wide sync only once every MMA is done
+      mma_commit_w(mma_drain);
+      mbar_wait_warp(mma_drain, 0, nullptr, ctl, kid | W_DRAIN);
     }
-    // TMEM is freed after the closing CTA-wide sync only once every MMA is done
-    mma_commit_w(mma_drain);
-    mbar_wait_warp(mma_drain, 0, nullptr, ctl, kid | W_DRAIN);
-  } else {
-    // ---------------- softmax warpgroup (warps 2..5) ----------------
+  } else if (warp < 8) {
+    regs_inc<kRegsSoftmax>();
+    // ---------------- softmax warpgroup (warps 4..7) ----------------
     const int sp = warp & 3;
     const int r = sp * 32 + lane;
-    const int rt = r / g.group, rh = r - rt * g.group;   // the row's token and head in the tile
+    const int rt = r / g.group;                  // the row's token in the tile
     const uint32_t lane_off = (uint32_t)(sp * 32) << 16;
     uint32_t gq = 0;
     int ne = 0;
@@ -366,19 +415,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     FwdItem it;
     for (uint32_t i = 0; ok && take(i, it); ++i) {
       const bool row_ok = rt < it.ntok;
-      const int head = it.kvh * g.group + rh;
-      const long long tok = (long long)it.tok + rt;
-      const long long prow = (long long)it.part * 128 + r;
-      if (it.nt == 0) {
-        if (row_ok && nsplit > 1) Lpart[prow] = -INFINITY;
-        if (row_ok && nsplit == 1) {
-          uint4* dst = reinterpret_cast<uint4*>(O + head * o_head + tok * o_tok);
-#pragma unroll
-          for (int q = 0; q < D / 8; ++q) dst[q] = make_uint4(0, 0, 0, 0);
-          LSE[(long long)head * g.Tq + tok] = -INFINITY;
-        }
-        continue;
-      }
       const int lim_r = g.causal ? min(it.left, it.lim0 + rt) : it.left;   // keys of this part that the row sees
       float m = 0.f, l = 0.f;
       uint32_t s_tested = 0u;   // S(n) already known complete (tested during tile n-1)
@@ -439,39 +475,38 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // covers a prefix of the part's keys, so a row that sees any of them
         // sees one in the first tile; one that sees none keeps 0).  A later
         // tile keeps it unless one of its values would pass 2^64.
-        float tsum;
         if (n == 0) {
           const float mx = row_max() * scale_log2;
           m = mx == -INFINITY ? 0.f : mx;
-          tsum = exponentiate(m);
-        } else {
+        }
+        float tsum;
+        bool redone = n == 0;
+        while (true) {
           tsum = exponentiate(m);
           // rows behind the tile's tokens hold another sequence's queries: they must not decide
-          if (__any_sync(0xffffffffu, row_ok && !(tsum <= 18446744073709551616.0f))) {   // 2^64
-            const float m_new = fmaxf(m, row_max() * scale_log2);
-            // rescale this warp's O rows once the previous PV product has landed
-            const uint32_t gp = gn - 1;
-            if (!mbar_wait_warp(&o_done[gp % NST], (gp / NST) & 1u, abort_flag, ctl, kid | W_O)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const float alpha = ex2(m - m_new);
-            l *= alpha;
-            m = m_new;
+          if (redone || !__any_sync(0xffffffffu, row_ok && !(tsum <= 18446744073709551616.0f))) break;   // 2^64
+          const float m_new = fmaxf(m, row_max() * scale_log2);
+          // rescale this warp's O rows once the previous PV product has landed
+          const uint32_t gp = gn - 1;
+          ok = mbar_wait_warp(&o_done[gp % NST], (gp / NST) & 1u, abort_flag, ctl, kid | W_O);
+          if (!ok) break;
+          tc_fence_after();
+          const float alpha = ex2(m - m_new);
+          l *= alpha;
+          m = m_new;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(tmem + lane_off + T::O_COL + c * 32, o);
-              tmem_ld_wait();
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lane_off + T::O_COL + c * 32, o);
+            tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-              tmem_st32(tmem + lane_off + T::O_COL + c * 32, o);
-            }
-            tmem_st_wait();
-            tsum = exponentiate(m);
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            tmem_st32(tmem + lane_off + T::O_COL + c * 32, o);
           }
+          tmem_st_wait();
+          redone = true;
         }
+        if (!ok) break;
         l += tsum;
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_st16(sb + c * 16, pk + c * 16);
@@ -479,38 +514,66 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         tc_fence_before();
         mbar_arrive(&p_full[s]);
       }
-      if (ok) ok = mbar_wait_warp(o_final, (uint32_t)ne & 1u, abort_flag, ctl, kid | W_OFINAL);
+      // one slot for the rows' statistics: the previous item's must have been read
+      if (ok && ne > 0) ok = mbar_wait_warp(o_free, (uint32_t)(ne - 1) & 1u, abort_flag, ctl, kid | W_OFREE);
       if (!ok) break;
-      tc_fence_after();
       // a row that saw no key has l = 0 and an O of zeros
-      const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
-      const float lse2 = m + log2f(l);
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32(tmem + lane_off + T::O_COL + c * 32, o);
-        tmem_ld_wait();
-        if (row_ok && nsplit > 1) {
-          float4* dst = reinterpret_cast<float4*>(Opart + prow * D + c * 32);
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            dst[q] = make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
-                                 __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
-        } else if (row_ok) {
-          uint32_t w[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            w[j] = pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
-          uint4* dst = reinterpret_cast<uint4*>(O + head * o_head + tok * o_tok + c * 32);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) dst[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-        }
-      }
-      if (row_ok) {
-        if (nsplit > 1) Lpart[prow] = lse2; else LSE[(long long)head * g.Tq + tok] = lse2 * kLn2;
-      }
+      stat[r] = make_float2(l > 0.f || l != l ? 1.0f / l : 0.f, m + log2f(l));
+      mbar_arrive(stat_full);
       gq += (uint32_t)it.nt;
       ++ne;
+    }
+  } else {
+    regs_dec<kRegsOut>();
+    // ---------------- output warpgroup (warps 8..11) ----------------
+    const int sp = warp & 3;
+    const int r = sp * 32 + lane;
+    const int rt = r / g.group, rh = r - rt * g.group;   // the row's token and head in the tile
+    const uint32_t lane_off = (uint32_t)(sp * 32) << 16;
+    int ne = 0;
+    FwdItem it;
+    for (uint32_t i = 0; take(i, it); ++i) {
+      const bool row_ok = rt < it.ntok;
+      const int head = it.kvh * g.group + rh;
+      const long long tok = (long long)it.tok + rt;
+      const long long prow = (long long)it.part * 128 + r;
+      __nv_bfloat16* dst = O + head * o_head + tok * o_tok;
+      float* ls = nsplit > 1 ? Lpart + prow : LSE + (long long)head * g.Tq + tok;
+      if (!mbar_wait_warp(stat_full, (uint32_t)ne & 1u, abort_flag, ctl, kid | W_STAT) ||
+          !mbar_wait_warp(o_final, (uint32_t)ne & 1u, abort_flag, ctl, kid | W_OFINAL))
+        break;
+      tc_fence_after();
+      uint32_t o[D];
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) tmem_ld32(tmem + lane_off + T::O_COL + c * 32, o + c * 32);
+      const float2 st = stat[r];
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(o_free);
+      ++ne;
+      if (row_ok) {
+#pragma unroll
+        for (int j = 0; j < D; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * st.x);
+        if (nsplit > 1) {
+#pragma unroll
+          for (int q = 0; q < D / 8; ++q) st_global_32(Opart + prow * D + q * 8, o + q * 8);
+          *ls = st.y;
+        } else {
+#pragma unroll
+          for (int j = 0; j < D / 2; ++j)
+            o[j] = pack_bf16x2(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
+          if (wide) {
+#pragma unroll
+            for (int q = 0; q < D / 16; ++q) st_global_32(dst + q * 16, o + q * 8);
+          } else {
+#pragma unroll
+            for (int q = 0; q < D / 8; ++q)
+              reinterpret_cast<uint4*>(dst)[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          }
+          *ls = st.y * kLn2;
+        }
+      }
+      __syncwarp();
     }
   }
 
@@ -573,12 +636,20 @@ cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
   auto kern = packed_fwd_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
   if (e != cudaSuccess) return e;
+  // a build with fewer registers per thread could not serve the warpgroups' split: never launch that
+  static const int launched = [&] {
+    cudaFuncAttributes a{};
+    return cudaFuncGetAttributes(&a, kern) == cudaSuccess ? a.numRegs : 0;
+  }();
+  if (launched < kRegsLaunch) return cudaErrorInvalidKernelImage;
   const long long total = (long long)g.Hkv * g.nslot_q * nsplit;
   float* Opart = nsplit > 1 ? static_cast<float*>(ws) : nullptr;
   float* Lpart = nsplit > 1 ? Opart + (size_t)total * 128 * D : nullptr;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(O.ptr);
+  // rows on 32-byte boundaries are stored a sector at a time
+  const int wide = (reinterpret_cast<uintptr_t>(O.ptr) % 32 == 0 && O.head_stride % 16 == 0 && O.token_stride % 16 == 0);
   kern<<<(unsigned)total, kFwdThreads, T::SMEM, st>>>(tmQ, tmK, tmV, g, nsplit, scale * 1.4426950408889634f, o,
-                                           O.head_stride, O.token_stride, lse, Opart, Lpart, ctl);
+                                           O.head_stride, O.token_stride, lse, Opart, Lpart, wide, ctl);
   if ((e = cudaGetLastError()) != cudaSuccess || nsplit == 1) return e;
   // rows of a tile over a few CTAs when the tiles alone would not fill the SMs
   const long long tiles = (long long)g.Hkv * g.nslot_q;
