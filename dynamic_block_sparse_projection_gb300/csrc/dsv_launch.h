@@ -123,7 +123,6 @@ struct PackedMaps {
 cudaError_t launch_packed_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                               const dsv_packed& p, const int32_t* q_ptr, const int32_t* k_ptr, int causal, float scale,
                               const dsv_view& O, float* lse, void* ws, const Ctl& ctl, cudaStream_t st);
-int packed_fwd_splits(const dsv_packed& p);
 size_t packed_fwd_ws_bytes(const dsv_packed& p);
 cudaError_t launch_packed_bwd(const PackedMaps& m, const dsv_packed& p, const int32_t* q_ptr, const int32_t* k_ptr,
                               int causal, float scale, const dsv_view& O, const dsv_view& dO, const float* lse,

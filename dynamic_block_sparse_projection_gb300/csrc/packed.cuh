@@ -78,6 +78,59 @@ __device__ __forceinline__ bool packed_find(const PackedGeom& g, const int32_t* 
   return ptr[lo] < (long long)(slot - lo + 1) * tile;
 }
 
+// Split tiles: item m of a key head, over the sequences in order, inside one
+// over its query tiles, inside a tile over the parts of `part_keys` keys.  One
+// warp adds up the sequences' item counts (they are few where tiles are split:
+// fewer than SMs).  part < 0: m is past the last item.
+struct PackedPart {
+  int tile, part, parts;
+};
+__device__ __forceinline__ int packed_items(const PackedGeom& g, int part_keys, int s, int& parts) {
+  const int a = g.q_ptr[s], b = g.q_ptr[s + 1], c = g.k_ptr[s], d = g.k_ptr[s + 1];
+  parts = 0;
+  if (a < 0 || b < a || b > g.Tq || c < 0 || d < c || d > g.Tk) return 0;
+  parts = max(1, (d - c + part_keys - 1) / part_keys);
+  return (b - a + g.TQ - 1) / g.TQ * parts;
+}
+__device__ __forceinline__ PackedPart packed_part(const PackedGeom& g, int part_keys, int m, int lane, PackedSeq& q) {
+  int base = 0;
+  for (int s0 = 0; s0 < g.S; s0 += 32) {
+    int parts = 0;
+    const int own = s0 + lane < g.S ? packed_items(g, part_keys, s0 + lane, parts) : 0;
+    int inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + inc > m);
+    if (hit != 0u) {
+      const int l = __ffs(hit) - 1;
+      const int first = base + __shfl_sync(0xffffffffu, inc - own, l);
+      parts = __shfl_sync(0xffffffffu, parts, l);
+      q.s = s0 + l;
+      q.q0 = g.q_ptr[q.s];
+      q.lq = g.q_ptr[q.s + 1] - q.q0;
+      q.k0 = g.k_ptr[q.s];
+      q.lk = g.k_ptr[q.s + 1] - q.k0;
+      const int in = m - first;
+      return {in / parts, in % parts, parts};
+    }
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return {0, -1, 0};
+}
+// Items of a key head before query tile `tile` of sequence s, by one warp.
+__device__ __forceinline__ int packed_part_base(const PackedGeom& g, int part_keys, int s, int tile, int lane,
+                                                int& parts) {
+  int sum = 0, p = 0;
+  for (int t = lane; t < s; t += 32) sum += packed_items(g, part_keys, t, p);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  packed_items(g, part_keys, s, parts);
+  return sum + tile * parts;
+}
+
 // Both row pointers must rise within [0, T]: one warp reports the first
 // sequence that breaks it (its tiles are skipped by packed_find).
 __device__ __forceinline__ void packed_check_ptrs(const PackedGeom& g, const Ctl& ctl, int lane) {

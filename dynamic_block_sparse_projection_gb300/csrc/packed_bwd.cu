@@ -12,8 +12,10 @@
 //            tokens, gets -inf there, so its P is exp2(-inf) = 0.
 //   kv       one CTA per key tile and key head, over the sequence's query
 //            tiles: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.
-//            Shared heads add up inside the product, so nothing is reduced
-//            afterwards and every output tile has one writer.
+//            Shared heads add up inside the product, and every output tile has
+//            one writer.  With fewer key tiles than SMs the query tiles of each
+//            are split over several CTAs and the join kernel adds their fp32
+//            sums in order.
 //   q        one CTA per SM over the query tiles, taking over the grid's other
 //            CTAs as it goes (packed_fwd.cu): S = Q K^T, dP = dO V^T, dQ += dS K.
 // S and dP are computed twice (seven products per tile pair instead of five),
@@ -115,13 +117,37 @@ struct PKVTraits {
   __host__ __device__ static constexpr int chunk_of(int q) { return (q % W) / (W / 2); }
 };
 
+// A key tile and the query tiles that see it, cut into `nsplit` runs of `per`
+// (the last ones may be empty).
+struct KeyTile {
+  PackedSeq q;
+  int kt0, keys;     // first key inside the sequence, keys in the tile
+  int off;           // causal: query token t sees key k when k <= t + off
+  int i0, cnt, per;
+};
+__device__ __forceinline__ bool key_tile(const PackedGeom& g, int slot, int nsplit, KeyTile& k) {
+  if (!packed_find(g, g.k_ptr, 128, slot, k.q)) return false;
+  k.kt0 = (slot - (k.q.k0 / 128 + k.q.s)) * 128;
+  if (k.kt0 >= k.q.lk) return false;
+  k.keys = min(128, k.q.lk - k.kt0);
+  k.off = k.q.lk - k.q.lq;
+  const int qtiles = (k.q.lq + g.TQ - 1) / g.TQ;
+  // the first query token that sees the tile's first key
+  const long long t = g.causal ? min((long long)k.q.lq, max(0LL, (long long)k.kt0 - k.off)) : 0;
+  k.i0 = (int)t / g.TQ;
+  k.cnt = max(0, qtiles - k.i0);
+  k.per = max((k.cnt + nsplit - 1) / nsplit, nsplit > 1 ? kPackedMinPart : 1);
+  return true;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kKVThreads, 1)
     packed_bwd_kv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
                          const __grid_constant__ PackedGeom g, const float* __restrict__ L2w,
                          const float* __restrict__ Dw, float scale, __nv_bfloat16* dK, long long dk_head,
-                         long long dk_tok, __nv_bfloat16* dV, long long dv_head, long long dv_tok, Ctl ctl) {
+                         long long dk_tok, __nv_bfloat16* dV, long long dv_head, long long dv_tok, int nsplit,
+                         float* part, Ctl ctl) {
   using T = PKVTraits<D>;
   constexpr int NST = T::NST;
   constexpr int W = T::W;
@@ -129,18 +155,14 @@ __global__ void __launch_bounds__(kKVThreads, 1)
 
   // the CTA's key tile; every thread works it out (the same loads for all)
   int kvh, slot;
-  packed_order(g, g.nslot_k, false, blockIdx.x, kvh, slot);
-  PackedSeq q;
-  if (!packed_find(g, g.k_ptr, 128, slot, q)) return;
-  const int kt0 = (slot - (q.k0 / 128 + q.s)) * 128;          // first key of the tile inside its sequence
-  if (kt0 >= q.lk) return;
-  const int keys = min(128, q.lk - kt0);
-  // query token t sees key k when k <= t + off (causal)
-  const int off = q.lk - q.lq;
-  const int qtiles = (q.lq + g.TQ - 1) / g.TQ;
-  const long long t_first = g.causal ? min((long long)q.lq, max(0LL, (long long)kt0 - off)) : 0;
-  const int i0 = (int)t_first / g.TQ;                         // first query tile that sees key kt0
-  const int cnt = max(0, qtiles - i0);
+  packed_order(g, g.nslot_k, false, blockIdx.x / nsplit, kvh, slot);
+  KeyTile kt;
+  if (!key_tile(g, slot, nsplit, kt)) return;
+  const PackedSeq& q = kt.q;
+  const int kt0 = kt.kt0, keys = kt.keys, off = kt.off;
+  const int piece = blockIdx.x % nsplit;
+  const int i0 = kt.i0 + piece * kt.per;                      // first query tile of this CTA
+  const int cnt = max(0, min(kt.per, kt.cnt - piece * kt.per));
   const int qslot0 = q.q0 / g.TQ + q.s + i0;
 
   uint8_t* sbase = smem_align1024(smem_raw);
@@ -164,7 +186,9 @@ __global__ void __launch_bounds__(kKVThreads, 1)
   const unsigned int kid = (unsigned int)KID_PACKED_KV << 8;
   const long long krow0 = (long long)q.k0 + kt0;
 
-  if (cnt == 0) {                                 // no query sees these keys
+  if (cnt == 0) {
+    if (nsplit > 1) return;                       // the join knows how many parts there are
+    // no query sees these keys
     for (int i = threadIdx.x; i < keys * (D / 8); i += blockDim.x) {
       const int r = i / (D / 8), c = i % (D / 8);
       *reinterpret_cast<uint4*>(dK + kvh * dk_head + (krow0 + r) * dk_tok + c * 8) = make_uint4(0, 0, 0, 0);
@@ -433,7 +457,11 @@ __global__ void __launch_bounds__(kKVThreads, 1)
           uint32_t o[32];
           tmem_ld32(tmem + lane_off + col + c * 32, o);
           tmem_ld_wait();
-          if (kr < keys) {
+          if (nsplit > 1) {
+            float* dst = part + (((long long)blockIdx.x * 2 + t) * 128 + kr) * D + hf * (D / 2) + c * 32;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) st_global_32(dst + p * 8, o + p * 8);
+          } else if (kr < keys) {
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -451,6 +479,39 @@ __global__ void __launch_bounds__(kKVThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, T::TMEM_COLS);
+}
+
+// Adds the parts of dV and dK (fp32, unscaled) in order.  One CTA per (key
+// tile, key head, matrix); D/4 threads a row.
+template <int D>
+__global__ void __launch_bounds__(256) packed_bwd_join_kernel(const __grid_constant__ PackedGeom g, int nsplit,
+                                                              const float* __restrict__ part, float scale,
+                                                              __nv_bfloat16* dK, long long dk_head, long long dk_tok,
+                                                              __nv_bfloat16* dV, long long dv_head, long long dv_tok) {
+  int kvh, slot;
+  packed_order(g, g.nslot_k, false, blockIdx.x, kvh, slot);
+  KeyTile kt;
+  if (!key_tile(g, slot, nsplit, kt)) return;
+  const int parts = (kt.cnt + kt.per - 1) / kt.per, t = blockIdx.y;
+  const float mul = t == 0 ? 1.0f : scale;
+  __nv_bfloat16* out = t == 0 ? dV + kvh * dv_head : dK + kvh * dk_head;
+  const long long tok = t == 0 ? dv_tok : dk_tok;
+  const int c = threadIdx.x % (D / 4);
+  for (int r = threadIdx.x / (D / 4); r < kt.keys; r += 256 / (D / 4)) {
+    const float4* src = reinterpret_cast<const float4*>(part) +
+                        (((long long)blockIdx.x * nsplit * 2 + t) * 128 + r) * (D / 4) + c;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+      const float4 v = __ldcs(src + (long long)p * 2 * 128 * (D / 4));
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    *reinterpret_cast<uint2*>(out + ((long long)kt.q.k0 + kt.kt0 + r) * tok + c * 4) =
+        make_uint2(pack_bf16x2(s.x * mul, s.y * mul), pack_bf16x2(s.z * mul, s.w * mul));
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -902,7 +963,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
 template <int D>
 cudaError_t launch_t(const PackedMaps& m, const PackedGeom& g, const dsv_view& O, const dsv_view& dO, const float* lse,
                      float scale, const dsv_view& dQ, const dsv_view& dK, const dsv_view& dV, void* ws,
-                     const Ctl& ctl, cudaStream_t st) {
+                     int nsplit, const Ctl& ctl, cudaStream_t st) {
   cudaError_t e;
   const size_t vec = (size_t)g.Hkv * g.nslot_q * 128;
   float* Dw = static_cast<float*>(ws);
@@ -917,9 +978,18 @@ cudaError_t launch_t(const PackedMaps& m, const PackedGeom& g, const dsv_view& O
     auto kv = packed_bwd_kv_kernel<D>;
     constexpr int smem = PKVTraits<D>::SMEM;
     if ((e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-    kv<<<(unsigned)((long long)g.Hkv * g.nslot_k), kKVThreads, smem, st>>>(
-        m.Q, m.K, m.V, m.dO, g, L2w, Dw, scale, static_cast<__nv_bfloat16*>(dK.ptr), dK.head_stride, dK.token_stride,
-        static_cast<__nv_bfloat16*>(dV.ptr), dV.head_stride, dV.token_stride, ctl);
+    const unsigned tiles = (unsigned)((long long)g.Hkv * g.nslot_k);
+    float* part = L2w + vec;
+    __nv_bfloat16* k_out = static_cast<__nv_bfloat16*>(dK.ptr);
+    __nv_bfloat16* v_out = static_cast<__nv_bfloat16*>(dV.ptr);
+    kv<<<tiles * nsplit, kKVThreads, smem, st>>>(m.Q, m.K, m.V, m.dO, g, L2w, Dw, scale, k_out, dK.head_stride,
+                                                 dK.token_stride, v_out, dV.head_stride, dV.token_stride, nsplit,
+                                                 part, ctl);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (nsplit > 1)
+      packed_bwd_join_kernel<D><<<dim3(tiles, 2), 256, 0, st>>>(g, nsplit, part, scale, k_out, dK.head_stride,
+                                                                 dK.token_stride, v_out, dV.head_stride,
+                                                                 dV.token_stride);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (g.Tq == 0) return cudaSuccess;
@@ -934,8 +1004,25 @@ cudaError_t launch_t(const PackedMaps& m, const PackedGeom& g, const dsv_view& O
 
 }  // namespace
 
+// Runs of query tiles per key tile in the kv kernel.  With at least one key
+// tile per SM each CTA takes all query tiles of its own.  With fewer (few keys
+// against many queries: text), they are cut into runs of at least
+// kPackedMinPart tiles, enough for two rounds of the SMs, whose fp32 sums the
+// join kernel adds.
+static int bwd_splits(const dsv_packed& p) {
+  if (p.S <= 0 || p.Tq <= 0 || p.Tk <= 0) return 1;
+  const long long k_tiles = (p.Tk + 127) / 128, TQ = 128 / (p.H / p.Hkv);
+  const long long ctas = (long long)p.Hkv * (k_tiles > p.S ? k_tiles : p.S);
+  if (ctas >= kPackedSMs) return 1;
+  const long long q_tiles = (p.Tq + TQ * p.S - 1) / (TQ * p.S);      // of a sequence, on average
+  const long long n = (2LL * kPackedSMs + ctas - 1) / ctas, most = (q_tiles + kPackedMinPart - 1) / kPackedMinPart;
+  return (int)(n < most ? n : most);
+}
+
 size_t packed_bwd_ws_bytes(const dsv_packed& p) {
-  return 2 * (size_t)p.Hkv * packed_slots(p.Tq, 128 / (p.H / p.Hkv), p.S) * 128 * sizeof(float);
+  const size_t vec = 2 * (size_t)p.Hkv * packed_slots(p.Tq, 128 / (p.H / p.Hkv), p.S) * 128 * sizeof(float);
+  const int n = bwd_splits(p);
+  return n == 1 ? vec : vec + (size_t)p.Hkv * packed_slots(p.Tk, 128, p.S) * n * 2 * 128 * p.d * sizeof(float);
 }
 
 cudaError_t launch_packed_bwd(const PackedMaps& m, const dsv_packed& p, const int32_t* q_ptr, const int32_t* k_ptr,
@@ -943,8 +1030,9 @@ cudaError_t launch_packed_bwd(const PackedMaps& m, const dsv_packed& p, const in
                               const dsv_view& dQ, const dsv_view& dK, const dsv_view& dV, void* ws, const Ctl& ctl,
                               cudaStream_t st) {
   const PackedGeom g = packed_geom(p, q_ptr, k_ptr, causal);
-  return p.d == 128 ? launch_t<128>(m, g, O, dO, lse, scale, dQ, dK, dV, ws, ctl, st)
-                    : launch_t<64>(m, g, O, dO, lse, scale, dQ, dK, dV, ws, ctl, st);
+  const int n = bwd_splits(p);
+  return p.d == 128 ? launch_t<128>(m, g, O, dO, lse, scale, dQ, dK, dV, ws, n, ctl, st)
+                    : launch_t<64>(m, g, O, dO, lse, scale, dQ, dK, dV, ws, n, ctl, st);
 }
 
 }  // namespace dsv

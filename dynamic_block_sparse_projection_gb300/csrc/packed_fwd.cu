@@ -38,6 +38,8 @@
 // results do not depend on which part finished first.
 #include <math.h>
 
+#include <type_traits>
+
 #include "packed.cuh"
 
 namespace dsv {
@@ -55,7 +57,7 @@ struct FwdItem {
   int nt;      // key tiles of this part
   int lim0;    // keys of this part that the first token sees (may be <= 0, may exceed the part)
   int left;    // keys of the sequence from key0 on
-  int part;    // (split * Hkv + kvh) * nslot + slot
+  int part;    // where a split item's part of O goes
   int pad;
 };
 
@@ -88,8 +90,8 @@ enum : unsigned int { W_Q = 1, W_KEMPTY, W_K, W_P, W_V, W_S, W_O, W_OFINAL, W_DR
 template <int D>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PackedGeom g, int nsplit,
-                      float scale_log2, __nv_bfloat16* O, long long o_head, long long o_tok,
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PackedGeom g, int part_keys,
+                      int part_rows, int head_items, float scale_log2, __nv_bfloat16* O, long long o_head, long long o_tok,
                       float* LSE, float* Opart, float* Lpart, int wide, Ctl ctl) {
   using T = PFwdTraits<D>;
   constexpr int NST = T::NST;
@@ -151,6 +153,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     tmem_alloc(tmem_slot, T::TMEM_COLS);
     tmem_relinquish();
   }
+  cudaTriggerProgrammaticLaunchCompletion();     // the combine kernel may come to wait (packed_combine_kernel)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -180,35 +183,44 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       for (uint32_t i = 0, asked = 0;; ++asked) {
         if (idx == 0) packed_check_ptrs(g, ctl, lane);
         FwdItem it = {};
-        const int sp = idx % nsplit;
-        int slot;
-        packed_order(g, g.nslot_q, true, idx / nsplit, it.kvh, slot);
         PackedSeq q;
-        if (packed_find(g, g.q_ptr, g.TQ, slot, q)) {
-          const int t0 = (slot - (q.q0 / g.TQ + q.s)) * g.TQ;
-          if (t0 < q.lq) {
-            it.valid = 1;
-            it.tok = q.q0 + t0;
-            it.ntok = min(g.TQ, q.lq - t0);
-            // keys that the first and the last token of the tile see
-            const int first = g.causal ? min(q.lk, q.lk - q.lq + t0 + 1) : q.lk;
-            const int last = g.causal ? min(q.lk, q.lk - q.lq + t0 + it.ntok) : q.lk;
-            const int tiles = last > 0 ? (last + 127) / 128 : 0;
-            // a part takes at least kPackedMinPart tiles, so that short sequences are not cut
-            const int per = max((tiles + nsplit - 1) / nsplit, nsplit > 1 ? kPackedMinPart : 1);
-            const int j0 = sp * per;
-            it.nt = max(0, min(per, tiles - j0));
-            it.key0 = q.k0 + j0 * 128;
-            it.left = q.lk - j0 * 128;
-            it.lim0 = first - j0 * 128;
-            it.part = (sp * g.Hkv + it.kvh) * g.nslot_q + slot;
+        int tile = 0, k_from = 0, k_to = 0;      // the item's query tile, its keys inside the sequence
+        bool found;
+        if (part_keys == 0) {
+          int slot;
+          packed_order(g, g.nslot_q, true, idx, it.kvh, slot);
+          found = packed_find(g, g.q_ptr, g.TQ, slot, q);
+          if (found) {
+            tile = slot - (q.q0 / g.TQ + q.s);
+            k_to = q.lk;
           }
+        } else {
+          it.kvh = idx / head_items;
+          const PackedPart part = packed_part(g, part_keys, idx - it.kvh * head_items, lane, q);
+          found = part.part >= 0;
+          tile = part.tile;
+          k_from = part.part * part_keys;
+          k_to = found ? min(q.lk, k_from + part_keys) : 0;
+          it.part = idx;
+        }
+        const int t0 = tile * g.TQ;
+        if (found && t0 < q.lq) {
+          it.valid = 1;
+          it.tok = q.q0 + t0;
+          it.ntok = min(g.TQ, q.lq - t0);
+          // keys that the first and the last token of the tile see
+          const int first = g.causal ? min(q.lk, q.lk - q.lq + t0 + 1) : q.lk;
+          const int last = min(k_to, g.causal ? min(q.lk, q.lk - q.lq + t0 + it.ntok) : q.lk);
+          it.nt = last > k_from ? (last - k_from + 127) / 128 : 0;
+          it.key0 = q.k0 + k_from;
+          it.left = q.lk - k_from;
+          it.lim0 = first - k_from;
         }
         if (it.valid && it.nt == 0) {
           // no key for any of its rows: written here, so that an item in the ring always has tiles
           for (int r = lane; r < it.ntok * g.group; r += 32) {
-            if (nsplit > 1) {
-              Lpart[(long long)it.part * 128 + r] = -INFINITY;
+            if (part_keys > 0) {
+              Lpart[(long long)it.part * part_rows + r] = -INFINITY;
               continue;
             }
             const int rt = r / g.group, head = it.kvh * g.group + (r - rt * g.group);
@@ -536,9 +548,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const bool row_ok = rt < it.ntok;
       const int head = it.kvh * g.group + rh;
       const long long tok = (long long)it.tok + rt;
-      const long long prow = (long long)it.part * 128 + r;
+      const long long prow = (long long)it.part * part_rows + r;
       __nv_bfloat16* dst = O + head * o_head + tok * o_tok;
-      float* ls = nsplit > 1 ? Lpart + prow : LSE + (long long)head * g.Tq + tok;
+      float* ls = part_keys > 0 ? Lpart + prow : LSE + (long long)head * g.Tq + tok;
       if (!mbar_wait_warp(stat_full, (uint32_t)ne & 1u, abort_flag, ctl, kid | W_STAT) ||
           !mbar_wait_warp(o_final, (uint32_t)ne & 1u, abort_flag, ctl, kid | W_OFINAL))
         break;
@@ -554,7 +566,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (row_ok) {
 #pragma unroll
         for (int j = 0; j < D; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * st.x);
-        if (nsplit > 1) {
+        if (part_keys > 0) {
 #pragma unroll
           for (int q = 0; q < D / 8; ++q) st_global_32(Opart + prow * D + q * 8, o + q * 8);
           *ls = st.y;
@@ -585,42 +597,64 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
 // Joins the parts of a tile: with L_p the base-2 log-sums, M = max L_p and
 // w_p = 2^(L_p - M):  O = sum w_p O_p / sum w_p,  lse = (M + log2 sum w_p) ln 2.
-// One warp per row, parts in order.
+// One warp per row; each lane weighs a part, then all add the parts up in
+// order, sixteen loads of O in flight.  A part that saw nothing of the row
+// wrote no O: its weight is 0 and its values are left out.  The kernel is
+// launched while the parts are still being worked on, finds its rows
+// meanwhile, and waits for them before it reads the first one.
 template <int D>
-__global__ void __launch_bounds__(128) packed_combine_kernel(const __grid_constant__ PackedGeom g, int nsplit,
+__global__ void __launch_bounds__(128) packed_combine_kernel(const __grid_constant__ PackedGeom g, int part_keys,
+                                                             int part_rows, int items,
                                                              const float* __restrict__ Opart,
                                                              const float* __restrict__ Lpart, __nv_bfloat16* O,
                                                              long long o_head, long long o_tok, float* LSE) {
   constexpr int V = D / 32;            // channels per lane
+  using Vec = std::conditional_t<V == 4, float4, float2>;
   const int slot = blockIdx.x, kvh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   PackedSeq q;
   if (!packed_find(g, g.q_ptr, g.TQ, slot, q)) return;
-  const int t0 = (slot - (q.q0 / g.TQ + q.s)) * g.TQ;
-  if (t0 >= q.lq) return;
-  const int rows = min(g.TQ, q.lq - t0) * g.group;
-  const long long step = (long long)g.Hkv * g.nslot_q * 128;
+  const int tile = slot - (q.q0 / g.TQ + q.s);
+  if (tile * g.TQ >= q.lq) return;
+  int parts;
+  const long long first = (long long)kvh * items + packed_part_base(g, part_keys, q.s, tile, lane, parts);
+  const int rows = min(g.TQ, q.lq - tile * g.TQ) * g.group;
+  cudaGridDependencySynchronize();
   for (int r = blockIdx.z * 4 + warp; r < rows; r += 4 * gridDim.z) {
-    const long long row = ((long long)kvh * g.nslot_q + slot) * 128 + r;
+    const float* L = Lpart + first * part_rows + r;
+    const float* src = Opart + (first * part_rows + r) * D + lane * V;
     float M = -INFINITY;
-    for (int p = lane; p < nsplit; p += 32) M = fmaxf(M, Lpart[row + p * step]);
+    for (int p = lane; p < parts; p += 32) M = fmaxf(M, L[(long long)p * part_rows]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float acc[V] = {};
     float sum = 0.f;
-    if (M != -INFINITY) {
-      for (int p = 0; p < nsplit; ++p) {
-        const float L = Lpart[row + p * step];
-        if (L == -INFINITY) continue;          // a part that saw nothing of this row wrote no O
-        const float w = ex2(L - M);
-        const float* src = Opart + (row + p * step) * D + lane * V;
+    for (int p0 = 0; p0 < parts && M != -INFINITY; p0 += 32) {
+      const float mine = p0 + lane < parts ? L[(long long)(p0 + lane) * part_rows] : -INFINITY;
+      const float w = mine == -INFINITY ? 0.f : ex2(mine - M);
+      const int n = min(32, parts - p0);
+      for (int j = 0; j < n; j += 16) {
+        Vec x[16];
+        float wj[16];
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = fmaf(w, src[i], acc[i]);
-        sum += w;
+        for (int k = 0; k < 16; ++k) {
+          wj[k] = __shfl_sync(0xffffffffu, w, (j + k) & 31);
+          x[k] = {};
+          if (j + k < n && wj[k] != 0.f)
+            x[k] = *reinterpret_cast<const Vec*>(src + (long long)(p0 + j + k) * part_rows * D);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          if (j + k >= n) continue;
+          sum += wj[k];
+          const float* xv = reinterpret_cast<const float*>(&x[k]);
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[i] = fmaf(wj[k], xv[i], acc[i]);
+        }
       }
     }
     const float inv = M != -INFINITY ? 1.0f / sum : 0.f;
     const int rt = r / g.group, head = kvh * g.group + (r - rt * g.group);
-    const long long tok = (long long)q.q0 + t0 + rt;
+    const long long tok = (long long)q.q0 + tile * g.TQ + rt;
     uint32_t* dst = reinterpret_cast<uint32_t*>(O + head * o_head + tok * o_tok + lane * V);
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) dst[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
@@ -628,9 +662,36 @@ __global__ void __launch_bounds__(128) packed_combine_kernel(const __grid_consta
   }
 }
 
+// Split over the keys.  With at least one query tile per SM the keys stay
+// whole.  With fewer, every tile's keys are cut into parts of equal size, as
+// small as fill six rounds of the SMs (the lengths are not known on the host:
+// uneven ones even out over the rounds), but of kPackedMinPart key tiles at
+// least.
+struct FwdSplit {
+  int part_keys;     // 0: not split
+  int items;         // bound on the items of a key head
+  int rows;          // rows of a part
+};
+FwdSplit fwd_split(const dsv_packed& p) {
+  FwdSplit sp{0, 0, 0};
+  if (p.S <= 0 || p.Tq <= 0 || p.Tk <= 0) return sp;
+  const int group = p.H / p.Hkv, TQ = 128 / group;
+  const long long q_tiles = (p.Tq + TQ - 1) / TQ;          // of one sequence at most
+  const long long most = q_tiles > p.S ? q_tiles : p.S;    // of all, roughly
+  if (p.Hkv * most >= kPackedSMs) return sp;
+  const long long key_tiles = (long long)p.Hkv * ((p.Tk + 127) / 128) * ((most + p.S - 1) / p.S);
+  long long part = (key_tiles + 6LL * kPackedSMs - 1) / (6LL * kPackedSMs);
+  part = part < kPackedMinPart ? kPackedMinPart : part;
+  if ((p.Tk + 127) / 128 <= part) return sp;               // one part at most
+  sp.part_keys = (int)part * 128;
+  sp.items = (int)(q_tiles * ((long long)p.Tk / sp.part_keys + p.S));
+  sp.rows = group * (p.Tq < TQ ? p.Tq : TQ);
+  return sp;
+}
+
 template <int D>
 cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV, const PackedGeom& g,
-                     int nsplit, float scale, const dsv_view& O, float* lse, void* ws, const Ctl& ctl,
+                     const FwdSplit& sp, float scale, const dsv_view& O, float* lse, void* ws, const Ctl& ctl,
                      cudaStream_t st) {
   using T = PFwdTraits<D>;
   auto kern = packed_fwd_kernel<D>;
@@ -642,55 +703,49 @@ cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
     return cudaFuncGetAttributes(&a, kern) == cudaSuccess ? a.numRegs : 0;
   }();
   if (launched < kRegsLaunch) return cudaErrorInvalidKernelImage;
-  const long long total = (long long)g.Hkv * g.nslot_q * nsplit;
-  float* Opart = nsplit > 1 ? static_cast<float*>(ws) : nullptr;
-  float* Lpart = nsplit > 1 ? Opart + (size_t)total * 128 * D : nullptr;
+  const int items = sp.part_keys > 0 ? sp.items : g.nslot_q;
+  const long long total = (long long)g.Hkv * items;
+  float* Opart = sp.part_keys > 0 ? static_cast<float*>(ws) : nullptr;
+  float* Lpart = sp.part_keys > 0 ? Opart + (size_t)total * sp.rows * D : nullptr;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(O.ptr);
   // rows on 32-byte boundaries are stored a sector at a time
   const int wide = (reinterpret_cast<uintptr_t>(O.ptr) % 32 == 0 && O.head_stride % 16 == 0 && O.token_stride % 16 == 0);
-  kern<<<(unsigned)total, kFwdThreads, T::SMEM, st>>>(tmQ, tmK, tmV, g, nsplit, scale * 1.4426950408889634f, o,
-                                           O.head_stride, O.token_stride, lse, Opart, Lpart, wide, ctl);
-  if ((e = cudaGetLastError()) != cudaSuccess || nsplit == 1) return e;
+  kern<<<(unsigned)total, kFwdThreads, T::SMEM, st>>>(tmQ, tmK, tmV, g, sp.part_keys, sp.rows, items,
+                                                      scale * 1.4426950408889634f, o, O.head_stride, O.token_stride,
+                                                      lse, Opart, Lpart, wide, ctl);
+  if ((e = cudaGetLastError()) != cudaSuccess || sp.part_keys == 0) return e;
   // rows of a tile over a few CTAs when the tiles alone would not fill the SMs
   const long long tiles = (long long)g.Hkv * g.nslot_q;
-  const int rows = g.group * (g.Tq < g.TQ ? g.Tq : g.TQ);
   long long z = (2LL * kPackedSMs + tiles - 1) / tiles;
-  z = z < (rows + 3) / 4 ? z : (rows + 3) / 4;
-  packed_combine_kernel<D><<<dim3((unsigned)g.nslot_q, (unsigned)g.Hkv, (unsigned)(z > 0 ? z : 1)), 128, 0, st>>>(
-      g, nsplit, Opart, Lpart, o, O.head_stride, O.token_stride, lse);
-  return cudaGetLastError();
+  z = z < (sp.rows + 3) / 4 ? z : (sp.rows + 3) / 4;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)g.nslot_q, (unsigned)g.Hkv, (unsigned)z);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, packed_combine_kernel<D>, g, sp.part_keys, sp.rows, items,
+                            static_cast<const float*>(Opart), static_cast<const float*>(Lpart), o,
+                            (long long)O.head_stride, (long long)O.token_stride, lse);
 }
 
 }  // namespace
 
-// Parts per query tile.  With at least one tile per SM the keys stay whole.
-// With fewer, parts of at least kPackedMinPart key tiles fill four rounds of
-// the SMs (the lengths are not known here: uneven ones even out over rounds).
-int packed_fwd_splits(const dsv_packed& p) {
-  if (p.S <= 0 || p.Tq <= 0 || p.Tk <= 0) return 1;
-  const int TQ = 128 / (p.H / p.Hkv);
-  const long long q_tiles = (p.Tq + TQ - 1) / TQ;
-  const long long tiles = (long long)p.Hkv * (q_tiles > p.S ? q_tiles : p.S);
-  if (tiles >= kPackedSMs) return 1;
-  long long n = (4LL * kPackedSMs + tiles - 1) / tiles;
-  const long long most = ((p.Tk + 127) / 128 + kPackedMinPart - 1) / kPackedMinPart;
-  n = n < most ? n : most;
-  return (int)(n < 1 ? 1 : n > 64 ? 64 : n);
-}
-
 size_t packed_fwd_ws_bytes(const dsv_packed& p) {
-  const int n = packed_fwd_splits(p);
-  if (n == 1) return 0;
-  return (size_t)n * p.Hkv * packed_slots(p.Tq, 128 / (p.H / p.Hkv), p.S) * 128 * (p.d + 1) * sizeof(float);
+  const FwdSplit sp = fwd_split(p);
+  return (size_t)p.Hkv * sp.items * sp.rows * (p.d + 1) * sizeof(float);
 }
 
 cudaError_t launch_packed_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                               const dsv_packed& p, const int32_t* q_ptr, const int32_t* k_ptr, int causal, float scale,
                               const dsv_view& O, float* lse, void* ws, const Ctl& ctl, cudaStream_t st) {
   const PackedGeom g = packed_geom(p, q_ptr, k_ptr, causal);
-  const int n = packed_fwd_splits(p);
-  return p.d == 128 ? launch_t<128>(tmQ, tmK, tmV, g, n, scale, O, lse, ws, ctl, st)
-                    : launch_t<64>(tmQ, tmK, tmV, g, n, scale, O, lse, ws, ctl, st);
+  const FwdSplit sp = fwd_split(p);
+  return p.d == 128 ? launch_t<128>(tmQ, tmK, tmV, g, sp, scale, O, lse, ws, ctl, st)
+                    : launch_t<64>(tmQ, tmK, tmV, g, sp, scale, O, lse, ws, ctl, st);
 }
 
 }  // namespace dsv

@@ -179,6 +179,22 @@ def test_packed_split_over_keys(dsv, ql, kl, causal, H, Hkv, d):
     _check(dsv, Case(H, Hkv, d, ql, kl), causal)
 
 
+@pytest.mark.parametrize("ql, kl, causal", [
+    ((2900,), (100,), False), ((1300, 2000, 5), (77, 300, 200), False), ((2500, 0, 600), (513, 40, 0), True),
+    ((1700,), (1700,), True), ((3000,), (130,), True)])
+@pytest.mark.parametrize("H, Hkv, d", [(2, 2, 128), (6, 2, 64)])
+def test_packed_gradient_split_over_queries(dsv, ql, kl, causal, H, Hkv, d):
+    """Few key tiles against many queries (text): the query tiles of a key tile
+    are split and the parts of dK and dV joined."""
+    S, Tq, Tk = len(ql), sum(ql), sum(kl)
+    whole = 2 * Hkv * (Tq // (128 // (H // Hkv)) + S) * 128 * 4
+    assert dsv.packed_attn_bwd_workspace_bytes(S, H, Hkv, Tq, Tk, d) > whole
+    c = Case(H, Hkv, d, ql, kl)
+    O, lse = _check(dsv, c, causal)
+    g, g2 = c.bwd(dsv, O, lse, causal), c.bwd(dsv, O, lse, causal)
+    assert all(torch.equal(a, b) for a, b in zip(g, g2))
+
+
 def test_packed_enough_tiles_are_not_split(dsv):
     c = Case(20, 20, 64, (1000, 30), (1000, 600))
     assert dsv.packed_attn_fwd_workspace_bytes(2, 20, 20, 1030, 1600, 64) == 0
