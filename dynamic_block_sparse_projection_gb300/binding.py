@@ -8,8 +8,8 @@ module raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 from pathlib import Path
 from typing import Optional, Sequence, Tuple
@@ -167,20 +167,26 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (2 us a call), where torch has the call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device: torch.device, stream=None) -> Optional[int]:
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
-_HERE = contextlib.nullcontext()
-
-
-def _on(device: torch.device):
-    """The context of a launch on `device`: nothing to do where it is the current
-    device already (torch.cuda.device costs more than a small kernel's launch)."""
+def _call(fn, what: str, device: torch.device, *args) -> None:
+    """fn(*args) under `device`: nothing to switch where it is the current one
+    already (torch.cuda.device costs as much as a small kernel's launch)."""
     if device.type == "cuda" and device.index == torch.cuda.current_device():
-        return _HERE
-    return torch.cuda.device(device)
+        _check(fn(*args), what)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args), what)
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, device: Optional[torch.device] = None):
@@ -210,6 +216,20 @@ def _need_rows(t: torch.Tensor, name: str, device: Optional[torch.device] = None
         raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
+def _need_rows_on(device: torch.device, index: int, **tensors) -> None:
+    """_need_rows for each tensor (None: left out); index: the device's, as get_device() gives it."""
+    for name, t in tensors.items():
+        if t is not None and (t.dtype is not torch.bfloat16 or t.get_device() != index or t.stride(-1) != 1):
+            _need_rows(t, name, device)
+
+
+def _need_on(device: torch.device, index: int, dtype: torch.dtype, **tensors) -> None:
+    """_need for each tensor (None: left out)."""
+    for name, t in tensors.items():
+        if t is not None and (t.dtype is not dtype or t.get_device() != index or not t.is_contiguous()):
+            _need(t, name, dtype, device)
+
+
 def _dims(t, name: str, n: int) -> Tuple[int, ...]:
     """The shape of t, which must be an n-dimensional tensor."""
     if not isinstance(t, torch.Tensor):
@@ -223,7 +243,7 @@ def _shape(t, name: str, shape) -> None:
     """t must have exactly this shape (the library reads and writes whole tensors)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -636,23 +656,25 @@ def _view(t: Optional[torch.Tensor]) -> View:
     """dsv_view of a [.., heads, tokens, d] tensor of 3 or 4 dimensions."""
     if t is None:
         return View(None, 0, 0, 0)
-    st = t.stride()
-    return View(t.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2])
+    return View(t.data_ptr(), *(t.stride()[:3] if t.dim() == 4 else (0, *t.stride()[:2])))
+
+
+@functools.lru_cache(maxsize=64)
+def _rope(B: int, H: int, N: int, d: int, sections: Tuple[int, ...], theta: float) -> Rope:
+    return Rope(B, H, N, d, len(sections), (ctypes.c_int32 * 4)(*sections), theta)
 
 
 def _rope_shape(t, name: str, pos, sections: Sequence[int], theta: float) -> Tuple[Rope, int]:
     """(dsv_rope, elements between batches of pos)."""
     B, H, N, d = _dims(t, name, 4)
-    sections = [int(c) for c in sections]
-    if not 1 <= len(sections) <= 4:
-        raise ValueError(f"sections has {len(sections)} entries, expected one per axis, 1 to 4")
+    A = len(sections)
+    if not 1 <= A <= 4:
+        raise ValueError(f"sections has {A} entries, expected one per axis, 1 to 4")
     if not isinstance(pos, torch.Tensor):
         raise TypeError("pos must be a torch.Tensor")
-    A = len(sections)
-    if tuple(pos.shape) not in ((N, A), (B, N, A)):
+    if pos.shape != (N, A) and pos.shape != (B, N, A):
         raise ValueError(f"pos has shape {tuple(pos.shape)}, expected {(N, A)} or {(B, N, A)}")
-    return (Rope(B, H, N, d, A, (ctypes.c_int32 * 4)(*sections), float(theta)),
-            N * A if pos.dim() == 3 else 0)
+    return _rope(B, H, N, d, tuple(sections), theta), N * A if pos.dim() == 3 else 0
 
 
 def rope_axes(x, pos, sections: Sequence[int], *, theta: float = 10000.0, weight=None, eps: float = 1e-6, out=None,
@@ -670,17 +692,14 @@ def rope_axes(x, pos, sections: Sequence[int], *, theta: float = 10000.0, weight
     if weight is not None:
         _shape(weight, "weight", (r.d,))
     _need_rows(x, "x")
-    dev = x.device
-    _need(pos, "pos", torch.int32, dev)
-    if weight is not None:
-        _need(weight, "weight", torch.float32, dev)
+    dev, at = x.device, x.get_device()
+    _need_on(dev, at, torch.int32, pos=pos)
+    _need_on(dev, at, torch.float32, weight=weight)
+    _need_rows_on(dev, at, out=out)
     if out is None:
         out = torch.empty_like(x)
-    else:
-        _need_rows(out, "out", dev)
-    with _on(dev):
-        _check(lib.dsv_rope_axes_fwd(_view(x), _ptr(pos), pos_b, r, _ptr(weight), float(eps), _view(out),
-                                     _stream(dev, stream)), "dsv_rope_axes_fwd")
+    _call(lib.dsv_rope_axes_fwd, "dsv_rope_axes_fwd", dev, _view(x), pos.data_ptr(), pos_b, r, _ptr(weight), eps,
+          _view(out), _stream(dev, stream))
     return out
 
 
@@ -705,25 +724,22 @@ def rope_axes_bwd(dy, pos, sections: Sequence[int], *, theta: float = 10000.0, x
     elif dweight is not None:
         raise ValueError("dweight without a weight")
     _need_rows(dy, "dy")
-    dev = dy.device
-    _need(pos, "pos", torch.int32, dev)
+    dev, at = dy.device, dy.get_device()
+    _need_on(dev, at, torch.int32, pos=pos)
+    _need_rows_on(dev, at, dx=dx)
     if dx is None:
         dx = torch.empty_like(dy)
-    else:
-        _need_rows(dx, "dx", dev)
     nbytes, ws = 0, None
     if weight is not None:
-        _need_rows(x, "x", dev)
-        _need(weight, "weight", torch.float32, dev)
+        _need_rows_on(dev, at, x=x)
+        _need_on(dev, at, torch.float32, weight=weight, dweight=dweight)
         if dweight is None:
             dweight = torch.empty(r.d, dtype=torch.float32, device=dev)
-        _need(dweight, "dweight", torch.float32, dev)
         nbytes = lib.dsv_rope_axes_bwd_workspace_bytes(r)
         ws = _scratch(nbytes, dev, workspace)
-    with _on(dev):
-        _check(lib.dsv_rope_axes_bwd(_view(dy), _view(x if weight is not None else None), _ptr(pos), pos_b, r,
-                                     _ptr(weight), float(eps), _view(dx), _ptr(dweight), _ptr(ws), nbytes,
-                                     _stream(dev, stream)), "dsv_rope_axes_bwd")
+    _call(lib.dsv_rope_axes_bwd, "dsv_rope_axes_bwd", dev, _view(dy), _view(x if weight is not None else None),
+          pos.data_ptr(), pos_b, r, _ptr(weight), eps, _view(dx), _ptr(dweight), _ptr(ws), nbytes,
+          _stream(dev, stream))
     return dx if weight is None else (dx, dweight)
 
 
@@ -734,11 +750,11 @@ def _packed_shape(Q, K, V, q_ptr, k_ptr) -> Packed:
         raise ValueError(f"K has head dimension {dk}, expected {d}")
     if Hkv < 1 or H % Hkv != 0:
         raise ValueError(f"Q has {H} heads, expected a multiple of K's {Hkv}")
-    _shape(V, "V", (Hkv, Tk, d))
+    _shape(V, "V", K.shape)
     S = _dims(q_ptr, "q_ptr", 1)[0] - 1
     if S < 0:
         raise ValueError("q_ptr must hold at least one element")
-    _shape(k_ptr, "k_ptr", (S + 1,))
+    _shape(k_ptr, "k_ptr", q_ptr.shape)
     return Packed(S, H, Hkv, Tq, Tk, d)
 
 
@@ -766,24 +782,19 @@ def packed_attn_fwd(Q, K, V, q_ptr, k_ptr, softmax_scale: float = 0.0, *, causal
     if lse is not None:
         _shape(lse, "lse", (p.H, p.Tq))
     _need_rows(Q, "Q")
-    dev = Q.device
-    _need_rows(K, "K", dev)
-    _need_rows(V, "V", dev)
-    _need(q_ptr, "q_ptr", torch.int32, dev)
-    _need(k_ptr, "k_ptr", torch.int32, dev)
+    dev, at = Q.device, Q.get_device()
+    _need_rows_on(dev, at, K=K, V=V, out=out)
+    _need_on(dev, at, torch.int32, q_ptr=q_ptr, k_ptr=k_ptr)
+    _need_on(dev, at, torch.float32, lse=lse)
     if out is None:
         out = torch.empty_like(Q)
-    else:
-        _need_rows(out, "out", dev)
     if lse is None:
         lse = torch.empty(p.H, p.Tq, dtype=torch.float32, device=dev)
-    _need(lse, "lse", torch.float32, dev)
     nbytes = lib.dsv_packed_attn_fwd_workspace_bytes(p)
     ws = _scratch(nbytes, dev, workspace) if nbytes else None
-    with _on(dev):
-        _check(lib.dsv_packed_attn_fwd(_view(Q), _view(K), _view(V), p, _ptr(q_ptr), _ptr(k_ptr), 1 if causal else 0,
-                                       float(softmax_scale), _view(out), _ptr(lse), _ptr(ws), nbytes,
-                                       _stream(dev, stream)), "dsv_packed_attn_fwd")
+    _call(lib.dsv_packed_attn_fwd, "dsv_packed_attn_fwd", dev, _view(Q), _view(K), _view(V), p, q_ptr.data_ptr(),
+          k_ptr.data_ptr(), 1 if causal else 0, softmax_scale, _view(out), lse.data_ptr(), _ptr(ws), nbytes,
+          _stream(dev, stream))
     return out, lse
 
 
@@ -801,24 +812,19 @@ def packed_attn_bwd(Q, K, V, O, dO, lse, q_ptr, k_ptr, softmax_scale: float = 0.
         for name, t, like in zip(("dQ", "dK", "dV"), outs, (Q, K, V)):
             _shape(t, name, like.shape)
     _need_rows(Q, "Q")
-    dev = Q.device
-    for name, t in (("K", K), ("V", V), ("O", O), ("dO", dO)):
-        _need_rows(t, name, dev)
-    _need(lse, "lse", torch.float32, dev)
-    _need(q_ptr, "q_ptr", torch.int32, dev)
-    _need(k_ptr, "k_ptr", torch.int32, dev)
+    dev, at = Q.device, Q.get_device()
+    _need_rows_on(dev, at, K=K, V=V, O=O, dO=dO)
+    _need_on(dev, at, torch.int32, q_ptr=q_ptr, k_ptr=k_ptr)
+    _need_on(dev, at, torch.float32, lse=lse)
     if outs is None:
         outs = (torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V))
     else:
-        for name, t in zip(("dQ", "dK", "dV"), outs):
-            _need_rows(t, name, dev)
+        _need_rows_on(dev, at, dQ=outs[0], dK=outs[1], dV=outs[2])
     nbytes = lib.dsv_packed_attn_bwd_workspace_bytes(p)
     ws = _scratch(nbytes, dev, workspace) if nbytes else None
-    with _on(dev):
-        _check(lib.dsv_packed_attn_bwd(_view(Q), _view(K), _view(V), _view(O), _view(dO), _ptr(lse), p, _ptr(q_ptr),
-                                       _ptr(k_ptr), 1 if causal else 0, float(softmax_scale),
-                                       *[_view(t) for t in outs], _ptr(ws), nbytes, _stream(dev, stream)),
-               "dsv_packed_attn_bwd")
+    _call(lib.dsv_packed_attn_bwd, "dsv_packed_attn_bwd", dev, _view(Q), _view(K), _view(V), _view(O), _view(dO),
+          lse.data_ptr(), p, q_ptr.data_ptr(), k_ptr.data_ptr(), 1 if causal else 0, softmax_scale, _view(outs[0]),
+          _view(outs[1]), _view(outs[2]), _ptr(ws), nbytes, _stream(dev, stream))
     return outs
 
 
