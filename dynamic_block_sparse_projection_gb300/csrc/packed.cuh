@@ -120,17 +120,6 @@ __device__ __forceinline__ PackedPart packed_part(const PackedGeom& g, int part_
   }
   return {0, -1, 0};
 }
-// Items of a key head before query tile `tile` of sequence s, by one warp.
-__device__ __forceinline__ int packed_part_base(const PackedGeom& g, int part_keys, int s, int tile, int lane,
-                                                int& parts) {
-  int sum = 0, p = 0;
-  for (int t = lane; t < s; t += 32) sum += packed_items(g, part_keys, t, p);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  packed_items(g, part_keys, s, parts);
-  return sum + tile * parts;
-}
-
 // Both row pointers must rise within [0, T]: one warp reports the first
 // sequence that breaks it (its tiles are skipped by packed_find).
 __device__ __forceinline__ void packed_check_ptrs(const PackedGeom& g, const Ctl& ctl, int lane) {

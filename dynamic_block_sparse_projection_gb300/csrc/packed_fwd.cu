@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PackedGeom g, int part_keys,
                       int part_rows, int head_items, float scale_log2, __nv_bfloat16* O, long long o_head, long long o_tok,
-                      float* LSE, float* Opart, float* Lpart, int wide, Ctl ctl) {
+                      float* LSE, float* Opart, float* Lpart, int4* tiles, int wide, Ctl ctl) {
   using T = PFwdTraits<D>;
   constexpr int NST = T::NST;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -202,6 +202,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           k_from = part.part * part_keys;
           k_to = found ? min(q.lk, k_from + part_keys) : 0;
           it.part = idx;
+          // what the combine kernel has to know of a tile, at its first part; nothing at the others
+          if (lane == 0)
+            tiles[idx] = found && part.part == 0
+                             ? make_int4(part.parts, q.q0 + tile * g.TQ, min(g.TQ, q.lq - tile * g.TQ), it.kvh)
+                             : make_int4(0, 0, 0, 0);
         }
         const int t0 = tile * g.TQ;
         if (found && t0 < q.lq) {
@@ -599,29 +604,25 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 // w_p = 2^(L_p - M):  O = sum w_p O_p / sum w_p,  lse = (M + log2 sum w_p) ln 2.
 // One warp per row; each lane weighs a part, then all add the parts up in
 // order, sixteen loads of O in flight.  A part that saw nothing of the row
-// wrote no O: its weight is 0 and its values are left out.  The kernel is
-// launched while the parts are still being worked on, finds its rows
-// meanwhile, and waits for them before it reads the first one.
+// wrote no O: its weight is 0 and its values are left out.  CTAs go over the
+// items of the forward grid (a tile is described at its first part) and, along
+// y, over the rows of a tile.
 template <int D>
-__global__ void __launch_bounds__(128) packed_combine_kernel(const __grid_constant__ PackedGeom g, int part_keys,
-                                                             int part_rows, int items,
+__global__ void __launch_bounds__(256) packed_combine_kernel(int H, int Hkv, int Tq, int part_rows,
+                                                             const int4* __restrict__ tiles,
                                                              const float* __restrict__ Opart,
                                                              const float* __restrict__ Lpart, __nv_bfloat16* O,
                                                              long long o_head, long long o_tok, float* LSE) {
   constexpr int V = D / 32;            // channels per lane
   using Vec = std::conditional_t<V == 4, float4, float2>;
-  const int slot = blockIdx.x, kvh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  PackedSeq q;
-  if (!packed_find(g, g.q_ptr, g.TQ, slot, q)) return;
-  const int tile = slot - (q.q0 / g.TQ + q.s);
-  if (tile * g.TQ >= q.lq) return;
-  int parts;
-  const long long first = (long long)kvh * items + packed_part_base(g, part_keys, q.s, tile, lane, parts);
-  const int rows = min(g.TQ, q.lq - tile * g.TQ) * g.group;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   cudaGridDependencySynchronize();
-  for (int r = blockIdx.z * 4 + warp; r < rows; r += 4 * gridDim.z) {
-    const float* L = Lpart + first * part_rows + r;
-    const float* src = Opart + (first * part_rows + r) * D + lane * V;
+  const int4 t = tiles[blockIdx.x];
+  const int parts = t.x, group = H / Hkv, rows = t.z * group;
+  if (parts == 0) return;
+  for (int r = blockIdx.y * 8 + warp; r < rows; r += 8 * gridDim.y) {
+    const float* L = Lpart + (long long)blockIdx.x * part_rows + r;
+    const float* src = Opart + ((long long)blockIdx.x * part_rows + r) * D + lane * V;
     float M = -INFINITY;
     for (int p = lane; p < parts; p += 32) M = fmaxf(M, L[(long long)p * part_rows]);
 #pragma unroll
@@ -634,31 +635,28 @@ __global__ void __launch_bounds__(128) packed_combine_kernel(const __grid_consta
       const int n = min(32, parts - p0);
       for (int j = 0; j < n; j += 16) {
         Vec x[16];
-        float wj[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          wj[k] = __shfl_sync(0xffffffffu, w, (j + k) & 31);
-          x[k] = {};
-          if (j + k < n && wj[k] != 0.f)
-            x[k] = *reinterpret_cast<const Vec*>(src + (long long)(p0 + j + k) * part_rows * D);
-        }
+        for (int k = 0; k < 16; ++k)
+          if (j + k < n) x[k] = *reinterpret_cast<const Vec*>(src + (long long)(p0 + j + k) * part_rows * D);
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           if (j + k >= n) continue;
-          sum += wj[k];
+          const float wk = __shfl_sync(0xffffffffu, w, (j + k) & 31);
+          if (wk == 0.f) continue;
+          sum += wk;
           const float* xv = reinterpret_cast<const float*>(&x[k]);
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[i] = fmaf(wj[k], xv[i], acc[i]);
+          for (int i = 0; i < V; ++i) acc[i] = fmaf(wk, xv[i], acc[i]);
         }
       }
     }
     const float inv = M != -INFINITY ? 1.0f / sum : 0.f;
-    const int rt = r / g.group, head = kvh * g.group + (r - rt * g.group);
-    const long long tok = (long long)q.q0 + tile * g.TQ + rt;
+    const int rt = r / group, head = t.w * group + (r - rt * group);
+    const long long tok = (long long)t.y + rt;
     uint32_t* dst = reinterpret_cast<uint32_t*>(O + head * o_head + tok * o_tok + lane * V);
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) dst[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    if (lane == 0) LSE[(long long)head * g.Tq + tok] = M != -INFINITY ? (M + log2f(sum)) * kLn2 : -INFINITY;
+    if (lane == 0) LSE[(long long)head * Tq + tok] = M != -INFINITY ? (M + log2f(sum)) * kLn2 : -INFINITY;
   }
 }
 
@@ -705,38 +703,40 @@ cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
   if (launched < kRegsLaunch) return cudaErrorInvalidKernelImage;
   const int items = sp.part_keys > 0 ? sp.items : g.nslot_q;
   const long long total = (long long)g.Hkv * items;
-  float* Opart = sp.part_keys > 0 ? static_cast<float*>(ws) : nullptr;
+  // workspace: a description of each item's tile, the parts' O, their log-sums
+  int4* tiles = sp.part_keys > 0 ? static_cast<int4*>(ws) : nullptr;
+  float* Opart = sp.part_keys > 0 ? reinterpret_cast<float*>(static_cast<char*>(ws) + align256(total * sizeof(int4)))
+                                  : nullptr;
   float* Lpart = sp.part_keys > 0 ? Opart + (size_t)total * sp.rows * D : nullptr;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(O.ptr);
   // rows on 32-byte boundaries are stored a sector at a time
   const int wide = (reinterpret_cast<uintptr_t>(O.ptr) % 32 == 0 && O.head_stride % 16 == 0 && O.token_stride % 16 == 0);
   kern<<<(unsigned)total, kFwdThreads, T::SMEM, st>>>(tmQ, tmK, tmV, g, sp.part_keys, sp.rows, items,
                                                       scale * 1.4426950408889634f, o, O.head_stride, O.token_stride,
-                                                      lse, Opart, Lpart, wide, ctl);
+                                                      lse, Opart, Lpart, tiles, wide, ctl);
   if ((e = cudaGetLastError()) != cudaSuccess || sp.part_keys == 0) return e;
-  // rows of a tile over a few CTAs when the tiles alone would not fill the SMs
-  const long long tiles = (long long)g.Hkv * g.nslot_q;
-  long long z = (2LL * kPackedSMs + tiles - 1) / tiles;
-  z = z < (sp.rows + 3) / 4 ? z : (sp.rows + 3) / 4;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)g.nslot_q, (unsigned)g.Hkv, (unsigned)z);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3((unsigned)total, (unsigned)((sp.rows + 15) / 16));
+  cfg.blockDim = dim3(256);
   cfg.stream = st;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, packed_combine_kernel<D>, g, sp.part_keys, sp.rows, items,
-                            static_cast<const float*>(Opart), static_cast<const float*>(Lpart), o,
-                            (long long)O.head_stride, (long long)O.token_stride, lse);
+  return cudaLaunchKernelEx(&cfg, packed_combine_kernel<D>, g.H, g.Hkv, g.Tq, sp.rows,
+                            static_cast<const int4*>(tiles), static_cast<const float*>(Opart),
+                            static_cast<const float*>(Lpart), o, (long long)O.head_stride, (long long)O.token_stride,
+                            lse);
 }
 
 }  // namespace
 
 size_t packed_fwd_ws_bytes(const dsv_packed& p) {
   const FwdSplit sp = fwd_split(p);
-  return (size_t)p.Hkv * sp.items * sp.rows * (p.d + 1) * sizeof(float);
+  if (sp.part_keys == 0) return 0;
+  const size_t total = (size_t)p.Hkv * sp.items;
+  return align256(total * sizeof(int4)) + total * sp.rows * (p.d + 1) * sizeof(float);
 }
 
 cudaError_t launch_packed_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
