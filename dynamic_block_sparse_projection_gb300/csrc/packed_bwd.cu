@@ -730,19 +730,24 @@ __global__ void __launch_bounds__(kQThreads, 1)
     bool ok = true;
     QItem it;
     for (uint32_t i = 0; ok && take(i, it); ++i) {
-      // Q and dO are A operands of every S and dP product: the previous tile's last ones must be done
-      if (qd_issued > 0 &&
-          !mbar_wait_warp(qd_free, (uint32_t)(qd_issued - 1) & 1u, abort_flag, ctl, kid | W_KVEMPTY))
-        break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(qd_full, 2 * q_bytes);
-        for (int c = 0; c < T::NCH; ++c) {
-          tma_load_3d(sdO + c * T::CHUNK, &tmdO, qd_full, c * 64, it.kvh * g.group, it.tok);
-          tma_load_3d(sQ + c * T::CHUNK, &tmQ, qd_full, c * 64, it.kvh * g.group, it.tok);
-        }
-      }
-      ++qd_issued;
       for (int n = 0; n < it.nt; ++n) {
+        // the first K tile goes ahead of Q and dO, whose buffers are free only
+        // when the previous item's last S and dP products are done
+        if (n == min(1, it.nt - 1)) {
+          if (qd_issued > 0 &&
+              !mbar_wait_warp(qd_free, (uint32_t)(qd_issued - 1) & 1u, abort_flag, ctl, kid | W_KVEMPTY)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(qd_full, 2 * q_bytes);
+            for (int c = 0; c < T::NCH; ++c) {
+              tma_load_3d(sdO + c * T::CHUNK, &tmdO, qd_full, c * 64, it.kvh * g.group, it.tok);
+              tma_load_3d(sQ + c * T::CHUNK, &tmQ, qd_full, c * 64, it.kvh * g.group, it.tok);
+            }
+          }
+          ++qd_issued;
+        }
         const int s = (int)(gq % NK);
         if (!mbar_wait_warp(&k_empty[s], ((gq / NK) & 1u) ^ 1u, abort_flag, ctl, kid | W_KVEMPTY)) {
           ok = false;

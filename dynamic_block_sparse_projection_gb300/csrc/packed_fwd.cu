@@ -270,17 +270,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       bool ok = true;
       FwdItem it;
       for (uint32_t i = 0; ok && take(i, it); ++i) {
-        // Q is the A operand of every S product: the previous item's last one must be done
-        if (q_issued > 0 &&
-            !mbar_wait_warp(&s_full[(gq - 1) % NST], ((gq - 1) / NST) & 1u, abort_flag, ctl, kid | W_QEMPTY))
-          break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(q_full, q_bytes);
-          for (int c = 0; c < T::NCH; ++c)
-            tma_load_3d(sQ + c * T::CHUNK, &tmQ, q_full, c * 64, it.kvh * g.group, it.tok);
-        }
-        ++q_issued;
+        // the first two K tiles go ahead of Q, whose buffer is free only when
+        // the previous item's last S product is done
         for (int n = 0; n < it.nt; ++n) {
+          if (n == min(2, it.nt - 1)) {
+            const uint32_t last = gq - (uint32_t)n - 1;        // the previous item's last tile
+            if (q_issued > 0 && !mbar_wait_warp(&s_full[last % NST], (last / NST) & 1u, abort_flag, ctl, kid | W_QEMPTY)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              mbar_arrive_expect_tx(q_full, q_bytes);
+              for (int c = 0; c < T::NCH; ++c)
+                tma_load_3d(sQ + c * T::CHUNK, &tmQ, q_full, c * 64, it.kvh * g.group, it.tok);
+            }
+            ++q_issued;
+          }
           const int s = (int)(gq % NST);
           if (gq >= NST && !mbar_wait_warp(&s_full[s], ((gq - NST) / NST) & 1u, abort_flag, ctl, kid | W_KEMPTY)) {
             ok = false;
@@ -662,7 +667,7 @@ __global__ void __launch_bounds__(256) packed_combine_kernel(int H, int Hkv, int
 
 // Split over the keys.  With at least one query tile per SM the keys stay
 // whole.  With fewer, every tile's keys are cut into parts of equal size, as
-// small as fill six rounds of the SMs (the lengths are not known on the host:
+// small as fill four rounds of the SMs (the lengths are not known on the host:
 // uneven ones even out over the rounds), but of kPackedMinPart key tiles at
 // least.
 struct FwdSplit {
@@ -678,7 +683,7 @@ FwdSplit fwd_split(const dsv_packed& p) {
   const long long most = q_tiles > p.S ? q_tiles : p.S;    // of all, roughly
   if (p.Hkv * most >= kPackedSMs) return sp;
   const long long key_tiles = (long long)p.Hkv * ((p.Tk + 127) / 128) * ((most + p.S - 1) / p.S);
-  long long part = (key_tiles + 6LL * kPackedSMs - 1) / (6LL * kPackedSMs);
+  long long part = (key_tiles + 4LL * kPackedSMs - 1) / (4LL * kPackedSMs);
   part = part < kPackedMinPart ? kPackedMinPart : part;
   if ((p.Tk + 127) / 128 <= part) return sp;               // one part at most
   sp.part_keys = (int)part * 128;
