@@ -349,76 +349,83 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const uint64_t dQ0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t dK0 = sdesc_sw128(smem_u32(sK), 16, 1024);
       const uint64_t dV0 = sdesc_sw128(smem_u32(sV), T::CHUNK, 1024);
-      auto issue_S = [&](uint32_t gn) -> bool {
-        const int s = (int)(gn % NST);
-        if (!mbar_wait_warp(&k_full[s], (gn / NST) & 1u, abort_flag, ctl, kid | W_K)) return false;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem + (uint32_t)s * T::S_COL;
-        const uint64_t kb = desc_off(dK0, (uint32_t)s * T::TILE);
-  #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * T::CHUNK + (kk & 3) * 32;
-          mma_ss_w(d_tmem, desc_off(dQ0, off), desc_off(kb, off), IDS, kk > 0 ? 1u : 0u);
+      // S runs up to three tiles ahead of PV, over item ends too: the next
+      // item's first scores are issued as soon as its Q is there, so that the
+      // softmax finds them when it is done with this item.  S(t+3) follows
+      // PV(t) without a wait between them (its K was tested before P(t) was
+      // waited for): the MMA queue holds only a few products and drains in any
+      // gap.  Each product has one place in the code: instructions that run
+      // once an item are fetched anew each time, and 8 MMAs then took ~3000
+      // clocks to issue.
+      uint32_t sg = 0, pg = 0;                   // tiles issued: S, PV
+      uint32_t i = 0, k_tested = 0;              // items taken; K of tile sg known to be there
+      int s_left = 0, pv_n = 0, ne = 0;          // S tiles left of item i - 1; PV tiles done of the current item, items done
+      int nt0 = 0, nt1 = 0, nt2 = 0;             // tiles of the items between PV's and S's, PV's first
+      bool ok = true, more = true, q_wait = false;
+      auto tested = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity) != 0u); };
+      // the next item and its Q; without `block` only if they are there
+      auto acquire = [&](bool block) -> bool {
+        if (s_left == 0) {
+          if (!more || (!block && !tested(&item_full[i & 1], (i >> 1) & 1u))) return false;
+          FwdItem it;
+          more = take(i, it);
+          if (!more) return false;
+          ++i;
+          s_left = it.nt;
+          q_wait = true;
+          if (nt0 == 0) nt0 = it.nt; else if (nt1 == 0) nt1 = it.nt; else nt2 = it.nt;
         }
-        mma_commit_w(&s_full[s]);
-        return true;
+        if (!block && !tested(q_full, (i - 1) & 1u)) return false;
+        ok = mbar_wait_warp(q_full, (i - 1) & 1u, abort_flag, ctl, kid | W_Q);
+        q_wait = !ok;
+        return ok;
       };
-      // S runs two tiles ahead of PV, and over the item's end: the next item's
-      // S(0) is issued before the last P of this one is waited for, so that the
-      // softmax finds it when it is done with this item.
-      uint32_t gq = 0;
-      int ne = 0;
-      FwdItem it;
-      bool ok = take(0, it);
-      if (ok) ok = mbar_wait_warp(q_full, 0, abort_flag, ctl, kid | W_Q) && issue_S(0);
-      while (ok) {
-        if (it.nt > 1 && !issue_S(gq + 1)) break;
-        FwdItem nx;
-        bool more = false;
-        for (int n = 0; n < it.nt; ++n) {
-          // S(n+2) reuses the buffer of P(n-1), whose PV product is already queued
-          const uint32_t gn = gq + (uint32_t)n;
-          const int s = (int)(gn % NST);
-          const uint32_t ph = (gn / NST) & 1u;
-          const uint32_t v_tested = mbar_test(&v_full[s], ph);   // V_n normally landed long ago
-          uint32_t ts = gn + 2;
-          bool ahead = n + 2 < it.nt;
-          if (n + 1 == it.nt) {
-            more = ahead = take((uint32_t)ne + 1, nx);
-            ts = gn + 1;
-            if (more && !mbar_wait_warp(q_full, (uint32_t)(ne + 1) & 1u, abort_flag, ctl, kid | W_Q)) {
-              ok = false;
-              break;
-            }
-          }
-          if (ahead && !issue_S(ts)) {
-            ok = false;
-            break;
-          }
-          // the first PV product overwrites O: the previous item's must have been read
-          if (n == 0 && ne > 0 && !mbar_wait_warp(o_free, (uint32_t)(ne - 1) & 1u, abort_flag, ctl, kid | W_OFREE)) {
-            ok = false;
-            break;
-          }
-          if (!mbar_wait_warp(&p_full[s], ph, abort_flag, ctl, kid | W_P) ||
-              !mbar_wait_warp_tested(&v_full[s], ph, v_tested, abort_flag, ctl, kid | W_V)) {
-            ok = false;
-            break;
-          }
+      while (true) {
+        while (sg - pg < 3) {
+          // S into buffer sg % 3: the PV product of tile sg - 3 is queued
+          if ((s_left == 0 || q_wait) && !acquire(sg - pg <= 1)) break;
+          const int s = (int)(sg % NST);
+          ok = mbar_wait_warp_tested(&k_full[s], (sg / NST) & 1u, k_tested, abort_flag, ctl, kid | W_K);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t p_tmem = tmem + (uint32_t)s * T::S_COL;
-          const uint64_t vb = desc_off(dV0, (uint32_t)s * T::TILE);
+          const uint32_t d_tmem = tmem + (uint32_t)s * T::S_COL;
+          const uint64_t kb = desc_off(dK0, (uint32_t)s * T::TILE);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts_w(tmem + T::O_COL, p_tmem + kk * 8, desc_off(vb, kk * 16 * 128), IDO, (n > 0 || kk > 0) ? 1u : 0u);
-          mma_commit_w(&o_done[s]);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * T::CHUNK + (kk & 3) * 32;
+            mma_ss_w(d_tmem, desc_off(dQ0, off), desc_off(kb, off), IDS, kk > 0 ? 1u : 0u);
+          }
+          mma_commit_w(&s_full[s]);
+          ++sg;
+          --s_left;
+          k_tested = 0;
         }
-        if (!ok) break;
-        mma_commit_w(o_final);
-        gq += (uint32_t)it.nt;
-        ++ne;
-        if (!more) break;
-        it = nx;
+        if (!ok || pg == sg) break;
+        const int s = (int)(pg % NST);
+        const uint32_t ph = (pg / NST) & 1u;
+        const uint32_t v_tested = mbar_test(&v_full[s], ph);   // V normally landed long ago
+        k_tested = mbar_test(&k_full[sg % NST], (sg / NST) & 1u);
+        // the first PV product overwrites O: the previous item's must have been read
+        if (pv_n == 0 && ne > 0 && !mbar_wait_warp(o_free, (uint32_t)(ne - 1) & 1u, abort_flag, ctl, kid | W_OFREE))
+          break;
+        if (!mbar_wait_warp(&p_full[s], ph, abort_flag, ctl, kid | W_P)) break;
+        if (!mbar_wait_warp_tested(&v_full[s], ph, v_tested, abort_flag, ctl, kid | W_V)) break;
+        tc_fence_after();
+        const uint32_t p_tmem = tmem + (uint32_t)s * T::S_COL;
+        const uint64_t vb = desc_off(dV0, (uint32_t)s * T::TILE);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts_w(tmem + T::O_COL, p_tmem + kk * 8, desc_off(vb, kk * 16 * 128), IDO, (pv_n > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_w(&o_done[s]);
+        ++pg;
+        if (++pv_n == nt0) {
+          mma_commit_w(o_final);
+          ++ne;
+          pv_n = 0;
+          nt0 = nt1;
+          nt1 = nt2;
+          nt2 = 0;
+        }
       }
       // TMEM is freed after the closing CTA-wide sync only once every MMA is done
       mma_commit_w(mma_drain);
@@ -455,9 +462,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         s_tested = (n + 1 < it.nt) ? mbar_test(&s_full[(gn + 1) % NST], ((gn + 1) / NST) & 1u) : 0u;
         tmem_ld_wait();
         if (n * 128 + 128 > it.lim0) {
+          // keys at or past the row's limit: 32 at a time, and only where some row of the warp has any
           const int lim = lim_r - n * 128;
 #pragma unroll
-          for (int j = 0; j < 128; ++j) xr[j] = j < lim ? xr[j] : 0xff800000u;   // -inf
+          for (int c = 0; c < 4; ++c) {
+            const int have = lim - c * 32;
+            if (__any_sync(0xffffffffu, have < 32)) {
+              const uint32_t keep = have >= 32 ? 0xffffffffu : have <= 0 ? 0u : (1u << have) - 1u;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) xr[c * 32 + j] = (keep >> j) & 1u ? xr[c * 32 + j] : 0xff800000u;   // -inf
+            }
+          }
         }
         // row max as 8 independent partial maxima (short dependency chains)
         auto row_max = [&]() -> float {
@@ -497,36 +512,39 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // covers a prefix of the part's keys, so a row that sees any of them
         // sees one in the first tile; one that sees none keeps 0).  A later
         // tile keeps it unless one of its values would pass 2^64.
-        if (n == 0) {
-          const float mx = row_max() * scale_log2;
-          m = mx == -INFINITY ? 0.f : mx;
-        }
         float tsum;
-        bool redone = n == 0;
+        bool take_max = n == 0;
         while (true) {
+          if (take_max) {
+            const float mx = row_max() * scale_log2;
+            if (n == 0) {
+              m = mx == -INFINITY ? 0.f : mx;
+            } else {
+              // rescale this warp's O rows once the previous PV product has landed
+              const float m_new = fmaxf(m, mx);
+              const uint32_t gp = gn - 1;
+              ok = mbar_wait_warp(&o_done[gp % NST], (gp / NST) & 1u, abort_flag, ctl, kid | W_O);
+              if (!ok) break;
+              tc_fence_after();
+              const float alpha = ex2(m - m_new);
+              l *= alpha;
+              m = m_new;
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tmem + lane_off + T::O_COL + c * 32, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                tmem_st32(tmem + lane_off + T::O_COL + c * 32, o);
+              }
+              tmem_st_wait();
+            }
+          }
           tsum = exponentiate(m);
           // rows behind the tile's tokens hold another sequence's queries: they must not decide
-          if (redone || !__any_sync(0xffffffffu, row_ok && !(tsum <= 18446744073709551616.0f))) break;   // 2^64
-          const float m_new = fmaxf(m, row_max() * scale_log2);
-          // rescale this warp's O rows once the previous PV product has landed
-          const uint32_t gp = gn - 1;
-          ok = mbar_wait_warp(&o_done[gp % NST], (gp / NST) & 1u, abort_flag, ctl, kid | W_O);
-          if (!ok) break;
-          tc_fence_after();
-          const float alpha = ex2(m - m_new);
-          l *= alpha;
-          m = m_new;
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tmem + lane_off + T::O_COL + c * 32, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-            tmem_st32(tmem + lane_off + T::O_COL + c * 32, o);
-          }
-          tmem_st_wait();
-          redone = true;
+          if (take_max || !__any_sync(0xffffffffu, row_ok && !(tsum <= 18446744073709551616.0f))) break;   // 2^64
+          take_max = true;
         }
         if (!ok) break;
         l += tsum;
