@@ -101,11 +101,15 @@ struct PKVTraits {
   static constexpr int NCH = D / 64;
   static constexpr int CHUNK = 128 * 128;
   static constexpr int TILE = NCH * CHUNK;
-  static constexpr int NST = 2;
+  // Q is read by S^T (early) and dK (late), dO by dP^T and dV (earlier): rings
+  // of their own, each slot given back as its last product is done.  A tile's
+  // copies then have about one and a half pairs' time to arrive; with two
+  // common stages they had half a pair's, and a pair took 3465 clocks instead
+  // of 2650 where Q and dO come from HBM.
+  static constexpr int NQ = 3, ND = 2;
   static constexpr int VEC_BYTES = 128 * 4;                    // -lse2 or D of a query tile
-  static constexpr int STAGE_BYTES = (2 * TILE + 2 * VEC_BYTES + 1023) / 1024 * 1024;
-  static constexpr int NBAR = 1 + 2 * NST + 7 + 1;
-  static constexpr int SMEM_USED = 1024 + 2 * TILE + NST * STAGE_BYTES + NBAR * 8 + 16;
+  static constexpr int NBAR = 1 + 2 * NQ + 3 * ND + 7 + 2;
+  static constexpr int SMEM_USED = (2 + NQ + ND) * TILE + 2 * ND * VEC_BYTES + NBAR * 8 + 16;
   static_assert(SMEM_USED <= 227 * 1024, "dK/dV tiles exceed shared memory");
   static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
   // TMEM: S^T at 0, dP^T at 128, dV at 256, dK at 256 + D; P^T and dS^T (bf16
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(kKVThreads, 1)
                          long long dk_tok, __nv_bfloat16* dV, long long dv_head, long long dv_tok, int nsplit,
                          float* part, Ctl ctl) {
   using T = PKVTraits<D>;
-  constexpr int NST = T::NST;
+  constexpr int NQ = T::NQ, ND = T::ND;
   constexpr int W = T::W;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
 
@@ -165,21 +169,32 @@ __global__ void __launch_bounds__(kKVThreads, 1)
   const int cnt = max(0, min(kt.per, kt.cnt - piece * kt.per));
   const int qslot0 = q.q0 / g.TQ + q.s + i0;
 
-  uint8_t* sbase = smem_align1024(smem_raw);
-  uint8_t* sK = sbase;
+  // the tiles take all but ~800 bytes, so the base itself has to be aligned
+  // (the array is declared so; a launch that broke it is reported)
+  if ((smem_u32(smem_raw) & 1023u) != 0u) {
+    if (threadIdx.x == 0) set_error(ctl, DSV_ERR_INTERNAL, blockIdx.x);
+    return;
+  }
+  uint8_t* sK = smem_raw;
   uint8_t* sV = sK + T::TILE;
-  uint8_t* sStage = sV + T::TILE;                 // NST x [Q | dO | lse2 | D]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sStage + NST * T::STAGE_BYTES);
+  uint8_t* sQ = sV + T::TILE;                     // [NQ]
+  uint8_t* sdO = sQ + NQ * T::TILE;               // [ND]
+  uint8_t* sVec = sdO + ND * T::TILE;             // [ND] -lse2 | D
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sVec + 2 * ND * T::VEC_BYTES);
   uint64_t* kv_full = bars;
-  uint64_t* g_full = bars + 1;
-  uint64_t* g_empty = g_full + NST;
-  uint64_t* s_full = g_empty + NST;               // S^T in TMEM
+  uint64_t* q_full = bars + 1;
+  uint64_t* q_empty = q_full + NQ;                // dK of the slot's tile is done (also frees its vectors)
+  uint64_t* d_full = q_empty + NQ;
+  uint64_t* d_empty = d_full + ND;                // dV of the slot's tile is done
+  uint64_t* v_full = d_empty + ND;
+  uint64_t* s_full = v_full + ND;                 // S^T in TMEM
   uint64_t* dp_full = s_full + 1;                 // dP^T in TMEM
   uint64_t* p_full = dp_full + 1;                 // [2] P^T chunk written back (bf16)
   uint64_t* ds_full = p_full + 2;                 // [2] dS^T chunk written back (bf16)
   uint64_t* acc_done = ds_full + 2;
-  uint64_t* g_tail = acc_done + 1;                // the sequence's last query tile, before its rows are cut
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(g_tail + 1);
+  uint64_t* q_tail = acc_done + 1;                // the sequence's last query tile, before its rows are cut
+  uint64_t* d_tail = q_tail + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(d_tail + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -200,9 +215,14 @@ __global__ void __launch_bounds__(kKVThreads, 1)
   const int box = g.group * g.TQ;                 // rows a query tile's copy brings
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
-    for (int s = 0; s < NST; ++s) {
-      mbar_init(&g_full[s], 1);
-      mbar_init(&g_empty[s], 1);
+    for (int s = 0; s < NQ; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+    }
+    for (int s = 0; s < ND; ++s) {
+      mbar_init(&d_full[s], 1);
+      mbar_init(&d_empty[s], 1);
+      mbar_init(&v_full[s], 1);
     }
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
@@ -211,15 +231,13 @@ __global__ void __launch_bounds__(kKVThreads, 1)
       mbar_init(&ds_full[c], kComputeThreads);
     }
     mbar_init(acc_done, 1);
-    mbar_init(g_tail, 1);
+    mbar_init(q_tail, 1);
+    mbar_init(d_tail, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (box < 128 && warp >= 2 && warp < 2 + 2 * NST) {
-    // rows box..127 of every query tile are never loaded
-    const int w = warp - 2;
-    zero_tile_rows(sStage + (w >> 1) * T::STAGE_BYTES + (w & 1) * T::TILE, T::NCH, box, lane);
-  }
+  // rows box..127 of every query tile are never loaded (sQ and sdO are adjacent)
+  if (box < 128 && warp >= 2 && warp < 2 + NQ + ND) zero_tile_rows(sQ + (warp - 2) * T::TILE, T::NCH, box, lane);
   if (warp == 1) {
     tmem_alloc(tmem_slot, T::TMEM_COLS);
     tmem_relinquish();
@@ -246,40 +264,77 @@ __global__ void __launch_bounds__(kKVThreads, 1)
         tma_load_3d(sV + c * T::CHUNK, &tmV, kv_full, c * 64, kvh, (int)krow0);
       }
     }
-    int issued = 0;
-    for (int n = 0; n < cnt; ++n) {
-      const int s = n % NST;
-      if (!mbar_wait_warp(&g_empty[s], ((uint32_t)(n / NST) & 1u) ^ 1u, abort_flag, ctl, kid | W_GEMPTY)) break;
-      const int t0 = (i0 + n) * g.TQ;
-      const int rows = min(g.TQ, q.lq - t0) * g.group;
-      const bool tail = rows < box;
-      uint64_t* bar = tail ? g_tail : &g_full[s];
-      uint8_t* st = sStage + s * T::STAGE_BYTES;
+    // rows of the last tile, when the box reaches past the sequence's end
+    const int last_rows = min(g.TQ, q.lq - (i0 + cnt - 1) * g.TQ) * g.group;
+    const bool cut = last_rows < box;
+    const uint32_t tx = (uint32_t)box * D * 2;
+    auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int n) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, tx);
+        for (int c = 0; c < T::NCH; ++c)
+          tma_load_3d(dst + c * T::CHUNK, map, bar, c * 64, kvh * g.group, q.q0 + (i0 + n) * g.TQ);
+      }
+    };
+    auto load_q = [&](int n) {
+      load(&tmQ, sQ + (n % NQ) * T::TILE, cut && n == cnt - 1 ? q_tail : &q_full[n % NQ], n);
+    };
+    auto load_do = [&](int n) {
+      load(&tmdO, sdO + (n % ND) * T::TILE, cut && n == cnt - 1 ? d_tail : &d_full[n % ND], n);
+    };
+    auto load_vec = [&](int n) {
       if (lane == 0) {
         const long long vec = ((long long)kvh * g.nslot_q + qslot0 + n) * 128;
-        mbar_arrive_expect_tx(bar, 2 * (uint32_t)box * D * 2 + 2 * T::VEC_BYTES);
-        for (int c = 0; c < T::NCH; ++c) {
-          tma_load_3d(st + c * T::CHUNK, &tmQ, bar, c * 64, kvh * g.group, q.q0 + t0);
-          tma_load_3d(st + T::TILE + c * T::CHUNK, &tmdO, bar, c * 64, kvh * g.group, q.q0 + t0);
-        }
-        bulk_load(st + 2 * T::TILE, L2w + vec, T::VEC_BYTES, bar);
-        bulk_load(st + 2 * T::TILE + T::VEC_BYTES, Dw + vec, T::VEC_BYTES, bar);
+        uint8_t* dst = sVec + (n % ND) * 2 * T::VEC_BYTES;
+        mbar_arrive_expect_tx(&v_full[n % ND], 2 * T::VEC_BYTES);
+        bulk_load(dst, L2w + vec, T::VEC_BYTES, &v_full[n % ND]);
+        bulk_load(dst + T::VEC_BYTES, Dw + vec, T::VEC_BYTES, &v_full[n % ND]);
       }
-      if (tail) {
-        if (!mbar_wait_warp(g_tail, 0, nullptr, ctl, kid | W_TAIL)) {
-          *abort_flag = 1;
-          break;
-        }
-        zero_tile_rows(st, T::NCH, rows, lane);
-        zero_tile_rows(st + T::TILE, T::NCH, rows, lane);
-        if (lane == 0) mbar_arrive(&g_full[s]);
+    };
+    for (int n = 0; n < min(cnt, NQ); ++n) {
+      load_q(n);
+      if (n < ND) {
+        load_do(n);
+        load_vec(n);
       }
-      issued = n + 1;
+    }
+    int nd = min(cnt, ND), nq = min(cnt, NQ);      // tiles whose dO and vectors, Q are under way
+    for (int n = 0; n + ND < cnt; ++n) {
+      if (!mbar_wait_warp(&d_empty[n % ND], (uint32_t)(n / ND) & 1u, abort_flag, ctl, kid | W_GEMPTY)) break;
+      load_do(n + ND);
+      ++nd;
+      const bool freed = mbar_wait_warp(&q_empty[n % NQ], (uint32_t)(n / NQ) & 1u, abort_flag, ctl, kid | W_GEMPTY);
+      load_vec(n + ND);                            // (loaded even on an abort: nd counts both)
+      if (!freed) break;
+      if (n + NQ < cnt) {
+        load_q(n + NQ);
+        ++nq;
+      }
+    }
+    if (cut && nq == cnt && nd == cnt) {
+      if (mbar_wait_warp(q_tail, 0, nullptr, ctl, kid | W_TAIL)) {
+        zero_tile_rows(sQ + ((cnt - 1) % NQ) * T::TILE, T::NCH, last_rows, lane);
+        if (lane == 0) mbar_arrive(&q_full[(cnt - 1) % NQ]);
+      } else {
+        *abort_flag = 1;
+      }
+      if (mbar_wait_warp(d_tail, 0, nullptr, ctl, kid | W_TAIL)) {
+        zero_tile_rows(sdO + ((cnt - 1) % ND) * T::TILE, T::NCH, last_rows, lane);
+        if (lane == 0) mbar_arrive(&d_full[(cnt - 1) % ND]);
+      } else {
+        *abort_flag = 1;
+      }
+    } else if (cut) {                              // an abort: only the drain is left
+      if (nq == cnt) mbar_wait(q_tail, 0, nullptr, ctl, kid | W_DRAIN);
+      if (nd == cnt) mbar_wait(d_tail, 0, nullptr, ctl, kid | W_DRAIN);
     }
     // every copy this warp started must land before the CTA exits
     mbar_wait(kv_full, 0, nullptr, ctl, kid | W_DRAIN);
-    for (int n = (issued > NST ? issued - NST : 0); n < issued; ++n)
-      mbar_wait(&g_full[n % NST], (uint32_t)(n / NST) & 1u, nullptr, ctl, kid | W_DRAIN);
+    for (int n = max(0, nq - NQ); n < nq; ++n)
+      if (!(cut && n == cnt - 1)) mbar_wait(&q_full[n % NQ], (uint32_t)(n / NQ) & 1u, nullptr, ctl, kid | W_DRAIN);
+    for (int n = max(0, nd - ND); n < nd; ++n) {
+      if (!(cut && n == cnt - 1)) mbar_wait(&d_full[n % ND], (uint32_t)(n / ND) & 1u, nullptr, ctl, kid | W_DRAIN);
+      mbar_wait(&v_full[n % ND], (uint32_t)(n / ND) & 1u, nullptr, ctl, kid | W_DRAIN);
+    }
   } else if (warp == 1) {
     // ---------------- MMA issuer (whole warp, one elected lane issues) ----------------
     // Order, as in attn_bwd.cu: S^T(0), dP^T(0), then per query tile n
@@ -290,12 +345,14 @@ __global__ void __launch_bounds__(kKVThreads, 1)
     constexpr uint32_t ID_G = idesc_bf16_f32(128, D, false, true);
     const uint64_t dK0 = sdesc_sw128(smem_u32(sK), 16, 1024);
     const uint64_t dV0 = sdesc_sw128(smem_u32(sV), 16, 1024);
-    const uint64_t dS0 = sdesc_sw128(smem_u32(sStage), 16, 1024);          // K-major view of a stage
-    const uint64_t dSmn0 = sdesc_sw128(smem_u32(sStage), T::CHUNK, 1024);  // MN-major view
+    const uint64_t dQ0 = sdesc_sw128(smem_u32(sQ), 16, 1024);               // K-major views
+    const uint64_t ddO0 = sdesc_sw128(smem_u32(sdO), 16, 1024);
+    const uint64_t dQmn0 = sdesc_sw128(smem_u32(sQ), T::CHUNK, 1024);       // MN-major views
+    const uint64_t ddOmn0 = sdesc_sw128(smem_u32(sdO), T::CHUNK, 1024);
     // S^T = K Q^T (t = 0) or dP^T = V dO^T (t = 1); returns the test of `probe`
     auto issue_sdp = [&](int n, int t, uint64_t* probe, uint32_t probe_par) -> uint32_t {
       const uint64_t a0 = t ? dV0 : dK0;
-      const uint64_t b0 = desc_off(dS0, (uint32_t)((n % NST) * T::STAGE_BYTES + t * T::TILE));
+      const uint64_t b0 = t ? desc_off(ddO0, (uint32_t)(n % ND) * T::TILE) : desc_off(dQ0, (uint32_t)(n % NQ) * T::TILE);
       uint32_t r = 0u;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
@@ -308,7 +365,7 @@ __global__ void __launch_bounds__(kKVThreads, 1)
     };
     // chunk c of dV += P^T dO (t = 0) or dK += dS^T Q (t = 1); returns the test of `probe`
     auto issue_grad = [&](int n, int t, int c, uint64_t* probe, uint32_t probe_par) -> uint32_t {
-      const uint64_t b0 = desc_off(dSmn0, (uint32_t)((n % NST) * T::STAGE_BYTES + (t ? 0 : T::TILE)));
+      const uint64_t b0 = t ? desc_off(dQmn0, (uint32_t)(n % NQ) * T::TILE) : desc_off(ddOmn0, (uint32_t)(n % ND) * T::TILE);
       uint32_t r = 0u;
       int m = 0;
 #pragma unroll
@@ -321,39 +378,51 @@ __global__ void __launch_bounds__(kKVThreads, 1)
       return r;
     };
     bool ok = mbar_wait_warp(kv_full, 0, abort_flag, ctl, kid | W_KV) &&
-              mbar_wait_warp(&g_full[0], 0, abort_flag, ctl, kid | W_GFULL);
+              mbar_wait_warp(&q_full[0], 0, abort_flag, ctl, kid | W_GFULL);
     uint32_t tp0 = 0u;
     if (ok) {
       tc_fence_after();
       issue_sdp(0, 0, nullptr, 0u);
-      tp0 = issue_sdp(0, 1, &p_full[0], 0u);
+      ok = mbar_wait_warp(&d_full[0], 0, abort_flag, ctl, kid | W_GFULL);
+      if (ok) {
+        tc_fence_after();
+        tp0 = issue_sdp(0, 1, &p_full[0], 0u);
+      }
     }
     for (int n = 0; ok && n < cnt; ++n) {
       const bool more = n + 1 < cnt;
       const uint32_t par = (uint32_t)n & 1u;
-      const uint32_t tg = more ? mbar_test(&g_full[(n + 1) % NST], (uint32_t)((n + 1) / NST) & 1u) : 0u;
+      const uint32_t tq = more ? mbar_test(&q_full[(n + 1) % NQ], (uint32_t)((n + 1) / NQ) & 1u) : 0u;
       if (!mbar_wait_warp_tested(&p_full[0], par, tp0, abort_flag, ctl, kid | W_P)) break;
       tc_fence_after();
       const uint32_t tp1 = issue_grad(n, 0, 0, &p_full[1], par);
       if (!mbar_wait_warp_tested(&p_full[1], par, tp1, abort_flag, ctl, kid | W_P)) break;
       tc_fence_after();
       issue_grad(n, 0, 1, nullptr, 0u);
+      mma_commit_w(&d_empty[n % ND]);
       uint32_t td0 = 0u;
       if (more) {
-        if (!mbar_wait_warp_tested(&g_full[(n + 1) % NST], (uint32_t)((n + 1) / NST) & 1u, tg, abort_flag, ctl,
+        if (!mbar_wait_warp_tested(&q_full[(n + 1) % NQ], (uint32_t)((n + 1) / NQ) & 1u, tq, abort_flag, ctl,
                                    kid | W_GFULL))
           break;
         tc_fence_after();
         td0 = issue_sdp(n + 1, 0, &ds_full[0], par);
       }
+      const uint32_t tdo = more ? mbar_test(&d_full[(n + 1) % ND], (uint32_t)((n + 1) / ND) & 1u) : 0u;
       if (!mbar_wait_warp_tested(&ds_full[0], par, td0, abort_flag, ctl, kid | W_DSFULL)) break;
       tc_fence_after();
       const uint32_t td1 = issue_grad(n, 1, 0, &ds_full[1], par);
       if (!mbar_wait_warp_tested(&ds_full[1], par, td1, abort_flag, ctl, kid | W_DSFULL)) break;
       tc_fence_after();
       issue_grad(n, 1, 1, nullptr, 0u);
-      mma_commit_w(&g_empty[n % NST]);
-      if (more) tp0 = issue_sdp(n + 1, 1, &p_full[0], par ^ 1u);
+      mma_commit_w(&q_empty[n % NQ]);
+      if (more) {
+        if (!mbar_wait_warp_tested(&d_full[(n + 1) % ND], (uint32_t)((n + 1) / ND) & 1u, tdo, abort_flag, ctl,
+                                   kid | W_GFULL))
+          break;
+        tc_fence_after();
+        tp0 = issue_sdp(n + 1, 1, &p_full[0], par ^ 1u);
+      }
     }
     mma_commit_w(acc_done);
     mbar_wait_warp(acc_done, 0, nullptr, ctl, kid | W_DRAIN);
@@ -370,14 +439,13 @@ __global__ void __launch_bounds__(kKVThreads, 1)
     const int q0 = hf * W;                         // first tile row of this warp's columns
     bool ok = true;
     for (int n = 0; ok && n < cnt; ++n) {
-      const int s = n % NST;
-      if (!mbar_wait_warp(&g_full[s], (uint32_t)(n / NST) & 1u, abort_flag, ctl, kid | W_GFULL) ||
+      if (!mbar_wait_warp(&v_full[n % ND], (uint32_t)(n / ND) & 1u, abort_flag, ctl, kid | W_GFULL) ||
           !mbar_wait_warp(s_full, (uint32_t)n & 1u, abort_flag, ctl, kid | W_S)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const float4* l4 = reinterpret_cast<const float4*>(sStage + s * T::STAGE_BYTES + 2 * T::TILE) + q0 / 4;
+      const float4* l4 = reinterpret_cast<const float4*>(sVec + (n % ND) * 2 * T::VEC_BYTES) + q0 / 4;
       const float4* d4 = l4 + 32;
       // causal: tile row q sees this thread's key from q >= lo on (tokens in order, heads inside a token)
       const int first = (i0 + n) * g.TQ + off;     // last key that the tile's first token sees
