@@ -53,6 +53,11 @@ inline PackedGeom packed_geom(const dsv_packed& p, const int32_t* q_ptr, const i
   return g;
 }
 
+// Rows on 32-byte boundaries.
+inline int wide_rows(const dsv_view& v) {
+  return reinterpret_cast<uintptr_t>(v.ptr) % 32 == 0 && v.head_stride % 16 == 0 && v.token_stride % 16 == 0;
+}
+
 struct PackedSeq {
   int s, q0, lq, k0, lk;
 };

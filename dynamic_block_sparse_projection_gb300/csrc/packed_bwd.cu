@@ -88,6 +88,18 @@ __global__ void __launch_bounds__(256) packed_bwd_prep_kernel(const __grid_const
   }
 }
 
+// 32 bf16 values of a row, a sector at a time where the rows' addresses allow it.
+__device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t* w, bool wide) {
+  if (wide) {
+    st_global_32(dst, w);
+    st_global_32(dst + 16, w + 8);
+  } else {
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      reinterpret_cast<uint4*>(dst)[p] = make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
+  }
+}
+
 enum : unsigned int {
   W_KV = 1, W_GFULL, W_GEMPTY, W_S, W_P, W_ACC, W_DRAIN, W_KFULL, W_VFULL, W_KVEMPTY, W_SPFREE, W_DSFULL, W_DSEMPTY,
   W_ITEM, W_ITEMFREE, W_TAIL
@@ -151,7 +163,7 @@ __global__ void __launch_bounds__(kKVThreads, 1)
                          const __grid_constant__ PackedGeom g, const float* __restrict__ L2w,
                          const float* __restrict__ Dw, float scale, __nv_bfloat16* dK, long long dk_head,
                          long long dk_tok, __nv_bfloat16* dV, long long dv_head, long long dv_tok, int nsplit,
-                         float* part, Ctl ctl) {
+                         float* part, int wide, Ctl ctl) {
   using T = PKVTraits<D>;
   constexpr int NQ = T::NQ, ND = T::ND;
   constexpr int W = T::W;
@@ -534,9 +546,7 @@ __global__ void __launch_bounds__(kKVThreads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               w[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * mul, __uint_as_float(o[2 * i + 1]) * mul);
-            uint4* dst = reinterpret_cast<uint4*>(outp + c * 32);
-#pragma unroll
-            for (int p = 0; p < 4; ++p) dst[p] = make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
+            store_row32(outp + c * 32, w, wide);
           }
         }
       }
@@ -608,7 +618,7 @@ struct PQTraits {
   static constexpr int NV = (8 * TILE + 2048 <= 227 * 1024) ? 3 : 2;
   static constexpr int NBAR = 1 + 2 * NK + 2 * NV + 8 + 4 + 2 + 1;   // even: the answer after it is 16-byte aligned
   static_assert(NBAR % 2 == 0, "alignment of the work request's answer");
-  static constexpr int SMEM_USED = 1024 + 2 * TILE + (NK + NV) * TILE + NBAR * 8 + 16 + 16 + 2 * (int)sizeof(QItem);
+  static constexpr int SMEM_USED = 1024 + 2 * TILE + (NK + NV) * TILE + NBAR * 8 + 16 + 16 + 2 * (int)sizeof(QItem) + 1024;
   static_assert(SMEM_USED <= 227 * 1024, "dQ tiles exceed shared memory");
   static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
   static constexpr uint32_t S_COL = 0, DP_COL = 128, DQ_COL = 256, DS_COL = 256 + D, TMEM_COLS = 512;
@@ -623,7 +633,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
                         const __grid_constant__ PackedGeom g, const float* __restrict__ L2w,
                         const float* __restrict__ Dw, float scale, __nv_bfloat16* dQ, long long dq_head,
-                        long long dq_tok, Ctl ctl) {
+                        long long dq_tok, int wide, Ctl ctl) {
   using T = PQTraits<D>;
   constexpr int NK = T::NK, NV = T::NV;
   constexpr int HALF = T::HALF;
@@ -651,8 +661,9 @@ __global__ void __launch_bounds__(kQThreads, 1)
   uint64_t* item_free = item_full + 2;            // [2]
   uint64_t* near_end = item_free + 2;             // the K producer is about to finish its item
   uint64_t* clc_full = near_end + 1;              // the work request's answer is there
-  void* clc = clc_full + 2;                       // 16 bytes
-  QItem* items = reinterpret_cast<QItem*>(clc_full + 4);
+  void* clc = bars + T::NBAR;                     // 16 bytes
+  float* sVec = reinterpret_cast<float*>(bars + T::NBAR + 2);   // -lse2 of the tile's rows, then D
+  QItem* items = reinterpret_cast<QItem*>(sVec + 256);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -802,13 +813,19 @@ __global__ void __launch_bounds__(kQThreads, 1)
         // the first K tile goes ahead of Q and dO, whose buffers are free only
         // when the previous item's last S and dP products are done
         if (n == min(1, it.nt - 1)) {
+          // (and the rows' vectors free once the compute warps hold the last tile)
+          const uint32_t last = gq - (uint32_t)n - 1;
           if (qd_issued > 0 &&
-              !mbar_wait_warp(qd_free, (uint32_t)(qd_issued - 1) & 1u, abort_flag, ctl, kid | W_KVEMPTY)) {
+              (!mbar_wait_warp(qd_free, (uint32_t)(qd_issued - 1) & 1u, abort_flag, ctl, kid | W_KVEMPTY) ||
+               !mbar_wait_warp(sp_free, last & 1u, abort_flag, ctl, kid | W_SPFREE))) {
             ok = false;
             break;
           }
           if (lane == 0) {
-            mbar_arrive_expect_tx(qd_full, 2 * q_bytes);
+            const long long vec = ((long long)it.kvh * g.nslot_q + it.slot) * 128;
+            mbar_arrive_expect_tx(qd_full, 2 * q_bytes + 1024);
+            bulk_load(sVec, L2w + vec, 512, qd_full);
+            bulk_load(sVec + 128, Dw + vec, 512, qd_full);
             for (int c = 0; c < T::NCH; ++c) {
               tma_load_3d(sdO + c * T::CHUNK, &tmdO, qd_full, c * 64, it.kvh * g.group, it.tok);
               tma_load_3d(sQ + c * T::CHUNK, &tmQ, qd_full, c * 64, it.kvh * g.group, it.tok);
@@ -857,57 +874,58 @@ __global__ void __launch_bounds__(kQThreads, 1)
     const uint64_t dK0 = sdesc_sw128(smem_u32(sK), 16, 1024);
     const uint64_t dV0 = sdesc_sw128(smem_u32(sV), 16, 1024);
     const uint64_t dKmn0 = sdesc_sw128(smem_u32(sK), T::CHUNK, 1024);
-    // tk / tv: early tests of K_n / V_n (see mbar_test); td: of dS of tile n-1
-    auto issue_sdp = [&](uint32_t gn, uint32_t tk, uint32_t tv, uint32_t* td) -> bool {
-      const int sk = (int)(gn % NK), sv = (int)(gn % NV);
-      if (!mbar_wait_warp_tested(&k_full[sk], (gn / NK) & 1u, tk, abort_flag, ctl, kid | W_KFULL)) return false;
-      tc_fence_after();
-      const uint64_t kb = desc_off(dK0, (uint32_t)sk * T::TILE);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t o = (kk >> 2) * T::CHUNK + (kk & 3) * 32;
-        mma_ss_w(tmem + T::S_COL, desc_off(dQ0, o), desc_off(kb, o), ID_S, kk > 0 ? 1u : 0u);
-      }
-      if (td != nullptr) *td = mbar_test(ds_full, (gn - 1) & 1u);
-      if (!mbar_wait_warp_tested(&v_full[sv], (gn / NV) & 1u, tv, abort_flag, ctl, kid | W_VFULL)) return false;
-      tc_fence_after();
-      const uint64_t vb = desc_off(dV0, (uint32_t)sv * T::TILE);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t o = (kk >> 2) * T::CHUNK + (kk & 3) * 32;
-        mma_ss_w(tmem + T::DP_COL, desc_off(ddO0, o), desc_off(vb, o), ID_S, kk > 0 ? 1u : 0u);
-      }
-      mma_commit_w(s_full);
-      mma_commit_w(&v_empty[sv]);   // V_j is only needed by dP
-      return true;
-    };
+    // S and dP run one tile ahead of dQ.  Step n = -1 issues an item's first
+    // ones; each product has one place in the code (the opaque asm keeps the
+    // compiler from giving that step a copy): instructions that run once an
+    // item are fetched anew each time and issue several times slower.
     uint32_t gq = 0;
     bool ok = true;
     QItem it;
     for (uint32_t i = 0; ok && take(i, it); ++i) {
-      // S and dP are single-buffered: the previous item's last ones must have been read
-      ok = mbar_wait_warp(qd_full, i & 1u, abort_flag, ctl, kid | W_KV) &&
-           (gq == 0 || mbar_wait_warp(sp_free, (gq - 1) & 1u, abort_flag, ctl, kid | W_SPFREE));
-      if (ok) ok = issue_sdp(gq, 0u, 0u, nullptr);
-      if (ok && it.nt == 1) mma_commit_w(qd_free);    // the item's last read of dO
-      for (int n = 0; ok && n < it.nt; ++n) {
+      int n = -1;
+      asm volatile("" : "+r"(n));
+      for (; n < it.nt; ++n) {
         const uint32_t gn = gq + (uint32_t)n;
         uint32_t td = 0u;
         if (n + 1 < it.nt) {
-          const uint32_t tk = mbar_test(&k_full[(gn + 1) % NK], ((gn + 1) / NK) & 1u);
-          const uint32_t tv = mbar_test(&v_full[(gn + 1) % NV], ((gn + 1) / NV) & 1u);
-          // overwrite S and dP once the compute warps hold tile n
-          if (!mbar_wait_warp(sp_free, gn & 1u, abort_flag, ctl, kid | W_SPFREE)) {
+          const int sk = (int)((gn + 1) % NK), sv = (int)((gn + 1) % NV);
+          const uint32_t phk = ((gn + 1) / NK) & 1u, phv = ((gn + 1) / NV) & 1u;
+          const uint32_t tk = mbar_test(&k_full[sk], phk);
+          const uint32_t tv = mbar_test(&v_full[sv], phv);
+          if (n < 0 && !mbar_wait_warp(qd_full, i & 1u, abort_flag, ctl, kid | W_KV)) {
+            ok = false;
+            break;
+          }
+          // S and dP are single-buffered: overwrite them once the compute warps hold tile n
+          if ((gn + 1 > 0 && !mbar_wait_warp(sp_free, gn & 1u, abort_flag, ctl, kid | W_SPFREE)) ||
+              !mbar_wait_warp_tested(&k_full[sk], phk, tk, abort_flag, ctl, kid | W_KFULL)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          if (!issue_sdp(gn + 1, tk, tv, &td)) {
+          const uint64_t kb = desc_off(dK0, (uint32_t)sk * T::TILE);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * T::CHUNK + (kk & 3) * 32;
+            mma_ss_w(tmem + T::S_COL, desc_off(dQ0, o), desc_off(kb, o), ID_S, kk > 0 ? 1u : 0u);
+          }
+          td = mbar_test(ds_full, gn & 1u);
+          if (!mbar_wait_warp_tested(&v_full[sv], phv, tv, abort_flag, ctl, kid | W_VFULL)) {
             ok = false;
             break;
           }
-          if (n + 2 == it.nt) mma_commit_w(qd_free);    // the item's last read of dO
+          tc_fence_after();
+          const uint64_t vb = desc_off(dV0, (uint32_t)sv * T::TILE);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * T::CHUNK + (kk & 3) * 32;
+            mma_ss_w(tmem + T::DP_COL, desc_off(ddO0, o), desc_off(vb, o), ID_S, kk > 0 ? 1u : 0u);
+          }
+          mma_commit_w(s_full);
+          mma_commit_w(&v_empty[sv]);                     // V_j is only needed by dP
+          if (n + 2 == it.nt) mma_commit_w(qd_free);      // the item's last read of Q and dO
         }
+        if (n < 0) continue;
         // ds_full of an item's first tile also means that the previous item's dQ has been read
         if (!mbar_wait_warp_tested(ds_full, gn & 1u, td, abort_flag, ctl, kid | W_DSFULL)) {
           ok = false;
@@ -946,9 +964,9 @@ __global__ void __launch_bounds__(kQThreads, 1)
       const bool row_ok = rt < it.ntok;
       __nv_bfloat16* out = dQ + (long long)(it.kvh * g.group + rh) * dq_head + ((long long)it.tok + rt) * dq_tok +
                            hf * (D / 2);
-      const long long vec = ((long long)it.kvh * g.nslot_q + it.slot) * 128 + r;
-      const float nlse2 = L2w[vec];                // -lse*log2(e); -inf for a row without keys
-      const float dd = Dw[vec];
+      if (!mbar_wait_warp(qd_full, i & 1u, abort_flag, ctl, kid | W_KV)) break;
+      const float nlse2 = sVec[r];                 // -lse*log2(e); -inf for a row without keys
+      const float dd = sVec[128 + r];
       const int lim_r = g.causal ? min(it.left, it.lim0 + rt) : it.left;   // keys that the row sees
 
       uint32_t s_tested = 0u;
@@ -1017,9 +1035,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             w[j] = pack_bf16x2(__uint_as_float(o[2 * j]) * scale, __uint_as_float(o[2 * j + 1]) * scale);
-          uint4* dst = reinterpret_cast<uint4*>(out + c * 32);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) dst[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+          store_row32(out + c * 32, w, wide);
         }
       }
       gq += (uint32_t)it.nt;
@@ -1057,7 +1073,7 @@ cudaError_t launch_t(const PackedMaps& m, const PackedGeom& g, const dsv_view& O
     __nv_bfloat16* v_out = static_cast<__nv_bfloat16*>(dV.ptr);
     kv<<<tiles * nsplit, kKVThreads, smem, st>>>(m.Q, m.K, m.V, m.dO, g, L2w, Dw, scale, k_out, dK.head_stride,
                                                  dK.token_stride, v_out, dV.head_stride, dV.token_stride, nsplit,
-                                                 part, ctl);
+                                                 part, wide_rows(dK) && wide_rows(dV), ctl);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (nsplit > 1)
       packed_bwd_join_kernel<D><<<dim3(tiles, 2), 256, 0, st>>>(g, nsplit, part, scale, k_out, dK.head_stride,
@@ -1071,7 +1087,7 @@ cudaError_t launch_t(const PackedMaps& m, const PackedGeom& g, const dsv_view& O
   if ((e = cudaFuncSetAttribute(qk, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
   qk<<<(unsigned)((long long)g.Hkv * g.nslot_q), kQThreads, smem, st>>>(
       m.Q, m.K, m.V, m.dO, g, L2w, Dw, scale, static_cast<__nv_bfloat16*>(dQ.ptr), dQ.head_stride, dQ.token_stride,
-      ctl);
+      wide_rows(dQ), ctl);
   return cudaGetLastError();
 }
 

@@ -732,8 +732,7 @@ cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
                                   : nullptr;
   float* Lpart = sp.part_keys > 0 ? Opart + (size_t)total * sp.rows * D : nullptr;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(O.ptr);
-  // rows on 32-byte boundaries are stored a sector at a time
-  const int wide = (reinterpret_cast<uintptr_t>(O.ptr) % 32 == 0 && O.head_stride % 16 == 0 && O.token_stride % 16 == 0);
+  const int wide = wide_rows(O);     // rows are stored a sector at a time
   kern<<<(unsigned)total, kFwdThreads, T::SMEM, st>>>(tmQ, tmK, tmV, g, sp.part_keys, sp.rows, items,
                                                       scale * 1.4426950408889634f, o, O.head_stride, O.token_stride,
                                                       lse, Opart, Lpart, tiles, wide, ctl);
