@@ -63,27 +63,37 @@ __global__ void __launch_bounds__(256) packed_bwd_prep_kernel(const __grid_const
   const int rows = min(g.TQ, q.lq - t0) * g.group;
   const int c = threadIdx.x % TPR;
   const long long base = ((long long)kvh * g.nslot_q + slot) * 128;
-#pragma unroll 4
-  for (int r = threadIdx.x / TPR; r < 128; r += RPC) {
-    const int rt = r / g.group, head = kvh * g.group + (r - rt * g.group);
-    const long long tok = (long long)q.q0 + t0 + rt;
-    float acc = 0.f;
-    if (r < rows) {
-      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(O + head * o_head + tok * o_tok) + c);
-      const uint4 b = __ldcs(reinterpret_cast<const uint4*>(dO + head * d_head + tok * d_tok) + c);
-      const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+  constexpr int BATCH = 4;               // rows of O and dO in flight per thread
+  for (int r0 = threadIdx.x / TPR; r0 < 128; r0 += BATCH * RPC) {
+    uint4 a[BATCH], b[BATCH];
+    float L[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int r = r0 + k * RPC, rt = r / g.group, head = kvh * g.group + (r - rt * g.group);
+      const long long tok = (long long)q.q0 + t0 + rt;
+      a[k] = b[k] = make_uint4(0, 0, 0, 0);
+      L[k] = -INFINITY;
+      if (r < rows) {
+        a[k] = __ldcs(reinterpret_cast<const uint4*>(O + head * o_head + tok * o_tok) + c);
+        b[k] = __ldcs(reinterpret_cast<const uint4*>(dO + head * d_head + tok * d_tok) + c);
+        if (c == 0) L[k] = lse[(long long)head * g.Tq + tok];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const uint32_t wa[4] = {a[k].x, a[k].y, a[k].z, a[k].w}, wb[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
+      float acc = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         acc = fmaf(__uint_as_float(wa[i] << 16), __uint_as_float(wb[i] << 16), acc);
         acc = fmaf(__uint_as_float(wa[i] & 0xFFFF0000u), __uint_as_float(wb[i] & 0xFFFF0000u), acc);
       }
-    }
 #pragma unroll
-    for (int o = TPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (c == 0) {
-      const float L = r < rows ? lse[(long long)head * g.Tq + tok] : -INFINITY;
-      Dw[base + r] = r < rows ? acc : 0.f;
-      L2w[base + r] = L == -INFINITY ? -INFINITY : -L * kLog2e;
+      for (int o = TPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+      if (c == 0) {
+        Dw[base + r0 + k * RPC] = acc;           // 0 behind the tile's rows
+        L2w[base + r0 + k * RPC] = L[k] == -INFINITY ? -INFINITY : -L[k] * kLog2e;
+      }
     }
   }
 }
@@ -169,6 +179,7 @@ __global__ void __launch_bounds__(kKVThreads, 1)
   constexpr int W = T::W;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
 
+  cudaTriggerProgrammaticLaunchCompletion();     // the q kernel may start as SMs become free
   // the CTA's key tile; every thread works it out (the same loads for all)
   int kvh, slot;
   packed_order(g, g.nslot_k, false, blockIdx.x / nsplit, kvh, slot);
@@ -559,8 +570,8 @@ __global__ void __launch_bounds__(kKVThreads, 1)
   if (warp == 1) tmem_dealloc(tmem_base, T::TMEM_COLS);
 }
 
-// Adds the parts of dV and dK (fp32, unscaled) in order.  One CTA per (key
-// tile, key head, matrix); D/4 threads a row.
+// Adds the parts of dV and dK (fp32, unscaled) in order.  CTAs per (key tile,
+// key head; matrix; sixteenth of the rows), D/4 threads a row.
 template <int D>
 __global__ void __launch_bounds__(256) packed_bwd_join_kernel(const __grid_constant__ PackedGeom g, int nsplit,
                                                               const float* __restrict__ part, float scale,
@@ -575,7 +586,7 @@ __global__ void __launch_bounds__(256) packed_bwd_join_kernel(const __grid_const
   __nv_bfloat16* out = t == 0 ? dV + kvh * dv_head : dK + kvh * dk_head;
   const long long tok = t == 0 ? dv_tok : dk_tok;
   const int c = threadIdx.x % (D / 4);
-  for (int r = threadIdx.x / (D / 4); r < kt.keys; r += 256 / (D / 4)) {
+  for (int r = blockIdx.z * 8 + threadIdx.x / (D / 4); r < min(kt.keys, (int)blockIdx.z * 8 + 8); r += 256 / (D / 4)) {
     const float4* src = reinterpret_cast<const float4*>(part) +
                         (((long long)blockIdx.x * nsplit * 2 + t) * 128 + r) * (D / 4) + c;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -875,15 +886,15 @@ __global__ void __launch_bounds__(kQThreads, 1)
     const uint64_t dV0 = sdesc_sw128(smem_u32(sV), 16, 1024);
     const uint64_t dKmn0 = sdesc_sw128(smem_u32(sK), T::CHUNK, 1024);
     // S and dP run one tile ahead of dQ.  Step n = -1 issues an item's first
-    // ones; each product has one place in the code (the opaque asm keeps the
-    // compiler from giving that step a copy): instructions that run once an
-    // item are fetched anew each time and issue several times slower.
+    // ones, so that each product has one place in the code: instructions that
+    // run once an item are fetched anew each time and issue several times
+    // slower.
     uint32_t gq = 0;
     bool ok = true;
     QItem it;
     for (uint32_t i = 0; ok && take(i, it); ++i) {
+      if (!mbar_wait_warp(qd_full, i & 1u, abort_flag, ctl, kid | W_KV)) break;
       int n = -1;
-      asm volatile("" : "+r"(n));
       for (; n < it.nt; ++n) {
         const uint32_t gn = gq + (uint32_t)n;
         uint32_t td = 0u;
@@ -892,12 +903,9 @@ __global__ void __launch_bounds__(kQThreads, 1)
           const uint32_t phk = ((gn + 1) / NK) & 1u, phv = ((gn + 1) / NV) & 1u;
           const uint32_t tk = mbar_test(&k_full[sk], phk);
           const uint32_t tv = mbar_test(&v_full[sv], phv);
-          if (n < 0 && !mbar_wait_warp(qd_full, i & 1u, abort_flag, ctl, kid | W_KV)) {
-            ok = false;
-            break;
-          }
-          // S and dP are single-buffered: overwrite them once the compute warps hold tile n
-          if ((gn + 1 > 0 && !mbar_wait_warp(sp_free, gn & 1u, abort_flag, ctl, kid | W_SPFREE)) ||
+          // S and dP are single-buffered: overwrite them once the compute warps hold
+          // tile n (before the first tile gn is -1 and its parity passes at once)
+          if (!mbar_wait_warp(sp_free, gn & 1u, abort_flag, ctl, kid | W_SPFREE) ||
               !mbar_wait_warp_tested(&k_full[sk], phk, tk, abort_flag, ctl, kid | W_KFULL)) {
             ok = false;
             break;
@@ -1047,6 +1055,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, T::TMEM_COLS);
+  // the call's work is done when this kernel is: not before the kv kernel's
+  cudaGridDependencySynchronize();
 }
 
 template <int D>
@@ -1075,19 +1085,35 @@ cudaError_t launch_t(const PackedMaps& m, const PackedGeom& g, const dsv_view& O
                                                  dK.token_stride, v_out, dV.head_stride, dV.token_stride, nsplit,
                                                  part, wide_rows(dK) && wide_rows(dV), ctl);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (nsplit > 1)
-      packed_bwd_join_kernel<D><<<dim3(tiles, 2), 256, 0, st>>>(g, nsplit, part, scale, k_out, dK.head_stride,
-                                                                 dK.token_stride, v_out, dV.head_stride,
-                                                                 dV.token_stride);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (g.Tq == 0) return cudaSuccess;
   auto qk = packed_bwd_q_kernel<D>;
   constexpr int smem = PQTraits<D>::SMEM;
   if ((e = cudaFuncSetAttribute(qk, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-  qk<<<(unsigned)((long long)g.Hkv * g.nslot_q), kQThreads, smem, st>>>(
-      m.Q, m.K, m.V, m.dO, g, L2w, Dw, scale, static_cast<__nv_bfloat16*>(dQ.ptr), dQ.head_stride, dQ.token_stride,
-      wide_rows(dQ), ctl);
+  // The q kernel needs what the prepare kernel wrote, not what the kv kernel
+  // does: its CTAs start as the kv kernel's last ones leave SMs free, and it
+  // ends no earlier than the kv kernel (packed_bwd_q_kernel's last lines).
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((long long)g.Hkv * g.nslot_q));
+  cfg.blockDim = dim3(kQThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = g.Tk > 0 ? 1 : 0;
+  if ((e = cudaLaunchKernelEx(&cfg, qk, m.Q, m.K, m.V, m.dO, g, static_cast<const float*>(L2w),
+                              static_cast<const float*>(Dw), scale, static_cast<__nv_bfloat16*>(dQ.ptr),
+                              (long long)dQ.head_stride, (long long)dQ.token_stride, wide_rows(dQ), ctl)) !=
+      cudaSuccess)
+    return e;
+  if (nsplit > 1) {
+    packed_bwd_join_kernel<D><<<dim3((unsigned)((long long)g.Hkv * g.nslot_k), 2, 16), 256, 0, st>>>(
+        g, nsplit, L2w + vec, scale, static_cast<__nv_bfloat16*>(dK.ptr), dK.head_stride, dK.token_stride,
+        static_cast<__nv_bfloat16*>(dV.ptr), dV.head_stride, dV.token_stride);
+    return cudaGetLastError();
+  }
   return cudaGetLastError();
 }
 
@@ -1096,15 +1122,16 @@ cudaError_t launch_t(const PackedMaps& m, const PackedGeom& g, const dsv_view& O
 // Runs of query tiles per key tile in the kv kernel.  With at least one key
 // tile per SM each CTA takes all query tiles of its own.  With fewer (few keys
 // against many queries: text), they are cut into runs of at least
-// kPackedMinPart tiles, enough for two rounds of the SMs, whose fp32 sums the
-// join kernel adds.
+// kPackedMinPart tiles, enough to fill the SMs once, whose fp32 sums the join
+// kernel adds (text case, 144 key tiles: 360 us a call; 370 with runs for two
+// rounds, 375 for three, 435 without).
 static int bwd_splits(const dsv_packed& p) {
   if (p.S <= 0 || p.Tq <= 0 || p.Tk <= 0) return 1;
   const long long k_tiles = (p.Tk + 127) / 128, TQ = 128 / (p.H / p.Hkv);
   const long long ctas = (long long)p.Hkv * (k_tiles > p.S ? k_tiles : p.S);
   if (ctas >= kPackedSMs) return 1;
   const long long q_tiles = (p.Tq + TQ * p.S - 1) / (TQ * p.S);      // of a sequence, on average
-  const long long n = (2LL * kPackedSMs + ctas - 1) / ctas, most = (q_tiles + kPackedMinPart - 1) / kPackedMinPart;
+  const long long n = (kPackedSMs + ctas - 1) / ctas, most = (q_tiles + kPackedMinPart - 1) / kPackedMinPart;
   return (int)(n < most ? n : most);
 }
 
