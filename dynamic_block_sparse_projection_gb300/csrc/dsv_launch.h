@@ -104,7 +104,7 @@ cudaError_t launch_cube_permute(const void* src, void* dst, const dsv_shape& s, 
 
 // Rotary positions with several axes, optionally behind an RMS norm (rope.cu).
 // dw (and ws) only with a weight.
-constexpr int kRopeParts = 1216;              // partial sums of the weight's gradient: 8 CTAs on each of 152 SMs
+constexpr int kRopeParts = 608;               // partial sums of the weight's gradient: 4 CTAs on each of 152 SMs
 cudaError_t launch_rope_fwd(const dsv_view& x, const int32_t* pos, int64_t pos_batch, const dsv_rope& r,
                             const float* weight, float eps, const dsv_view& y, cudaStream_t st);
 cudaError_t launch_rope_bwd(const dsv_view& dy, const dsv_view& x, const int32_t* pos, int64_t pos_batch,

@@ -25,7 +25,12 @@
 // at ~7 fp32 operations each.  D/8 lanes hold a token's row, 16 bytes each;
 // the four rotations of a lane serve the token's heads in turn, so that
 // sincospif costs 4 per (token, 8 channels) and not per element; the rows of
-// four heads are loaded before any is worked on.
+// a few heads are loaded before any is worked on, and registers are held to 64
+// a thread so that four CTAs share an SM (what counts is bytes in flight: at 80
+// registers the backward with norm took 86 us instead of 64).  Measured (a
+// call, share of the copy bandwidth): forward with norm, 1.0 GB: 170 us, 87 %;
+// backward without norm, 1.5 GB: 222 us, 100 %; backward with norm, 0.3 GB: 64
+// us, 70 % (the partial sums' kernel is 5 us of it).
 #include <math.h>
 
 #include "dsv_launch.h"
@@ -35,7 +40,7 @@ namespace dsv {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeBatch = 4;            // rows in flight per thread
+constexpr int kRopeBatch = 3;            // rows in flight per thread (2: 180 us on the stress queries, 3: 170, 4: 175)
 
 struct RopeTable {
   uint64_t turn[64];                     // frequency of a channel pair, fraction of a turn * 2^64
@@ -121,7 +126,7 @@ struct RopeOut {
 
 // x may be y (each 16-byte piece is read and written by one thread).
 template <int D, bool NORM>
-__global__ void __launch_bounds__(kRopeThreads) rope_fwd_kernel(RopeView x, RopeOut y, RopeArgs a,
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_fwd_kernel(RopeView x, RopeOut y, RopeArgs a,
                                                                 const __grid_constant__ RopeTable table,
                                                                 const float* __restrict__ weight) {
   constexpr int LPR = D / 8, TOK = kRopeThreads / LPR;
@@ -170,13 +175,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_fwd_kernel(RopeView x, Rope
 // gridDim.x, ... and writes its sum of g x^ to part[i]; rope_dw_kernel adds
 // the parts in order, so dw does not depend on which CTA ran first.
 template <int D, bool NORM>
-__global__ void __launch_bounds__(kRopeThreads) rope_bwd_kernel(RopeView dy, RopeView x, RopeOut dx, RopeArgs a,
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_bwd_kernel(RopeView dy, RopeView x, RopeOut dx, RopeArgs a,
                                                                 const __grid_constant__ RopeTable table,
                                                                 const float* __restrict__ weight,
                                                                 float* __restrict__ part, long long items,
                                                                 int tiles, int chunks) {
   constexpr int LPR = D / 8, TOK = kRopeThreads / LPR;
-  constexpr int BATCH = NORM ? kRopeBatch / 2 : kRopeBatch;    // rows of both inputs in flight
+  constexpr int BATCH = NORM ? 2 : 4;    // rows of both inputs in flight
   __shared__ RopeTable tab;
   __shared__ float red[TOK][D + 8];
   if (threadIdx.x < D / 2) {
@@ -247,22 +252,22 @@ __global__ void __launch_bounds__(kRopeThreads) rope_bwd_kernel(RopeView dy, Rop
   }
 }
 
-// dw[channel] = sum of the parts: 32 channels per CTA, 32 interleaved runs of
-// parts each, joined in order.
+// dw[channel] = sum of the parts: 8 channels per CTA, 128 interleaved runs of
+// parts each, joined pairwise (a fixed order).
 __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__ part, int parts, int d,
                                                        float* __restrict__ dw) {
-  __shared__ float red[32][33];
-  const int c = blockIdx.x * 32 + threadIdx.x;
+  __shared__ float red[128][8];
+  const int c = blockIdx.x * 8 + threadIdx.x, y = threadIdx.y;
   float s = 0.f;
-  for (int p = threadIdx.y; p < parts; p += 32) s += part[(long long)p * d + c];
-  red[threadIdx.y][threadIdx.x] = s;
+#pragma unroll 5
+  for (int p = y; p < parts; p += 128) s += part[(long long)p * d + c];
+  red[y][threadIdx.x] = s;
   __syncthreads();
-  if (threadIdx.y == 0) {
-    float t = 0.f;
-#pragma unroll
-    for (int r = 0; r < 32; ++r) t += red[r][threadIdx.x];
-    dw[c] = t;
+  for (int o = 64; o > 0; o >>= 1) {
+    if (y < o) red[y][threadIdx.x] += red[y + o][threadIdx.x];
+    __syncthreads();
   }
+  if (y == 0) dw[c] = red[0][threadIdx.x];
 }
 
 RopeTable rope_table(const dsv_rope& r) {
@@ -282,11 +287,11 @@ RopeTable rope_table(const dsv_rope& r) {
   return t;
 }
 
-// Heads per CTA: as many as leave at least four CTAs per SM to run (the
+// Heads per CTA: as many as leave at least `per` CTAs per SM to run (the
 // rotations are worked out once per CTA, so few heads make them dear).
-int head_chunk(const dsv_rope& r, int tiles) {
+int head_chunk(const dsv_rope& r, int tiles, int per = 4) {
   int hc = r.H;
-  while (hc > 1 && (long long)tiles * r.B * ((r.H + hc - 1) / hc) < 4 * kPackedSMs) hc = (hc + 1) / 2;
+  while (hc > 1 && (long long)tiles * r.B * ((r.H + hc - 1) / hc) < (long long)per * kPackedSMs) hc = (hc + 1) / 2;
   return hc;
 }
 
@@ -307,7 +312,7 @@ cudaError_t bwd_t(const RopeView& dy, const RopeView& x, const RopeOut& dx, Rope
                   const dsv_rope& r, const float* weight, float* dw, float* part, cudaStream_t st) {
   constexpr int TOK = kRopeThreads / (D / 8);
   const int tiles = (r.N + TOK - 1) / TOK;
-  a.chunk = head_chunk(r, tiles);
+  a.chunk = head_chunk(r, tiles, weight ? 12 : 4);
   const int chunks = (r.H + a.chunk - 1) / a.chunk;
   const long long items = (long long)tiles * chunks * r.B;
   if (!weight) {
@@ -320,7 +325,7 @@ cudaError_t bwd_t(const RopeView& dy, const RopeView& x, const RopeOut& dx, Rope
                                                                      chunks);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  rope_dw_kernel<<<D / 32, dim3(32, 32), 0, st>>>(part, parts, D, dw);
+  rope_dw_kernel<<<D / 8, dim3(8, 128), 0, st>>>(part, parts, D, dw);
   return cudaGetLastError();
 }
 
