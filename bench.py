@@ -60,6 +60,9 @@ def parse_args(argv=None):
                         "(dsv_predict_scores_max) of each group x key-block tile of low-rank logits")
     p.add_argument("--cube", default="", metavar="CT,CY,CX",
                    help="regroup tokens into ct x cy x cx cubes of the latent grid inside the step")
+    p.add_argument("--rope", choices=["plain", "norm"], default=None,
+                   help="rotate Q and K by their (t, y, x) positions inside the step (dsv_rope_axes_fwd, its gradient "
+                        "on dQ and dK at the end); norm: behind the per-row RMS norm of queries and keys")
     p.add_argument("--predict", choices=["fused", "two-call"], default="fused",
                    help="fused: dsv_predict_topk_blocks (scores stay on chip); two-call: dsv_predict_scores "
                         "then dsv_topk_blocks (the score matrix goes through HBM)")
@@ -180,9 +183,13 @@ class HotPath:
     With cube = (ct, cy, cx) the step also regroups the tokens into 3D cubes
     of the latent grid (dsv_cube_permute on Q, K, V, dO before the path, and
     its inverse on O, dQ, dK, dV after it), so that query groups and key
-    blocks are cubes; O and the gradients then come out in raster order."""
+    blocks are cubes; O and the gradients then come out in raster order.
 
-    def __init__(self, dsv, x, w, k_per_head, cube=None, mass=None, scores="mean", fused=False):
+    With rope ("plain" or "norm") the step first rotates Q and K by their
+    (t, y, x) positions, behind the RMS norm of each row for "norm", and takes
+    dQ and dK back through it (and the norm weights' gradients) at the end."""
+
+    def __init__(self, dsv, x, w, k_per_head, cube=None, mass=None, scores="mean", fused=False, rope=None):
         import torch
         self.dsv, self.x, self.w = dsv, x, w
         # the fused predictor + top-k serves the mean block scores with a fixed k per head
@@ -194,6 +201,18 @@ class HotPath:
         self.grid = (w.T, w.Hl, w.Wl)
         dev = x.Q.device
         B, H, N, d, G = w.B, w.H, w.N, w.d, w.nb
+        self.rope = rope
+        if rope:
+            from dynamic_block_sparse_projection_gb300 import workloads as wl
+            self.pos, self.bands = wl.grid_positions(*self.grid, device=dev), wl.axis_bands(d)
+            self.xr = _Tensors()
+            self.xr.Q, self.xr.K = torch.empty_like(x.Q), torch.empty_like(x.K)
+            self.xr.V, self.xr.dO, self.xr.Wq, self.xr.Wk = x.V, x.dO, x.Wq, x.Wk
+            self.rope_grads = (torch.empty_like(x.Q), torch.empty_like(x.K))
+            self.norm_w = tuple(torch.ones(d, device=dev) for _ in range(2)) if rope == "norm" else (None, None)
+            self.norm_dw = tuple(torch.empty(d, device=dev) for _ in range(2)) if rope == "norm" else (None, None)
+            self.ws_r = (torch.empty(dsv.rope_axes_bwd_workspace_bytes(d), dtype=torch.uint8, device=dev)
+                         if rope == "norm" else None)
         # the mass selection's list sizes are known only on the device: room for every block
         self.nnz = B * H * G * G if mass else dsv.nnz_of(B, G, self.k)
         self.S = None if self.fused else torch.empty(B, H, G, G, dtype=torch.float32, device=dev)
@@ -225,7 +244,8 @@ class HotPath:
     @property
     def stages(self):
         core = FUSED_STAGES if self.fused else STAGES
-        return (("cube_in",) if self.cube else ()) + core + (("cube_out",) if self.cube else ())
+        return ((("rope_in",) if self.rope else ()) + (("cube_in",) if self.cube else ()) + core +
+                (("cube_out",) if self.cube else ()) + (("rope_out",) if self.rope else ()))
 
     def run(self, ev=None):
         """The four public calls (six with cube order).  With ev (one CUDA
@@ -241,6 +261,11 @@ class HotPath:
 
         mark()
         x = self.x
+        if self.rope:
+            for src, dst, nw in zip((x.Q, x.K), (self.xr.Q, self.xr.K), self.norm_w):
+                d.rope_axes(src, self.pos, self.bands, weight=nw, out=dst)
+            mark()
+            x = self.xr
         if self.cube:
             for src, dst in zip((x.Q, x.K, x.V, x.dO), (self.xc.Q, self.xc.K, self.xc.V, self.xc.dO)):
                 d.cube_permute(src, self.grid, self.cube, out=dst)
@@ -277,13 +302,24 @@ class HotPath:
             for src, dst in zip((self.O, *self.grads), self.out_raster):
                 d.cube_permute(src, self.grid, self.cube, inverse=True, out=dst)
             mark()
+        if self.rope:
+            dQ, dK = (self.out_raster[1:3] if self.cube else self.grads[:2])
+            for g, src, out, nw, dw in zip((dQ, dK), (self.x.Q, self.x.K), self.rope_grads, self.norm_w, self.norm_dw):
+                d.rope_axes_bwd(g, self.pos, self.bands, x=src if nw is not None else None, weight=nw, dx=out,
+                                dweight=dw, workspace=self.ws_r)
+            mark()
 
     def results(self):
         """O, LSE and the gradients as the step hands them out (raster order;
-        LSE stays in the path's token order)."""
+        LSE stays in the path's token order; with the norm also the gradients
+        of its two weights)."""
         if self.cube:
-            return (self.out_raster[0], self.lse, *self.out_raster[1:])
-        return (self.O, self.lse, *self.grads)
+            out = (self.out_raster[0], self.lse, *self.out_raster[1:])
+        else:
+            out = (self.O, self.lse, *self.grads)
+        if self.rope:
+            out = (*out[:2], *self.rope_grads, out[4], *(t for t in self.norm_dw if t is not None))
+        return out
 
     def attention_only(self):
         d, x, w = self.dsv, self.x, self.w
@@ -294,7 +330,7 @@ class HotPath:
 
 
 KERNELS_PER_STEP = {"predict": 2, "topk": 4, "predict_topk": 7, "fwd": 1, "bwd_pre": 1, "bwd_kv": 2, "bwd_q": 1,
-                    "cube_in": 4, "cube_out": 4}
+                    "cube_in": 4, "cube_out": 4, "rope_in": 2, "rope_out": 2}
 
 
 def predict_topk_launches(w) -> int:
@@ -365,7 +401,7 @@ def run_ours(args):
         dispatch = {"profile": f"profiles/dispatch_{w.name}.json", "threshold_rho": prof.get("threshold_rho"),
                     "dense_heads": [h for h, d in enumerate(dense) if d]}
     hp = HotPath(dsv, x, w, ks, cube=cube, mass=args.mass or None, scores=args.scores,
-                 fused=args.predict == "fused")
+                 fused=args.predict == "fused", rope=args.rope)
     fwd_f, bwd_f = pair_flops(w.block, w.d)
     flush = torch.empty(L2_FLUSH_BYTES, dtype=torch.uint8, device=dev)
 
@@ -421,7 +457,7 @@ def run_ours(args):
         dense = time_dense(dsv, x, w, hp, flush, attn_ms=attn_ms, pre_ms=pre_ms(per_call))
 
     # roofline of the dominant kernel (the predictor and the top-k are whole calls of several launches)
-    dom = max(hp.stages, key=lambda k: per_call[k])
+    dom = max((k for k in hp.stages if k in KERNEL_SRC), key=lambda k: per_call[k])
     roofline = roofline_entry(dom, per_call, w, hp, peaks, peak_src, bf16_peak, bf16_kind)
     bwd_eff = step_flops * bwd_f / (fwd_f + bwd_f) / (per_call["bwd"] * 1e-3) / 1e12
 
@@ -440,6 +476,9 @@ def run_ours(args):
                    **({"dispatch": dispatch} if dispatch else {}),
                    **({"cube": list(cube), "token_order": "3D cubes (dsv_cube_permute in and out, timed)"}
                       if cube else {}),
+                   **({"rope": "Q and K " + ("normalised and " if args.rope == "norm" else "") +
+                       "rotated by (t, y, x), gradients taken back (dsv_rope_axes_fwd, dsv_rope_axes_bwd, timed)"}
+                      if args.rope else {}),
                    **({"selection": f"mass threshold tau={args.mass}, temperature 1/sqrt(d), k in [1, nb]"}
                       if args.mass else {}),
                    **({"block_scores": "tile maximum of the low-rank logits (dsv_predict_scores_max)"}
@@ -461,13 +500,14 @@ def run_ours(args):
         "speedup_vs_dense": dense,
         "roofline": roofline,
         "gpu_launches": (sum(predict_topk_launches(w) if k == "predict_topk" else KERNELS_PER_STEP[k] for k in stages)
-                         + (2 if args.mass else 0)) * args.steps,
+                         + (2 if args.mass else 0) + (2 if args.rope == "norm" else 0)) * args.steps,
         "clocks": clk.summary(),
         "e2e": e2e,
         "peaks_source": peak_src,
     }
     if rank == 0 and world == 1 and not args.no_cpu_baseline:
-        out["cpu_baseline"] = cpu_baseline(w, x, cube=cube, mass=args.mass or None, scores=args.scores)
+        out["cpu_baseline"] = cpu_baseline(w, x, cube=cube, mass=args.mass or None, scores=args.scores,
+                                           rope=args.rope)
     if rank == 0:
         print(json.dumps(out), flush=True)
     if world > 1:
@@ -646,7 +686,8 @@ def time_e2e(dsv, x, w, hp, args, flops_per_step):
         dev_in = [torch.empty_like(t) for t in (x.Q, x.K, x.V, x.dO, x.Wq, x.Wk)]
         xd = X()
         xd.Q, xd.K, xd.V, xd.dO, xd.Wq, xd.Wk = dev_in
-        hp2 = HotPath(dsv, xd, w, hp.k, cube=hp.cube, mass=hp.mass, scores=hp.scores, fused=hp.fused)
+        hp2 = HotPath(dsv, xd, w, hp.k, cube=hp.cube, mass=hp.mass, scores=hp.scores, fused=hp.fused,
+                      rope=hp.rope)
         if host_out is None:
             host_out = [torch.empty(t.shape, dtype=t.dtype, pin_memory=True) for t in hp2.results()]
         sets.append((dev_in, hp2, host_out))
@@ -751,9 +792,15 @@ def _oracle_worker(conn, path, meta):
     Wq = np.load(os.path.join(path, "Wq.npy"))[None]
     Wk = np.load(os.path.join(path, "Wk.npy"))[None]
     block, d, k, nb = meta["block"], meta["d"], meta["k"], meta["nb"]
+    if meta["rope"]:
+        from dynamic_block_sparse_projection_gb300 import workloads as wl
+        pos = wl.grid_positions(*meta["grid"]).numpy()
+        for nm in ("Q", "K"):
+            X[nm] = oracle.rope_axes(X[nm].full(), pos, wl.axis_bands(d),
+                                     weight=np.ones(d) if meta["rope"] == "norm" else None)
     if meta["cube"]:
         perm = oracle.cube_order(*meta["grid"], *meta["cube"])
-        X = {nm: oracle.permute_tokens(t.full(), perm) for nm, t in X.items()}
+        X = {nm: oracle.permute_tokens(t.full() if isinstance(t, _Bf16Head) else t, perm) for nm, t in X.items()}
     Q, K, V, dO = X["Q"], X["K"], X["V"], X["dO"]
     conn.send("ready")
     while True:
@@ -782,7 +829,7 @@ class OraclePool:
     slowest process.  BLAS runs single-threaded in each process, so the
     cores used are the processes."""
 
-    def __init__(self, w, x_heads, cube=None, mass=None, scores="mean", cores=None):
+    def __init__(self, w, x_heads, cube=None, mass=None, scores="mean", cores=None, rope=None):
         import multiprocessing as mp
 
         import numpy as np
@@ -806,7 +853,7 @@ class OraclePool:
                 np.save(os.path.join(path, "Wq.npy"), x_heads.Wq[hi].double().cpu().numpy())
                 np.save(os.path.join(path, "Wk.npy"), x_heads.Wk[hi].double().cpu().numpy())
                 meta = {"block": w.block, "d": w.d, "k": int(x_heads.k_per_head[hi]), "nb": w.nb, "cube": cube,
-                        "grid": (w.T, w.Hl, w.Wl), "mass": mass, "scores": scores}
+                        "grid": (w.T, w.Hl, w.Wl), "mass": mass, "scores": scores, "rope": rope}
                 for part in range(min(per_head, len(groups))):
                     mine = groups[part::per_head]
                     a, bconn = ctx.Pipe()
@@ -885,7 +932,7 @@ def oracle_inputs(w, device):
     return x
 
 
-def cpu_baseline(w, x, min_s=10.0, max_s=30.0, cube=None, mass=None, scores="mean"):
+def cpu_baseline(w, x, min_s=10.0, max_s=30.0, cube=None, mass=None, scores="mean", rope=None):
     """The oracle on the host cores over the seeded sample, in the metric's
     unit: effective FLOPs of the pairs it processed over its wall time.
     Rounds repeat (cycling through the sample) until min_s has passed."""
@@ -893,7 +940,7 @@ def cpu_baseline(w, x, min_s=10.0, max_s=30.0, cube=None, mass=None, scores="mea
     for nm in ("Q", "K", "V", "dO", "Wq", "Wk", "k_per_head"):
         setattr(xs, nm, getattr(x, nm))
     xs.head_index = {h: h for h in range(w.H)}
-    pool = OraclePool(w, xs, cube=cube, mass=mass, scores=scores)
+    pool = OraclePool(w, xs, cube=cube, mass=mass, scores=scores, rope=rope)
     try:
         fwd_f, bwd_f = pair_flops(w.block, w.d)
         pairs, el = 0, 0.0
@@ -921,7 +968,7 @@ def run_reference(args):
     cube = tuple(int(v) for v in args.cube.split(",")) if args.cube else None
     # the inputs come from the seeded generators on the GPU when there is one (the values the GPU arm sees)
     x = oracle_inputs(w, "cuda" if torch.cuda.is_available() else "cpu")
-    pool = OraclePool(w, x, cube=cube, mass=args.mass or None, scores=args.scores)
+    pool = OraclePool(w, x, cube=cube, mass=args.mass or None, scores=args.scores, rope=args.rope)
     try:
         fwd_f, bwd_f = pair_flops(w.block, w.d)
         for _ in range(max(3, args.warmup)):
@@ -940,7 +987,7 @@ def run_reference(args):
         "steps": args.steps, "warmup": max(3, args.warmup), "ms_per_step": round(1e3 * el / args.steps, 3),
         "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "f64", "data": "synthetic",
         "config": {"workload": w.name, "description": w.description, "pairs": pairs,
-                   **({"cube": list(cube)} if cube else {}),
+                   **({"cube": list(cube)} if cube else {}), **({"rope": args.rope} if args.rope else {}),
                    **({"selection": f"mass threshold tau={args.mass}, temperature 1/sqrt(d), k in [1, nb]"}
                       if args.mass else {}),
                    **({"block_scores": "tile maximum of the low-rank logits"} if args.scores == "max" else {})},

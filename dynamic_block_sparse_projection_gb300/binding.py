@@ -8,6 +8,7 @@ module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import math
@@ -652,6 +653,19 @@ def _scratch(nbytes: int, device, workspace: Optional[torch.Tensor]) -> torch.Te
     return _workspace(nbytes, device, workspace)
 
 
+_AS_IT_IS = contextlib.nullcontext()
+
+
+def _alloc_on(stream):
+    """The context in which a call launched on `stream` allocates: the allocator
+    then knows the stream that uses the memory."""
+    if stream is None:
+        return _AS_IT_IS
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
 def _view(t: Optional[torch.Tensor]) -> View:
     """dsv_view of a [.., heads, tokens, d] tensor of 3 or 4 dimensions."""
     if t is None:
@@ -697,7 +711,8 @@ def rope_axes(x, pos, sections: Sequence[int], *, theta: float = 10000.0, weight
     _need_on(dev, at, torch.float32, weight=weight)
     _need_rows_on(dev, at, out=out)
     if out is None:
-        out = torch.empty_like(x)
+        with _alloc_on(stream):
+            out = torch.empty_like(x)
     _call(lib.dsv_rope_axes_fwd, "dsv_rope_axes_fwd", dev, _view(x), pos.data_ptr(), pos_b, r, _ptr(weight), eps,
           _view(out), _stream(dev, stream))
     return out
@@ -727,16 +742,18 @@ def rope_axes_bwd(dy, pos, sections: Sequence[int], *, theta: float = 10000.0, x
     dev, at = dy.device, dy.get_device()
     _need_on(dev, at, torch.int32, pos=pos)
     _need_rows_on(dev, at, dx=dx)
-    if dx is None:
-        dx = torch.empty_like(dy)
     nbytes, ws = 0, None
     if weight is not None:
         _need_rows_on(dev, at, x=x)
         _need_on(dev, at, torch.float32, weight=weight, dweight=dweight)
-        if dweight is None:
-            dweight = torch.empty(r.d, dtype=torch.float32, device=dev)
-        nbytes = lib.dsv_rope_axes_bwd_workspace_bytes(r)
-        ws = _scratch(nbytes, dev, workspace)
+    with _alloc_on(stream):
+        if dx is None:
+            dx = torch.empty_like(dy)
+        if weight is not None:
+            if dweight is None:
+                dweight = torch.empty(r.d, dtype=torch.float32, device=dev)
+            nbytes = lib.dsv_rope_axes_bwd_workspace_bytes(r)
+            ws = _scratch(nbytes, dev, workspace)
     _call(lib.dsv_rope_axes_bwd, "dsv_rope_axes_bwd", dev, _view(dy), _view(x if weight is not None else None),
           pos.data_ptr(), pos_b, r, _ptr(weight), eps, _view(dx), _ptr(dweight), _ptr(ws), nbytes,
           _stream(dev, stream))
@@ -786,12 +803,13 @@ def packed_attn_fwd(Q, K, V, q_ptr, k_ptr, softmax_scale: float = 0.0, *, causal
     _need_rows_on(dev, at, K=K, V=V, out=out)
     _need_on(dev, at, torch.int32, q_ptr=q_ptr, k_ptr=k_ptr)
     _need_on(dev, at, torch.float32, lse=lse)
-    if out is None:
-        out = torch.empty_like(Q)
-    if lse is None:
-        lse = torch.empty(p.H, p.Tq, dtype=torch.float32, device=dev)
     nbytes = lib.dsv_packed_attn_fwd_workspace_bytes(p)
-    ws = _scratch(nbytes, dev, workspace) if nbytes else None
+    with _alloc_on(stream):
+        if out is None:
+            out = torch.empty_like(Q)
+        if lse is None:
+            lse = torch.empty(p.H, p.Tq, dtype=torch.float32, device=dev)
+        ws = _scratch(nbytes, dev, workspace) if nbytes else None
     _call(lib.dsv_packed_attn_fwd, "dsv_packed_attn_fwd", dev, _view(Q), _view(K), _view(V), p, q_ptr.data_ptr(),
           k_ptr.data_ptr(), 1 if causal else 0, softmax_scale, _view(out), lse.data_ptr(), _ptr(ws), nbytes,
           _stream(dev, stream))
@@ -816,12 +834,13 @@ def packed_attn_bwd(Q, K, V, O, dO, lse, q_ptr, k_ptr, softmax_scale: float = 0.
     _need_rows_on(dev, at, K=K, V=V, O=O, dO=dO)
     _need_on(dev, at, torch.int32, q_ptr=q_ptr, k_ptr=k_ptr)
     _need_on(dev, at, torch.float32, lse=lse)
-    if outs is None:
-        outs = (torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V))
-    else:
+    if outs is not None:
         _need_rows_on(dev, at, dQ=outs[0], dK=outs[1], dV=outs[2])
     nbytes = lib.dsv_packed_attn_bwd_workspace_bytes(p)
-    ws = _scratch(nbytes, dev, workspace) if nbytes else None
+    with _alloc_on(stream):
+        if outs is None:
+            outs = (torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V))
+        ws = _scratch(nbytes, dev, workspace) if nbytes else None
     _call(lib.dsv_packed_attn_bwd, "dsv_packed_attn_bwd", dev, _view(Q), _view(K), _view(V), _view(O), _view(dO),
           lse.data_ptr(), p, q_ptr.data_ptr(), k_ptr.data_ptr(), 1 if causal else 0, softmax_scale, _view(outs[0]),
           _view(outs[1]), _view(outs[2]), _ptr(ws), nbytes, _stream(dev, stream))

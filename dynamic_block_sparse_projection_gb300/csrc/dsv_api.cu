@@ -217,6 +217,13 @@ dsv_status check_packed(const dsv_packed& p) {
   if (q * p.Hkv >= (1LL << 31) || k * p.Hkv >= (1LL << 31)) return DSV_ERR_UNSUPPORTED;
   return DSV_OK;
 }
+// Waits of a packed call: some last as long as a tile's whole stream of other
+// tiles, so the limit grows with the longest possible one (10 us a tile, some
+// ten times what it takes).
+void widen_wait(Ctl* ctl, const dsv_packed& p) {
+  const unsigned long long tiles = (unsigned long long)p.Tk / 128 + (unsigned long long)p.Tq / (128 / (p.H / p.Hkv)) + 2;
+  ctl->wait_limit_ns += tiles * 10000ull;
+}
 bool no_queries(const dsv_packed& p) { return p.S == 0 || p.H == 0 || p.Tq == 0; }
 bool no_keys(const dsv_packed& p) { return p.S == 0 || p.H == 0 || p.Tk == 0; }
 float packed_scale(int d, float scale) { return (scale > 0.f && isfinite(scale)) ? scale : 1.0f / sqrtf((float)d); }
@@ -675,6 +682,7 @@ dsv_status dsv_packed_attn_fwd(dsv_view Q, dsv_view K, dsv_view V, dsv_packed p,
   if (need > 0 && (!workspace || !al256(workspace) || workspace_bytes < need)) return DSV_ERR_INVALID_ARG;
   Ctl ctl;
   if (current_ctl(&ctl) != cudaSuccess) return DSV_ERR_CUDA;
+  widen_wait(&ctl, p);
   const int group = p.H / p.Hkv;
   CUtensorMap tq, tk, tv;
   if (make_map_view(&tq, Q, p.H, p.Tq, p.d, group, 128 / group) != cudaSuccess) return DSV_ERR_CUDA;
@@ -723,6 +731,7 @@ dsv_status dsv_packed_attn_bwd(dsv_view Q, dsv_view K, dsv_view V, dsv_view O, d
   if (need > 0 && (!workspace || !al256(workspace) || workspace_bytes < need)) return DSV_ERR_INVALID_ARG;
   Ctl ctl;
   if (current_ctl(&ctl) != cudaSuccess) return DSV_ERR_CUDA;
+  widen_wait(&ctl, p);
   const int group = p.H / p.Hkv;
   PackedMaps m;
   if (!nq && (make_map_view(&m.Q, Q, p.H, p.Tq, p.d, group, 128 / group) != cudaSuccess ||

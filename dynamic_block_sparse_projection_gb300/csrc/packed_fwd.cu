@@ -203,8 +203,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           k_to = found ? min(q.lk, k_from + part_keys) : 0;
           it.part = idx;
           // what the combine kernel has to know of a tile, at its first part; nothing at the others
+          // (nor of a tile whose parts do not fit, which takes overlapping sequences: bad pointers)
           if (lane == 0)
-            tiles[idx] = found && part.part == 0
+            tiles[idx] = found && part.part == 0 && idx - it.kvh * head_items + part.parts <= head_items
                              ? make_int4(part.parts, q.q0 + tile * g.TQ, min(g.TQ, q.lq - tile * g.TQ), it.kvh)
                              : make_int4(0, 0, 0, 0);
         }

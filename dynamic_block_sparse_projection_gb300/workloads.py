@@ -147,6 +147,17 @@ def posemb_3d(T: int, Hl: int, Wl: int, d: int, device="cpu") -> torch.Tensor:
     return pe.to(torch.float32)
 
 
+def grid_positions(T: int, Hl: int, Wl: int, device="cpu") -> torch.Tensor:
+    """The (t, y, x) coordinates of every token in raster order, int32 [T*Hl*Wl, 3]."""
+    n = torch.arange(T * Hl * Wl, device=device)
+    return torch.stack([n // (Hl * Wl), (n // Wl) % Hl, n % Wl], 1).to(torch.int32).contiguous()
+
+
+def axis_bands(d: int) -> Tuple[int, int, int]:
+    """Channels of each axis' band, as posemb_3d cuts them."""
+    return (2 * (d // 6),) * 3
+
+
 @dataclass
 class Inputs:
     w: Workload

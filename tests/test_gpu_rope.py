@@ -205,3 +205,79 @@ def test_rope_on_a_stream_and_in_a_graph(dsv):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, ref) and torch.equal(dx, dxr) and torch.equal(dw, dwr)
+
+
+def test_sparse_path_on_normalised_and_rotated_queries(dsv):
+    """The benchmark's step with norm and rotation: Q and K as the oracle's,
+    the sparse path on them, and dQ, dK and the weights' gradients back through
+    rotation and norm."""
+    import bench
+    from dynamic_block_sparse_projection_gb300 import workloads as wl
+    from parity_util import O_REL_L2, SMALL, rel_l2
+    w = SMALL["latent16k_small"]
+    x = wl.make_inputs(w, device="cuda")
+    hp = bench.HotPath(dsv, x, w, x.k_per_head, fused=True, rope="norm")
+    hp.run()
+    torch.cuda.synchronize()
+    assert dsv.device_error()[0] == 0
+    O, _, dQ, dK, dV, dwq, dwk = hp.results()
+    pos, bands, one = wl.grid_positions(w.T, w.Hl, w.Wl).numpy(), wl.axis_bands(w.d), np.ones(w.d)
+    for src, got in ((x.Q, hp.xr.Q), (x.K, hp.xr.K)):
+        ref = oracle.rope_axes(to64(src), pos, bands, weight=one)
+        _close(got, ref, _pair_size(ref), "rotated")
+    fp, fc = (t.cpu().numpy() for t in hp.lists[:2])
+    Q, K, V, dO = (to64(t) for t in (hp.xr.Q, hp.xr.K, x.V, x.dO))
+    O_ref, _ = oracle.attn_fwd_groups(Q, K, V, fp, fc, w.block)
+    gQ, gK, gV = oracle.attn_bwd_groups(Q, K, V, dO, fp, fc, w.block)
+    assert rel_l2(to64(O), O_ref) <= O_REL_L2
+    # The attention's gradients, element by element: P and dS are rounded to
+    # bf16 (u = 2^-8 each), the fp32 part is e = 2^-12 of P, and D = dO . O takes
+    # the error of the bf16 O, which dS carries as P * tol(D).  Where the softmax
+    # is peaked, dP - D cancels and that is the largest term (3 % of dQ here in
+    # norm, which a bound in norm alone would not separate from a slip).
+    u, e, scale = 2.0 ** -8, 2.0 ** -12, w.d ** -0.5
+    tq, tk, tv = u * np.abs(gQ), u * np.abs(gK), u * np.abs(gV)
+    for h in range(w.H):
+        mask = np.zeros((w.nb, w.nb), bool)
+        for g in range(w.nb):
+            mask[g, fc[fp[h * w.nb + g]:fp[h * w.nb + g + 1]]] = True
+        mask = np.repeat(np.repeat(mask, w.block, 0), w.block, 1)
+        q, k, v, do = (t[0, h] for t in (Q, K, V, dO))
+        P = np.where(mask, scale * (q @ k.T), -np.inf)
+        P = np.exp(P - P.max(-1, keepdims=True))
+        P /= P.sum(-1, keepdims=True)
+        tO = (u + e) * (P @ np.abs(v)) + u * np.abs(O_ref[0, h])
+        dP = do @ v.T
+        dS = P * (dP - np.sum(P * dP, -1, keepdims=True))
+        tS = (u + 2 * e) * np.abs(dS) + P * (np.sum(np.abs(do) * tO, -1, keepdims=True) + e * (np.abs(do) @ np.abs(v).T))
+        tv[0, h] += (u + 2 * e) * (P.T @ np.abs(do))
+        tq[0, h] += scale * (tS @ np.abs(k))
+        tk[0, h] += scale * (tS.T @ np.abs(q))
+    assert np.all(np.abs(to64(dV) - gV) <= tv)
+    # through the rotation (a pair's error at most sqrt(2) larger) and the norm's Jacobian, absolute values throughout
+    for got, dw, src, g, t in ((dQ, dwq, x.Q, gQ, tq), (dK, dwk, x.K, gK, tk)):
+        s64 = to64(src)
+        ref, dwr = oracle.rope_axes_bwd(g, pos, bands, x=s64, weight=one)
+        r = 1 / np.sqrt((s64 ** 2).mean(-1, keepdims=True) + 1e-6)
+        xh, tr = s64 * r, _pair_size(t)
+        tol = r * (tr + np.abs(xh) * np.mean(tr * np.abs(xh), -1, keepdims=True))
+        gr = _pair_size(oracle.rope_axes_bwd(g, pos, bands))
+        tol += 2.0 ** -20 * r * (gr + np.abs(xh) * np.mean(gr * np.abs(xh), -1, keepdims=True)) + u * np.abs(ref)
+        assert np.all(np.abs(to64(got) - ref) <= tol), np.max(np.abs(to64(got) - ref) / tol)
+        assert np.all(np.abs(to64(dw) - dwr) <= np.sum((tr + 2.0 ** -10 * gr) * np.abs(xh), axis=(0, 1, 2)))
+
+
+def test_rope_launched_on_a_stream_that_is_not_current(dsv):
+    """Results and workspace are allocated for the stream of the launch."""
+    x, dy, pos = _rand(8, 1, 4, 300, 64), _rand(9, 1, 4, 300, 64), _grid_pos(3, 10, 10)
+    w = torch.full((64,), 1.5, device="cuda")
+    ref = (dsv.rope_axes(x, pos, (16, 24, 24), weight=w), *dsv.rope_axes_bwd(dy, pos, (16, 24, 24), x=x, weight=w))
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    for _ in range(5):
+        y = dsv.rope_axes(x, pos, (16, 24, 24), weight=w, stream=st)
+        dx, dw = dsv.rope_axes_bwd(dy, pos, (16, 24, 24), x=x, weight=w, stream=st)
+        junk = [torch.full((1 << 20,), 3.0, device="cuda") for _ in range(3)]       # the current stream's allocations
+        st.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((y, dx, dw), ref))
+        del junk
