@@ -130,7 +130,7 @@ struct PKVTraits {
   // of 2650 where Q and dO come from HBM.
   static constexpr int NQ = 3, ND = 2;
   static constexpr int VEC_BYTES = 128 * 4;                    // -lse2 or D of a query tile
-  static constexpr int NBAR = 1 + 2 * NQ + 3 * ND + 7 + 2;
+  static constexpr int NBAR = 2 + 2 * NQ + 3 * ND + 7 + 2;
   static constexpr int SMEM_USED = (2 + NQ + ND) * TILE + 2 * ND * VEC_BYTES + NBAR * 8 + 16;
   static_assert(SMEM_USED <= 227 * 1024, "dK/dV tiles exceed shared memory");
   static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
@@ -204,8 +204,9 @@ __global__ void __launch_bounds__(kKVThreads, 1)
   uint8_t* sdO = sQ + NQ * T::TILE;               // [ND]
   uint8_t* sVec = sdO + ND * T::TILE;             // [ND] -lse2 | D
   uint64_t* bars = reinterpret_cast<uint64_t*>(sVec + 2 * ND * T::VEC_BYTES);
-  uint64_t* kv_full = bars;
-  uint64_t* q_full = bars + 1;
+  uint64_t* kt_full = bars;                       // the key tile, and V's
+  uint64_t* vt_full = bars + 1;
+  uint64_t* q_full = bars + 2;
   uint64_t* q_empty = q_full + NQ;                // dK of the slot's tile is done (also frees its vectors)
   uint64_t* d_full = q_empty + NQ;
   uint64_t* d_empty = d_full + ND;                // dV of the slot's tile is done
@@ -237,7 +238,8 @@ __global__ void __launch_bounds__(kKVThreads, 1)
 
   const int box = g.group * g.TQ;                 // rows a query tile's copy brings
   if (threadIdx.x == 0) {
-    mbar_init(kv_full, 1);
+    mbar_init(kt_full, 1);
+    mbar_init(vt_full, 1);
     for (int s = 0; s < NQ; ++s) {
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], 1);
@@ -259,6 +261,66 @@ __global__ void __launch_bounds__(kKVThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
+  // rows of the last tile, when the box reaches past the sequence's end
+  const int last_rows = min(g.TQ, q.lq - (i0 + cnt - 1) * g.TQ) * g.group;
+  const bool cut = last_rows < box;
+  const uint32_t tx = (uint32_t)box * D * 2;
+  auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int n) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar, tx);
+      for (int c = 0; c < T::NCH; ++c)
+        tma_load_3d(dst + c * T::CHUNK, map, bar, c * 64, kvh * g.group, q.q0 + (i0 + n) * g.TQ);
+    }
+  };
+  auto load_q = [&](int n) {
+    load(&tmQ, sQ + (n % NQ) * T::TILE, cut && n == cnt - 1 ? q_tail : &q_full[n % NQ], n);
+  };
+  auto load_do = [&](int n) {
+    load(&tmdO, sdO + (n % ND) * T::TILE, cut && n == cnt - 1 ? d_tail : &d_full[n % ND], n);
+  };
+  auto load_vec = [&](int n) {
+    if (lane == 0) {
+      const long long vec = ((long long)kvh * g.nslot_q + qslot0 + n) * 128;
+      uint8_t* dst = sVec + (n % ND) * 2 * T::VEC_BYTES;
+      mbar_arrive_expect_tx(&v_full[n % ND], 2 * T::VEC_BYTES);
+      bulk_load(dst, L2w + vec, T::VEC_BYTES, &v_full[n % ND]);
+      bulk_load(dst + T::VEC_BYTES, Dw + vec, T::VEC_BYTES, &v_full[n % ND]);
+    }
+  };
+  int nd = min(cnt, ND), nq = min(cnt, NQ);        // tiles whose dO and vectors, Q are under way
+  if (warp == 0) {
+    // the first copies, before the tensor memory is there: K and Q first, which S^T(0) needs
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive_expect_tx(kt_full, T::TILE);
+      for (int c = 0; c < T::NCH; ++c) tma_load_3d(sK + c * T::CHUNK, &tmK, kt_full, c * 64, kvh, (int)krow0);
+    }
+    load_q(0);
+    if (lane == 0) {
+      mbar_arrive_expect_tx(vt_full, T::TILE);
+      for (int c = 0; c < T::NCH; ++c) tma_load_3d(sV + c * T::CHUNK, &tmV, vt_full, c * 64, kvh, (int)krow0);
+    }
+    load_do(0);
+    load_vec(0);
+    for (int n = 1; n < nq; ++n) {
+      load_q(n);
+      if (n < nd) {
+        load_do(n);
+        load_vec(n);
+      }
+    }
+  }
+  // every copy warp 0 started must land before the CTA exits
+  auto drain = [&]() {
+    mbar_wait(kt_full, 0, nullptr, ctl, kid | W_DRAIN);
+    mbar_wait(vt_full, 0, nullptr, ctl, kid | W_DRAIN);
+    for (int n = max(0, nq - NQ); n < nq; ++n)
+      if (!(cut && n == cnt - 1)) mbar_wait(&q_full[n % NQ], (uint32_t)(n / NQ) & 1u, nullptr, ctl, kid | W_DRAIN);
+    for (int n = max(0, nd - ND); n < nd; ++n) {
+      if (!(cut && n == cnt - 1)) mbar_wait(&d_full[n % ND], (uint32_t)(n / ND) & 1u, nullptr, ctl, kid | W_DRAIN);
+      mbar_wait(&v_full[n % ND], (uint32_t)(n / ND) & 1u, nullptr, ctl, kid | W_DRAIN);
+    }
+  };
   // rows box..127 of every query tile are never loaded (sQ and sdO are adjacent)
   if (box < 128 && warp >= 2 && warp < 2 + NQ + ND) zero_tile_rows(sQ + (warp - 2) * T::TILE, T::NCH, box, lane);
   if (warp == 1) {
@@ -274,53 +336,13 @@ __global__ void __launch_bounds__(kKVThreads, 1)
 
   if (tmem_base != tmem) {
     if (threadIdx.x == 0) set_error(ctl, DSV_ERR_INTERNAL, blockIdx.x);
+    if (warp == 0) {
+      if (cut && nq == cnt) mbar_wait(q_tail, 0, nullptr, ctl, kid | W_DRAIN);
+      if (cut && nd == cnt) mbar_wait(d_tail, 0, nullptr, ctl, kid | W_DRAIN);
+      drain();
+    }
   } else if (warp == 0) {
-    // ---------------- TMA producer ----------------
-    if (lane == 0) {
-      tma_prefetch_desc(&tmQ);
-      tma_prefetch_desc(&tmK);
-      tma_prefetch_desc(&tmV);
-      tma_prefetch_desc(&tmdO);
-      mbar_arrive_expect_tx(kv_full, 2 * T::TILE);
-      for (int c = 0; c < T::NCH; ++c) {
-        tma_load_3d(sK + c * T::CHUNK, &tmK, kv_full, c * 64, kvh, (int)krow0);
-        tma_load_3d(sV + c * T::CHUNK, &tmV, kv_full, c * 64, kvh, (int)krow0);
-      }
-    }
-    // rows of the last tile, when the box reaches past the sequence's end
-    const int last_rows = min(g.TQ, q.lq - (i0 + cnt - 1) * g.TQ) * g.group;
-    const bool cut = last_rows < box;
-    const uint32_t tx = (uint32_t)box * D * 2;
-    auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int n) {
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar, tx);
-        for (int c = 0; c < T::NCH; ++c)
-          tma_load_3d(dst + c * T::CHUNK, map, bar, c * 64, kvh * g.group, q.q0 + (i0 + n) * g.TQ);
-      }
-    };
-    auto load_q = [&](int n) {
-      load(&tmQ, sQ + (n % NQ) * T::TILE, cut && n == cnt - 1 ? q_tail : &q_full[n % NQ], n);
-    };
-    auto load_do = [&](int n) {
-      load(&tmdO, sdO + (n % ND) * T::TILE, cut && n == cnt - 1 ? d_tail : &d_full[n % ND], n);
-    };
-    auto load_vec = [&](int n) {
-      if (lane == 0) {
-        const long long vec = ((long long)kvh * g.nslot_q + qslot0 + n) * 128;
-        uint8_t* dst = sVec + (n % ND) * 2 * T::VEC_BYTES;
-        mbar_arrive_expect_tx(&v_full[n % ND], 2 * T::VEC_BYTES);
-        bulk_load(dst, L2w + vec, T::VEC_BYTES, &v_full[n % ND]);
-        bulk_load(dst + T::VEC_BYTES, Dw + vec, T::VEC_BYTES, &v_full[n % ND]);
-      }
-    };
-    for (int n = 0; n < min(cnt, NQ); ++n) {
-      load_q(n);
-      if (n < ND) {
-        load_do(n);
-        load_vec(n);
-      }
-    }
-    int nd = min(cnt, ND), nq = min(cnt, NQ);      // tiles whose dO and vectors, Q are under way
+    // ---------------- TMA producer: the tiles after the first ----------------
     for (int n = 0; n + ND < cnt; ++n) {
       if (!mbar_wait_warp(&d_empty[n % ND], (uint32_t)(n / ND) & 1u, abort_flag, ctl, kid | W_GEMPTY)) break;
       load_do(n + ND);
@@ -350,14 +372,7 @@ __global__ void __launch_bounds__(kKVThreads, 1)
       if (nq == cnt) mbar_wait(q_tail, 0, nullptr, ctl, kid | W_DRAIN);
       if (nd == cnt) mbar_wait(d_tail, 0, nullptr, ctl, kid | W_DRAIN);
     }
-    // every copy this warp started must land before the CTA exits
-    mbar_wait(kv_full, 0, nullptr, ctl, kid | W_DRAIN);
-    for (int n = max(0, nq - NQ); n < nq; ++n)
-      if (!(cut && n == cnt - 1)) mbar_wait(&q_full[n % NQ], (uint32_t)(n / NQ) & 1u, nullptr, ctl, kid | W_DRAIN);
-    for (int n = max(0, nd - ND); n < nd; ++n) {
-      if (!(cut && n == cnt - 1)) mbar_wait(&d_full[n % ND], (uint32_t)(n / ND) & 1u, nullptr, ctl, kid | W_DRAIN);
-      mbar_wait(&v_full[n % ND], (uint32_t)(n / ND) & 1u, nullptr, ctl, kid | W_DRAIN);
-    }
+    drain();
   } else if (warp == 1) {
     // ---------------- MMA issuer (whole warp, one elected lane issues) ----------------
     // Order, as in attn_bwd.cu: S^T(0), dP^T(0), then per query tile n
@@ -400,13 +415,14 @@ __global__ void __launch_bounds__(kKVThreads, 1)
       }
       return r;
     };
-    bool ok = mbar_wait_warp(kv_full, 0, abort_flag, ctl, kid | W_KV) &&
+    bool ok = mbar_wait_warp(kt_full, 0, abort_flag, ctl, kid | W_KV) &&
               mbar_wait_warp(&q_full[0], 0, abort_flag, ctl, kid | W_GFULL);
     uint32_t tp0 = 0u;
     if (ok) {
       tc_fence_after();
       issue_sdp(0, 0, nullptr, 0u);
-      ok = mbar_wait_warp(&d_full[0], 0, abort_flag, ctl, kid | W_GFULL);
+      ok = mbar_wait_warp(vt_full, 0, abort_flag, ctl, kid | W_KV) &&
+           mbar_wait_warp(&d_full[0], 0, abort_flag, ctl, kid | W_GFULL);
       if (ok) {
         tc_fence_after();
         tp0 = issue_sdp(0, 1, &p_full[0], 0u);
