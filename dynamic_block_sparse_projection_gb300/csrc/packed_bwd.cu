@@ -640,12 +640,15 @@ struct PQTraits {
   static constexpr int NCH = D / 64;
   static constexpr int CHUNK = 128 * 128;
   static constexpr int TILE = NCH * CHUNK;
-  // K_j is read by S (early) and by dQ (late); V_j only by dP: separate rings
-  static constexpr int NK = 3;
-  static constexpr int NV = (8 * TILE + 2048 <= 227 * 1024) ? 3 : 2;
-  static constexpr int NBAR = 1 + 2 * NK + 2 * NV + 8 + 4 + 2 + 1;   // even: the answer after it is 16-byte aligned
-  static_assert(NBAR % 2 == 0, "alignment of the work request's answer");
-  static constexpr int SMEM_USED = 1024 + 2 * TILE + (NK + NV) * TILE + NBAR * 8 + 16 + 16 + 2 * (int)sizeof(QItem) + 1024;
+  // K_j is read by S (early) and by dQ (late); V_j only by dP: separate rings.
+  // Q and dO twice where there is room.  (At d = 128 the room would have to
+  // come from the rings: two K, one V and Q, dO twice took 161 us instead of
+  // 149 even where an item has two to four key tiles, the text case.)
+  static constexpr int NQD = D == 64 ? 2 : 1, NK = 3, NV = D == 64 ? 3 : 2;
+  static constexpr int BARS = 3 * NQD + 2 * NK + 2 * NV + 7 + 4 + 2;
+  static constexpr int NBAR = (BARS + 1) / 2 * 2;   // even: the answer after it is 16-byte aligned
+  static constexpr int SMEM_USED = (2 * NQD + NK + NV) * TILE + NBAR * 8 + 16 + 16 + 2 * (int)sizeof(QItem) +
+                                   1024 * NQD;
   static_assert(SMEM_USED <= 227 * 1024, "dQ tiles exceed shared memory");
   static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
   static constexpr uint32_t S_COL = 0, DP_COL = 128, DQ_COL = 256, DS_COL = 256 + D, TMEM_COLS = 512;
@@ -662,17 +665,25 @@ __global__ void __launch_bounds__(kQThreads, 1)
                         const float* __restrict__ Dw, float scale, __nv_bfloat16* dQ, long long dq_head,
                         long long dq_tok, int wide, Ctl ctl) {
   using T = PQTraits<D>;
-  constexpr int NK = T::NK, NV = T::NV;
+  constexpr int NK = T::NK, NV = T::NV, NQD = T::NQD;
   constexpr int HALF = T::HALF;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* sbase = smem_align1024(smem_raw);
-  uint8_t* sdO = sbase;
-  uint8_t* sQ = sdO + T::TILE;
-  uint8_t* sK = sQ + T::TILE;
+  // the tiles take all but ~800 bytes, so the base itself has to be aligned
+  // (the array is declared so; a launch that broke it is reported)
+  if ((smem_u32(smem_raw) & 1023u) != 0u) {
+    if (threadIdx.x == 0) set_error(ctl, DSV_ERR_INTERNAL, blockIdx.x);
+    cudaGridDependencySynchronize();
+    return;
+  }
+  uint8_t* sdO = smem_raw;                        // [NQD]
+  uint8_t* sQ = sdO + NQD * T::TILE;              // [NQD]
+  uint8_t* sK = sQ + NQD * T::TILE;
   uint8_t* sV = sK + NK * T::TILE;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sV + NV * T::TILE);
-  uint64_t* qd_full = bars;                       // Q and dO landed in smem
-  uint64_t* k_full = bars + 1;
+  uint64_t* qd_full = bars;                       // [NQD] Q, dO and the rows' vectors landed in smem
+  uint64_t* qd_free = qd_full + NQD;              // [NQD] the item's last dP product is done
+  uint64_t* vec_free = qd_free + NQD;             // [NQD] the compute warps have read the rows' vectors
+  uint64_t* k_full = vec_free + NQD;
   uint64_t* k_empty = k_full + NK;
   uint64_t* v_full = k_empty + NK;
   uint64_t* v_empty = v_full + NV;
@@ -682,15 +693,14 @@ __global__ void __launch_bounds__(kQThreads, 1)
   uint64_t* ds_empty = ds_full + 1;
   uint64_t* acc_done = ds_empty + 1;              // dQ of the current tile is complete
   uint64_t* mma_drain = acc_done + 1;
-  uint64_t* qd_free = mma_drain + 1;              // the current tile's last dP product is done
-  uint64_t* k_tail = qd_free + 1;                 // the last K tile of a sequence, before its rows are cut
+  uint64_t* k_tail = mma_drain + 1;                // the last K tile of a sequence, before its rows are cut
   uint64_t* item_full = k_tail + 1;               // [2]
   uint64_t* item_free = item_full + 2;            // [2]
   uint64_t* near_end = item_free + 2;             // the K producer is about to finish its item
   uint64_t* clc_full = near_end + 1;              // the work request's answer is there
   void* clc = bars + T::NBAR;                     // 16 bytes
-  float* sVec = reinterpret_cast<float*>(bars + T::NBAR + 2);   // -lse2 of the tile's rows, then D
-  QItem* items = reinterpret_cast<QItem*>(sVec + 256);
+  float* sVec = reinterpret_cast<float*>(bars + T::NBAR + 2);   // [NQD] -lse2 of the tile's rows, then D
+  QItem* items = reinterpret_cast<QItem*>(sVec + 256 * NQD);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(items + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -699,7 +709,11 @@ __global__ void __launch_bounds__(kQThreads, 1)
   const uint32_t q_bytes = (uint32_t)(g.group * g.TQ) * D * 2;
 
   if (threadIdx.x == 0) {
-    mbar_init(qd_full, 1);
+    for (int s = 0; s < NQD; ++s) {
+      mbar_init(&qd_full[s], 1);
+      mbar_init(&qd_free[s], 1);
+      mbar_init(&vec_free[s], 8);
+    }
     for (int s = 0; s < NK; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
@@ -714,7 +728,6 @@ __global__ void __launch_bounds__(kQThreads, 1)
     mbar_init(ds_empty, 1);
     mbar_init(acc_done, 1);
     mbar_init(mma_drain, 1);
-    mbar_init(qd_free, 1);
     mbar_init(k_tail, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&item_full[s], 1);
@@ -832,31 +845,30 @@ __global__ void __launch_bounds__(kQThreads, 1)
       tma_prefetch_desc(&tmQ);
     }
     uint32_t gq = 0, tails = 0;
-    int qd_issued = 0;
+    uint32_t qd_issued = 0;
     bool ok = true;
     QItem it;
     for (uint32_t i = 0; ok && take(i, it); ++i) {
       for (int n = 0; n < it.nt; ++n) {
-        // the first K tile goes ahead of Q and dO, whose buffers are free only
-        // when the previous item's last S and dP products are done
-        if (n == min(1, it.nt - 1)) {
-          // (and the rows' vectors free once the compute warps hold the last tile)
-          const uint32_t last = gq - (uint32_t)n - 1;
-          if (qd_issued > 0 &&
-              (!mbar_wait_warp(qd_free, (uint32_t)(qd_issued - 1) & 1u, abort_flag, ctl, kid | W_KVEMPTY) ||
-               !mbar_wait_warp(sp_free, last & 1u, abort_flag, ctl, kid | W_SPFREE))) {
+        // With one buffer for them the first K tile goes ahead of Q and dO, whose
+        // place is free only when the item before is through with it.
+        if (n == min(NQD == 1 ? 1 : 0, it.nt - 1)) {
+          const int b = (int)(i % NQD);
+          const uint32_t before = i / NQD - 1;     // the use of this buffer before this one
+          if (i >= NQD && (!mbar_wait_warp(&qd_free[b], before & 1u, abort_flag, ctl, kid | W_KVEMPTY) ||
+                           !mbar_wait_warp(&vec_free[b], before & 1u, abort_flag, ctl, kid | W_SPFREE))) {
             ok = false;
             break;
           }
           if (lane == 0) {
             const long long vec = ((long long)it.kvh * g.nslot_q + it.slot) * 128;
-            mbar_arrive_expect_tx(qd_full, 2 * q_bytes + 1024);
-            bulk_load(sVec, L2w + vec, 512, qd_full);
-            bulk_load(sVec + 128, Dw + vec, 512, qd_full);
-            for (int c = 0; c < T::NCH; ++c) {
-              tma_load_3d(sdO + c * T::CHUNK, &tmdO, qd_full, c * 64, it.kvh * g.group, it.tok);
-              tma_load_3d(sQ + c * T::CHUNK, &tmQ, qd_full, c * 64, it.kvh * g.group, it.tok);
-            }
+            mbar_arrive_expect_tx(&qd_full[b], 2 * q_bytes + 1024);
+            for (int c = 0; c < T::NCH; ++c)
+              tma_load_3d(sQ + b * T::TILE + c * T::CHUNK, &tmQ, &qd_full[b], c * 64, it.kvh * g.group, it.tok);
+            for (int c = 0; c < T::NCH; ++c)
+              tma_load_3d(sdO + b * T::TILE + c * T::CHUNK, &tmdO, &qd_full[b], c * 64, it.kvh * g.group, it.tok);
+            bulk_load(sVec + b * 256, L2w + vec, 512, &qd_full[b]);
+            bulk_load(sVec + b * 256 + 128, Dw + vec, 512, &qd_full[b]);
           }
           ++qd_issued;
         }
@@ -889,7 +901,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
       }
     }
     // every copy this warp started must land before the CTA exits
-    if (qd_issued > 0) mbar_wait(qd_full, (uint32_t)(qd_issued - 1) & 1u, nullptr, ctl, kid | W_DRAIN);
+    for (uint32_t n = (qd_issued > NQD ? qd_issued - NQD : 0u); n < qd_issued; ++n)
+      mbar_wait(&qd_full[n % NQD], (n / NQD) & 1u, nullptr, ctl, kid | W_DRAIN);
     for (uint32_t n = (gq > NK ? gq - NK : 0u); n < gq; ++n)
       mbar_wait(&k_full[n % NK], (n / NK) & 1u, nullptr, ctl, kid | W_DRAIN);
   } else if (warp == 1) {
@@ -909,7 +922,9 @@ __global__ void __launch_bounds__(kQThreads, 1)
     bool ok = true;
     QItem it;
     for (uint32_t i = 0; ok && take(i, it); ++i) {
-      if (!mbar_wait_warp(qd_full, i & 1u, abort_flag, ctl, kid | W_KV)) break;
+      const uint32_t qb = i % NQD;
+      if (!mbar_wait_warp(&qd_full[qb], (i / NQD) & 1u, abort_flag, ctl, kid | W_KV)) break;
+      const uint64_t dq = desc_off(dQ0, qb * T::TILE), ddo = desc_off(ddO0, qb * T::TILE);
       int n = -1;
       for (; n < it.nt; ++n) {
         const uint32_t gn = gq + (uint32_t)n;
@@ -931,7 +946,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t o = (kk >> 2) * T::CHUNK + (kk & 3) * 32;
-            mma_ss_w(tmem + T::S_COL, desc_off(dQ0, o), desc_off(kb, o), ID_S, kk > 0 ? 1u : 0u);
+            mma_ss_w(tmem + T::S_COL, desc_off(dq, o), desc_off(kb, o), ID_S, kk > 0 ? 1u : 0u);
           }
           td = mbar_test(ds_full, gn & 1u);
           if (!mbar_wait_warp_tested(&v_full[sv], phv, tv, abort_flag, ctl, kid | W_VFULL)) {
@@ -943,11 +958,11 @@ __global__ void __launch_bounds__(kQThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t o = (kk >> 2) * T::CHUNK + (kk & 3) * 32;
-            mma_ss_w(tmem + T::DP_COL, desc_off(ddO0, o), desc_off(vb, o), ID_S, kk > 0 ? 1u : 0u);
+            mma_ss_w(tmem + T::DP_COL, desc_off(ddo, o), desc_off(vb, o), ID_S, kk > 0 ? 1u : 0u);
           }
           mma_commit_w(s_full);
           mma_commit_w(&v_empty[sv]);                     // V_j is only needed by dP
-          if (n + 2 == it.nt) mma_commit_w(qd_free);      // the item's last read of Q and dO
+          if (n + 2 == it.nt) mma_commit_w(&qd_free[qb]);      // the item's last read of Q and dO
         }
         if (n < 0) continue;
         // ds_full of an item's first tile also means that the previous item's dQ has been read
@@ -988,9 +1003,12 @@ __global__ void __launch_bounds__(kQThreads, 1)
       const bool row_ok = rt < it.ntok;
       __nv_bfloat16* out = dQ + (long long)(it.kvh * g.group + rh) * dq_head + ((long long)it.tok + rt) * dq_tok +
                            hf * (D / 2);
-      if (!mbar_wait_warp(qd_full, i & 1u, abort_flag, ctl, kid | W_KV)) break;
-      const float nlse2 = sVec[r];                 // -lse*log2(e); -inf for a row without keys
-      const float dd = sVec[128 + r];
+      const uint32_t qb = i % NQD;
+      if (!mbar_wait_warp(&qd_full[qb], (i / NQD) & 1u, abort_flag, ctl, kid | W_KV)) break;
+      const float nlse2 = sVec[qb * 256 + r];      // -lse*log2(e); -inf for a row without keys
+      const float dd = sVec[qb * 256 + 128 + r];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&vec_free[qb]);
       const int lim_r = g.causal ? min(it.left, it.lim0 + rt) : it.left;   // keys that the row sees
 
       uint32_t s_tested = 0u;
