@@ -112,33 +112,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
-// One bounded step of a wait for either of several things: gives `bar` up to
-// `hint_ns` to complete its phase; true when it has.  t0 (0 at first) carries
-// the start of the wait: past the time limit, or when *abort is raised, `ok`
-// becomes false (with DSV_ERR_TIMEOUT and *abort as in mbar_wait).  Warp-wide.
-__device__ __forceinline__ bool mbar_step_warp(uint64_t* bar, uint32_t parity, uint32_t hint_ns, uint64_t& t0,
-                                               volatile int* abort, const Ctl& ctl, unsigned int where, bool& ok) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
-      : "memory");
-  if (__all_sync(0xffffffffu, done != 0u)) return true;
-  const uint64_t now = globaltimer();
-  if (t0 == 0) t0 = now;
-  bool late = now - t0 > ctl.wait_limit_ns;
-  late = __any_sync(0xffffffffu, late);
-  if (late) {
-    set_error(ctl, DSV_ERR_TIMEOUT, where);
-    *abort = 1;
-  }
-  if (__any_sync(0xffffffffu, late || *abort)) ok = false;
-  return false;
-}
-
 // Warp-uniform variant: every lane of the warp waits and the result is the
 // AND over the warp, so that .sync.aligned instructions after it are reached
 // by all lanes or by none.

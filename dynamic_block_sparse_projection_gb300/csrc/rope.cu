@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_bwd_kernel(RopeView dy, 
                                                                 int tiles, int chunks) {
   constexpr int LPR = D / 8, TOK = kRopeThreads / LPR;
   constexpr int BATCH = NORM ? 2 : 4;    // rows of both inputs in flight
+  if (NORM) cudaTriggerProgrammaticLaunchCompletion();   // rope_dw_kernel may come to wait
   __shared__ RopeTable tab;
   __shared__ float red[TOK][D + 8];
   if (threadIdx.x < D / 2) {
@@ -259,6 +260,7 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__
   __shared__ float red[128][8];
   const int c = blockIdx.x * 8 + threadIdx.x, y = threadIdx.y;
   float s = 0.f;
+  cudaGridDependencySynchronize();
 #pragma unroll 5
   for (int p = y; p < parts; p += 128) s += part[(long long)p * d + c];
   red[y][threadIdx.x] = s;
@@ -325,8 +327,16 @@ cudaError_t bwd_t(const RopeView& dy, const RopeView& x, const RopeOut& dx, Rope
                                                                      chunks);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  rope_dw_kernel<<<D / 8, dim3(8, 128), 0, st>>>(part, parts, D, dw);
-  return cudaGetLastError();
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(D / 8);
+  cfg.blockDim = dim3(8, 128);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rope_dw_kernel, static_cast<const float*>(part), parts, D, dw);
 }
 
 RopeView view(const dsv_view& v) {

@@ -406,7 +406,9 @@ dsv_status dsv_rope_axes_bwd(dsv_view dy, dsv_view x, const int32_t* pos, int64_
  * A query that sees no key gets O = 0, lse = -inf and a zero gradient; a key
  * that no query sees gets zero gradients.  Tokens outside [ptr[0], ptr[S])
  * are neither read into any result nor written.  A non-finite value of a
- * sequence reaches no other sequence.
+ * sequence reaches no other sequence; inside its own it may reach results that
+ * its pairs are masked from, as 0 * NaN does in the products above (a row of V
+ * or dO; the scores themselves are masked by selection).
  *
  * Q, O, dO, dQ   views of [H, Tq, d];  K, V, dK, dV  views of [Hkv, Tk, d]
  *           (batch_stride is not read).  No output overlaps an input or
