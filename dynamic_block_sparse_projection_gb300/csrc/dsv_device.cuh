@@ -521,6 +521,7 @@ enum : unsigned int {
   KID_PACKED_FWD = 6,
   KID_PACKED_KV = 7,
   KID_PACKED_Q = 8,
+  KID_PACKED_ROWS = 9,
 };
 
 }  // namespace dsv

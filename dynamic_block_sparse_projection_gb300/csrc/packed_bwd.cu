@@ -10,6 +10,8 @@
 //   prepare  D_i and -lse_i log2(e) into 128-row slots, one per query tile.  A
 //            row that saw no key (lse = -inf), and a row behind the tile's
 //            tokens, gets -inf there, so its P is exp2(-inf) = 0.
+//   rows     D_i = sum_j P_ij dP_ij instead, for the query tiles whose keys all
+//            lie in one key tile (below).
 //   kv       one CTA per key tile and key head, over the sequence's query
 //            tiles: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.
 //            Shared heads add up inside the product, and every output tile has
@@ -20,6 +22,12 @@
 //            CTAs as it goes (packed_fwd.cu): S = Q K^T, dP = dO V^T, dQ += dS K.
 // S and dP are computed twice (seven products per tile pair instead of five),
 // which buys results that do not depend on the order CTAs run in.
+//
+// D_i from O.  O is bf16, so dO . O is off by some 2^-9 |dO| |O| / sqrt(d).  Over
+// many keys O is small against the v_j and that vanishes beside the rounding
+// of dS to bf16 (the tensor core's operand); over a handful of keys it does not:
+// in sequences of 1 to 20 keys dQ and dK were off by up to twice what their own
+// rounding to bf16 costs, with the rows kernel by 1.4 times, as everywhere else.
 //
 // Rows of a tile that belong to no token of it are other sequences' data.  As
 // rows of the A operands they only reach accumulator rows that are not stored;
@@ -41,6 +49,13 @@ constexpr int kQItemWarp = 11;         // q kernel: takes the work items
 constexpr int kQThreads = 384;
 constexpr int kAskAhead = 6;           // q kernel: key tiles before an item's last one at which the next is asked for
 constexpr int kComputeThreads = 256;
+constexpr int kRowsThreads = 160;      // rows kernel: 4 compute warps, one for copies and MMAs
+
+// Whether the keys that a query tile sees (from token t0 of its sequence on) lie in one key tile.
+__device__ __forceinline__ bool one_key_tile(const PackedGeom& g, const PackedSeq& q, int t0) {
+  const int last = g.causal ? min(q.lk, q.lk - q.lq + t0 + min(g.TQ, q.lq - t0)) : q.lk;
+  return last > 0 && last <= 128;
+}
 
 // ---------------------------------------------------------------------------
 // D_i and -lse_i log2(e), 128 rows per query tile
@@ -57,10 +72,14 @@ __global__ void __launch_bounds__(256) packed_bwd_prep_kernel(const __grid_const
   const int slot = blockIdx.x, kvh = blockIdx.y;
   if (slot == 0 && kvh == 0 && threadIdx.x < 32) packed_check_ptrs(g, ctl, threadIdx.x);
   PackedSeq q;
-  if (!packed_find(g, g.q_ptr, g.TQ, slot, q)) return;
-  const int t0 = (slot - (q.q0 / g.TQ + q.s)) * g.TQ;
-  if (t0 >= q.lq) return;
+  const bool found = packed_find(g, g.q_ptr, g.TQ, slot, q);
+  const int t0 = found ? (slot - (q.q0 / g.TQ + q.s)) * g.TQ : 0;
+  if (!found || t0 >= q.lq) {
+    cudaGridDependencySynchronize();
+    return;
+  }
   const int rows = min(g.TQ, q.lq - t0) * g.group;
+  const bool from_o = !one_key_tile(g, q, t0);   // else D is the rows kernel's
   const int c = threadIdx.x % TPR;
   const long long base = ((long long)kvh * g.nslot_q + slot) * 128;
   constexpr int BATCH = 4;               // rows of O and dO in flight per thread
@@ -74,8 +93,10 @@ __global__ void __launch_bounds__(256) packed_bwd_prep_kernel(const __grid_const
       a[k] = b[k] = make_uint4(0, 0, 0, 0);
       L[k] = -INFINITY;
       if (r < rows) {
-        a[k] = __ldcs(reinterpret_cast<const uint4*>(O + head * o_head + tok * o_tok) + c);
-        b[k] = __ldcs(reinterpret_cast<const uint4*>(dO + head * d_head + tok * d_tok) + c);
+        if (from_o) {
+          a[k] = __ldcs(reinterpret_cast<const uint4*>(O + head * o_head + tok * o_tok) + c);
+          b[k] = __ldcs(reinterpret_cast<const uint4*>(dO + head * d_head + tok * d_tok) + c);
+        }
         if (c == 0) L[k] = lse[(long long)head * g.Tq + tok];
       }
     }
@@ -91,11 +112,12 @@ __global__ void __launch_bounds__(256) packed_bwd_prep_kernel(const __grid_const
 #pragma unroll
       for (int o = TPR / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
       if (c == 0) {
-        Dw[base + r0 + k * RPC] = acc;           // 0 behind the tile's rows
+        if (from_o) Dw[base + r0 + k * RPC] = acc;           // 0 behind the tile's rows
         L2w[base + r0 + k * RPC] = L[k] == -INFINITY ? -INFINITY : -L[k] * kLog2e;
       }
     }
   }
+  cudaGridDependencySynchronize();       // what waits for this kernel waits for the rows kernel too
 }
 
 // 32 bf16 values of a row, a sector at a time where the rows' addresses allow it.
@@ -112,8 +134,183 @@ __device__ __forceinline__ void store_row32(__nv_bfloat16* dst, const uint32_t* 
 
 enum : unsigned int {
   W_KV = 1, W_GFULL, W_GEMPTY, W_S, W_P, W_ACC, W_DRAIN, W_KFULL, W_VFULL, W_KVEMPTY, W_SPFREE, W_DSFULL, W_DSEMPTY,
-  W_ITEM, W_ITEMFREE, W_TAIL
+  W_ITEM, W_ITEMFREE, W_TAIL, W_KVFULL
 };
+
+// ---------------------------------------------------------------------------
+// D_i = sum_j P_ij dP_ij where a query tile's keys lie in one key tile
+// ---------------------------------------------------------------------------
+// One CTA per SM looks 128 slots at a time over for such tiles and takes them
+// one after the other: S = Q K^T and dP = dO V^T, a row per thread.  Runs beside
+// the prepare kernel, which leaves these tiles' D alone.  Rows of Q and dO that
+// are no token of the tile reach only rows that are not kept; keys past a row's
+// limit are left out by selection.
+template <int D>
+struct PRowsTraits {
+  static constexpr int NCH = D / 64;
+  static constexpr int CHUNK = 128 * 128;
+  static constexpr int TILE = NCH * CHUNK;
+  static constexpr int SMEM_USED = 1024 + 4 * TILE + 5 * 8 + 4 * 4 + 8;
+  // at least 120 KB so that one CTA owns an SM (and its 512 TMEM columns)
+  static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
+  static constexpr uint32_t TMEM_COLS = 512;      // two buffers of S and dP
+};
+
+template <int D>
+__global__ void __launch_bounds__(kRowsThreads, 1)
+    packed_bwd_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                           const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
+                           const __grid_constant__ PackedGeom g, const float* __restrict__ lse, float scale,
+                           float* __restrict__ Dw, Ctl ctl) {
+  using T = PRowsTraits<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  cudaTriggerProgrammaticLaunchCompletion();     // the prepare kernel may run beside this one
+  uint8_t* sQ = smem_align1024(smem_raw);
+  uint8_t* sdO = sQ + T::TILE;
+  uint8_t* sK = sdO + T::TILE;
+  uint8_t* sV = sK + T::TILE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sV + T::TILE);   // the tiles landed
+  uint64_t* acc_full = full + 1;                  // [2] S and dP in TMEM (and the tiles read)
+  uint64_t* acc_free = full + 3;                  // [2]
+  uint32_t* hits = reinterpret_cast<uint32_t*>(full + 5);       // [4] which of 128 slots
+  uint32_t* tmem_slot = hits + 4;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned int kid = (unsigned int)KID_PACKED_ROWS << 8;
+  const int total = g.Hkv * g.nslot_q;
+  const float c2 = scale * kLog2e;
+  bool ready = false, ok = true;                  // ready: the same in all threads
+  uint32_t n = 0;                                 // tiles taken
+  uint32_t tmem_base = 0;
+  constexpr uint32_t tmem = 0;
+  auto tile_of = [&](int idx, int& kvh, int& slot, PackedSeq& q, int& t0) -> bool {
+    kvh = idx / g.nslot_q;
+    slot = idx - kvh * g.nslot_q;
+    if (!packed_find(g, g.q_ptr, g.TQ, slot, q)) return false;
+    t0 = (slot - (q.q0 / g.TQ + q.s)) * g.TQ;
+    return t0 < q.lq && one_key_tile(g, q, t0);
+  };
+
+  for (long long base = blockIdx.x; base < total; base += 128LL * gridDim.x) {
+    auto index = [&](int bit) { return base + (long long)bit * gridDim.x; };
+    if (warp < 4) {
+      int kvh, slot, t0;
+      PackedSeq q;
+      const long long idx = index(threadIdx.x);
+      const uint32_t hit = __ballot_sync(0xffffffffu, idx < total && tile_of((int)idx, kvh, slot, q, t0));
+      if (lane == 0) hits[warp] = hit;
+    }
+    __syncthreads();
+    if ((hits[0] | hits[1] | hits[2] | hits[3]) != 0u && !ready) {
+      if (threadIdx.x == 0) {
+        mbar_init(full, 1);
+        for (int b = 0; b < 2; ++b) {
+          mbar_init(&acc_full[b], 1);
+          mbar_init(&acc_free[b], 128);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+      }
+      if (warp == 4) {
+        tmem_alloc(tmem_slot, T::TMEM_COLS);
+        tmem_relinquish();
+      }
+      tc_fence_before();
+      __syncthreads();
+      tc_fence_after();
+      // one CTA owns the SM's whole TMEM, so its addresses start at 0 (attn_fwd.cu)
+      tmem_base = *tmem_slot;
+      ready = true;
+      if (tmem_base != tmem) {
+        if (threadIdx.x == 0) set_error(ctl, DSV_ERR_INTERNAL, blockIdx.x);
+        ok = false;
+      }
+    }
+#pragma unroll 1
+    for (int w = 0; w < 4; ++w) {
+#pragma unroll 1
+      for (uint32_t left = hits[w]; ok && left != 0u; left &= left - 1u, ++n) {
+        int kvh, slot, t0;
+        PackedSeq q;
+        tile_of((int)index(w * 32 + __ffs(left) - 1), kvh, slot, q, t0);
+        const uint32_t b = n & 1u, use = n >> 1;
+        if (warp == 4) {
+          // the tiles are free when the MMAs before are done
+          if (n > 0 && !mbar_wait_warp(&acc_full[b ^ 1u], ((n - 1) >> 1) & 1u, nullptr, ctl, kid | W_KVEMPTY)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            const uint32_t box = (uint32_t)(g.group * g.TQ) * D * 2;
+            mbar_arrive_expect_tx(full, 2 * box + 2 * T::TILE);
+            for (int c = 0; c < T::NCH; ++c) {
+              tma_load_3d(sQ + c * T::CHUNK, &tmQ, full, c * 64, kvh * g.group, q.q0 + t0);
+              tma_load_3d(sK + c * T::CHUNK, &tmK, full, c * 64, kvh, q.k0);
+              tma_load_3d(sdO + c * T::CHUNK, &tmdO, full, c * 64, kvh * g.group, q.q0 + t0);
+              tma_load_3d(sV + c * T::CHUNK, &tmV, full, c * 64, kvh, q.k0);
+            }
+          }
+          // (its own copies: waited for whatever happens)
+          const bool landed = mbar_wait_warp(full, n & 1u, nullptr, ctl, kid | W_KVFULL);
+          if (!landed || !mbar_wait_warp(&acc_free[b], (use & 1u) ^ 1u, abort_flag, ctl, kid | W_SPFREE)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          constexpr uint32_t ID_S = idesc_bf16_f32(128, 128, false, false);
+          const uint64_t dq = sdesc_sw128(smem_u32(sQ), 16, 1024), dk = sdesc_sw128(smem_u32(sK), 16, 1024);
+          const uint64_t ddo = sdesc_sw128(smem_u32(sdO), 16, 1024), dv = sdesc_sw128(smem_u32(sV), 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * T::CHUNK + (kk & 3) * 32;
+            mma_ss_w(tmem + b * 256, desc_off(dq, o), desc_off(dk, o), ID_S, kk > 0 ? 1u : 0u);
+            mma_ss_w(tmem + b * 256 + 128, desc_off(ddo, o), desc_off(dv, o), ID_S, kk > 0 ? 1u : 0u);
+          }
+          mma_commit_w(&acc_full[b]);
+        } else {
+          const int r = warp * 32 + lane, rt = r / g.group;
+          const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+          const int ntok = min(g.TQ, q.lq - t0);
+          const int head = kvh * g.group + (r - rt * g.group);
+          const float L = rt < ntok ? lse[(long long)head * g.Tq + q.q0 + t0 + rt] : -INFINITY;
+          const float nl = L == -INFINITY ? -INFINITY : -L * kLog2e;
+          const int lim = g.causal ? min(q.lk, q.lk - q.lq + t0 + 1 + rt) : q.lk;
+          if (!mbar_wait_warp(&acc_full[b], use & 1u, abort_flag, ctl, kid | W_S)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t xs[32], xp[32];
+            tmem_ld32(tmem + lane_off + b * 256 + c * 32, xs);
+            tmem_ld32(tmem + lane_off + b * 256 + 128 + c * 32, xp);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c * 32 + j < lim)
+                sum[j & 3] = fmaf(ex2(fmaf(__uint_as_float(xs[j]), c2, nl)), __uint_as_float(xp[j]), sum[j & 3]);
+          }
+          tc_fence_before();
+          mbar_arrive(&acc_free[b]);
+          // a row without keys, and a row behind the tile's tokens: 0
+          Dw[((long long)kvh * g.nslot_q + slot) * 128 + r] =
+              rt < ntok && L != -INFINITY ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.f;
+        }
+      }
+    }
+    __syncthreads();                              // `hits` has been read
+  }
+  if (!ready) return;
+  if (warp == 4 && n > 0) mbar_wait_warp(&acc_full[(n - 1) & 1u], ((n - 1) >> 1) & 1u, nullptr, ctl, kid | W_DRAIN);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 4) tmem_dealloc(tmem_base, T::TMEM_COLS);
+}
 
 // ---------------------------------------------------------------------------
 // dK, dV: one CTA per key tile and key head
@@ -1093,11 +1290,31 @@ cudaError_t launch_t(const PackedMaps& m, const PackedGeom& g, const dsv_view& O
   const size_t vec = (size_t)g.Hkv * g.nslot_q * 128;
   float* Dw = static_cast<float*>(ws);
   float* L2w = Dw + vec;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = g.Tk > 0 ? 1 : 0;
   if (g.Tq > 0) {
-    packed_bwd_prep_kernel<D><<<dim3((unsigned)g.nslot_q, (unsigned)g.Hkv), 256, 0, st>>>(
-        g, static_cast<const __nv_bfloat16*>(O.ptr), O.head_stride, O.token_stride,
-        static_cast<const __nv_bfloat16*>(dO.ptr), dO.head_stride, dO.token_stride, lse, Dw, L2w, ctl);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (g.Tk > 0) {
+      auto rows = packed_bwd_rows_kernel<D>;
+      constexpr int smem = PRowsTraits<D>::SMEM;
+      if ((e = cudaFuncSetAttribute(rows, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+      const long long slots = (long long)g.Hkv * g.nslot_q;
+      rows<<<(unsigned)(slots < kPackedSMs ? slots : kPackedSMs), kRowsThreads, smem, st>>>(m.Q, m.K, m.V, m.dO, g, lse,
+                                                                                            scale, Dw, ctl);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    // beside the rows kernel; it ends no earlier (its last lines)
+    cfg.gridDim = dim3((unsigned)g.nslot_q, (unsigned)g.Hkv);
+    cfg.blockDim = dim3(256);
+    if ((e = cudaLaunchKernelEx(&cfg, packed_bwd_prep_kernel<D>, g, static_cast<const __nv_bfloat16*>(O.ptr),
+                                (long long)O.head_stride, (long long)O.token_stride,
+                                static_cast<const __nv_bfloat16*>(dO.ptr), (long long)dO.head_stride,
+                                (long long)dO.token_stride, lse, Dw, L2w, ctl)) != cudaSuccess)
+      return e;
   }
   if (g.Tk > 0) {
     auto kv = packed_bwd_kv_kernel<D>;
@@ -1119,16 +1336,9 @@ cudaError_t launch_t(const PackedMaps& m, const PackedGeom& g, const dsv_view& O
   // The q kernel needs what the prepare kernel wrote, not what the kv kernel
   // does: its CTAs start as the kv kernel's last ones leave SMs free, and it
   // ends no earlier than the kv kernel (packed_bwd_q_kernel's last lines).
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((long long)g.Hkv * g.nslot_q));
   cfg.blockDim = dim3(kQThreads);
   cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = &early;
-  cfg.numAttrs = g.Tk > 0 ? 1 : 0;
   if ((e = cudaLaunchKernelEx(&cfg, qk, m.Q, m.K, m.V, m.dO, g, static_cast<const float*>(L2w),
                               static_cast<const float*>(Dw), scale, static_cast<__nv_bfloat16*>(dQ.ptr),
                               (long long)dQ.head_stride, (long long)dQ.token_stride, wide_rows(dQ), ctl)) !=

@@ -8,6 +8,8 @@ exponential are good to that, relative to P):
        (u + e) sum_j P |v| + u |O|
   lse  e + 2^-20 |lse|
   D    dO . O with the bf16 O:            sum_c |dO| tol(O)
+       (where a tile of queries sees at most 128 keys, sum_j P dP in fp32:
+       2e sum_j P |dO| |v|; only `_bounds(exact_d=True)` counts on it)
   dV   (u + 2e) sum_i P |dO| + u |dV|
   dS   (u + 2e) |dS| + P (tol(D) + e sum_c |dO v|)
   dQ   scale sum_j tol(dS) |k| + u |dQ|;  dK likewise with q."""
@@ -70,7 +72,7 @@ class Case:
         return tuple(to64(t) for t in (self.Q, self.K, self.V, self.dO))
 
 
-def _bounds(Q, K, V, dO, qp, kp, causal, scale):
+def _bounds(Q, K, V, dO, qp, kp, causal, scale, exact_d=False):
     """Reference values and tolerances of every output."""
     scale = scale or 1 / np.sqrt(Q.shape[-1])
     O, lse = oracle.packed_attn_fwd(Q, K, V, qp, kp, causal, scale)
@@ -93,6 +95,9 @@ def _bounds(Q, K, V, dO, qp, kp, causal, scale):
             g, v, k, q = dO[h, qs], V[j, ks], K[j, ks], Q[h, qs]
             tO[h, qs] += (U + E) * (P @ np.abs(v))
             tD = np.sum(np.abs(g) * tO[h, qs], -1, keepdims=True)
+            if exact_d:
+                assert lk <= 128
+                tD = 2 * E * np.sum(P * (np.abs(g) @ np.abs(v).T), -1, keepdims=True)
             dP = g @ v.T
             dS = P * (dP - np.sum(P * dP, -1, keepdims=True))
             tS = (U + 2 * E) * np.abs(dS) + P * (tD + E * (np.abs(g) @ np.abs(v).T))
@@ -219,6 +224,21 @@ def test_packed_scores_that_grow_along_the_keys(dsv, kl):
     assert np.max(np.abs(to64(lse) - lref)) <= 2.0 ** -7
     assert np.max(np.abs(to64(O) - ref)) <= (2 * U + 2.0 ** -7) * np.max(np.abs(to64(c.V)))
     assert dsv.device_error()[0] == 0
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(2, 2, 128), (3, 1, 64), (5, 1, 128)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_packed_gradient_over_a_handful_of_keys(dsv, H, Hkv, d, causal):
+    """Few keys: O is as large as V, and D from the bf16 O would be too coarse
+    beside dS (0 for a row that sees one key)."""
+    for ql, kl in (((1, 2, 3, 300, 7, 20, 500), (1, 2, 3, 1, 0, 20, 128)), ((40, 9) * 40, (3, 11) * 40)):
+        c = Case(H, Hkv, d, ql, kl, pad=5)
+        O, lse = c.fwd(dsv, causal)
+        Q, K, V, dO = c.np()
+        b = _bounds(Q, K, V, dO, c.qp, c.kp, causal, 0.0, exact_d=True)
+        rq, rk = slice(c.qp[0], c.qp[-1]), slice(c.kp[0], c.kp[-1])
+        for got, ref, rows, what in zip(c.bwd(dsv, O, lse, causal), b[2:], (rq, rk, rk), ("dQ", "dK", "dV")):
+            _near(got, ref, rows, what)
 
 
 def test_packed_not_a_number_stays_in_its_sequence(dsv):
