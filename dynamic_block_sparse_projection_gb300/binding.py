@@ -11,6 +11,8 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import math
 from pathlib import Path
 from typing import Optional, Sequence, Tuple
@@ -18,6 +20,7 @@ from typing import Optional, Sequence, Tuple
 import torch
 
 _LIB_PATH = Path(__file__).resolve().parent / "_build" / "libdsv.so"
+_CALLS_PATH = _LIB_PATH.with_name("dsv_calls.so")
 
 DSV_OK, DSV_ERR_INVALID_ARG, DSV_ERR_UNSUPPORTED, DSV_ERR_CUDA, DSV_ERR_BAD_INDEX, DSV_ERR_TIMEOUT, DSV_ERR_INTERNAL = range(7)
 
@@ -131,25 +134,28 @@ def _load() -> ctypes.CDLL:
     lib.dsv_dispatch_heads.restype = ctypes.c_int
     lib.dsv_selftest_wait_timeout.argtypes = [vp]
     lib.dsv_selftest_wait_timeout.restype = ctypes.c_int
-    f32, i64 = ctypes.c_float, ctypes.c_int64
-    lib.dsv_rope_axes_fwd.argtypes = [View, vp, i64, Rope, vp, f32, View, vp]
-    lib.dsv_rope_axes_fwd.restype = ctypes.c_int
     lib.dsv_rope_axes_bwd_workspace_bytes.argtypes = [Rope]
     lib.dsv_rope_axes_bwd_workspace_bytes.restype = sz
-    lib.dsv_rope_axes_bwd.argtypes = [View, View, vp, i64, Rope, vp, f32, View, vp, vp, sz, vp]
-    lib.dsv_rope_axes_bwd.restype = ctypes.c_int
     lib.dsv_packed_attn_fwd_workspace_bytes.argtypes = [Packed]
     lib.dsv_packed_attn_fwd_workspace_bytes.restype = sz
-    lib.dsv_packed_attn_fwd.argtypes = [View, View, View, Packed, vp, vp, i32, f32, View, vp, vp, sz, vp]
-    lib.dsv_packed_attn_fwd.restype = ctypes.c_int
     lib.dsv_packed_attn_bwd_workspace_bytes.argtypes = [Packed]
     lib.dsv_packed_attn_bwd_workspace_bytes.restype = sz
-    lib.dsv_packed_attn_bwd.argtypes = [View, View, View, View, View, vp, Packed, vp, vp, i32, f32, View, View, View,
-                                        vp, sz, vp]
-    lib.dsv_packed_attn_bwd.restype = ctypes.c_int
     lib.dsv_version.argtypes = []
     lib.dsv_version.restype = i32
+    # the calls with several structures, by C (pycalls.c): the same arguments
+    calls = _load_calls()
+    for name in ("dsv_rope_axes_fwd", "dsv_rope_axes_bwd", "dsv_packed_attn_fwd", "dsv_packed_attn_bwd"):
+        setattr(lib, name, getattr(calls, name))
     return lib
+
+
+def _load_calls():
+    if not _CALLS_PATH.exists():
+        raise ImportError(f"dsv_calls.so is not built ({_CALLS_PATH}); run __graft_entry__.build() first")
+    loader = importlib.machinery.ExtensionFileLoader("dsv_calls", str(_CALLS_PATH))
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("dsv_calls", loader))
+    loader.exec_module(module)
+    return module
 
 
 lib = _load()

@@ -1,8 +1,9 @@
 """Build libdsv.so (the C-ABI library) for sm_103a with nvcc, in-tree.
 
 One nvcc process per translation unit, run in parallel, then one link step.
-Output: dynamic_block_sparse_projection_gb300/_build/libdsv.so.  Rebuilds only
-when a source or header is newer than the library.
+Output: dynamic_block_sparse_projection_gb300/_build/libdsv.so, and beside it the
+CPython module dsv_calls.so, linked against it.  Rebuilds only when a source or
+header is newer than the outputs.
 """
 from __future__ import annotations
 
@@ -10,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
@@ -19,6 +21,7 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 OUT = PKG / "_build"
 LIB = OUT / "libdsv.so"
+CALLS = OUT / "dsv_calls.so"
 SOURCES = ["dsv_api.cu", "predict.cu", "topk.cu", "attn_fwd.cu", "attn_bwd.cu", "topk_noalloc.cu", "cube.cu",
            "predict_max.cu", "predict_topk.cu", "packed_fwd.cu", "packed_bwd.cu", "rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -32,13 +35,13 @@ def _nvcc() -> str:
 
 
 def _inputs():
-    return [CSRC / s for s in SOURCES] + list(CSRC.glob("*.cuh")) + list(CSRC.glob("*.h")) + list(INCLUDE.glob("*.h"))
+    return [CSRC / s for s in SOURCES + ["pycalls.c"]] + list(CSRC.glob("*.cuh")) + list(CSRC.glob("*.h")) + list(INCLUDE.glob("*.h"))
 
 
 def up_to_date() -> bool:
-    if not LIB.exists():
+    if not LIB.exists() or not CALLS.exists():
         return False
-    t = LIB.stat().st_mtime
+    t = min(LIB.stat().st_mtime, CALLS.stat().st_mtime)
     return all(p.stat().st_mtime <= t for p in _inputs())
 
 
@@ -71,6 +74,14 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = False)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
     os.replace(tmp, LIB)
+    tmp = OUT / "dsv_calls.so.tmp"
+    cmd = [shutil.which("gcc") or "cc", "-shared", "-fPIC", "-O2", "-I", str(INCLUDE), "-I",
+           sysconfig.get_paths()["include"], str(CSRC / "pycalls.c"), "-o", str(tmp), "-L", str(OUT), "-ldsv",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("building dsv_calls.so failed:\n" + r.stdout + r.stderr)
+    os.replace(tmp, CALLS)
     return LIB
 
 
