@@ -225,8 +225,9 @@ def _need_rows(t: torch.Tensor, name: str, device: Optional[torch.device] = None
 
 def _need_rows_on(device: torch.device, index: int, **tensors) -> None:
     """_need_rows for each tensor (None: left out); index: the device's, as get_device() gives it."""
+    bf16 = torch.bfloat16
     for name, t in tensors.items():
-        if t is not None and (t.dtype is not torch.bfloat16 or t.get_device() != index or t.stride(-1) != 1):
+        if t is not None and (t.dtype is not bf16 or t.get_device() != index or t.stride(-1) != 1):
             _need_rows(t, name, device)
 
 
@@ -241,9 +242,10 @@ def _dims(t, name: str, n: int) -> Tuple[int, ...]:
     """The shape of t, which must be an n-dimensional tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != n:
-        raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
-    return tuple(t.shape)
+    shape = tuple(t.shape)
+    if len(shape) != n:
+        raise ValueError(f"{name} must have {n} dimensions, got shape {shape}")
+    return shape
 
 
 def _shape(t, name: str, shape) -> None:
@@ -676,7 +678,10 @@ def _view(t: Optional[torch.Tensor]) -> View:
     """dsv_view of a [.., heads, tokens, d] tensor of 3 or 4 dimensions."""
     if t is None:
         return View(None, 0, 0, 0)
-    return View(t.data_ptr(), *(t.stride()[:3] if t.dim() == 4 else (0, *t.stride()[:2])))
+    st = t.stride()
+    if len(st) == 4:
+        return View(t.data_ptr(), st[0], st[1], st[2])
+    return View(t.data_ptr(), 0, st[0], st[1])
 
 
 @functools.lru_cache(maxsize=64)
