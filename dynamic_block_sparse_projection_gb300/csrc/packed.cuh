@@ -128,6 +128,7 @@ __device__ __forceinline__ PackedPart packed_part(const PackedGeom& g, int part_
 // Both row pointers must rise within [0, T]: one warp reports the first
 // sequence that breaks it (its tiles are skipped by packed_find).
 __device__ __forceinline__ void packed_check_ptrs(const PackedGeom& g, const Ctl& ctl, int lane) {
+#pragma unroll 4
   for (int s = lane; s < g.S; s += 32) {
     const int a = g.q_ptr[s], b = g.q_ptr[s + 1], c = g.k_ptr[s], d = g.k_ptr[s + 1];
     if (a < 0 || b < a || b > g.Tq || c < 0 || d < c || d > g.Tk) set_error(ctl, DSV_ERR_BAD_INDEX, (unsigned)s);

@@ -418,12 +418,15 @@ dsv_status dsv_rope_axes_bwd(dsv_view dy, dsv_view x, const int32_t* pos, int64_
  *           pointers break this is skipped and DSV_ERR_BAD_INDEX recorded in
  *           the device error word, with the sequence as its info.
  * causal    0 or 1.  softmax_scale <= 0 selects 1/sqrt(d).
- * lse       fp32 [H, Tq] contiguous; the backward reads the forward's O and lse.
+ * lse       fp32 [H, Tq] contiguous; the backward reads the forward's O and lse
+ *           (those of the same keys: D_i is dO_i . O_i, or the equal sum of
+ *           P_ij dO_i . v_j where the keys of a run of queries fit one tile).
  * workspace >= the matching _workspace_bytes(p) bytes, 256-byte aligned (may
  *           be NULL where that is 0).  Forward: where query tiles are fewer
  *           than the SMs, the keys of a tile are split over several CTAs and
- *           their fp32 parts joined in order.  Backward: D_i = dO_i . O_i and
- *           -lse_i log2(e).
+ *           their fp32 parts joined in order.  Backward: D_i and
+ *           -lse_i log2(e), and the fp32 parts of dK and dV where key tiles are
+ *           fewer than the SMs.
  * d in {64, 128}; H <= 1024, a multiple of Hkv; H / Hkv <= 128;
  * Tq + 128 S and Tk + 128 S < 2^31.  Outputs are bit-identical from run to run
  * (one writer per output tile, no atomics).  The waits inside the kernels run

@@ -204,3 +204,19 @@ def test_binding_refuses_what_is_not_a_row_view(dsv):
         dsv._need_rows(cpu.float(), "x")
     with pytest.raises(TypeError):
         dsv._need_rows([1.0], "x")
+
+
+def test_c_entries_check_their_arguments(dsv):
+    """The C module's functions take ctypes' place: wrong counts, structures and values raise, nothing is called."""
+    v, p = dsv.View(FAKE, 0, 64, 64), dsv.Packed(0, 0, 0, 0, 0, 64)
+    good = [v, v, v, p, FAKE, FAKE, 0, 0.0, v, FAKE, None, 0, None]
+    assert dsv.lib.dsv_packed_attn_fwd(*good) == dsv.DSV_OK             # no sequences: nothing to do
+    with pytest.raises(TypeError, match="arguments"):
+        dsv.lib.dsv_packed_attn_fwd(*good[:-1])
+    for at, bad, err in ((0, p, TypeError), (3, v, TypeError), (0, 5, TypeError), (6, 1 << 40, OverflowError),
+                         (7, "1", TypeError), (11, -1, OverflowError), (4, "x", TypeError)):
+        with pytest.raises(err):
+            dsv.lib.dsv_packed_attn_fwd(*good[:at], bad, *good[at + 1:])
+    for name, n in (("dsv_packed_attn_bwd", 17), ("dsv_rope_axes_fwd", 8), ("dsv_rope_axes_bwd", 12)):
+        with pytest.raises(TypeError, match=f"expected {n} arguments"):
+            getattr(dsv.lib, name)()
