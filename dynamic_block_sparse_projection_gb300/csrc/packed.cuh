@@ -125,6 +125,14 @@ __device__ __forceinline__ PackedPart packed_part(const PackedGeom& g, int part_
   }
   return {0, -1, 0};
 }
+// The items of a key head that lie before sequence s's, by one warp.
+__device__ __forceinline__ int packed_items_before(const PackedGeom& g, int part_keys, int s, int lane) {
+  int n = 0, parts;
+  for (int i = lane; i < s; i += 32) n += packed_items(g, part_keys, i, parts);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n;
+}
 // Both row pointers must rise within [0, T]: one warp reports the first
 // sequence that breaks it (its tiles are skipped by packed_find).
 __device__ __forceinline__ void packed_check_ptrs(const PackedGeom& g, const Ctl& ctl, int lane) {

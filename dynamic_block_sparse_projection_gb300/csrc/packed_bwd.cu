@@ -1356,19 +1356,48 @@ cudaError_t launch_t(const PackedMaps& m, const PackedGeom& g, const dsv_view& O
 }  // namespace
 
 // Runs of query tiles per key tile in the kv kernel.  With at least one key
-// tile per SM each CTA takes all query tiles of its own.  With fewer (few keys
-// against many queries: text), they are cut into runs of at least
-// kPackedMinPart tiles, enough to fill the SMs once, whose fp32 sums the join
-// kernel adds (text case, 144 key tiles: 360 us a call; 370 with runs for two
-// rounds, 375 for three, 435 without).
+// tile per SM each CTA takes all query tiles of its own.  With fewer they may be
+// cut into `n` runs of at least kPackedMinPart tiles, whose fp32 sums the join
+// kernel adds.  The q kernel's CTAs fill the SMs that the kv kernel leaves free,
+// so what counts is when both are done: worked out below for n that fill half
+// an SM's rounds, in microseconds at d = 128 (a pair of tiles 1.4 and 1.0, a
+// CTA's start 5 and 4, the join 4 and 0.033 for each run's 131 KB), the lengths, which the host does not know,
+// taken half-way between equal ones and a single long one.  Measured with and
+// without runs: 24 heads of two clips against 226 and 512 keys 344 / 315 us, 2
+// heads of one clip of 4000 83 / 57 us, but one head of 20 000 against 300 keys
+// 41 / 225 us, three heads over one of three clips up to 5095 72 / 156 us.
 static int bwd_splits(const dsv_packed& p) {
   if (p.S <= 0 || p.Tq <= 0 || p.Tk <= 0) return 1;
-  const long long k_tiles = (p.Tk + 127) / 128, TQ = 128 / (p.H / p.Hkv);
+  const long long TQ = 128 / (p.H / p.Hkv);
+  const long long k_tiles = (p.Tk + 127) / 128, q_tiles = (p.Tq + TQ - 1) / TQ;
   const long long ctas = (long long)p.Hkv * (k_tiles > p.S ? k_tiles : p.S);
   if (ctas >= kPackedSMs) return 1;
-  const long long q_tiles = (p.Tq + TQ * p.S - 1) / (TQ * p.S);      // of a sequence, on average
-  const long long n = (kPackedSMs + ctas - 1) / ctas, most = (q_tiles + kPackedMinPart - 1) / kPackedMinPart;
-  return (int)(n < most ? n : most);
+  const long long items = (long long)p.Hkv * (q_tiles > p.S ? q_tiles : p.S);
+  const double part = 0.5 * (1.0 + 1.0 / p.S);
+  const double q = q_tiles * part < 1 ? 1 : q_tiles * part, k = k_tiles * part < 1 ? 1 : k_tiles * part;
+  const double item_us = k * 1.0 + 4;
+  const long long most = (long long)ceil(q / kPackedMinPart);
+  double best = 0;
+  long long splits = 1, last = 0;
+  for (long long half = 0; half <= 8; ++half) {
+    long long n = half == 0 ? 1 : half * kPackedSMs / 2 / ctas;
+    if (n > most) n = most;
+    if (n <= last) continue;
+    last = n;
+    const double run_us = ceil(q / n) * 1.4 + 5;
+    const long long rounds = ctas * n / kPackedSMs, rest = ctas * n % kPackedSMs, open = kPackedSMs - rest;
+    // items per SM that is free after the full rounds; the others come `late` items later
+    const long long late = (long long)ceil(run_us / item_us);
+    long long each = (items + open - 1) / open;
+    if (each > late) each = (items + rest * late + kPackedSMs - 1) / kPackedSMs;
+    const double kv_us = (rounds + (rest > 0)) * run_us, q_us = rounds * run_us + each * item_us;
+    const double us = (kv_us > q_us ? kv_us : q_us) + (n > 1 ? 4 + 0.033 * (ctas * n) : 0);
+    if (half == 0 || us < best) {
+      best = us;
+      splits = n;
+    }
+  }
+  return (int)splits;
 }
 
 size_t packed_bwd_ws_bytes(const dsv_packed& p) {

@@ -34,8 +34,9 @@
 // threads: the warpgroups split the CTA's registers 88 : 256 : 160.
 //
 // Split over the keys.  Each part writes its normalised O (fp32) and base-2
-// log-sum to the workspace and combine_kernel joins them in part order:
-// results do not depend on which part finished first.
+// log-sum to the workspace and packed_combine_kernel joins them in an order of
+// its own: results do not depend on which part finished first.  A tile with one
+// part writes its result at once.
 #include <math.h>
 
 #include <type_traits>
@@ -58,7 +59,7 @@ struct FwdItem {
   int lim0;    // keys of this part that the first token sees (may be <= 0, may exceed the part)
   int left;    // keys of the sequence from key0 on
   int part;    // where a split item's part of O goes
-  int pad;
+  int parts;   // parts of its tile: one alone is the result
 };
 
 template <int D>
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PackedGeom g, int part_keys,
                       int part_rows, int head_items, float scale_log2, __nv_bfloat16* O, long long o_head, long long o_tok,
-                      float* LSE, float* Opart, float* Lpart, int4* tiles, int wide, Ctl ctl) {
+                      float* LSE, float* Opart, float* Lpart, int wide, Ctl ctl) {
   using T = PFwdTraits<D>;
   constexpr int NST = T::NST;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -202,12 +203,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           k_from = part.part * part_keys;
           k_to = found ? min(q.lk, k_from + part_keys) : 0;
           it.part = idx;
-          // what the combine kernel has to know of a tile, at its first part; nothing at the others
-          // (nor of a tile whose parts do not fit, which takes overlapping sequences: bad pointers)
-          if (lane == 0)
-            tiles[idx] = found && part.part == 0 && idx - it.kvh * head_items + part.parts <= head_items
-                             ? make_int4(part.parts, q.q0 + tile * g.TQ, min(g.TQ, q.lq - tile * g.TQ), it.kvh)
-                             : make_int4(0, 0, 0, 0);
+          it.parts = part.parts;
+          // (parts that do not fit take overlapping sequences: bad pointers)
+          found = found && idx - it.kvh * head_items - part.part + part.parts <= head_items;
         }
         const int t0 = tile * g.TQ;
         if (found && t0 < q.lq) {
@@ -225,7 +223,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (it.valid && it.nt == 0) {
           // no key for any of its rows: written here, so that an item in the ring always has tiles
           for (int r = lane; r < it.ntok * g.group; r += 32) {
-            if (part_keys > 0) {
+            if (it.parts > 1) {
               Lpart[(long long)it.part * part_rows + r] = -INFINITY;
               continue;
             }
@@ -579,7 +577,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const long long tok = (long long)it.tok + rt;
       const long long prow = (long long)it.part * part_rows + r;
       __nv_bfloat16* dst = O + head * o_head + tok * o_tok;
-      float* ls = part_keys > 0 ? Lpart + prow : LSE + (long long)head * g.Tq + tok;
+      float* ls = it.parts > 1 ? Lpart + prow : LSE + (long long)head * g.Tq + tok;
       if (!mbar_wait_warp(stat_full, (uint32_t)ne & 1u, abort_flag, ctl, kid | W_STAT) ||
           !mbar_wait_warp(o_final, (uint32_t)ne & 1u, abort_flag, ctl, kid | W_OFINAL))
         break;
@@ -595,7 +593,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (row_ok) {
 #pragma unroll
         for (int j = 0; j < D; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * st.x);
-        if (part_keys > 0) {
+        if (it.parts > 1) {
 #pragma unroll
           for (int q = 0; q < D / 8; ++q) st_global_32(Opart + prow * D + q * 8, o + q * 8);
           *ls = st.y;
@@ -626,61 +624,100 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
 // Joins the parts of a tile: with L_p the base-2 log-sums, M = max L_p and
 // w_p = 2^(L_p - M):  O = sum w_p O_p / sum w_p,  lse = (M + log2 sum w_p) ln 2.
-// One warp per row; each lane weighs a part, then all add the parts up in
-// order, sixteen loads of O in flight.  A part that saw nothing of the row
-// wrote no O: its weight is 0 and its values are left out.  CTAs go over the
-// items of the forward grid (a tile is described at its first part) and, along
-// y, over the rows of a tile.
+// A part that saw nothing of the row wrote no O: its weight is 0 and its values
+// are left out.  One CTA per query slot and key head (along x) and run of rows
+// (along y); `wpr` warps share a row, each adding up every wpr-th part, and the
+// first adds their sums in order.  Latency-bound: what a CTA has to know of its
+// tile it works out before it waits for the parts, and few enough registers
+// that all CTAs of a call are there at once (one wave of 147 registers took 25
+// us where the parts themselves took 20).
 template <int D>
-__global__ void __launch_bounds__(256) packed_combine_kernel(int H, int Hkv, int Tq, int part_rows,
-                                                             const int4* __restrict__ tiles,
-                                                             const float* __restrict__ Opart,
-                                                             const float* __restrict__ Lpart, __nv_bfloat16* O,
-                                                             long long o_head, long long o_tok, float* LSE) {
+__global__ void __launch_bounds__(256, 4)
+    packed_combine_kernel(const __grid_constant__ PackedGeom g, int part_keys, int head_items, int part_rows, int wpr,
+                          const float* __restrict__ Opart, const float* __restrict__ Lpart, __nv_bfloat16* O,
+                          long long o_head, long long o_tok, float* LSE) {
   constexpr int V = D / 32;            // channels per lane
+  constexpr int BATCH = 8;             // parts in flight
   using Vec = std::conditional_t<V == 4, float4, float2>;
+  __shared__ Vec acc_s[8][32];
+  __shared__ float sum_s[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kvh = blockIdx.x / g.nslot_q, slot = blockIdx.x - kvh * g.nslot_q;
+  PackedSeq q;
+  int tile = 0, parts = 0, base = 0;
+  if (packed_find(g, g.q_ptr, g.TQ, slot, q)) {
+    tile = slot - (q.q0 / g.TQ + q.s);
+    if (tile * g.TQ < q.lq) {
+      base = packed_items_before(g, part_keys, q.s, lane);
+      packed_items(g, part_keys, q.s, parts);
+      base += tile * parts;
+      if (base + parts > head_items) parts = 0;
+    }
+  }
   cudaGridDependencySynchronize();
-  const int4 t = tiles[blockIdx.x];
-  const int parts = t.x, group = H / Hkv, rows = t.z * group;
-  if (parts == 0) return;
-  for (int r = blockIdx.y * 8 + warp; r < rows; r += 8 * gridDim.y) {
-    const float* L = Lpart + (long long)blockIdx.x * part_rows + r;
-    const float* src = Opart + ((long long)blockIdx.x * part_rows + r) * D + lane * V;
-    float M = -INFINITY;
-    for (int p = lane; p < parts; p += 32) M = fmaxf(M, L[(long long)p * part_rows]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (parts <= 1) return;              // the part wrote the result itself
+  const int t0 = tile * g.TQ, rows = min(g.TQ, q.lq - t0) * g.group;
+  const int k = warp % wpr, per = 8 / wpr;
+  const long long item0 = (long long)kvh * head_items + base;
+  for (int r0 = blockIdx.y * per; r0 < rows; r0 += per * gridDim.y) {
+    const int r = r0 + warp / wpr;
+    const bool live = r < rows;
+    float M = -INFINITY, sum = 0.f;
     float acc[V] = {};
-    float sum = 0.f;
-    for (int p0 = 0; p0 < parts && M != -INFINITY; p0 += 32) {
-      const float mine = p0 + lane < parts ? L[(long long)(p0 + lane) * part_rows] : -INFINITY;
-      const float w = mine == -INFINITY ? 0.f : ex2(mine - M);
-      const int n = min(32, parts - p0);
-      for (int j = 0; j < n; j += 16) {
-        Vec x[16];
+    if (live) {
+      const float* L = Lpart + item0 * part_rows + r;
+      const float* src = Opart + (item0 * part_rows + r) * D + lane * V;
+      for (int p = lane; p < parts; p += 32) M = fmaxf(M, L[(long long)p * part_rows]);
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          if (j + k < n) x[k] = *reinterpret_cast<const Vec*>(src + (long long)(p0 + j + k) * part_rows * D);
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      for (int p0 = k; p0 < parts && M != -INFINITY; p0 += BATCH * wpr) {
+        Vec x[BATCH];
+        float lp[BATCH];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          if (j + k >= n) continue;
-          const float wk = __shfl_sync(0xffffffffu, w, (j + k) & 31);
-          if (wk == 0.f) continue;
-          sum += wk;
-          const float* xv = reinterpret_cast<const float*>(&x[k]);
+        for (int j = 0; j < BATCH; ++j) {
+          const long long p = p0 + j * wpr;
+          lp[j] = -INFINITY;
+          if (p < parts) {
+            lp[j] = L[p * part_rows];
+            x[j] = *reinterpret_cast<const Vec*>(src + p * part_rows * D);
+          }
+        }
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[i] = fmaf(wk, xv[i], acc[i]);
+        for (int j = 0; j < BATCH; ++j) {
+          if (lp[j] == -INFINITY) continue;
+          const float w = ex2(lp[j] - M);
+          sum += w;
+          const float* xv = reinterpret_cast<const float*>(&x[j]);
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[i] = fmaf(w, xv[i], acc[i]);
         }
       }
     }
+    if (wpr > 1) {
+      if (k > 0) {
+        acc_s[warp][lane] = *reinterpret_cast<const Vec*>(acc);
+        if (lane == 0) sum_s[warp] = sum;
+      }
+      __syncthreads();
+      if (k == 0) {
+        for (int o = 1; o < wpr; ++o) {
+          const Vec x = acc_s[warp + o][lane];
+          const float* xv = reinterpret_cast<const float*>(&x);
+          sum += sum_s[warp + o];
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[i] += xv[i];
+        }
+      }
+      __syncthreads();
+    }
+    if (!live || k > 0) continue;
     const float inv = M != -INFINITY ? 1.0f / sum : 0.f;
-    const int rt = r / group, head = t.w * group + (r - rt * group);
-    const long long tok = (long long)t.y + rt;
+    const int rt = r / g.group, head = kvh * g.group + (r - rt * g.group);
+    const long long tok = (long long)q.q0 + t0 + rt;
     uint32_t* dst = reinterpret_cast<uint32_t*>(O + head * o_head + tok * o_tok + lane * V);
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) dst[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    if (lane == 0) LSE[(long long)head * Tq + tok] = M != -INFINITY ? (M + log2f(sum)) * kLn2 : -INFINITY;
+    if (lane == 0) LSE[(long long)head * g.Tq + tok] = M != -INFINITY ? (M + log2f(sum)) * kLn2 : -INFINITY;
   }
 }
 
@@ -727,30 +764,30 @@ cudaError_t launch_t(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUten
   if (launched < kRegsLaunch) return cudaErrorInvalidKernelImage;
   const int items = sp.part_keys > 0 ? sp.items : g.nslot_q;
   const long long total = (long long)g.Hkv * items;
-  // workspace: a description of each item's tile, the parts' O, their log-sums
-  int4* tiles = sp.part_keys > 0 ? static_cast<int4*>(ws) : nullptr;
-  float* Opart = sp.part_keys > 0 ? reinterpret_cast<float*>(static_cast<char*>(ws) + align256(total * sizeof(int4)))
-                                  : nullptr;
+  // workspace: the parts' O, their log-sums
+  float* Opart = sp.part_keys > 0 ? static_cast<float*>(ws) : nullptr;
   float* Lpart = sp.part_keys > 0 ? Opart + (size_t)total * sp.rows * D : nullptr;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(O.ptr);
   const int wide = wide_rows(O);     // rows are stored a sector at a time
   kern<<<(unsigned)total, kFwdThreads, T::SMEM, st>>>(tmQ, tmK, tmV, g, sp.part_keys, sp.rows, items,
                                                       scale * 1.4426950408889634f, o, O.head_stride, O.token_stride,
-                                                      lse, Opart, Lpart, tiles, wide, ctl);
+                                                      lse, Opart, Lpart, wide, ctl);
   if ((e = cudaGetLastError()) != cudaSuccess || sp.part_keys == 0) return e;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)total, (unsigned)((sp.rows + 15) / 16));
+  // a row's warps: up to eight parts each in one batch of loads
+  const int most_parts = (g.Tk + sp.part_keys - 1) / sp.part_keys;
+  const int wpr = most_parts <= 8 ? 1 : most_parts <= 16 ? 2 : most_parts <= 32 ? 4 : 8;
+  cfg.gridDim = dim3((unsigned)(g.Hkv * g.nslot_q), (unsigned)((sp.rows * wpr + 15) / 16));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, packed_combine_kernel<D>, g.H, g.Hkv, g.Tq, sp.rows,
-                            static_cast<const int4*>(tiles), static_cast<const float*>(Opart),
-                            static_cast<const float*>(Lpart), o, (long long)O.head_stride, (long long)O.token_stride,
-                            lse);
+  return cudaLaunchKernelEx(&cfg, packed_combine_kernel<D>, g, sp.part_keys, items, sp.rows, wpr,
+                            static_cast<const float*>(Opart), static_cast<const float*>(Lpart), o,
+                            (long long)O.head_stride, (long long)O.token_stride, lse);
 }
 
 }  // namespace
@@ -759,7 +796,7 @@ size_t packed_fwd_ws_bytes(const dsv_packed& p) {
   const FwdSplit sp = fwd_split(p);
   if (sp.part_keys == 0) return 0;
   const size_t total = (size_t)p.Hkv * sp.items;
-  return align256(total * sizeof(int4)) + total * sp.rows * (p.d + 1) * sizeof(float);
+  return total * sp.rows * (p.d + 1) * sizeof(float);
 }
 
 cudaError_t launch_packed_fwd(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
