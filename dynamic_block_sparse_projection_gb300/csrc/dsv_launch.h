@@ -114,7 +114,7 @@ size_t rope_bwd_ws_bytes(const dsv_rope& r);
 
 // Attention of packed sequences (packed_fwd.cu, packed_bwd.cu).
 constexpr int kPackedSMs = 152;               // what the split rules and head chunks are sized for
-constexpr int kPackedMinPart = 4;             // fewest key tiles of one part of a split query tile
+constexpr int kPackedMinPart = 4;             // fewest query tiles of one run of a split key tile
 // Tile slots of T tokens in S sequences (packed.cuh).
 inline long long packed_slots(int T, int tile, int S) { return (long long)T / tile + S; }
 struct PackedMaps {

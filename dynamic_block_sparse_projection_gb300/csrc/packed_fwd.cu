@@ -722,10 +722,15 @@ __global__ void __launch_bounds__(256, 4)
 }
 
 // Split over the keys.  With at least one query tile per SM the keys stay
-// whole.  With fewer, every tile's keys are cut into parts of equal size, as
-// small as fill four rounds of the SMs (the lengths are not known on the host:
-// uneven ones even out over the rounds), but of kPackedMinPart key tiles at
-// least.
+// whole.  With fewer, every tile's keys are cut into parts of equal size.  What
+// a part costs beside its keys is its rows: the load of Q, the fp32 O written
+// and read again.  With few rows (single new tokens) the parts are as small as
+// fill four rounds of the SMs (the lengths are not known on the host: uneven
+// ones even out over the rounds), of four key tiles at least; with 32 rows or
+// more, two rounds and eight tiles.  Measured, the one rule against the other:
+// eight streams of one token, 3 rows, 67 / 69 us, one stream of 1 row 12.7 /
+// 14.6; one head of 4096 tokens 24 / 21 us, two heads of two clips up to 4173
+// tokens 42 / 32, 48 rows against 16 000 keys 22.6 / 19.8.
 struct FwdSplit {
   int part_keys;     // 0: not split
   int items;         // bound on the items of a key head
@@ -739,12 +744,16 @@ FwdSplit fwd_split(const dsv_packed& p) {
   const long long most = q_tiles > p.S ? q_tiles : p.S;    // of all, roughly
   if (p.Hkv * most >= kPackedSMs) return sp;
   const long long key_tiles = (long long)p.Hkv * ((p.Tk + 127) / 128) * ((most + p.S - 1) / p.S);
-  long long part = (key_tiles + 4LL * kPackedSMs - 1) / (4LL * kPackedSMs);
-  part = part < kPackedMinPart ? kPackedMinPart : part;
+  sp.rows = group * (p.Tq < TQ ? p.Tq : TQ);
+  const long long fill = (sp.rows < 32 ? 4LL : 2LL) * kPackedSMs, least = sp.rows < 32 ? 4 : 8;
+  long long part = (key_tiles + fill - 1) / fill;
+  part = part < least ? least : part;
   if ((p.Tk + 127) / 128 <= part) return sp;               // one part at most
   sp.part_keys = (int)part * 128;
-  sp.items = (int)(q_tiles * ((long long)p.Tk / sp.part_keys + p.S));
-  sp.rows = group * (p.Tq < TQ ? p.Tq : TQ);
+  // sum over sequences of tiles x parts: no sequence has more tiles than q_tiles, nor more parts than all keys
+  const long long by_parts = q_tiles * ((long long)p.Tk / sp.part_keys + p.S);
+  const long long by_tiles = packed_slots(p.Tq, TQ, p.S) * (((long long)p.Tk + sp.part_keys - 1) / sp.part_keys);
+  sp.items = (int)(by_parts < by_tiles ? by_parts : by_tiles);
   return sp;
 }
 
