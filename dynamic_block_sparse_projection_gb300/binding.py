@@ -46,15 +46,22 @@ EXPORTS = (
 SELFTEST_WAIT_ID = 0xD5F0
 
 
+def _load_calls():
+    if not _CALLS_PATH.exists():
+        raise ImportError(f"dsv_calls.so is not built ({_CALLS_PATH}); run __graft_entry__.build() first")
+    loader = importlib.machinery.ExtensionFileLoader("dsv_calls", str(_CALLS_PATH))
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("dsv_calls", loader))
+    loader.exec_module(module)
+    return module
+
+
+_calls = _load_calls()
+View = _calls.View            # dsv_view
+
+
 class Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("N", ctypes.c_int32),
                 ("d", ctypes.c_int32), ("block", ctypes.c_int32), ("r", ctypes.c_int32)]
-
-
-class View(ctypes.Structure):
-    """dsv_view: the address and element strides of a [batch, heads, tokens, d] tensor."""
-    _fields_ = [("ptr", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
-                ("token_stride", ctypes.c_int64)]
 
 
 class Rope(ctypes.Structure):
@@ -143,19 +150,9 @@ def _load() -> ctypes.CDLL:
     lib.dsv_version.argtypes = []
     lib.dsv_version.restype = i32
     # the calls with several structures, by C (pycalls.c): the same arguments
-    calls = _load_calls()
     for name in ("dsv_rope_axes_fwd", "dsv_rope_axes_bwd", "dsv_packed_attn_fwd", "dsv_packed_attn_bwd"):
-        setattr(lib, name, getattr(calls, name))
+        setattr(lib, name, getattr(_calls, name))
     return lib
-
-
-def _load_calls():
-    if not _CALLS_PATH.exists():
-        raise ImportError(f"dsv_calls.so is not built ({_CALLS_PATH}); run __graft_entry__.build() first")
-    loader = importlib.machinery.ExtensionFileLoader("dsv_calls", str(_CALLS_PATH))
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("dsv_calls", loader))
-    loader.exec_module(module)
-    return module
 
 
 lib = _load()
@@ -221,14 +218,6 @@ def _need_rows(t: torch.Tensor, name: str, device: Optional[torch.device] = None
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.stride(-1) != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-
-
-def _need_rows_on(device: torch.device, index: int, **tensors) -> None:
-    """_need_rows for each tensor (None: left out); index: the device's, as get_device() gives it."""
-    bf16 = torch.bfloat16
-    for name, t in tensors.items():
-        if t is not None and (t.dtype is not bf16 or t.get_device() != index or t.stride(-1) != 1):
-            _need_rows(t, name, device)
 
 
 def _need_on(device: torch.device, index: int, dtype: torch.dtype, **tensors) -> None:
@@ -674,14 +663,16 @@ def _alloc_on(stream):
     return torch.cuda.stream(stream)
 
 
-def _view(t: Optional[torch.Tensor]) -> View:
-    """dsv_view of a [.., heads, tokens, d] tensor of 3 or 4 dimensions."""
-    if t is None:
-        return View(None, 0, 0, 0)
-    st = t.stride()
-    if len(st) == 4:
-        return View(t.data_ptr(), st[0], st[1], st[2])
-    return View(t.data_ptr(), 0, st[0], st[1])
+def _rows(device: torch.device, index: int, **tensors) -> Tuple[View, ...]:
+    """The views of [.., heads, tokens, d] tensors (None: the null view), each
+    checked as _need_rows does; index: the device's, as get_device() gives it."""
+    views = _calls.row_views(torch.bfloat16, index, *tensors.values())
+    if views is None:
+        for name, t in tensors.items():
+            if t is not None:
+                _need_rows(t, name, device)
+        raise ValueError("the tensors must be rows of bf16 on one device: " + ", ".join(tensors))
+    return views
 
 
 @functools.lru_cache(maxsize=64)
@@ -719,13 +710,14 @@ def rope_axes(x, pos, sections: Sequence[int], *, theta: float = 10000.0, weight
     _need_rows(x, "x")
     dev, at = x.device, x.get_device()
     _need_on(dev, at, torch.int32, pos=pos)
-    _need_on(dev, at, torch.float32, weight=weight)
-    _need_rows_on(dev, at, out=out)
+    if weight is not None:
+        _need_on(dev, at, torch.float32, weight=weight)
     if out is None:
         with _alloc_on(stream):
             out = torch.empty_like(x)
-    _call(lib.dsv_rope_axes_fwd, "dsv_rope_axes_fwd", dev, _view(x), pos.data_ptr(), pos_b, r, _ptr(weight), eps,
-          _view(out), _stream(dev, stream))
+    vx, vy = _rows(dev, at, x=x, out=out)
+    _call(lib.dsv_rope_axes_fwd, "dsv_rope_axes_fwd", dev, vx, pos.data_ptr(), pos_b, r, _ptr(weight), eps, vy,
+          _stream(dev, stream))
     return out
 
 
@@ -752,10 +744,8 @@ def rope_axes_bwd(dy, pos, sections: Sequence[int], *, theta: float = 10000.0, x
     _need_rows(dy, "dy")
     dev, at = dy.device, dy.get_device()
     _need_on(dev, at, torch.int32, pos=pos)
-    _need_rows_on(dev, at, dx=dx)
     nbytes, ws = 0, None
     if weight is not None:
-        _need_rows_on(dev, at, x=x)
         _need_on(dev, at, torch.float32, weight=weight, dweight=dweight)
     with _alloc_on(stream):
         if dx is None:
@@ -765,10 +755,15 @@ def rope_axes_bwd(dy, pos, sections: Sequence[int], *, theta: float = 10000.0, x
                 dweight = torch.empty(r.d, dtype=torch.float32, device=dev)
             nbytes = lib.dsv_rope_axes_bwd_workspace_bytes(r)
             ws = _scratch(nbytes, dev, workspace)
-    _call(lib.dsv_rope_axes_bwd, "dsv_rope_axes_bwd", dev, _view(dy), _view(x if weight is not None else None),
-          pos.data_ptr(), pos_b, r, _ptr(weight), eps, _view(dx), _ptr(dweight), _ptr(ws), nbytes,
-          _stream(dev, stream))
+    vdy, vx, vdx = _rows(dev, at, dy=dy, x=x if weight is not None else None, dx=dx)
+    _call(lib.dsv_rope_axes_bwd, "dsv_rope_axes_bwd", dev, vdy, vx, pos.data_ptr(), pos_b, r, _ptr(weight), eps, vdx,
+          _ptr(dweight), _ptr(ws), nbytes, _stream(dev, stream))
     return dx if weight is None else (dx, dweight)
+
+
+@functools.lru_cache(maxsize=64)
+def _packed(*sizes: int) -> Packed:
+    return Packed(*sizes)
 
 
 def _packed_shape(Q, K, V, q_ptr, k_ptr) -> Packed:
@@ -783,7 +778,7 @@ def _packed_shape(Q, K, V, q_ptr, k_ptr) -> Packed:
     if S < 0:
         raise ValueError("q_ptr must hold at least one element")
     _shape(k_ptr, "k_ptr", q_ptr.shape)
-    return Packed(S, H, Hkv, Tq, Tk, d)
+    return _packed(S, H, Hkv, Tq, Tk, d)
 
 
 def packed_attn_fwd_workspace_bytes(S: int, H: int, Hkv: int, Tq: int, Tk: int, d: int) -> int:
@@ -811,9 +806,9 @@ def packed_attn_fwd(Q, K, V, q_ptr, k_ptr, softmax_scale: float = 0.0, *, causal
         _shape(lse, "lse", (p.H, p.Tq))
     _need_rows(Q, "Q")
     dev, at = Q.device, Q.get_device()
-    _need_rows_on(dev, at, K=K, V=V, out=out)
     _need_on(dev, at, torch.int32, q_ptr=q_ptr, k_ptr=k_ptr)
-    _need_on(dev, at, torch.float32, lse=lse)
+    if lse is not None:
+        _need_on(dev, at, torch.float32, lse=lse)
     nbytes = lib.dsv_packed_attn_fwd_workspace_bytes(p)
     with _alloc_on(stream):
         if out is None:
@@ -821,9 +816,9 @@ def packed_attn_fwd(Q, K, V, q_ptr, k_ptr, softmax_scale: float = 0.0, *, causal
         if lse is None:
             lse = torch.empty(p.H, p.Tq, dtype=torch.float32, device=dev)
         ws = _scratch(nbytes, dev, workspace) if nbytes else None
-    _call(lib.dsv_packed_attn_fwd, "dsv_packed_attn_fwd", dev, _view(Q), _view(K), _view(V), p, q_ptr.data_ptr(),
-          k_ptr.data_ptr(), 1 if causal else 0, softmax_scale, _view(out), lse.data_ptr(), _ptr(ws), nbytes,
-          _stream(dev, stream))
+    vq, vk, vv, vo = _rows(dev, at, Q=Q, K=K, V=V, out=out)
+    _call(lib.dsv_packed_attn_fwd, "dsv_packed_attn_fwd", dev, vq, vk, vv, p, q_ptr.data_ptr(), k_ptr.data_ptr(),
+          1 if causal else 0, softmax_scale, vo, lse.data_ptr(), _ptr(ws), nbytes, _stream(dev, stream))
     return out, lse
 
 
@@ -842,19 +837,17 @@ def packed_attn_bwd(Q, K, V, O, dO, lse, q_ptr, k_ptr, softmax_scale: float = 0.
             _shape(t, name, like.shape)
     _need_rows(Q, "Q")
     dev, at = Q.device, Q.get_device()
-    _need_rows_on(dev, at, K=K, V=V, O=O, dO=dO)
     _need_on(dev, at, torch.int32, q_ptr=q_ptr, k_ptr=k_ptr)
     _need_on(dev, at, torch.float32, lse=lse)
-    if outs is not None:
-        _need_rows_on(dev, at, dQ=outs[0], dK=outs[1], dV=outs[2])
     nbytes = lib.dsv_packed_attn_bwd_workspace_bytes(p)
     with _alloc_on(stream):
         if outs is None:
             outs = (torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V))
         ws = _scratch(nbytes, dev, workspace) if nbytes else None
-    _call(lib.dsv_packed_attn_bwd, "dsv_packed_attn_bwd", dev, _view(Q), _view(K), _view(V), _view(O), _view(dO),
-          lse.data_ptr(), p, q_ptr.data_ptr(), k_ptr.data_ptr(), 1 if causal else 0, softmax_scale, _view(outs[0]),
-          _view(outs[1]), _view(outs[2]), _ptr(ws), nbytes, _stream(dev, stream))
+    vq, vk, vv, vo, vdo, vdq, vdk, vdv = _rows(dev, at, Q=Q, K=K, V=V, O=O, dO=dO, dQ=outs[0], dK=outs[1], dV=outs[2])
+    _call(lib.dsv_packed_attn_bwd, "dsv_packed_attn_bwd", dev, vq, vk, vv, vo, vdo, lse.data_ptr(), p,
+          q_ptr.data_ptr(), k_ptr.data_ptr(), 1 if causal else 0, softmax_scale, vdq, vdk, vdv, _ptr(ws), nbytes,
+          _stream(dev, stream))
     return outs
 
 
