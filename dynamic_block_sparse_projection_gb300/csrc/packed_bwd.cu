@@ -15,13 +15,22 @@
 //   kv       one CTA per key tile and key head, over the sequence's query
 //            tiles: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.
 //            Shared heads add up inside the product, and every output tile has
-//            one writer.  With fewer key tiles than SMs the query tiles of each
-//            are split over several CTAs and the join kernel adds their fp32
-//            sums in order.
+//            one writer.  With far fewer key tiles than SMs the query tiles of
+//            each are split over several CTAs (bwd_splits) and the join kernel
+//            adds their fp32 sums in order.
 //   q        one CTA per SM over the query tiles, taking over the grid's other
 //            CTAs as it goes (packed_fwd.cu): S = Q K^T, dP = dO V^T, dQ += dS K.
 // S and dP are computed twice (seven products per tile pair instead of five),
 // which buys results that do not depend on the order CTAs run in.
+//
+// P and dS are rounded to bf16, the type of the products' other operand; sums
+// stay in fp32 in tensor memory.  Measured, d = 128: 24 heads of four clips of
+// 515 to 8192 tokens, kv 1237 us (1722 TFLOP/s of its four products, 92 % of what
+// a large library product reaches in a burst), q 960 us (1664 TFLOP/s), prepare
+// 31 us; causal, 24 heads over 8 key heads, five clips of 64 to 6000 tokens, kv
+// 380 us (1655), q 299 us (1577), prepare 27, rows 13; text (16 384 and 8192
+// tokens against 226 and 512 keys, 24 heads), prepare 49 us (HBM), the call 335.
+// Tensor cores bound kv and q, under the power cap when calls follow closely.
 //
 // D_i from O.  O is bf16, so dO . O is off by some 2^-9 |dO| |O| / sqrt(d).  Over
 // many keys O is small against the v_j and that vanishes beside the rounding
