@@ -633,7 +633,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 // Joins the parts of a tile: with L_p the base-2 log-sums, M = max L_p and
 // w_p = 2^(L_p - M):  O = sum w_p O_p / sum w_p,  lse = (M + log2 sum w_p) ln 2.
 // A part that saw nothing of the row wrote no O: its weight is 0 and its values
-// are left out.  One CTA per query slot and key head (along x) and run of rows
+// are left out.  A NaN among the L_p makes M and with it the row NaN (fmaxf
+// alone would drop it, and a row of NaN parts would pass for one without keys).
+// One CTA per query slot and key head (along x) and run of rows
 // (along y); `wpr` warps share a row, each adding up every wpr-th part, and the
 // first adds their sums in order.  Latency-bound: what a CTA has to know of its
 // tile it works out before it waits for the parts, and few enough registers
@@ -675,9 +677,15 @@ __global__ void __launch_bounds__(256, 4)
     if (live) {
       const float* L = Lpart + item0 * part_rows + r;
       const float* src = Opart + (item0 * part_rows + r) * D + lane * V;
-      for (int p = lane; p < parts; p += 32) M = fmaxf(M, L[(long long)p * part_rows]);
+      bool nan = false;
+      for (int p = lane; p < parts; p += 32) {
+        const float lp = L[(long long)p * part_rows];
+        nan |= lp != lp;
+        M = fmaxf(M, lp);
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      if (__any_sync(0xffffffffu, nan)) M = NAN;
       for (int p0 = k; p0 < parts && M != -INFINITY; p0 += BATCH * wpr) {
         Vec x[BATCH];
         float lp[BATCH];

@@ -440,3 +440,26 @@ def test_packed_equals_the_dense_sparse_call(dsv):
     O2, lse2 = dsv.sparse_attn_fwd(c.Q[None], c.K[None], c.V[None], fp, fc, blk)
     assert torch.equal(O, O2[0]) or (O.float() - O2[0].float()).abs().max() <= 2 * U * c.V.float().abs().max()
     assert (lse - lse2[0]).abs().max() <= 2 * E
+
+
+
+@pytest.mark.parametrize("H, Hkv, ql, kl, split", [(2, 2, (1, 3), (1300, 700), True), (6, 2, (40,), (3000,), True),
+                                                   (20, 20, (1000, 30), (1000, 600), False)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_packed_a_query_that_is_not_a_number_gives_none(dsv, H, Hkv, ql, kl, split, causal):
+    """O and lse of a NaN query, and of one whose scores overflow, are NaN
+    whether its keys are split or not (0 and -inf are for rows without keys);
+    so is its gradient.  The other rows stay right."""
+    assert (dsv.packed_attn_fwd_workspace_bytes(len(ql), H, Hkv, sum(ql), sum(kl), 64) > 0) == split
+    c = Case(H, Hkv, 64, ql, kl)
+    b = _bounds(*c.np(), c.qp, c.kp, causal, 0.0)
+    bad = torch.zeros(H, sum(ql), dtype=torch.bool, device="cuda")
+    bad[0, 0] = bad[1, -1] = True
+    c.Q[0, 0, 5], c.Q[1, -1, 3] = float("nan"), float("inf")
+    O, lse = c.fwd(dsv, causal)
+    assert O[bad].isnan().all() and lse[bad].isnan().all()
+    dQ = c.bwd(dsv, O, lse, causal)[0]
+    assert dQ[bad].isnan().all()
+    ok = ~bad.cpu().numpy()
+    for got, (ref, tol), what in ((O, b[0], "O"), (lse, b[1], "lse")):
+        assert np.all(np.abs(to64(got)[ok] - ref[ok]) <= tol[ok]), what
