@@ -8,7 +8,8 @@
 // The dense companion of the block-sparse forward (attn_fwd.cu): the same
 // pipeline of one 128-row query tile against a stream of 128-key tiles with S,
 // P and O in tensor memory and an online softmax whose reference is the first
-// tile's row maximum, redone only when a later value of P would pass 2^64.
+// tile's row maximum, redone only when a later value of P would pass 2^64 (or no
+// score before was finite).
 // What differs: tiles come from packed.cuh's slots (a tile's rows are tokens x
 // shared heads), rows end at their own limit, and where there are fewer tiles
 // than SMs each tile's keys are split over several CTAs.
@@ -450,8 +451,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     bool ok = true;
     FwdItem it;
     for (uint32_t i = 0; ok && take(i, it); ++i) {
-      const bool row_ok = rt < it.ntok;
       const int lim_r = g.causal ? min(it.left, it.lim0 + rt) : it.left;   // keys of this part that the row sees
+      // a token's row that sees keys: rows behind the tile's tokens hold another sequence's queries
+      const bool counts = rt < it.ntok && lim_r > 0;
       float m = 0.f, l = 0.f;
       uint32_t s_tested = 0u;   // S(n) already known complete (tested during tile n-1)
       for (int n = 0; n < it.nt; ++n) {
@@ -518,7 +520,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // The reference is the first tile's row maximum (every row's limit
         // covers a prefix of the part's keys, so a row that sees any of them
         // sees one in the first tile; one that sees none keeps 0).  A later
-        // tile keeps it unless one of its values would pass 2^64.
+        // tile keeps it unless one of its values would pass 2^64, or all scores
+        // before it were -inf (l = 0): those set no reference, and against the 0
+        // in its place finite scores far below it would all vanish.
         float tsum;
         bool take_max = n == 0;
         while (true) {
@@ -528,12 +532,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
               m = mx == -INFINITY ? 0.f : mx;
             } else {
               // rescale this warp's O rows once the previous PV product has landed
-              const float m_new = fmaxf(m, mx);
+              const float m_new = l != 0.f ? fmaxf(m, mx) : mx == -INFINITY ? 0.f : mx;
               const uint32_t gp = gn - 1;
               ok = mbar_wait_warp(&o_done[gp % NST], (gp / NST) & 1u, abort_flag, ctl, kid | W_O);
               if (!ok) break;
               tc_fence_after();
-              const float alpha = ex2(m - m_new);
+              const float alpha = l != 0.f ? ex2(m - m_new) : 1.f;   // (O is 0 where l is)
               l *= alpha;
               m = m_new;
 #pragma unroll
@@ -549,8 +553,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
           }
           tsum = exponentiate(m);
-          // rows behind the tile's tokens hold another sequence's queries: they must not decide
-          if (take_max || !__any_sync(0xffffffffu, row_ok && !(tsum <= 18446744073709551616.0f))) break;   // 2^64
+          if (take_max || !__any_sync(0xffffffffu, counts && !(tsum <= 18446744073709551616.0f && l != 0.f))) break;   // 2^64
           take_max = true;
         }
         if (!ok) break;

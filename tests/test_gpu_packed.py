@@ -463,3 +463,25 @@ def test_packed_a_query_that_is_not_a_number_gives_none(dsv, H, Hkv, ql, kl, spl
     ok = ~bad.cpu().numpy()
     for got, (ref, tol), what in ((O, b[0], "O"), (lse, b[1], "lse")):
         assert np.all(np.abs(to64(got)[ok] - ref[ok]) <= tol[ok]), what
+
+
+
+@pytest.mark.parametrize("H, ql, split", [(2, (150,), True), (20, (1000,), False)])
+def test_packed_first_keys_that_weigh_nothing(dsv, H, ql, split):
+    """Every score of the first key tile is -inf and the others lie far below
+    zero: the row's reference is the first finite maximum, not 0, against which
+    every exponential would be 0."""
+    N = 1500
+    assert (dsv.packed_attn_fwd_workspace_bytes(1, H, H, ql[0], N, 64) > 0) == split
+    c = Case(H, H, 64, ql, (N,))
+    c.Q = (c.Q.float().abs() + 0.5).clamp(max=3.0).to(torch.bfloat16)
+    c.K = -(14.0 + c.K.float().abs().clamp(max=4.0)).to(torch.bfloat16)
+    c.K[:, :200] = float("-inf")
+    O, lse = c.fwd(dsv, False)
+    ref, lref = oracle.packed_attn_fwd(*c.np()[:3], c.qp, c.kp)
+    # scores of one sign: an fp32 sum of 64 products is good to 64 2^-24 |s|, |s| <= 64 * 3 * 18 / 8 = 432 < 2^9
+    assert np.max(lref) < -104 and np.min(lref) > -432        # exp(-104) is 0 in fp32
+    s = 64 * 2.0 ** -24 * 2.0 ** 9
+    assert np.max(np.abs(to64(lse) - lref)) <= s + E + 2.0 ** -20 * 432
+    assert np.max(np.abs(to64(O) - ref)) <= (2 * U + E + 2 * s) * np.max(np.abs(to64(c.V)))
+    assert dsv.device_error()[0] == 0
