@@ -1305,26 +1305,25 @@ cudaError_t launch_t(const PackedMaps& m, const PackedGeom& g, const dsv_view& O
   cudaLaunchConfig_t cfg{};
   cfg.stream = st;
   cfg.attrs = &early;
-  cfg.numAttrs = g.Tk > 0 ? 1 : 0;
-  if (g.Tq > 0) {
-    if (g.Tk > 0) {
-      auto rows = packed_bwd_rows_kernel<D>;
-      constexpr int smem = PRowsTraits<D>::SMEM;
-      if ((e = cudaFuncSetAttribute(rows, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-      const long long slots = (long long)g.Hkv * g.nslot_q;
-      rows<<<(unsigned)(slots < kPackedSMs ? slots : kPackedSMs), kRowsThreads, smem, st>>>(m.Q, m.K, m.V, m.dO, g, lse,
-                                                                                            scale, Dw, ctl);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    // beside the rows kernel; it ends no earlier (its last lines)
-    cfg.gridDim = dim3((unsigned)g.nslot_q, (unsigned)g.Hkv);
-    cfg.blockDim = dim3(256);
-    if ((e = cudaLaunchKernelEx(&cfg, packed_bwd_prep_kernel<D>, g, static_cast<const __nv_bfloat16*>(O.ptr),
-                                (long long)O.head_stride, (long long)O.token_stride,
-                                static_cast<const __nv_bfloat16*>(dO.ptr), (long long)dO.head_stride,
-                                (long long)dO.token_stride, lse, Dw, L2w, ctl)) != cudaSuccess)
-      return e;
+  cfg.numAttrs = g.Tk > 0 && g.Tq > 0 ? 1 : 0;
+  if (g.Tk > 0 && g.Tq > 0) {
+    auto rows = packed_bwd_rows_kernel<D>;
+    constexpr int smem = PRowsTraits<D>::SMEM;
+    if ((e = cudaFuncSetAttribute(rows, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    const long long slots = (long long)g.Hkv * g.nslot_q;
+    rows<<<(unsigned)(slots < kPackedSMs ? slots : kPackedSMs), kRowsThreads, smem, st>>>(m.Q, m.K, m.V, m.dO, g, lse,
+                                                                                          scale, Dw, ctl);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
+  // beside the rows kernel; it ends no earlier (its last lines).  Without
+  // queries one CTA is left of it, for its check of the pointers.
+  cfg.gridDim = g.Tq > 0 ? dim3((unsigned)g.nslot_q, (unsigned)g.Hkv) : dim3(1);
+  cfg.blockDim = dim3(256);
+  if ((e = cudaLaunchKernelEx(&cfg, packed_bwd_prep_kernel<D>, g, static_cast<const __nv_bfloat16*>(O.ptr),
+                              (long long)O.head_stride, (long long)O.token_stride,
+                              static_cast<const __nv_bfloat16*>(dO.ptr), (long long)dO.head_stride,
+                              (long long)dO.token_stride, lse, Dw, L2w, ctl)) != cudaSuccess)
+    return e;
   if (g.Tk > 0) {
     auto kv = packed_bwd_kv_kernel<D>;
     constexpr int smem = PKVTraits<D>::SMEM;

@@ -417,6 +417,8 @@ dsv_status dsv_rope_axes_bwd(dsv_view dy, dsv_view x, const int32_t* pos, int64_
  *           an empty sequence) within [0, Tq] and [0, Tk].  A sequence whose
  *           pointers break this is skipped and DSV_ERR_BAD_INDEX recorded in
  *           the device error word, with the sequence as its info.
+ *           (A forward without query tokens, or a backward without any tokens,
+ *           has nothing to do and does not read them.)
  * causal    0 or 1.  softmax_scale <= 0 selects 1/sqrt(d).
  * lse       fp32 [H, Tq] contiguous; the backward reads the forward's O and lse
  *           (those of the same keys: D_i is dO_i . O_i, or the equal sum of

@@ -485,3 +485,22 @@ def test_packed_first_keys_that_weigh_nothing(dsv, H, ql, split):
     assert np.max(np.abs(to64(lse) - lref)) <= s + E + 2.0 ** -20 * 432
     assert np.max(np.abs(to64(O) - ref)) <= (2 * U + E + 2 * s) * np.max(np.abs(to64(c.V)))
     assert dsv.device_error()[0] == 0
+
+
+
+def test_packed_gradient_without_queries_checks_its_pointers(dsv):
+    K = _rand(1, 2, 300, 64)
+    none = torch.empty(2, 0, 64, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(2, 0, device="cuda")
+    p = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")               # noqa: E731
+    for kp, bad in (((0, 130, 290), None), ((0, 130, 301), 1), ((0, 130, 120), 1), ((-1, 130, 290), 0)):
+        outs = (none.clone(), *(torch.full_like(K, 7.0) for _ in range(2)))
+        dsv.packed_attn_bwd(K[:, :0], K, K.clone(), none, none.clone(), lse, p(0, 0, 0), p(*kp), outs=outs)
+        st, info = dsv.device_error()
+        dsv.clear_device_error()
+        assert (st, info) == ((0, 0) if bad is None else (dsv.DSV_ERR_BAD_INDEX, bad))
+        for t in outs[1:]:
+            for s in (0, 1):
+                rows = t[:, max(kp[s], 0):kp[s + 1]]
+                assert (rows == (7 if s == bad else 0)).all() or kp[s + 1] < kp[s]
+            assert (t[:, 290:] == 7).all()
