@@ -708,6 +708,8 @@ dsv_status dsv_packed_attn_bwd(dsv_view Q, dsv_view K, dsv_view V, dsv_view O, d
   dsv_status v = check_packed(p);
   if (v != DSV_OK) return v;
   if (causal != 0 && causal != 1) return DSV_ERR_INVALID_ARG;
+  // keys without any query head: their gradients are zeros that no kernel here would write
+  if (p.S > 0 && p.H == 0 && p.Hkv > 0 && p.Tk > 0) return DSV_ERR_INVALID_ARG;
   const bool nq = no_queries(p), nk = no_keys(p);
   if (nq && nk) return DSV_OK;
   if (!q_ptr || !k_ptr || !al4(q_ptr) || !al4(k_ptr)) return DSV_ERR_INVALID_ARG;

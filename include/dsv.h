@@ -429,7 +429,8 @@ dsv_status dsv_rope_axes_bwd(dsv_view dy, dsv_view x, const int32_t* pos, int64_
  *           their fp32 parts joined in order.  Backward: D_i and
  *           -lse_i log2(e), and the fp32 parts of dK and dV where key tiles are
  *           fewer than the SMs.
- * d in {64, 128}; H <= 1024, a multiple of Hkv; H / Hkv <= 128;
+ * d in {64, 128}; H <= 1024, a multiple of Hkv (in the backward not 0 where
+ * there are keys); H / Hkv <= 128;
  * Tq + 128 S and Tk + 128 S < 2^31.  Outputs are bit-identical from run to run
  * (one writer per output tile, no atomics).  The waits inside the kernels run
  * to dsv_set_wait_limit_ns plus 10 us for every tile of tokens in the call.

@@ -220,3 +220,21 @@ def test_c_entries_check_their_arguments(dsv):
     for name, n in (("dsv_packed_attn_bwd", 17), ("dsv_rope_axes_fwd", 8), ("dsv_rope_axes_bwd", 12)):
         with pytest.raises(TypeError, match=f"expected {n} arguments"):
             getattr(dsv.lib, name)()
+
+
+def test_packed_gradient_of_keys_without_query_heads_is_refused(dsv):
+    """No query heads beside key heads: dK and dV would be left unwritten."""
+    L, P, none = dsv.lib, dsv.Packed, dsv.View(None, 0, 0, 0)
+
+    def b(p):
+        k = [_v3(dsv, a, 4, 30) for a in FAR[1:3]]
+        dk = [_v3(dsv, a, 4, 30) for a in FAR[6:8]]
+        return L.dsv_packed_attn_bwd(none, *k, none, none, None, p, FAKE, FAKE, 0, 0.0, none, *dk, None, 0, None)
+
+    assert b(P(2, 0, 4, 40, 30, 128)) == dsv.DSV_ERR_INVALID_ARG
+    assert b(P(2, 0, 4, 0, 30, 128)) == dsv.DSV_ERR_INVALID_ARG
+    # nothing to write: no keys, no sequences, no heads at all
+    for p in (P(2, 0, 4, 40, 0, 128), P(0, 0, 4, 40, 30, 128), P(2, 0, 0, 40, 30, 128)):
+        assert b(p) == dsv.DSV_OK
+    assert L.dsv_packed_attn_fwd(none, none, none, P(2, 0, 4, 40, 30, 128), FAKE, FAKE, 0, 0.0, none, None, None, 0,
+                                 None) == dsv.DSV_OK
