@@ -241,6 +241,7 @@ dsv_status check_rope(const dsv_rope& r) {
   if (!(r.theta >= 1.0) || !isfinite(r.theta)) return DSV_ERR_INVALID_ARG;
   if (r.H > kMaxHeads || r.B > 65535) return DSV_ERR_UNSUPPORTED;
   if ((long long)r.B * r.H * (r.N / 16 + 1) >= (1LL << 31)) return DSV_ERR_UNSUPPORTED;
+  if (r.N > INT32_MAX - 32) return DSV_ERR_UNSUPPORTED;   // token indexes of the last tile stay inside 32 bits
   return DSV_OK;
 }
 bool empty_rope(const dsv_rope& r) { return r.B == 0 || r.H == 0 || r.N == 0; }

@@ -374,7 +374,9 @@ typedef struct {
  * workspace >= dsv_rope_axes_bwd_workspace_bytes(r) bytes, 256-byte aligned
  *           (partial sums of dweight).
  * d in {64, 128}; 1 to 4 axes; sections even, at least 2, together at most d;
- * theta >= 1, finite; H <= 1024; B <= 65535.  Sums are fp32 in a fixed order.
+ * theta >= 1, finite; H <= 1024; B <= 65535; N < 2^31 - 32 and
+ * B * H * (N / 16 + 1) < 2^31 (DSV_ERR_UNSUPPORTED otherwise).  Sums are fp32 in
+ * a fixed order.
  * With B*H*N == 0 only dweight is written (zeros).
  * ------------------------------------------------------------------------ */
 typedef struct {

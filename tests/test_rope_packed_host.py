@@ -238,3 +238,17 @@ def test_packed_gradient_of_keys_without_query_heads_is_refused(dsv):
         assert b(p) == dsv.DSV_OK
     assert L.dsv_packed_attn_fwd(none, none, none, P(2, 0, 4, 40, 30, 128), FAKE, FAKE, 0, 0.0, none, None, None, 0,
                                  None) == dsv.DSV_OK
+
+
+def test_rope_refuses_token_counts_whose_last_tile_leaves_32_bits(dsv):
+    L = dsv.lib
+    for N in (2 ** 31 - 1, 2 ** 31 - 16, 2 ** 31 - 32):
+        for d in (64, 128):
+            r = _rope(dsv, B=1, H=1, N=N, d=d, sections=(d,))
+            x, y = (dsv.View(a, 0, d, d) for a in FAR[:2])
+            assert L.dsv_rope_axes_fwd(x, FAKE, 0, r, None, 1e-6, y, None) == dsv.DSV_ERR_UNSUPPORTED
+            assert L.dsv_rope_axes_bwd(x, x, FAKE, 0, r, None, 1e-6, y, None, None, 0, None) == dsv.DSV_ERR_UNSUPPORTED
+            assert L.dsv_rope_axes_bwd_workspace_bytes(r) == 0
+    # below that, and below the limit on all rows, sizes are taken
+    assert L.dsv_rope_axes_bwd_workspace_bytes(_rope(dsv, B=1, H=1, N=2 ** 31 - 33, sections=(64,))) > 0
+    assert L.dsv_rope_axes_bwd_workspace_bytes(_rope(dsv, B=1, H=17, N=2 ** 31 - 33, sections=(64,))) == 0
