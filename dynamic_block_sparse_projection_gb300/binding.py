@@ -675,8 +675,16 @@ def _rows(device: torch.device, index: int, **tensors) -> Tuple[View, ...]:
     return views
 
 
+def _fit32(**sizes: int) -> None:
+    """Sizes that the library takes as 32-bit integers (ctypes would keep their low bits)."""
+    for name, v in sizes.items():
+        if not -(1 << 31) <= v < 1 << 31:
+            raise ValueError(f"{name} = {v} does not fit in 32 bits")
+
+
 @functools.lru_cache(maxsize=64)
 def _rope(B: int, H: int, N: int, d: int, sections: Tuple[int, ...], theta: float) -> Rope:
+    _fit32(B=B, H=H, N=N, d=d, **{f"sections[{i}]": c for i, c in enumerate(sections)})
     return Rope(B, H, N, d, len(sections), (ctypes.c_int32 * 4)(*sections), theta)
 
 
@@ -722,7 +730,7 @@ def rope_axes(x, pos, sections: Sequence[int], *, theta: float = 10000.0, weight
 
 
 def rope_axes_bwd_workspace_bytes(d: int) -> int:
-    return int(lib.dsv_rope_axes_bwd_workspace_bytes(Rope(1, 1, 1, d, 1, (ctypes.c_int32 * 4)(d), 10000.0)))
+    return int(lib.dsv_rope_axes_bwd_workspace_bytes(_rope(1, 1, 1, d, (d,), 10000.0)))
 
 
 def rope_axes_bwd(dy, pos, sections: Sequence[int], *, theta: float = 10000.0, x=None, weight=None, eps: float = 1e-6,
@@ -762,8 +770,9 @@ def rope_axes_bwd(dy, pos, sections: Sequence[int], *, theta: float = 10000.0, x
 
 
 @functools.lru_cache(maxsize=64)
-def _packed(*sizes: int) -> Packed:
-    return Packed(*sizes)
+def _packed(S: int, H: int, Hkv: int, Tq: int, Tk: int, d: int) -> Packed:
+    _fit32(S=S, H=H, Hkv=Hkv, Tq=Tq, Tk=Tk, d=d)
+    return Packed(S, H, Hkv, Tq, Tk, d)
 
 
 def _packed_shape(Q, K, V, q_ptr, k_ptr) -> Packed:
@@ -782,11 +791,11 @@ def _packed_shape(Q, K, V, q_ptr, k_ptr) -> Packed:
 
 
 def packed_attn_fwd_workspace_bytes(S: int, H: int, Hkv: int, Tq: int, Tk: int, d: int) -> int:
-    return int(lib.dsv_packed_attn_fwd_workspace_bytes(Packed(S, H, Hkv, Tq, Tk, d)))
+    return int(lib.dsv_packed_attn_fwd_workspace_bytes(_packed(S, H, Hkv, Tq, Tk, d)))
 
 
 def packed_attn_bwd_workspace_bytes(S: int, H: int, Hkv: int, Tq: int, Tk: int, d: int) -> int:
-    return int(lib.dsv_packed_attn_bwd_workspace_bytes(Packed(S, H, Hkv, Tq, Tk, d)))
+    return int(lib.dsv_packed_attn_bwd_workspace_bytes(_packed(S, H, Hkv, Tq, Tk, d)))
 
 
 def packed_attn_fwd(Q, K, V, q_ptr, k_ptr, softmax_scale: float = 0.0, *, causal: bool = False, out=None, lse=None,

@@ -252,3 +252,25 @@ def test_rope_refuses_token_counts_whose_last_tile_leaves_32_bits(dsv):
     # below that, and below the limit on all rows, sizes are taken
     assert L.dsv_rope_axes_bwd_workspace_bytes(_rope(dsv, B=1, H=1, N=2 ** 31 - 33, sections=(64,))) > 0
     assert L.dsv_rope_axes_bwd_workspace_bytes(_rope(dsv, B=1, H=17, N=2 ** 31 - 33, sections=(64,))) == 0
+
+
+def test_binding_refuses_sizes_past_32_bits(fake):
+    """A size is not cut to its low 32 bits (2^32 + 1 keys would pass for one)."""
+    dsv, calls = fake
+    many, bf = 2 ** 32 + 1, torch.bfloat16
+    row, ptr = torch.zeros(1, 1, 64, dtype=bf), torch.zeros(2, dtype=torch.int32)
+    far, far_ptr = row.expand(1, many, 64), torch.zeros(1, dtype=torch.int32).expand(many + 1)
+    for args in ((row, far, far, ptr, ptr), (far, row, row, ptr, ptr), (row, row, row, far_ptr, far_ptr)):
+        with pytest.raises(ValueError, match="32 bits"):
+            dsv.packed_attn_fwd(*args)
+        with pytest.raises(ValueError, match="32 bits"):
+            dsv.packed_attn_bwd(*args[:3], args[0], args[0], torch.zeros(1).expand(1, args[0].shape[1]), *args[3:])
+    pos = torch.zeros(1, 1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="32 bits"):
+        dsv.rope_axes(far[None], pos.expand(many, 1), (64,))
+    with pytest.raises(ValueError, match="32 bits"):
+        dsv.rope_axes(row[None], pos, (2 ** 32 + 64,))
+    for f in (dsv.packed_attn_fwd_workspace_bytes, dsv.packed_attn_bwd_workspace_bytes):
+        with pytest.raises(ValueError, match="32 bits"):
+            f(1, 1, 1, 1, many, 64)
+    assert not calls
