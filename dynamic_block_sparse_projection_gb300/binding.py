@@ -20,7 +20,7 @@ from typing import Optional, Sequence, Tuple
 import torch
 
 _LIB_PATH = Path(__file__).resolve().parent / "_build" / "libdsv.so"
-_CALLS_PATH = _LIB_PATH.with_name("dsv_calls.so")
+_CALLS_PATH = _LIB_PATH.with_name("dsv_calls" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
 DSV_OK, DSV_ERR_INVALID_ARG, DSV_ERR_UNSUPPORTED, DSV_ERR_CUDA, DSV_ERR_BAD_INDEX, DSV_ERR_TIMEOUT, DSV_ERR_INTERNAL = range(7)
 
@@ -46,9 +46,17 @@ EXPORTS = (
 SELFTEST_WAIT_ID = 0xD5F0
 
 
+class _NoCalls:
+    """In the place of the C module where it has not been built: the calls that go through it raise, the others work."""
+
+    def __getattr__(self, name):
+        raise ImportError(f"dsv_calls is not built for this interpreter ({_CALLS_PATH}); "
+                          "run __graft_entry__.build() first")
+
+
 def _load_calls():
     if not _CALLS_PATH.exists():
-        raise ImportError(f"dsv_calls.so is not built ({_CALLS_PATH}); run __graft_entry__.build() first")
+        return _NoCalls()
     loader = importlib.machinery.ExtensionFileLoader("dsv_calls", str(_CALLS_PATH))
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("dsv_calls", loader))
     loader.exec_module(module)
@@ -56,7 +64,7 @@ def _load_calls():
 
 
 _calls = _load_calls()
-View = _calls.View            # dsv_view
+View = None if isinstance(_calls, _NoCalls) else _calls.View       # dsv_view
 
 
 class Shape(ctypes.Structure):
@@ -150,8 +158,9 @@ def _load() -> ctypes.CDLL:
     lib.dsv_version.argtypes = []
     lib.dsv_version.restype = i32
     # the calls with several structures, by C (pycalls.c): the same arguments
-    for name in ("dsv_rope_axes_fwd", "dsv_rope_axes_bwd", "dsv_packed_attn_fwd", "dsv_packed_attn_bwd"):
-        setattr(lib, name, getattr(_calls, name))
+    if View is not None:
+        for name in ("dsv_rope_axes_fwd", "dsv_rope_axes_bwd", "dsv_packed_attn_fwd", "dsv_packed_attn_bwd"):
+            setattr(lib, name, getattr(_calls, name))
     return lib
 
 

@@ -2,11 +2,14 @@
 
 One nvcc process per translation unit, run in parallel, then one link step.
 Output: dynamic_block_sparse_projection_gb300/_build/libdsv.so, and beside it the
-CPython module dsv_calls.so, linked against it.  Rebuilds only when a source or
-header is newer than the outputs.
+CPython module dsv_calls, linked against it.  The module's file name carries the
+interpreter's version and machine, so that one built for another interpreter is
+neither loaded nor taken for this one's.  Rebuilds only when a source or header
+is newer than the outputs.
 """
 from __future__ import annotations
 
+import importlib.machinery
 import os
 import shutil
 import subprocess
@@ -21,7 +24,7 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 OUT = PKG / "_build"
 LIB = OUT / "libdsv.so"
-CALLS = OUT / "dsv_calls.so"
+CALLS = OUT / ("dsv_calls" + importlib.machinery.EXTENSION_SUFFIXES[0])
 SOURCES = ["dsv_api.cu", "predict.cu", "topk.cu", "attn_fwd.cu", "attn_bwd.cu", "topk_noalloc.cu", "cube.cu",
            "predict_max.cu", "predict_topk.cu", "packed_fwd.cu", "packed_bwd.cu", "rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -74,13 +77,13 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = False)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
     os.replace(tmp, LIB)
-    tmp = OUT / "dsv_calls.so.tmp"
+    tmp = CALLS.with_name(CALLS.name + ".tmp")
     cmd = [shutil.which("gcc") or "cc", "-shared", "-fPIC", "-O2", "-I", str(INCLUDE), "-I",
            sysconfig.get_paths()["include"], str(CSRC / "pycalls.c"), "-o", str(tmp), "-L", str(OUT), "-ldsv",
            "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("building dsv_calls.so failed:\n" + r.stdout + r.stderr)
+        raise RuntimeError("building dsv_calls failed:\n" + r.stdout + r.stderr)
     os.replace(tmp, CALLS)
     return LIB
 

@@ -274,3 +274,46 @@ def test_binding_refuses_sizes_past_32_bits(fake):
         with pytest.raises(ValueError, match="32 bits"):
             f(1, 1, 1, 1, many, 64)
     assert not calls
+
+
+def test_c_module_is_that_of_this_interpreter(dsv, monkeypatch, tmp_path):
+    """The module's file carries the interpreter's tag, so one of another version neither counts as built nor is loaded."""
+    import importlib.machinery
+    import os
+    import shutil
+
+    from dynamic_block_sparse_projection_gb300 import build
+    assert build.CALLS == dsv._CALLS_PATH and build.CALLS.name == "dsv_calls" + importlib.machinery.EXTENSION_SUFFIXES[0]
+    other = tmp_path / "dsv_calls.cpython-399-other-linux-gnu.so"
+    shutil.copy(build.CALLS, other)
+    os.utime(other)
+    assert build.up_to_date()
+    monkeypatch.setattr(build, "CALLS", tmp_path / build.CALLS.name)
+    assert not build.up_to_date()
+    monkeypatch.setattr(dsv, "_CALLS_PATH", build.CALLS)
+    with pytest.raises(ImportError, match="not built for this interpreter"):
+        dsv._load_calls().row_views
+
+
+def test_calls_of_the_library_do_not_need_the_c_module(dsv, tmp_path):
+    """A tree whose C module is missing still has every call that does not go through it."""
+    import shutil
+    import subprocess
+    import sys
+    from pathlib import Path
+    pkg = Path(dsv.__file__).parent
+    shutil.copytree(pkg, tmp_path / pkg.name, ignore=shutil.ignore_patterns("dsv_calls*", "*.o", "__pycache__", "csrc"))
+    code = f"""
+import torch
+from {pkg.name} import binding as d
+assert d.status_string(0) and d.lib.dsv_version() > 0 and d.packed_attn_fwd_workspace_bytes(1, 1, 1, 1, 9000, 64) > 0
+x = torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16)
+d._need_rows = lambda *a, **k: None
+d._need = lambda *a, **k: None
+try:
+    d.rope_axes(x, torch.zeros(4, 1, dtype=torch.int32), (64,))
+except ImportError as e:
+    print(e)
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True)
+    assert r.returncode == 0 and "not built for this interpreter" in r.stdout, r.stdout + r.stderr
