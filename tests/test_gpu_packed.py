@@ -504,3 +504,14 @@ def test_packed_gradient_without_queries_checks_its_pointers(dsv):
                 rows = t[:, max(kp[s], 0):kp[s + 1]]
                 assert (rows == (7 if s == bad else 0)).all() or kp[s + 1] < kp[s]
             assert (t[:, 290:] == 7).all()
+
+
+
+def test_packed_split_over_the_keys_of_many_sequences(dsv):
+    """More split sequences than a warp has lanes: their items are counted 32 at a time."""
+    g = np.random.default_rng(17)
+    for S, H, Hkv in ((33, 4, 4), (70, 6, 2), (140, 3, 1)):
+        ql, kl = tuple(g.integers(0, 4, S)), tuple(g.choice([0, 1, 63, 128, 129, 700, 1500], S))
+        assert Hkv * S < 152 and dsv.packed_attn_fwd_workspace_bytes(S, H, Hkv, sum(ql), sum(kl), 64) > 0
+        for causal in (False, True):
+            _check(dsv, Case(H, Hkv, 64, ql, kl), causal)
