@@ -281,3 +281,37 @@ def test_rope_launched_on_a_stream_that_is_not_current(dsv):
         st.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((y, dx, dw), ref))
         del junk
+
+
+def _far_view(*tags):
+    """[2, 2, 70, 64] views whose last batch lies wholly past 2^31 elements of a buffer of 4.3 GB each."""
+    N = (1 << 23) + 4096
+    for tag in tags:
+        v = torch.empty(2, N, 2, 64, dtype=torch.bfloat16, device="cuda").transpose(1, 2)[:, :, -70:]
+        assert (v[1, 0, 0].data_ptr() - v._base.data_ptr()) // 2 >= 1 << 31
+        yield v if tag is None else v.copy_(_rand(tag, 2, 2, 70, 64))
+
+
+def test_rope_rows_past_two_to_the_31_elements(dsv):
+    """Inputs and outputs whose element offsets do not fit in 32 bits, forward and backward, with and without the norm."""
+    pos, sec = _grid_pos(1, 7, 10, 5), (20, 20, 20)
+    w = 1 + 0.25 * torch.randn(64, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    x, y = _far_view(6, None)
+    near = x.clone()
+    for weight in (None, w):
+        want = dsv.rope_axes(near, pos, sec, weight=weight)
+        assert torch.equal(dsv.rope_axes(x, pos, sec, weight=weight, out=y), want)
+    ref = oracle.rope_axes(to64(near), pos.cpu().numpy(), sec, weight=to64(w))
+    _close(y, ref, _pair_size(ref), "y")
+    dy = y.copy_(_rand(7, 2, 2, 70, 64))
+    dx, = _far_view(None)
+    assert torch.equal(dsv.rope_axes_bwd(dy, pos, sec, dx=dx), dsv.rope_axes_bwd(dy.clone(), pos, sec))
+    want, dww = dsv.rope_axes_bwd(dy.clone(), pos, sec, x=near, weight=w)
+    got, dw = dsv.rope_axes_bwd(dy, pos, sec, x=x, weight=w, dx=dx)
+    assert torch.equal(got, want) and torch.equal(dw, dww)
+    ref, _ = oracle.rope_axes_bwd(to64(dy), pos.cpu().numpy(), sec, x=to64(near), weight=to64(w))
+    x64 = to64(near)
+    r = 1 / np.sqrt((x64 ** 2).mean(-1, keepdims=True) + 1e-6)
+    g = oracle.rope_axes_bwd(to64(dy), pos.cpu().numpy(), sec)
+    size = r * (_pair_size(g * to64(w)) + np.abs(x64 * r) * np.mean(np.abs(g * to64(w) * x64 * r), -1, keepdims=True))
+    _close(got, ref, size, "dx")
