@@ -64,7 +64,10 @@ struct PackedSeq {
 
 // Sequence of a slot (tile = rows per tile, ptr = q_ptr or k_ptr), false for
 // a slot before the first sequence or a sequence whose pointers are out of
-// range (packed_check_ptrs reports those).
+// range (packed_check_ptrs reports those).  Pointers that do not rise send the
+// search anywhere, but what it returns true for is a sequence whose own
+// pointers are in range and a slot at or after its first: tiles, and the slots
+// of its rows in the workspace, stay in bounds.
 __device__ __forceinline__ bool packed_find(const PackedGeom& g, const int32_t* ptr, int tile, int slot,
                                             PackedSeq& q) {
   int lo = 0, hi = g.S - 1;
@@ -133,8 +136,8 @@ __device__ __forceinline__ int packed_items_before(const PackedGeom& g, int part
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   return n;
 }
-// Both row pointers must rise within [0, T]: one warp reports the first
-// sequence that breaks it (its tiles are skipped by packed_find).
+// Both row pointers must rise within [0, T]: one warp reports a sequence that
+// breaks it (its tiles are skipped by packed_find).
 __device__ __forceinline__ void packed_check_ptrs(const PackedGeom& g, const Ctl& ctl, int lane) {
 #pragma unroll 4
   for (int s = lane; s < g.S; s += 32) {

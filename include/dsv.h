@@ -416,9 +416,12 @@ dsv_status dsv_rope_axes_bwd(dsv_view dy, dsv_view x, const int32_t* pos, int64_
  *           (batch_stride is not read).  No output overlaps an input or
  *           another output.
  * q_ptr, k_ptr   int32 [S + 1] on the device, each rising (equal neighbours:
- *           an empty sequence) within [0, Tq] and [0, Tk].  A sequence whose
- *           pointers break this is skipped and DSV_ERR_BAD_INDEX recorded in
- *           the device error word, with the sequence as its info.
+ *           an empty sequence) within [0, Tq] and [0, Tk].  Where they do not,
+ *           DSV_ERR_BAD_INDEX is recorded in the device error word, with a
+ *           sequence whose own pointers break this as its info; that sequence
+ *           is skipped.  The call still reads and writes inside its tensors
+ *           only, but tiles are found by a search in the pointers: which rows
+ *           of the other sequences are then computed is not specified.
  *           (A forward without query tokens, or a backward without any tokens,
  *           has nothing to do and does not read them.)
  * causal    0 or 1.  softmax_scale <= 0 selects 1/sqrt(d).

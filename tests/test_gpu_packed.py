@@ -515,3 +515,35 @@ def test_packed_split_over_the_keys_of_many_sequences(dsv):
         assert Hkv * S < 152 and dsv.packed_attn_fwd_workspace_bytes(S, H, Hkv, sum(ql), sum(kl), 64) > 0
         for causal in (False, True):
             _check(dsv, Case(H, Hkv, 64, ql, kl), causal)
+
+
+
+def test_packed_overlapping_sequences_are_reported_and_stay_in_range(dsv):
+    """Pointers that fall and rise again make later sequences overlap earlier
+    ones: the call is reported, and writes rows of its own tensors only."""
+    T, H, Hkv, d = 1000, 4, 2, 64
+
+    def frame(heads, value):
+        big = torch.full((T + 64, heads + 2, d), value, dtype=torch.bfloat16, device="cuda")
+        return big, big[32:-32, 1:-1].transpose(0, 1)
+
+    for qp, kp in (((0, 1000, 50, 200, 300), (0, 300, 600, 800, 1000)),
+                   ((0, 300, 600, 800, 1000), (0, 1000, 50, 200, 300)),
+                   ((0, 900, 100, 1000), (0, 900, 100, 1000))):
+        for tq in (1000, 3):                           # 3: the keys are split
+            q_ptr = torch.tensor([v * tq // 1000 for v in qp], dtype=torch.int32, device="cuda")
+            k_ptr = torch.tensor(kp, dtype=torch.int32, device="cuda")
+            Q, K, V, dO = _rand(1, H, tq, d), _rand(2, Hkv, T, d), _rand(3, Hkv, T, d), _rand(4, H, tq, d)
+            frames = [frame(n, 7.0) for n in (H, H, Hkv, Hkv)]
+            O, dQ, dK, dV = (f[1][:, :(tq if i < 2 else T)] for i, f in enumerate(frames))
+            lse = torch.zeros(H, tq, device="cuda")
+            dsv.packed_attn_fwd(Q, K, V, q_ptr, k_ptr, causal=True, out=O, lse=lse)
+            assert dsv.device_error()[0] == dsv.DSV_ERR_BAD_INDEX
+            dsv.clear_device_error()
+            dsv.packed_attn_bwd(Q, K, V, O, dO, lse, q_ptr, k_ptr, causal=True, outs=(dQ, dK, dV))
+            assert dsv.device_error()[0] == dsv.DSV_ERR_BAD_INDEX
+            dsv.clear_device_error()
+            for (big, own), t in zip(frames, (O, dQ, dK, dV)):
+                inside = torch.zeros(big.shape[:2], dtype=torch.bool, device="cuda")
+                inside[32:32 + t.shape[1], 1:1 + t.shape[0]] = True
+                assert (big[~inside] == 7).all()
