@@ -17,9 +17,11 @@
 // Angles.  p theta^(-2i/c) in fp32 is off by p 2^-24 rad: 0.06 rad at p = 10^6.
 // Here the frequency is a 64-bit fixed-point fraction of a turn and the product
 // with the integer coordinate wraps modulo 2^64, which is modulo whole turns:
-// the fraction is exact to p 2^-56 turns (the frequency comes from fp64),
-// whatever the coordinate's size or sign, for one integer multiplication.  Its
-// top 32 bits go to sincospif.
+// the fraction is good to p 2^-54 turns (the frequency comes from fp64: 2^-54.8
+// at worst over 48 thetas and all bands), whatever the coordinate's size or
+// sign, for one integer multiplication.  Its top 32 bits go to sincospif as
+// fp32, which rounds the fraction by up to 2^-26 turns: 9e-8 rad, as much as
+// fp32 can say of an angle.
 //
 // HBM-bound: 4 bytes per element (read, write; 6 for the backward with norm)
 // at ~7 fp32 operations each.  D/8 lanes hold a token's row, 16 bytes each;

@@ -368,7 +368,8 @@ typedef struct {
  *           allowed.
  * pos       int32 [N, axes], or [B, N, axes] with pos_batch_stride = N * axes
  *           (0: shared by the batch).  Any value: an angle is worked out to
- *           |pos| * 2^-56 turns, far positions included.
+ *           |pos| * 2^-54 turns (the frequency) + 2^-25 turns (its fraction of
+ *           a turn in fp32), far positions included.
  * weight    fp32 [d], or NULL (no norm; then x, dweight and the workspace of
  *           the backward may be NULL, and eps is not read).  eps > 0.
  * workspace >= dsv_rope_axes_bwd_workspace_bytes(r) bytes, 256-byte aligned

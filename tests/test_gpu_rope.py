@@ -315,3 +315,34 @@ def test_rope_rows_past_two_to_the_31_elements(dsv):
     g = oracle.rope_axes_bwd(to64(dy), pos.cpu().numpy(), sec)
     size = r * (_pair_size(g * to64(w)) + np.abs(x64 * r) * np.mean(np.abs(g * to64(w) * x64 * r), -1, keepdims=True))
     _close(got, ref, size, "dx")
+
+
+@pytest.mark.parametrize("theta", [10000.0, 2.0, 1e6])
+def test_rope_angles_are_as_good_as_stated(dsv, theta):
+    """Sine and cosine of near and far positions, read in fp32 off the norm
+    weight's gradient of one row (x = 1, dy = 1, 0, 1, 0, ...: cos, -sin, ...).
+
+    The angle is good to 2 pi (|p| 2^-54 + 2^-25); sincospif is good to 2^-23, x^ = 1
+    by rsqrtf to 2^-22, and two products are rounded: 2^-21 together."""
+    import math
+    from decimal import Decimal, getcontext
+    getcontext().prec = 50
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582")
+    d, sec = 64, (40, 20)
+    x, dy = torch.ones(1, 1, 1, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 1, 1, d, device="cuda")
+    dy[..., 0::2] = 1
+    w = torch.ones(d, device="cuda")
+    for p in ((0, 1), (1, -1), (3, 100), (-77, 4097), (65537, -1000003), (1 << 24, (1 << 24) + 1),
+              ((1 << 31) - 1, -(1 << 31)), (123456789, -987654321)):
+        _, dw = dsv.rope_axes_bwd(dy.to(torch.bfloat16), torch.tensor([p], dtype=torch.int32, device="cuda"), sec,
+                                  theta=theta, x=x, weight=w, eps=1e-30)
+        at = 0
+        for a, c in zip(p, sec):
+            for i in range(c // 2):
+                turns = a * Decimal(theta) ** (Decimal(-2 * i) / c) / two_pi        # to 50 digits
+                ang = float(turns - turns.to_integral_value()) * 2 * math.pi
+                tol = 2 * math.pi * (abs(a) * 2.0 ** -54 + 2.0 ** -25) + 2.0 ** -21
+                got = to64(dw)[2 * (at + i):2 * (at + i) + 2]
+                assert abs(got[0] - math.cos(ang)) <= tol and abs(got[1] + math.sin(ang)) <= tol, (p, a, c, i)
+            at += c // 2
+    assert dsv.device_error()[0] == 0
