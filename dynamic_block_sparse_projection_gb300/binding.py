@@ -716,9 +716,10 @@ def rope_axes(x, pos, sections: Sequence[int], *, theta: float = 10000.0, weight
     of each row where a weight (fp32 [d]) is given; see dsv_rope_axes_fwd.
 
     sections: channels of each axis' band; pos: int32 [N, axes] or [B, N,
-    axes].  x may be any view whose last dimension is contiguous (such as the
-    transposed [B,N,H,d] of a projection).  out may be x; without it the result
-    has x's dimension order in memory."""
+    axes].  x may be a view such as the transposed [B,N,H,d] of a projection:
+    the last dimension contiguous, the other strides multiples of 8 elements, no
+    broadcast dimension.  out may be x; without it the result has x's dimension
+    order in memory."""
     r, pos_b = _rope_shape(x, "x", pos, sections, theta)
     if out is not None:
         _shape(out, "out", x.shape)
@@ -813,10 +814,10 @@ def packed_attn_fwd(Q, K, V, q_ptr, k_ptr, softmax_scale: float = 0.0, *, causal
     axis: sequence s owns the queries q_ptr[s]:q_ptr[s+1] and the keys
     k_ptr[s]:k_ptr[s+1]; see dsv_packed_attn_fwd.
 
-    Q [H,Tq,d], K and V [Hkv,Tk,d] may be any views whose last dimension is
-    contiguous (such as transposed [T,H,d] projections).  Rows outside the
-    sequences are not written: in an output that this call allocates they are
-    uninitialised."""
+    Q [H,Tq,d], K and V [Hkv,Tk,d] may be views such as transposed [T,H,d]
+    projections: the last dimension contiguous, the other strides multiples of 8
+    elements, no broadcast dimension.  Rows outside the sequences are not
+    written: in an output that this call allocates they are uninitialised."""
     p = _packed_shape(Q, K, V, q_ptr, k_ptr)
     if out is not None:
         _shape(out, "out", Q.shape)
@@ -843,7 +844,8 @@ def packed_attn_fwd(Q, K, V, q_ptr, k_ptr, softmax_scale: float = 0.0, *, causal
 def packed_attn_bwd(Q, K, V, O, dO, lse, q_ptr, k_ptr, softmax_scale: float = 0.0, *, causal: bool = False, outs=None,
                     workspace=None, stream=None):
     """(dQ [H,Tq,d], dK, dV [Hkv,Tk,d]) bf16 of packed_attn_fwd, from its O and
-    lse; see dsv_packed_attn_bwd."""
+    lse; see dsv_packed_attn_bwd.  Views and rows outside the sequences as there
+    (the gradient of a sum is a broadcast tensor: pass dO.contiguous())."""
     p = _packed_shape(Q, K, V, q_ptr, k_ptr)
     _shape(O, "O", Q.shape)
     _shape(dO, "dO", Q.shape)

@@ -29,7 +29,8 @@
 // a large library product reaches in a burst), q 960 us (1664 TFLOP/s), prepare
 // 31 us; causal, 24 heads over 8 key heads, five clips of 64 to 6000 tokens, kv
 // 380 us (1655), q 299 us (1577), prepare 27, rows 13; text (16 384 and 8192
-// tokens against 226 and 512 keys, 24 heads), prepare 49 us (HBM), the call 335.
+// tokens against 226 and 512 keys, 24 heads), prepare 49 us (HBM), kv 187, q 152
+// alone, most of it beside kv, the call 335.
 // Tensor cores bound kv and q, under the power cap when calls follow closely.
 //
 // D_i from O.  O is bf16, so dO . O is off by some 2^-9 |dO| |O| / sqrt(d).  Over
@@ -1370,7 +1371,10 @@ cudaError_t launch_t(const PackedMaps& m, const PackedGeom& g, const dsv_view& O
 // so what counts is when both are done: worked out below for n that fill half
 // an SM's rounds, in microseconds at d = 128 (a pair of tiles 1.4 and 1.0, a
 // CTA's start 5 and 4, the join 4 and 0.033 for each run's 131 KB), the lengths, which the host does not know,
-// taken half-way between equal ones and a single long one.  Measured with and
+// taken half-way between equal ones and a single long one.  It ranks the choices
+// of n and no more: for the text call below it says 459 us whole and 476 in two,
+// as it takes an item of dQ for 4.5 key tiles where those have two and four.
+// The constants decide d = 64 as well, where they were not measured.  Measured with and
 // without runs: 24 heads of two clips against 226 and 512 keys 344 / 315 us, 2
 // heads of one clip of 4000 83 / 57 us, but one head of 20 000 against 300 keys
 // 41 / 225 us, three heads over one of three clips up to 5095 72 / 156 us.

@@ -37,9 +37,9 @@
 // Measured, d = 128: 24 heads of 16 384 tokens 2050 us alone (1609 TFLOP/s, 86 % of
 // what a large library product reaches in a burst), 2250 us back to back under
 // the power cap; causal, 24 heads over 8 key heads, eight clips of 1 to 8191
-// tokens, 430 us (1481 TFLOP/s of the tiles it multiplies); one new token of
-// eight streams against up to 30 720 keys each, 63 us (6.1 TB/s), 67 with the
-// join.  Long clips are bound by the softmax warps' chain beside the products,
+// tokens, 422 us (1509 TFLOP/s of the tiles it multiplies); one new token of
+// eight streams against up to 30 720 keys each, 62 us (6.2 TB/s), 68 a call with
+// the join.  Long clips are bound by the softmax warps' chain beside the products,
 // single tokens by HBM.
 //
 // Split over the keys.  Each part writes its normalised O (fp32) and base-2

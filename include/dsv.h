@@ -415,7 +415,8 @@ dsv_status dsv_rope_axes_bwd(dsv_view dy, dsv_view x, const int32_t* pos, int64_
  *
  * Q, O, dO, dQ   views of [H, Tq, d];  K, V, dK, dV  views of [Hkv, Tk, d]
  *           (batch_stride is not read).  No output overlaps an input or
- *           another output.
+ *           another output.  |V| < 2^39: weights are held against an earlier
+ *           maximum of the row, up to 2^64 times it, and summed in fp32.
  * q_ptr, k_ptr   int32 [S + 1] on the device, each rising (equal neighbours:
  *           an empty sequence) within [0, Tq] and [0, Tk].  Where they do not,
  *           DSV_ERR_BAD_INDEX is recorded in the device error word, with a
