@@ -42,6 +42,8 @@ EXPORTS = (
     "dsv_rope_axes_fwd", "dsv_rope_axes_bwd_workspace_bytes", "dsv_rope_axes_bwd",
     "dsv_packed_attn_fwd_workspace_bytes", "dsv_packed_attn_fwd",
     "dsv_packed_attn_bwd_workspace_bytes", "dsv_packed_attn_bwd",
+    "dsv_layer_norm_fwd", "dsv_layer_norm_bwd_workspace_bytes", "dsv_layer_norm_bwd",
+    "dsv_quantize_fp8", "dsv_matmul_fp8",
 )
 SELFTEST_WAIT_ID = 0xD5F0
 
@@ -65,6 +67,10 @@ def _load_calls():
 
 _calls = _load_calls()
 View = None if isinstance(_calls, _NoCalls) else _calls.View       # dsv_view
+Rows = None if isinstance(_calls, _NoCalls) else _calls.Rows       # dsv_rows
+DSV_BF16, DSV_F32, DSV_E4M3, DSV_E5M2 = range(4)                   # dsv_type
+if Rows is not None:
+    _calls.set_types(torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.float8_e5m2)
 
 
 class Shape(ctypes.Structure):
@@ -80,6 +86,15 @@ class Rope(ctypes.Structure):
 class Packed(ctypes.Structure):
     _fields_ = [("S", ctypes.c_int32), ("H", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("Tq", ctypes.c_int32),
                 ("Tk", ctypes.c_int32), ("d", ctypes.c_int32)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("C", ctypes.c_int32), ("S", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class Matmul(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("a_rows", ctypes.c_int32),
+                ("b_rows", ctypes.c_int32), ("accumulate", ctypes.c_int32)]
 
 
 class DsvError(RuntimeError):
@@ -155,11 +170,14 @@ def _load() -> ctypes.CDLL:
     lib.dsv_packed_attn_fwd_workspace_bytes.restype = sz
     lib.dsv_packed_attn_bwd_workspace_bytes.argtypes = [Packed]
     lib.dsv_packed_attn_bwd_workspace_bytes.restype = sz
+    lib.dsv_layer_norm_bwd_workspace_bytes.argtypes = [Norm]
+    lib.dsv_layer_norm_bwd_workspace_bytes.restype = sz
     lib.dsv_version.argtypes = []
     lib.dsv_version.restype = i32
     # the calls with several structures, by C (pycalls.c): the same arguments
     if View is not None:
-        for name in ("dsv_rope_axes_fwd", "dsv_rope_axes_bwd", "dsv_packed_attn_fwd", "dsv_packed_attn_bwd"):
+        for name in ("dsv_rope_axes_fwd", "dsv_rope_axes_bwd", "dsv_packed_attn_fwd", "dsv_packed_attn_bwd",
+                     "dsv_layer_norm_fwd", "dsv_layer_norm_bwd", "dsv_quantize_fp8", "dsv_matmul_fp8"):
             setattr(lib, name, getattr(_calls, name))
     return lib
 
@@ -869,6 +887,243 @@ def packed_attn_bwd(Q, K, V, O, dO, lse, q_ptr, k_ptr, softmax_scale: float = 0.
           q_ptr.data_ptr(), k_ptr.data_ptr(), 1 if causal else 0, softmax_scale, vdq, vdk, vdv, _ptr(ws), nbytes,
           _stream(dev, stream))
     return outs
+
+
+# ---------------------------------------------------------------------------
+# Layer norm, 8-bit quantiser and product
+# ---------------------------------------------------------------------------
+
+def _need_matrix(t, name: str, dtypes, device: Optional[torch.device] = None) -> None:
+    """t is a 2D CUDA tensor of one of the dtypes with contiguous rows; the library checks its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got shape {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.stride(1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+_BF16, _REAL, _FP8 = (torch.bfloat16,), (torch.bfloat16, torch.float32), (torch.float8_e4m3fn, torch.float8_e5m2)
+
+
+def _matrices(device: torch.device, index: int, **tensors):
+    """dsv_rows of (tensor, its allowed dtypes) pairs (a None tensor: null)."""
+    for name, (t, dtypes) in tensors.items():
+        if t is not None and t.dtype not in dtypes:
+            _need_matrix(t, name, dtypes, device)
+    rows = _calls.matrices(index, *[t for t, _ in tensors.values()])
+    if rows is None:
+        for name, (t, dtypes) in tensors.items():
+            if t is not None:
+                _need_matrix(t, name, dtypes, device)
+        raise ValueError("the tensors must be matrices on one device: " + ", ".join(tensors))
+    return rows
+
+
+@functools.lru_cache(maxsize=64)
+def _norm(T: int, C: int, S: int, eps: float) -> Norm:
+    _fit32(T=T, C=C, S=S)
+    return Norm(T, C, S, eps)
+
+
+def _norm_shape(x, weight, seq_ptr, eps: float) -> Norm:
+    T, C = _dims(x, "x", 2)
+    S = 1
+    if seq_ptr is not None:
+        S = _dims(seq_ptr, "seq_ptr", 1)[0] - 1
+        if S < 0:
+            raise ValueError("seq_ptr must hold at least one element")
+        if weight is not None:
+            _shape(weight, "weight", (S, C))
+    elif weight is not None:
+        if not isinstance(weight, torch.Tensor):
+            raise TypeError("weight must be a torch.Tensor")
+        if weight.dim() == 2:
+            S = weight.shape[0]
+            _shape(weight, "weight", (S, C))
+            if S < 1 or T % S != 0:
+                raise ValueError(f"{T} rows do not divide into {S} sequences of equal lengths: pass seq_ptr")
+        else:
+            _shape(weight, "weight", (C,))
+    return _norm(T, C, S, eps)
+
+
+def layer_norm(x, weight=None, bias=None, seq_ptr=None, *, eps: float = 1e-6, out=None, stats=None,
+               stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(y bf16 [T,C], stats fp32 [2,T]: mean, 1/deviation) of the rows of x, bf16
+    or fp32 [T,C] with any row stride; see dsv_layer_norm_fwd.
+
+    weight and bias: fp32 [C], or [S,C] with a row for each sequence: sequence s
+    owns the rows seq_ptr[s]:seq_ptr[s+1] (int32 [S+1]), or without seq_ptr the
+    s-th part of T/S rows.  Rows outside the sequences are not written: in an
+    output that this call allocates they are uninitialised.  out may be x."""
+    p = _norm_shape(x, weight, seq_ptr, eps)
+    if bias is not None:
+        if weight is None:
+            raise ValueError("bias without a weight")
+        _shape(bias, "bias", weight.shape)
+    if out is not None:
+        _shape(out, "out", x.shape)
+    if stats is not None:
+        _shape(stats, "stats", (2, p.T))
+    _need_matrix(x, "x", _REAL)
+    dev, at = x.device, x.get_device()
+    _need_on(dev, at, torch.float32, weight=weight, bias=bias, stats=stats)
+    if seq_ptr is not None:
+        _need_on(dev, at, torch.int32, seq_ptr=seq_ptr)
+    with _alloc_on(stream):
+        if out is None:
+            out = torch.empty(p.T, p.C, dtype=torch.bfloat16, device=dev)
+        if stats is None:
+            stats = torch.empty(2, p.T, dtype=torch.float32, device=dev)
+    vx, vy = _matrices(dev, at, x=(x, _REAL), out=(out, _BF16))
+    _call(lib.dsv_layer_norm_fwd, "dsv_layer_norm_fwd", dev, vx, p, _ptr(seq_ptr), _ptr(weight), _ptr(bias), vy,
+          stats.data_ptr(), _stream(dev, stream))
+    return out, stats
+
+
+def layer_norm_bwd_workspace_bytes(T: int, C: int, S: int = 1) -> int:
+    return int(lib.dsv_layer_norm_bwd_workspace_bytes(_norm(T, C, S, 1e-6)))
+
+
+def layer_norm_bwd(dy, x, stats, weight=None, seq_ptr=None, *, dx=None, dweight=None, dbias=None, workspace=None,
+                   stream=None):
+    """Gradient of layer_norm from its input x and stats: dx (x's type), or with a
+    weight (dx, dweight, dbias fp32 of the weight's shape); see
+    dsv_layer_norm_bwd.  dx may be dy or x."""
+    p = _norm_shape(x, weight, seq_ptr, 1e-6)
+    _shape(dy, "dy", x.shape)
+    _shape(stats, "stats", (2, p.T))
+    if dx is not None:
+        _shape(dx, "dx", x.shape)
+    for name, t in (("dweight", dweight), ("dbias", dbias)):
+        if t is not None:
+            if weight is None:
+                raise ValueError(f"{name} without a weight")
+            _shape(t, name, weight.shape)
+    _need_matrix(x, "x", _REAL)
+    dev, at = x.device, x.get_device()
+    _need_on(dev, at, torch.float32, stats=stats, weight=weight, dweight=dweight, dbias=dbias)
+    if seq_ptr is not None:
+        _need_on(dev, at, torch.int32, seq_ptr=seq_ptr)
+    nbytes, ws = 0, None
+    with _alloc_on(stream):
+        if dx is None:
+            dx = torch.empty(p.T, p.C, dtype=x.dtype, device=dev)
+        if weight is not None:
+            if dweight is None:
+                dweight = torch.empty(weight.shape, dtype=torch.float32, device=dev)
+            if dbias is None:
+                dbias = torch.empty(weight.shape, dtype=torch.float32, device=dev)
+            nbytes = lib.dsv_layer_norm_bwd_workspace_bytes(p)
+            ws = _scratch(nbytes, dev, workspace)
+    vdy, vx, vdx = _matrices(dev, at, dy=(dy, _BF16), x=(x, _REAL), dx=(dx, (x.dtype,)))
+    _call(lib.dsv_layer_norm_bwd, "dsv_layer_norm_bwd", dev, vdy, vx, stats.data_ptr(), p, _ptr(seq_ptr), _ptr(weight),
+          vdx, _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes, _stream(dev, stream))
+    return dx if weight is None else (dx, dweight, dbias)
+
+
+def _fp8_matrix(R: int, C: int, dtype: torch.dtype, device) -> torch.Tensor:
+    """[R, C] with rows a multiple of 16 bytes apart."""
+    t = torch.empty(R, (C + 15) // 16 * 16, dtype=dtype, device=device)
+    return t if C % 16 == 0 else t[:, :C]
+
+
+def quantize_fp8(x, *, rows: int = 1, transpose: bool = False, dtype: torch.dtype = torch.float8_e4m3fn, outs=None,
+                 stream=None):
+    """(q, scale) of x, bf16 or fp32 [R,C] with any row stride: 8-bit floating
+    point with a power-of-two scale for each block of 128 columns of one row
+    (rows=1) or of 128 rows (rows=128); see dsv_quantize_fp8.
+
+    q [R,C] of `dtype` (float8_e4m3fn or float8_e5m2), its rows a multiple of 16
+    bytes apart; scale fp32 [ceil(C/128), R] or [ceil(C/128), ceil(R/128)].  With
+    transpose (q, scale, qt, scale_t): also the transposed matrix [C,R] with its
+    own blocks along R.  outs: those tensors."""
+    R, C = _dims(x, "x", 2)
+    if rows not in (1, 128):
+        raise ValueError(f"rows is {rows}, expected 1 or 128")
+    if dtype not in _FP8:
+        raise TypeError(f"dtype must be {_FP8[0]} or {_FP8[1]}, got {dtype}")
+    cb, rb = (C + 127) // 128, (R + 127) // 128
+    shapes = ((R, C), (cb, R if rows == 1 else rb), (C, R), (rb, C if rows == 1 else cb))
+    if outs is not None:
+        names = ("q", "scale", "qt", "scale_t")[:4 if transpose else 2]
+        if len(outs) != len(names):
+            raise ValueError(f"outs must be ({', '.join(names)})")
+        for name, t, shape in zip(names, outs, shapes):
+            _shape(t, name, shape)
+    _need_matrix(x, "x", _REAL)
+    dev, at = x.device, x.get_device()
+    if outs is None:
+        with _alloc_on(stream):
+            outs = (_fp8_matrix(R, C, dtype, dev), torch.empty(shapes[1], dtype=torch.float32, device=dev))
+            if transpose:
+                outs += (_fp8_matrix(C, R, dtype, dev), torch.empty(shapes[3], dtype=torch.float32, device=dev))
+    qt, scale_t = (outs[2], outs[3]) if transpose else (None, None)
+    _need_on(dev, at, torch.float32, scale=outs[1], scale_t=scale_t)
+    vx, vq, vqt = _matrices(dev, at, x=(x, _REAL), q=(outs[0], (dtype,)), qt=(qt, (dtype,)))
+    _call(lib.dsv_quantize_fp8, "dsv_quantize_fp8", dev, vx, R, C, rows, vq, outs[1].data_ptr(), vqt, _ptr(scale_t),
+          _stream(dev, stream))
+    return outs
+
+
+@functools.lru_cache(maxsize=64)
+def _matmul(M: int, N: int, K: int, a_rows: int, b_rows: int, accumulate: int) -> Matmul:
+    _fit32(M=M, N=N, K=K)
+    return Matmul(M, N, K, a_rows, b_rows, accumulate)
+
+
+def _scale_rows(scale, name: str, R: int, K: int) -> int:
+    """The rows of a block that the scale's shape stands for."""
+    kb, got = (K + 127) // 128, _dims(scale, name, 2)
+    for rows in (1, 128):
+        if got == (kb, -(-R // rows)):
+            return rows
+    raise ValueError(f"{name} has shape {got}, expected {(kb, R)} or {(kb, -(-R // 128))}")
+
+
+def matmul_fp8(a, a_scale, b, b_scale, *, out_dtype: torch.dtype = torch.bfloat16, out=None, accumulate: bool = False,
+               stream=None) -> torch.Tensor:
+    """[M,N] = a b^T of 8-bit matrices a [M,K] and b [N,K] as quantize_fp8 makes
+    them (e4m3 or e5m2 each, rows a multiple of 16 bytes apart) with fp32 scales
+    [ceil(K/128), rows] or [ceil(K/128), ceil(rows/128)]; see dsv_matmul_fp8.
+
+    out_dtype: bf16 or fp32, or that of `out` [M,N] (any row stride).
+    accumulate: adds to `out` (fp32).  A projection y = x w^T and its gradients:
+        y  = matmul_fp8(*quantize_fp8(x), *quantize_fp8(w, rows=128))
+        dx = matmul_fp8(*quantize_fp8(dy), wt, wt_scale)          # w's transposed copy
+        dw = matmul_fp8(dyt, dyt_scale, xt, xt_scale)             # both transposed copies"""
+    M, K = _dims(a, "a", 2)
+    N, Kb = _dims(b, "b", 2)
+    if Kb != K:
+        raise ValueError(f"b has {Kb} columns, expected {K}")
+    p = _matmul(M, N, K, _scale_rows(a_scale, "a_scale", M, K), _scale_rows(b_scale, "b_scale", N, K),
+                1 if accumulate else 0)
+    if out is not None:
+        _shape(out, "out", (M, N))
+        out_dtype = out.dtype
+    elif accumulate:
+        raise ValueError("accumulate needs out")
+    if out_dtype not in _REAL:
+        raise TypeError(f"out must be {_REAL[0]} or {_REAL[1]}, got {out_dtype}")
+    if accumulate and out_dtype != torch.float32:
+        raise TypeError("accumulate needs an fp32 out")
+    _need_matrix(a, "a", _FP8)
+    dev, at = a.device, a.get_device()
+    _need_on(dev, at, torch.float32, a_scale=a_scale, b_scale=b_scale)
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty(M, N, dtype=out_dtype, device=dev)
+    va, vb, vc = _matrices(dev, at, a=(a, _FP8), b=(b, _FP8), out=(out, (out_dtype,)))
+    _call(lib.dsv_matmul_fp8, "dsv_matmul_fp8", dev, va, a_scale.data_ptr(), vb, b_scale.data_ptr(), p, vc,
+          _stream(dev, stream))
+    return out
 
 
 # ---------------------------------------------------------------------------

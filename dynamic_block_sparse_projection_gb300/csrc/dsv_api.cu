@@ -247,6 +247,44 @@ dsv_status check_rope(const dsv_rope& r) {
 bool empty_rope(const dsv_rope& r) { return r.B == 0 || r.H == 0 || r.N == 0; }
 bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Matrices of the calls behind the packed attention.
+int size_of(int type) { return type == DSV_F32 ? 4 : type == DSV_BF16 ? 2 : 1; }
+bool real_type(const dsv_rows& v) { return v.type == DSV_BF16 || v.type == DSV_F32; }
+bool fp8_type(const dsv_rows& v) { return v.type == DSV_E4M3 || v.type == DSV_E5M2; }
+bool rows_ok(const dsv_rows& v, long long rows, long long cols) {
+  if (!v.ptr || reinterpret_cast<uintptr_t>(v.ptr) % size_of(v.type) != 0) return false;
+  return rows <= 1 || (v.stride >= cols && v.stride < kMaxStride);
+}
+bool fp8_ok(const dsv_rows& v, long long rows, long long cols) {
+  return fp8_type(v) && rows_ok(v, rows, cols) && al16(v.ptr) && (rows <= 1 || v.stride % 16 == 0);
+}
+// The same rows as `a`, where both start at the same address.
+bool same_or_apart(const dsv_rows& a, const dsv_rows& b, long long rows) {
+  return a.ptr != b.ptr || (a.type == b.type && (rows <= 1 || a.stride == b.stride));
+}
+
+dsv_status check_norm(const dsv_norm& p) {
+  if (p.T < 0 || p.C < 0 || p.S < 0) return DSV_ERR_INVALID_ARG;
+  if (p.T >= (1 << 30) || p.C < 1 || p.C > 16384 || p.S > 65535) return DSV_ERR_UNSUPPORTED;
+  return DSV_OK;
+}
+
+// 2D map over a [rows, cols] matrix of bytes, box = [box_rows, 128 bytes], 128-byte swizzle.
+cudaError_t make_map_bytes(CUtensorMap* map, const dsv_rows& v, long long rows, long long cols, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  cudaError_t e = get_encode(&enc);
+  if (e != cudaSuccess) return e;
+  // the stride of a single row is never used: any valid one will do
+  const long long stride = rows > 1 ? v.stride : (cols + 15) / 16 * 16;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)stride};
+  cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1u, 1u};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, v.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 bool empty(const dsv_shape& s) { return (long long)s.B * s.H * s.N == 0; }
 
 float resolve_scale(const dsv_shape& s, float scale) {
@@ -787,6 +825,91 @@ dsv_status dsv_rope_axes_bwd(dsv_view dy, dsv_view x, const int32_t* pos, int64_
   }
   return from_cuda(launch_rope_bwd(dy, x, pos, pos_batch_stride, r, weight, eps, dx, dweight, workspace,
                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dsv_status dsv_layer_norm_fwd(dsv_rows x, dsv_norm p, const int32_t* seq_ptr, const float* weight, const float* bias,
+                              dsv_rows y, float* stats, dsv_stream_t stream) {
+  dsv_status v = check_norm(p);
+  if (v != DSV_OK) return v;
+  if (!(p.eps > 0.f) || !isfinite(p.eps) || !al4(seq_ptr) || !al4(weight) || !al4(bias)) return DSV_ERR_INVALID_ARG;
+  if ((bias && !weight) || (!seq_ptr && (p.S == 0 || p.T % p.S != 0))) return DSV_ERR_INVALID_ARG;
+  if (p.T == 0 || p.S == 0) return DSV_OK;
+  if (!real_type(x) || y.type != DSV_BF16 || !stats || !al4(stats)) return DSV_ERR_INVALID_ARG;
+  if (!rows_ok(x, p.T, p.C) || !rows_ok(y, p.T, p.C) || !same_or_apart(x, y, p.T)) return DSV_ERR_INVALID_ARG;
+  Ctl ctl;
+  if (current_ctl(&ctl) != cudaSuccess) return DSV_ERR_CUDA;
+  return from_cuda(
+      launch_norm_fwd(x, p, seq_ptr, weight, bias, y, stats, ctl, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t dsv_layer_norm_bwd_workspace_bytes(dsv_norm p) {
+  if (check_norm(p) != DSV_OK || p.T == 0 || p.S == 0) return 0;
+  return norm_bwd_ws_bytes(p);
+}
+
+dsv_status dsv_layer_norm_bwd(dsv_rows dy, dsv_rows x, const float* stats, dsv_norm p, const int32_t* seq_ptr,
+                              const float* weight, dsv_rows dx, float* dweight, float* dbias, void* workspace,
+                              size_t workspace_bytes, dsv_stream_t stream) {
+  dsv_status v = check_norm(p);
+  if (v != DSV_OK) return v;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (!al4(seq_ptr) || !al4(weight) || !al4(dweight) || !al4(dbias)) return DSV_ERR_INVALID_ARG;
+  if ((weight && (!dweight || !dbias)) || (!seq_ptr && (p.S == 0 || p.T % p.S != 0))) return DSV_ERR_INVALID_ARG;
+  if (!weight) dweight = dbias = nullptr;
+  if (p.T == 0 || p.S == 0) {              // no rows: the sums over them are zero
+    if (!weight || p.S == 0) return DSV_OK;
+    const size_t bytes = (size_t)p.S * p.C * sizeof(float);
+    cudaError_t e = cudaMemsetAsync(dweight, 0, bytes, st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, bytes, st);
+    return from_cuda(e);
+  }
+  if (!real_type(x) || dx.type != x.type || dy.type != DSV_BF16 || !stats || !al4(stats)) return DSV_ERR_INVALID_ARG;
+  if (!rows_ok(x, p.T, p.C) || !rows_ok(dy, p.T, p.C) || !rows_ok(dx, p.T, p.C)) return DSV_ERR_INVALID_ARG;
+  if (!same_or_apart(x, dx, p.T) || !same_or_apart(dy, dx, p.T)) return DSV_ERR_INVALID_ARG;
+  if (weight && (!workspace || !al256(workspace) || workspace_bytes < norm_bwd_ws_bytes(p))) return DSV_ERR_INVALID_ARG;
+  Ctl ctl;
+  if (current_ctl(&ctl) != cudaSuccess) return DSV_ERR_CUDA;
+  return from_cuda(launch_norm_bwd(dy, x, stats, p, seq_ptr, weight, dx, dweight, dbias, workspace, ctl, st));
+}
+
+dsv_status dsv_quantize_fp8(dsv_rows x, int32_t R, int32_t C, int32_t rows, dsv_rows q, float* scale, dsv_rows qt,
+                            float* scale_t, dsv_stream_t stream) {
+  if (R < 0 || C < 0 || (rows != 1 && rows != 128)) return DSV_ERR_INVALID_ARG;
+  if (R >= INT32_MAX - 128 || C >= INT32_MAX - 128) return DSV_ERR_UNSUPPORTED;
+  if (((long long)R + 127) / 128 * (((long long)C + 127) / 128) > INT32_MAX) return DSV_ERR_UNSUPPORTED;
+  if (R == 0 || C == 0) return DSV_OK;
+  if (!real_type(x) || !rows_ok(x, R, C) || !fp8_ok(q, R, C) || !scale || !al4(scale)) return DSV_ERR_INVALID_ARG;
+  if (qt.ptr && (!fp8_ok(qt, C, R) || qt.type != q.type || !scale_t || !al4(scale_t) || qt.ptr == q.ptr))
+    return DSV_ERR_INVALID_ARG;
+  if (q.ptr == x.ptr || qt.ptr == x.ptr) return DSV_ERR_INVALID_ARG;
+  return from_cuda(launch_quantize(x, R, C, rows, q, scale, qt, scale_t, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dsv_status dsv_matmul_fp8(dsv_rows a, const float* a_scale, dsv_rows b, const float* b_scale, dsv_matmul p, dsv_rows c,
+                          dsv_stream_t stream) {
+  if (p.M < 0 || p.N < 0 || p.K < 0) return DSV_ERR_INVALID_ARG;
+  if ((p.a_rows != 1 && p.a_rows != 128) || (p.b_rows != 1 && p.b_rows != 128)) return DSV_ERR_INVALID_ARG;
+  if (p.accumulate != 0 && p.accumulate != 1) return DSV_ERR_INVALID_ARG;
+  const int most = INT32_MAX - 256;
+  if (p.M > most || p.N > most || p.K > most) return DSV_ERR_UNSUPPORTED;
+  if (((long long)p.M + 127) / 128 * (((long long)p.N + 127) / 128) > INT32_MAX) return DSV_ERR_UNSUPPORTED;
+  if (p.M == 0 || p.N == 0) return DSV_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (!real_type(c) || !rows_ok(c, p.M, p.N) || (p.accumulate && c.type != DSV_F32)) return DSV_ERR_INVALID_ARG;
+  if (p.K == 0) {                          // the sum over nothing
+    if (p.accumulate) return DSV_OK;
+    const size_t size = (size_t)size_of(c.type), width = (size_t)p.N * size;
+    return from_cuda(cudaMemset2DAsync(c.ptr, p.M > 1 ? (size_t)c.stride * size : width, 0, width, (size_t)p.M, st));
+  }
+  if (!fp8_ok(a, p.M, p.K) || !fp8_ok(b, p.N, p.K)) return DSV_ERR_INVALID_ARG;
+  if (!a_scale || !b_scale || !al4(a_scale) || !al4(b_scale)) return DSV_ERR_INVALID_ARG;
+  if (c.ptr == a.ptr || c.ptr == b.ptr) return DSV_ERR_INVALID_ARG;
+  Ctl ctl;
+  if (current_ctl(&ctl) != cudaSuccess) return DSV_ERR_CUDA;
+  CUtensorMap ta, tb;
+  if (make_map_bytes(&ta, a, p.M, p.K, 128) != cudaSuccess || make_map_bytes(&tb, b, p.N, p.K, 128) != cudaSuccess)
+    return DSV_ERR_CUDA;
+  return from_cuda(launch_matmul_fp8(ta, tb, p, a.type == DSV_E5M2, b.type == DSV_E5M2, a_scale, b_scale, c, ctl, st));
 }
 
 }  // extern "C"

@@ -522,6 +522,7 @@ enum : unsigned int {
   KID_PACKED_KV = 7,
   KID_PACKED_Q = 8,
   KID_PACKED_ROWS = 9,
+  KID_MATMUL = 10,
 };
 
 }  // namespace dsv

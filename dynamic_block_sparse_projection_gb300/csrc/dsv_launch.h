@@ -130,6 +130,21 @@ cudaError_t launch_packed_bwd(const PackedMaps& m, const dsv_packed& p, const in
                               cudaStream_t st);
 size_t packed_bwd_ws_bytes(const dsv_packed& p);
 
+// Layer norm (norm.cu).  dweight and dbias (and ws) only with a weight.
+cudaError_t launch_norm_fwd(const dsv_rows& x, const dsv_norm& p, const int32_t* ptr, const float* weight,
+                            const float* bias, const dsv_rows& y, float* stats, const Ctl& ctl, cudaStream_t st);
+size_t norm_bwd_ws_bytes(const dsv_norm& p);
+cudaError_t launch_norm_bwd(const dsv_rows& dy, const dsv_rows& x, const float* stats, const dsv_norm& p,
+                            const int32_t* ptr, const float* weight, const dsv_rows& dx, float* dweight, float* dbias,
+                            void* ws, const Ctl& ctl, cudaStream_t st);
+
+// 8-bit quantiser and product (quantize.cu, matmul_fp8.cu).  Tensor maps of the
+// product: [rows, K] bytes, boxes of 128 bytes x the tile's rows.
+cudaError_t launch_quantize(const dsv_rows& x, int R, int C, int rows, const dsv_rows& q, float* scale,
+                            const dsv_rows& qt, float* scale_t, cudaStream_t st);
+cudaError_t launch_matmul_fp8(const CUtensorMap& tmA, const CUtensorMap& tmB, const dsv_matmul& p, bool a_e5, bool b_e5,
+                              const float* sa, const float* sb, const dsv_rows& c, const Ctl& ctl, cudaStream_t st);
+
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace dsv

@@ -131,8 +131,127 @@ static PyObject* row_views(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 // ---------------------------------------------------------------------------
+// dsv_rows
+// ---------------------------------------------------------------------------
+typedef struct {
+  PyObject_HEAD
+  dsv_rows v;
+} Rows;
+static PyTypeObject RowsType;
+static PyObject* types[4];               // the dtypes of dsv_type, in its order (set_types)
+
+static PyObject* rows_make(void* ptr, int64_t stride, int32_t type) {
+  Rows* o = PyObject_New(Rows, &RowsType);
+  if (o == NULL) return NULL;
+  o->v.ptr = ptr;
+  o->v.stride = stride;
+  o->v.type = type;
+  return (PyObject*)o;
+}
+static PyObject* rows_new(PyTypeObject* type, PyObject* args, PyObject* kw) {
+  PyObject* address;
+  long long stride;
+  int of;
+  void* ptr;
+  if (kw != NULL && PyDict_GET_SIZE(kw) != 0) {
+    PyErr_SetString(PyExc_TypeError, "Rows(ptr, stride, type)");
+    return NULL;
+  }
+  if (!PyArg_ParseTuple(args, "OLi", &address, &stride, &of) || !address_of(address, &ptr)) return NULL;
+  return rows_make(ptr, stride, of);
+}
+static PyObject* rows_ptr(PyObject* o, void* unused) {
+  void* p = ((Rows*)o)->v.ptr;
+  if (p == NULL) Py_RETURN_NONE;
+  return PyLong_FromUnsignedLongLong((unsigned long long)(uintptr_t)p);
+}
+static PyMemberDef rows_members[] = {{"stride", T_LONGLONG, offsetof(Rows, v.stride), READONLY, NULL},
+                                     {"type", T_INT, offsetof(Rows, v.type), READONLY, NULL},
+                                     {NULL, 0, 0, 0, NULL}};
+static PyGetSetDef rows_getset[] = {{"ptr", rows_ptr, NULL, NULL, NULL}, {NULL, NULL, NULL, NULL, NULL}};
+static PyTypeObject RowsType = {
+    PyVarObject_HEAD_INIT(NULL, 0).tp_name = "dsv_calls.Rows",
+    .tp_basicsize = sizeof(Rows),
+    .tp_flags = Py_TPFLAGS_DEFAULT,
+    .tp_doc = "dsv_rows: the address, row stride and type of a matrix",
+    .tp_new = rows_new,
+    .tp_dealloc = view_free,
+    .tp_members = rows_members,
+    .tp_getset = rows_getset,
+};
+static PyObject* set_types(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  if (n != 4) {
+    PyErr_SetString(PyExc_TypeError, "set_types(bf16, f32, e4m3, e5m2)");
+    return NULL;
+  }
+  for (int i = 0; i < 4; ++i) {
+    Py_INCREF(a[i]);
+    Py_XDECREF(types[i]);
+    types[i] = a[i];
+  }
+  Py_RETURN_NONE;
+}
+// The rows of a 2D tensor, NULL without an error set where its type, device or
+// last stride is another than a matrix has.
+static PyObject* rows_of_tensor(PyObject* t, long index) {
+  PyObject* got = PyObject_GetAttr(t, s_dtype);
+  if (got == NULL) return NULL;
+  int type = 0;
+  while (type < 4 && got != types[type]) ++type;
+  Py_DECREF(got);
+  if (type == 4) return NULL;
+  if ((got = PyObject_CallMethodNoArgs(t, s_get_device)) == NULL) return NULL;
+  const long at = PyLong_AsLong(got);
+  Py_DECREF(got);
+  if (at != index || PyErr_Occurred()) return NULL;
+  PyObject* st = PyObject_CallMethodNoArgs(t, s_stride);
+  if (st == NULL) return NULL;
+  PyObject* made = NULL;
+  if (PyTuple_Check(st) && PyTuple_GET_SIZE(st) == 2) {
+    const long long r = PyLong_AsLongLong(PyTuple_GET_ITEM(st, 0)), c = PyLong_AsLongLong(PyTuple_GET_ITEM(st, 1));
+    if (!PyErr_Occurred() && c == 1 && (got = PyObject_CallMethodNoArgs(t, s_data_ptr)) != NULL) {
+      void* ptr;
+      if (address_of(got, &ptr)) made = rows_make(ptr, r, type);
+      Py_DECREF(got);
+    }
+  }
+  Py_DECREF(st);
+  return made;
+}
+// matrices(index, *tensors): a tuple of their rows (None: null), or None where
+// one of them is not a matrix of a known type on device `index` with
+// contiguous rows.
+static PyObject* matrices(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  if (n < 1) {
+    PyErr_SetString(PyExc_TypeError, "matrices(index, *tensors)");
+    return NULL;
+  }
+  const long index = PyLong_AsLong(a[0]);
+  if (index == -1 && PyErr_Occurred()) return NULL;
+  PyObject* all = PyTuple_New(n - 1);
+  for (Py_ssize_t i = 1; all != NULL && i < n; ++i) {
+    PyObject* v = a[i] == Py_None ? rows_make(NULL, 0, 0) : rows_of_tensor(a[i], index);
+    if (v == NULL) {
+      Py_DECREF(all);
+      if (PyErr_Occurred()) return NULL;
+      Py_RETURN_NONE;
+    }
+    PyTuple_SET_ITEM(all, i - 1, v);
+  }
+  return all;
+}
+
+// ---------------------------------------------------------------------------
 // Arguments
 // ---------------------------------------------------------------------------
+static int rows_of(PyObject* o, dsv_rows* v) {
+  if (Py_TYPE(o) != &RowsType) {
+    PyErr_Format(PyExc_TypeError, "expected Rows, got %.80s", Py_TYPE(o)->tp_name);
+    return 0;
+  }
+  *v = ((Rows*)o)->v;
+  return 1;
+}
 static int view_of(PyObject* o, dsv_view* v) {
   if (Py_TYPE(o) != &ViewType) {
     PyErr_Format(PyExc_TypeError, "expected a View, got %.80s", Py_TYPE(o)->tp_name);
@@ -257,16 +376,82 @@ static PyObject* packed_attn_bwd(PyObject* self, PyObject* const* a, Py_ssize_t 
   return PyLong_FromLong(st);
 }
 
+static PyObject* layer_norm_fwd(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  dsv_rows x, y;
+  dsv_norm p;
+  void *ptr, *weight, *bias, *stats, *stream;
+  if (!count_is(n, 8) || !rows_of(a[0], &x) || !bytes_of(a[1], &p, sizeof p) || !address_of(a[2], &ptr) ||
+      !address_of(a[3], &weight) || !address_of(a[4], &bias) || !rows_of(a[5], &y) || !address_of(a[6], &stats) ||
+      !address_of(a[7], &stream))
+    return NULL;
+  dsv_status st;
+  Py_BEGIN_ALLOW_THREADS
+  st = dsv_layer_norm_fwd(x, p, ptr, weight, bias, y, stats, stream);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+
+static PyObject* layer_norm_bwd(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  dsv_rows dy, x, dx;
+  dsv_norm p;
+  void *stats, *ptr, *weight, *dweight, *dbias, *ws, *stream;
+  size_t bytes;
+  if (!count_is(n, 12) || !rows_of(a[0], &dy) || !rows_of(a[1], &x) || !address_of(a[2], &stats) ||
+      !bytes_of(a[3], &p, sizeof p) || !address_of(a[4], &ptr) || !address_of(a[5], &weight) || !rows_of(a[6], &dx) ||
+      !address_of(a[7], &dweight) || !address_of(a[8], &dbias) || !address_of(a[9], &ws) || !size_of(a[10], &bytes) ||
+      !address_of(a[11], &stream))
+    return NULL;
+  dsv_status st;
+  Py_BEGIN_ALLOW_THREADS
+  st = dsv_layer_norm_bwd(dy, x, stats, p, ptr, weight, dx, dweight, dbias, ws, bytes, stream);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+
+static PyObject* quantize_fp8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  dsv_rows x, q, qt;
+  int32_t R, C, rows;
+  void *scale, *scale_t, *stream;
+  if (!count_is(n, 9) || !rows_of(a[0], &x) || !i32_of(a[1], &R) || !i32_of(a[2], &C) || !i32_of(a[3], &rows) ||
+      !rows_of(a[4], &q) || !address_of(a[5], &scale) || !rows_of(a[6], &qt) || !address_of(a[7], &scale_t) ||
+      !address_of(a[8], &stream))
+    return NULL;
+  dsv_status st;
+  Py_BEGIN_ALLOW_THREADS
+  st = dsv_quantize_fp8(x, R, C, rows, q, scale, qt, scale_t, stream);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+
+static PyObject* matmul_fp8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  dsv_rows x, y, c;
+  dsv_matmul p;
+  void *sx, *sy, *stream;
+  if (!count_is(n, 7) || !rows_of(a[0], &x) || !address_of(a[1], &sx) || !rows_of(a[2], &y) || !address_of(a[3], &sy) ||
+      !bytes_of(a[4], &p, sizeof p) || !rows_of(a[5], &c) || !address_of(a[6], &stream))
+    return NULL;
+  dsv_status st;
+  Py_BEGIN_ALLOW_THREADS
+  st = dsv_matmul_fp8(x, sx, y, sy, p, c, stream);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+
 #define ENTRY(name) {"dsv_" #name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, "dsv_" #name " of dsv.h"}
 static PyMethodDef methods[] = {ENTRY(rope_axes_fwd), ENTRY(rope_axes_bwd), ENTRY(packed_attn_fwd),
-                                ENTRY(packed_attn_bwd),
+                                ENTRY(packed_attn_bwd), ENTRY(layer_norm_fwd), ENTRY(layer_norm_bwd),
+                                ENTRY(quantize_fp8), ENTRY(matmul_fp8),
+                                {"set_types", (PyCFunction)(void (*)(void))set_types, METH_FASTCALL,
+                                 "the dtypes of dsv_type"},
+                                {"matrices", (PyCFunction)(void (*)(void))matrices, METH_FASTCALL,
+                                 "rows of matrices on one device, or None"},
                                 {"row_views", (PyCFunction)(void (*)(void))row_views, METH_FASTCALL,
                                  "views of rows of one type on one device, or None"},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "dsv_calls", "calls of dsv.h that take structures", -1, methods,
                                     NULL, NULL, NULL, NULL};
 PyMODINIT_FUNC PyInit_dsv_calls(void) {
-  if (PyType_Ready(&ViewType) != 0) return NULL;
+  if (PyType_Ready(&ViewType) != 0 || PyType_Ready(&RowsType) != 0) return NULL;
   s_dtype = PyUnicode_InternFromString("dtype");
   s_get_device = PyUnicode_InternFromString("get_device");
   s_stride = PyUnicode_InternFromString("stride");
@@ -277,6 +462,12 @@ PyMODINIT_FUNC PyInit_dsv_calls(void) {
   Py_INCREF(&ViewType);
   if (PyModule_AddObject(m, "View", (PyObject*)&ViewType) != 0) {
     Py_DECREF(&ViewType);
+    Py_DECREF(m);
+    return NULL;
+  }
+  Py_INCREF(&RowsType);
+  if (PyModule_AddObject(m, "Rows", (PyObject*)&RowsType) != 0) {
+    Py_DECREF(&RowsType);
     Py_DECREF(m);
     return NULL;
   }

@@ -456,6 +456,116 @@ dsv_status dsv_packed_attn_bwd(dsv_view Q, dsv_view K, dsv_view V, dsv_view O, d
                                size_t workspace_bytes, dsv_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Matrices, for the calls below: element (r, c) is at ptr + r * stride + c
+ * (stride in elements of `type`, at least the number of columns where there is
+ * more than one row, below 2^38).
+ * ------------------------------------------------------------------------ */
+typedef enum { DSV_BF16 = 0, DSV_F32 = 1, DSV_E4M3 = 2, DSV_E5M2 = 3 } dsv_type;
+typedef struct {
+  void* ptr;
+  int64_t stride;
+  int32_t type;
+} dsv_rows;
+
+/* ------------------------------------------------------------------------
+ * dsv_layer_norm_fwd, dsv_layer_norm_bwd — layer norm of the rows of a
+ * [T, C] matrix, as a block's residual stream passes through it before the
+ * projections to Q, K and V ([nl] 1: the layers of a video DiT; the pages leave
+ * the norm open).  One weight and bias for all rows, or a row of them for each
+ * sequence of tokens (scale and shift from each clip's conditioning).
+ *
+ *   mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps)     over the C columns
+ *   y = (x - mu) r w_s + b_s
+ * The backward, with x^ = (x - mu) r and g = dy w_s:
+ *   dx = r (g - mean(g) - x^ mean(g x^))
+ *   dweight_s = sum over the rows of s of dy x^,  dbias_s = sum of dy
+ *
+ * x, dx     bf16 or fp32, of one type;  y, dy  bf16.  Any stride and alignment
+ *           of an element; 16-byte aligned rows and C % 8 == 0 take the wider
+ *           loads.  y may be x (bf16), dx may be x or dy (the same rows and
+ *           type); other overlaps of an output with an input are not allowed.
+ * seq_ptr   int32 [S + 1] on the device, rising within [0, T]: sequence s owns
+ *           the rows seq_ptr[s] .. seq_ptr[s+1] - 1, and rows outside of all are
+ *           neither read into any sum nor written.  NULL: S sequences of T / S
+ *           rows each.  Where the pointers do not rise, DSV_ERR_BAD_INDEX is
+ *           recorded with a sequence as its info; the call still reads and
+ *           writes inside its tensors only, with results that are not specified.
+ * weight    fp32 [S, C], or NULL (w = 1; then bias, dweight, dbias and the
+ *           workspace may be NULL).
+ * bias      fp32 [S, C], or NULL (b = 0).  NULL where weight is.
+ * stats     fp32 [2, T]: mu, then r; the backward reads the forward's.
+ * dweight, dbias  fp32 [S, C], zeros for a sequence without rows.
+ * workspace >= dsv_layer_norm_bwd_workspace_bytes(p) bytes, 256-byte aligned
+ *           (partial sums of dweight and dbias).
+ * T < 2^30; 1 <= C <= 16384; S <= 65535 (DSV_ERR_UNSUPPORTED otherwise); eps > 0.
+ * Sums are fp32 in a fixed order: outputs are bit-identical from run to run.
+ * With T == 0 only dweight and dbias are written (zeros), with S == 0 nothing.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t T, C, S;
+  float eps;
+} dsv_norm;
+dsv_status dsv_layer_norm_fwd(dsv_rows x, dsv_norm p, const int32_t* seq_ptr, const float* weight, const float* bias,
+                              dsv_rows y, float* stats, dsv_stream_t stream);
+size_t dsv_layer_norm_bwd_workspace_bytes(dsv_norm p);
+dsv_status dsv_layer_norm_bwd(dsv_rows dy, dsv_rows x, const float* stats, dsv_norm p, const int32_t* seq_ptr,
+                              const float* weight, dsv_rows dx, float* dweight, float* dbias, void* workspace,
+                              size_t workspace_bytes, dsv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * dsv_quantize_fp8 — a matrix in 8-bit floating point with a power-of-two
+ * scale for each block, for dsv_matmul_fp8.
+ *
+ * A block is 128 columns of one row (rows = 1) or of 128 rows (rows = 128);
+ * the last ones may be smaller.
+ *   scale = 2^k, k the least integer >= -126 with max |x| <= M 2^k
+ *           (M = 448 for DSV_E4M3, 57344 for DSV_E5M2), 1 for a block of zeros
+ *   q     = x / scale, rounded to nearest (halves to even)
+ * A block that holds an infinity or a NaN gets NaN for its scale and all its
+ * elements; no other block is touched by it.
+ *
+ * x         bf16 or fp32 [R, C], any stride and alignment of an element.
+ * q         [R, C], type DSV_E4M3 or DSV_E5M2; 16-byte aligned, stride a multiple
+ *           of 16.  Bytes between the rows are not written.
+ * scale     fp32 [ceil(C/128), R] for rows = 1, [ceil(C/128), ceil(R/128)] for 128.
+ * qt        NULL ptr, or [C, R] of q's type: the transposed matrix quantised in
+ *           the same way, blocks along R, from the same read of x.
+ * scale_t   with qt: fp32 [ceil(R/128), C] or [ceil(R/128), ceil(C/128)].
+ * R, C < 2^31 - 128 and fewer than 2^31 blocks of 128 x 128 (DSV_ERR_UNSUPPORTED
+ * otherwise).
+ * ------------------------------------------------------------------------ */
+dsv_status dsv_quantize_fp8(dsv_rows x, int32_t R, int32_t C, int32_t rows, dsv_rows q, float* scale, dsv_rows qt,
+                            float* scale_t, dsv_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * dsv_matmul_fp8 — product of two such matrices along their rows: a
+ * projection of a block, or, from the transposed copies, its gradients.
+ *
+ *   c[m, n] (+)= sum over k of (a[m, k] a_scale[k/128, m/a_rows]) (b[n, k] b_scale[k/128, n/b_rows])
+ *
+ * a, b      [M, K] and [N, K], DSV_E4M3 or DSV_E5M2 each; 16-byte aligned,
+ *           strides multiples of 16.
+ * a_scale   fp32 [ceil(K/128), M] with a_rows = 1, [ceil(K/128), ceil(M/128)] with
+ *           128; any values, not only powers of two.  b_scale likewise with N, b_rows.
+ * c         [M, N], bf16 or fp32, any stride; rows do not overlap; no overlap with
+ *           the inputs.  32-byte aligned rows take the wider stores.
+ * accumulate  1: added to c (fp32 only); 0: c is overwritten.
+ * The products of a block of 128 are summed by the tensor cores in fp32, and
+ * the scaled sums of the blocks in fp32 registers; bit-identical from run to run.
+ * A NaN of row m of a or its scales reaches row m of c only, one of b column n
+ * (with scales of 128 rows: those rows or columns).
+ * M, N, K < 2^31 - 256 and ceil(M/128) ceil(N/128) < 2^31 (DSV_ERR_UNSUPPORTED
+ * otherwise).  With K == 0 the sum is zero.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t M, N, K;
+  int32_t a_rows, b_rows;    /* 1 or 128 */
+  int32_t accumulate;
+} dsv_matmul;
+dsv_status dsv_matmul_fp8(dsv_rows a, const float* a_scale, dsv_rows b, const float* b_scale, dsv_matmul p, dsv_rows c,
+                          dsv_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Status and device-side error reporting.
  * ------------------------------------------------------------------------ */
 const char* dsv_status_string(dsv_status status);

@@ -618,3 +618,97 @@ def packed_attn_bwd(Q, K, V, dO, q_ptr, k_ptr, causal=False, scale=None):
         dQ[h, qs] = scale * (dS @ K[j, ks])
         dK[j, ks] += scale * (dS.T @ Q[h, qs])
     return dQ, dK, dV
+
+
+# ---------------------------------------------------------------------------
+# Layer norm with a weight for each sequence; 8-bit blocks and their product
+# ---------------------------------------------------------------------------
+
+def _norm_rows(T, S, seq_ptr):
+    """The rows of each sequence."""
+    p = np.linspace(0, T, S + 1).astype(np.int64) if seq_ptr is None else np.asarray(seq_ptr, np.int64)
+    return [slice(int(a), int(b)) for a, b in zip(p[:-1], p[1:])]
+
+
+def layer_norm(x, weight=None, bias=None, seq_ptr=None, eps=1e-6):
+    """(y [T, C], mean [T], 1/deviation [T]); weight and bias [C] or [S, C].
+    Rows outside the sequences: NaN."""
+    x = np.asarray(x, np.float64)
+    T, C = x.shape
+    mean = x.mean(-1)
+    rstd = 1.0 / np.sqrt(np.mean((x - mean[:, None]) ** 2, axis=-1) + eps)
+    w = np.ones((1, C)) if weight is None else np.asarray(weight, np.float64).reshape(-1, C)
+    b = np.zeros_like(w) if bias is None else np.asarray(bias, np.float64).reshape(-1, C)
+    y = np.full_like(x, np.nan)
+    for s, r in enumerate(_norm_rows(T, w.shape[0] if seq_ptr is None else len(seq_ptr) - 1, seq_ptr)):
+        k = s if weight is not None else 0
+        y[r] = (x[r] - mean[r, None]) * rstd[r, None] * w[k] + b[k]
+    return y, mean, rstd
+
+
+def layer_norm_bwd(dy, x, mean, rstd, weight=None, seq_ptr=None):
+    """dx, dweight and dbias (weight's shape; [S, C] of ones where it is None),
+    by the Jacobian of a row, J = r (I - 1 1^T / C - x^ x^T / C).  Rows outside
+    the sequences: NaN."""
+    dy, x = np.asarray(dy, np.float64), np.asarray(x, np.float64)
+    T, C = x.shape
+    h = (x - np.asarray(mean, np.float64)[:, None]) * np.asarray(rstd, np.float64)[:, None]
+    S = len(seq_ptr) - 1 if seq_ptr is not None else 1 if weight is None else np.asarray(weight).reshape(-1, C).shape[0]
+    w = np.ones((S, C)) if weight is None else np.asarray(weight, np.float64).reshape(-1, C)
+    dx, dw, db = np.full_like(x, np.nan), np.zeros((S, C)), np.zeros((S, C))
+    for s, r in enumerate(_norm_rows(T, S, seq_ptr)):
+        g = dy[r] * w[s]
+        J = g - g.sum(-1, keepdims=True) / C - h[r] * (h[r] * g).sum(-1, keepdims=True) / C
+        dx[r] = np.asarray(rstd, np.float64)[r, None] * J
+        dw[s], db[s] = (dy[r] * h[r]).sum(0), dy[r].sum(0)
+    shape = (S, C) if weight is None else np.asarray(weight).shape
+    return dx, dw.reshape(shape), db.reshape(shape)
+
+
+FP8_TYPES = {"e4m3": (3, -6, 448.0), "e5m2": (2, -14, 57344.0)}   # fraction bits, least exponent, largest value
+
+
+def round_fp8(v, to="e4m3"):
+    """The nearest 8-bit values, halves to even; |v| at most the largest value."""
+    bits, least, _ = FP8_TYPES[to]
+    v = np.asarray(v, np.float64)
+    with np.errstate(divide="ignore"):
+        e = np.maximum(np.floor(np.log2(np.abs(v))), least)
+    step = 2.0 ** (e - bits)
+    return np.round(v / step) * step
+
+
+def quantize_fp8(x, rows=1, to="e4m3"):
+    """(q, scale) of x [R, C]: blocks of `rows` rows x 128 columns; scale
+    [ceil(C/128), ceil(R/rows)], the least power of two >= 2^-126 that brings the
+    block inside the type (1 for a block of zeros)."""
+    x = np.asarray(x, np.float64)
+    R, C = x.shape
+    top = FP8_TYPES[to][2]
+    q, scale = np.empty_like(x), np.empty((-(-C // 128), -(-R // rows)))
+    for j in range(scale.shape[0]):
+        for i in range(scale.shape[1]):
+            b = np.s_[i * rows:(i + 1) * rows, j * 128:(j + 1) * 128]
+            m = np.abs(x[b]).max()
+            if not np.isfinite(m):
+                q[b], scale[j, i] = np.nan, np.nan
+                continue
+            k = 0 if m == 0 else -126
+            while m > top * 2.0 ** k:
+                k += 1
+            scale[j, i] = 2.0 ** k
+            q[b] = round_fp8(x[b] / scale[j, i], to)
+    return q, scale
+
+
+def dequantize_fp8(q, scale):
+    """The numbers that q [R, C] and its scales stand for."""
+    q, scale = np.asarray(q, np.float64), np.asarray(scale, np.float64)
+    R, C = q.shape
+    row = np.arange(R) // (1 if scale.shape[1] == R else 128)
+    return q * scale[np.arange(C) // 128][:, row].T
+
+
+def matmul_fp8(a, a_scale, b, b_scale):
+    """[M, N] = dequantised a times dequantised b, transposed."""
+    return dequantize_fp8(a, a_scale) @ dequantize_fp8(b, b_scale).T

@@ -1,0 +1,426 @@
+"""GPU parity of the layer norm, the 8-bit quantiser and the 8-bit product
+against the fp64 oracle (needs a GB300).
+
+Tolerances.  An output is rounded once to its type (half a step: eps/2 of the
+value).  A mean over C <= 16384 columns is summed as at most 64 values of a
+thread, 5 shuffles and 8 warps, each addition good to 2^-24 of a partial sum:
+2^-17 mean|x| holds with room.  r is then good to 2^-17 and the few roundings
+of an element to 2^-21 of its terms.  dweight and dbias are fp32 sums of R
+terms: (2^-20 + R 2^-24) sum |term|.  The quantiser is exact (a power of two
+divides without rounding).  A product of two 8-bit values is exact in fp32 (at
+most 8 bits); the tensor cores add 32 of them at a time at no less than fp32's
+22 leading bits of the largest (2^-22 each, 33 terms, 4 steps a block: 2^-15 of
+the sum of magnitudes), the blocks' sums in fp32 (2^-23 a block for scaling and
+adding)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from parity_util import to64
+
+pytestmark = pytest.mark.gpu
+BF, F32, E4, E5 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.float8_e5m2
+HALF = {BF: 2.0 ** -8, F32: 2.0 ** -24}
+NAME = {E4: "e4m3", E5: "e5m2"}
+
+
+@pytest.fixture(scope="module")
+def dsv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from dynamic_block_sparse_projection_gb300 import binding
+    binding.clear_device_error()
+    return binding
+
+
+def _rand(seed, *shape):
+    return torch.randn(*shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+
+
+def _clean(dsv):
+    assert dsv.device_error() == (0, 0)
+
+
+def _check(got, ref, tol, what):
+    got, ref = to64(got), np.asarray(ref)
+    bad = np.abs(got - ref) / (tol + 1e-30)
+    assert np.all(bad <= 1.0), f"{what}: {np.nanmax(bad):.3f} of the tolerance"
+
+
+# ---------------------------------------------------------------------------
+# Layer norm
+# ---------------------------------------------------------------------------
+
+NORMS = [  # T, C, sequences (None: one weight; int: equal parts; list: pointers), x type, layout, offset
+    (1, 1, None, BF, "flat", 0), (1, 8, None, F32, "flat", 0), (256, 128, None, BF, "flat", 0),
+    (37, 1160, [0, 5, 5, 36, 37], F32, "flat", 0), (64, 2048, 2, BF, "flat", 0),
+    (19, 2050, [0, 1, 19], BF, "flat", 0),                     # no 16-byte rows
+    (33, 257, 3, F32, "flat", 0), (40, 72, [3, 3, 10, 31, 31], BF, "slice", 0),     # rows outside, a slice's rows
+    (9, 8192, None, BF, "flat", 0), (5, 16384, 5, F32, "flat", 0), (6, 16383, [0, 6], BF, "flat", 0),
+    (50, 1000, 50, BF, "odd", 0),                              # rows that start at odd elements
+    (31, 640, None, F32, "flat", 1000.0), (700, 320, [0, 0, 699, 699, 700], BF, "flat", 30.0), (12, 5120, 4, BF, "slice", 0),
+]
+
+
+def _norm_case(seed, T, C, seq, dt, layout, offset):
+    S = 1 if seq is None else seq if isinstance(seq, int) else len(seq) - 1
+    x = _rand(seed, T, C) * torch.exp(0.5 * _rand(seed + 1, C)) + offset
+    dy, w, b = _rand(seed + 2, T, C).to(BF), 1 + 0.3 * _rand(seed + 3, S, C), _rand(seed + 4, S, C)
+    if seq is None:
+        w, b = w[0], b[0]
+    if layout != "flat":                                      # a wider matrix' columns
+        wide = torch.full((T, C + 24), 7.0, device="cuda")
+        at = 8 if layout == "slice" else 3
+        wide[:, at:at + C] = x
+        x = wide.to(dt)[:, at:at + C]
+        big = torch.zeros(T, C + 24, device="cuda", dtype=BF)
+        big[:, at:at + C] = dy
+        dy = big[:, at:at + C]
+    ptr = torch.tensor(seq, dtype=torch.int32, device="cuda") if isinstance(seq, list) else None
+    return x.to(dt), dy, w, b, ptr
+
+
+def _inside(T, seq):
+    rows = np.ones(T, bool)
+    if isinstance(seq, list):
+        rows[:seq[0]] = rows[seq[-1]:] = False
+    return rows
+
+
+@pytest.mark.parametrize("case", NORMS)
+@pytest.mark.parametrize("kind", ["weight, bias", "weight", "none"])
+def test_layer_norm(dsv, case, kind):
+    T, C, seq, dt, layout, offset = case
+    x, _, w, b, ptr = _norm_case(3, *case)
+    if kind == "none" and isinstance(seq, int):
+        pytest.skip("equal parts belong to a weight")
+    w, b = (None if kind == "none" else w), (b if kind == "weight, bias" else None)
+    y, stats = dsv.layer_norm(x, w, b, ptr, eps=1e-5)
+    n64 = lambda t: None if t is None else to64(t)   # noqa: E731
+    x64 = to64(x)
+    ref, mean, rstd = oracle.layer_norm(x64, n64(w), n64(b), seq if isinstance(seq, list) else None, eps=1e-5)
+    rows = _inside(T, seq)
+    size = np.mean(np.abs(x64), -1)
+    _check(stats[0][rows], mean[rows], 2.0 ** -17 * size[rows], "mean")
+    # an error m of the mean adds m^2 to the variance
+    rtol = 2.0 ** -17 + (2.0 ** -17 * size * rstd) ** 2
+    _check(stats[1][rows], rstd[rows], (rtol * rstd)[rows], "rstd")
+    if rows.any():
+        first = ref if b is None else ref - oracle.layer_norm(x64 * 0, n64(w), n64(b), seq if isinstance(seq, list) else None)[0]
+        wmag = np.abs(oracle.layer_norm(x64 * 0, None if w is None else 0 * n64(w) + n64(w), None if w is None else n64(w),
+                                        seq if isinstance(seq, list) else None)[0]) if w is not None else np.ones_like(ref)
+        tol = HALF[BF] * np.abs(ref) + 2.0 ** -21 * (np.abs(ref) + np.abs(first)) + rtol[:, None] * np.abs(first) \
+            + wmag * (2.0 ** -17 * size * rstd)[:, None]
+        _check(y[rows], ref[rows], tol[rows], "y")
+    assert torch.equal(y[rows], dsv.layer_norm(x, w, b, ptr, eps=1e-5)[0][rows])
+    # into the caller's tensors, on a stream of its own: rows outside stay as they were
+    out = torch.full((T, C + 16), 5.0, dtype=BF, device="cuda")[:, 8:8 + C]
+    st = torch.full((2, T), 5.0, device="cuda")
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    dsv.layer_norm(x, w, b, ptr, eps=1e-5, out=out, stats=st, stream=stream)
+    torch.cuda.current_stream().wait_stream(stream)
+    assert torch.equal(out[rows], y[rows]) and torch.equal(st[:, rows], stats[:, rows])
+    assert (out[~rows] == 5).all() and (st[:, ~rows] == 5).all()
+    if dt == BF:                                              # in place
+        z = x.clone()
+        assert dsv.layer_norm(z, w, b, ptr, eps=1e-5, out=z)[0] is z and torch.equal(z[rows], y[rows])
+        assert torch.equal(z[~rows], x[~rows])
+    _clean(dsv)
+
+
+@pytest.mark.parametrize("case", NORMS)
+@pytest.mark.parametrize("weighted", [True, False])
+def test_layer_norm_bwd(dsv, case, weighted):
+    T, C, seq, dt, layout, offset = case
+    if not weighted and isinstance(seq, int):
+        pytest.skip("equal parts belong to a weight")
+    x, dy, w, _, ptr = _norm_case(5, *case)
+    w = w if weighted else None
+    stats = dsv.layer_norm(x, w, None, ptr, eps=1e-5)[1]
+    res = dsv.layer_norm_bwd(dy, x, stats, w, ptr)
+    dx = res[0] if weighted else res
+    assert dx.dtype == dt
+    rows, ptrs = _inside(T, seq), seq if isinstance(seq, list) else None
+    st = np.where(np.isfinite(to64(stats)), to64(stats), 0.0)
+    x64, g64 = to64(x), to64(dy)
+    ref, dw, db = oracle.layer_norm_bwd(g64, x64, st[0], st[1], None if w is None else to64(w), ptrs)
+    if rows.any():
+        h = (x64 - st[0][:, None]) * st[1][:, None]
+        # the weight of each row, from the sum of a row of ones
+        one = np.ones_like(x64) if w is None else oracle.layer_norm(0 * x64, to64(w), to64(w), ptrs)[0]
+        g = np.abs(g64 * one)
+        mg, mgh = g.mean(-1, keepdims=True), (g * np.abs(h)).mean(-1, keepdims=True)
+        tol = HALF[dt] * np.abs(ref) + st[1][:, None] * (2.0 ** -21 * (g + mg + np.abs(h) * mgh) + 2.0 ** -17 * (mg + np.abs(h) * mgh))
+        _check(dx[rows], ref[rows], tol[rows], "dx")
+    if weighted:
+        mags = oracle.layer_norm_bwd(np.abs(g64), np.abs(np.where(rows[:, None], (x64 - st[0][:, None]) * st[1][:, None], 0)),
+                                     0 * st[0], 0 * st[1] + 1, to64(w), ptrs)
+        for got, want, mag, what in ((res[1], dw, mags[1], "dweight"), (res[2], db, mags[2], "dbias")):
+            assert got.shape == w.shape
+            _check(got, want, (2.0 ** -20 + T * 2.0 ** -24) * mag, what)
+        # the same bits again, into the caller's tensors, with dx over dy or x
+        ws = torch.full((dsv.layer_norm_bwd_workspace_bytes(T, C, 1 if seq is None else w.shape[0]),), 255,
+                        dtype=torch.uint8, device="cuda")
+        over = x.clone() if dt == F32 else dy.clone()
+        was = over.clone()
+        a = (dy, over) if dt == F32 else (over, x)
+        dw2, db2 = torch.full_like(w, 9), torch.full_like(w, 9)
+        res2 = dsv.layer_norm_bwd(*a, stats, w, ptr, dx=over, dweight=dw2, dbias=db2, workspace=ws)
+        assert res2[0] is over and torch.equal(over[rows], dx[rows]) and torch.equal(over[~rows], was[~rows])
+        assert torch.equal(dw2, res[1]) and torch.equal(db2, res[2])
+    _clean(dsv)
+
+
+def test_layer_norm_gradient_against_differences(dsv):
+    """<dx, u>, <dw, u> and <db, u> of the kernels against central differences of the fp64 forward."""
+    T, C, seq = 30, 96, [0, 11, 30]
+    x, dy, w, b, ptr = _norm_case(7, T, C, seq, F32, "flat", 0)
+    stats = dsv.layer_norm(x, w, b, ptr, eps=1e-5)[1]
+    grads = dsv.layer_norm_bwd(dy, x, stats, w, ptr)
+    at = [to64(t) for t in (x, w, b)]
+    rng = np.random.default_rng(1)
+    for i, g in enumerate(grads):
+        u = rng.standard_normal(at[i].shape)
+        f = lambda h: (oracle.layer_norm(*[v + (h * u if j == i else 0) for j, v in enumerate(at)], seq, eps=1e-5)[0] * to64(dy)).sum()  # noqa: E731,B023
+        num = (f(1e-5) - f(-1e-5)) / 2e-5
+        assert abs(num - (to64(g) * u).sum()) <= 1e-5 * np.abs(to64(g) * u).sum() + 1e-6
+
+
+def test_layer_norm_non_finite_rows_stay_alone(dsv):
+    x, dy, w, b, _ = _norm_case(9, 24, 264, None, BF, "flat", 0)
+    y = dsv.layer_norm(x, w, b)[0]
+    z = x.clone()
+    z[5, 7], z[11, 200], z[12] = float("inf"), float("nan"), 2.0
+    y2, stats = dsv.layer_norm(z, w, b)
+    other = [i for i in range(24) if i not in (5, 11, 12)]
+    assert torch.equal(y[other], y2[other]) and y2[[5, 11]].isnan().all()
+    assert torch.equal(y2[12], b.to(BF)) and stats[1, 12] == 1 / torch.tensor(1e-6).sqrt()     # a constant row
+    dx = dsv.layer_norm_bwd(dy, z, stats, w)[0]
+    assert torch.equal(dx[other], dsv.layer_norm_bwd(dy, x, dsv.layer_norm(x, w, b)[1], w)[0][other])
+
+
+def test_layer_norm_bad_pointers_are_recorded(dsv):
+    x, dy, w, b, _ = _norm_case(11, 40, 64, [0, 10, 20, 40], BF, "flat", 0)
+    stats = dsv.layer_norm(x, w, b, torch.tensor([0, 10, 20, 40], dtype=torch.int32, device="cuda"))[1]
+    for bad, s in (([0, 30, 20, 40], 1), ([-1, 10, 20, 40], 0), ([0, 10, 20, 41], 2)):
+        ptr = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        dsv.layer_norm(x, w, b, ptr)
+        assert dsv.device_error() == (dsv.DSV_ERR_BAD_INDEX, s)
+        dsv.clear_device_error()
+        dsv.layer_norm_bwd(dy, x, stats, w, ptr)
+        assert dsv.device_error() == (dsv.DSV_ERR_BAD_INDEX, s)
+        dsv.clear_device_error()
+
+
+def test_layer_norm_empty(dsv):
+    w = torch.ones(3, 16, device="cuda")
+    x = torch.zeros(0, 16, dtype=BF, device="cuda")
+    y, st = dsv.layer_norm(x, w, w)
+    dx, dw, db = dsv.layer_norm_bwd(x, x, st, w)
+    assert y.shape == (0, 16) and dx.shape == (0, 16) and (dw == 0).all() and (db == 0).all()
+    x = torch.full((4, 16), 3.0, dtype=BF, device="cuda")
+    ptr = torch.tensor([2], dtype=torch.int32, device="cuda")
+    out = x.clone()
+    dsv.layer_norm(x, None, None, ptr, out=out)
+    assert torch.equal(out, x)
+    _clean(dsv)
+
+
+# ---------------------------------------------------------------------------
+# Quantiser
+# ---------------------------------------------------------------------------
+
+QUANTS = [(1, 1), (1, 128), (128, 1), (128, 128), (130, 300), (37, 1160), (300, 257), (5, 4096), (1000, 40), (129, 129), (17, 250)]
+
+
+def _quant_input(seed, R, C, dt):
+    x = _rand(seed, R, C) * torch.exp(2 * _rand(seed + 1, R, 1)) * torch.exp(2 * _rand(seed + 2, 1, C))
+    return x.to(dt)
+
+
+@pytest.mark.parametrize("shape", QUANTS)
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("dt,to", [(BF, E4), (F32, E4), (BF, E5), (F32, E5)])
+def test_quantize(dsv, shape, rows, dt, to):
+    R, C = shape
+    x = _quant_input(2, R, C, dt)
+    q, s, qt, st = dsv.quantize_fp8(x, rows=rows, transpose=True, dtype=to)
+    assert q.dtype == to and qt.shape == (C, R) and q.stride(0) % 16 == 0 or R == 1
+    ref, sref = oracle.quantize_fp8(to64(x), rows, NAME[to])
+    assert np.array_equal(to64(s), sref) and np.array_equal(to64(q.float()), ref)
+    ref, sref = oracle.quantize_fp8(to64(x).T, rows, NAME[to])
+    assert np.array_equal(to64(st), sref) and np.array_equal(to64(qt.float()), ref)
+    q2, s2 = dsv.quantize_fp8(x, rows=rows, dtype=to)
+    assert torch.equal(q2.float(), q.float()) and torch.equal(s2, s)
+    # a matrix inside another, into the caller's memory: what lies beside it stays
+    big = torch.zeros(R, C + 7, dtype=dt, device="cuda")
+    big[:, 3:3 + C] = x
+    wide = -(-C // 16) * 16 + 16
+    store = torch.full((R, wide), 0x55, dtype=torch.uint8, device="cuda")
+    tall = -(-R // 16) * 16 + 16
+    store_t = torch.full((C, tall), 0x55, dtype=torch.uint8, device="cuda")
+    s3, st3 = torch.empty_like(s), torch.empty_like(st)
+    dsv.quantize_fp8(big[:, 3:3 + C], rows=rows, transpose=True, dtype=to,
+                     outs=(store.view(to)[:, :C], s3, store_t.view(to)[:, :R], st3))
+    assert torch.equal(store[:, :C], q.contiguous().view(torch.uint8)) and (store[:, C:] == 0x55).all()
+    assert torch.equal(store_t[:, :R], qt.contiguous().view(torch.uint8)) and (store_t[:, R:] == 0x55).all()
+    assert torch.equal(s3, s) and torch.equal(st3, st)
+    _clean(dsv)
+
+
+@pytest.mark.parametrize("rows", [1, 128])
+def test_quantize_corners(dsv, rows):
+    """Zeros, the type's border, halves between two values, the smallest and largest numbers, NaN and infinity."""
+    x = torch.zeros(300, 300, device="cuda")
+    x[0, 0], x[0, 1] = 448.0, 17.0                  # 17: a half between 16 and 18
+    x[1, 0], x[1, 1] = 448.0001, 19.0
+    x[2, 130], x[2, 131] = 1e-45, -1e-45            # least denormal
+    x[3, 130] = float(np.finfo(np.float32).max)
+    x[4, 290], x[4, 291] = 1.75 * 2.0 ** -100, 2.0 ** -109
+    x[200, 10], x[250, 150] = float("inf"), float("nan")
+    q, s, qt, st = dsv.quantize_fp8(x, rows=rows, transpose=True)
+    for got, gs, src in ((q, s, x), (qt, st, x.t())):
+        ref, sref = oracle.quantize_fp8(to64(src), rows)
+        assert np.array_equal(to64(gs), sref, equal_nan=True) and np.array_equal(to64(got.float()), ref, equal_nan=True)
+
+
+def test_quantize_empty(dsv):
+    q, s, qt, st = dsv.quantize_fp8(torch.zeros(0, 40, dtype=BF, device="cuda"), transpose=True)
+    assert q.shape == (0, 40) and s.shape == (1, 0) and qt.shape == (40, 0) and st.shape == (0, 40)
+
+
+# ---------------------------------------------------------------------------
+# Product
+# ---------------------------------------------------------------------------
+
+MMS = [  # M, N, K
+    (1, 1, 1), (1, 128, 128), (128, 1, 129), (128, 128, 128), (1, 1001, 640), (7, 300, 2050), (33, 2048, 512), (64, 515, 1160),
+    (129, 257, 385), (200, 130, 4097), (515, 700, 200), (1000, 260, 96), (300, 1536, 16), (2049, 1100, 260), (4100, 520, 130),
+]
+
+
+def _mm_case(seed, M, N, K, ar, br, ta, tb):
+    a = _rand(seed, M, K) * torch.exp(_rand(seed + 1, M, 1))
+    b = _rand(seed + 2, N, K) * torch.exp(_rand(seed + 3, N, 1))
+    out = []
+    for t, r, to in ((a, ar, ta), (b, br, tb)):
+        q, s = oracle.quantize_fp8(to64(t), r, NAME[to])
+        store = torch.zeros(t.shape[0], -(-K // 16) * 16, dtype=torch.uint8, device="cuda").view(to)
+        store.view(torch.uint8)[:, :K] = torch.tensor(q).float().to(to).view(torch.uint8).cuda()
+        s = torch.tensor(s).float().cuda() * (1 + 0.5 * torch.rand(s.shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed)))
+        out += [store[:, :K], s]                    # scales of any value
+    return out
+
+
+def _mm_tol(a, sa, b, sb, dt, K):
+    n = lambda t: to64(t.float())                   # noqa: E731
+    ref = oracle.matmul_fp8(n(a), n(sa), n(b), n(sb))
+    mag = oracle.matmul_fp8(np.abs(n(a)), n(sa), np.abs(n(b)), n(sb))
+    return ref, HALF[dt] * np.abs(ref) + (2.0 ** -15 + -(-K // 128) * 2.0 ** -23) * mag * (1 + 2.0 ** -8)
+
+
+@pytest.mark.parametrize("shape", MMS)
+@pytest.mark.parametrize("ar,br,ta,tb,dt", [(1, 128, E4, E4, BF), (1, 1, E4, E4, F32), (1, 128, E5, E4, F32), (128, 128, E4, E5, BF),
+                                            (128, 1, E5, E5, BF)])
+def test_matmul(dsv, shape, ar, br, ta, tb, dt):
+    M, N, K = shape
+    a, sa, b, sb = _mm_case(1, M, N, K, ar, br, ta, tb)
+    c = dsv.matmul_fp8(a, sa, b, sb, out_dtype=dt)
+    ref, tol = _mm_tol(a, sa, b, sb, dt, K)
+    assert c.dtype == dt and c.shape == (M, N)
+    _check(c, ref, tol, "c")
+    assert torch.equal(c, dsv.matmul_fp8(a, sa, b, sb, out_dtype=dt))
+    # into a slice of a wider matrix: what lies beside it stays
+    for at in (0, 32, 3):
+        wide = torch.full((M + 1, N + 48), 7.0, dtype=dt, device="cuda")
+        out = wide[:M, at:at + N]
+        assert dsv.matmul_fp8(a, sa, b, sb, out=out) is out and torch.equal(out, c)
+        wide[:M, at:at + N] = 7
+        assert (wide == 7).all()
+    if dt == F32:
+        acc = _rand(5, M, N)
+        was = acc.clone()
+        dsv.matmul_fp8(a, sa, b, sb, out=acc, accumulate=True)
+        _check(acc, ref + to64(was), tol + 2.0 ** -23 * (np.abs(ref) + np.abs(to64(was))), "c + a b^T")
+    _clean(dsv)
+
+
+def test_matmul_empty(dsv):
+    a, b = (torch.zeros(n, 0, dtype=E4, device="cuda") for n in (5, 9))
+    sa, sb = torch.zeros(0, 5, device="cuda"), torch.zeros(0, 1, device="cuda")
+    out = torch.full((6, 12), 3.0, device="cuda")
+    dsv.matmul_fp8(a, sa, b, sb, out=out[:5, 1:10], accumulate=True)
+    assert (out == 3).all()
+    dsv.matmul_fp8(a, sa, b, sb, out=out[:5, 1:10])
+    assert (out[:5, 1:10] == 0).all() and out.sum() == 3 * (72 - 45)
+    a, sa = torch.zeros(0, 16, dtype=E4, device="cuda"), torch.zeros(1, 0, device="cuda")
+    assert dsv.matmul_fp8(a, sa, torch.zeros(9, 16, dtype=E4, device="cuda"), torch.ones(1, 1, device="cuda")).shape == (0, 9)
+
+
+def test_matmul_non_finite_stays_in_its_row(dsv):
+    a, sa, b, sb = _mm_case(9, 200, 300, 400, 1, 1, E4, E4)
+    c = dsv.matmul_fp8(a, sa, b, sb)
+    a2, sb2 = a.clone(), sb.clone()
+    a2.view(torch.uint8)[17, 130] = 0x7F
+    sb2[2, 250] = float("inf")
+    d = dsv.matmul_fp8(a2, sa, b, sb2)
+    assert d[17].isnan().all() and not d[:, 250].isfinite().any()
+    keep = torch.ones_like(c, dtype=torch.bool)
+    keep[17], keep[:, 250] = False, False
+    assert torch.equal(c[keep], d[keep])
+
+
+# ---------------------------------------------------------------------------
+# Together
+# ---------------------------------------------------------------------------
+
+def test_projection_of_a_block_and_its_gradients(dsv):
+    """Norm, quantiser and products as a block uses them: forward to Q, K, V, and back to x, the weights and the norm."""
+    lens, H, d = [130, 77, 1], 2, 64
+    C, T = H * d, sum(lens)
+    ptr = torch.tensor([0, 130, 207, 208], dtype=torch.int32, device="cuda")
+    x, ln_w, ln_b = _rand(1, T, C).to(BF), 1 + 0.2 * _rand(2, 3, C), 0.2 * _rand(3, 3, C)
+    w = _rand(4, 3 * C, C) / C ** 0.5
+
+    def passes():
+        y, stats = dsv.layer_norm(x, ln_w, ln_b, ptr)
+        yq, ys, yt, yts = dsv.quantize_fp8(y, transpose=True)
+        wq, ws, wt, wts = dsv.quantize_fp8(w, rows=128, transpose=True)
+        qkv = dsv.matmul_fp8(yq, ys, wq, ws)
+        q, k, v = (qkv.view(T, 3, H, d)[:, i].transpose(0, 1) for i in range(3))
+        O, lse = dsv.packed_attn_fwd(q, k, v, ptr, ptr)
+        dqkv = torch.empty(T, 3, H, d, dtype=BF, device="cuda")
+        outs = tuple(dqkv[:, i].transpose(0, 1) for i in range(3))
+        dsv.packed_attn_bwd(q, k, v, O, O, lse, ptr, ptr, outs=outs)
+        gq, gs, gt, gts = dsv.quantize_fp8(dqkv.view(T, 3 * C), transpose=True, dtype=E5)
+        dy = dsv.matmul_fp8(gq, gs, wt, wts)
+        dw = dsv.matmul_fp8(gt, gts, yt, yts, out_dtype=F32)
+        return (y, stats, qkv, dqkv, dy, dw, yq, ys, wq, ws, gq, gs, wt, wts, gt, gts, yt, yts) + dsv.layer_norm_bwd(dy, x, stats, ln_w, ptr)
+
+    r = passes()
+    (y, stats, qkv, dqkv, dy, dw, yq, ys, wq, ws, gq, gs, wt, wts, gt, gts, yt, yts, dx, dlw, dlb) = r
+    for c, ops, K in ((qkv, (yq, ys, wq, ws), C), (dy, (gq, gs, wt, wts), 3 * C), (dw, (gt, gts, yt, yts), T)):
+        ref, tol = _mm_tol(*ops, c.dtype, K)
+        _check(c, ref, tol, "product")
+    # 8 bits in each factor: the products are within the elements' own rounding of the exact ones
+    f = lambda t: to64(t.float())     # noqa: E731
+    assert np.all(np.abs(f(dw) - f(dqkv).reshape(T, -1).T @ f(y)) <= (2.0 ** -3 + 2.0 ** -4 + 2.0 ** -6) * (np.abs(f(dqkv).reshape(T, -1).T) @ np.abs(f(y))) + 1e-4)
+    ref = oracle.layer_norm_bwd(f(dy), f(x), f(stats)[0], f(stats)[1], f(ln_w), [0, 130, 207, 208])
+    for got, want in zip((dx, dlw, dlb), ref):
+        assert np.linalg.norm(f(got) - want) <= 2.0 ** -8 * np.linalg.norm(want)
+    # captured and replayed twice: the same bits
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        passes()
+    torch.cuda.current_stream().wait_stream(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = passes()
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.float(), b.float()) for a, b in zip(got, r))
+    _clean(dsv)
