@@ -523,6 +523,7 @@ enum : unsigned int {
   KID_PACKED_Q = 8,
   KID_PACKED_ROWS = 9,
   KID_MATMUL = 10,
+  KID_NORM = 11,
 };
 
 }  // namespace dsv
