@@ -32,26 +32,33 @@ struct QuantArgs {
   float* scale_t;
 };
 
-// The block's scale and the multiplier that divides by it, from the bits of
-// its largest magnitude.  TOP: the exponent of the type's largest value.  A
-// block with an infinity or a NaN gets NaN for both.
+// The exponent of a block's scale, from the bits of its largest magnitude;
+// kBad for a block with an infinity or a NaN.  TOP: the exponent of the type's
+// largest value.
+constexpr int kBad = 1 << 20;
 template <int TOP>
-__device__ __forceinline__ void block_scale(uint32_t amax, float* scale, float* inv) {
-  int k = (int)(amax >> 23) - 127 - TOP + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);   // past 1.75
-  k = max(k, -126);
-  if (amax == 0u) k = 0;
-  const bool bad = amax >= 0x7F800000u;
-  *scale = bad ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float((uint32_t)(127 + k) << 23);
-  *inv = bad ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float((uint32_t)(127 - k) << 23);
+__device__ __forceinline__ int block_exponent(uint32_t amax) {
+  const int k = max((int)((amax + 0x1FFFFFu) >> 23) - 127 - TOP, -126);      // past 1.75: one more
+  return amax == 0u ? 0 : amax >= 0x7F800000u ? kBad : k;
+}
+// 2^k, NaN for kBad
+__device__ __forceinline__ float power_of_two(int k) {
+  return k >= kBad / 2 ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float((uint32_t)(127 + k) << 23);
+}
+__device__ __forceinline__ float inverse_of(int k) {
+  return k >= kBad / 2 ? __uint_as_float(0x7FFFFFFFu) : __uint_as_float((uint32_t)(127 - k) << 23);
 }
 template <bool E5>
-__device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d) {
-  constexpr __nv_fp8_interpretation_t T = E5 ? __NV_E5M2 : __NV_E4M3;
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, T);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, T);
-  return lo | (hi << 16);
+__device__ __forceinline__ uint32_t fp8x2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, E5 ? __NV_E5M2 : __NV_E4M3);
 }
-__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+template <bool E5>
+__device__ __forceinline__ uint32_t fp8x4(uint64_t a, uint64_t b) {
+  float a0, a1, b0, b1;
+  f2_unpack(a, a0, a1);
+  f2_unpack(b, b0, b1);
+  return fp8x2<E5>(a0, a1) | (fp8x2<E5>(b0, b1) << 16);
+}
 
 // n of the 8 bytes of v, at an address that is a multiple of 8.
 __device__ __forceinline__ void store_bytes(uint8_t* p, uint2 v, int n) {
@@ -62,123 +69,185 @@ __device__ __forceinline__ void store_bytes(uint8_t* p, uint2 v, int n) {
   }
 }
 
-template <typename X, bool AL>
-__device__ __forceinline__ void load_row8(const X* row, int c, int C, float* v) {
-  if constexpr (AL && sizeof(X) == 2) {
-    const uint4 q = c < C ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+// 8 columns of a row as they are in memory, and their magnitudes' maxima as
+// ordered integers (NaN ranks above infinity, infinity above numbers): two
+// columns to a word for bf16, one for fp32.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <typename X>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  static constexpr int W = 4;
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+  }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int n) {     // the first n columns, zeros behind
+    const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      const uint32_t a = 2 * j < n ? __ldg(h + 2 * j) : 0u, b = 2 * j + 1 < n ? __ldg(h + 2 * j + 1) : 0u;
+      w[j] = a | (b << 16);
     }
-  } else if constexpr (AL) {
-    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 p = c < C ? *reinterpret_cast<const float4*>(row + c) : z;
-    const float4 q = c < C ? *reinterpret_cast<const float4*>(row + c + 4) : z;
-    v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w, v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < C ? (float)row[c + j] : 0.f;
   }
-}
+  __device__ __forceinline__ uint32_t mag(int j) const { return w[j] & 0x7FFF7FFFu; }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max_u16x2(a, b); }
+  // a word's maxima as fp32 bits: over both columns, of column c of them
+  static __device__ __forceinline__ uint32_t whole(uint32_t m) { return max(m << 16, m & 0xFFFF0000u); }
+  static __device__ __forceinline__ uint32_t part(uint32_t m, int c) { return c ? m & 0xFFFF0000u : m << 16; }
+  // columns 2 j, 2 j + 1
+  __device__ __forceinline__ uint64_t pair(int j) const {
+    return f2_pack(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+  }
+};
+template <>
+struct Raw<float> {
+  static constexpr int W = 8;
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const float* p) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+  __device__ __forceinline__ void load(const float* p, int n) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = j < n ? __ldg(reinterpret_cast<const uint32_t*>(p) + j) : 0u;
+  }
+  __device__ __forceinline__ uint32_t mag(int j) const { return w[j] & 0x7FFFFFFFu; }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
+  static __device__ __forceinline__ uint32_t whole(uint32_t m) { return m; }
+  static __device__ __forceinline__ uint32_t part(uint32_t m, int) { return m; }
+  __device__ __forceinline__ uint64_t pair(int j) const {
+    return f2_pack(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+  }
+};
 
 // Thread: rows 8 u .. 8 u + 7 and columns 8 l .. 8 l + 7 of the tile, u = tid / 16, l = tid % 16.
 template <typename X, bool AL, bool E5, bool SQUARE, bool TRANS>
-__global__ void __launch_bounds__(kQThreads) quantize_kernel(QuantArgs a, int tiles_c) {
-  constexpr int TOP = E5 ? 15 : 8;
-  __shared__ uint32_t red[kQThreads / 32][kTile];
+__global__ void __launch_bounds__(kQThreads, sizeof(X) == 2 ? 4 : 2) quantize_kernel(QuantArgs a, int tiles_c) {
+  using Row = Raw<X>;
+  constexpr int TOP = E5 ? 15 : 8, W = Row::W, WARPS = kQThreads / 32;
+  __shared__ uint32_t red[WARPS][16 * W];                 // maxima of a warp's 16 rows, a word of columns each
+  __shared__ float inv_t[kTile];
   __shared__ uint2 turn[TRANS ? kTile * 16 : 1];          // [column][8 rows each], its units swapped by column / 8
-  const int u = threadIdx.x >> 4, l = threadIdx.x & 15, warp = threadIdx.x >> 5;
+  const int u = threadIdx.x >> 4, l = threadIdx.x & 15, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tc = (int)(blockIdx.x % tiles_c), tr = (int)(blockIdx.x / tiles_c);
   const int row0 = tr * kTile + 8 * u, col0 = tc * kTile + 8 * l;
-  const X* x = static_cast<const X*>(a.x);
-  float v[8][8];
+  const X* x = static_cast<const X*>(a.x) + (long long)row0 * a.xs + col0;
+  Row v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (row0 + i < a.R) {
-      load_row8<X, AL>(x + (long long)(row0 + i) * a.xs, col0, a.C, v[i]);
+    if (row0 + i < a.R && col0 < a.C) {
+      if (AL) v[i].load(x + i * a.xs); else v[i].load(x + i * a.xs, a.C - col0);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+      for (int j = 0; j < W; ++j) v[i].w[j] = 0u;
     }
-  }
-  // magnitudes as bit patterns: NaN ranks above infinity, infinity above numbers
-  uint32_t rmax[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t m = 0u;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, mag(v[i][j]));
-    rmax[i] = m;
   }
   float inv[8];
   if constexpr (SQUARE) {
     uint32_t m = 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, rmax[i]);
-    m = __reduce_max_sync(0xffffffffu, m);
-    if ((threadIdx.x & 31) == 0) red[0][warp] = m;
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < W; ++j) m = Row::larger(m, v[i].mag(j));
+    m = __reduce_max_sync(0xffffffffu, Row::whole(m));
+    if (lane == 0) red[0][warp] = m;
     __syncthreads();
     m = 0u;
 #pragma unroll
-    for (int w = 0; w < kQThreads / 32; ++w) m = max(m, red[0][w]);
-    float sc;
-    block_scale<TOP>(m, &sc, &inv[0]);
+    for (int w = 0; w < WARPS; ++w) m = max(m, red[0][w]);
+    const int k = block_exponent<TOP>(m);
 #pragma unroll
-    for (int i = 1; i < 8; ++i) inv[i] = inv[0];
+    for (int i = 0; i < 8; ++i) inv[i] = inverse_of(k);
     if (threadIdx.x == 0) {
-      a.scale[(long long)tc * ((a.R + kTile - 1) / kTile) + tr] = sc;
-      if (TRANS) a.scale_t[(long long)tr * tiles_c + tc] = sc;
+      a.scale[(long long)tc * ((a.R + kTile - 1) / kTile) + tr] = power_of_two(k);
+      if (TRANS) a.scale_t[(long long)tr * tiles_c + tc] = power_of_two(k);
     }
   } else {
+    // maxima of 8 rows over 16 lanes: a lane gives away half of its rows at each of three steps
+    uint32_t m[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      uint32_t m = rmax[i];
+      uint32_t t = v[i].mag(0);
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      float sc;
-      block_scale<TOP>(m, &sc, &inv[i]);
-      if (l == 0 && row0 + i < a.R) a.scale[(long long)tc * a.R + row0 + i] = sc;
+      for (int j = 1; j < W; ++j) t = Row::larger(t, v[i].mag(j));
+      m[i] = Row::whole(t);
+    }
+#pragma unroll
+    for (int n = 4; n > 0; n >>= 1) {
+      const bool up = lane & (2 * n);
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const uint32_t keep = up ? m[i + n] : m[i], give = up ? m[i] : m[i + n];
+        m[i] = max(keep, __shfl_xor_sync(0xffffffffu, give, 2 * n));
+      }
+    }
+    m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
+    const int k = block_exponent<TOP>(m[0]);              // of row l / 2
+    if (!(l & 1) && row0 + (l >> 1) < a.R) a.scale[(long long)tc * a.R + row0 + (l >> 1)] = power_of_two(k);
+    const float f = inverse_of(k);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) inv[i] = __shfl_sync(0xffffffffu, f, (lane & 16) + 2 * i);
+  }
+  if constexpr (TRANS && !SQUARE) {
+    uint32_t m[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      m[j] = v[0].mag(j);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) m[j] = Row::larger(m[j], v[i].mag(j));
+      m[j] = Row::larger(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+    }
+    if (lane < 16) {
+#pragma unroll
+      for (int j = 0; j < W; j += 4) *reinterpret_cast<uint4*>(&red[warp][l * W + j]) = make_uint4(m[j], m[j + 1], m[j + 2], m[j + 3]);
     }
   }
+  if (col0 < a.C) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float f = inv[i];
-    const uint2 b = make_uint2(fp8x4<E5>(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f),
-                               fp8x4<E5>(v[i][4] * f, v[i][5] * f, v[i][6] * f, v[i][7] * f));
-    if (row0 + i < a.R && col0 < a.C) store_bytes(a.q + (long long)(row0 + i) * a.qs + col0, b, a.C - col0);
+    for (int i = 0; i < 8; ++i) {
+      const uint64_t f = f2_pack(inv[i], inv[i]);
+      const uint2 b = make_uint2(fp8x4<E5>(mul2(v[i].pair(0), f), mul2(v[i].pair(1), f)),
+                                 fp8x4<E5>(mul2(v[i].pair(2), f), mul2(v[i].pair(3), f)));
+      if (row0 + i < a.R) store_bytes(a.q + (long long)(row0 + i) * a.qs + col0, b, a.C - col0);
+    }
   }
   if constexpr (TRANS) {
-    float ct[8];
-    if constexpr (SQUARE) {
+    if constexpr (!SQUARE) {
+      __syncthreads();
+      constexpr int PER = kTile / (16 * W);               // columns of a word
+      if (threadIdx.x < kTile) {
+        const int word = threadIdx.x / PER, c = threadIdx.x % PER, col = tc * kTile + (int)threadIdx.x;
+        uint32_t m = red[0][word];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ct[j] = inv[0];
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint32_t m = 0u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, mag(v[i][j]));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        if ((threadIdx.x & 31) < 16) red[warp][8 * l + j] = m;
+        for (int w = 1; w < WARPS; ++w) m = Row::larger(m, red[w][word]);
+        const int k = block_exponent<TOP>(Row::part(m, c));
+        inv_t[threadIdx.x] = inverse_of(k);
+        if (col < a.C) a.scale_t[(long long)tr * a.C + col] = power_of_two(k);
       }
       __syncthreads();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint32_t m = 0u;
-#pragma unroll
-        for (int w = 0; w < kQThreads / 32; ++w) m = max(m, red[w][8 * l + j]);
-        float sc;
-        block_scale<TOP>(m, &sc, &ct[j]);
-        if (u == 0 && col0 + j < a.C) a.scale_t[(long long)tr * a.C + col0 + j] = sc;
-      }
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float f = ct[j];
-      turn[(8 * l + j) * 16 + (u ^ l)] = make_uint2(fp8x4<E5>(v[0][j] * f, v[1][j] * f, v[2][j] * f, v[3][j] * f),
-                                                    fp8x4<E5>(v[4][j] * f, v[5][j] * f, v[6][j] * f, v[7][j] * f));
+    for (int j = 0; j < 4; ++j) {
+      uint64_t f = f2_pack(inv[0], inv[0]);
+      if constexpr (!SQUARE) f = *reinterpret_cast<const uint64_t*>(&inv_t[8 * l + 2 * j]);
+      uint32_t lo[4], hi[4];                              // two rows of column 2 j, of column 2 j + 1
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float a0, a1, b0, b1;
+        f2_unpack(mul2(v[2 * i].pair(j), f), a0, a1);
+        f2_unpack(mul2(v[2 * i + 1].pair(j), f), b0, b1);
+        lo[i] = fp8x2<E5>(a0, b0);
+        hi[i] = fp8x2<E5>(a1, b1);
+      }
+      const int c = 8 * l + 2 * j;
+      turn[c * 16 + (u ^ l)] = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+      turn[(c + 1) * 16 + (u ^ l)] = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
     }
     __syncthreads();
     const int r0 = tr * kTile + 8 * l;                    // this thread writes rows r0 .. r0 + 7 of column 16 k + u
