@@ -269,18 +269,22 @@ dsv_status check_norm(const dsv_norm& p) {
   return DSV_OK;
 }
 
-// 2D map over a [rows, cols] matrix of bytes, box = [box_rows, 128 bytes], 128-byte swizzle.
-cudaError_t make_map_bytes(CUtensorMap* map, const dsv_rows& v, long long rows, long long cols, int box_rows) {
+// 2D map over a [rows, cols] matrix, box = [box_rows, 128 bytes], 128-byte swizzle.
+cudaError_t make_map_rows(CUtensorMap* map, const dsv_rows& v, long long rows, long long cols, int box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 enc;
   cudaError_t e = get_encode(&enc);
   if (e != cudaSuccess) return e;
+  const int size = size_of(v.type);
   // the stride of a single row is never used: any valid one will do
-  const long long stride = rows > 1 ? v.stride : (cols + 15) / 16 * 16;
+  const long long stride = rows > 1 ? v.stride * size : (cols * size + 15) / 16 * 16;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)stride};
-  cuuint32_t box[2] = {128u, (cuuint32_t)box_rows};
+  cuuint32_t box[2] = {128u / size, (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1u, 1u};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, v.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  const CUtensorMapDataType type = size == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : size == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                               : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  CUresult r = enc(map, type, 2, v.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -906,10 +910,13 @@ dsv_status dsv_matmul_fp8(dsv_rows a, const float* a_scale, dsv_rows b, const fl
   if (c.ptr == a.ptr || c.ptr == b.ptr) return DSV_ERR_INVALID_ARG;
   Ctl ctl;
   if (current_ctl(&ctl) != cudaSuccess) return DSV_ERR_CUDA;
-  CUtensorMap ta, tb;
-  if (make_map_bytes(&ta, a, p.M, p.K, 128) != cudaSuccess || make_map_bytes(&tb, b, p.N, p.K, 128) != cudaSuccess)
+  CUtensorMap ta, tb, tc;
+  if (make_map_rows(&ta, a, p.M, p.K, 128) != cudaSuccess || make_map_rows(&tb, b, p.N, p.K, 128) != cudaSuccess)
     return DSV_ERR_CUDA;
-  return from_cuda(launch_matmul_fp8(ta, tb, p, a.type == DSV_E5M2, b.type == DSV_E5M2, a_scale, b_scale, c, ctl, st));
+  const bool copies = !p.accumulate && al16(c.ptr) && (p.M == 1 || c.stride * size_of(c.type) % 16 == 0);
+  if (copies && make_map_rows(&tc, c, p.M, p.N, 32) != cudaSuccess) return DSV_ERR_CUDA;
+  return from_cuda(launch_matmul_fp8(ta, tb, copies ? &tc : nullptr, p, a.type == DSV_E5M2, b.type == DSV_E5M2, a_scale,
+                                     b_scale, c, ctl, st));
 }
 
 }  // extern "C"
