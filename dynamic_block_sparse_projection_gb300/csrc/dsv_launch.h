@@ -130,7 +130,7 @@ cudaError_t launch_packed_bwd(const PackedMaps& m, const dsv_packed& p, const in
                               cudaStream_t st);
 size_t packed_bwd_ws_bytes(const dsv_packed& p);
 
-// Layer norm (norm.cu).  dweight and dbias (and ws) only with a weight.
+// Layer norm (norm_fwd.cu, norm_bwd.cu).  dweight and dbias (and ws) only with a weight.
 cudaError_t launch_norm_fwd(const dsv_rows& x, const dsv_norm& p, const int32_t* ptr, const float* weight,
                             const float* bias, const dsv_rows& y, float* stats, const Ctl& ctl, cudaStream_t st);
 size_t norm_bwd_ws_bytes(const dsv_norm& p);
