@@ -70,7 +70,7 @@ View = None if isinstance(_calls, _NoCalls) else _calls.View       # dsv_view
 Rows = None if isinstance(_calls, _NoCalls) else _calls.Rows       # dsv_rows
 DSV_BF16, DSV_F32, DSV_E4M3, DSV_E5M2 = range(4)                   # dsv_type
 if Rows is not None:
-    _calls.set_types(torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.float8_e5m2)
+    _calls.set_types(torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.float8_e5m2, torch.int32)
 
 
 class Shape(ctypes.Structure):
@@ -909,6 +909,20 @@ def _need_matrix(t, name: str, dtypes, device: Optional[torch.device] = None) ->
         raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
+# The current device's index without the checks around it.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _ready(x, stream) -> int:
+    """The device of x where a call can go out at once: the current device's, on its current stream; else -1.  The
+    C module then checks the arguments; where it does not take them, the checks below say why."""
+    if stream is None and Rows is not None and _raw_stream is not None and isinstance(x, torch.Tensor):
+        at = x.get_device()
+        if at >= 0 and x.dim() == 2 and at == _current_device():
+            return at
+    return -1
+
+
 _BF16, _REAL, _FP8 = (torch.bfloat16,), (torch.bfloat16, torch.float32), (torch.float8_e4m3fn, torch.float8_e5m2)
 
 
@@ -963,6 +977,15 @@ def layer_norm(x, weight=None, bias=None, seq_ptr=None, *, eps: float = 1e-6, ou
     owns the rows seq_ptr[s]:seq_ptr[s+1] (int32 [S+1]), or without seq_ptr the
     s-th part of T/S rows.  Rows outside the sequences are not written: in an
     output that this call allocates they are uninitialised.  out may be x."""
+    at = _ready(x, stream)
+    if at >= 0:
+        T, C = x.shape
+        y = torch.empty(T, C, dtype=torch.bfloat16, device=x.device) if out is None else out
+        kept = torch.empty(2, T, dtype=torch.float32, device=x.device) if stats is None else stats
+        st = _calls.norm_fwd(x, weight, bias, seq_ptr, eps, y, kept, at, _raw_stream(at))
+        if st is not None:
+            _check(st, "dsv_layer_norm_fwd")
+            return y, kept
     p = _norm_shape(x, weight, seq_ptr, eps)
     if bias is not None:
         if weight is None:
@@ -997,6 +1020,20 @@ def layer_norm_bwd(dy, x, stats, weight=None, seq_ptr=None, *, dx=None, dweight=
     """Gradient of layer_norm from its input x and stats: dx (x's type), or with a
     weight (dx, dweight, dbias fp32 of the weight's shape); see
     dsv_layer_norm_bwd.  dx may be dy or x."""
+    at = _ready(x, stream)
+    if at >= 0 and workspace is None and (weight is not None or (dweight is None and dbias is None)):
+        dev, dw, db, ws = x.device, dweight, dbias, None
+        nbytes = 0 if weight is None else _calls.norm_bwd_bytes(x, weight, seq_ptr, at)
+        if nbytes is not None:
+            to = torch.empty(x.shape, dtype=x.dtype, device=dev) if dx is None else dx
+            if weight is not None:
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+                dw = torch.empty(weight.shape, dtype=torch.float32, device=dev) if dw is None else dw
+                db = torch.empty(weight.shape, dtype=torch.float32, device=dev) if db is None else db
+            st = _calls.norm_bwd(dy, x, stats, weight, seq_ptr, to, dw, db, _ptr(ws), nbytes, at, _raw_stream(at))
+            if st is not None:
+                _check(st, "dsv_layer_norm_bwd")
+                return to if weight is None else (to, dw, db)
     p = _norm_shape(x, weight, seq_ptr, 1e-6)
     _shape(dy, "dy", x.shape)
     _shape(stats, "stats", (2, p.T))
@@ -1045,6 +1082,20 @@ def quantize_fp8(x, *, rows: int = 1, transpose: bool = False, dtype: torch.dtyp
     bytes apart; scale fp32 [ceil(C/128), R] or [ceil(C/128), ceil(R/128)].  With
     transpose (q, scale, qt, scale_t): also the transposed matrix [C,R] with its
     own blocks along R.  outs: those tensors."""
+    at = _ready(x, stream)
+    if at >= 0 and outs is None and dtype in _FP8 and (rows == 1 or rows == 128):
+        (R, C), dev = x.shape, x.device
+        cb, rb = (C + 127) // 128, (R + 127) // 128
+        q = _fp8_matrix(R, C, dtype, dev)
+        scale = torch.empty(cb, R if rows == 1 else rb, dtype=torch.float32, device=dev)
+        qt = scale_t = None
+        if transpose:
+            qt = _fp8_matrix(C, R, dtype, dev)
+            scale_t = torch.empty(rb, C if rows == 1 else cb, dtype=torch.float32, device=dev)
+        st = _calls.quantize(x, rows, q, scale, qt, scale_t, at, _raw_stream(at))
+        if st is not None:
+            _check(st, "dsv_quantize_fp8")
+            return (q, scale, qt, scale_t) if transpose else (q, scale)
     R, C = _dims(x, "x", 2)
     if rows not in (1, 128):
         raise ValueError(f"rows is {rows}, expected 1 or 128")
@@ -1099,6 +1150,13 @@ def matmul_fp8(a, a_scale, b, b_scale, *, out_dtype: torch.dtype = torch.bfloat1
         y  = matmul_fp8(*quantize_fp8(x), *quantize_fp8(w, rows=128))
         dx = matmul_fp8(*quantize_fp8(dy), wt, wt_scale)          # w's transposed copy
         dw = matmul_fp8(dyt, dyt_scale, xt, xt_scale)             # both transposed copies"""
+    at = _ready(a, stream)
+    if at >= 0 and isinstance(b, torch.Tensor) and b.dim() == 2 and out_dtype in _REAL and (out is not None or not accumulate):
+        c = torch.empty(a.shape[0], b.shape[0], dtype=out_dtype, device=a.device) if out is None else out
+        st = _calls.matmul(a, a_scale, b, b_scale, c, 1 if accumulate else 0, at, _raw_stream(at))
+        if st is not None:
+            _check(st, "dsv_matmul_fp8")
+            return c
     M, K = _dims(a, "a", 2)
     N, Kb = _dims(b, "b", 2)
     if Kb != K:
