@@ -911,7 +911,9 @@ dsv_status dsv_matmul_fp8(dsv_rows a, const float* a_scale, dsv_rows b, const fl
   Ctl ctl;
   if (current_ctl(&ctl) != cudaSuccess) return DSV_ERR_CUDA;
   CUtensorMap ta, tb, tc;
-  if (make_map_rows(&ta, a, p.M, p.K, 128) != cudaSuccess || make_map_rows(&tb, b, p.N, p.K, 128) != cudaSuccess)
+  int box_a, box_b;
+  matmul_boxes(p, &box_a, &box_b);
+  if (make_map_rows(&ta, a, p.M, p.K, box_a) != cudaSuccess || make_map_rows(&tb, b, p.N, p.K, box_b) != cudaSuccess)
     return DSV_ERR_CUDA;
   const bool copies = !p.accumulate && al16(c.ptr) && (p.M == 1 || c.stride * size_of(c.type) % 16 == 0);
   if (copies && make_map_rows(&tc, c, p.M, p.N, 32) != cudaSuccess) return DSV_ERR_CUDA;

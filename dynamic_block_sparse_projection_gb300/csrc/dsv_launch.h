@@ -139,10 +139,11 @@ cudaError_t launch_norm_bwd(const dsv_rows& dy, const dsv_rows& x, const float* 
                             void* ws, const Ctl& ctl, cudaStream_t st);
 
 // 8-bit quantiser and product (quantize.cu, matmul_fp8.cu).  Tensor maps of the
-// product: [rows, K] bytes, boxes of 128 bytes x the tile's rows; C in boxes of
+// product: [rows, K] bytes, boxes of 128 bytes x matmul_boxes' rows; C in boxes of
 // 128 bytes x 32 rows, null where its rows do not lie on 16 bytes or it is added to.
 cudaError_t launch_quantize(const dsv_rows& x, int R, int C, int rows, const dsv_rows& q, float* scale,
                             const dsv_rows& qt, float* scale_t, cudaStream_t st);
+void matmul_boxes(const dsv_matmul& p, int* a, int* b);
 cudaError_t launch_matmul_fp8(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap* tmC, const dsv_matmul& p,
                               bool a_e5, bool b_e5, const float* sa, const float* sb, const dsv_rows& c, const Ctl& ctl,
                               cudaStream_t st);

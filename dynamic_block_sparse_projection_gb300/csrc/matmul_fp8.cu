@@ -16,8 +16,7 @@ namespace dsv {
 
 namespace {
 
-constexpr int kMmThreads = 320;            // 8 warps that scale, then the copying and the issuing warp
-constexpr int kCopyWarp = 8, kIssueWarp = 9;
+constexpr int kSMs = 152;
 constexpr int kPairs = 76;                 // pairs of SMs
 constexpr int kKb = 128;                   // elements and bytes of a block along K: one swizzle row
 
@@ -34,6 +33,7 @@ struct MmArgs {
   int sa_shift, sb_shift;                  // 0: a scale for each row, 7: for 128 rows
   void* c;
   long long ldc;
+  int split, vec;                          // small tiles: CTAs that share the blocks of K; rows of C on 4 values
   int accumulate, tma;                     // tma: C takes tensor copies (2: of every chunk, 1: not of a cut one)
   uint32_t idesc;
 };
@@ -55,13 +55,34 @@ uint32_t idesc_f8(int M, int N, bool a_e5, bool b_e5) {
          ((uint32_t)(M >> 4) << 24);
 }
 
-template <int BN>
-struct MmTraits {
-  static constexpr int BM = 128, STAGES = 5;
-  static constexpr int A_BYTES = BM * kKb, B_BYTES = BN * kKb, STAGE = A_BYTES + B_BYTES;
-  static constexpr int SMEM = STAGES * STAGE + kStoreBytes + 1024;
-  static constexpr int TMEM = 2 * BN;
-};
+// Waits for the loads from tensor memory; the registers pass through, so that no
+// use of them can be moved ahead of the wait.
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+// 4 bytes to shared memory beside what the thread does (zero where !in).
+__device__ __forceinline__ void copy4(float* dst, const float* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+// N registers that a wait before this has covered.
+template <int N>
+__device__ __forceinline__ void tmem_pass(uint32_t* r) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i])::"memory");
+}
 
 // A warp's part of C: 32 rows from `row0` (a lane has one of them), 2 PAIRS
 // columns from `col`, by way of 4 KB of shared memory: 32 rows of 128 bytes, the
@@ -141,28 +162,104 @@ __device__ __forceinline__ void stores_done(const MmArgs& g) {
   if (g.tma && (threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-// COLV: b has a scale for each row (a column of C); else one for 128.
-template <int BN, bool COLV, bool F32>
-__global__ void __launch_bounds__(kMmThreads, 1)
-    matmul_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                  const __grid_constant__ CUtensorMap tmC, MmArgs g, Ctl ctl) {
-  using T = MmTraits<BN>;
-  constexpr int NST = T::STAGES, HALF = BN / 2;
+// ---------------------------------------------------------------------------
+// Small products: a tile of 128 x BN, its blocks of K split over a cluster
+// ---------------------------------------------------------------------------
+// Where tiles are too few for the SMs, or one side is short (single tokens: the
+// weight's rows then take the tile's 128 and the tokens its columns, SWAP).  The
+// CTAs of a cluster take a run of the blocks of K each; then each adds up a part of
+// the tile, out of all CTAs' shared memory in their order, and writes it.
+constexpr int kSmallThreads = 320;         // 8 warps that scale, then the copying and the issuing warp
+constexpr int kCopyWarp = 8, kIssueWarp = 9;
+constexpr int kAhead = 16;                 // blocks whose scales are under way: as much as a first read of memory takes
+
+template <int BN>
+struct SmallTraits {
+  static constexpr int P_BYTES = 128 * kKb, Q_BYTES = BN * kKb, STAGE = P_BYTES + Q_BYTES;
+  static constexpr int STAGES = BN == 128 ? 5 : BN == 64 ? 7 : 9;
+  static constexpr int BUFS = BN == 128 ? 4 : 8;
+  static constexpr int TMEM = BUFS * BN;
+  static constexpr int SMEM = STAGES * STAGE + kAhead * 2 * 256 * 4 + 1024;
+  static_assert(STAGES * STAGE >= 128 * BN * 4, "the tile's sums take the stages' place");
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 16 bytes of shared memory of the cluster's CTA `rank`, at this CTA's address `at`.
+__device__ __forceinline__ float4 cluster_load(uint32_t at, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(at), "r"(rank)
+      : "memory");
+  return v;
+}
+// Four neighbouring values of C from (row, col), those inside it.
+template <bool F32>
+__device__ __forceinline__ void store4(const MmArgs& g, int rows, int cols, int row, int col, float4 v) {
+  if (row >= rows || col >= cols) return;
+  const float x[4] = {v.x, v.y, v.z, v.w};
+  const long long at = (long long)row * g.ldc + col;
+  if constexpr (F32) {
+    float* out = static_cast<float*>(g.c) + at;
+    if (g.vec && col + 4 <= cols) {
+      float4 o = v;
+      if (g.accumulate) {
+        o = *reinterpret_cast<const float4*>(out);
+        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+      }
+      *reinterpret_cast<float4*>(out) = o;
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (col + i < cols) out[i] = g.accumulate ? out[i] + x[i] : x[i];
+  } else {
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(g.c) + at;
+    if (g.vec && col + 4 <= cols) {
+      *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (col + i < cols) out[i] = __float2bfloat16_rn(x[i]);
+  }
+}
+
+// g is that of the tile's rows (M, sa: b's with SWAP) and columns (N, sb).
+// COLV: a scale for each column; else one for 128 of them.
+template <int BN, bool SWAP, bool COLV, bool F32>
+__global__ void __launch_bounds__(kSmallThreads, 1)
+    matmul_small_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, MmArgs g, Ctl ctl) {
+  using T = SmallTraits<BN>;
+  constexpr int NST = T::STAGES, NB = T::BUFS, HALF = BN / 2;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = smem_align1024(raw);
-  __shared__ uint64_t full[NST], empty[NST], sums[2], freed[2], drain;
+  __shared__ uint64_t full[NST], empty[NST], sums[NB], freed[NB], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
-  __shared__ float colscale[2][2][HALF];
+  float* scales = reinterpret_cast<float*>(ring + NST * T::STAGE);     // [slot][rows', columns'][thread]
   volatile int* abort_flag = &abort_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned int kid = KID_MATMUL << 8;
+  const int rank = g.split > 1 ? (int)cluster_rank() : 0, tile = (int)blockIdx.x / g.split;
+  const int row0 = (tile % g.tm) * 128, col0 = (tile / g.tm) * BN;
+  const int kb0 = (int)((long long)g.kbs * rank / g.split), kbs = (int)((long long)g.kbs * (rank + 1) / g.split) - kb0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NB; ++i) {
       mbar_init(&sums[i], 1);
       mbar_init(&freed[i], 8);
     }
@@ -178,109 +275,172 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
-  const int tiles = g.tm * g.tn;
+  bool ok = true;
 
   if (warp == kCopyWarp) {
     if (lane == 0) {
-      uint32_t n = 0;
-      bool ok = true;
-      for (int t = (int)blockIdx.x; ok && t < tiles; t += (int)gridDim.x) {
-        const int row = (t % g.tm) * T::BM, col = (t / g.tm) * BN;
-        for (int kb = 0; kb < g.kbs; ++kb, ++n) {
-          const int s = (int)(n % NST);
-          if (n >= NST && !mbar_wait(&empty[s], (n / NST - 1) & 1u, abort_flag, ctl, kid | W_EMPTY)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&full[s], T::STAGE);
-          tma_load_2d(ring + s * T::STAGE, &tmA, &full[s], kb * kKb, row);
-          tma_load_2d(ring + s * T::STAGE + T::A_BYTES, &tmB, &full[s], kb * kKb, col);
-        }
+      int n = 0;
+      for (; n < kbs; ++n) {
+        const int s = n % NST;
+        if (n >= NST && !mbar_wait(&empty[s], (uint32_t)(n / NST - 1) & 1u, abort_flag, ctl, kid | W_EMPTY)) break;
+        mbar_arrive_expect_tx(&full[s], T::STAGE);
+        tma_load_2d(ring + s * T::STAGE, &tmP, &full[s], (kb0 + n) * kKb, row0);
+        tma_load_2d(ring + s * T::STAGE + T::P_BYTES, &tmQ, &full[s], (kb0 + n) * kKb, col0);
       }
       // every copy this thread started must land before the CTA exits
-      for (uint32_t i = n > NST ? n - NST : 0u; i < n; ++i)
-        mbar_wait(&full[i % NST], (i / NST) & 1u, nullptr, ctl, kid | W_DRAIN);
+      for (int i = n > NST ? n - NST : 0; i < n; ++i)
+        mbar_wait(&full[i % NST], (uint32_t)(i / NST) & 1u, nullptr, ctl, kid | W_DRAIN);
     }
   } else if (warp == kIssueWarp) {
-    const uint64_t a0 = sdesc_sw128(smem_u32(ring), 16, 1024);
-    const uint64_t b0 = sdesc_sw128(smem_u32(ring + T::A_BYTES), 16, 1024);
-    uint32_t n = 0;
-    bool ok = true;
-    for (int t = (int)blockIdx.x; ok && t < tiles; t += (int)gridDim.x) {
-      for (int kb = 0; kb < g.kbs; ++kb, ++n) {
-        const int s = (int)(n % NST), buf = (int)(n & 1u);
-        if (n >= 2) ok = mbar_wait_warp(&freed[buf], (n / 2 - 1) & 1u, abort_flag, ctl, kid | W_FREE);
-        if (ok) ok = mbar_wait_warp(&full[s], (n / NST) & 1u, abort_flag, ctl, kid | W_FULL);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t a = desc_off(a0, (uint32_t)s * T::STAGE), b = desc_off(b0, (uint32_t)s * T::STAGE);
+    const uint64_t p0 = sdesc_sw128(smem_u32(ring), 16, 1024);
+    const uint64_t q0 = sdesc_sw128(smem_u32(ring + T::P_BYTES), 16, 1024);
+    // a wait costs 200 clocks even where there is nothing to wait for: the next block's
+    // barriers are tested ahead, beside the issuing of this one's products
+    uint32_t here = 0, room = 1;
+    for (int n = 0; n < kbs; ++n) {
+      const int s = n % NST, buf = n % NB;
+      ok = mbar_wait_warp_tested(&full[s], (uint32_t)(n / NST) & 1u, here, abort_flag, ctl, kid | W_FULL);
+      if (ok && n >= NB)
+        ok = mbar_wait_warp_tested(&freed[buf], (uint32_t)(n / NB - 1) & 1u, room, abort_flag, ctl, kid | W_FREE);
+      if (!ok) break;
+      here = mbar_test(&full[(n + 1) % NST], (uint32_t)((n + 1) / NST) & 1u);
+      room = n + 1 >= NB ? mbar_test(&freed[(n + 1) % NB], (uint32_t)((n + 1) / NB - 1) & 1u) : 1u;
+      tc_fence_after();
+      const uint64_t p = desc_off(p0, (uint32_t)s * T::STAGE), q = desc_off(q0, (uint32_t)s * T::STAGE);
 #pragma unroll
-        for (int k = 0; k < kKb / 32; ++k)
-          mma_f8_w(tmem + (uint32_t)buf * BN, desc_off(a, k * 32), desc_off(b, k * 32), g.idesc, k > 0 ? 1u : 0u);
-        mma_commit_w(&empty[s]);
-        mma_commit_w(&sums[buf]);
-      }
+      for (int k = 0; k < kKb / 32; ++k)
+        mma_f8_w(tmem + (uint32_t)buf * BN, desc_off(p, k * 32), desc_off(q, k * 32), g.idesc, k > 0 ? 1u : 0u);
+      mma_commit_w(&sums[buf]);
+      mma_commit_w(&empty[s]);
     }
     mma_commit_w(&drain);
     mbar_wait_warp(&drain, 0, nullptr, ctl, kid | W_DRAIN);
   } else {
     // warps 0-3: the first half of the tile's columns, warps 4-7 the second
-    const int half = warp >> 2, r = (warp & 3) * 32 + lane;
+    const int half = warp >> 2, r = (warp & 3) * 32 + lane, row = row0 + r, col = col0 + half * HALF;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    uint32_t n = 0;
-    bool ok = true;                            // a failed wait: the loops go on, past the barriers, without work
-    for (int t = (int)blockIdx.x; t < tiles; t += (int)gridDim.x) {
-      const int row = (t % g.tm) * T::BM + r, col = (t / g.tm) * BN + half * HALF;
-      const bool in = row < g.M;
-      const float* pa = g.sa + (row >> g.sa_shift);
-      const float* pb = COLV ? g.sb + col + r : g.sb + (col >> 7);
-      const bool col_in = COLV ? r < HALF && col + r < g.N : col < g.N;
-      uint64_t acc[HALF / 2];
+    const bool in = row < g.M, col_in = COLV ? r < HALF && col + r < g.N : col < g.N;
+    const float* pa = g.sa + (in ? row >> g.sa_shift : 0) + kb0 * g.sa_ld;
+    const float* pb = g.sb + (col_in ? (COLV ? col + r : col) >> g.sb_shift : 0) + kb0 * g.sb_ld;
+    uint64_t acc[HALF / 2];
 #pragma unroll
-      for (int j = 0; j < HALF / 2; ++j) acc[j] = 0ull;
-      float sa_next = in && g.kbs > 0 ? __ldg(pa) : 0.f, sb_next = col_in && g.kbs > 0 ? __ldg(pb) : 0.f;
-      for (int kb = 0; kb < g.kbs; ++kb, ++n) {
-        const int buf = (int)(n & 1u);
-        const float sa = sa_next, sb = sb_next;
-        if (kb + 1 < g.kbs) {
-          sa_next = in ? __ldg(pa + (kb + 1) * g.sa_ld) : 0.f;
-          sb_next = col_in ? __ldg(pb + (kb + 1) * g.sb_ld) : 0.f;
-        }
+    for (int j = 0; j < HALF / 2; ++j) acc[j] = 0ull;
+    // a thread brings in the scales of its row and of a column, kAhead blocks before their use
+    const int me = (int)threadIdx.x;
+    auto fetch = [&](int n) {
+      if (n < kbs) {
+        copy4(scales + (n % kAhead) * 512 + me, in ? pa + n * g.sa_ld : g.sa, in);
+        copy4(scales + (n % kAhead) * 512 + 256 + me, col_in ? pb + n * g.sb_ld : g.sb, col_in);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int i = 0; i < kAhead - 2; ++i) fetch(i);
+    uint32_t here = 0;                         // the next block's sums are known to be complete
+    // a failed wait: the loop goes on, past the barriers, without work
+    for (int n = 0; n < kbs; ++n) {
+      const int buf = n % NB;
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 3) : "memory");
+      if (COLV) asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+      fetch(n + kAhead - 2);
+      const float* w = scales + (n % kAhead) * 512 + 256;
+      const float f = COLV ? scales[(n % kAhead) * 512 + me] : scales[(n % kAhead) * 512 + me] * w[me];
+      if (ok) ok = mbar_wait_warp_tested(&sums[buf], (uint32_t)(n / NB) & 1u, here, abort_flag, ctl, kid | W_SUMS);
+      if (!ok) continue;
+      tc_fence_after();
+      const uint64_t f2 = f2_pack(f, f);
+      w += half * 128;
+      uint32_t v[HALF];
+      const uint32_t from = tmem + lane_off + (uint32_t)(buf * BN + half * HALF);
+      if constexpr (HALF == 16) tmem_ld16(from, v); else tmem_ld32(from, v);
+      if constexpr (HALF == 64) tmem_ld32(from + 32, v + 32);
+      tmem_ld_wait16(v);
+      if constexpr (HALF > 16) tmem_pass<HALF - 16>(v + 16);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&freed[buf]);
+      here = mbar_test(&sums[(n + 1) % NB], (uint32_t)((n + 1) / NB) & 1u);
+#pragma unroll
+      for (int j = 0; j < HALF / 2; j += 2) {
+        uint64_t x = f2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+        uint64_t y = f2_pack(__uint_as_float(v[2 * j + 2]), __uint_as_float(v[2 * j + 3]));
         if (COLV) {
-          if (r < HALF) colscale[half][buf][r] = sb;
-          asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+          const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(w + 2 * j);
+          x = mul2(x, c.x);
+          y = mul2(y, c.y);
         }
-        if (ok) ok = mbar_wait_warp(&sums[buf], (n / 2) & 1u, abort_flag, ctl, kid | W_SUMS);
-        if (!ok) continue;
-        tc_fence_after();
-        const float sc = COLV ? sa : sa * sb;
-        const uint64_t sc2 = f2_pack(sc, sc);
+        acc[j] = fma2(x, f2, acc[j]);
+        acc[j + 1] = fma2(y, f2, acc[j + 1]);
+      }
+    }
+    // The sums take the stages' place: all products have read them.  SWAP: [column]
+    // [row]; else [row][column], the 16-byte units of a row swapped by the row.
+    if (ok) {
+      float* part = reinterpret_cast<float*>(ring);
 #pragma unroll
-        for (int c = 0; c < HALF / 32; ++c) {
-          uint32_t p[32];
-          tmem_ld32(tmem + lane_off + (uint32_t)(buf * BN + half * HALF + c * 32), p);
-          tmem_ld_wait();
-          if (c == HALF / 32 - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&freed[buf]);
-          }
+      for (int j = 0; j < HALF / 2; j += 2) {
+        float x[4];
+        f2_unpack(acc[j], x[0], x[1]);
+        f2_unpack(acc[j + 1], x[2], x[3]);
+        const int c = half * HALF + 2 * j;
+        if constexpr (SWAP) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            uint64_t v = f2_pack(__uint_as_float(p[2 * j]), __uint_as_float(p[2 * j + 1]));
-            if (COLV) v = mul2(v, *reinterpret_cast<const uint64_t*>(&colscale[half][buf][c * 32 + 2 * j]));
-            acc[c * 16 + j] = fma2(v, sc2, acc[c * 16 + j]);
-          }
+          for (int i = 0; i < 4; ++i) part[(c + i) * 128 + r] = x[i];
+        } else {
+          *reinterpret_cast<float4*>(part + r * BN + (((c >> 2) ^ (r & 7)) << 2)) = make_float4(x[0], x[1], x[2], x[3]);
         }
       }
-      if (ok) store_rows<F32, HALF / 2>(g, &tmC, ring + NST * T::STAGE + warp * 4096, row - lane, col, acc);
     }
-    stores_done(g);
   }
+  if (!ok) abort_word = 1;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == kIssueWarp) tmem_dealloc(tmem, T::TMEM);
+  if (g.split > 1) cluster_sync();
+  // this CTA's part of the tile: SWAP: columns, else rows
+  constexpr int UNITS = 32 * BN;                         // of 4 values
+  const int first = UNITS / g.split * rank, last = first + UNITS / g.split;
+  if (warp < 8 && !*abort_flag) {
+    for (int u = first + (int)threadIdx.x; u < last; u += 256) {
+      const int line = SWAP ? u / 32 : u / (BN / 4), q = SWAP ? u % 32 : u % (BN / 4);
+      const uint32_t at = smem_u32(ring) + 16u * (uint32_t)(SWAP ? u : line * (BN / 4) + (q ^ (line & 7)));
+      float4 v = cluster_load(at, 0u);
+      for (int k = 1; k < g.split; ++k) {
+        const float4 x = cluster_load(at, (uint32_t)k);
+        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+      }
+      if constexpr (SWAP) store4<F32>(g, g.N, g.M, col0 + line, row0 + 4 * q, v);
+      else store4<F32>(g, g.M, g.N, row0 + line, col0 + 4 * q, v);
+    }
+  }
+  if (g.split > 1) cluster_sync();                       // no CTA leaves while its sums are read
+}
+
+template <int BN, bool SWAP, bool COLV, bool F32>
+cudaError_t small_t(const CUtensorMap& tmP, const CUtensorMap& tmQ, const MmArgs& g, const Ctl& ctl, cudaStream_t st) {
+  using T = SmallTraits<BN>;
+  auto kern = matmul_small_kernel<BN, SWAP, COLV, F32>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute cluster{};
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = (unsigned)g.split;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(g.tm * g.tn * g.split));
+  cfg.blockDim = dim3(kSmallThreads);
+  cfg.dynamicSmemBytes = T::SMEM;
+  cfg.stream = st;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = g.split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, tmP, tmQ, g, ctl);
+}
+template <int BN, bool SWAP>
+cudaError_t small_pick(const CUtensorMap& tmP, const CUtensorMap& tmQ, const MmArgs& g, bool colv, bool f32, const Ctl& ctl,
+                       cudaStream_t st) {
+  if (colv)
+    return f32 ? small_t<BN, SWAP, true, true>(tmP, tmQ, g, ctl, st) : small_t<BN, SWAP, true, false>(tmP, tmQ, g, ctl, st);
+  return f32 ? small_t<BN, SWAP, false, true>(tmP, tmQ, g, ctl, st) : small_t<BN, SWAP, false, false>(tmP, tmQ, g, ctl, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -297,14 +457,6 @@ constexpr int kPairStages = 5, kPairHalf = 128 * kKb, kPairStage = 2 * kPairHalf
 constexpr int kScaleSlots = 4, kScaleWords = 384;     // scales of a block: see the scale warp
 constexpr int kPairSmem = kPairStages * kPairStage + kStoreBytes + kScaleSlots * kScaleWords * 4 + 1024;
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // Arrive on the barrier at the same place in the cluster's first CTA.  What the
 // arrival stands for (tensor memory read, operands in place) is ordered by the
 // tcgen05 and copy instructions themselves; no thread reads memory that another
@@ -345,24 +497,6 @@ __device__ __forceinline__ void pair_commit_w(uint64_t* bar) {
       "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
           smem_u32(bar))
       : "memory");
-}
-// Waits for the loads from tensor memory; the registers pass through, so that no
-// use of them can be moved ahead of the wait.
-__device__ __forceinline__ void tmem_ld_wait16(uint32_t* r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tmem_ld_wait32(uint32_t* r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
-                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
 }
 // Tiles in the order they are worked on: `group` columns of tiles at a time,
 // row by row, so that the tiles under work share rows of a, and the group's
@@ -632,16 +766,40 @@ cudaError_t pair_t(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtenso
   return cudaGetLastError();
 }
 
-template <int BN, bool COLV, bool F32>
-cudaError_t matmul_t(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmC, MmArgs g, const Ctl& ctl,
-                   cudaStream_t st) {
-  using T = MmTraits<BN>;
-  auto kern = matmul_kernel<BN, COLV, F32>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
-  if (e != cudaSuccess) return e;
-  const int tiles = g.tm * g.tn;
-  kern<<<tiles < 152 ? tiles : 152, kMmThreads, T::SMEM, st>>>(tmA, tmB, tmC, g, ctl);
-  return cudaGetLastError();
+// How a product is worked on: by pairs of CTAs or in small tiles, and there over
+// how many CTAs a tile's blocks of K are split.  The times behind the choice are
+// those measured (in 10 ns; 152 SMs): a block of K 0.34 us in a small tile and 0.47
+// in a pair's (0.49 and 0.80 with a scale for each column), a tile's beginning and
+// end 4.5 us, or 1.4 in a pair that goes on to the next tile; joining the sums 0.8
+// to 3 us; and clusters of 2, 4 and 8 CTAs find 148, 128 and 104 SMs.  Against
+// measured calls it is off by up to 10 %: 640 x 1160 x 40000 has 160 us as small
+// tiles, 85 split in two and 89 in four, and is estimated at 158, 82 and 88.
+struct Plan {
+  bool pair, swap;
+  int bn, split;           // without pairs
+};
+Plan plan_of(const dsv_matmul& p) {
+  Plan plan = {false, false, 128, 1};
+  const int kbs = (p.K + kKb - 1) / kKb;
+  plan.swap = p.M <= 64 && p.M < p.N;
+  const int rows = plan.swap ? p.N : p.M, cols = plan.swap ? p.M : p.N;
+  const bool colv = (plan.swap ? p.a_rows : p.b_rows) == 1;
+  plan.bn = cols <= 32 ? 32 : cols <= 64 ? 64 : 128;
+  const long long tiles = (long long)((rows + 127) / 128) * ((cols + plan.bn - 1) / plan.bn);
+  const int block = colv && plan.bn == 128 ? 49 : 34;
+  const int slots[4] = {kSMs, 148, 128, 104}, join[4] = {0, 80, 110, 300};
+  long long best = 0;
+  for (int i = 0; i < 4 && 1 << i <= kbs; ++i) {
+    const long long waves = ((tiles << i) + slots[i] - 1) / slots[i];
+    const long long time = waves * ((long long)((kbs + (1 << i) - 1) >> i) * block + 450) + join[i];
+    if (i == 0 || time < best) best = time, plan.split = 1 << i;
+  }
+  if (p.M > 128 && p.N > 128) {
+    const long long pairs = (long long)((p.M + 255) / 256) * ((p.N + 255) / 256);
+    const long long time = (pairs + kPairs - 1) / kPairs * ((long long)kbs * (p.b_rows == 1 ? 80 : 47) + 140) + 350;
+    plan.pair = time <= best;
+  }
+  return plan;
 }
 
 }  // namespace
@@ -668,16 +826,43 @@ cudaError_t launch_matmul_fp8(const CUtensorMap& tmA, const CUtensorMap& tmB, co
   const bool f32 = c.type == DSV_F32;
   g.tma = tmC == nullptr ? 0 : (long long)p.N * (f32 ? 4 : 2) % 16 == 0 ? 2 : 1;
   const CUtensorMap& tm_c = tmC != nullptr ? *tmC : tmA;      // not used without
-  g.idesc = idesc_f8(128, 128, a_e5, b_e5);
-  if (p.M > 128 && p.N > 128) {
+  g.split = 1;
+  const int size = f32 ? 4 : 2;
+  g.vec = reinterpret_cast<uintptr_t>(c.ptr) % (4 * size) == 0 && c.stride % 4 == 0;
+  const Plan plan = plan_of(p);
+  if (plan.pair) {
     g.idesc = idesc_f8(256, 256, a_e5, b_e5);
     if (p.b_rows == 1)
       return f32 ? pair_t<true, true>(tmA, tmB, tm_c, g, ctl, st) : pair_t<true, false>(tmA, tmB, tm_c, g, ctl, st);
     return f32 ? pair_t<false, true>(tmA, tmB, tm_c, g, ctl, st) : pair_t<false, false>(tmA, tmB, tm_c, g, ctl, st);
   }
-  if (p.b_rows == 1)
-    return f32 ? matmul_t<128, true, true>(tmA, tmB, tm_c, g, ctl, st) : matmul_t<128, true, false>(tmA, tmB, tm_c, g, ctl, st);
-  return f32 ? matmul_t<128, false, true>(tmA, tmB, tm_c, g, ctl, st) : matmul_t<128, false, false>(tmA, tmB, tm_c, g, ctl, st);
+  g.split = plan.split;
+  if (plan.swap) {
+    g.M = p.N, g.N = p.M;
+    g.sa = sb, g.sb = sa;
+    const MmArgs h = g;
+    g.sa_ld = h.sb_ld, g.sb_ld = h.sa_ld;
+    g.sa_shift = h.sb_shift, g.sb_shift = h.sa_shift;
+    g.idesc = idesc_f8(128, plan.bn, b_e5, a_e5);
+  } else {
+    g.idesc = idesc_f8(128, plan.bn, a_e5, b_e5);
+  }
+  g.tm = (g.M + 127) / 128;
+  g.tn = (g.N + plan.bn - 1) / plan.bn;
+  const bool colv = (plan.swap ? p.a_rows : p.b_rows) == 1;
+  if (plan.swap)
+    return plan.bn == 32 ? small_pick<32, true>(tmB, tmA, g, colv, f32, ctl, st)
+                         : small_pick<64, true>(tmB, tmA, g, colv, f32, ctl, st);
+  return plan.bn == 32   ? small_pick<32, false>(tmA, tmB, g, colv, f32, ctl, st)
+         : plan.bn == 64 ? small_pick<64, false>(tmA, tmB, g, colv, f32, ctl, st)
+                         : small_pick<128, false>(tmA, tmB, g, colv, f32, ctl, st);
+}
+
+// Rows of the boxes that a's and b's tensor maps have.
+void matmul_boxes(const dsv_matmul& p, int* a, int* b) {
+  const Plan plan = plan_of(p);
+  *a = plan.pair || !plan.swap ? 128 : plan.bn;
+  *b = plan.pair || plan.swap ? 128 : plan.bn;
 }
 
 }  // namespace dsv
