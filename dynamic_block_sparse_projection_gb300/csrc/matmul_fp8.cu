@@ -73,6 +73,15 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t* r) {
                :
                : "memory");
 }
+// Tensor memory -> registers, 16 lanes x 32 columns: r[4 i], r[4 i + 1] are columns 8 i + 2 (lane % 4) and the
+// next of row lane / 4, and r[4 i + 2], r[4 i + 3] those of row lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 // 4 bytes to shared memory beside what the thread does (zero where !in).
 __device__ __forceinline__ void copy4(float* dst, const float* src, bool in) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 4 : 0) : "memory");
@@ -84,43 +93,56 @@ __device__ __forceinline__ void tmem_pass(uint32_t* r) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i])::"memory");
 }
 
-// A warp's part of C: 32 rows from `row0` (a lane has one of them), 2 PAIRS
-// columns from `col`, by way of 4 KB of shared memory: 32 rows of 128 bytes, the
+// A warp's part of C: 32 rows from `row0` and 128 columns from `col`, by way of 4 KB of shared memory: 32 rows of 128 bytes, the
 // 16-byte units of a row swapped by the row, as tensor copies with the 128-byte
 // swizzle have them.  The tensor copy out runs beside the next tile; where C's
 // rows do not lie on 16 bytes, or are added to, the warp writes row by row.
 // (A lane that stores its row itself takes 32 lines an instruction: 13 % of a
-// product with K = 2048.)
-template <bool F32, int PAIRS>
+// product with K = 2048.)  acc: the pairs of a lane's own row in their order; or
+// (SPREAD) [32 columns][16 rows][8 columns][8 rows] as tmem_ld_rows16 gives them.
+template <bool F32, bool SPREAD>
 __device__ __forceinline__ void store_rows(const MmArgs& g, const CUtensorMap* tmC, uint8_t* stage, int row0, int col,
                                            const uint64_t* acc) {
   constexpr int COLS = F32 ? 32 : 64;                    // columns of a chunk
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int c0 = 0; c0 < 2 * PAIRS; c0 += COLS) {
+  for (int c0 = 0; c0 < 128; c0 += COLS) {
     // the last chunk has left shared memory
     if (g.tma && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncwarp();
+    if constexpr (SPREAD) {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      uint32_t w[4];
-      if constexpr (F32) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float x, y;
-          f2_unpack(acc[c0 / 2 + 2 * u + i], x, y);
-          w[2 * i] = __float_as_uint(x);
-          w[2 * i + 1] = __float_as_uint(y);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x, y;
-          f2_unpack(acc[c0 / 2 + 4 * u + i], x, y);
-          w[i] = pack_bf16x2(x, y);
-        }
+      for (int i = 0; i < COLS / 2; ++i) {                 // 8 columns and 8 rows a step
+        const int c = c0 + i / 4 * 8, h = i / 2 % 2, k = i % 2;
+        float x, y;
+        f2_unpack(acc[c / 32 * 16 + h * 8 + c / 8 % 4 * 2 + k], x, y);
+        const int row = lane / 4 + 16 * h + 8 * k, at = (c - c0 + 2 * (lane & 3)) * (F32 ? 4 : 2);
+        uint8_t* to = stage + row * 128 + (((at >> 4) ^ (row & 7)) << 4) + (at & 15);
+        if constexpr (F32) *reinterpret_cast<float2*>(to) = make_float2(x, y);
+        else *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(x, y);
       }
-      *reinterpret_cast<uint4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        uint32_t w[4];
+        if constexpr (F32) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float x, y;
+            f2_unpack(acc[c0 / 2 + 2 * u + i], x, y);
+            w[2 * i] = __float_as_uint(x);
+            w[2 * i + 1] = __float_as_uint(y);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float x, y;
+            f2_unpack(acc[c0 / 2 + 4 * u + i], x, y);
+            w[i] = pack_bf16x2(x, y);
+          }
+        }
+        *reinterpret_cast<uint4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
     if (row0 >= g.M || col + c0 >= g.N) continue;
     // a copy that the end of the rows cuts writes up to the next 16 bytes
@@ -454,7 +476,7 @@ cudaError_t small_pick(const CUtensorMap& tmP, const CUtensorMap& tmQ, const MmA
 // of its own, 128 x 128, it would be twice that, more than shared memory gives.
 constexpr int kPairThreads = 384;          // 4 warps that copy and issue, 8 that scale
 constexpr int kPairStages = 5, kPairHalf = 128 * kKb, kPairStage = 2 * kPairHalf;
-constexpr int kScaleSlots = 4, kScaleWords = 384;     // scales of a block: see the scale warp
+constexpr int kScaleSlots = 8, kScaleWords = 384;     // scales of a block: see the scale warp
 constexpr int kPairSmem = kPairStages * kPairStage + kStoreBytes + kScaleSlots * kScaleWords * 4 + 1024;
 
 // Arrive on the barrier at the same place in the cluster's first CTA.  What the
@@ -593,68 +615,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
       }
     } else if (warp == 3) {
-      // The scale warp: a block's scales, four blocks ahead in registers, into a
-      // slot in shared memory.  One for each row and half of the columns, sa sb;
-      // or (COLV) those of the 128 rows and then those of the 256 columns.  A slot
-      // is free when the products of the block two before are done: they waited for
-      // the sums of the block four before to be read, and its scales are read first.
-      constexpr int NB = COLV ? 8 : 2;
-      float ra[kScaleSlots][4], rb[kScaleSlots][NB];
-      int st = t0, skb = 0, a_left = 0, b_left = 0;
+      // The scale warp: a block's scales into a slot in shared memory, four blocks
+      // ahead and beside what the warp does: those of the 128 rows, and then (COLV) of the
+      // 256 columns; else sa sb for the rows and the first 128 columns, and the others.  A slot is free when its block's scales
+      // are read: at block n the products of block n - 2 are done, which waited for the
+      // sums of block n - 4 to be read, and a warp reads the scales before it says so.
+      // (Loads into registers and then stores held a block up by 660 clocks with a
+      // scale for each column: 359 -> 237 us at 6144 x 2048 x 17152.)
+      constexpr int AHEAD = kScaleSlots - 4;
+      int st = t0, skb = 0, a_left = 0, b_left = 0, slot = 0;
       const float *pa = nullptr, *pb = nullptr;
       const int a_step = g.sa_shift ? 0 : 32;        // 128 rows at a multiple of 128 share a scale, or have one each
-      auto fetch = [&](float* va, float* vb) {
-        if (st >= tiles) return;
-        if (skb == 0) {
-          int tm, tn;
-          tile_at(g, st, &tm, &tn);
-          const int row = tm * 256 + (int)rank * 128 + lane, col = tn * 256 + (COLV ? lane : 0);
-          a_left = g.M - row;
-          b_left = g.N - col;
-          pa = g.sa + (row >> g.sa_shift);
-          pb = g.sb + (col >> g.sb_shift);
-        }
+      // of 16 columns, the 4 that a reading lane scales are neighbours: 8 i + 2 q + e goes to 4 q + 2 i + e
+      const int spread = (lane & 16) + (lane >> 1 & 3) * 4 + (lane >> 3 & 1) * 2 + (lane & 1);
+      auto fetch = [&] {
+        if (st < tiles) {
+          if (skb == 0) {
+            int tm, tn;
+            tile_at(g, st, &tm, &tn);
+            const int row = tm * 256 + (int)rank * 128 + lane, col = tn * 256 + (COLV ? lane : 128 * (lane & 1));
+            a_left = g.M - row;
+            b_left = g.N - col;
+            pa = g.sa + (a_left > 0 ? row >> g.sa_shift : 0);
+            pb = g.sb + (b_left > 0 ? col >> g.sb_shift : 0);
+          }
+          float* to = scales + slot * kScaleWords;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) va[i] = 32 * i < a_left ? __ldg(pa + i * a_step) : 0.f;
-#pragma unroll
-        for (int i = 0; i < NB; ++i) vb[i] = (COLV ? 32 : 128) * i < b_left ? __ldg(pb + (COLV ? 32 : 1) * i) : 0.f;
-        pa += g.sa_ld;
-        pb += g.sb_ld;
-        if (++skb == g.kbs) {
-          skb = 0;
-          st += step;
-        }
-      };
-#pragma unroll
-      for (int i = 0; i < kScaleSlots; ++i) fetch(ra[i], rb[i]);
-      const long long blocks = t0 < tiles ? (long long)((tiles - 1 - t0) / step + 1) * g.kbs : 0;
-      bool ok = true;
-      for (long long n0 = 0; ok && n0 < blocks; n0 += kScaleSlots) {
-#pragma unroll
-        for (int i = 0; i < kScaleSlots; ++i) {
-          const long long n = n0 + i;
-          if (!ok || n >= blocks) break;
-          if (n >= 2) ok = mbar_wait_warp(&sums[i & 1], (uint32_t)(n / 2 - 1) & 1u, abort_flag, ctl, kid | W_SUMS);
-          if (!ok) break;
-          float* to = scales + i * kScaleWords + lane;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if constexpr (COLV) {
-              to[32 * j] = ra[i][j];
-            } else {
-              to[32 * j] = ra[i][j] * rb[i][0];
-              to[128 + 32 * j] = ra[i][j] * rb[i][1];
-            }
+          for (int i = 0; i < 4; ++i) {
+            const bool in = 32 * i < a_left;
+            copy4(to + 32 * i + lane, in ? pa + i * a_step : g.sa, in);
           }
           if constexpr (COLV) {
 #pragma unroll
-            for (int j = 0; j < NB; ++j) to[128 + 32 * j] = rb[i][j];
+            for (int i = 0; i < 8; ++i) {
+              const bool in = 32 * i < b_left;
+              copy4(to + 128 + 32 * i + spread, in ? pb + 32 * i : g.sb, in);
+            }
+          } else if (lane < 2) {
+            copy4(to + 256 + lane, b_left > 0 ? pb : g.sb, b_left > 0);
           }
+          slot = slot + 1 < kScaleSlots ? slot + 1 : 0;
+          pa += g.sa_ld;
+          pb += g.sb_ld;
+          if (++skb == g.kbs) {
+            skb = 0;
+            st += step;
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      for (int i = 0; i < AHEAD; ++i) fetch();
+      uint32_t n = 0;
+      bool ok = true;
+      for (int t = t0; ok && t < tiles; t += step) {
+        for (int kb = 0; kb < g.kbs; ++kb, ++n) {
+          if (n >= 2) ok = mbar_wait_warp(&sums[n & 1u], (n / 2 - 1) & 1u, abort_flag, ctl, kid | W_SUMS);
+          if (!ok) break;
+          fetch();
+          asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sums[i & 1]);
-          fetch(ra[i], rb[i]);
+          if constexpr (!COLV) {
+            float* to = scales + (n % kScaleSlots) * kScaleWords;
+            const float b0 = to[256], b1 = to[257];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float f = to[32 * i + lane];
+              to[32 * i + lane] = f * b0;
+              to[128 + 32 * i + lane] = f * b1;
+            }
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(&sums[n & 1u]);
         }
       }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else if (warp == 1) {
       const uint64_t a0 = sdesc_sw128(smem_u32(ring), 16, 1024);
       const uint64_t b0 = sdesc_sw128(smem_u32(ring + kPairHalf), 16, 1024);
@@ -684,7 +718,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // warps 4-7: the tile's first 128 columns, warps 8-11 the others
     const int half = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const float* my_scale = scales + (COLV ? r : half * 128 + r);
     uint32_t n = 0, here = 0;                  // here: the next block's sums are known to be complete
     bool ok = true;
     for (int t = t0; ok && t < tiles; t += step) {
@@ -699,47 +732,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (ok) ok = mbar_wait_warp_tested(&sums[buf], (n / 2) & 1u, here, abort_flag, ctl, kid | W_SUMS);
         if (!ok) break;
         tc_fence_after();
-        // 32 and 16 columns in turn: the next ones come in while these are scaled
-        uint32_t p[32], q[16];
         const uint32_t from = tmem + lane_off + (uint32_t)(buf * BN + half * 128);
-        tmem_ld32(from, p);
-        const float sc = my_scale[(n % kScaleSlots) * kScaleWords];
-        const uint64_t sc2 = f2_pack(sc, sc);
-        const float* w = scales + (n % kScaleSlots) * kScaleWords + 128 + half * 128;
-        auto add = [&](const uint32_t* v, int c0, int pairs) {
-#pragma unroll
-          for (int j = 0; j < pairs; j += 2) {
-            uint64_t v0 = f2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-            uint64_t v1 = f2_pack(__uint_as_float(v[2 * j + 2]), __uint_as_float(v[2 * j + 3]));
-            if (COLV) {
-              const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(w + c0 + 2 * j);
-              v0 = mul2(v0, x.x);
-              v1 = mul2(v1, x.y);
-            }
-            acc[c0 / 2 + j] = fma2(v0, sc2, acc[c0 / 2 + j]);
-            acc[c0 / 2 + j + 1] = fma2(v1, sc2, acc[c0 / 2 + j + 1]);
-          }
+        const float* at = scales + (n % kScaleSlots) * kScaleWords;
+        auto done = [&] {                      // this block's sums are in registers
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&freed[buf]);
+          here = mbar_test(&sums[buf ^ 1], ((n + 1) / 2) & 1u);
         };
-        tmem_ld_wait32(p);
-        tmem_ld16(from + 32, q);
-        add(p, 0, 16);
-        tmem_ld_wait16(q);
-        tmem_ld32(from + 48, p);
-        add(q, 32, 8);
-        tmem_ld_wait32(p);
-        tmem_ld16(from + 80, q);
-        add(p, 48, 16);
-        tmem_ld_wait16(q);
-        tmem_ld32(from + 96, p);
-        add(q, 80, 8);
-        tmem_ld_wait32(p);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&freed[buf]);
-        here = mbar_test(&sums[buf ^ 1], ((n + 1) / 2) & 1u);
-        add(p, 96, 16);
+        if constexpr (COLV) {
+          // 16 rows x 32 columns in turn, a lane with 4 rows and a quarter of the columns, so that it
+          // reads 8 of the columns' scales for 32 sums (with a row of its own, 32: 64 KB out of shared
+          // memory a block and SM beside the operands' 32)
+          uint32_t p[16], q[16];
+          uint64_t rs[4];
+          tmem_ld_rows16(from, p);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float f = at[(warp & 3) * 32 + 8 * i + lane / 4];
+            rs[i] = f2_pack(f, f);
+          }
+          const float* w = at + 128 + half * 128 + (lane & 3) * 4;
+          auto add = [&](const uint32_t* v, const uint64_t* cs, int c, int h) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint64_t& a = acc[c * 16 + h * 8 + j];
+              a = fma2(mul2(f2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), cs[j / 2]), rs[2 * h + j % 2], a);
+            }
+          };
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const ulonglong2 c0 = *reinterpret_cast<const ulonglong2*>(w + 32 * c);
+            const ulonglong2 c1 = *reinterpret_cast<const ulonglong2*>(w + 32 * c + 16);
+            const uint64_t cs[4] = {c0.x, c0.y, c1.x, c1.y};
+            tmem_ld_wait16(p);
+            tmem_ld_rows16(from + (16u << 16) + 32 * c, q);
+            add(p, cs, c, 0);
+            tmem_ld_wait16(q);
+            if (c < 3) tmem_ld_rows16(from + 32 * c + 32, p); else done();
+            add(q, cs, c, 1);
+          }
+        } else {
+          // 32 and 16 columns in turn: the next ones come in while these are scaled
+          uint32_t p[32], q[16];
+          tmem_ld32(from, p);
+          const float sc = at[half * 128 + r];
+          const uint64_t sc2 = f2_pack(sc, sc);
+          auto add = [&](const uint32_t* v, int c0, int pairs) {
+#pragma unroll
+            for (int j = 0; j < pairs; ++j)
+              acc[c0 / 2 + j] =
+                  fma2(f2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), sc2, acc[c0 / 2 + j]);
+          };
+          tmem_ld_wait32(p);
+          tmem_ld16(from + 32, q);
+          add(p, 0, 16);
+          tmem_ld_wait16(q);
+          tmem_ld32(from + 48, p);
+          add(q, 32, 8);
+          tmem_ld_wait32(p);
+          tmem_ld16(from + 80, q);
+          add(p, 48, 16);
+          tmem_ld_wait16(q);
+          tmem_ld32(from + 96, p);
+          add(q, 80, 8);
+          tmem_ld_wait32(p);
+          done();
+          add(p, 96, 16);
+        }
       }
-      if (ok) store_rows<F32, 64>(g, &tmC, ring + NST * kPairStage + (warp - 4) * 4096, row0, col, acc);
+      if (ok) store_rows<F32, COLV>(g, &tmC, ring + NST * kPairStage + (warp - 4) * 4096, row0, col, acc);
     }
     stores_done(g);
   }
@@ -769,7 +831,7 @@ cudaError_t pair_t(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtenso
 // How a product is worked on: by pairs of CTAs or in small tiles, and there over
 // how many CTAs a tile's blocks of K are split.  The times behind the choice are
 // those measured (in 10 ns; 152 SMs): a block of K 0.34 us in a small tile and 0.47
-// in a pair's (0.49 and 0.80 with a scale for each column), a tile's beginning and
+// in a pair's (0.49 and 0.57 with a scale for each column), a tile's beginning and
 // end 4.5 us, or 1.4 in a pair that goes on to the next tile; joining the sums 0.8
 // to 3 us; and clusters of 2, 4 and 8 CTAs find 148, 128 and 104 SMs.  Against
 // measured calls it is off by up to 10 %: 640 x 1160 x 40000 has 160 us as small
@@ -796,7 +858,7 @@ Plan plan_of(const dsv_matmul& p) {
   }
   if (p.M > 128 && p.N > 128) {
     const long long pairs = (long long)((p.M + 255) / 256) * ((p.N + 255) / 256);
-    const long long time = (pairs + kPairs - 1) / kPairs * ((long long)kbs * (p.b_rows == 1 ? 80 : 47) + 140) + 350;
+    const long long time = (pairs + kPairs - 1) / kPairs * ((long long)kbs * (p.b_rows == 1 ? 57 : 47) + 140) + 350;
     plan.pair = time <= best;
   }
   return plan;
