@@ -63,6 +63,10 @@ def parse_args(argv=None):
     p.add_argument("--rope", choices=["plain", "norm"], default=None,
                    help="rotate Q and K by their (t, y, x) positions inside the step (dsv_rope_axes_fwd, its gradient "
                         "on dQ and dK at the end); norm: behind the per-row RMS norm of queries and keys")
+    p.add_argument("--proj", choices=["fp8"], default=None,
+                   help="the step begins at the hidden state [B, N, H d]: per-clip layer norm, 8-bit quantiser and "
+                        "Q, K, V product, and takes dQ, dK, dV back to the product's weight, the hidden state and the "
+                        "norm's weights (dsv_layer_norm_fwd, dsv_quantize_fp8, dsv_matmul_fp8, dsv_layer_norm_bwd)")
     p.add_argument("--predict", choices=["fused", "two-call"], default="fused",
                    help="fused: dsv_predict_topk_blocks (scores stay on chip); two-call: dsv_predict_scores "
                         "then dsv_topk_blocks (the score matrix goes through HBM)")
@@ -78,7 +82,10 @@ def parse_args(argv=None):
                    help="write profiles/traffic.json from an ncu --csv log of dram__bytes_read.sum and "
                         "dram__bytes_write.sum for this bench's kernels, then exit (no GPU needed)")
     p.add_argument("--traffic-command", default="", help="the ncu command line recorded with --traffic-from")
-    return p.parse_args(argv)
+    args = p.parse_args(argv)
+    if args.proj and args.impl == "reference":
+        p.error("--proj has no oracle arm: one query group would need the projection of every token")
+    return args
 
 
 def load_peaks():
@@ -177,6 +184,66 @@ class _Tensors:
     pass
 
 
+class Projection:
+    """Q, K and V out of the hidden state X [B, N, H d], and their gradients back to it: layer norm with a weight
+    and a bias for each clip, 8-bit operands (rows for the forward and the hidden state's gradient, columns for the
+    weight's), products with a scale for each block of 128."""
+
+    def __init__(self, dsv, x, w):
+        import torch
+        self.dsv, self.x = dsv, x
+        B, N, C = x.X.shape
+        T, dev = B * N, x.X.device
+
+        def new(*shape, dtype=torch.bfloat16):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+        f32 = torch.float32
+        self.flat = x.X.view(T, C)
+        self.seq_ptr = torch.arange(B + 1, dtype=torch.int32, device=dev) * N
+        self.y, self.stats = new(T, C), new(2, T, dtype=f32)
+        self.y8 = self.w8 = self.g8 = None                   # the first step's results take the others'
+        self.e5 = torch.float8_e5m2
+        self.qkv, self.dqkv, self.dy, self.dx = new(T, 3 * C), new(T, 3 * C), new(T, C), new(B, N, C)
+        self.dw = new(3 * C, C, dtype=f32)
+        self.dln = new(B, C, dtype=f32), new(B, C, dtype=f32)
+        self.ws = torch.empty(max(1, dsv.layer_norm_bwd_workspace_bytes(T, C, B)), dtype=torch.uint8, device=dev)
+        # [B, H, N, d] views of the projections and of their gradients
+        self.out, self.grads = (tuple(t.view(B, N, 3, w.H, w.d)[:, :, i].transpose(1, 2) for i in range(3))
+                                for t in (self.qkv, self.dqkv))
+
+    def forward(self):
+        d, x = self.dsv, self.x
+        d.layer_norm(self.flat, x.ln_w, x.ln_b, self.seq_ptr, out=self.y, stats=self.stats)
+        self.y8 = d.quantize_fp8(self.y, transpose=True, outs=self.y8)
+        self.w8 = d.quantize_fp8(x.Wqkv, rows=128, transpose=True, outs=self.w8)
+        d.matmul_fp8(*self.y8[:2], *self.w8[:2], out=self.qkv)
+
+    def backward(self):
+        d, x = self.dsv, self.x
+        self.g8 = d.quantize_fp8(self.dqkv, transpose=True, dtype=self.e5, outs=self.g8)
+        d.matmul_fp8(*self.g8[:2], *self.w8[2:], out=self.dy)
+        d.matmul_fp8(*self.g8[2:], *self.y8[2:], out=self.dw)
+        d.layer_norm_bwd(self.dy, self.flat, self.stats, x.ln_w, self.seq_ptr, dx=self.dx.view_as(self.flat),
+                         dweight=self.dln[0], dbias=self.dln[1], workspace=self.ws)
+
+    def results(self):
+        return (self.dx, self.dw, *self.dln)
+
+
+def projection_inputs(x, w, seed=11):
+    """x with a seeded hidden state, projection weight and per-clip norm weights in place of Q, K and V."""
+    import torch
+    g = torch.Generator(device=x.dO.device).manual_seed(seed)
+    out, C, dev = _Tensors(), w.H * w.d, x.dO.device
+    out.dO, out.Wq, out.Wk = x.dO, x.Wq, x.Wk
+    out.X = torch.randn(w.B, w.N, C, generator=g, dtype=torch.bfloat16, device=dev)
+    out.Wqkv = torch.randn(3 * C, C, generator=g, device=dev) / math.sqrt(C)
+    out.ln_w = 1 + 0.1 * torch.randn(w.B, C, generator=g, device=dev)
+    out.ln_b = 0.1 * torch.randn(w.B, C, generator=g, device=dev)
+    return out
+
+
 class HotPath:
     """Preallocated buffers of one step; run() enqueues the four C-ABI calls.
 
@@ -187,10 +254,22 @@ class HotPath:
 
     With rope ("plain" or "norm") the step first rotates Q and K by their
     (t, y, x) positions, behind the RMS norm of each row for "norm", and takes
-    dQ and dK back through it (and the norm weights' gradients) at the end."""
+    dQ and dK back through it (and the norm weights' gradients) at the end.
 
-    def __init__(self, dsv, x, w, k_per_head, cube=None, mass=None, scores="mean", fused=False, rope=None):
+    With proj ("fp8") x has a hidden state instead of Q, K and V (see
+    projection_inputs): the step begins with their projection and ends with its
+    gradients.  The rotation reads and writes the projection's own layout;
+    what it does not pass through is copied to and from the attention's."""
+
+    def __init__(self, dsv, x, w, k_per_head, cube=None, mass=None, scores="mean", fused=False, rope=None, proj=None):
         import torch
+        self.proj, self.inputs = None, ("Q", "K", "V", "dO", "Wq", "Wk")
+        if proj:
+            self.proj, self.inputs = Projection(dsv, x, w), ("X", "dO", "Wq", "Wk")
+            dO, Wq, Wk = x.dO, x.Wq, x.Wk
+            x = _Tensors()
+            x.Q, x.K, x.V = (torch.empty_like(dO) for _ in range(3))
+            x.dO, x.Wq, x.Wk = dO, Wq, Wk
         self.dsv, self.x, self.w = dsv, x, w
         # the fused predictor + top-k serves the mean block scores with a fixed k per head
         self.fused = bool(fused) and not mass and scores == "mean"
@@ -208,7 +287,8 @@ class HotPath:
             self.xr = _Tensors()
             self.xr.Q, self.xr.K = torch.empty_like(x.Q), torch.empty_like(x.K)
             self.xr.V, self.xr.dO, self.xr.Wq, self.xr.Wk = x.V, x.dO, x.Wq, x.Wk
-            self.rope_grads = (torch.empty_like(x.Q), torch.empty_like(x.K))
+            self.rope_src = self.proj.out[:2] if proj else (x.Q, x.K)
+            self.rope_grads = self.proj.grads[:2] if proj else (torch.empty_like(x.Q), torch.empty_like(x.K))
             self.norm_w = tuple(torch.ones(d, device=dev) for _ in range(2)) if rope == "norm" else (None, None)
             self.norm_dw = tuple(torch.empty(d, device=dev) for _ in range(2)) if rope == "norm" else (None, None)
             self.ws_r = (torch.empty(dsv.rope_axes_bwd_workspace_bytes(d), dtype=torch.uint8, device=dev)
@@ -244,8 +324,9 @@ class HotPath:
     @property
     def stages(self):
         core = FUSED_STAGES if self.fused else STAGES
-        return ((("rope_in",) if self.rope else ()) + (("cube_in",) if self.cube else ()) + core +
-                (("cube_out",) if self.cube else ()) + (("rope_out",) if self.rope else ()))
+        return ((("proj_in",) if self.proj else ()) + (("rope_in",) if self.rope else ()) +
+                (("cube_in",) if self.cube else ()) + core + (("cube_out",) if self.cube else ()) +
+                (("rope_out",) if self.rope else ()) + (("proj_out",) if self.proj else ()))
 
     def run(self, ev=None):
         """The four public calls (six with cube order).  With ev (one CUDA
@@ -261,8 +342,14 @@ class HotPath:
 
         mark()
         x = self.x
+        copied = 2 if self.rope else 0                       # Q and K pass through the rotation
+        if self.proj:
+            self.proj.forward()
+            for src, dst in list(zip(self.proj.out, (x.Q, x.K, x.V)))[copied:]:
+                dst.copy_(src)
+            mark()
         if self.rope:
-            for src, dst, nw in zip((x.Q, x.K), (self.xr.Q, self.xr.K), self.norm_w):
+            for src, dst, nw in zip(self.rope_src, (self.xr.Q, self.xr.K), self.norm_w):
                 d.rope_axes(src, self.pos, self.bands, weight=nw, out=dst)
             mark()
             x = self.xr
@@ -304,21 +391,30 @@ class HotPath:
             mark()
         if self.rope:
             dQ, dK = (self.out_raster[1:3] if self.cube else self.grads[:2])
-            for g, src, out, nw, dw in zip((dQ, dK), (self.x.Q, self.x.K), self.rope_grads, self.norm_w, self.norm_dw):
+            for g, src, out, nw, dw in zip((dQ, dK), self.rope_src, self.rope_grads, self.norm_w, self.norm_dw):
                 d.rope_axes_bwd(g, self.pos, self.bands, x=src if nw is not None else None, weight=nw, dx=out,
                                 dweight=dw, workspace=self.ws_r)
+            mark()
+        if self.proj:
+            grads = self.out_raster[1:] if self.cube else self.grads
+            for src, dst in list(zip(grads, self.proj.grads))[copied:]:
+                dst.copy_(src)
+            self.proj.backward()
             mark()
 
     def results(self):
         """O, LSE and the gradients as the step hands them out (raster order;
         LSE stays in the path's token order; with the norm also the gradients
-        of its two weights)."""
+        of its two weights; with the projection the gradients of the hidden
+        state, the weight and the layer norm's in place of dQ, dK and dV)."""
         if self.cube:
             out = (self.out_raster[0], self.lse, *self.out_raster[1:])
         else:
             out = (self.O, self.lse, *self.grads)
         if self.rope:
             out = (*out[:2], *self.rope_grads, out[4], *(t for t in self.norm_dw if t is not None))
+        if self.proj:
+            out = (*out[:2], *self.proj.results(), *out[5:])
         return out
 
     def attention_only(self):
@@ -330,7 +426,7 @@ class HotPath:
 
 
 KERNELS_PER_STEP = {"predict": 2, "topk": 4, "predict_topk": 7, "fwd": 1, "bwd_pre": 1, "bwd_kv": 2, "bwd_q": 1,
-                    "cube_in": 4, "cube_out": 4, "rope_in": 2, "rope_out": 2}
+                    "cube_in": 4, "cube_out": 4, "rope_in": 2, "rope_out": 2, "proj_in": 4, "proj_out": 5}
 
 
 def predict_topk_launches(w) -> int:
@@ -393,6 +489,9 @@ def run_ours(args):
     if args.heads and args.heads < w.H:
         w = wl.scaled(w, name=w.name, H=args.heads)
     x = wl.make_inputs(w, device=dev)
+    if args.proj:
+        ks_of_x, x = x.k_per_head, projection_inputs(x, w)
+        x.k_per_head = ks_of_x
     cube = tuple(int(v) for v in args.cube.split(",")) if args.cube else None
     ks, dispatch = list(x.k_per_head), None
     if args.dispatch:
@@ -401,7 +500,7 @@ def run_ours(args):
         dispatch = {"profile": f"profiles/dispatch_{w.name}.json", "threshold_rho": prof.get("threshold_rho"),
                     "dense_heads": [h for h, d in enumerate(dense) if d]}
     hp = HotPath(dsv, x, w, ks, cube=cube, mass=args.mass or None, scores=args.scores,
-                 fused=args.predict == "fused", rope=args.rope)
+                 fused=args.predict == "fused", rope=args.rope, proj=args.proj)
     fwd_f, bwd_f = pair_flops(w.block, w.d)
     flush = torch.empty(L2_FLUSH_BYTES, dtype=torch.uint8, device=dev)
 
@@ -454,7 +553,7 @@ def run_ours(args):
     # dense run of the same kernels (k = nb) for the speedup
     dense = None
     if not args.no_dense:
-        dense = time_dense(dsv, x, w, hp, flush, attn_ms=attn_ms, pre_ms=pre_ms(per_call))
+        dense = time_dense(dsv, hp.x, w, hp, flush, attn_ms=attn_ms, pre_ms=pre_ms(per_call))
 
     # roofline of the dominant kernel (the predictor and the top-k are whole calls of several launches)
     dom = max((k for k in hp.stages if k in KERNEL_SRC), key=lambda k: per_call[k])
@@ -479,6 +578,8 @@ def run_ours(args):
                    **({"rope": "Q and K " + ("normalised and " if args.rope == "norm" else "") +
                        "rotated by (t, y, x), gradients taken back (dsv_rope_axes_fwd, dsv_rope_axes_bwd, timed)"}
                       if args.rope else {}),
+                   **({"proj": "Q, K, V out of the hidden state [B, N, H d] and its gradients in 8 bits "
+                       "(layer norm, quantiser, product, timed)"} if args.proj else {}),
                    **({"selection": f"mass threshold tau={args.mass}, temperature 1/sqrt(d), k in [1, nb]"}
                       if args.mass else {}),
                    **({"block_scores": "tile maximum of the low-rank logits (dsv_predict_scores_max)"}
@@ -505,7 +606,7 @@ def run_ours(args):
         "e2e": e2e,
         "peaks_source": peak_src,
     }
-    if rank == 0 and world == 1 and not args.no_cpu_baseline:
+    if rank == 0 and world == 1 and not args.no_cpu_baseline and not args.proj:
         out["cpu_baseline"] = cpu_baseline(w, x, cube=cube, mass=args.mass or None, scores=args.scores,
                                            rope=args.rope)
     if rank == 0:
@@ -668,14 +769,15 @@ def hbm_fractions(w, hp, per_call, peaks):
 
 def time_e2e(dsv, x, w, hp, args, flops_per_step):
     """Same metric through the public API with host buffers.  Every step copies
-    its inputs (Q, K, V, dO, W^Q, W^K) from pinned host memory to the device,
+    its inputs (Q, K, V, dO, W^Q, W^K; with a projection X, dO, W^Q, W^K) from pinned host memory to the device,
     runs the four calls and copies O, LSE and the three gradients back to pinned
     host memory.  Copies run on their own streams, so a step's transfers overlap
     the neighbouring steps' compute (two device buffer sets alternate); the timed
     region runs from the first host-to-device copy to the last device-to-host
     copy."""
     import torch
-    host_in = [torch.empty(t.shape, dtype=t.dtype, pin_memory=True).copy_(t) for t in (x.Q, x.K, x.V, x.dO, x.Wq, x.Wk)]
+    src = [getattr(x, name) for name in hp.inputs]
+    host_in = [torch.empty(t.shape, dtype=t.dtype, pin_memory=True).copy_(t) for t in src]
     host_out = None     # one set of pinned result buffers: the device-to-host copies run in order on one stream
 
     class X:
@@ -683,11 +785,11 @@ def time_e2e(dsv, x, w, hp, args, flops_per_step):
 
     sets = []
     for _ in range(2):
-        dev_in = [torch.empty_like(t) for t in (x.Q, x.K, x.V, x.dO, x.Wq, x.Wk)]
+        dev_in = [torch.empty_like(t) for t in src]
         xd = X()
-        xd.Q, xd.K, xd.V, xd.dO, xd.Wq, xd.Wk = dev_in
+        xd.__dict__.update(vars(x), **dict(zip(hp.inputs, dev_in)))
         hp2 = HotPath(dsv, xd, w, hp.k, cube=hp.cube, mass=hp.mass, scores=hp.scores, fused=hp.fused,
-                      rope=hp.rope)
+                      rope=hp.rope, proj="fp8" if hp.proj else None)
         if host_out is None:
             host_out = [torch.empty(t.shape, dtype=t.dtype, pin_memory=True) for t in hp2.results()]
         sets.append((dev_in, hp2, host_out))

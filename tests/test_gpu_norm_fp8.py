@@ -430,3 +430,47 @@ def test_projection_of_a_block_and_its_gradients(dsv):
         torch.cuda.synchronize()
         assert all(torch.equal(a.float(), b.float()) for a, b in zip(got, r))
     _clean(dsv)
+
+
+@pytest.mark.parametrize("rope, cube", [("norm", None), (None, None), ("plain", (2, 8, 8))])
+def test_benchmark_step_from_the_hidden_state(dsv, rope, cube):
+    """The benchmark's step with the projection: every part against the oracle on the part's own inputs, and Q, K, V and
+    their gradients in their places; the sparse path between them has its own tests."""
+    import bench
+    from dynamic_block_sparse_projection_gb300 import workloads as wl
+    from parity_util import SMALL
+    w = SMALL["latent16k_small"]
+    x0 = wl.make_inputs(w, device="cuda")
+    x = bench.projection_inputs(x0, w)
+    hp = bench.HotPath(dsv, x, w, x0.k_per_head, fused=True, rope=rope, cube=cube, proj="fp8")
+    for _ in range(2):
+        hp.run()
+    torch.cuda.synchronize()
+    _clean(dsv)
+    p, C, T = hp.proj, w.H * w.d, w.B * w.N
+    f = lambda t: to64(t.float())     # noqa: E731
+    ptr = [w.N * i for i in range(w.B + 1)]
+    y_ref, _ = oracle.layer_norm(f(p.flat), f(x.ln_w), f(x.ln_b), ptr, 1e-6)[:2]
+    size = np.abs(f(x.ln_w)).repeat(w.N, 0) * (np.abs(y_ref) + 1) + np.abs(f(x.ln_b)).repeat(w.N, 0)
+    _check(p.y, y_ref, HALF[BF] * np.abs(y_ref) + 2.0 ** -14 * size, "y")
+    for c, ops, K in ((p.qkv, p.y8[:2] + p.w8[:2], C), (p.dy, p.g8[:2] + p.w8[2:], 3 * C), (p.dw, p.g8[2:] + p.y8[2:], T)):
+        ref, tol = _mm_tol(*ops, c.dtype, K)
+        _check(c, ref, tol, "product")
+    views = [t.reshape(w.B, w.N, 3, w.H, w.d)[:, :, i].transpose(1, 2) for t in (p.qkv, p.dqkv) for i in range(3)]
+    assert torch.equal(hp.x.V, views[2])
+    if rope is None:
+        assert torch.equal(hp.x.Q, views[0]) and torch.equal(hp.x.K, views[1])
+        assert all(torch.equal(g, v) for g, v in zip(hp.grads, views[3:]))
+    else:
+        grads = hp.out_raster[1:] if cube else hp.grads
+        for i, (src, g, nw) in enumerate(zip(views[:2], grads, hp.norm_w)):
+            kw = {} if nw is None else {"weight": nw}
+            assert torch.equal((hp.xr.Q, hp.xr.K)[i], dsv.rope_axes(src.contiguous(), hp.pos, hp.bands, **kw))
+            back = dsv.rope_axes_bwd(g, hp.pos, hp.bands, x=None if nw is None else src.contiguous(), weight=nw)
+            assert torch.equal(views[3 + i], back[0] if isinstance(back, tuple) else back)
+        assert torch.equal(views[5], grads[2])
+    ref = oracle.layer_norm_bwd(f(p.dy), f(p.flat), f(p.stats)[0], f(p.stats)[1], f(x.ln_w), ptr)
+    out = hp.results()
+    assert out[2] is p.dx and out[3] is p.dw and len(out) == (8 if rope == "norm" else 6)
+    for got, want in zip((p.dx.view(T, C), *p.dln), ref):
+        assert np.linalg.norm(f(got) - want) <= 2.0 ** -8 * np.linalg.norm(want)

@@ -166,3 +166,11 @@ def test_binding_refuses_sizes_past_32_bits(dsv):
     a = torch.zeros(1, 16, dtype=torch.float8_e4m3fn)
     with pytest.raises(ValueError, match="32 bits"):
         dsv.matmul_fp8(a.expand(many, 16), torch.zeros(1, 1).expand(1, many), a, torch.zeros(1, 1))
+
+
+def test_benchmark_projection_arguments(capsys):
+    import bench
+    assert bench.parse_args([]).proj is None and bench.parse_args(["--proj", "fp8"]).proj == "fp8"
+    with pytest.raises(SystemExit):
+        bench.parse_args(["--proj", "fp8", "--impl", "reference"])
+    assert "no oracle arm" in capsys.readouterr().err
