@@ -481,8 +481,9 @@ typedef struct {
  *   dweight_s = sum over the rows of s of dy x^,  dbias_s = sum of dy
  *
  * x, dx     bf16 or fp32, of one type;  y, dy  bf16.  Any stride and alignment
- *           of an element; 16-byte aligned rows and C % 8 == 0 take the wider
- *           loads.  y may be x (bf16), dx may be x or dy (the same rows and
+ *           of an element.  Rows that all start on 4 elements, C % 4 == 0 (forward),
+ *           or on 16 bytes, C % 8 == 0 (backward), with weight and bias on 16 bytes
+ *           take the wider loads; other rows take other orders of the sums.  y may be x (bf16), dx may be x or dy (the same rows and
  *           type); other overlaps of an output with an input are not allowed.
  * seq_ptr   int32 [S + 1] on the device, rising within [0, T]: sequence s owns
  *           the rows seq_ptr[s] .. seq_ptr[s+1] - 1, and rows outside of all are
@@ -548,10 +549,12 @@ dsv_status dsv_quantize_fp8(dsv_rows x, int32_t R, int32_t C, int32_t rows, dsv_
  * a_scale   fp32 [ceil(K/128), M] with a_rows = 1, [ceil(K/128), ceil(M/128)] with
  *           128; any values, not only powers of two.  b_scale likewise with N, b_rows.
  * c         [M, N], bf16 or fp32, any stride; rows do not overlap; no overlap with
- *           the inputs.  32-byte aligned rows take the wider stores.
+ *           the inputs.  Rows on 16 bytes take the wider stores.
  * accumulate  1: added to c (fp32 only); 0: c is overwritten.
  * The products of a block of 128 are summed by the tensor cores in fp32, and
  * the scaled sums of the blocks in fp32 registers; bit-identical from run to run.
+ * A block's sum is scaled in fp32, by one scale and then the other or by the
+ * product of both: where such a step leaves fp32's range, so does the result.
  * A NaN of row m of a or its scales reaches row m of c only, one of b column n
  * (with scales of 128 rows: those rows or columns).
  * M, N, K < 2^31 - 256 and ceil(M/128) ceil(N/128) < 2^31 (DSV_ERR_UNSUPPORTED

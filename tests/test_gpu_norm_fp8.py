@@ -179,6 +179,32 @@ def test_layer_norm_bwd(dsv, case, weighted):
     _clean(dsv)
 
 
+# every number of threads and columns a thread that a width can get
+WIDTHS = [8, 24, 56, 90, 120, 180, 252, 380, 504, 510, 700, 1016, 1020, 1500, 1544, 2044, 2056, 2500, 3080, 4000, 4104, 5116, 6152,
+          8188, 8200, 10000, 12280, 12296, 14000, 16376, 16380, 16384]
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_layer_norm_widths(dsv, C, dt):
+    T = 900 if C <= 1200 else 330
+    for width in (C, C - 1):
+        case = (T, width, [0, 1, T // 3, T - 2, T], dt, "flat", 0)
+        test_layer_norm(dsv, case, "weight, bias")
+        test_layer_norm_bwd(dsv, case, True)
+
+
+@pytest.mark.parametrize("S", [300, 899, 900])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_layer_norm_of_many_sequences(dsv, S, dt):
+    T = 900
+    ends = [T * s // S for s in range(S + 1)]
+    for seq in (ends, [0] * (S - 4) + [2, 2, 700, 899, 900]) + ((S,) if T % S == 0 else ()):
+        for C in (72, 75):
+            test_layer_norm(dsv, (T, C, seq, dt, "flat", 0), "weight, bias")
+            test_layer_norm_bwd(dsv, (T, C, seq, dt, "flat", 0), True)
+
+
 def test_layer_norm_gradient_against_differences(dsv):
     """<dx, u>, <dw, u> and <db, u> of the kernels against central differences of the fp64 forward."""
     T, C, seq = 30, 96, [0, 11, 30]
@@ -304,6 +330,10 @@ def test_quantize_empty(dsv):
 MMS = [  # M, N, K
     (1, 1, 1), (1, 128, 128), (128, 1, 129), (128, 128, 128), (1, 1001, 640), (7, 300, 2050), (33, 2048, 512), (64, 515, 1160),
     (129, 257, 385), (200, 130, 4097), (515, 700, 200), (1000, 260, 96), (300, 1536, 16), (2049, 1100, 260), (4100, 520, 130),
+    # few tiles and many blocks of K: shared out over a cluster, tokens as rows or as columns of the tile
+    (130, 200, 9000), (300, 70, 8100), (33, 129, 4097), (64, 300, 5000), (1, 3000, 2100), (20, 40, 20000), (700, 24, 6000),
+    # more tiles than pairs of SMs, more blocks than slots for scales
+    (2300, 2208, 2500), (2303, 2203, 1300),
 ]
 
 
@@ -474,3 +504,98 @@ def test_benchmark_step_from_the_hidden_state(dsv, rope, cube):
     assert out[2] is p.dx and out[3] is p.dw and len(out) == (8 if rope == "norm" else 6)
     for got, want in zip((p.dx.view(T, C), *p.dln), ref):
         assert np.linalg.norm(f(got) - want) <= 2.0 ** -8 * np.linalg.norm(want)
+
+
+def test_offsets_past_32_bits(dsv):
+    """Matrices of more than 2^31 elements: the first and the last rows as those of a small call."""
+    T, C = (1 << 20) + 77, 2056
+    x = torch.empty(T, C, dtype=BF, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    w, b = 1 + 0.2 * _rand(2, C), _rand(3, C)
+    y, stats = dsv.layer_norm(x, w, b)
+    dx = dsv.layer_norm_bwd(y, x, stats, w)[0]
+    for rows in (slice(0, 300), slice(T - 300, T)):
+        small, st = dsv.layer_norm(x[rows], w, b)
+        assert torch.equal(small, y[rows]) and torch.equal(st, stats[:, rows])
+        assert torch.equal(dx[rows], dsv.layer_norm_bwd(y[rows], x[rows], st, w)[0])
+    del dx
+    q, s, qt, st = dsv.quantize_fp8(y, transpose=True)
+    first = T // 128 * 128                                     # blocks of the transposed copy begin at multiples of 128
+    for rows in (slice(0, 256), slice(first - 256, T)):
+        small = dsv.quantize_fp8(y[rows], transpose=True)
+        same = lambda u, v: torch.equal(u.view(torch.uint8), v.view(torch.uint8))      # noqa: E731
+        assert same(small[0], q[rows]) and torch.equal(small[1], s[:, rows])
+        assert same(small[2].contiguous(), qt[:, rows].contiguous())
+        assert torch.equal(small[3], st[rows.start // 128:-(-rows.stop // 128)])
+    wq, ws = dsv.quantize_fp8(0.02 * _rand(4, 2100, C), rows=128)
+    c = dsv.matmul_fp8(q, s, wq, ws)                            # 2^31 elements and more in c too
+    for rows in (slice(0, 256), slice(T - T % 256 - 256, T)):
+        n = rows.stop - rows.start
+        ref, tol = _mm_tol(q[rows], s[:, rows], wq, ws, BF, C)
+        assert c[rows].shape == (n, 2100)
+        _check(c[rows], ref, tol, "c")
+    _clean(dsv)
+
+
+def test_calls_on_two_streams_at_once(dsv):
+    """Two streams, each with its own tensors and workspace: the bits of the calls one after the other."""
+    def passes(seed):
+        x, w = _rand(seed, 3000, 1160).to(BF), 1 + 0.1 * _rand(seed + 1, 1160)
+        m = _rand(seed + 2, 1536, 1160)
+
+        def run():
+            y, st = dsv.layer_norm(x, w)
+            yq, ys, yt, yts = dsv.quantize_fp8(y, transpose=True)
+            wq, ws, _, _ = dsv.quantize_fp8(m, rows=128, transpose=True)
+            c = dsv.matmul_fp8(yq, ys, wq, ws)
+            one = dsv.matmul_fp8(yq[:1], ys[:, :1].contiguous(), wq, ws)
+            cq, cs, ct, cts = dsv.quantize_fp8(c, transpose=True, dtype=E5)
+            dw = dsv.matmul_fp8(ct, cts, yt, yts, out_dtype=F32)
+            return (y, c, one, dw, *dsv.layer_norm_bwd(y, x, st, w))
+        return run
+
+    runs = [passes(1), passes(10)]
+    want = [r() for r in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(4):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(runs[i]())
+    torch.cuda.synchronize()
+    for i in range(2):
+        for res in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(res, want[i]))
+    _clean(dsv)
+
+
+def test_replays_read_the_tensors_as_they_are(dsv):
+    """A captured chain, replayed after its inputs changed, and a second graph over the same tensors between."""
+    x, w, m = _rand(1, 700, 512).to(BF), 1 + 0.1 * _rand(2, 512), _rand(3, 900, 512)
+    ws = torch.empty(dsv.layer_norm_bwd_workspace_bytes(700, 512, 1), dtype=torch.uint8, device="cuda")
+
+    def run():
+        y, st = dsv.layer_norm(x, w)
+        q, s, wq, wsc = *dsv.quantize_fp8(y), *dsv.quantize_fp8(m, rows=128)
+        return (y, dsv.matmul_fp8(q, s, wq, wsc), dsv.matmul_fp8(q[:3], s[:, :3].contiguous(), wq, wsc),
+                *dsv.layer_norm_bwd(y, x, st, w, workspace=ws))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    for g in graphs:
+        with torch.cuda.graph(g):
+            outs.append(run())
+    for seed in (5, 6):
+        x.copy_(_rand(seed, 700, 512))
+        m.copy_(_rand(seed + 10, 900, 512))
+        for g in graphs:
+            g.replay()
+        want = run()
+        torch.cuda.synchronize()
+        for out in outs:
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+    _clean(dsv)
