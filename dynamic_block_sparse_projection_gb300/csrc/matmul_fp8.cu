@@ -10,6 +10,8 @@
 // products run into the other half of the tensor memory.
 #include <math.h>
 
+#include <type_traits>
+
 #include "dsv_launch.h"
 
 namespace dsv {
@@ -19,8 +21,7 @@ namespace {
 constexpr int kSMs = 152;
 constexpr int kPairs = 76;                 // pairs of SMs
 constexpr int kKb = 128;                   // elements and bytes of a block along K: one swizzle row
-
-constexpr int kStoreBytes = 8 * 4096;       // on C's way out, 4 KB a warp
+constexpr int kStoreBytes = 8 * 4096;      // on C's way out, 4 KB a warp
 
 enum : unsigned int { W_EMPTY = 1, W_FULL = 2, W_FREE = 3, W_SUMS = 4, W_DRAIN = 5 };
 
@@ -96,13 +97,14 @@ __device__ __forceinline__ void tmem_pass(uint32_t* r) {
 // A warp's part of C: 32 rows from `row0` and 128 columns from `col`, by way of 4 KB of shared memory: 32 rows of 128 bytes, the
 // 16-byte units of a row swapped by the row, as tensor copies with the 128-byte
 // swizzle have them.  The tensor copy out runs beside the next tile; where C's
-// rows do not lie on 16 bytes, or are added to, the warp writes row by row.
+// rows do not lie on 16 bytes, or are added to, the warp writes them itself.
 // (A lane that stores its row itself takes 32 lines an instruction: 13 % of a
 // product with K = 2048.)  acc: the pairs of a lane's own row in their order; or
 // (SPREAD) [32 columns][16 rows][8 columns][8 rows] as tmem_ld_rows16 gives them.
-template <bool F32, bool SPREAD>
+template <bool F32, bool ADD, bool SPREAD>
 __device__ __forceinline__ void store_rows(const MmArgs& g, const CUtensorMap* tmC, uint8_t* stage, int row0, int col,
                                            const uint64_t* acc) {
+  using C = typename std::conditional<F32, float, __nv_bfloat16>::type;
   constexpr int COLS = F32 ? 32 : 64;                    // columns of a chunk
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -156,25 +158,60 @@ __device__ __forceinline__ void store_rows(const MmArgs& g, const CUtensorMap* t
                      : "memory");
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
-    } else {
-      __syncwarp();
-      const int rows = min(32, g.M - row0);
-      for (int i = 0; i < rows; ++i) {
+    } else if (ADD && g.vec) {
+      // added to rows on 16 bytes: a lane has unit lane % 8 of every fourth row (70 us at
+      // 6144 x 2048 x 2048, 44 without adding; value by value 80)
+      if constexpr (ADD) {
+        const int c = col + c0 + 4 * (lane & 7), n = g.N - c, rows = g.M - row0 - lane / 8;
+        float* out = static_cast<float*>(g.c) + (long long)(row0 + lane / 8) * g.ldc + c;
+        float4 was[8];
 #pragma unroll
-        for (int j = 0; j < COLS; j += 32) {
-          const int c = j + lane, at = c * (F32 ? 4 : 2);
-          const uint8_t* from = stage + i * 128 + (((at >> 4) ^ (i & 7)) << 4) + (at & 15);
-          if (col + c0 + c < g.N) {
-            if constexpr (F32) {
-              float* out = static_cast<float*>(g.c) + (long long)(row0 + i) * g.ldc + col + c0 + c;
-              const float v = *reinterpret_cast<const float*>(from);
-              *out = g.accumulate ? *out + v : v;
-            } else {
-              static_cast<__nv_bfloat16*>(g.c)[(long long)(row0 + i) * g.ldc + col + c0 + c] =
-                  *reinterpret_cast<const __nv_bfloat16*>(from);
-            }
+        for (int j = 0; j < 8; ++j)
+          if (4 * j < rows && n >= 4) was[j] = *reinterpret_cast<const float4*>(out + 4LL * j * g.ldc);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (4 * j >= rows || n <= 0) continue;
+          const int i = 4 * j + lane / 8;
+          const float4 x = *reinterpret_cast<const float4*>(stage + i * 128 + (((lane & 7) ^ (i & 7)) << 4));
+          float* to = out + 4LL * j * g.ldc;
+          if (n >= 4) {
+            *reinterpret_cast<float4*>(to) = make_float4(was[j].x + x.x, was[j].y + x.y, was[j].z + x.z, was[j].w + x.w);
+          } else {
+            to[0] += x.x;
+            if (n > 1) to[1] += x.y;
+            if (n > 2) to[2] += x.z;
           }
         }
+      }
+    } else {
+      __syncwarp();
+      // eight rows at a time, so that their reads do not wait for one another (one by one:
+      // 40 us and not 35 at 30000 x 1001 x 200)
+      constexpr int WORDS = COLS / 32;
+      const int rows = min(32, g.M - row0);
+      for (int i0 = 0; i0 < rows; i0 += 8) {
+        C v[8][WORDS];
+        C* out = static_cast<C*>(g.c) + (long long)(row0 + i0) * g.ldc + col + c0 + lane;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int j = 0; j < WORDS; ++j) {
+            const int at = (32 * j + lane) * (int)sizeof(C);
+            v[i][j] = *reinterpret_cast<const C*>(stage + (i0 + i) * 128 + (((at >> 4) ^ i) << 4) + (at & 15));
+          }
+        if constexpr (ADD) {
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = i0 + i < rows && col + c0 + lane < g.N ? out[i * g.ldc] : 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i][0] = o[i] + v[i][0];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int j = 0; j < WORDS; ++j)
+            if (i0 + i < rows && col + c0 + 32 * j + lane < g.N) out[i * g.ldc + 32 * j] = v[i][j];
       }
     }
   }
@@ -423,16 +460,33 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   constexpr int UNITS = 32 * BN;                         // of 4 values
   const int first = UNITS / g.split * rank, last = first + UNITS / g.split;
   if (warp < 8 && !*abort_flag) {
-    for (int u = first + (int)threadIdx.x; u < last; u += 256) {
+    auto put = [&](int u, float4 v) {
       const int line = SWAP ? u / 32 : u / (BN / 4), q = SWAP ? u % 32 : u % (BN / 4);
-      const uint32_t at = smem_u32(ring) + 16u * (uint32_t)(SWAP ? u : line * (BN / 4) + (q ^ (line & 7)));
-      float4 v = cluster_load(at, 0u);
-      for (int k = 1; k < g.split; ++k) {
-        const float4 x = cluster_load(at, (uint32_t)k);
-        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-      }
       if constexpr (SWAP) store4<F32>(g, g.N, g.M, col0 + line, row0 + 4 * q, v);
       else store4<F32>(g, g.M, g.N, row0 + line, col0 + 4 * q, v);
+    };
+    auto place = [&](int u) { return SWAP ? u : u / (BN / 4) * (BN / 4) + (u % (BN / 4) ^ (u / (BN / 4) & 7)); };
+    if (g.split == 1) {
+      const float4* part = reinterpret_cast<const float4*>(ring);
+#pragma unroll 4
+      for (int i = 0; i < UNITS / 256; ++i) {
+        const int u = i * 256 + (int)threadIdx.x;
+        put(u, part[place(u)]);
+      }
+    } else {
+      // all CTAs' parts are asked for before the first is added
+      for (int u = first + (int)threadIdx.x; u < last; u += 256) {
+        const uint32_t at = smem_u32(ring) + 16u * (uint32_t)place(u);
+        float4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < g.split) x[k] = cluster_load(at, (uint32_t)k);
+        float4 v = x[0];
+#pragma unroll
+        for (int k = 1; k < 8; ++k)
+          if (k < g.split) v.x += x[k].x, v.y += x[k].y, v.z += x[k].z, v.w += x[k].w;
+        put(u, v);
+      }
     }
   }
   if (g.split > 1) cluster_sync();                       // no CTA leaves while its sums are read
@@ -529,7 +583,7 @@ __device__ __forceinline__ void tile_at(const MmArgs& g, int t, int* m, int* n) 
   *n = first + i % wide;
 }
 
-template <bool COLV, bool F32>
+template <bool COLV, bool F32, bool ADD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     matmul_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmC, MmArgs g, Ctl ctl) {
@@ -801,7 +855,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           add(p, 96, 16);
         }
       }
-      if (ok) store_rows<F32, COLV>(g, &tmC, ring + NST * kPairStage + (warp - 4) * 4096, row0, col, acc);
+      if (ok) store_rows<F32, ADD, COLV>(g, &tmC, ring + NST * kPairStage + (warp - 4) * 4096, row0, col, acc);
     }
     stores_done(g);
   }
@@ -812,10 +866,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (warp == 1) pair_dealloc(tmem, 2 * BN);
 }
 
-template <bool COLV, bool F32>
+template <bool COLV, bool F32, bool ADD>
 cudaError_t pair_t(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmC, MmArgs g, const Ctl& ctl,
                    cudaStream_t st) {
-  auto kern = matmul_pair_kernel<COLV, F32>;
+  auto kern = matmul_pair_kernel<COLV, F32, ADD>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
   if (e != cudaSuccess) return e;
   g.tm = (g.M + 255) / 256;
@@ -826,6 +880,14 @@ cudaError_t pair_t(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtenso
   const int tiles = g.tm * g.tn;
   kern<<<2 * (tiles < kPairs ? tiles : kPairs), kPairThreads, kPairSmem, st>>>(tmA, tmB, tmC, g, ctl);
   return cudaGetLastError();
+}
+
+template <bool COLV>
+cudaError_t pair_pick(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmC, const MmArgs& g, bool f32,
+                      const Ctl& ctl, cudaStream_t st) {
+  if (!f32) return pair_t<COLV, false, false>(tmA, tmB, tmC, g, ctl, st);
+  return g.accumulate ? pair_t<COLV, true, true>(tmA, tmB, tmC, g, ctl, st)
+                      : pair_t<COLV, true, false>(tmA, tmB, tmC, g, ctl, st);
 }
 
 // How a product is worked on: by pairs of CTAs or in small tiles, and there over
@@ -894,9 +956,8 @@ cudaError_t launch_matmul_fp8(const CUtensorMap& tmA, const CUtensorMap& tmB, co
   const Plan plan = plan_of(p);
   if (plan.pair) {
     g.idesc = idesc_f8(256, 256, a_e5, b_e5);
-    if (p.b_rows == 1)
-      return f32 ? pair_t<true, true>(tmA, tmB, tm_c, g, ctl, st) : pair_t<true, false>(tmA, tmB, tm_c, g, ctl, st);
-    return f32 ? pair_t<false, true>(tmA, tmB, tm_c, g, ctl, st) : pair_t<false, false>(tmA, tmB, tm_c, g, ctl, st);
+    return p.b_rows == 1 ? pair_pick<true>(tmA, tmB, tm_c, g, f32, ctl, st)
+                         : pair_pick<false>(tmA, tmB, tm_c, g, f32, ctl, st);
   }
   g.split = plan.split;
   if (plan.swap) {

@@ -380,6 +380,11 @@ def test_matmul(dsv, shape, ar, br, ta, tb, dt):
         was = acc.clone()
         dsv.matmul_fp8(a, sa, b, sb, out=acc, accumulate=True)
         _check(acc, ref + to64(was), tol + 2.0 ** -23 * (np.abs(ref) + np.abs(to64(was))), "c + a b^T")
+        # rows on 16 bytes that end inside a unit of 16 bytes
+        wide = torch.full((M, -(-N // 4) * 4 + 4), 7.0, device="cuda")
+        wide[:, :N] = was
+        dsv.matmul_fp8(a, sa, b, sb, out=wide[:, :N], accumulate=True)
+        assert torch.equal(wide[:, :N], acc) and (wide[:, N:] == 7).all()
     _clean(dsv)
 
 
