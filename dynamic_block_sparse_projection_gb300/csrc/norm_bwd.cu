@@ -587,14 +587,19 @@ Stream stream_of(const dsv_norm& p, int xsize) {
     s.ch = ceil_div(chunks, s.gw);
     s.rows = s.gw == 32 ? 2 : 1;
   } else {
-    // Whole warps: the time of a row goes by (chunks a thread + 1) / teams.
+    // Whole warps: a row of 1, 2 or 3 chunks a thread takes a team a time of 10, 16 or 28,
+    // and a quarter more where shared memory has no room for two rows at once.  Measured,
+    // 1, 2 and 3 chunks: rows of 1160 (17154, fp32) 48.4, 47.8, 52 us, of 2048 (122880) 314,
+    // 246, 263, of 640 (30000, fp32) 45.7, 47.8, 52, of 5120 (16384) -, 119, 108.
     s.rows = 2;
     s.gw = 0;
+    const int cost[4] = {10, 16, 28, 0};
     int best = 0;
     for (int ch = 1; ch <= 4; ++ch) {
       const int gw = ceil_div(ceil_div(chunks, ch), 32) * 32, teams = kTeamThreads / gw;
       if (teams == 0 || (ch == 4 && s.gw != 0)) continue;
-      const int speed = 1000 * teams / (ch + 1);
+      const bool two = 4 * teams * row + sums <= kStreamBytes;
+      const int speed = ch == 4 ? 1 : teams * (two ? 5000 : 4000) / cost[ch - 1];
       if (speed > best) best = speed, s.gw = gw, s.ch = ceil_div(chunks, gw);
     }
   }
@@ -648,16 +653,21 @@ cudaError_t bwd_stream(const dsv_rows& dy, const dsv_rows& x, const float* stats
 template <typename X>
 cudaError_t bwd_pick(const dsv_rows& dy, const dsv_rows& x, const float* stats, const NormArgs& a, const Stream& s,
                      const float* w, const dsv_rows& dx, float* parts, const Ctl& ctl, cudaStream_t st) {
-  switch (2 * s.ch + s.rows) {
-    case 3: return bwd_stream<X, 1, 1>(dy, x, stats, a, s, w, dx, parts, ctl, st);
-    case 4: return bwd_stream<X, 1, 2>(dy, x, stats, a, s, w, dx, parts, ctl, st);
-    case 5: return bwd_stream<X, 2, 1>(dy, x, stats, a, s, w, dx, parts, ctl, st);
-    case 6: return bwd_stream<X, 2, 2>(dy, x, stats, a, s, w, dx, parts, ctl, st);
-    case 7: return bwd_stream<X, 3, 1>(dy, x, stats, a, s, w, dx, parts, ctl, st);
-    case 8: return bwd_stream<X, 3, 2>(dy, x, stats, a, s, w, dx, parts, ctl, st);
-    case 9: return bwd_stream<X, 4, 1>(dy, x, stats, a, s, w, dx, parts, ctl, st);
-    default: return bwd_stream<X, 4, 2>(dy, x, stats, a, s, w, dx, parts, ctl, st);
+  constexpr bool WORDS = sizeof(X) == 4;         // what only one type's rows get
+  switch (10 * s.ch + s.rows) {
+    case 11: return bwd_stream<X, 1, 1>(dy, x, stats, a, s, w, dx, parts, ctl, st);
+    case 21: return bwd_stream<X, 2, 1>(dy, x, stats, a, s, w, dx, parts, ctl, st);
+    case 22: return bwd_stream<X, 2, 2>(dy, x, stats, a, s, w, dx, parts, ctl, st);
+    case 32: return bwd_stream<X, 3, 2>(dy, x, stats, a, s, w, dx, parts, ctl, st);
+    case 41: return bwd_stream<X, 4, 1>(dy, x, stats, a, s, w, dx, parts, ctl, st);
   }
+  if constexpr (WORDS) {
+    if (s.ch == 1) return bwd_stream<X, 1, 2>(dy, x, stats, a, s, w, dx, parts, ctl, st);
+    if (s.ch == 3) return bwd_stream<X, 3, 1>(dy, x, stats, a, s, w, dx, parts, ctl, st);
+  } else {
+    if (s.ch == 4) return bwd_stream<X, 4, 2>(dy, x, stats, a, s, w, dx, parts, ctl, st);
+  }
+  return cudaErrorInvalidValue;                  // no width gives another pair
 }
 
 template <typename X, int LG, int NE>
