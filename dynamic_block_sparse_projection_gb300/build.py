@@ -27,7 +27,7 @@ LIB = OUT / "libdsv.so"
 CALLS = OUT / ("dsv_calls" + importlib.machinery.EXTENSION_SUFFIXES[0])
 SOURCES = ["dsv_api.cu", "predict.cu", "topk.cu", "attn_fwd.cu", "attn_bwd.cu", "topk_noalloc.cu", "cube.cu",
            "predict_max.cu", "predict_topk.cu", "packed_fwd.cu", "packed_bwd.cu", "rope.cu", "norm_fwd.cu",
-           "norm_bwd.cu", "quantize.cu", "matmul_fp8.cu"]
+           "norm_bwd.cu", "norm_narrow.cu", "quantize.cu", "matmul_fp8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

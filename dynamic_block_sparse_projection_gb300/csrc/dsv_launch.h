@@ -137,6 +137,11 @@ size_t norm_bwd_ws_bytes(const dsv_norm& p);
 cudaError_t launch_norm_bwd(const dsv_rows& dy, const dsv_rows& x, const float* stats, const dsv_norm& p,
                             const int32_t* ptr, const float* weight, const dsv_rows& dx, float* dweight, float* dbias,
                             void* ws, const Ctl& ctl, cudaStream_t st);
+// Its rows without 16-byte accesses (norm_narrow.cu): rows of a CTA, and the kernel; parts: null, or as in norm_bwd.cu.
+int norm_narrow_rows(const dsv_norm& p);
+cudaError_t launch_norm_bwd_narrow(const dsv_rows& dy, const dsv_rows& x, const float* stats, const dsv_norm& p,
+                                   const int32_t* ptr, const float* weight, const dsv_rows& dx, float* parts, const Ctl& ctl,
+                                   cudaStream_t st);
 
 // 8-bit quantiser and product (quantize.cu, matmul_fp8.cu).  Tensor maps of the
 // product: [rows, K] bytes, boxes of 128 bytes x matmul_boxes' rows; C in boxes of

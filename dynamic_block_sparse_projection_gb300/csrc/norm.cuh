@@ -80,6 +80,60 @@ __device__ __forceinline__ float both(uint64_t v) {
   return a + b;
 }
 
+// How a CTA of the backward goes through its rows.
+struct StreamArgs {
+  int R;                   // rows of a CTA
+  int unit, teams, slots;  // rows that a team works on at once; teams; slots of a team's ring
+  int one;                 // the rows of x (bit 0) and dy (bit 1) follow each other without gaps
+  int sums;                // room in shared memory for sums: none, a team's, all teams'
+};
+
+// A team's way through the CTA's rows: the parts of the sequences in them, and in each the team's units.
+struct Walk {
+  const NormArgs& a;
+  const StreamArgs& sa;
+  int row0, row1, s, p, q, r;              // sequence, its rows here, the unit's first row
+  int slot;
+  uint32_t phase;
+  __device__ Walk(const NormArgs& args, const StreamArgs& stream)
+      : a(args), sa(stream), s(-1), p(0), q(0), r(0), slot(-1), phase(0) {
+    row0 = (int)blockIdx.x * sa.R;
+    row1 = (int)min((long long)row0 + sa.R, (long long)a.T);
+    if (a.ptr == nullptr) {
+      if (a.S > 1) s = row0 / a.even - 1;
+    } else {                                      // the first sequence that ends behind row0
+      int lo = 0, hi = a.S;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(a.ptr + mid + 1) > row0) hi = mid; else lo = mid + 1;
+      }
+      s = lo - 1;
+    }
+  }
+  // the next sequence with rows here, and the team's first unit in it
+  __device__ bool next_sequence(int team) {
+    while (++s < a.S) {
+      p = a.ptr == nullptr ? (a.S == 1 ? 0 : s * a.even) : __ldg(a.ptr + s);
+      q = a.ptr == nullptr ? (a.S == 1 ? a.T : (s + 1) * a.even) : __ldg(a.ptr + s + 1);
+      if (p >= row1) return false;
+      p = max(p, row0);
+      q = min(q, row1);
+      r = p + team * sa.unit;
+      if (p < q) return true;
+    }
+    return false;
+  }
+  __device__ void next_unit() { r += sa.teams * sa.unit; }
+  __device__ void take_slot() {
+    if (++slot == sa.slots) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+__device__ __forceinline__ void cta_sync() { asm volatile("bar.sync 0;" ::: "memory"); }
+
 inline int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 inline NormArgs norm_args(const dsv_norm& p, const int32_t* ptr) {
   NormArgs a;

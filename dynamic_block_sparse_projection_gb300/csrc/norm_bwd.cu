@@ -16,7 +16,7 @@ namespace {
 // ---------------------------------------------------------------------------
 // A row belongs to `gw` neighbouring threads, 2 to 512 of them, CH chunks of 8
 // columns each.  The warps that share a row, or the one warp that holds several,
-// are a team, which works on two rows at once where they are whole warps: an
+// are a team, which works on two rows (of a thread) at once where two slots of them fit: an
 // exchange of sums, a wait and the rest of the fixed cost (some 200 instructions)
 // serve both.  Every team has a ring of slots that its first warp fills by bulk
 // copies, so that bytes in flight cost no registers and no team waits for another.
@@ -26,57 +26,6 @@ namespace {
 // rows of 5120 109 us, 68 %; 16384 of 8192 146 us, 81 %.
 constexpr int kStreamBytes = 220 * 1024;       // of shared memory
 constexpr int kTeamThreads = 512, kTeamWarps = kTeamThreads / 32, kMaxSlots = 8;
-
-struct StreamArgs {
-  int R;                   // rows of a CTA
-  int unit, teams, slots;  // rows that a team works on at once; teams; slots of a team's ring
-  int one;                 // the rows of x (bit 0) and dy (bit 1) follow each other without gaps
-  int sums;                // the teams' joined sums in shared memory
-};
-
-// A team's way through the CTA's rows: the parts of the sequences in them, and in each the team's units.
-struct Walk {
-  const NormArgs& a;
-  const StreamArgs& sa;
-  int row0, row1, s, p, q, r;              // sequence, its rows here, the unit's first row
-  int slot;
-  uint32_t phase;
-  __device__ Walk(const NormArgs& args, const StreamArgs& stream)
-      : a(args), sa(stream), s(-1), p(0), q(0), r(0), slot(-1), phase(0) {
-    row0 = (int)blockIdx.x * sa.R;
-    row1 = (int)min((long long)row0 + sa.R, (long long)a.T);
-    if (a.ptr == nullptr) {
-      if (a.S > 1) s = row0 / a.even - 1;
-    } else {                                      // the first sequence that ends behind row0
-      int lo = 0, hi = a.S;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(a.ptr + mid + 1) > row0) hi = mid; else lo = mid + 1;
-      }
-      s = lo - 1;
-    }
-  }
-  // the next sequence with rows here, and the team's first unit in it
-  __device__ bool next_sequence(int team) {
-    while (++s < a.S) {
-      p = a.ptr == nullptr ? (a.S == 1 ? 0 : s * a.even) : __ldg(a.ptr + s);
-      q = a.ptr == nullptr ? (a.S == 1 ? a.T : (s + 1) * a.even) : __ldg(a.ptr + s + 1);
-      if (p >= row1) return false;
-      p = max(p, row0);
-      q = min(q, row1);
-      r = p + team * sa.unit;
-      if (p < q) return true;
-    }
-    return false;
-  }
-  __device__ void next_unit() { r += sa.teams * sa.unit; }
-  __device__ void take_slot() {
-    if (++slot == sa.slots) {
-      slot = 0;
-      phase ^= 1u;
-    }
-  }
-};
 
 // 8 columns as four pairs of fp32
 __device__ __forceinline__ void pairs8(const __nv_bfloat16* p, uint64_t* v) {
@@ -103,7 +52,6 @@ __device__ __forceinline__ void store_pairs8(float* p, const uint64_t* v) {
   *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(v[0], v[1]);
   *reinterpret_cast<ulonglong2*>(p + 4) = make_ulonglong2(v[2], v[3]);
 }
-__device__ __forceinline__ void cta_sync() { asm volatile("bar.sync 0;" ::: "memory"); }
 
 // Sums of N values over the threads of a row, N = 1, 2 or 4.  Over whole
 // warps, a lane gives away half of its values at each of the first steps, so
@@ -221,16 +169,16 @@ struct Loader {
 // What the streamed kernels begin with: the barriers, and the thread's place.
 struct Place {
   int gw, team, gl, lane;                         // threads of a row; team; thread in the row; lane
-  int sub;                                        // row of the unit
+  int sub;                                        // its first row of the unit
   bool first, idle;                               // is this the team's first warp; in no team
-  __device__ Place(const NormArgs& a, const StreamArgs& sa) {
+  __device__ Place(const NormArgs& a, const StreamArgs& sa, int rows) {
     gw = a.gw;
     lane = threadIdx.x & 31;
     team = gw > 32 ? threadIdx.x / gw : threadIdx.x >> 5;
     idle = team >= sa.teams;
     first = !idle && (int)threadIdx.x - team * max(gw, 32) < 32;
     gl = threadIdx.x % gw;
-    sub = gw < 32 ? lane / gw : 0;
+    sub = gw < 32 ? lane / gw * rows : 0;
   }
 };
 __device__ __forceinline__ void stream_begin(uint64_t* full, int n, int* abort_word) {
@@ -290,7 +238,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1)
   volatile int* abort_flag = &abort_word;
   cudaTriggerProgrammaticLaunchCompletion();      // norm_sums_kernel may come to wait
   stream_begin(full, sa.teams * sa.slots, &abort_word);
-  const Place me(a, sa);
+  const Place me(a, sa, ROWS);
   const uint32_t xbytes = (uint32_t)sa.unit * a.C * sizeof(X), unit_bytes = xbytes + (uint32_t)sa.unit * a.C * 2u;
   uint8_t* mine = ring + (size_t)me.team * sa.slots * unit_bytes;
   uint64_t* bar = full + me.team * sa.slots;
@@ -414,6 +362,27 @@ __global__ void __launch_bounds__(kTeamThreads, 1)
         }
     }
     const int turns = min(sa.teams, (at.q - at.p + sa.unit - 1) / sa.unit);
+    if (CH <= 2 && sa.sums > 1 && turns > 1) {
+      // few columns: all teams at once (6 sequences of 22620 rows of 360: 42 us with 16 turns, 35 so)
+      if (me.team < turns && me.sub == 0) {
+        float* to = near + 2 * a.C * me.team;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          if (i < CH - 1 || last) {
+            store_pairs8(to + 8 * (i * gw + gl), dw[i]);
+            store_pairs8(to + a.C + 8 * (i * gw + gl), db[i]);
+          }
+        }
+      }
+      cta_sync();
+      for (int c = threadIdx.x; c < 2 * a.C; c += kTeamThreads) {
+        float t = near[c];
+        for (int k = 1; k < turns; ++k) t += near[2 * a.C * k + c];
+        out[c] = t;
+      }
+      cta_sync();
+      continue;
+    }
     for (int k = 0; k < turns; ++k) {
       if (me.team == k && me.sub == 0) {
         float* to = k == turns - 1 ? out : held;
@@ -442,92 +411,6 @@ __global__ void __launch_bounds__(kTeamThreads, 1)
   if (me.first && used < in.issued) in.drain(used, ctl);
 }
 
-// ---------------------------------------------------------------------------
-// Rows without 16-byte accesses (an odd width, an odd start)
-// ---------------------------------------------------------------------------
-// One element at a time, neighbouring threads on neighbouring columns: thread gl of
-// a row's 2^LG holds the columns e 2^LG + gl, e < NE, of which those of the first
-// half lie inside the row.  dx may be dy or x.
-__host__ __device__ constexpr int narrow_threads(int lg) { return lg > 8 ? 1 << lg : kNormThreads; }
-template <typename X, int LG, int NE>
-__global__ void __launch_bounds__(narrow_threads(LG), LG <= 8 ? 2 : 1)
-    norm_bwd_narrow_kernel(const __nv_bfloat16* dy, long long dys, const X* x, long long xs,
-                           const float* __restrict__ stats, const float* __restrict__ weight, X* dx, long long dxs,
-                           float* parts, int R, NormArgs a, Ctl ctl) {
-  constexpr int GW = 1 << LG, THREADS = narrow_threads(LG), GROUPS = THREADS / GW;
-  cudaTriggerProgrammaticLaunchCompletion();      // norm_sums_kernel may come to wait
-  extern __shared__ float sums[];                 // 2 C floats
-  __shared__ float slot[2][2][THREADS / 32];
-  check_ptr(a, ctl);
-  const int group = threadIdx.x >> LG, gl = threadIdx.x & (GW - 1);
-  const float inv_c = 1.0f / (float)a.C;
-  auto in = [&](int e) { return (NE > 4 && e < NE / 2) || e * GW + gl < a.C; };
-  StreamArgs sa;
-  sa.R = R;
-  sa.unit = 1;
-  sa.teams = GROUPS;
-  Walk at(a, sa);
-  int parity = 0;
-  while (at.next_sequence(group)) {
-    const float* w = weight + (long long)at.s * a.C + gl;
-    float dw[NE], db[NE], wk[NE <= 16 ? NE : 1];
-#pragma unroll
-    for (int e = 0; e < NE; ++e) {
-      dw[e] = db[e] = 0.f;
-      if constexpr (NE <= 16) wk[e] = weight != nullptr && in(e) ? __ldg(w + e * GW) : 1.f;
-    }
-    for (; at.r < at.q; at.next_unit()) {
-      const X* px = x + at.r * xs + gl;
-      const __nv_bfloat16* pg = dy + at.r * dys + gl;
-      X* out = dx + at.r * dxs + gl;
-      float h[NE], g[NE];
-#pragma unroll
-      for (int e = 0; e < NE; ++e) {
-        h[e] = in(e) ? to_f32(px[e * GW]) : 0.f;
-        g[e] = in(e) ? to_f32(pg[e * GW]) : 0.f;
-      }
-      const float mean = __ldg(stats + at.r), rstd = __ldg(stats + a.T + at.r);
-      float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-      for (int e = 0; e < NE; ++e) {
-        h[e] = in(e) ? (h[e] - mean) * rstd : 0.f;
-        dw[e] = fmaf(g[e], h[e], dw[e]);
-        db[e] += g[e];
-        if constexpr (NE <= 16) {
-          g[e] *= wk[e];
-        } else {
-          if (weight != nullptr && in(e)) g[e] *= __ldg(w + e * GW);
-        }
-        s1 += g[e];
-        s2 = fmaf(g[e], h[e], s2);
-      }
-      s1 = row_sum<GW>(s1, slot[parity][0]) * inv_c;
-      s2 = row_sum<GW>(s2, slot[parity][1]) * inv_c;
-      parity ^= 1;
-#pragma unroll
-      for (int e = 0; e < NE; ++e)
-        if (in(e)) put(out + e * GW, rstd * (g[e] - s1 - h[e] * s2));
-    }
-    if (parts == nullptr) continue;
-    // the groups' sums, one behind the other
-    float* out = parts + 2LL * a.C * ((long long)blockIdx.x + at.s);
-    for (int k = 0; k < GROUPS; ++k) {
-      if (group == k) {
-        float* to = k == GROUPS - 1 ? out : sums;
-#pragma unroll
-        for (int e = 0; e < NE; ++e) {
-          const int c = e * GW + gl;
-          if (in(e)) {
-            to[c] = k > 0 ? sums[c] + dw[e] : dw[e];
-            to[a.C + c] = k > 0 ? sums[a.C + c] + db[e] : db[e];
-          }
-        }
-      }
-      if (GROUPS > 1) cta_sync();
-    }
-  }
-}
-
 // dw_s, db_s: the parts of sequence s, in the order of their rows.  WARPS warps
 // share 32 columns and take every WARPS-th part; with many sequences of few parts
 // each, a warp has its columns to itself (the gradient of 2000 sequences of 30 rows of
@@ -549,14 +432,14 @@ __global__ void __launch_bounds__(kNormThreads) norm_sums_kernel(const float* pa
     const long long step = 2LL * a.C;
     const float* at = parts + step * s + c2;
     int k = p / R + turn;
-    for (; k + 3 * WARPS <= last; k += 4 * WARPS) {
-      float v[4];
+    constexpr int N = WARPS > 1 ? 20 : 4;            // 152 parts of one CTA an SM: 19 a warp
+    for (; k <= last; k += N * WARPS) {
+      float v[N];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __ldcg(at + step * (k + i * WARPS));
+      for (int i = 0; i < N; ++i) v[i] = k + i * WARPS <= last ? __ldcg(at + step * (k + i * WARPS)) : 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) t += v[i];
+      for (int i = 0; i < N; ++i) t += v[i];
     }
-    for (; k <= last; k += WARPS) t += __ldcg(at + step * k);
   }
   if constexpr (WARPS > 1) {
     sum[warp][lane] = t;
@@ -579,13 +462,14 @@ struct Stream {
 Stream stream_of(const dsv_norm& p, int xsize) {
   Stream s;
   const int chunks = p.C / 8;
-  s.a.sums = p.C <= 2048 ? 1 : 0;
-  const int row = p.C * (xsize + 2), sums = s.a.sums ? 8 * p.C : 0;
+  // all teams' sums leave room for two slots of two rows up to 512 columns
+  s.a.sums = p.C <= 512 ? 2 : p.C <= 2048 ? 1 : 0;
+  const int row = p.C * (xsize + 2), sums = s.a.sums == 2 ? 8 * p.C * kTeamWarps : s.a.sums ? 8 * p.C : 0;
   if (chunks <= 64) {                              // part of a warp, two chunks a thread
     s.gw = 2;
     while (chunks > 2 * s.gw) s.gw *= 2;
     s.ch = ceil_div(chunks, s.gw);
-    s.rows = s.gw == 32 ? 2 : 1;
+    s.rows = 2;
   } else {
     // Whole warps: a row of 1, 2 or 3 chunks a thread takes a team a time of 10, 16 or 28,
     // and a quarter more where shared memory has no room for two rows at once.  Measured,
@@ -604,7 +488,7 @@ Stream stream_of(const dsv_norm& p, int xsize) {
     }
   }
   for (;;) {                                       // two slots a team, or one row at once, or fewer teams
-    s.a.unit = s.gw < 32 ? 32 / s.gw : s.rows;
+    s.a.unit = s.gw < 32 ? 32 / s.gw * s.rows : s.rows;
     s.a.teams = kTeamThreads / max(s.gw, 32);
     if (2 * s.a.teams * s.a.unit * row + sums <= kStreamBytes) break;
     if (s.rows == 2) {
@@ -623,22 +507,6 @@ Stream stream_of(const dsv_norm& p, int xsize) {
   return s;
 }
 
-// Narrow rows: threads of a row (2^lg), columns of a thread, rows of a CTA.
-struct Narrow {
-  int lg, ne, R;
-};
-Narrow narrow_of(const dsv_norm& p) {
-  Narrow n;
-  n.lg = 5;
-  n.ne = 4;
-  while (n.ne << n.lg < p.C && n.ne < 16) n.ne *= 2;
-  while (n.ne << n.lg < p.C && n.lg < 9) ++n.lg;
-  if (n.ne << n.lg < p.C) n.ne *= 2;
-  const int groups = narrow_threads(n.lg) >> n.lg;
-  n.R = ceil_div(ceil_div(p.T, 2 * kSMs), groups) * groups;
-  return n;
-}
-
 template <typename X, int CH, int ROWS>
 cudaError_t bwd_stream(const dsv_rows& dy, const dsv_rows& x, const float* stats, const NormArgs& a, const Stream& s,
                        const float* w, const dsv_rows& dx, float* parts, const Ctl& ctl, cudaStream_t st) {
@@ -653,16 +521,14 @@ cudaError_t bwd_stream(const dsv_rows& dy, const dsv_rows& x, const float* stats
 template <typename X>
 cudaError_t bwd_pick(const dsv_rows& dy, const dsv_rows& x, const float* stats, const NormArgs& a, const Stream& s,
                      const float* w, const dsv_rows& dx, float* parts, const Ctl& ctl, cudaStream_t st) {
-  constexpr bool WORDS = sizeof(X) == 4;         // what only one type's rows get
   switch (10 * s.ch + s.rows) {
-    case 11: return bwd_stream<X, 1, 1>(dy, x, stats, a, s, w, dx, parts, ctl, st);
-    case 21: return bwd_stream<X, 2, 1>(dy, x, stats, a, s, w, dx, parts, ctl, st);
+    case 12: return bwd_stream<X, 1, 2>(dy, x, stats, a, s, w, dx, parts, ctl, st);
     case 22: return bwd_stream<X, 2, 2>(dy, x, stats, a, s, w, dx, parts, ctl, st);
     case 32: return bwd_stream<X, 3, 2>(dy, x, stats, a, s, w, dx, parts, ctl, st);
     case 41: return bwd_stream<X, 4, 1>(dy, x, stats, a, s, w, dx, parts, ctl, st);
   }
-  if constexpr (WORDS) {
-    if (s.ch == 1) return bwd_stream<X, 1, 2>(dy, x, stats, a, s, w, dx, parts, ctl, st);
+  if constexpr (sizeof(X) == 4) {                // what only one type's rows get
+    if (s.ch == 2) return bwd_stream<X, 2, 1>(dy, x, stats, a, s, w, dx, parts, ctl, st);
     if (s.ch == 3) return bwd_stream<X, 3, 1>(dy, x, stats, a, s, w, dx, parts, ctl, st);
   } else {
     if (s.ch == 4) return bwd_stream<X, 4, 2>(dy, x, stats, a, s, w, dx, parts, ctl, st);
@@ -670,36 +536,11 @@ cudaError_t bwd_pick(const dsv_rows& dy, const dsv_rows& x, const float* stats, 
   return cudaErrorInvalidValue;                  // no width gives another pair
 }
 
-template <typename X, int LG, int NE>
-cudaError_t bwd_narrow(const dsv_rows& dy, const dsv_rows& x, const float* stats, const NormArgs& a, const float* w,
-                       const dsv_rows& dx, float* parts, int R, const Ctl& ctl, cudaStream_t st) {
-  const int smem = LG < 8 ? 2 * a.C * (int)sizeof(float) : 0;       // at most 16 KB
-  norm_bwd_narrow_kernel<X, LG, NE><<<ceil_div(a.T, R), narrow_threads(LG), smem, st>>>(
-      static_cast<const __nv_bfloat16*>(dy.ptr), dy.stride, static_cast<const X*>(x.ptr), x.stride, stats, w,
-      static_cast<X*>(dx.ptr), dx.stride, parts, R, a, ctl);
-  return cudaGetLastError();
-}
-template <typename X>
-cudaError_t narrow_pick(const dsv_rows& dy, const dsv_rows& x, const float* stats, const NormArgs& a, const Narrow& n,
-                        const float* w, const dsv_rows& dx, float* parts, const Ctl& ctl, cudaStream_t st) {
-  switch (100 * n.lg + n.ne) {
-    case 504: return bwd_narrow<X, 5, 4>(dy, x, stats, a, w, dx, parts, n.R, ctl, st);
-    case 508: return bwd_narrow<X, 5, 8>(dy, x, stats, a, w, dx, parts, n.R, ctl, st);
-    case 516: return bwd_narrow<X, 5, 16>(dy, x, stats, a, w, dx, parts, n.R, ctl, st);
-    case 616: return bwd_narrow<X, 6, 16>(dy, x, stats, a, w, dx, parts, n.R, ctl, st);
-    case 716: return bwd_narrow<X, 7, 16>(dy, x, stats, a, w, dx, parts, n.R, ctl, st);
-    case 816: return bwd_narrow<X, 8, 16>(dy, x, stats, a, w, dx, parts, n.R, ctl, st);
-    case 916: return bwd_narrow<X, 9, 16>(dy, x, stats, a, w, dx, parts, n.R, ctl, st);
-    case 932: return bwd_narrow<X, 9, 32>(dy, x, stats, a, w, dx, parts, n.R, ctl, st);
-    default: return cudaErrorInvalidValue;         // no width gives another pair
-  }
-}
-
 }  // namespace
 
 // The call's alignment is not known here: room for either way.
 size_t norm_bwd_ws_bytes(const dsv_norm& p) {
-  const int R = min(narrow_of(p).R, min(stream_of(p, 2).a.R, stream_of(p, 4).a.R));
+  const int R = min(norm_narrow_rows(p), min(stream_of(p, 2).a.R, stream_of(p, 4).a.R));
   return ((size_t)ceil_div(p.T, R) + p.S) * 2 * p.C * sizeof(float);
 }
 
@@ -720,10 +561,8 @@ cudaError_t launch_norm_bwd(const dsv_rows& dy, const dsv_rows& x, const float* 
     e = x.type == DSV_F32 ? bwd_pick<float>(dy, x, stats, a, s, weight, dx, parts, ctl, st)
                           : bwd_pick<__nv_bfloat16>(dy, x, stats, a, s, weight, dx, parts, ctl, st);
   } else {
-    const Narrow n = narrow_of(p);
-    R = n.R;
-    e = x.type == DSV_F32 ? narrow_pick<float>(dy, x, stats, a, n, weight, dx, parts, ctl, st)
-                          : narrow_pick<__nv_bfloat16>(dy, x, stats, a, n, weight, dx, parts, ctl, st);
+    R = norm_narrow_rows(p);
+    e = launch_norm_bwd_narrow(dy, x, stats, p, a.ptr, weight, dx, parts, ctl, st);
   }
   if (e != cudaSuccess || parts == nullptr) return e;
   // it comes as the rows' CTAs leave room, and waits for them
