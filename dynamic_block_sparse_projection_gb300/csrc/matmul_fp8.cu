@@ -230,15 +230,16 @@ __device__ __forceinline__ void stores_done(const MmArgs& g) {
 // the tile, out of all CTAs' shared memory in their order, and writes it.
 constexpr int kSmallThreads = 320;         // 8 warps that scale, then the copying and the issuing warp
 constexpr int kCopyWarp = 8, kIssueWarp = 9;
-constexpr int kAhead = 16;                 // blocks whose scales are under way: as much as a first read of memory takes
 
 template <int BN>
 struct SmallTraits {
   static constexpr int P_BYTES = 128 * kKb, Q_BYTES = BN * kKb, STAGE = P_BYTES + Q_BYTES;
-  static constexpr int STAGES = BN == 128 ? 5 : BN == 64 ? 7 : 9;
+  static constexpr int CTAS = BN == 32 ? 2 : 1;            // of an SM
+  static constexpr int STAGES = BN == 128 ? 5 : BN == 64 ? 7 : 4;
+  static constexpr int AHEAD = BN == 32 ? 12 : 16;         // blocks whose scales are under way: a first read of memory's time
   static constexpr int BUFS = BN == 128 ? 4 : 8;
   static constexpr int TMEM = BUFS * BN;
-  static constexpr int SMEM = STAGES * STAGE + kAhead * 2 * 256 * 4 + 1024;
+  static constexpr int SMEM = STAGES * STAGE + AHEAD * 2 * 256 * 4 + 1024;
   static_assert(STAGES * STAGE >= 128 * BN * 4, "the tile's sums take the stages' place");
 };
 
@@ -297,10 +298,10 @@ __device__ __forceinline__ void store4(const MmArgs& g, int rows, int cols, int 
 // g is that of the tile's rows (M, sa: b's with SWAP) and columns (N, sb).
 // COLV: a scale for each column; else one for 128 of them.
 template <int BN, bool SWAP, bool COLV, bool F32>
-__global__ void __launch_bounds__(kSmallThreads, 1)
+__global__ void __launch_bounds__(kSmallThreads, SmallTraits<BN>::CTAS)
     matmul_small_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, MmArgs g, Ctl ctl) {
   using T = SmallTraits<BN>;
-  constexpr int NST = T::STAGES, NB = T::BUFS, HALF = BN / 2;
+  constexpr int NST = T::STAGES, NB = T::BUFS, HALF = BN / 2, AHEAD = T::AHEAD;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = smem_align1024(raw);
   __shared__ uint64_t full[NST], empty[NST], sums[NB], freed[NB], drain;
@@ -384,25 +385,25 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     uint64_t acc[HALF / 2];
 #pragma unroll
     for (int j = 0; j < HALF / 2; ++j) acc[j] = 0ull;
-    // a thread brings in the scales of its row and of a column, kAhead blocks before their use
+    // a thread brings in the scales of its row and of a column, AHEAD blocks before their use
     const int me = (int)threadIdx.x;
     auto fetch = [&](int n) {
       if (n < kbs) {
-        copy4(scales + (n % kAhead) * 512 + me, in ? pa + n * g.sa_ld : g.sa, in);
-        copy4(scales + (n % kAhead) * 512 + 256 + me, col_in ? pb + n * g.sb_ld : g.sb, col_in);
+        copy4(scales + (n % AHEAD) * 512 + me, in ? pa + n * g.sa_ld : g.sa, in);
+        copy4(scales + (n % AHEAD) * 512 + 256 + me, col_in ? pb + n * g.sb_ld : g.sb, col_in);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    for (int i = 0; i < kAhead - 2; ++i) fetch(i);
+    for (int i = 0; i < AHEAD - 2; ++i) fetch(i);
     uint32_t here = 0;                         // the next block's sums are known to be complete
     // a failed wait: the loop goes on, past the barriers, without work
     for (int n = 0; n < kbs; ++n) {
       const int buf = n % NB;
-      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 3) : "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 3) : "memory");
       if (COLV) asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-      fetch(n + kAhead - 2);
-      const float* w = scales + (n % kAhead) * 512 + 256;
-      const float f = COLV ? scales[(n % kAhead) * 512 + me] : scales[(n % kAhead) * 512 + me] * w[me];
+      fetch(n + AHEAD - 2);
+      const float* w = scales + (n % AHEAD) * 512 + 256;
+      const float f = COLV ? scales[(n % AHEAD) * 512 + me] : scales[(n % AHEAD) * 512 + me] * w[me];
       if (ok) ok = mbar_wait_warp_tested(&sums[buf], (uint32_t)(n / NB) & 1u, here, abort_flag, ctl, kid | W_SUMS);
       if (!ok) continue;
       tc_fence_after();
@@ -894,10 +895,13 @@ cudaError_t pair_pick(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUte
 // how many CTAs a tile's blocks of K are split.  The times behind the choice are
 // those measured (in 10 ns; 152 SMs): a block of K 0.34 us in a small tile and 0.47
 // in a pair's (0.49 and 0.57 with a scale for each column), a tile's beginning and
-// end 4.5 us, or 1.4 in a pair that goes on to the next tile; joining the sums 0.8
-// to 3 us; and clusters of 2, 4 and 8 CTAs find 148, 128 and 104 SMs.  Against
-// measured calls it is off by up to 10 %: 640 x 1160 x 40000 has 160 us as small
-// tiles, 85 split in two and 89 in four, and is estimated at 158, 82 and 88.
+// end 4.5 us, or 1.4 in a pair that goes on to the next tile; joining the sums 1 to
+// 3 us; and clusters of 2, 4 and 8 CTAs find 148, 128 and 104 SMs.  Tiles of 32
+// columns, two CTAs an SM, share its 0.34 us a block (0.40 alone) and begin and end
+// beside each other: one token x [24576, 2048] 24 -> 19 us, 30000 x 32 x 2048 24 -> 21,
+// [12288, 2048] 14 either way.  Against measured calls it is off by up to 10 %: 640 x
+// 1160 x 40000 has 160 us as small tiles, 85 split in two and 89 in four, and is
+// estimated at 158, 82 and 88.
 struct Plan {
   bool pair, swap;
   int bn, split;           // without pairs
@@ -911,11 +915,13 @@ Plan plan_of(const dsv_matmul& p) {
   plan.bn = cols <= 32 ? 32 : cols <= 64 ? 64 : 128;
   const long long tiles = (long long)((rows + 127) / 128) * ((cols + plan.bn - 1) / plan.bn);
   const int block = colv && plan.bn == 128 ? 49 : 34;
-  const int slots[4] = {kSMs, 148, 128, 104}, join[4] = {0, 80, 110, 300};
+  const int ctas = plan.bn == 32 ? 2 : 1;
+  const int slots[4] = {kSMs, 148, 128, 104}, join[4] = {0, 100, 110, 300};
   long long best = 0;
   for (int i = 0; i < 4 && 1 << i <= kbs; ++i) {
-    const long long waves = ((tiles << i) + slots[i] - 1) / slots[i];
-    const long long time = waves * ((long long)((kbs + (1 << i) - 1) >> i) * block + 450) + join[i];
+    const long long n = tiles << i, rounds = (n + slots[i] - 1) / slots[i], waves = (rounds + ctas - 1) / ctas;
+    const long long time =
+        rounds * ((kbs + (1 << i) - 1) >> i) * (ctas == 2 && rounds == 1 ? 40 : block) + waves * 450 + join[i];
     if (i == 0 || time < best) best = time, plan.split = 1 << i;
   }
   if (p.M > 128 && p.N > 128) {
