@@ -231,12 +231,12 @@ __device__ __forceinline__ void stores_done(const MmArgs& g) {
 constexpr int kSmallThreads = 320;         // 8 warps that scale, then the copying and the issuing warp
 constexpr int kCopyWarp = 8, kIssueWarp = 9;
 
-template <int BN>
+// DUAL: two CTAs an SM, where there are more of them than SMs (BN = 32).
+template <int BN, bool DUAL>
 struct SmallTraits {
   static constexpr int P_BYTES = 128 * kKb, Q_BYTES = BN * kKb, STAGE = P_BYTES + Q_BYTES;
-  static constexpr int CTAS = BN == 32 ? 2 : 1;            // of an SM
-  static constexpr int STAGES = BN == 128 ? 5 : BN == 64 ? 7 : 4;
-  static constexpr int AHEAD = BN == 32 ? 12 : 16;         // blocks whose scales are under way: a first read of memory's time
+  static constexpr int STAGES = BN == 128 ? 5 : BN == 64 ? 7 : DUAL ? 4 : 9;
+  static constexpr int AHEAD = DUAL ? 12 : 16;             // blocks whose scales are under way: a first read of memory's time
   static constexpr int BUFS = BN == 128 ? 4 : 8;
   static constexpr int TMEM = BUFS * BN;
   static constexpr int SMEM = STAGES * STAGE + AHEAD * 2 * 256 * 4 + 1024;
@@ -297,10 +297,10 @@ __device__ __forceinline__ void store4(const MmArgs& g, int rows, int cols, int 
 
 // g is that of the tile's rows (M, sa: b's with SWAP) and columns (N, sb).
 // COLV: a scale for each column; else one for 128 of them.
-template <int BN, bool SWAP, bool COLV, bool F32>
-__global__ void __launch_bounds__(kSmallThreads, SmallTraits<BN>::CTAS)
+template <int BN, bool DUAL, bool SWAP, bool COLV, bool F32>
+__global__ void __launch_bounds__(kSmallThreads, DUAL ? 2 : 1)
     matmul_small_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ, MmArgs g, Ctl ctl) {
-  using T = SmallTraits<BN>;
+  using T = SmallTraits<BN, DUAL>;
   constexpr int NST = T::STAGES, NB = T::BUFS, HALF = BN / 2, AHEAD = T::AHEAD;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = smem_align1024(raw);
@@ -493,10 +493,10 @@ __global__ void __launch_bounds__(kSmallThreads, SmallTraits<BN>::CTAS)
   if (g.split > 1) cluster_sync();                       // no CTA leaves while its sums are read
 }
 
-template <int BN, bool SWAP, bool COLV, bool F32>
+template <int BN, bool DUAL, bool SWAP, bool COLV, bool F32>
 cudaError_t small_t(const CUtensorMap& tmP, const CUtensorMap& tmQ, const MmArgs& g, const Ctl& ctl, cudaStream_t st) {
-  using T = SmallTraits<BN>;
-  auto kern = matmul_small_kernel<BN, SWAP, COLV, F32>;
+  using T = SmallTraits<BN, DUAL>;
+  auto kern = matmul_small_kernel<BN, DUAL, SWAP, COLV, F32>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute cluster{};
@@ -512,12 +512,20 @@ cudaError_t small_t(const CUtensorMap& tmP, const CUtensorMap& tmQ, const MmArgs
   cfg.numAttrs = g.split > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, tmP, tmQ, g, ctl);
 }
+template <int BN, bool DUAL, bool SWAP>
+cudaError_t small_of(const CUtensorMap& tmP, const CUtensorMap& tmQ, const MmArgs& g, bool colv, bool f32, const Ctl& ctl,
+                     cudaStream_t st) {
+  if (colv)
+    return f32 ? small_t<BN, DUAL, SWAP, true, true>(tmP, tmQ, g, ctl, st) : small_t<BN, DUAL, SWAP, true, false>(tmP, tmQ, g, ctl, st);
+  return f32 ? small_t<BN, DUAL, SWAP, false, true>(tmP, tmQ, g, ctl, st) : small_t<BN, DUAL, SWAP, false, false>(tmP, tmQ, g, ctl, st);
+}
 template <int BN, bool SWAP>
 cudaError_t small_pick(const CUtensorMap& tmP, const CUtensorMap& tmQ, const MmArgs& g, bool colv, bool f32, const Ctl& ctl,
                        cudaStream_t st) {
-  if (colv)
-    return f32 ? small_t<BN, SWAP, true, true>(tmP, tmQ, g, ctl, st) : small_t<BN, SWAP, true, false>(tmP, tmQ, g, ctl, st);
-  return f32 ? small_t<BN, SWAP, false, true>(tmP, tmQ, g, ctl, st) : small_t<BN, SWAP, false, false>(tmP, tmQ, g, ctl, st);
+  if constexpr (BN == 32) {
+    if ((long long)g.tm * g.tn * g.split > kSMs) return small_of<BN, true, SWAP>(tmP, tmQ, g, colv, f32, ctl, st);
+  }
+  return small_of<BN, false, SWAP>(tmP, tmQ, g, colv, f32, ctl, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -896,11 +904,11 @@ cudaError_t pair_pick(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUte
 // those measured (in 10 ns; 152 SMs): a block of K 0.34 us in a small tile and 0.47
 // in a pair's (0.49 and 0.57 with a scale for each column), a tile's beginning and
 // end 4.5 us, or 1.4 in a pair that goes on to the next tile; joining the sums 1 to
-// 3 us; and clusters of 2, 4 and 8 CTAs find 148, 128 and 104 SMs.  Tiles of 32
-// columns, two CTAs an SM, share its 0.34 us a block (0.40 alone) and begin and end
-// beside each other: one token x [24576, 2048] 24 -> 19 us, 30000 x 32 x 2048 24 -> 21,
-// [12288, 2048] 14 either way.  Against measured calls it is off by up to 10 %: 640 x
-// 1160 x 40000 has 160 us as small tiles, 85 split in two and 89 in four, and is
+// 3 us; and clusters of 4 and 8 CTAs find 128 and 104 SMs.  Tiles of 32 columns, two
+// CTAs an SM where there are more of them than SMs, share its 0.34 us a block and begin
+// and end beside each other: one token x [24576, 2048] 24 -> 19 us, 30000 x 32 x 2048
+// 24 -> 21, [12288, 2048] 15 either way.  Against measured calls it is off by up to 10 %:
+// 640 x 1160 x 40000 has 160 us as small tiles, 85 split in two and 89 in four, and is
 // estimated at 158, 82 and 88.
 struct Plan {
   bool pair, swap;
@@ -916,12 +924,11 @@ Plan plan_of(const dsv_matmul& p) {
   const long long tiles = (long long)((rows + 127) / 128) * ((cols + plan.bn - 1) / plan.bn);
   const int block = colv && plan.bn == 128 ? 49 : 34;
   const int ctas = plan.bn == 32 ? 2 : 1;
-  const int slots[4] = {kSMs, 148, 128, 104}, join[4] = {0, 100, 110, 300};
+  const int slots[4] = {kSMs, kSMs, 128, 104}, join[4] = {0, 120, 110, 300};
   long long best = 0;
   for (int i = 0; i < 4 && 1 << i <= kbs; ++i) {
     const long long n = tiles << i, rounds = (n + slots[i] - 1) / slots[i], waves = (rounds + ctas - 1) / ctas;
-    const long long time =
-        rounds * ((kbs + (1 << i) - 1) >> i) * (ctas == 2 && rounds == 1 ? 40 : block) + waves * 450 + join[i];
+    const long long time = rounds * ((kbs + (1 << i) - 1) >> i) * block + waves * 450 + join[i];
     if (i == 0 || time < best) best = time, plan.split = 1 << i;
   }
   if (p.M > 128 && p.N > 128) {
