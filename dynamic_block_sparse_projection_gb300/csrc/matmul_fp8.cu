@@ -248,6 +248,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+__device__ __forceinline__ void cta_meets() { asm volatile("bar.sync 0;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -314,44 +315,53 @@ __global__ void __launch_bounds__(kSmallThreads, DUAL ? 2 : 1)
   const int rank = g.split > 1 ? (int)cluster_rank() : 0, tile = (int)blockIdx.x / g.split;
   const int row0 = (tile % g.tm) * 128, col0 = (tile / g.tm) * BN;
   const int kb0 = (int)((long long)g.kbs * rank / g.split), kbs = (int)((long long)g.kbs * (rank + 1) / g.split) - kb0;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < NST; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
-    for (int i = 0; i < NB; ++i) {
-      mbar_init(&sums[i], 1);
-      mbar_init(&freed[i], 8);
-    }
-    mbar_init(&drain, 1);
-    abort_word = 0;
-    fence_mbar_init();
-  }
-  if (warp == kIssueWarp) {
-    tmem_alloc(&tmem_slot, T::TMEM);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
+  // The first copies are under way while the tensor memory is allotted: every warp
+  // does what it can before it meets the others.
+  uint32_t tmem = 0;
+  auto begin = [&] {
+    tc_fence_before();
+    cta_meets();
+    tc_fence_after();
+    tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
+  };
   bool ok = true;
 
   if (warp == kCopyWarp) {
+    int n = 0;
+    auto load = [&](int s) {
+      mbar_arrive_expect_tx(&full[s], T::STAGE);
+      tma_load_2d(ring + s * T::STAGE, &tmP, &full[s], (kb0 + n) * kKb, row0);
+      tma_load_2d(ring + s * T::STAGE + T::P_BYTES, &tmQ, &full[s], (kb0 + n) * kKb, col0);
+    };
     if (lane == 0) {
-      int n = 0;
+      for (int i = 0; i < NST; ++i) {
+        mbar_init(&full[i], 1);
+        mbar_init(&empty[i], 1);
+      }
+      for (int i = 0; i < NB; ++i) {
+        mbar_init(&sums[i], 1);
+        mbar_init(&freed[i], 8);
+      }
+      mbar_init(&drain, 1);
+      abort_word = 0;
+      fence_mbar_init();
+      for (; n < kbs && n < NST; ++n) load(n);
+    }
+    __syncwarp();
+    begin();
+    if (lane == 0) {
       for (; n < kbs; ++n) {
-        const int s = n % NST;
-        if (n >= NST && !mbar_wait(&empty[s], (uint32_t)(n / NST - 1) & 1u, abort_flag, ctl, kid | W_EMPTY)) break;
-        mbar_arrive_expect_tx(&full[s], T::STAGE);
-        tma_load_2d(ring + s * T::STAGE, &tmP, &full[s], (kb0 + n) * kKb, row0);
-        tma_load_2d(ring + s * T::STAGE + T::P_BYTES, &tmQ, &full[s], (kb0 + n) * kKb, col0);
+        if (!mbar_wait(&empty[n % NST], (uint32_t)(n / NST - 1) & 1u, abort_flag, ctl, kid | W_EMPTY)) break;
+        load(n % NST);
       }
       // every copy this thread started must land before the CTA exits
       for (int i = n > NST ? n - NST : 0; i < n; ++i)
         mbar_wait(&full[i % NST], (uint32_t)(i / NST) & 1u, nullptr, ctl, kid | W_DRAIN);
     }
   } else if (warp == kIssueWarp) {
+    tmem_alloc(&tmem_slot, T::TMEM);
+    tmem_relinquish();
+    begin();
     const uint64_t p0 = sdesc_sw128(smem_u32(ring), 16, 1024);
     const uint64_t q0 = sdesc_sw128(smem_u32(ring + T::P_BYTES), 16, 1024);
     // a wait costs 200 clocks even where there is nothing to wait for: the next block's
@@ -395,6 +405,7 @@ __global__ void __launch_bounds__(kSmallThreads, DUAL ? 2 : 1)
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     for (int i = 0; i < AHEAD - 2; ++i) fetch(i);
+    begin();
     uint32_t here = 0;                         // the next block's sums are known to be complete
     // a failed wait: the loop goes on, past the barriers, without work
     for (int n = 0; n < kbs; ++n) {
@@ -607,51 +618,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const unsigned int kid = KID_MATMUL << 8;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < NST; ++i) {
-      mbar_init(&full[i], rank == 0 ? 2 : 1);    // the first CTA's: its own copies, and word of the other's
-      mbar_init(&empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sums[i], 2);                     // the products, and the scales
-      mbar_init(&freed[i], rank == 0 ? 9 : 8);   // the first CTA's: its 8 warps, and word of the other's
-    }
-    mbar_init(&drain, 1);
-    abort_word = 0;
-    fence_mbar_init();
-  }
-  if (warp == 1) pair_alloc(&tmem_slot, 2 * BN);
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();
-  tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
+  // The first copies are under way while the tensor memory is allotted and the CTAs
+  // meet: every warp does what it can before.
+  uint32_t tmem = 0;
+  auto begin = [&] {
+    tc_fence_before();
+    cta_meets();
+    cluster_sync();
+    tc_fence_after();
+    tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
+  };
   const int tiles = g.tm * g.tn, t0 = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
 
   if (warp < 4) {
     regs_dec<72>();
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       uint32_t n = 0;
-      bool ok = true;
-      for (int t = t0; ok && t < tiles; t += step) {
-        int tm, tn;
-        tile_at(g, t, &tm, &tn);
-        const int row = tm * 256 + (int)rank * 128, col = tn * 256 + (int)rank * 128;
-        for (int kb = 0; kb < g.kbs; ++kb, ++n) {
-          const int s = (int)(n % NST);
-          if (n >= NST && !mbar_wait(&empty[s], (n / NST - 1) & 1u, abort_flag, ctl, kid | W_EMPTY)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&full[s], kPairStage);
-          tma_load_2d(ring + s * kPairStage, &tmA, &full[s], kb * kKb, row);
-          tma_load_2d(ring + s * kPairStage + kPairHalf, &tmB, &full[s], kb * kKb, col);
+      int t = t0, kb = 0, row = 0, col = 0;
+      auto load = [&] {                              // the next block, to a slot that is free
+        if (kb == 0) {
+          int tm, tn;
+          tile_at(g, t, &tm, &tn);
+          row = tm * 256 + (int)rank * 128, col = tn * 256 + (int)rank * 128;
         }
+        const int s = (int)(n % NST);
+        mbar_arrive_expect_tx(&full[s], kPairStage);
+        tma_load_2d(ring + s * kPairStage, &tmA, &full[s], kb * kKb, row);
+        tma_load_2d(ring + s * kPairStage + kPairHalf, &tmB, &full[s], kb * kKb, col);
+        ++n;
+        if (++kb == g.kbs) kb = 0, t += step;
+      };
+      if (lane == 0) {
+        for (int i = 0; i < NST; ++i) {
+          mbar_init(&full[i], rank == 0 ? 2 : 1);    // the first CTA's: its own copies, and word of the other's
+          mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+          mbar_init(&sums[i], 2);                     // the products, and the scales
+          mbar_init(&freed[i], rank == 0 ? 9 : 8);   // the first CTA's: its 8 warps, and word of the other's
+        }
+        mbar_init(&drain, 1);
+        abort_word = 0;
+        fence_mbar_init();
+        while (t < tiles && n < NST) load();
+      }
+      __syncwarp();
+      begin();
+      if (lane > 0) t = tiles, n = 0;                // one lane copies
+      while (t < tiles) {
+        if (!mbar_wait(&empty[n % NST], (n / NST - 1) & 1u, abort_flag, ctl, kid | W_EMPTY)) break;
+        load();
       }
       // every copy this thread started must land before the CTA exits
       for (uint32_t i = n > NST ? n - NST : 0u; i < n; ++i)
         mbar_wait(&full[i % NST], (i / NST) & 1u, nullptr, ctl, kid | W_DRAIN);
     } else if (warp == 1 && rank == 1) {
+      pair_alloc(&tmem_slot, 2 * BN);
+      begin();
       // tell the first CTA which of this one's operands are here
       uint32_t n = 0;
       bool ok = true;
@@ -668,6 +691,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     } else if (warp == 2 && rank == 1) {
       // and which of its sums have been read.  (The 8 warps that read them would
       // stand still for an arrival at the other CTA, 210 clocks: 576 -> 513 us at 8192^3.)
+      begin();
       uint32_t n = 0;
       bool ok = true;
       for (int t = t0; ok && t < tiles; t += step) {
@@ -728,6 +752,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
       for (int i = 0; i < AHEAD; ++i) fetch();
+      begin();
       uint32_t n = 0;
       bool ok = true;
       for (int t = t0; ok && t < tiles; t += step) {
@@ -753,6 +778,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else if (warp == 1) {
+      pair_alloc(&tmem_slot, 2 * BN);
+      begin();
       const uint64_t a0 = sdesc_sw128(smem_u32(ring), 16, 1024);
       const uint64_t b0 = sdesc_sw128(smem_u32(ring + kPairHalf), 16, 1024);
       uint32_t n = 0, here = 0;                  // here: the next block's operands are known to be in place
@@ -775,9 +802,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       pair_commit_w(&drain);
       mbar_wait_warp(&drain, 0, nullptr, ctl, kid | W_DRAIN);
+    } else {                                         // warp 2 of the first CTA has nothing to do
+      begin();
     }
   } else {
     regs_inc<216>();
+    begin();
     // warps 4-7: the tile's first 128 columns, warps 8-11 the others
     const int half = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
