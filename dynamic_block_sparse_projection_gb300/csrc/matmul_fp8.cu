@@ -229,7 +229,7 @@ __device__ __forceinline__ void stores_done(const MmArgs& g) {
 // CTAs of a cluster take a run of the blocks of K each; then each adds up a part of
 // the tile, out of all CTAs' shared memory in their order, and writes it.  One token x
 // [12288, 2048], 25 MB, 11 us a call, of which 4 begin and end it; 640 x 1160 x 40000 with
-// a scale for each column 76 us (257 unsplit by pairs of CTAs).
+// a scale for each column 69 us, split in five (137 unsplit).
 constexpr int kSmallThreads = 320;         // 8 warps that scale, then the copying and the issuing warp
 constexpr int kCopyWarp = 8, kIssueWarp = 9;
 
@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kSmallThreads, DUAL ? 2 : 1)
   if (g.split > 1) cluster_sync();
   // this CTA's part of the tile: SWAP: columns, else rows
   constexpr int UNITS = 32 * BN;                         // of 4 values
-  const int first = UNITS / g.split * rank, last = first + UNITS / g.split;
+  const int first = UNITS * rank / g.split, last = UNITS * (rank + 1) / g.split;
   if (warp < 8 && !*abort_flag) {
     auto put = [&](int u, float4 v) {
       const int line = SWAP ? u / 32 : u / (BN / 4), q = SWAP ? u % 32 : u % (BN / 4);
@@ -938,16 +938,15 @@ cudaError_t pair_pick(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUte
 }
 
 // How a product is worked on: by pairs of CTAs or in small tiles, and there over
-// how many CTAs a tile's blocks of K are split.  The times behind the choice are
-// those measured (in 10 ns; 152 SMs): a block of K 0.34 us in a small tile and 0.47
+// how many CTAs, up to eight, a tile's blocks of K are split.  The times behind the choice
+// are those measured (in 10 ns; 152 SMs): a block of K 0.34 us in a small tile and 0.47
 // in a pair's (0.49 and 0.57 with a scale for each column), a tile's beginning and
-// end 4.5 us, or 1.4 in a pair that goes on to the next tile; joining the sums 1 to
-// 3 us; and clusters of 4 and 8 CTAs find 128 and 104 SMs.  Tiles of 32 columns, two
-// CTAs an SM where there are more of them than SMs, share its 0.34 us a block and begin
-// and end beside each other: one token x [24576, 2048] 24 -> 19 us, 30000 x 32 x 2048
-// 24 -> 21, [12288, 2048] 15 either way.  Against measured calls it is off by up to 10 %:
-// 640 x 1160 x 40000 has 160 us as small tiles, 85 split in two and 89 in four, and is
-// estimated at 158, 82 and 88.
+// end 4.5 us, or 1.4 in a pair that goes on to the next tile; joining the sums 1.2 to
+// 3.6 us; and a cluster of so many CTAs finds so many SMs at once (two CTAs each: the second
+// row, for tiles of 32 columns, which then share 0.34 us a block and begin and end beside
+// each other: one token x [24576, 2048] 24 -> 19 us, [12288, 2048] 15 either way).  Measured
+// and estimated, split 1, 2, 3, 4, 5: 552 x 968 x 37776 112, 63, 47, 67, 62 us, 105, 57, 40, 61,
+// 52; 640 x 1160 x 40000 with a scale for each column 138, 76, 102, 82, 69 us, 158, 83, 114, 88, 73.
 struct Plan {
   bool pair, swap;
   int bn, split;           // without pairs
@@ -961,13 +960,15 @@ Plan plan_of(const dsv_matmul& p) {
   plan.bn = cols <= 32 ? 32 : cols <= 64 ? 64 : 128;
   const long long tiles = (long long)((rows + 127) / 128) * ((cols + plan.bn - 1) / plan.bn);
   const int block = colv && plan.bn == 128 ? 49 : 34;
-  const int ctas = plan.bn == 32 ? 2 : 1;
-  const int slots[4] = {kSMs, kSMs, 128, 104}, join[4] = {0, 120, 110, 300};
+  static const int slots[2][8] = {{kSMs, kSMs, 138, 144, 140, 138, 105, 120}, {304, 304, 291, 296, 290, 276, 266, 288}};
+  static const int join[8] = {0, 120, 120, 130, 150, 170, 250, 300};
   long long best = 0;
-  for (int i = 0; i < 4 && 1 << i <= kbs; ++i) {
-    const long long n = tiles << i, rounds = (n + slots[i] - 1) / slots[i], waves = (rounds + ctas - 1) / ctas;
-    const long long time = rounds * ((kbs + (1 << i) - 1) >> i) * block + waves * 450 + join[i];
-    if (i == 0 || time < best) best = time, plan.split = 1 << i;
+  for (int split = 1; split <= 8 && split <= kbs; ++split) {
+    const int i = split - 1;
+    const long long n = tiles * split, rounds = (n + slots[0][i] - 1) / slots[0][i];
+    const long long waves = plan.bn == 32 ? (n + slots[1][i] - 1) / slots[1][i] : rounds;
+    const long long time = rounds * ((kbs + i) / split) * block + waves * 450 + join[i] + (i > 0 && plan.bn == 128 ? 60 : 0);
+    if (split == 1 || time < best) best = time, plan.split = split;
   }
   if (p.M > 128 && p.N > 128) {
     const long long pairs = (long long)((p.M + 255) / 256) * ((p.N + 255) / 256);

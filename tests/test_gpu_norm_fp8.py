@@ -332,6 +332,7 @@ MMS = [  # M, N, K
     (129, 257, 385), (200, 130, 4097), (515, 700, 200), (1000, 260, 96), (300, 1536, 16), (2049, 1100, 260), (4100, 520, 130),
     # few tiles and many blocks of K: shared out over a cluster, tokens as rows or as columns of the tile
     (130, 200, 9000), (300, 70, 8100), (33, 129, 4097), (64, 300, 5000), (1, 3000, 2100), (20, 40, 20000), (700, 24, 6000),
+    (300, 500, 3000), (600, 640, 2000), (40, 2000, 3000), (2, 1900, 6100),
     # more tiles than pairs of SMs, more blocks than slots for scales
     (2300, 2208, 2500), (2303, 2203, 1300),
 ]
