@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kQThreads, AL && sizeof(X) == 2 ? 4 : 2) quant
   __shared__ uint32_t red[WARPS][16 * W];                 // maxima of a warp's 16 rows, a word of columns each
   __shared__ float inv_t[kTile];
   __shared__ uint2 turn[TRANS ? kTile * 16 : 1];          // [column][8 rows each], its units swapped by column / 8
+  cudaTriggerProgrammaticLaunchCompletion();              // a product behind this may come to wait
   const int u = threadIdx.x >> 4, l = threadIdx.x & 15, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tc = (int)(blockIdx.x % tiles_c), tr = (int)(blockIdx.x / tiles_c);
   const int row0 = tr * kTile + 8 * u, col0 = tc * kTile + 8 * l;

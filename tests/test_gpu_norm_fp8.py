@@ -605,3 +605,81 @@ def test_replays_read_the_tensors_as_they_are(dsv):
         for out in outs:
             assert all(torch.equal(a, b) for a, b in zip(out, want))
     _clean(dsv)
+
+
+def test_products_behind_what_they_read(dsv):
+    """A product may be launched before the kernel in front of it is done: behind kernels that write its operands,
+    scales and output, behind copies and events, in a graph behind a fork, a memset and as the first node."""
+    x, y = _rand(1, 4000, 1024).to(BF), _rand(2, 4000, 1024).to(BF)
+    w = [dsv.quantize_fp8(_rand(s, 768, 1024), rows=128) for s in (3, 4)]
+    one = [dsv.quantize_fp8(t, rows=1) for t in (x, y)]
+    acc = torch.zeros(4000, 768, device="cuda")
+    q = [t.clone() for t in one[0]]
+
+    def chain(out):
+        """Operands, scales and outputs are overwritten right before and right after the products that use them."""
+        for src in (x, y, x):
+            dsv.quantize_fp8(src, outs=tuple(q))
+            out.append(dsv.matmul_fp8(*q, *w[0]))
+            out.append(dsv.matmul_fp8(q[0][:5], q[1][:, :5].contiguous(), *w[0]))
+        acc.zero_()
+        for k in range(3):
+            dsv.matmul_fp8(*q, *w[k % 2], out=acc, accumulate=True)
+        out.append(acc.clone())
+        q[0].view(torch.uint8).copy_(one[1][0].view(torch.uint8))
+        q[1].copy_(one[1][1])
+        out.append(dsv.matmul_fp8(*q, *w[1]))
+        qkv = dsv.matmul_fp8(*q, *w[0])                    # each product's output is the next one's input, quantised
+        for _ in range(3):
+            g = dsv.quantize_fp8(qkv, dtype=E5)
+            qkv = dsv.matmul_fp8(*g, *dsv.quantize_fp8(qkv[:768], dtype=E4))
+        out.append(qkv)
+        return out
+
+    def slow():
+        """The same, each call by itself."""
+        out, sync = [], torch.cuda.synchronize
+        real = dsv.matmul_fp8, dsv.quantize_fp8
+
+        def alone(f):
+            def call(*a, **k):
+                sync()
+                r = f(*a, **k)
+                sync()
+                return r
+            return call
+        dsv.matmul_fp8, dsv.quantize_fp8 = map(alone, real)
+        try:
+            return chain(out)
+        finally:
+            dsv.matmul_fp8, dsv.quantize_fp8 = real
+
+    want = slow()
+    for _ in range(5):
+        got = chain([])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    c, d, e = (torch.empty(4000, 768, dtype=BF, device="cuda") for _ in range(3))
+    z = torch.empty_like(c)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        dsv.matmul_fp8(*one[0], *w[0], out=c)              # the first node
+        other.wait_stream(side)
+        with torch.cuda.stream(other):
+            dsv.matmul_fp8(*one[1], *w[0], out=d)          # behind a fork
+            dsv.matmul_fp8(*one[1], *w[1], out=e)
+        z.zero_()
+        dsv.matmul_fp8(*one[0], *w[1], out=z)              # behind a memset or a kernel of another library
+        side.wait_stream(other)
+        dsv.matmul_fp8(*one[0], *w[0], out=d[:4000])       # behind two at once
+        got = chain([])
+    for _ in range(3):
+        for t in (c, d, e, z):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.equal(c, dsv.matmul_fp8(*one[0], *w[0])) and torch.equal(d, c)
+        assert torch.equal(e, dsv.matmul_fp8(*one[1], *w[1])) and torch.equal(z, dsv.matmul_fp8(*one[0], *w[1]))
+    _clean(dsv)
