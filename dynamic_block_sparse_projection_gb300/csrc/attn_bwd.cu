@@ -100,7 +100,7 @@ struct KVTraits {
   static constexpr int STAGE_BYTES = (2 * B_BYTES + 2 * VEC_BYTES + 1023) / 1024 * 1024;  // keeps tiles 1024-aligned
   static constexpr int NBAR = 1 + 2 * NST + 7;
   static constexpr int SMEM_USED = 1024 + 2 * A_BYTES + NST * STAGE_BYTES + NBAR * 8 + 16;
-  static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
+  static constexpr int SMEM = SMEM_USED > kTmemOwnerSmem ? SMEM_USED : kTmemOwnerSmem;
   // TMEM: S^T (fp32, BETA columns) at 0, dP^T at 128, dV at 256, dK at 256+D.
   // S^T and dP^T are whole-group products (N = BETA): an M=128, N=128
   // smem x smem product reads 8 KB in its 64 clocks, the shared-memory port's
@@ -456,7 +456,7 @@ struct QTraits {
   static constexpr int NV = (2 * A_BYTES + 6 * KV_BYTES + 2048 <= 227 * 1024) ? 3 : 2;
   static constexpr int NBAR = 2 + 2 * NK + 2 * NV + 2 + 2 + 3;
   static constexpr int SMEM_USED = 1024 + 2 * A_BYTES + (NK + NV) * KV_BYTES + NBAR * 8 + 16;
-  static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
+  static constexpr int SMEM = SMEM_USED > kTmemOwnerSmem ? SMEM_USED : kTmemOwnerSmem;
   // TMEM: S and dP (fp32), dQ (fp32), dS (bf16 pairs, BETA/2 columns).  S and
   // dP take both operands from shared memory (an M=128, N=128 product reads 8 KB
   // in its 64 clocks, the port's 128 B/clock); dQ takes dS from TMEM.

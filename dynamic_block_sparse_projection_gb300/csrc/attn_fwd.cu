@@ -60,7 +60,7 @@ struct FwdTraits {
   static constexpr int SMEM_USED = 1024 + Q_BYTES + 2 * NST * KV_BYTES + NBAR * 8 + 16;
   static_assert(SMEM_USED <= 227 * 1024, "forward tiles exceed shared memory");
   // at least 120 KB so that one CTA owns an SM (and its 512 TMEM columns)
-  static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
+  static constexpr int SMEM = SMEM_USED > kTmemOwnerSmem ? SMEM_USED : kTmemOwnerSmem;
   static constexpr uint32_t S_COL = 128;         // column stride of the S/P buffers
   static constexpr uint32_t O_COL = 384;
   static constexpr uint32_t TMEM_COLS = 512;

@@ -193,6 +193,16 @@ __device__ __forceinline__ int clc_answer(const void* answer) {
 // ---------------------------------------------------------------------------
 // tcgen05: tensor memory and MMA
 // ---------------------------------------------------------------------------
+// An SM's shared memory, and what a CTA takes of it beside its own.
+constexpr int kSmSmem = 228 * 1024, kCtaSmem = 1024;
+// A kernel that takes all 512 columns of an SM's tensor memory, and counts on their
+// first address, takes at least this much shared memory, and one that takes some of
+// the columns more than what is left: no two of them share an SM.  It must not come
+// about in any other way: a CTA that is launched early holds its columns while it
+// waits for the kernel in front of it, which may still wait for its own.
+constexpr int kTmemOwnerSmem = 120 * 1024;
+constexpr bool fits_beside_owner(int smem) { return kTmemOwnerSmem + smem + 2 * kCtaSmem <= kSmSmem; }
+
 __device__ __forceinline__ void tmem_alloc(uint32_t* smem_slot, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_slot)),
                "r"(ncols)

@@ -148,6 +148,15 @@ cudaError_t launch_norm_bwd_narrow(const dsv_rows& dy, const dsv_rows& x, const 
 // 128 bytes x 32 rows, null where its rows do not lie on 16 bytes or it is added to.
 cudaError_t launch_quantize(const dsv_rows& x, int R, int C, int rows, const dsv_rows& q, float* scale,
                             const dsv_rows& qt, float* scale_t, cudaStream_t st);
+// How a product is worked on.
+struct MatmulPlan {
+  int pair;                // pairs of CTAs on 256 x 256 tiles; else small tiles, and:
+  int swap;                // b's rows are the tile's 128, a's its columns
+  int bn, split;           // columns of a tile; CTAs that share its blocks of K
+  int dual;                // two CTAs an SM
+  int smem;                // a CTA's shared memory
+};
+MatmulPlan matmul_plan(const dsv_matmul& p);
 void matmul_boxes(const dsv_matmul& p, int* a, int* b);
 cudaError_t launch_matmul_fp8(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap* tmC, const dsv_matmul& p,
                               bool a_e5, bool b_e5, const float* sa, const float* sb, const dsv_rows& c, const Ctl& ctl,

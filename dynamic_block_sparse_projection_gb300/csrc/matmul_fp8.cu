@@ -241,7 +241,11 @@ struct SmallTraits {
   static constexpr int AHEAD = DUAL ? 12 : 16;             // blocks whose scales are under way: a first read of memory's time
   static constexpr int BUFS = BN == 128 ? 4 : 8;
   static constexpr int TMEM = BUFS * BN;
-  static constexpr int SMEM = STAGES * STAGE + AHEAD * 2 * 256 * 4 + 1024;
+  static constexpr int SMEM_USED = STAGES * STAGE + AHEAD * 2 * 256 * 4 + 1024;
+  // two CTAs an SM, and none beside a kernel that takes all of its tensor memory (105 KB are used)
+  static constexpr int SMEM = DUAL ? 110 * 1024 : SMEM_USED;
+  static_assert(SMEM_USED <= SMEM && !fits_beside_owner(SMEM), "beside a kernel that takes all tensor memory");
+  static_assert(!DUAL || (2 * (SMEM + kCtaSmem + 512) <= kSmSmem && 2 * TMEM <= 512), "two CTAs an SM (512: the barriers)");
   static_assert(STAGES * STAGE >= 128 * BN * 4, "the tile's sums take the stages' place");
 };
 
@@ -549,9 +553,9 @@ cudaError_t small_of(const CUtensorMap& tmP, const CUtensorMap& tmQ, const MmArg
 }
 template <int BN, bool SWAP>
 cudaError_t small_pick(const CUtensorMap& tmP, const CUtensorMap& tmQ, const MmArgs& g, bool colv, bool f32, const Ctl& ctl,
-                       cudaStream_t st) {
+                       bool dual, cudaStream_t st) {
   if constexpr (BN == 32) {
-    if ((long long)g.tm * g.tn * g.split > kSMs) return small_of<BN, true, SWAP>(tmP, tmQ, g, colv, f32, ctl, st);
+    if (dual) return small_of<BN, true, SWAP>(tmP, tmQ, g, colv, f32, ctl, st);
   }
   return small_of<BN, false, SWAP>(tmP, tmQ, g, colv, f32, ctl, st);
 }
@@ -574,6 +578,7 @@ constexpr int kPairThreads = 384;          // 4 warps that copy and issue, 8 tha
 constexpr int kPairStages = 5, kPairHalf = 128 * kKb, kPairStage = 2 * kPairHalf;
 constexpr int kScaleSlots = 8, kScaleWords = 384;     // scales of a block: see the scale warp
 constexpr int kPairSmem = kPairStages * kPairStage + kStoreBytes + kScaleSlots * kScaleWords * 4 + 1024;
+static_assert(!fits_beside_owner(kPairSmem), "beside a kernel that takes all tensor memory");
 
 // Arrive on the barrier at the same place in the cluster's first CTA.  What the
 // arrival stands for (tensor memory read, operands in place) is ordered by the
@@ -954,6 +959,8 @@ cudaError_t pair_pick(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUte
                       : pair_t<COLV, true, false>(tmA, tmB, tmC, g, ctl, st);
 }
 
+}  // namespace
+
 // How a product is worked on: by pairs of CTAs or in small tiles, and there over
 // how many CTAs, up to eight, a tile's blocks of K are split.  The times behind the choice
 // are those measured (in 10 ns; 152 SMs): a block of K 0.34 us in a small tile and 0.47
@@ -964,12 +971,8 @@ cudaError_t pair_pick(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUte
 // each other: one token x [24576, 2048] 24 -> 19 us, [12288, 2048] 15 either way).  Measured
 // and estimated, split 1, 2, 3, 4, 5: 552 x 968 x 37776 112, 63, 47, 67, 62 us, 105, 57, 40, 61,
 // 52; 640 x 1160 x 40000 with a scale for each column 138, 76, 102, 82, 69 us, 158, 83, 114, 88, 73.
-struct Plan {
-  bool pair, swap;
-  int bn, split;           // without pairs
-};
-Plan plan_of(const dsv_matmul& p) {
-  Plan plan = {false, false, 128, 1};
+MatmulPlan matmul_plan(const dsv_matmul& p) {
+  MatmulPlan plan = {0, 0, 128, 1, 0, 0};
   const int kbs = (p.K + kKb - 1) / kKb;
   plan.swap = p.M <= 64 && p.M < p.N;
   const int rows = plan.swap ? p.N : p.M, cols = plan.swap ? p.M : p.N;
@@ -990,12 +993,16 @@ Plan plan_of(const dsv_matmul& p) {
   if (p.M > 128 && p.N > 128) {
     const long long pairs = (long long)((p.M + 255) / 256) * ((p.N + 255) / 256);
     const long long time = (pairs + kPairs - 1) / kPairs * ((long long)kbs * (p.b_rows == 1 ? 57 : 47) + 140) + 350;
-    plan.pair = time <= best;
+    if (time <= best) plan.pair = 1, plan.split = 1;
   }
+  plan.dual = plan.bn == 32 && tiles * plan.split > kSMs;
+  plan.smem = plan.pair        ? kPairSmem
+              : plan.dual      ? SmallTraits<32, true>::SMEM
+              : plan.bn == 32  ? SmallTraits<32, false>::SMEM
+              : plan.bn == 64  ? SmallTraits<64, false>::SMEM
+                               : SmallTraits<128, false>::SMEM;
   return plan;
 }
-
-}  // namespace
 
 cudaError_t launch_matmul_fp8(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap* tmC, const dsv_matmul& p,
                               bool a_e5, bool b_e5, const float* sa, const float* sb, const dsv_rows& c, const Ctl& ctl,
@@ -1022,7 +1029,7 @@ cudaError_t launch_matmul_fp8(const CUtensorMap& tmA, const CUtensorMap& tmB, co
   g.split = 1;
   const int size = f32 ? 4 : 2;
   g.vec = reinterpret_cast<uintptr_t>(c.ptr) % (4 * size) == 0 && c.stride % 4 == 0;
-  const Plan plan = plan_of(p);
+  const MatmulPlan plan = matmul_plan(p);
   if (plan.pair) {
     g.idesc = idesc_f8(256, 256, a_e5, b_e5);
     return p.b_rows == 1 ? pair_pick<true>(tmA, tmB, tm_c, g, f32, ctl, st)
@@ -1043,16 +1050,16 @@ cudaError_t launch_matmul_fp8(const CUtensorMap& tmA, const CUtensorMap& tmB, co
   g.tn = (g.N + plan.bn - 1) / plan.bn;
   const bool colv = (plan.swap ? p.a_rows : p.b_rows) == 1;
   if (plan.swap)
-    return plan.bn == 32 ? small_pick<32, true>(tmB, tmA, g, colv, f32, ctl, st)
-                         : small_pick<64, true>(tmB, tmA, g, colv, f32, ctl, st);
-  return plan.bn == 32   ? small_pick<32, false>(tmA, tmB, g, colv, f32, ctl, st)
-         : plan.bn == 64 ? small_pick<64, false>(tmA, tmB, g, colv, f32, ctl, st)
-                         : small_pick<128, false>(tmA, tmB, g, colv, f32, ctl, st);
+    return plan.bn == 32 ? small_pick<32, true>(tmB, tmA, g, colv, f32, ctl, plan.dual, st)
+                         : small_pick<64, true>(tmB, tmA, g, colv, f32, ctl, plan.dual, st);
+  return plan.bn == 32   ? small_pick<32, false>(tmA, tmB, g, colv, f32, ctl, plan.dual, st)
+         : plan.bn == 64 ? small_pick<64, false>(tmA, tmB, g, colv, f32, ctl, plan.dual, st)
+                         : small_pick<128, false>(tmA, tmB, g, colv, f32, ctl, plan.dual, st);
 }
 
 // Rows of the boxes that a's and b's tensor maps have.
 void matmul_boxes(const dsv_matmul& p, int* a, int* b) {
-  const Plan plan = plan_of(p);
+  const MatmulPlan plan = matmul_plan(p);
   *a = plan.pair || !plan.swap ? 128 : plan.bn;
   *b = plan.pair || plan.swap ? 128 : plan.bn;
 }

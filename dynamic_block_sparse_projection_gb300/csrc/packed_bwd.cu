@@ -162,7 +162,7 @@ struct PRowsTraits {
   static constexpr int TILE = NCH * CHUNK;
   static constexpr int SMEM_USED = 1024 + 4 * TILE + 5 * 8 + 4 * 4 + 8;
   // at least 120 KB so that one CTA owns an SM (and its 512 TMEM columns)
-  static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
+  static constexpr int SMEM = SMEM_USED > kTmemOwnerSmem ? SMEM_USED : kTmemOwnerSmem;
   static constexpr uint32_t TMEM_COLS = 512;      // two buffers of S and dP
 };
 
@@ -340,7 +340,7 @@ struct PKVTraits {
   static constexpr int NBAR = 2 + 2 * NQ + 3 * ND + 7 + 2;
   static constexpr int SMEM_USED = (2 + NQ + ND) * TILE + 2 * ND * VEC_BYTES + NBAR * 8 + 16;
   static_assert(SMEM_USED <= 227 * 1024, "dK/dV tiles exceed shared memory");
-  static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
+  static constexpr int SMEM = SMEM_USED > kTmemOwnerSmem ? SMEM_USED : kTmemOwnerSmem;
   // TMEM: S^T at 0, dP^T at 128, dV at 256, dK at 256 + D; P^T and dS^T (bf16
   // pairs) go over the columns they were read from, each warp half hf packing
   // its 64 queries into its first 32 columns, handed over in two chunks.
@@ -857,7 +857,7 @@ struct PQTraits {
   static constexpr int SMEM_USED = (2 * NQD + NK + NV) * TILE + NBAR * 8 + 16 + 16 + 2 * (int)sizeof(QItem) +
                                    1024 * NQD;
   static_assert(SMEM_USED <= 227 * 1024, "dQ tiles exceed shared memory");
-  static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
+  static constexpr int SMEM = SMEM_USED > kTmemOwnerSmem ? SMEM_USED : kTmemOwnerSmem;
   static constexpr uint32_t S_COL = 0, DP_COL = 128, DQ_COL = 256, DS_COL = 256 + D, TMEM_COLS = 512;
   static constexpr uint32_t TX = 128 * D * 2;
   static constexpr int HALF = 64;

@@ -82,7 +82,7 @@ struct PFwdTraits {
   static_assert(NBAR % 2 == 0, "alignment of the work request's answer");
   static_assert(SMEM_USED <= 227 * 1024, "forward tiles exceed shared memory");
   // at least 120 KB so that one CTA owns an SM (and its 512 TMEM columns)
-  static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
+  static constexpr int SMEM = SMEM_USED > kTmemOwnerSmem ? SMEM_USED : kTmemOwnerSmem;
   static constexpr uint32_t S_COL = 128, O_COL = 384, TMEM_COLS = 512;
   static constexpr uint32_t TX = 128 * D * 2;
 };

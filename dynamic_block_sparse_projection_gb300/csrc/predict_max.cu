@@ -162,7 +162,7 @@ struct MaxTraits {
   static constexpr int NSTAGE = RING_ROOM / SB >= 4 ? 4 : RING_ROOM / SB;
   static constexpr int SMEM_USED = 1024 + NQ * TB + NSTAGE * SB + MISC;
   // at least 120 KB, so that one CTA holds an SM (and its whole TMEM)
-  static constexpr int SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
+  static constexpr int SMEM = SMEM_USED > kTmemOwnerSmem ? SMEM_USED : kTmemOwnerSmem;
   static_assert(NSTAGE >= 2, "tile too large for a two-stage ring");
   static_assert(2 * ZC * NQ * 4 * CG * 4 + (1 + 2 * NSTAGE + 2 * NACC + 1) * 8 + 16 <= MISC, "misc area");
   static_assert(ZC * NQ * 4 * KT <= 256, "one combined score per reduction thread");

@@ -851,6 +851,7 @@ constexpr int kSelSmem = 1024 + 2 * kTileBytes + 2 * kNSlot * kTileBytes + kBins
                          kRows * (int)sizeof(RowShared) + kKStat * 4 + (1 + 2 * kNSlot + 2 * kNBuf + 1) * 8 + 16;
 static_assert((kRows * (int)sizeof(RowShared) + kKStat * 4) % 8 == 0, "barriers must stay 8-byte aligned");
 static_assert(kSelSmem <= 227 * 1024, "score/select tiles exceed shared memory");
+static_assert(kSelSmem >= kTmemOwnerSmem, "the CTA takes the SM's whole tensor memory");
 static_assert(kRadixBins * 4 <= kCand * 8, "the fallback's digit histograms must fit the candidate region");
 
 }  // namespace

@@ -1,0 +1,44 @@
+"""Host side of how the 8-bit product is dispatched (CPU only)."""
+import ctypes
+from pathlib import Path
+
+import pytest
+
+SM_SMEM, CTA_SMEM = 228 * 1024, 1024          # an SM's shared memory, and what a CTA takes beside its own
+OWNER_SMEM = 120 * 1024                       # the least of a kernel that takes an SM's whole tensor memory
+
+
+class Plan(ctypes.Structure):
+    """MatmulPlan (csrc/dsv_launch.h)."""
+    _fields_ = [(n, ctypes.c_int) for n in ("pair", "swap", "bn", "split", "dual", "smem")]
+
+
+@pytest.fixture(scope="module")
+def plan():
+    from dynamic_block_sparse_projection_gb300.build import LIB, build
+    build()
+    from dynamic_block_sparse_projection_gb300 import binding
+    f = ctypes.CDLL(str(LIB))["_ZN3dsv11matmul_planERK10dsv_matmul"]
+    f.restype, f.argtypes = Plan, [ctypes.POINTER(binding.Matmul)]
+    return lambda *p: f(ctypes.byref(binding.Matmul(*p)))
+
+
+# M, N, K, a_rows, b_rows of every kind of tile
+TILES = [(1, 24576, 2048, 1, 128), (30000, 32, 2048, 1, 128), (1, 128, 128, 1, 128), (33, 2048, 512, 1, 128),
+         (1000, 50, 300, 1, 128), (300, 500, 3000, 1, 1), (2300, 2208, 2500, 1, 128)]
+
+
+def test_products_share_no_sm_with_a_kernel_that_takes_all_tensor_memory(plan):
+    """A product that is launched early holds its tensor memory while it waits for the kernel in front of it: that one
+    must have its own by then, so the two may not be able to meet on an SM."""
+    kinds = set()
+    for p in TILES:
+        t = plan(*p, 0)
+        kinds.add((t.pair, t.bn, t.dual))
+        assert t.smem + OWNER_SMEM + 2 * CTA_SMEM > SM_SMEM, p
+        assert (2 if t.dual else 1) * (t.smem + CTA_SMEM) <= SM_SMEM, p
+    assert kinds == {(0, 32, 0), (0, 32, 1), (0, 64, 0), (0, 128, 0), (1, 128, 0)}
+    src = Path(__file__).resolve().parent.parent / "dynamic_block_sparse_projection_gb300" / "csrc"
+    for f in src.glob("*.cu"):                # whoever allots tensor memory is one or the other
+        if "tmem_alloc(" in f.read_text():
+            assert "kTmemOwnerSmem" in f.read_text() or "fits_beside_owner(" in f.read_text(), f.name
