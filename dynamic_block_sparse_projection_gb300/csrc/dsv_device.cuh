@@ -68,15 +68,27 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
 // they share a scheduler with; the bounded waits below re-check their limits
 // after every return.
 constexpr uint32_t kSuspendHintNs = 20000;
+// CLUSTER: on a barrier that another CTA of the cluster arrives on.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendHintNs)
-      : "memory");
+  if constexpr (CLUSTER) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendHintNs)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendHintNs)
+        : "memory");
+  }
   return ok != 0;
 }
 
@@ -93,14 +105,15 @@ constexpr uint64_t kDrainLimitNs = 2000000000ull;
 // and raises `*abort` so that every other waiter in the CTA gives up too.
 // abort == nullptr: a drain wait; only the time limit applies, and it is at
 // least kDrainLimitNs.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, const Ctl& ctl,
                                           unsigned int where) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
   const uint64_t limit =
       (abort == nullptr && ctl.wait_limit_ns < kDrainLimitNs) ? kDrainLimitNs : ctl.wait_limit_ns;
   for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
     if ((it & 31u) == 0u) {
       if (abort != nullptr && *abort) return false;
       if (globaltimer() - t0 > limit || it > (1u << 30)) {
@@ -115,9 +128,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 // Warp-uniform variant: every lane of the warp waits and the result is the
 // AND over the warp, so that .sync.aligned instructions after it are reached
 // by all lanes or by none.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort,
                                                const Ctl& ctl, unsigned int where) {
-  bool ok = mbar_wait(bar, parity, abort, ctl, where);
+  bool ok = mbar_wait<CLUSTER>(bar, parity, abort, ctl, where);
   return __all_sync(0xffffffffu, ok) != 0;
 }
 
@@ -125,21 +139,33 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, v
 // phase is long complete.  Where the next wait is known early, its test is
 // issued early (mbar_test, non-blocking) and consumed at the wait
 // (mbar_wait_warp_tested), so the round trip overlaps other work.
+template <bool CLUSTER = false>
 __device__ __forceinline__ uint32_t mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
+  if constexpr (CLUSTER) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+  }
   return ok;
 }
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_warp_tested(uint64_t* bar, uint32_t parity, uint32_t tested,
                                                       volatile int* abort, const Ctl& ctl, unsigned int where) {
   if (__all_sync(0xffffffffu, tested != 0u)) return true;
-  return mbar_wait_warp(bar, parity, abort, ctl, where);
+  return mbar_wait_warp<CLUSTER>(bar, parity, abort, ctl, where);
 }
 
 // ---------------------------------------------------------------------------

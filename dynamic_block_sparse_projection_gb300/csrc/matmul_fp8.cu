@@ -580,17 +580,28 @@ constexpr int kScaleSlots = 8, kScaleWords = 384;     // scales of a block: see 
 constexpr int kPairSmem = kPairStages * kPairStage + kStoreBytes + kScaleSlots * kScaleWords * 4 + 1024;
 static_assert(!fits_beside_owner(kPairSmem), "beside a kernel that takes all tensor memory");
 
-// Arrive on the barrier at the same place in the cluster's first CTA.  What the
-// arrival stands for (tensor memory read, operands in place) is ordered by the
-// tcgen05 and copy instructions themselves; no thread reads memory that another
-// CTA's thread wrote.  Release and acquire of the cluster's scope would cost a
-// block 2350 clocks instead of the 900 it takes: each waits for all of the
-// thread's memory accesses.
+// What the first CTA learns of the second, at the cluster's scope.
+// Operands: the second CTA's tensor copies count on the first one's barrier themselves,
+// and the issuing warp acquires.
+__device__ __forceinline__ void pair_load_2d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %4, 0;\n\t"
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
+      "[a];\n\t}" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+// Tensor memory that has been read: an arrival on the barrier at this place in the first
+// CTA.  It needs the order of the two threads' instructions and of their tensor memory
+// accesses, which the tcgen05 fences on both sides give, and hands over no memory, so it
+// is relaxed; a release of the cluster's scope takes some 800 clocks a block (8192^3 782 us and
+// not 400; the acquire on the other side takes none).
 __device__ __forceinline__ void mbar_arrive_first(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\t"
       "mapa.shared::cluster.u32 a, %0, 0;\n\t"
-      "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void pair_alloc(uint32_t* slot, uint32_t ncols) {
@@ -672,15 +683,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           row = tm * 256 + (int)rank * 128, col = tn * 256 + (int)rank * 128;
         }
         const int s = (int)(n % NST);
-        mbar_arrive_expect_tx(&full[s], kPairStage);
-        tma_load_2d(ring + s * kPairStage, &tmA, &full[s], kb * kKb, row);
-        tma_load_2d(ring + s * kPairStage + kPairHalf, &tmB, &full[s], kb * kKb, col);
+        // the second CTA's bytes may come before this: the slot's phase waits for the arrival all the same
+        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStage);
+        pair_load_2d(ring + s * kPairStage, &tmA, &full[s], kb * kKb, row);
+        pair_load_2d(ring + s * kPairStage + kPairHalf, &tmB, &full[s], kb * kKb, col);
         ++n;
         if (++kb == g.kbs) kb = 0, t += step;
       };
       if (lane == 0) {
         for (int i = 0; i < NST; ++i) {
-          mbar_init(&full[i], rank == 0 ? 2 : 1);    // the first CTA's: its own copies, and word of the other's
+          mbar_init(&full[i], 1);                    // the first CTA's, for both CTAs' copies
           mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -695,31 +707,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       begin();
       if (lane > 0) t = tiles;                       // one lane copies
       while (t < tiles && n < NST) load();
+      bool ok = true;
       while (t < tiles) {
-        if (!mbar_wait(&empty[n % NST], (n / NST - 1) & 1u, abort_flag, ctl, kid | W_EMPTY)) break;
+        ok = mbar_wait(&empty[n % NST], (n / NST - 1) & 1u, abort_flag, ctl, kid | W_EMPTY);
+        if (!ok) break;
         load();
       }
-      // every copy this thread started must land before the CTA exits
-      for (uint32_t i = n > NST ? n - NST : 0u; i < n; ++i)
-        mbar_wait(&full[i % NST], (i / NST) & 1u, nullptr, ctl, kid | W_DRAIN);
+      // Every copy of the pair must land before its CTAs exit, which they do together.  The
+      // first CTA's barriers count those of both.  Blocks that only the second has asked for,
+      // after a wait that gave up, get the time that a copy takes, many times over.
+      if (rank == 0) {
+        for (uint32_t i = n > NST ? n - NST : 0u; i < n; ++i)
+          mbar_wait<true>(&full[i % NST], (i / NST) & 1u, nullptr, ctl, kid | W_DRAIN);
+      }
+      if (!ok) {
+        const uint64_t from = globaltimer();
+        while (globaltimer() - from < 10000000ull) __nanosleep(10000);
+      }
     } else if (warp == 1 && rank == 1) {
       pair_alloc(&tmem_slot, 2 * BN);
       begin();
-      // tell the first CTA which of this one's operands are here
-      uint32_t n = 0;
-      bool ok = true;
-      for (int t = t0; ok && t < tiles; t += step) {
-        for (int kb = 0; kb < g.kbs; ++kb, ++n) {
-          const int s = (int)(n % NST);
-          ok = mbar_wait_warp(&full[s], (n / NST) & 1u, abort_flag, ctl, kid | W_FULL);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_first(&full[s]);
-        }
-      }
       // the first CTA's last arrival here must land before this CTA exits
       mbar_wait_warp(&drain, 0, nullptr, ctl, kid | W_DRAIN);
     } else if (warp == 2 && rank == 1) {
-      // and which of its sums have been read.  (The 8 warps that read them would
+      // Tell the first CTA which of this one's sums have been read.  (The 8 warps that read them would
       // stand still for an arrival at the other CTA, 210 clocks: 576 -> 513 us at 8192^3.)
       begin();
       uint32_t n = 0;
@@ -728,6 +739,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         for (int kb = 0; kb < g.kbs; ++kb, ++n) {
           ok = mbar_wait_warp(&freed[n & 1u], (n / 2) & 1u, abort_flag, ctl, kid | W_FREE);
           if (!ok) break;
+          tc_fence_after();                          // behind the reads that the 8 warps told of
+          tc_fence_before();
           if (lane == 0) mbar_arrive_first(&freed[n & 1u]);
         }
       }
@@ -817,8 +830,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       for (int t = t0; ok && t < tiles; t += step) {
         for (int kb = 0; kb < g.kbs; ++kb, ++n) {
           const int s = (int)(n % NST), buf = (int)(n & 1u);
-          ok = mbar_wait_warp_tested(&full[s], (n / NST) & 1u, here, abort_flag, ctl, kid | W_FULL);
-          if (ok && n >= 2) ok = mbar_wait_warp(&freed[buf], (n / 2 - 1) & 1u, abort_flag, ctl, kid | W_FREE);
+          ok = mbar_wait_warp_tested<true>(&full[s], (n / NST) & 1u, here, abort_flag, ctl, kid | W_FULL);
+          if (ok && n >= 2) ok = mbar_wait_warp<true>(&freed[buf], (n / 2 - 1) & 1u, abort_flag, ctl, kid | W_FREE);
           if (!ok) break;
           tc_fence_after();
           const uint64_t a = desc_off(a0, (uint32_t)s * kPairStage), b = desc_off(b0, (uint32_t)s * kPairStage);
@@ -827,7 +840,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             pair_mma_w(tmem + (uint32_t)buf * BN, desc_off(a, k * 32), desc_off(b, k * 32), g.idesc, k > 0 ? 1u : 0u);
           pair_commit_w(&sums[buf]);
           pair_commit_w(&empty[s]);
-          here = mbar_test(&full[(n + 1) % NST], ((n + 1) / NST) & 1u);
+          here = mbar_test<true>(&full[(n + 1) % NST], ((n + 1) / NST) & 1u);
         }
       }
       pair_commit_w(&drain);

@@ -42,3 +42,16 @@ def test_products_share_no_sm_with_a_kernel_that_takes_all_tensor_memory(plan):
     for f in src.glob("*.cu"):                # whoever allots tensor memory is one or the other
         if "tmem_alloc(" in f.read_text():
             assert "kTmemOwnerSmem" in f.read_text() or "fits_beside_owner(" in f.read_text(), f.name
+
+
+def test_arrivals_at_another_cta_are_of_the_clusters_scope():
+    """An arrival on a barrier in another CTA's shared memory orders nothing between the two where its scope is the
+    CTA's, which it is where none is named."""
+    import re
+    csrc = Path(__file__).resolve().parent.parent / "dynamic_block_sparse_projection_gb300" / "csrc"
+    found = 0
+    for f in sorted(csrc.glob("*.cu*")):
+        for op in re.findall(r"mbarrier\.arrive[a-z0-9_.:]*\.shared::cluster[a-z0-9_.:]*", f.read_text()):
+            found += 1
+            assert re.match(r"mbarrier\.arrive(\.expect_tx)?\.(release|relaxed)\.cluster\.", op), f"{f.name}: {op}"
+    assert found
