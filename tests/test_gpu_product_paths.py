@@ -1,9 +1,18 @@
-"""The 8-bit product behind every kernel that lets it start early (needs a GB300)."""
+"""The 8-bit product by every way through its dispatch, and behind every kernel that lets it start early; what its
+operands and the layer norm's rows may hold beside ordinary numbers (needs a GB300).
+
+Tolerances of a product: an output is rounded once (half a step of its type).  The products of two 8-bit values are
+exact in fp32; the tensor cores add 32 of them at a time at no less than 22 leading bits of the largest (2^-22 each, 33
+terms, 4 steps a block of 128: 2^-15 of the sum of magnitudes), the blocks' sums are scaled and added in fp32 (2^-23 a
+block); the magnitudes here are those of the reference, in fp64."""
 import pytest
 import torch
 
+import product_cases
+
 pytestmark = pytest.mark.gpu
-BF, F32, E4 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+BF, F32, E4, E5 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.float8_e5m2
+HALF = {BF: 2.0 ** -8, F32: 2.0 ** -24}
 
 
 @pytest.fixture(scope="module")
@@ -107,4 +116,93 @@ def test_product_directly_behind_a_kernel_that_lets_it_come_early(dsv, case):
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(_bits(c), _bits(want)) for c in got)
+    assert dsv.device_error() == (0, 0)
+
+
+# ---------------------------------------------------------------------------
+# Every way through the dispatch
+# ---------------------------------------------------------------------------
+
+def _operand(seed, R, K, rows, to):
+    """8-bit values of a few sizes, NaN in the bytes behind a row's K, and scales of any value."""
+    q = (_rand(seed, R, K) * torch.exp(_rand(seed + 1, R, 1))).clamp(-448, 448).to(to)
+    wide = torch.full((R, -(-K // 16) * 16 + 16), 0x7F, dtype=torch.uint8, device="cuda")
+    wide[:, :K] = q.view(torch.uint8)
+    return wide.view(to)[:, :K], torch.exp(0.5 * _rand(seed + 2, -(-K // 128), -(-R // rows)))
+
+
+def _values(q, scale, rows):
+    R, K = q.shape
+    s = scale.double().t().repeat_interleave(rows, 0)[:R]
+    return q.double() * s.repeat_interleave(128, 1)[:, :K]
+
+
+def _product(dsv, shape, ar, br, ta, tb, dt):
+    M, N, K = shape
+    a, sa = _operand(1, M, K, ar, ta)
+    b, sb = _operand(5, N, K, br, tb)
+    c = dsv.matmul_fp8(a, sa, b, sb, out_dtype=dt)
+    va, vb = _values(a, sa, ar), _values(b, sb, br)
+    ref, mag = va @ vb.t(), va.abs() @ vb.abs().t()
+    tol = HALF[dt] * ref.abs() + (2.0 ** -15 + -(-K // 128) * 2.0 ** -23) * mag * (1 + 2.0 ** -8)
+    bad = ((c.double() - ref).abs() / (tol + 1e-30)).max().item()
+    assert bad <= 1.0, f"{bad:.3f} of the tolerance"
+    # rows that start anywhere, beside numbers that stay
+    wide = torch.full((M + 1, N + 9), 7.0, dtype=dt, device="cuda")
+    assert torch.equal(dsv.matmul_fp8(a, sa, b, sb, out=wide[:M, 3:3 + N]), c)
+    wide[:M, 3:3 + N] = 7
+    assert (wide == 7).all()
+    if dt == F32:
+        acc = _rand(9, M, N)
+        was = acc.double()
+        dsv.matmul_fp8(a, sa, b, sb, out=acc, accumulate=True)
+        bad = ((acc.double() - ref - was).abs() / (tol + 2.0 ** -23 * (ref.abs() + was.abs()) + 1e-30)).max().item()
+        assert bad <= 1.0, f"added to c: {bad:.3f} of the tolerance"
+    assert dsv.device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("shape", product_cases.SMALL + product_cases.PAIRS)
+@pytest.mark.parametrize("rows", product_cases.LAYOUTS)
+@pytest.mark.parametrize("ta,tb,dt", [(E4, E5, BF), (E5, E4, F32)])
+def test_product_by_every_way(dsv, shape, rows, ta, tb, dt):
+    _product(dsv, shape, *rows, ta, tb, dt)
+
+
+# ---------------------------------------------------------------------------
+# Beside ordinary numbers
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("R,C", [(1, 1), (1, 128), (1, 250), (2, 250), (300, 1)])
+@pytest.mark.parametrize("to", [E4, E5])
+def test_quantiser_gives_a_products_operands(dsv, R, C, to):
+    for rows in (1, 128):
+        q, s, qt, st = dsv.quantize_fp8(_rand(1, R, C), rows=rows, transpose=True, dtype=to)
+        assert q.dtype == to and qt.dtype == to and q.shape == (R, C) and qt.shape == (C, R)
+        assert s.shape == (-(-C // 128), -(-R // rows)) and st.shape == (-(-R // 128), -(-C // rows))
+        assert (R == 1 or q.stride(0) % 16 == 0) and (C == 1 or qt.stride(0) % 16 == 0)
+
+
+@pytest.mark.parametrize("C", [1, 264, 1001, 5120, 16384])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_constant_rows(dsv, C, dt):
+    """y = b up to what the mean's own rounding is multiplied with: r = 1 / sqrt(eps).  The mean of C equal values is
+    good to 2^-17 of it (at most 64 values of a thread, 5 shuffles, 8 warps, 2^-24 each), mu r to 2^-23 more."""
+    w, b = 1 + 0.3 * _rand(1, C), _rand(2, C)
+    for value in (3.3, -0.1, 0.0, 1.0e4):
+        x = torch.full((9, C), value, device="cuda").to(dt)
+        y, stats = dsv.layer_norm(x, w, b, eps=1e-5)
+        v = x[0, 0].double().abs().item()
+        assert ((stats[0].double() - x[0, 0].double()).abs() <= 2.0 ** -17 * v).all()
+        r = stats[1].double()
+        assert (r <= 1e-5 ** -0.5 * (1 + 2.0 ** -20)).all() and (r >= (1e-5 + (2.0 ** -17 * v) ** 2) ** -0.5 * (1 - 2.0 ** -20)).all()
+        tol = HALF[BF] * b.double().abs() + w.double().abs() * 1e-5 ** -0.5 * v * (2.0 ** -17 + 2.0 ** -23) * (1 + HALF[BF])
+        assert ((y.double() - b.double()).abs() <= tol + 2.0 ** -21 * b.double().abs()).all()
+        # x^ is what is left of that: dy has mean zero where it is taken out
+        dy = _rand(3, 9, C).to(BF)
+        dx = dsv.layer_norm_bwd(dy, x, stats)
+        g = dy.double()
+        h = ((x.double() - stats[0].double()[:, None]) * r[:, None])
+        want = r[:, None] * (g - g.mean(-1, keepdim=True) - h * (g * h).mean(-1, keepdim=True))
+        size = g.abs() + g.abs().mean(-1, keepdim=True) + h.abs() * (g * h).abs().mean(-1, keepdim=True)
+        assert ((dx.double() - want).abs() <= HALF[dt] * want.abs() + 2.0 ** -17 * r[:, None] * size).all()
     assert dsv.device_error() == (0, 0)

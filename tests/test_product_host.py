@@ -4,6 +4,8 @@ from pathlib import Path
 
 import pytest
 
+import product_cases
+
 SM_SMEM, CTA_SMEM = 228 * 1024, 1024          # an SM's shared memory, and what a CTA takes beside its own
 OWNER_SMEM = 120 * 1024                       # the least of a kernel that takes an SM's whole tensor memory
 
@@ -55,3 +57,23 @@ def test_arrivals_at_another_cta_are_of_the_clusters_scope():
             found += 1
             assert re.match(r"mbarrier\.arrive(\.expect_tx)?\.(release|relaxed)\.cluster\.", op), f"{f.name}: {op}"
     assert found
+
+
+def test_the_listed_sizes_take_every_way(plan):
+    """Columns of a tile, their side, scales, splits of K and CTAs of an SM: each that a sweep of sizes meets."""
+    def kind(m, n, k, ar, br):
+        t = plan(m, n, k, ar, br, 0)
+        return t.pair, t.bn, t.dual, t.swap, (ar if t.swap else br), 0 if t.pair else t.split
+
+    listed = {kind(*p, *r) for p in product_cases.SMALL + product_cases.PAIRS for r in product_cases.LAYOUTS}
+    sizes = [1, 2, 9, 31, 33, 60, 64, 65, 100, 129, 250, 600, 1300, 2500, 5000, 6200, 9900, 15000, 19500, 25000]
+    met = {kind(m, n, k, *r) for m in sizes for n in sizes for r in product_cases.LAYOUTS
+           for k in (1, 130, 300, 500, 700, 900, 1030, 1300, 1458, 2050, 3000, 6100, 8100, 10000, 11600, 13300, 20000, 40000)}
+    assert met <= listed, sorted(met - listed)
+    for s in range(1, 9):
+        for bn in (32, 64):
+            assert {(0, bn, 0, swap, r, s) for swap in (0, 1) for r in (1, 128)} <= listed, (bn, s)
+        assert {(0, 128, 0, 0, r, s) for r in (1, 128)} <= listed, s
+    groups = [(-(-n // 256), product_cases.columns_of_a_group(k)) for _, n, k in product_cases.PAIRS]
+    assert any(tn <= g for tn, g in groups) and sum(tn > g and tn % g for tn, g in groups) >= 2
+    assert all(plan(*p, *r, 0).pair for p in product_cases.PAIRS for r in product_cases.LAYOUTS)
