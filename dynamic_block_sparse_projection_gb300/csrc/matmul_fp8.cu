@@ -321,7 +321,6 @@ __global__ void __launch_bounds__(kSmallThreads, DUAL ? 2 : 1)
   const int rank = g.split > 1 ? (int)cluster_rank() : 0, tile = (int)blockIdx.x / g.split;
   const int row0 = (tile % g.tm) * 128, col0 = (tile / g.tm) * BN;
   const int kb0 = (int)((long long)g.kbs * rank / g.split), kbs = (int)((long long)g.kbs * (rank + 1) / g.split) - kb0;
-  cudaTriggerProgrammaticLaunchCompletion();
   // The first copies are under way while the tensor memory is allotted: every warp
   // does what it can before it meets the others.
   uint32_t tmem = 0;
@@ -369,6 +368,7 @@ __global__ void __launch_bounds__(kSmallThreads, DUAL ? 2 : 1)
   } else if (warp == kIssueWarp) {
     tmem_alloc(&tmem_slot, T::TMEM);
     tmem_relinquish();
+    cudaTriggerProgrammaticLaunchCompletion();
     begin();
     const uint64_t p0 = sdesc_sw128(smem_u32(ring), 16, 1024);
     const uint64_t q0 = sdesc_sw128(smem_u32(ring + T::P_BYTES), 16, 1024);
@@ -514,7 +514,8 @@ __global__ void __launch_bounds__(kSmallThreads, DUAL ? 2 : 1)
 }
 
 // The kernel may come before the one in front of it on the stream is done, and lets the
-// next product come early in its turn: it waits for that one (cudaGridDependencySynchronize) before it
+// next product come early in its turn, once each CTA has its tensor memory (what comes may take the rest
+// of an SM's, and keeps it until this kernel is done): it waits for that one (cudaGridDependencySynchronize) before it
 // touches memory that others use.  What it reads then is not read-only while it runs, so
 // nothing here goes by way of the read-only path.  Back to back a call takes 2 to 3 us less
 // (one token x [2048, 2048]: 8.2 -> 5.6 us).
@@ -656,7 +657,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const unsigned int kid = KID_MATMUL << 8;
-  cudaTriggerProgrammaticLaunchCompletion();
   // Every warp meets the others once it has done what they wait for.  (First copies and
   // scales before that, as small products have them: 14.4 and not 12.4 us at 4864 x
   // 1000 x 1160, the CTAs meet later.)
@@ -726,6 +726,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     } else if (warp == 1 && rank == 1) {
       pair_alloc(&tmem_slot, 2 * BN);
+      cudaTriggerProgrammaticLaunchCompletion();
       begin();
       // the first CTA's last arrival here must land before this CTA exits
       mbar_wait_warp(&drain, 0, nullptr, ctl, kid | W_DRAIN);
@@ -822,6 +823,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else if (warp == 1) {
       pair_alloc(&tmem_slot, 2 * BN);
+      cudaTriggerProgrammaticLaunchCompletion();
       begin();
       const uint64_t a0 = sdesc_sw128(smem_u32(ring), 16, 1024);
       const uint64_t b0 = sdesc_sw128(smem_u32(ring + kPairHalf), 16, 1024);

@@ -77,3 +77,14 @@ def test_the_listed_sizes_take_every_way(plan):
     groups = [(-(-n // 256), product_cases.columns_of_a_group(k)) for _, n, k in product_cases.PAIRS]
     assert any(tn <= g for tn, g in groups) and sum(tn > g and tn % g for tn, g in groups) >= 2
     assert all(plan(*p, *r, 0).pair for p in product_cases.PAIRS for r in product_cases.LAYOUTS)
+
+
+def test_a_product_lets_the_next_kernel_come_with_its_tensor_memory_in_hand():
+    """What comes early, a kernel of another library too, may take the rest of an SM's tensor memory until the product
+    in front of it is done: that one must not still want some."""
+    text = (Path(__file__).resolve().parent.parent / "dynamic_block_sparse_projection_gb300" / "csrc" / "matmul_fp8.cu").read_text()
+    lines = [line.strip() for line in text.splitlines()]
+    at = [i for i, line in enumerate(lines) if line == "cudaTriggerProgrammaticLaunchCompletion();"]
+    assert len(at) == 3                                      # the small tile's, and each CTA's of a pair
+    for i in at:
+        assert any("_alloc(&tmem_slot" in line for line in lines[i - 2:i]), lines[i - 2:i]
