@@ -1,4 +1,4 @@
-// norm.cuh — what the layer norm's forward and backward share.
+// norm.cuh — what the layer norm's kernels share (the way through the rows: the two of the backward).
 //
 // A video transformer's block normalises the residual stream before its
 // attention and scales and shifts the result by vectors that come from the

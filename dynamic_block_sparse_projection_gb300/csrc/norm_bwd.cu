@@ -22,8 +22,8 @@ namespace {
 // copies, so that bytes in flight cost no registers and no team waits for another.
 // One CTA an SM; a thread keeps the weight of its columns in registers too (in
 // shared memory, with 4 chunks a thread and a row at a time: 330 us and not 246).
-// Measured: 122880 rows of 2048, 1.5 GB, 246 us, 90 % of the copy bandwidth; 16384
-// rows of 5120 109 us, 68 %; 16384 of 8192 146 us, 81 %.
+// Measured: 122880 rows of 2048, 1.5 GB, 244 us, 91 % of the copy bandwidth; 16384
+// rows of 5120 105 us, 71 %; 16384 of 8192 142 us, 84 %.
 constexpr int kStreamBytes = 220 * 1024;       // of shared memory
 constexpr int kTeamThreads = 512, kTeamWarps = kTeamThreads / 32, kMaxSlots = 8;
 
@@ -111,7 +111,7 @@ __device__ __forceinline__ void group_sums(float* v, float (*slot)[4], int group
 }
 
 // A team's first warp brings in its rows, unit by unit.
-template <typename X, bool BWD>
+template <typename X>
 struct Loader {
   const X* x;
   long long xs;
@@ -127,7 +127,7 @@ struct Loader {
                     const NormArgs& a, const StreamArgs& sa, int team_)
       : x(x_), xs(xs_), dy(dy_), dys(dys_), ring(ring_), full(full_), at(a, sa), team(team_), issued(0) {
     xb = (uint32_t)a.C * sizeof(X);
-    yb = BWD ? (uint32_t)a.C * 2u : 0u;
+    yb = (uint32_t)a.C * 2u;
     more = at.next_sequence(team);
     skip();
   }
@@ -147,11 +147,11 @@ struct Loader {
     if (lane == 0) {
       mbar_arrive_expect_tx(bar, (uint32_t)rows * (xb + yb));
       if (sa.one & 1) bulk_load(dst, x + at.r * xs, (uint32_t)rows * xb, bar);
-      if (BWD && (sa.one & 2)) bulk_load(dst2, dy + at.r * dys, (uint32_t)rows * yb, bar);
+      if (sa.one & 2) bulk_load(dst2, dy + at.r * dys, (uint32_t)rows * yb, bar);
     }
     __syncwarp();
     if (!(sa.one & 1) && lane < rows) bulk_load(dst + lane * xb, x + (at.r + lane) * xs, xb, bar);
-    if (BWD && !(sa.one & 2) && lane < rows) bulk_load(dst2 + lane * yb, dy + (at.r + lane) * dys, yb, bar);
+    if (!(sa.one & 2) && lane < rows) bulk_load(dst2 + lane * yb, dy + (at.r + lane) * dys, yb, bar);
     ++issued;
     at.next_unit();
     skip();
@@ -166,7 +166,7 @@ struct Loader {
   }
 };
 
-// What the streamed kernels begin with: the barriers, and the thread's place.
+// What the kernel begins with: the barriers, and the thread's place.
 struct Place {
   int gw, team, gl, lane;                         // threads of a row; team; thread in the row; lane
   int sub;                                        // its first row of the unit
@@ -188,7 +188,7 @@ __device__ __forceinline__ void stream_begin(uint64_t* full, int n, int* abort_w
   __syncthreads();
 }
 
-// The weight and bias of a thread's columns, in registers where they are few.
+// The weight of a thread's columns, in registers where they are few.
 template <int CH>
 struct Columns {
   static constexpr bool KEEP = CH <= 3;
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kTeamThreads, 1)
   const uint32_t xbytes = (uint32_t)sa.unit * a.C * sizeof(X), unit_bytes = xbytes + (uint32_t)sa.unit * a.C * 2u;
   uint8_t* mine = ring + (size_t)me.team * sa.slots * unit_bytes;
   uint64_t* bar = full + me.team * sa.slots;
-  Loader<X, true> in(x, xs, dy, dys, mine, bar, a, sa, me.team);
+  Loader<X> in(x, xs, dy, dys, mine, bar, a, sa, me.team);
   if (me.first)
     for (int i = 0; i < sa.slots; ++i) in.load();
   check_ptr(a, ctl);
