@@ -159,8 +159,8 @@ __device__ __forceinline__ void store_rows(const MmArgs& g, const CUtensorMap* t
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
     } else if (ADD && g.vec) {
-      // added to rows on 16 bytes: a lane has unit lane % 8 of every fourth row (70 us at
-      // 6144 x 2048 x 2048, 44 without adding; value by value 80)
+      // added to rows on 16 bytes: a lane has unit lane % 8 of every fourth row (64 us at
+      // 6144 x 2048 x 2048, 38 without adding; value by value 10 more; these kernels spill 116 bytes a thread)
       if constexpr (ADD) {
         const int c = col + c0 + 4 * (lane & 7), n = g.N - c, rows = g.M - row0 - lane / 8;
         float* out = static_cast<float*>(g.c) + (long long)(row0 + lane / 8) * g.ldc + c;
@@ -228,8 +228,8 @@ __device__ __forceinline__ void stores_done(const MmArgs& g) {
 // weight's rows then take the tile's 128 and the tokens its columns, SWAP).  The
 // CTAs of a cluster take a run of the blocks of K each; then each adds up a part of
 // the tile, out of all CTAs' shared memory in their order, and writes it.  One token x
-// [12288, 2048], 25 MB, 8.5 us back to back, of which 4 begin and end it; 640 x 1160 x 40000 with
-// a scale for each column 69 us, split in five (137 unsplit).
+// [12288, 2048], 25 MB, 8.0 us in a graph, of which 4 begin and end it; 640 x 1160 x 40000 with
+// a scale for each column 64 us, split in five (twice that unsplit).
 constexpr int kSmallThreads = 320;         // 8 warps that scale, then the copying and the issuing warp
 constexpr int kCopyWarp = 8, kIssueWarp = 9;
 
@@ -570,11 +570,12 @@ cudaError_t small_pick(const CUtensorMap& tmP, const CUtensorMap& tmQ, const MmA
 // CTA gets the sums of its own 128 rows.  An SM so reads 32 KB of operands from
 // shared memory for the 512 clocks of a block, and takes in as much: with a tile
 // of its own, 128 x 128, it would be twice that, more than shared memory gives.
-// Measured: 8192^3 402 us, 2.73 PFLOP/s (529 with a scale for each column); 61440 x 6144
-// x 2048 621 us, 2.49; 6144 x 2048 x 17154 with a scale for each column 238 us, 1.81.  A
+// Measured: 8192^3 429 us, 2.56 PFLOP/s (526 with a scale for each column); 61440 x 6144
+// x 2048 652 us, 2.37; 6144 x 2048 x 17154 with a scale for each column 235 us, 1.83.  A
 // block takes 850 clocks and not 512: its products, word of them, the sums' way into
 // registers and word of that to the first CTA follow each other, over two buffers.
-// Without b's copies 406 and not 414 us at 8192^3, with half of the products 371.
+// With the same inputs again and again 8192^3 took 414 us, without
+// b's copies 406, with half of the products 371.
 constexpr int kPairThreads = 384;          // 4 warps that copy and issue, 8 that scale
 constexpr int kPairStages = 5, kPairHalf = 128 * kKb, kPairStage = 2 * kPairHalf;
 constexpr int kScaleSlots = 8, kScaleWords = 384;     // scales of a block: see the scale warp
@@ -983,7 +984,7 @@ cudaError_t pair_pick(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUte
 // end 4.5 us, or 1.4 in a pair that goes on to the next tile; joining the sums 1.2 to
 // 3.6 us; and a cluster of so many CTAs finds so many SMs at once (two CTAs each: the second
 // row, for tiles of 32 columns, which then share 0.34 us a block and begin and end beside
-// each other: one token x [24576, 2048] 24 -> 19 us, [12288, 2048] 15 either way).  Measured
+// each other: one token x [24576, 2048] 24 -> 19 us, 13 by what came after).  Measured when chosen
 // and estimated, split 1, 2, 3, 4, 5: 552 x 968 x 37776 112, 63, 47, 67, 62 us, 105, 57, 40, 61,
 // 52; 640 x 1160 x 40000 with a scale for each column 138, 76, 102, 82, 69 us, 158, 83, 114, 88, 73.
 MatmulPlan matmul_plan(const dsv_matmul& p) {

@@ -8,9 +8,9 @@
 // weight and bias of a warp's quads are then whole lines, not halves of lines.
 // What bounds it is the number of instructions, so the place of every quad is known
 // when the kernel is compiled (200 us with it worked out at run time).  Two clips of
-// 61440 rows of 2048, 1.0 GB: 170 us, 87 % of the copy bandwidth; rings in shared
+// 61440 rows of 2048, 1.0 GB: 163 us, 91 % of the copy bandwidth; rings in shared
 // memory as the backward has them, 16 warps an SM that wait for two exchanges of
-// sums a row, took 219; 16384 rows of 5120: 69 us (one row a CTA of 256 threads 77).
+// sums a row, took 219; 16384 rows of 5120: 64 us.
 // Rows that do not lie on 4 elements (an odd width, an odd start) are read and
 // written one element at a time, neighbouring threads on neighbouring columns.
 #include "norm.cuh"

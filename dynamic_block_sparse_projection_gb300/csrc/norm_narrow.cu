@@ -4,9 +4,9 @@
 // One element at a time, or two where all rows start on two elements and the width is
 // even; neighbouring threads have neighbouring columns.  2^LG threads have a row, each
 // K columns of it, and hold the next row's elements, as they are in memory, while
-// they work on this one's.  40000 rows of 1001 (bf16): 77 us, 46 % of the copy bandwidth
+// they work on this one's.  40000 rows of 1001 (bf16): 71 us, 50 % of the copy bandwidth
 // (107 without the next row in hand and a pair of columns to an instruction); 43076 of
-// 2310: 206 us, 43 % (334 one element at a time).
+// 2310: 201 us, 44 % (334 one element at a time).
 #include "norm.cuh"
 
 namespace dsv {

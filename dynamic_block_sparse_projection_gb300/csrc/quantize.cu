@@ -11,10 +11,10 @@
 // read of x.  A CTA holds a 128 x 128 tile in registers, 8 x 8 elements a
 // thread as they are in memory, so both copies' block maxima are inside the CTA, and
 // four CTAs an SM hide each other's loads, exchanges and stores.  HBM-bound: 61440 x
-// 2048 bf16 with both copies, 0.5 GB, 80 us, 6.3 TB/s (93 % of the copy bandwidth); a
-// weight of 6144 x 2048 in fp32, 75 MB, 18 us, of which 16 us are the kernel's: two CTAs
-// an SM (120 registers a thread) and three waves.  Rows off 16 bytes are read by the
-// 16-byte words that hold them (30000 x 1001: bf16 with both copies 48 -> 40 us, fp32 60 -> 38).
+// 2048 bf16 with both copies, 0.5 GB, 80 us, 6.4 TB/s (94 % of the copy bandwidth); a
+// weight of 6144 x 2048 in fp32, 75 MB, 16 us: two CTAs an SM (120 registers a
+// thread) and 2.5 waves.  Rows off 16 bytes are read by the
+// 16-byte words that hold them (30000 x 1001 with both copies: bf16 37 us, 48 one by one, fp32 42 and 60).
 #include <cuda_fp8.h>
 
 #include "dsv_launch.h"
